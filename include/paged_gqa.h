@@ -61,7 +61,8 @@ typedef enum {
   PG_F16 = 2,   /* accepted by no entry point today; reserved */
   PG_E4M3 = 3,  /* OCP FP8 e4m3fn (max 448, no inf, 0x7F/0xFF are NaN) */
   PG_I32 = 4,
-  PG_F32 = 5
+  PG_F32 = 5,
+  PG_FP4 = 6    /* bytes of a 4-bit cache (paged_gqa_cache_write_fp4) */
 } pg_dtype;
 
 /* A strided view. Unused trailing shape/stride entries are ignored. */
@@ -228,6 +229,104 @@ int paged_gqa_cache_write(const pg_tensor* k_new, const pg_tensor* v_new, const 
                           const pg_tensor* v_cache, const pg_tensor* block_table, const pg_tensor* seq_lens,
                           const pg_tensor* query_start_loc, float k_descale, float v_descale,
                           pg_stream_t stream);
+
+/*
+ * 4-bit caches: paged_gqa_cache_write_fp4, paged_gqa_cache_read_fp4, paged_gqa_attn_fp4.
+ *
+ * 256 values of a (token, kv head) take 144 bytes: 128 bytes of e2m1 codes (0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives; byte i holds d = 2i in its low nibble and d = 2i + 1 in its
+ * high one) and 16 e4m3 scales, one per 16 consecutive d. value = code * scale * descale,
+ * descale being the tensor's factor as for e4m3 caches. That is 288 bytes per token and kv
+ * head for K and V, 9/16 of an e4m3 cache.
+ *
+ *   k_cache, v_cache  [NB, Hkv, P, 144]  PG_FP4; the last two dims contiguous (a page of one
+ *                     kv head is P * 144 bytes), any strides on dims 0 and 1 that are
+ *                     multiples of 16 bytes, base 16-byte aligned. Inside a page:
+ *     K  token by token: [128 code bytes][16 scales]
+ *     V  in blocks of 16 tokens, 2304 bytes each: code byte i of token j at i * 16 + j
+ *        (i < 128), then the scale of group g at 2048 + g * 16 + j (g < 16)
+ * Page sizes are 16, 32, 64 and 128. Every byte belongs to one token. block_table, seq_lens
+ * and query_start_loc are those of paged_gqa_attn.
+ *
+ * The pages describe no 4-bit cache: its format is this library's own.
+ */
+
+/*
+ * paged_gqa_cache_write_fp4 -- writes the new tokens' K and V ([T, Hkv, 256] bf16, in
+ * query_start_loc order) into 4-bit caches, at the positions paged_gqa_cache_write takes.
+ * For each group of 16 values x, in fp32:
+ *   y = x * inv, inv = 1 / descale rounded to fp32 once per call
+ *   scale = e4m3(max |y| * fp32(1/6)), nearest even, at most 448
+ *   code = e2m1(y * r), r = fp32(1 / scale) (0 if scale is 0), nearest even, at most +-6
+ * A group with a NaN gets a NaN scale, so its values read back as NaN; infinities saturate.
+ * A descale near amax / (6 * 448) of the tensor uses the scales' whole range.
+ * Nothing else in the caches changes. k_new and v_new need 16-byte aligned rows; the caches'
+ * (page, head) blocks must not overlap. Descales must be finite, positive and have a finite
+ * reciprocal. Errors as paged_gqa_cache_write (a bad position or page: that row is skipped).
+ * Allocates nothing.
+ */
+int paged_gqa_cache_write_fp4(const pg_tensor* k_new, const pg_tensor* v_new, const pg_tensor* k_cache,
+                              const pg_tensor* v_cache, const pg_tensor* block_table, const pg_tensor* seq_lens,
+                              const pg_tensor* query_start_loc, float k_descale, float v_descale,
+                              pg_stream_t stream);
+
+/*
+ * paged_gqa_cache_read_fp4 -- the way back: k_out and v_out ([T, Hkv, 256] bf16, rows 16-byte
+ * aligned and disjoint) get the values held for the last query_start_loc[s + 1] -
+ * query_start_loc[s] positions of each sequence (its whole context, where that is
+ * seq_lens[s]), rounded to bf16 once; with a power-of-two descale they are exact. For moving
+ * a prefix to another cache, or a kernel that wants bf16. A bad position or page is flagged
+ * and its rows are zeros. Arguments otherwise as paged_gqa_cache_write_fp4. Allocates nothing.
+ */
+int paged_gqa_cache_read_fp4(const pg_tensor* k_cache, const pg_tensor* v_cache, const pg_tensor* block_table,
+                             const pg_tensor* seq_lens, const pg_tensor* query_start_loc, float k_descale,
+                             float v_descale, pg_tensor* k_out, pg_tensor* v_out, pg_stream_t stream);
+
+/*
+ * paged_gqa_attn_fp4 -- paged_gqa_attn on 4-bit caches: single new tokens, verify steps and
+ * prefill chunks in one batch. q and out are bf16 [T, Hq, 256]; the other arguments, the mask,
+ * the errors and what is left untouched are those of paged_gqa_attn. K and V enter the
+ * products exactly (code * scale has 6 significant bits); scores, sums and outputs are held
+ * in fp32. A new call and an older one on another stream are ordered by the library (they
+ * share its workspace), so such calls do not overlap; in a stream capture the call returns
+ * PG_ERR_WORKSPACE: use paged_gqa_attn_fp4_ex there, with a workspace of
+ * paged_gqa_workspace_size(...) bytes, 256-byte aligned, that no overlapping call uses (two
+ * graphs that can run at once need one each). _ex allocates nothing.
+ */
+int paged_gqa_attn_fp4(const pg_tensor* q, const pg_tensor* k_cache, const pg_tensor* v_cache,
+                       const pg_tensor* block_table, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                       float k_descale, float v_descale, float softmax_scale, pg_tensor* out, pg_stream_t stream);
+int paged_gqa_attn_fp4_ex(const pg_tensor* q, const pg_tensor* k_cache, const pg_tensor* v_cache,
+                          const pg_tensor* block_table, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                          float k_descale, float v_descale, float softmax_scale, pg_tensor* out, void* workspace,
+                          size_t workspace_bytes, pg_stream_t stream);
+
+/*
+ * paged_gqa_rope -- rotary positions with up to four axes (time, height, width, ...) for the
+ * new tokens' q and k, before the cache write and the attention.
+ *
+ *   q, k          [T, Hq, 256], [T, Hkv, 256] bf16; rows 16-byte aligned, any such strides
+ *   positions     [A, T] int32, 1 <= A <= 4 (text: all axes alike), last dim contiguous
+ *   inv_freq      [R / 2] float32, finite (a non-finite one makes its token's pairs near it
+ *                 NaN); R = 16, 32, .. 256 values of each head are rotated, the rest pass through
+ *   sections      host array of A counts that add up to R / 2: how many entries of inv_freq
+ *                 go with each axis
+ *   interleaved   0: the first sections[0] entries go with axis 0, the next sections[1] with
+ *                 axis 1, ..; 1: entry i goes with axis i mod A until that axis has its
+ *                 number, what is left over with axis 0 (each axis but 0 must find its number)
+ *   adjacent      0: pair i is (i, i + R / 2); 1: (2i, 2i + 1)
+ *   q_out, k_out  bf16, shapes of q and k, rows disjoint; each may be its input (same data
+ *                 and strides: then only the rotated values are touched) and must otherwise
+ *                 not overlap any input
+ *
+ * Pair (u, w) becomes (u cos a - w sin a, w cos a + u sin a), a = position * inv_freq[i], in
+ * fp32, rounded once. The angle keeps its phase for every 32-bit position (negative ones turn
+ * back): it is reduced modulo whole turns in fixed point, off by less than 2^-31 turns.
+ * Allocates nothing. (The pages do not describe the rotation; Q and K arrive rotated there.)
+ */
+int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* positions, const pg_tensor* inv_freq,
+                   const int32_t* sections, int interleaved, int adjacent, pg_tensor* q_out, pg_tensor* k_out,
+                   pg_stream_t stream);
 
 /*
  * Workspace bytes for a call with these host-known sizes on `device`

@@ -17,6 +17,11 @@ from ._binding import (  # noqa: F401
     paged_gqa_attn_quant_q,
     paged_gqa_sparse_attn,
     paged_gqa_cache_write,
+    paged_gqa_cache_write_fp4,
+    paged_gqa_cache_read_fp4,
+    paged_gqa_attn_fp4,
+    paged_gqa_attn_fp4_ex,
+    paged_gqa_rope,
     paged_gqa_check_device_errors,
     paged_gqa_last_error,
     paged_gqa_last_plan,

@@ -11,13 +11,15 @@ import torch
 
 from . import build as _build
 
-PG_BF16, PG_F16, PG_E4M3, PG_I32, PG_F32 = 1, 2, 3, 4, 5
+PG_BF16, PG_F16, PG_E4M3, PG_I32, PG_F32, PG_FP4 = 1, 2, 3, 4, 5, 6
 STATUS_NAMES = {0: "PG_OK", -1: "PG_ERR_INVALID_ARG", -2: "PG_ERR_UNSUPPORTED", -3: "PG_ERR_CUDA",
                 -4: "PG_ERR_TIMEOUT", -5: "PG_ERR_DEVICE_BOUNDS", -6: "PG_ERR_WORKSPACE"}
 
 # Every symbol include/paged_gqa.h declares.
 EXPORTED = ("paged_gqa_attn", "paged_gqa_attn_ex", "paged_gqa_attn_noalloc", "paged_gqa_attn_quant_q",
             "paged_gqa_sparse_attn", "paged_gqa_cache_write",
+            "paged_gqa_cache_write_fp4", "paged_gqa_cache_read_fp4", "paged_gqa_attn_fp4", "paged_gqa_attn_fp4_ex",
+            "paged_gqa_rope",
             "paged_gqa_workspace_size",
             "paged_gqa_last_error",
             "paged_gqa_check_device_errors", "paged_gqa_set_path", "paged_gqa_set_stall_test", "paged_gqa_last_plan",
@@ -81,6 +83,13 @@ def load(build_if_missing: bool = True):
             lib.paged_gqa_sparse_attn.restype = ctypes.c_int
             lib.paged_gqa_sparse_attn.argtypes = [P, P, P, P, P, P, P, f, f, f, P, c_vp]
             lib.paged_gqa_cache_write.restype = ctypes.c_int
+            lib.paged_gqa_cache_write_fp4.argtypes = [P, P, P, P, P, P, P, f, f, c_vp]
+            lib.paged_gqa_cache_read_fp4.argtypes = [P, P, P, P, P, f, f, P, P, c_vp]
+            lib.paged_gqa_attn_fp4.argtypes = [P, P, P, P, P, P, f, f, f, P, c_vp]
+            lib.paged_gqa_attn_fp4_ex.argtypes = [P, P, P, P, P, P, f, f, f, P, c_vp, ctypes.c_size_t, c_vp]
+            lib.paged_gqa_rope.argtypes = [P, P, P, P, ctypes.POINTER(ctypes.c_int32), ctypes.c_int, ctypes.c_int, P, P, c_vp]
+            for name in ("cache_write_fp4", "cache_read_fp4", "attn_fp4", "attn_fp4_ex", "rope"):
+                getattr(lib, "paged_gqa_" + name).restype = ctypes.c_int
             lib.paged_gqa_workspace_size.argtypes = [ctypes.c_int] * 7
             lib.paged_gqa_workspace_size.restype = ctypes.c_size_t
             lib.paged_gqa_last_error.restype = ctypes.c_char_p
@@ -205,6 +214,86 @@ def paged_gqa_cache_write(k_new, v_new, k_cache, v_cache, block_table, seq_lens,
     lib = load()
     d = _pack(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_start_loc)
     _check(lib.paged_gqa_cache_write(*d, float(k_descale), float(v_descale), _stream(stream)))
+
+
+def _on_device(*tensors) -> None:
+    """The tensors are on the current CUDA device (the library launches there)."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        d = t.device
+        if d.type != "cuda" or d.index != cur:
+            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{cur}), got one on {d}")
+
+
+def _pack_fp4(first_cache: int, *tensors):
+    """_pack with tensors[first_cache] and the next one as 4-bit caches (uint8 rows of 144 bytes)."""
+    for t in tensors[first_cache:first_cache + 2]:
+        if t.dtype != torch.uint8:
+            raise ValueError(f"4-bit caches are uint8 tensors, got {t.dtype}")
+    out = _pack(*tensors)
+    arr = _desc_buf()[0]
+    arr[first_cache].dtype = arr[first_cache + 1].dtype = PG_FP4
+    return out
+
+
+def paged_gqa_cache_write_fp4(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_start_loc,
+                              k_descale: float, v_descale: float, stream=None) -> None:
+    """Write the new tokens' K and V (bf16 [T, Hkv, 256]) into 4-bit caches (uint8 [NB, Hkv, P, 144])."""
+    lib = load()
+    _on_device(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_start_loc)
+    d = _pack_fp4(2, k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_start_loc)
+    _check(lib.paged_gqa_cache_write_fp4(*d, float(k_descale), float(v_descale), _stream(stream)))
+
+
+def paged_gqa_cache_read_fp4(k_cache, v_cache, block_table, seq_lens, query_start_loc, k_descale: float,
+                             v_descale: float, k_out, v_out, stream=None) -> None:
+    """The values 4-bit caches hold for the last tokens of each sequence, as bf16 [T, Hkv, 256]."""
+    lib = load()
+    _on_device(k_cache, v_cache, block_table, seq_lens, query_start_loc, k_out, v_out)
+    d = _pack_fp4(0, k_cache, v_cache, block_table, seq_lens, query_start_loc, k_out, v_out)
+    _check(lib.paged_gqa_cache_read_fp4(*d[:5], float(k_descale), float(v_descale), d[5], d[6], _stream(stream)))
+
+
+def paged_gqa_attn_fp4(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, k_descale: float,
+                       v_descale: float, softmax_scale: float, out, stream=None) -> None:
+    """paged_gqa_attn on 4-bit caches (uint8 [NB, Hkv, P, 144]); q and out are bf16."""
+    lib = load()
+    _on_device(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, out)
+    d = _pack_fp4(1, q, k_cache, v_cache, block_table, seq_lens, query_start_loc, out)
+    _check(lib.paged_gqa_attn_fp4(*d[:6], float(k_descale), float(v_descale), float(softmax_scale), d[6],
+                                  _stream(stream)))
+
+
+def paged_gqa_attn_fp4_ex(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, k_descale: float,
+                          v_descale: float, softmax_scale: float, out, workspace, stream=None) -> None:
+    """paged_gqa_attn_fp4 with a caller-owned workspace tensor (for stream capture)."""
+    lib = load()
+    _on_device(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, out)
+    d = _pack_fp4(1, q, k_cache, v_cache, block_table, seq_lens, query_start_loc, out)
+    ptr = nbytes = 0
+    if workspace is not None:
+        _on_device(workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous")
+        ptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.paged_gqa_attn_fp4_ex(*d[:6], float(k_descale), float(v_descale), float(softmax_scale), d[6],
+                                     ptr or None, nbytes, _stream(stream)))
+
+
+def paged_gqa_rope(q, k, positions, inv_freq, sections, q_out=None, k_out=None, interleaved: bool = False,
+                   adjacent: bool = False, stream=None) -> None:
+    """Rotary positions [A, T] for q and k (bf16 [T, H, 256]), in place where no output is given.
+
+    sections: A counts that add up to inv_freq's length (float32 [R / 2])."""
+    lib = load()
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    _on_device(q, k, positions, inv_freq, q_out, k_out)
+    if len(sections) != positions.shape[0]:
+        raise ValueError(f"{len(sections)} sections for {positions.shape[0]} axes")
+    d = _pack(q, k, positions, inv_freq, q_out, k_out)
+    _check(lib.paged_gqa_rope(*d[:4], (ctypes.c_int32 * len(sections))(*sections), int(interleaved), int(adjacent),
+                              d[4], d[5], _stream(stream)))
 
 
 def paged_gqa_workspace_size(num_seqs: int, total_q: int, num_q_heads: int, num_kv_heads: int,

@@ -61,10 +61,10 @@ int cuda_fail(cudaError_t e, const char* what) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Whether the rows of a written tensor are pairwise disjoint: dims 0 .. nd-1 index rows of
-// kHeadDim contiguous elements. Sufficient test: taken in increasing stride order, every
+// `span` contiguous elements. Sufficient test: taken in increasing stride order, every
 // dim of extent > 1 must step past everything the smaller dims span (no zero, negative or
 // interleaved strides), so no two (index tuples) write the same element.
-bool rows_disjoint(const pg_tensor* t, int nd) {
+bool rows_disjoint(const pg_tensor* t, int nd, long long span = kHeadDim) {
   long long ext[4], str[4];
   int n = 0;
   for (int i = 0; i < nd; ++i) {
@@ -79,8 +79,7 @@ bool rows_disjoint(const pg_tensor* t, int nd) {
       std::swap(str[j], str[j - 1]);
       std::swap(ext[j], ext[j - 1]);
     }
-  long long span = kHeadDim;  // elements covered by one index of the dims taken so far
-  for (int i = 0; i < n; ++i) {
+  for (int i = 0; i < n; ++i) {  // span: elements covered by one index of the dims taken so far
     if (str[i] < span) return false;
     span = (ext[i] - 1) * str[i] + span;
   }
@@ -95,6 +94,12 @@ struct DeviceState {
   uint32_t* err = nullptr;   // address of g_error_word on this device
   void* ws = nullptr;        // library-owned workspace
   size_t ws_bytes = 0;
+  // The 4-bit attention's own one; a call on another stream than the last waits for its event.
+  void* ws4 = nullptr;
+  size_t ws4_bytes = 0;
+  cudaEvent_t ws4_done = nullptr;
+  cudaStream_t ws4_stream = nullptr;
+  bool ws4_used = false;
 };
 DeviceState g_dev[kMaxDevices];
 
@@ -281,6 +286,7 @@ int validate(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
   p.NB = (int)NB;
   p.q_is_fp8 = q->dtype == PG_E4M3;
   p.kv_is_fp8 = k->dtype == PG_E4M3;
+  p.kv_is_fp4 = 0;
   p.q_cast = q_cast ? 1 : 0;
   p.q_amax_parts = 0;
   p.q_st = q->stride[0];
@@ -448,6 +454,280 @@ int attn_common(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, cons
       ds->ws_bytes = want;
     }
     st = run(val, k, v, ds->ws, ds->ws_bytes, L, ds, stream);
+  }
+  if (st == PG_OK) t_last_error.clear();
+  return st;
+}
+
+// ---------------------------------------------------------------- 4-bit caches --
+
+// Caches [NB, Hkv, P, 144] of packed 4-bit rows: a page of one kv head is contiguous.
+int check_fp4_caches(const pg_tensor* k, const pg_tensor* v, bool written) {
+  int st;
+  if ((st = check_tensor(k, "k_cache", 4)) || (st = check_tensor(v, "v_cache", 4))) return st;
+  if (k->dtype != PG_FP4 || v->dtype != PG_FP4)
+    return fail(PG_ERR_UNSUPPORTED, "the caches must be packed 4-bit rows (uint8)");
+  if (k->shape[3] != kFp4Row || v->shape[3] != kFp4Row)
+    return fail(PG_ERR_UNSUPPORTED, "4-bit cache rows must have %d bytes (k_cache %lld, v_cache %lld)", kFp4Row,
+                (long long)k->shape[3], (long long)v->shape[3]);
+  for (int i = 0; i < 4; ++i)
+    if (k->shape[i] != v->shape[i]) return fail(PG_ERR_INVALID_ARG, "k_cache and v_cache shapes differ");
+  const long long NB = k->shape[0], P = k->shape[2];
+  if (P != 16 && P != 32 && P != 64 && P != 128)
+    return fail(PG_ERR_UNSUPPORTED, "page size %lld not in {16, 32, 64, 128}", P);
+  if (NB > INT32_MAX || k->shape[1] > 65535) return fail(PG_ERR_UNSUPPORTED, "sizes beyond the supported range");
+  for (const pg_tensor* t : {k, v}) {
+    if (t->stride[3] != 1 || t->stride[2] != kFp4Row)
+      return fail(PG_ERR_INVALID_ARG, "a kv head's page must be contiguous (strides %d and 1 of the last two axes)", kFp4Row);
+    if (!aligned16(t->data)) return fail(PG_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
+    if (t->stride[0] % 16 || t->stride[1] % 16)
+      return fail(PG_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes");
+    if (written && !rows_disjoint(t, 2, P * kFp4Row))
+      return fail(PG_ERR_INVALID_ARG, "cache strides make (page, head) blocks overlap");
+    if (NB > 0 && !t->data) return fail(PG_ERR_INVALID_ARG, "null data pointer");
+  }
+  return PG_OK;
+}
+
+// block_table, seq_lens and query_start_loc of a call; *W gets the table's width.
+int check_tables(const pg_tensor* bt, const pg_tensor* sl, const pg_tensor* qsl, long long* W) {
+  int st;
+  if ((st = check_tensor(bt, "block_table", 2)) || (st = check_tensor(sl, "seq_lens", 1)) ||
+      (st = check_tensor(qsl, "query_start_loc", 1)))
+    return st;
+  if (bt->dtype != PG_I32 || sl->dtype != PG_I32 || qsl->dtype != PG_I32)
+    return fail(PG_ERR_INVALID_ARG, "block_table, seq_lens and query_start_loc must be int32");
+  const long long S = sl->shape[0];
+  *W = bt->shape[1];
+  if (bt->shape[0] != S || qsl->shape[0] != S + 1)
+    return fail(PG_ERR_INVALID_ARG, "block_table rows / query_start_loc length must match seq_lens");
+  if (S > INT32_MAX / 2 || *W > INT32_MAX / 2) return fail(PG_ERR_UNSUPPORTED, "sizes beyond the supported range");
+  if (*W > 1 && bt->stride[1] != 1) return fail(PG_ERR_INVALID_ARG, "block_table rows must be contiguous");
+  if ((S > 1 && sl->stride[0] != 1) || (S > 0 && qsl->stride[0] != 1))
+    return fail(PG_ERR_INVALID_ARG, "seq_lens and query_start_loc must be contiguous");
+  if (!qsl->data || (S > 0 && (!sl->data || (*W > 0 && !bt->data))))
+    return fail(PG_ERR_INVALID_ARG, "null data pointer");
+  for (const pg_tensor* t : {bt, sl, qsl})
+    if (reinterpret_cast<uintptr_t>(t->data) & 3u)
+      return fail(PG_ERR_INVALID_ARG, "block_table, seq_lens and query_start_loc must be 4-byte aligned");
+  return PG_OK;
+}
+
+// bf16 [T, H, 256] rows with 16-byte aligned (token, head) rows.
+int check_rows(const pg_tensor* t, const char* name, bool written) {
+  int st;
+  if ((st = check_tensor(t, name, 3))) return st;
+  if (t->dtype != PG_BF16) return fail(PG_ERR_UNSUPPORTED, "%s must be bf16", name);
+  if (t->shape[2] != kHeadDim) return fail(PG_ERR_UNSUPPORTED, "%s: head_dim must be 256", name);
+  if (t->shape[0] > INT32_MAX / 2 || t->shape[1] > 65535)
+    return fail(PG_ERR_UNSUPPORTED, "sizes beyond the supported range");
+  if (t->stride[2] != 1) return fail(PG_ERR_INVALID_ARG, "%s: the head_dim axis must be contiguous", name);
+  if (!aligned16(t->data)) return fail(PG_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  for (int i = 0; i < 2; ++i)
+    if (t->shape[i] > 1 && (t->stride[i] * 2) % 16)
+      return fail(PG_ERR_INVALID_ARG, "%s strides must be multiples of 16 bytes", name);
+  if (t->shape[0] > 0 && t->shape[1] > 0 && !t->data) return fail(PG_ERR_INVALID_ARG, "%s: null data pointer", name);
+  if (written && !rows_disjoint(t, 2)) return fail(PG_ERR_INVALID_ARG, "%s strides make (token, head) rows overlap", name);
+  return PG_OK;
+}
+
+int current_device(DeviceState** ds) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  return device_state(dev, ds);
+}
+
+int fp4_cache_call(bool write, const pg_tensor* kx, const pg_tensor* vx, const pg_tensor* kc, const pg_tensor* vc,
+                   const pg_tensor* bt, const pg_tensor* sl, const pg_tensor* qsl, float k_descale, float v_descale,
+                   cudaStream_t stream) {
+  int st;
+  long long W = 0;
+  const char* kn = write ? "k_new" : "k_out";
+  const char* vn = write ? "v_new" : "v_out";
+  if ((st = check_rows(kx, kn, !write)) || (st = check_rows(vx, vn, !write)) || (st = check_fp4_caches(kc, vc, write)) ||
+      (st = check_tables(bt, sl, qsl, &W)))
+    return st;
+  if (kx->shape[0] != vx->shape[0] || kx->shape[1] != vx->shape[1])
+    return fail(PG_ERR_INVALID_ARG, "%s and %s shapes differ", kn, vn);
+  const long long T = kx->shape[0], Hkv = kx->shape[1], S = sl->shape[0];
+  if (kc->shape[1] != Hkv) return fail(PG_ERR_INVALID_ARG, "%s and the caches disagree on num_kv_heads", kn);
+  if (S == 0 && T > 0) return fail(PG_ERR_INVALID_ARG, "tokens without sequences");
+  // 1 / descale has to be finite too (a descale below 2^-128 has no fp32 reciprocal)
+  if (!(std::isfinite(k_descale) && k_descale > 0.f && std::isfinite(v_descale) && v_descale > 0.f &&
+        std::isfinite(1.f / k_descale) && std::isfinite(1.f / v_descale)))
+    return fail(PG_ERR_INVALID_ARG, "descales and their reciprocals must be finite and positive");
+  if (T == 0 || Hkv == 0) {
+    t_last_error.clear();
+    return PG_OK;
+  }
+  DeviceState* ds = nullptr;
+  if ((st = current_device(&ds))) return st;
+  Fp4CacheArgs a;
+  a.kx = static_cast<uint16_t*>(kx->data);
+  a.vx = static_cast<uint16_t*>(vx->data);
+  a.kx_st = kx->stride[0];
+  a.kx_sh = kx->stride[1];
+  a.vx_st = vx->stride[0];
+  a.vx_sh = vx->stride[1];
+  a.kc = static_cast<uint8_t*>(kc->data);
+  a.vc = static_cast<uint8_t*>(vc->data);
+  a.kc_sb = kc->stride[0];
+  a.kc_sh = kc->stride[1];
+  a.vc_sb = vc->stride[0];
+  a.vc_sh = vc->stride[1];
+  a.bt = static_cast<const int32_t*>(bt->data);
+  a.bt_stride = W > 0 ? bt->stride[0] : 1;
+  a.seq_lens = static_cast<const int32_t*>(sl->data);
+  a.qsl = static_cast<const int32_t*>(qsl->data);
+  a.num_seqs = (int)S;
+  a.T = (int)T;
+  a.Hkv = (int)Hkv;
+  a.P = (int)kc->shape[2];
+  a.p_shift = __builtin_ctz((unsigned)a.P);
+  a.W = (int)W;
+  a.NB = (int)kc->shape[0];
+  a.k_mul = write ? 1.f / k_descale : k_descale;
+  a.v_mul = write ? 1.f / v_descale : v_descale;
+  a.err = ds->err;
+  const cudaError_t e = write ? launch_fp4_cache_write(a, ds->sms, stream) : launch_fp4_cache_read(a, ds->sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, write ? "4-bit cache write launch" : "4-bit cache read launch");
+  t_last_error.clear();
+  return PG_OK;
+}
+
+int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, cudaStream_t stream) {
+  Problem p = val.p;
+  Pointers ptr = val.ptr;
+  ptr.err = ds->err;
+  ClassPlan cp[kNumClasses];
+  for (int c = 0; c < kNumClasses; ++c) cp[c] = class_plan(L, c, static_cast<char*>(ws));
+  int64_t plan_info[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  int launched = 0, used = 0;
+  p.call_tag = next_call_tag();
+  p.fused_verify = 0;
+  cudaError_t e = launch_plan(p, ptr, cp[0], cp[1], true, false, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "plan launch");
+  ++launched;
+  for (int c = 0; c < kNumClasses; ++c) {
+    e = launch_portable(p, ptr, cp[c], c == 0 ? kVerifyRows : kPrefillRows, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit attention launch");
+    used |= 8 << c;
+    ++launched;
+  }
+  plan_info[0] = cp[0].num_ctas;
+  plan_info[1] = cp[1].num_ctas;
+  plan_info[2] = launched;
+  plan_info[3] = used;
+  plan_info[4] = cp[0].max_blocks;
+  plan_info[5] = cp[1].max_blocks;
+  plan_info[6] = (int64_t)L.total;
+  plan_info[7] = p.fused_verify;
+  memcpy(t_last_plan, plan_info, sizeof plan_info);
+  return PG_OK;
+}
+
+int attn_fp4(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* bt, const pg_tensor* sl,
+             const pg_tensor* qsl, float k_descale, float v_descale, float softmax_scale, const pg_tensor* out,
+             void* user_ws, size_t user_ws_bytes, bool use_user_ws, cudaStream_t stream) {
+  int st;
+  long long W = 0;
+  if ((st = check_rows(q, "q", false)) || (st = check_fp4_caches(k, v, false)) || (st = check_tables(bt, sl, qsl, &W)) ||
+      (st = check_rows(out, "out", true)))
+    return st;
+  const long long T = q->shape[0], Hq = q->shape[1], Hkv = k->shape[1], S = sl->shape[0];
+  if (out->shape[0] != T || out->shape[1] != Hq) return fail(PG_ERR_INVALID_ARG, "out shape must equal q shape");
+  if (Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0)
+    return fail(PG_ERR_INVALID_ARG, "num_q_heads (%lld) must be a positive multiple of num_kv_heads (%lld)", Hq, Hkv);
+  if (!std::isfinite(softmax_scale) || !std::isfinite(k_descale) || !std::isfinite(v_descale))
+    return fail(PG_ERR_INVALID_ARG, "scales must be finite");
+  const double score = (double)softmax_scale * (double)k_descale * 1.4426950408889634;
+  if (!(std::fabs(score) <= 3.4e38)) return fail(PG_ERR_INVALID_ARG, "softmax_scale * k_descale must fit fp32");
+  if (S == 0 || T == 0) {
+    t_last_error.clear();
+    return PG_OK;
+  }
+  if (k->shape[0] == 0 || W == 0) return fail(PG_ERR_INVALID_ARG, "new tokens without pages");
+  Validated val{};
+  Problem& p = val.p;
+  p.num_seqs = (int)S;
+  p.T = (int)T;
+  p.Hq = (int)Hq;
+  p.Hkv = (int)Hkv;
+  p.G = (int)(Hq / Hkv);
+  p.P = (int)k->shape[2];
+  p.W = (int)W;
+  p.NB = (int)k->shape[0];
+  p.kv_is_fp4 = 1;
+  p.q_st = q->stride[0];
+  p.q_sh = q->stride[1];
+  p.k_sb = k->stride[0];
+  p.k_sh = k->stride[1];
+  p.v_sb = v->stride[0];
+  p.v_sh = v->stride[1];
+  p.o_st = out->stride[0];
+  p.o_sh = out->stride[1];
+  p.bt_stride = bt->stride[0];
+  p.score_scale_log2 = (float)score;
+  p.out_scale = v_descale;
+  p.stall_test_ns = g_stall_test_ns.load();
+  val.ptr.q = q->data;
+  val.ptr.k = k->data;
+  val.ptr.v = v->data;
+  val.ptr.block_table = static_cast<const int32_t*>(bt->data);
+  val.ptr.seq_lens = static_cast<const int32_t*>(sl->data);
+  val.ptr.qsl = static_cast<const int32_t*>(qsl->data);
+  val.ptr.out = out->data;
+  DeviceState* ds = nullptr;
+  if ((st = current_device(&ds))) return st;
+  const WsLayout L = make_layout(p.num_seqs, p.T, p.Hq, p.Hkv, ds->sms);
+  cudaError_t e;
+  if (use_user_ws) {
+    if (!user_ws || (reinterpret_cast<uintptr_t>(user_ws) & 255u))
+      return fail(PG_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
+    if (user_ws_bytes < L.total)
+      return fail(PG_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", user_ws_bytes, L.total);
+    st = run_fp4(val, user_ws, L, ds, stream);
+  } else {
+    // A graph would keep the library's workspace, which may grow (and move) or serve another
+    // stream while the graph replays.
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    e = cudaStreamIsCapturing(stream, &cap);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+    if (cap != cudaStreamCaptureStatusNone)
+      return fail(PG_ERR_WORKSPACE, "a captured call needs its own workspace: paged_gqa_attn_fp4_ex");
+    std::lock_guard<std::mutex> lk(ds->mu);
+    if (!ds->ws4_done && (e = cudaEventCreateWithFlags(&ds->ws4_done, cudaEventDisableTiming)) != cudaSuccess)
+      return cuda_fail(e, "cudaEventCreate");
+    if (ds->ws4_bytes < L.total) {
+      if (ds->ws4) {
+        e = cudaDeviceSynchronize();  // work already queued may still use the old buffer
+        if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize before workspace growth");
+        cudaFree(ds->ws4);
+        ds->ws4 = nullptr;
+        ds->ws4_bytes = 0;
+        ds->ws4_used = false;
+      }
+      const size_t want = L.total + L.total / 4;
+      e = cudaMalloc(&ds->ws4, want);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
+      ds->ws4_bytes = want;
+      // the counters are tagged per call and need no clearing; defined contents all the same
+      e = cudaMemsetAsync(ds->ws4, 0, want, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace)");
+    }
+    // One workspace, any streams: a call on another stream than the last one's waits for that
+    // one (the per-thread default stream's handle names another stream in every thread).
+    if (ds->ws4_used && (ds->ws4_stream != stream || stream == cudaStreamPerThread)) {
+      e = cudaStreamWaitEvent(stream, ds->ws4_done, 0);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
+    }
+    st = run_fp4(val, ds->ws4, L, ds, stream);
+    // also after a failed launch: what was launched before it may be running
+    e = cudaEventRecord(ds->ws4_done, stream);
+    if (e != cudaSuccess && st == PG_OK) return cuda_fail(e, "cudaEventRecord");
+    ds->ws4_stream = stream;
+    ds->ws4_used = true;
   }
   if (st == PG_OK) t_last_error.clear();
   return st;
@@ -725,6 +1005,108 @@ int paged_gqa_cache_write(const pg_tensor* k_new, const pg_tensor* v_new, const 
   a.err = ds->err;
   e = launch_cache_write(a, ds->sms, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
+  return PG_OK;
+}
+
+int paged_gqa_cache_write_fp4(const pg_tensor* k_new, const pg_tensor* v_new, const pg_tensor* k_cache,
+                              const pg_tensor* v_cache, const pg_tensor* block_table, const pg_tensor* seq_lens,
+                              const pg_tensor* query_start_loc, float k_descale, float v_descale,
+                              pg_stream_t stream) {
+  return fp4_cache_call(true, k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_start_loc, k_descale,
+                        v_descale, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int paged_gqa_cache_read_fp4(const pg_tensor* k_cache, const pg_tensor* v_cache, const pg_tensor* block_table,
+                             const pg_tensor* seq_lens, const pg_tensor* query_start_loc, float k_descale,
+                             float v_descale, pg_tensor* k_out, pg_tensor* v_out, pg_stream_t stream) {
+  return fp4_cache_call(false, k_out, v_out, k_cache, v_cache, block_table, seq_lens, query_start_loc, k_descale,
+                        v_descale, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int paged_gqa_attn_fp4(const pg_tensor* q, const pg_tensor* k_cache, const pg_tensor* v_cache,
+                       const pg_tensor* block_table, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                       float k_descale, float v_descale, float softmax_scale, pg_tensor* out, pg_stream_t stream) {
+  return attn_fp4(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, k_descale, v_descale, softmax_scale,
+                  out, nullptr, 0, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int paged_gqa_attn_fp4_ex(const pg_tensor* q, const pg_tensor* k_cache, const pg_tensor* v_cache,
+                          const pg_tensor* block_table, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                          float k_descale, float v_descale, float softmax_scale, pg_tensor* out, void* workspace,
+                          size_t workspace_bytes, pg_stream_t stream) {
+  return attn_fp4(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, k_descale, v_descale, softmax_scale,
+                  out, workspace, workspace_bytes, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* positions, const pg_tensor* inv_freq,
+                   const int32_t* sections, int interleaved, int adjacent, pg_tensor* q_out, pg_tensor* k_out,
+                   pg_stream_t stream) {
+  int st;
+  const pg_tensor* in[2] = {q, k};
+  const pg_tensor* out[2] = {q_out, k_out};
+  const char* names[2][2] = {{"q", "q_out"}, {"k", "k_out"}};
+  RopeArgs a{};
+  for (int i = 0; i < 2; ++i) {
+    if ((st = check_rows(in[i], names[i][0], false)) || (st = check_rows(out[i], names[i][1], true))) return st;
+    for (int d = 0; d < 2; ++d)
+      if (in[i]->shape[d] != out[i]->shape[d])
+        return fail(PG_ERR_INVALID_ARG, "%s shape must equal %s shape", names[i][1], names[i][0]);
+    a.in_place[i] = in[i]->data && in[i]->data == out[i]->data;
+    if (a.in_place[i])
+      for (int d = 0; d < 2; ++d)
+        if (in[i]->shape[d] > 1 && in[i]->stride[d] != out[i]->stride[d])
+          return fail(PG_ERR_INVALID_ARG, "%s in place of %s needs the same strides", names[i][1], names[i][0]);
+    a.x[i] = static_cast<const uint16_t*>(in[i]->data);
+    a.y[i] = static_cast<uint16_t*>(out[i]->data);
+    a.x_st[i] = in[i]->stride[0];
+    a.x_sh[i] = in[i]->stride[1];
+    a.y_st[i] = out[i]->stride[0];
+    a.y_sh[i] = out[i]->stride[1];
+    a.heads[i] = (int)in[i]->shape[1];
+  }
+  if (q->shape[0] != k->shape[0]) return fail(PG_ERR_INVALID_ARG, "q and k disagree on the number of tokens");
+  if ((st = check_tensor(positions, "positions", 2)) || (st = check_tensor(inv_freq, "inv_freq", 1))) return st;
+  const long long T = q->shape[0], A = positions->shape[0], half = inv_freq->shape[0];
+  if (positions->dtype != PG_I32) return fail(PG_ERR_INVALID_ARG, "positions must be int32");
+  if (inv_freq->dtype != PG_F32) return fail(PG_ERR_INVALID_ARG, "inv_freq must be float32");
+  if (A < 1 || A > kRopeMaxAxes) return fail(PG_ERR_UNSUPPORTED, "positions must have 1 to %d axes", kRopeMaxAxes);
+  if (positions->shape[1] != T) return fail(PG_ERR_INVALID_ARG, "positions must be [axes, T]");
+  if (half < 8 || half > kHeadDim / 2 || half % 8)
+    return fail(PG_ERR_UNSUPPORTED, "inv_freq must have 8 to 128 entries, a multiple of 8");
+  if ((T > 1 && positions->stride[1] != 1) || inv_freq->stride[0] != 1)
+    return fail(PG_ERR_INVALID_ARG, "the last axis of positions and inv_freq must be contiguous");
+  if (!inv_freq->data || (T > 0 && !positions->data)) return fail(PG_ERR_INVALID_ARG, "null data pointer");
+  if ((reinterpret_cast<uintptr_t>(positions->data) & 3u) || (reinterpret_cast<uintptr_t>(inv_freq->data) & 3u))
+    return fail(PG_ERR_INVALID_ARG, "positions and inv_freq must be 4-byte aligned");
+  if (!sections) return fail(PG_ERR_INVALID_ARG, "null sections");
+  long long sum = 0;
+  for (int x = 0; x < A; ++x) {
+    if (sections[x] < 0) return fail(PG_ERR_INVALID_ARG, "sections must not be negative");
+    a.sections[x] = sections[x];
+    sum += sections[x];
+  }
+  if (sum != half) return fail(PG_ERR_INVALID_ARG, "sections must add up to the %lld entries of inv_freq", half);
+  if (interleaved)  // axis x > 0 takes the entries x, x + A, ..: sections[x] of them have to be there
+    for (int x = 1; x < A; ++x)
+      if (sections[x] > 0 && (long long)(sections[x] - 1) * A + x >= half)
+        return fail(PG_ERR_INVALID_ARG, "interleaved sections: axis %d has no %d-th entry", x, sections[x]);
+  a.pos = static_cast<const int32_t*>(positions->data);
+  a.pos_sa = positions->stride[0];
+  a.inv_freq = static_cast<const float*>(inv_freq->data);
+  a.T = (int)T;
+  a.rot = (int)half * 2;
+  a.axes = (int)A;
+  a.interleaved = interleaved != 0;
+  a.adjacent = adjacent != 0;
+  if (T == 0) {
+    t_last_error.clear();
+    return PG_OK;
+  }
+  DeviceState* ds = nullptr;
+  if ((st = current_device(&ds))) return st;
+  const cudaError_t e = launch_rope(a, ds->sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
+  t_last_error.clear();
   return PG_OK;
 }
 

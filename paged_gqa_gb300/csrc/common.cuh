@@ -28,6 +28,15 @@ constexpr int kPrefillRows = 128;     // rows of a prefill block
 constexpr int kSlotRows = 128;        // rows per partial-result slot
 constexpr int kNumClasses = 2;        // 0 = verify, 1 = prefill
 
+// 4-bit caches: 256 values of a (token, kv head) are 128 bytes of e2m1 codes and 16 e4m3
+// scales, one per 16 values; a page of one kv head is P * kFp4Row contiguous bytes (fp4.cuh).
+constexpr int kFp4Row = 144;
+constexpr int kFp4Codes = 128;        // code bytes of a row
+constexpr int kFp4Group = 16;         // values that share a scale
+constexpr int kFp4Block = 16;         // tokens of a block of a V page
+constexpr int kFp4BlockBytes = kFp4Block * kFp4Row;
+constexpr int kFp4BlockScales = kFp4Block * kFp4Codes;  // offset of a V block's scales
+
 // How a tcgen05 attention kernel stages Q (its template argument).
 constexpr int kQSplit = 0;  // bf16 Q as e4m3 hi + lo parts under a per-tile power-of-two scale
 constexpr int kQGiven = 1;  // e4m3 Q as given (its descale folded into the score scale)
@@ -95,6 +104,7 @@ struct WorkItem {
 struct Problem {
   int num_seqs, T, Hq, Hkv, G, P, W, NB;
   int q_is_fp8, kv_is_fp8;
+  int kv_is_fp4;           // 4-bit caches: the k_ / v_ strides are bytes and *_sp is unused
   int q_cast;              // bf16 Q quantised per tensor inside the call (kQCast)
   int q_amax_parts;        // entries of Pointers::q_amax (q_cast only)
   // strides in elements

@@ -62,6 +62,44 @@ int sparse_tc_min_keys();
 int q_amax_parts(int sms);
 cudaError_t launch_q_amax(const Problem& p, const Pointers& ptr, float* parts, cudaStream_t stream);
 
+// Arguments of the 4-bit cache's write and read (fp4_cache.cu).
+struct Fp4CacheArgs {
+  // bf16 rows [T, Hkv, 256]: the new tokens of a write, the destination of a read
+  uint16_t* kx;
+  uint16_t* vx;
+  long long kx_st, kx_sh, vx_st, vx_sh;  // elements
+  uint8_t* kc;
+  uint8_t* vc;
+  long long kc_sb, kc_sh, vc_sb, vc_sh;  // bytes
+  const int32_t* bt;
+  long long bt_stride;
+  const int32_t* seq_lens;
+  const int32_t* qsl;
+  int num_seqs, T, Hkv, P, p_shift, W, NB;
+  int window;              // tokens per warp (set by the launcher)
+  float k_mul, v_mul;      // 1 / descale (write) or descale (read)
+  uint32_t* err;
+};
+cudaError_t launch_fp4_cache_write(const Fp4CacheArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_fp4_cache_read(const Fp4CacheArgs& a, int sms, cudaStream_t stream);
+
+// Arguments of the rotary positions (rope.cu).
+constexpr int kRopeMaxAxes = 4;
+struct RopeArgs {
+  const uint16_t* x[2];    // q [T, heads[0], 256], k [T, heads[1], 256], bf16
+  uint16_t* y[2];
+  long long x_st[2], x_sh[2], y_st[2], y_sh[2];  // elements
+  int heads[2];
+  int in_place[2];         // y[i] is x[i]: what is not rotated stays as it is
+  const int32_t* pos;      // [axes, T]
+  long long pos_sa;
+  const float* inv_freq;   // [rot / 2]
+  int T, rot, axes;
+  int sections[kRopeMaxAxes];
+  int interleaved, adjacent;
+};
+cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t stream);
+
 // Warp-level MMA (mma.sync, tf32) kernel for one class's items; any dtype mix.
 cudaError_t launch_portable(const Problem& p, const Pointers& ptr, const ClassPlan& cp,
                             int block_rows, cudaStream_t stream);

@@ -11,9 +11,11 @@
 // block table into shared memory ("Optimize Qwen3.5 MTP unified attention on gfx950":
 // the kv tile is loaded once and reused by all q_len x G rows of the kv head).
 // Online softmax per row with quad shuffles; split pieces write partial results that
-// the last piece merges.
+// the last piece merges. The kFp4 instance gathers 4-bit K/V (code times scale is exact in
+// tf32 too): the simplest form of that attention, and the cross-check of its tcgen05 kernel.
 #include "common.cuh"
 #include "device_util.cuh"
+#include "fp4.cuh"
 #include "plan.cuh"
 #include "tc_kernels.cuh"
 
@@ -79,8 +81,30 @@ __device__ __forceinline__ void load32(float* dst, const void* src, bool fp8, fl
   }
 }
 
+// Values [32 seg, 32 seg + 32) of one token of a 4-bit page, times their scales, as fp32.
+__device__ __forceinline__ void load32_fp4(float* dst, const uint8_t* page, int slot, int seg, bool is_v,
+                                           bool valid) {
+  if (!valid) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  const uint8_t* blk = page + (slot / kFp4Block) * kFp4BlockBytes;
+  const int tok = slot % kFp4Block;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int byte = seg * 16 + i, grp = seg * 2 + i / 8;
+    const uint32_t code = is_v ? blk[byte * kFp4Block + tok] : page[slot * kFp4Row + byte];
+    const uint32_t sc = is_v ? blk[kFp4BlockScales + grp * kFp4Block + tok] : page[slot * kFp4Row + kFp4Codes + grp];
+    const float2 x = fp4::code_pair(code);
+    const float s = fp4::scale_value(sc);
+    *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(x.x * s, x.y * s);
+  }
+}
+
 }  // namespace
 
+template <bool kFp4>
 __global__ void __launch_bounds__(kPThreads, 1)
 portable_attn_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   extern __shared__ __align__(16) float smem[];
@@ -145,14 +169,24 @@ portable_attn_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             valid = false;
           } else {
             const int r = j % p.P;
-            koff = ((size_t)blk * p.k_sb + (size_t)r * p.k_sp + (size_t)rb.kvh * p.k_sh + seg * 32) * esz_kv;
-            voff = ((size_t)blk * p.v_sb + (size_t)r * p.v_sp + (size_t)rb.kvh * p.v_sh + seg * 32) * esz_kv;
+            if (kFp4) {
+              koff = (size_t)blk * p.k_sb + (size_t)rb.kvh * p.k_sh;
+              voff = (size_t)blk * p.v_sb + (size_t)rb.kvh * p.v_sh;
+            } else {
+              koff = ((size_t)blk * p.k_sb + (size_t)r * p.k_sp + (size_t)rb.kvh * p.k_sh + seg * 32) * esz_kv;
+              voff = ((size_t)blk * p.v_sb + (size_t)r * p.v_sp + (size_t)rb.kvh * p.v_sh + seg * 32) * esz_kv;
+            }
           }
         }
-        load32(Ks + key * kPitch + seg * 32, static_cast<const char*>(ptr.k) + koff, p.kv_is_fp8,
-               valid ? 0.f : 1.f);
-        load32(Vs + key * kPitch + seg * 32, static_cast<const char*>(ptr.v) + voff, p.kv_is_fp8,
-               valid ? 0.f : 1.f);
+        if (kFp4) {
+          load32_fp4(Ks + key * kPitch + seg * 32, static_cast<const uint8_t*>(ptr.k) + koff, j % p.P, seg, false, valid);
+          load32_fp4(Vs + key * kPitch + seg * 32, static_cast<const uint8_t*>(ptr.v) + voff, j % p.P, seg, true, valid);
+        } else {
+          load32(Ks + key * kPitch + seg * 32, static_cast<const char*>(ptr.k) + koff, p.kv_is_fp8,
+                 valid ? 0.f : 1.f);
+          load32(Vs + key * kPitch + seg * 32, static_cast<const char*>(ptr.v) + voff, p.kv_is_fp8,
+                 valid ? 0.f : 1.f);
+        }
       }
       __syncthreads();
       if (!warp_active) continue;
@@ -287,14 +321,18 @@ portable_attn_kernel(Problem p, Pointers ptr, ClassPlan cp) {
 cudaError_t launch_portable(const Problem& p, const Pointers& ptr, const ClassPlan& cp, int block_rows,
                             cudaStream_t stream) {
   (void)block_rows;
-  static bool attr_set = false;  // per process; the attribute is per function, not per device
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(portable_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kPSmemBytes);
+  // per device: the attribute belongs to the function on the device that is current
+  static bool attr_set[2][64] = {};
+  auto kern = p.kv_is_fp4 ? portable_attn_kernel<true> : portable_attn_kernel<false>;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  bool* done = dev >= 0 && dev < 64 ? &attr_set[p.kv_is_fp4 ? 1 : 0][dev] : nullptr;
+  if (!done || !*done) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPSmemBytes);
     if (e != cudaSuccess) return e;
-    attr_set = true;
+    if (done) *done = true;
   }
-  cudaError_t e = launch_pdl(false, portable_attn_kernel, cp.num_ctas, kPThreads, kPSmemBytes, stream, p, ptr, cp);
+  cudaError_t e = launch_pdl(false, kern, cp.num_ctas, kPThreads, kPSmemBytes, stream, p, ptr, cp);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
