@@ -603,16 +603,36 @@ int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, 
   ClassPlan cp[kNumClasses];
   for (int c = 0; c < kNumClasses; ++c) cp[c] = class_plan(L, c, static_cast<char*>(ws));
   int64_t plan_info[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  int launched = 0, used = 0;
+  const int path = g_path.load();
+  const bool tc = path != 1;  // the tcgen05 kernel; under path 1 the warp-level one
   p.call_tag = next_call_tag();
-  p.fused_verify = 0;
-  cudaError_t e = launch_plan(p, ptr, cp[0], cp[1], true, false, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "plan launch");
-  ++launched;
+  // As in run(): the verify class plans itself where its blocks fit a CTA's list, unless the
+  // one sequence is all prefill.
+  const long long max_tiles = ((long long)p.W * p.P + kTileKeys - 1) / kTileKeys;
+  const bool single_prefill = p.num_seqs == 1 && (long long)p.T * p.G > kVerifyRows;
+  p.fused_verify = tc && path != 3 && !single_prefill && (long long)p.num_seqs * p.Hkv <= kFusedMaxBlocks &&
+                   max_tiles < (1 << 16) && (long long)p.num_seqs * p.Hkv * (max_tiles + fixed_cost(0)) < (1LL << 31);
+  int launched = 0, used = 0;
+  cudaError_t e;
   for (int c = 0; c < kNumClasses; ++c) {
-    e = launch_portable(p, ptr, cp[c], c == 0 ? kVerifyRows : kPrefillRows, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "4-bit attention launch");
-    used |= 8 << c;
+    // the plan kernel goes before the verify class, or after it where that plans itself
+    const bool plan_here = c == (p.fused_verify ? 1 : 0);
+    if (plan_here) {
+      e = launch_plan(p, ptr, cp[0], cp[1], !p.fused_verify, p.fused_verify, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "plan launch");
+      ++launched;
+    }
+    // no sequence of at most kVerifyRows rows in all can be of the prefill class
+    if (c == 1 && (long long)p.T * p.G <= kVerifyRows) break;
+    if (tc) {
+      if (launch_fp4_tc(p, ptr, cp[c], c, stream, c == 1) < 0)
+        return fail(PG_ERR_CUDA, "tcgen05 4-bit launch failed: %s", tc_last_error());
+      used |= 2 << c;
+    } else {
+      e = launch_portable(p, ptr, cp[c], c == 0 ? kVerifyRows : kPrefillRows, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "4-bit attention launch");
+      used |= 8 << c;
+    }
     ++launched;
   }
   plan_info[0] = cp[0].num_ctas;

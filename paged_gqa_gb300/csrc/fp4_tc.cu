@@ -1,0 +1,966 @@
+// fp4_tc.cu -- tcgen05 (TMEM) attention kernel over a 4-bit paged KV cache (fp4.cuh), bf16 Q,
+// for verify blocks (kN = 64 rows: single tokens and MTP / speculative verify) and prefill
+// blocks (kN = 128 rows), bottom-right causal.
+//
+// Both products take the cache as their A operand, with up to kN query rows as N:
+//   S^T[key, row] = K Q^T          A = K   [128 keys, 256 d]
+//   O^T[d, row] += V^T P^T         A = V^T [256 d, 128 keys], as two 128-lane tiles
+// so the MMA's 128 lanes are full however few rows a block has, its cost follows the rows
+// (N = rows rounded up to 16), and A can come from TMEM: the packed pages (144 bytes per key)
+// go from HBM to shared memory by bulk copies, eight warps widen them to f16 (code * scale,
+// exact) and store them with tcgen05.st, and no widened value ever passes through shared memory.
+// (Through it, 1 KB per key written and read again would cost 16 of the ~12 cycles per key
+// that a CTA has at full HBM bandwidth.) Widening thread t owns TMEM lane t: key t of the
+// tile for K (its row's bytes are d pairs, K's order), code byte t of every key for V, i.e. d =
+// 2t for tile 0 and 2t + 1 for tile 1; a V page's blocks hold 16 keys of a byte contiguously.
+//
+// The widened operand passes through a ring of 64-column TMEM buffers in chunks that one of
+// the MMA issuers frees as a whole: 128 d of the 128 keys for K, 64 keys of both tiles for V, in
+// the order K(0) K(1) V(0) K(2) V(1) ..: while the softmax works on S(g), the tensor core has
+// K(g + 1) to multiply and the widening warps V(g) to fetch.
+//
+// Q is staged in f16 with a power of two per row (its largest value to [2^14, 2^15)): a bf16
+// value has 8 significant bits, so everything within 2^-28 of the row's largest is exact, and
+// the power goes into the row's score scale. P = 2^(s - m + 4) is rounded to f16 (2^-11), the
+// row sums take it before that rounding. The softmax, its lazy rescale, the split-KV pieces and
+// their merge follow the FP8 verify kernel (verify_tc.cu): keys on lanes, rows on columns.
+//
+// Warp roles (1024 threads): warp 0 S issuer (+ TMEM owner), warp 1 P.V issuer, warps 2, 28,
+// 29 K copies, warps 3, 30, 31 V copies, warps 4-19 softmax and epilogue (row group (w - 4) / 4
+// owns kN / 4 rows), warps 20-27 widening (lane quarter w % 4, half (w - 20) / 4 of a chunk).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdio>
+
+#include "common.cuh"
+#include "device_util.cuh"
+#include "fp4.cuh"
+#include "self_plan.cuh"
+#include "tc_kernels.cuh"
+#include "tc_util.cuh"
+
+namespace pgqa {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 1024;
+constexpr int kSoftWarps = 16, kSoftWarp0 = 4;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kWideWarps = 8, kWideWarp0 = 20;
+constexpr int kProdPerOp = 3;
+constexpr float kTau = 4.f;         // rescale when a score exceeds the reference by 2^kTau
+constexpr float kSigma = 4.f;       // P is scaled by 2^kSigma (at most 2^8; f16 holds 2^-24)
+constexpr float kMInit = -1.0e30f;  // reference of a row before its first key
+
+// Registers: 1024 threads start with 64 each; the warpgroups' shares below add up to that.
+constexpr int kLaunchRegs = 64, kOtherRegs = 40;
+
+constexpr uint32_t kTile = kTileKeys * kFp4Row;  // packed bytes of a tile of K or V (18 KB)
+constexpr uint32_t kChunkCols = 64;              // TMEM columns of a ring buffer
+
+template <int kN>
+struct Cfg {
+  static constexpr int kCols = kN / 4;              // rows per softmax thread
+  static constexpr int kSoftRegs = kN == 64 ? 72 : 80, kWideRegs = kN == 64 ? 72 : 56;
+  static_assert(4 * kSoftRegs + 2 * kWideRegs + 2 * kOtherRegs == 8 * kLaunchRegs, "register split");
+  static constexpr int kKStages = kN == 64 ? 3 : 2, kVStages = kN == 64 ? 4 : 2;
+  static constexpr int kSBufs = kN == 64 ? 2 : 1;
+  static constexpr int kRing = kN == 64 ? 4 : 2;    // TMEM ring buffers
+  static constexpr uint32_t kColS = 0, kColO = 128, kColA = 128 + 2 * kN;
+  static_assert(kSBufs * kN <= 128 && kColA + kRing * kChunkCols <= 512, "TMEM columns");
+  static constexpr uint32_t kQQuarter = kN * 128;   // [kN rows][64 d] f16, 128-byte swizzle
+  static constexpr uint32_t kPBlock = kTileKeys * 128;       // [128 keys][64 rows] f16
+  static constexpr uint32_t kPBuf = kPBlock * (kN / 64);
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffP = kOffQ + 4 * kQQuarter;
+  static constexpr uint32_t kOffK = kOffP + 2 * kPBuf;
+  static constexpr uint32_t kOffV = kOffK + kKStages * kTile;
+  static constexpr uint32_t kOffMisc = kOffV + kVStages * kTile;
+  static_assert(2 * kPBuf >= kN * kHeadDim * 2, "a split piece's f16 partial fits the P buffers");
+};
+
+template <int kN, bool kFused>
+struct Misc {
+  using C = Cfg<kN>;
+  alignas(16) float m[2][kN];
+  alignas(16) float mo[2][kN];   // kSigma - m
+  alignas(16) float cs[2][kN];   // score scale of the row (log2 units, Q's power of two removed)
+  alignas(16) float red[4][kN];
+  alignas(16) float alpha[kN];
+  alignas(16) int lim[2][kN];
+  alignas(16) long long out_off[2][kN];
+  alignas(16) float merge_w[kMergeMaxSplits * kSlotRows];
+  alignas(16) float lse_stage[kN];
+  alignas(8) uint64_t k_full[C::kKStages], k_empty[C::kKStages], v_full[C::kVStages], v_empty[C::kVStages];
+  uint64_t ak_full[C::kRing], av_full[C::kRing], a_free[C::kRing];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t q_full, q_free, o_ready, o_free, drain[2], merge_full;
+  uint64_t never;  // no thread ever arrives (the failure-path test waits on it)
+  uint32_t tmem_base;
+  int abort_flag;
+  int merge_flag;
+  int fcount;
+  int4 fitem[kFused ? kFusedMaxBlocks : 1];
+  int4 fseq[kFused ? kFusedMaxBlocks : 1];
+};
+
+template <int kN, bool kFused>
+constexpr size_t smem_bytes() {
+  return Cfg<kN>::kOffMisc + sizeof(Misc<kN, kFused>) + 1024;
+}
+static_assert(smem_bytes<64, true>() <= 232448 && smem_bytes<128, false>() <= 232448, "shared memory of one CTA");
+static_assert(sizeof(self_plan::Scratch) <= Cfg<64>::kKStages * kTile, "the self-plan scratch fits the K stages");
+
+struct Item {
+  int block, seq, kvh, row0, nrows, nsplit, split, slot_base;
+  int tile_begin, ntiles, kv_hi;
+  int q0, qn, L;
+};
+
+template <int kN, bool kFused>
+__device__ __forceinline__ Item load_item(const Problem& p, const ClassPlan& cp, const Pointers& ptr,
+                                          const Misc<kN, kFused>& ms, int it) {
+  Item r;
+  if (kFused) {
+    const self_plan::Piece f = self_plan::unpack(p, ms.fitem[it]);
+    const int4 sq = ms.fseq[it];
+    r.block = f.block;
+    r.seq = f.seq;
+    r.kvh = f.kvh;
+    r.tile_begin = f.tile_begin;
+    r.ntiles = f.ntiles;
+    r.split = f.split;
+    r.nsplit = f.nsplit;
+    r.slot_base = f.slot_base;
+    r.q0 = sq.x;
+    r.qn = sq.y;
+    r.L = sq.z;
+    r.row0 = 0;
+    r.nrows = r.qn * p.G;
+    r.kv_hi = min((r.tile_begin + r.ntiles) * kTileKeys, r.L);
+  } else {
+    const WorkItem w = cp.items[it];
+    const RowBlock b = cp.blocks[w.block];
+    r.block = w.block;
+    r.seq = b.seq;
+    r.kvh = b.kvh;
+    r.row0 = b.row0;
+    r.nrows = b.nrows;
+    r.nsplit = b.nsplit;
+    r.split = w.split;
+    r.slot_base = b.slot_base;
+    r.tile_begin = w.tile_begin;
+    r.ntiles = w.tile_end - w.tile_begin;
+    r.kv_hi = min(w.tile_end * kTileKeys, b.kv_end);
+    r.q0 = ptr.qsl[b.seq];
+    r.qn = ptr.qsl[b.seq + 1] - r.q0;
+    r.L = ptr.seq_lens[b.seq];
+  }
+  return r;
+}
+
+// Where the first chunk of K(g) and of V(g) lies in the ring (the second one in the buffer after
+// it), g counting a CTA's tiles, and which phase of its barrier that is. The order K(0) K(1)
+// V(0) K(2) V(1) .. makes K(0) and the last V exceptions where the ring has four buffers. K and V
+// have a barrier each per buffer: an issuer has to wait for every phase of a barrier in turn (a
+// parity wait cannot tell a phase from the one two before it), and it only follows its own
+// operand.
+struct Place {
+  uint32_t buf, phase;
+};
+template <int kN>
+__device__ __forceinline__ Place k_place(uint32_t g) {
+  if (Cfg<kN>::kRing == 2) return Place{0, g};
+  return g ? Place{2, g - 1} : Place{0, 0};
+}
+template <int kN>
+__device__ __forceinline__ Place v_place(uint32_t g, bool last) {
+  if (Cfg<kN>::kRing == 2) return Place{0, g};
+  return last ? Place{2, 0} : Place{0, g};
+}
+
+// Byte mask of tokens 4w .. 4w + 3 of a 16-token block whose first n tokens are there.
+__device__ __forceinline__ uint32_t token_mask(int n, int w) {
+  const int k = n - 4 * w;
+  return k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
+}
+
+}  // namespace
+
+template <int kN, bool kFused>
+__global__ void __launch_bounds__(kThreads, 1)
+fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
+  using C = Cfg<kN>;
+  constexpr int kCols = C::kCols;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Misc<kN, kFused>& ms = *reinterpret_cast<Misc<kN, kFused>*>(smem + C::kOffMisc);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &ms.abort_flag;
+  auto bar = [&](const uint64_t& b) { return smem_u32(&b); };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int item_begin = 0, item_end = 0;
+  self_plan::Scratch& fs = *reinterpret_cast<self_plan::Scratch*>(smem + C::kOffK);
+  if (kFused) {
+    self_plan::load(p, ptr, fs);  // the set-up below overlaps these reads
+  } else {
+    item_begin = cp.cta_item_begin[blockIdx.x];
+    item_end = cp.cta_item_begin[blockIdx.x + 1];
+    if (item_begin >= item_end) return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kKStages; ++s) {
+      mbar_init(bar(ms.k_full[s]), kProdPerOp);
+      mbar_init(bar(ms.k_empty[s]), kWideWarps);
+    }
+    for (int s = 0; s < C::kVStages; ++s) {
+      mbar_init(bar(ms.v_full[s]), kProdPerOp);
+      mbar_init(bar(ms.v_empty[s]), kWideWarps);
+    }
+    for (int b = 0; b < C::kRing; ++b) {
+      mbar_init(bar(ms.ak_full[b]), kWideWarps);
+      mbar_init(bar(ms.av_full[b]), kWideWarps);
+      mbar_init(bar(ms.a_free[b]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(ms.s_full[b]), 1);
+      mbar_init(bar(ms.s_free[b]), kSoftThreads);
+      mbar_init(bar(ms.p_full[b]), kSoftThreads);
+      mbar_init(bar(ms.pv_done[b]), 1);
+    }
+    mbar_init(bar(ms.q_full), kSoftThreads);
+    mbar_init(bar(ms.q_free), 1);
+    mbar_init(bar(ms.o_ready), 1);
+    mbar_init(bar(ms.o_free), kSoftThreads);
+    mbar_init(bar(ms.drain[0]), 1);
+    mbar_init(bar(ms.drain[1]), 1);
+    mbar_init(bar(ms.merge_full), 1);
+    mbar_init(bar(ms.never), 1);
+    ms.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&ms.tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (kFused) {
+    __syncthreads();  // the sequences are staged
+    if (warp == 1) self_plan::plan_warp(p, fs, cp.num_ctas, lane, ms.fitem, ms.fseq, &ms.fcount);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem_base;
+  if (kFused) {
+    item_end = ms.fcount;
+    if (item_end == 0) {  // no range or no tile in it: give the columns back and leave
+      if (warp == 0) tmem_dealloc(tmem, 512);
+      return;
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int wg = warp >> 2;
+  if (wg >= 1 && wg <= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
+    // ------------------------------------------------------------ softmax + epilogue
+    const int sw = warp - kSoftWarp0;      // 0..15
+    const int gi = sw * 32 + lane;         // 0..511
+    const int q4 = warp & 3;               // TMEM lane quarter
+    const int rg = sw >> 2;                // row group
+    const int c0 = rg * kCols;             // first row (column) this thread owns
+    const int group_bar = 3 + rg;          // named barrier of the row group's four warps
+    const int ti = q4 * 32 + lane;         // TMEM lane: key of the tile; for O^T, d = 2 ti and 2 ti + 1
+    const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
+    float l[kCols];
+#pragma unroll
+    for (int n = 0; n < kCols; ++n) l[n] = 0.f;
+    bool bad = false;
+    uint32_t merge_phase = 0;
+    // Failure-path test: every softmax thread's bounded wait on a barrier nothing arrives on
+    // runs out; they skip the items, no Q is published, and every other role gives up and
+    // drains what it has in flight.
+    const bool stalled = p.stall_test_ns && !mbar_wait(bar(ms.never), 0, abort_flag, ptr.err, p.stall_test_ns);
+    if (!stalled) {
+      const unsigned long long ctag = gi == 0 ? split_tag(p, cp) : 0ull;
+
+      auto q_prep = [&](const Item& I, int ii) {
+        const int pi = ii & 1;
+        if (ii >= 1 && !mbar_wait(bar(ms.q_free), (ii - 1) & 1, abort_flag, ptr.err)) bad = true;
+        if (gi < kN) {
+          const int n = gi;
+          const bool real = n < I.nrows;
+          const RowMap m = map_row(I.row0 + n, p.G, I.kvh);
+          ms.lim[pi][n] = real ? I.L - I.qn + m.t : -1;
+          ms.out_off[pi][n] = real ? (long long)(I.q0 + m.t) * p.o_st + (long long)m.h * p.o_sh : 0;
+          // padding rows: a finite reference, so their (discarded) scores never vote
+          ms.m[pi][n] = real ? kMInit : 0.f;
+          ms.mo[pi][n] = kSigma - ms.m[pi][n];
+        }
+        // A warp takes whole rows (32 lanes of 16 bytes), four at a time.
+#pragma unroll 1
+        for (int k0 = 0; k0 < kN / kSoftWarps; k0 += 4) {
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = (k0 + k) * kSoftWarps + sw;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (r < I.nrows) {
+              const RowMap m = map_row(I.row0 + r, p.G, I.kvh);
+              v[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(ptr.q) +
+                                                     (long long)(I.q0 + m.t) * p.q_st + (long long)m.h * p.q_sh + lane * 8);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = (k0 + k) * kSoftWarps + sw;
+            uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                    __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+            top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+            // 2^(141 - e) takes a row whose largest value has exponent field e to [2^14, 2^15)
+            // (at most 2^127: a row below 2^-113 stays smaller, and exact all the same)
+            const int e = max((int)(top >> 7), 14);
+            const float up = __uint_as_float((uint32_t)(268 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+            const int qd = lane >> 3, cc = lane & 7;
+            *reinterpret_cast<uint4*>(smem + C::kOffQ + qd * C::kQQuarter + r * 128 + ((cc ^ (r & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+            if (lane == 0) ms.cs[pi][r] = ldexpf(p.score_scale_log2, e - 141);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(ms.q_full));
+      };
+
+      int ii = 0;
+      uint32_t g = 0;
+      q_prep(load_item<kN, kFused>(p, cp, ptr, ms, item_begin), 0);
+      for (int it = item_begin; it < item_end; ++it, ++ii) {
+        const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
+        const int pi = ii & 1;
+        named_barrier(1, kSoftThreads);  // q_prep's shared writes are visible
+        const int n16 = (I.nrows + 15) & ~15;
+        const int min_lim = I.L - I.qn + map_row(I.row0, p.G, I.kvh).t;
+        // A failed wait (timeout or abort) does not leave the loops: every later wait then
+        // fails fast, so all softmax warps still pass the same barriers and finish.
+        for (int j = 0; j < I.ntiles; ++j, ++g) {
+          const int sb = g % C::kSBufs, pb = g & 1;
+          const int key0 = (I.tile_begin + j) * kTileKeys;
+          const int key = key0 + ti;
+          const bool need_mask = (key0 + kTileKeys > I.kv_hi) || (key0 + kTileKeys - 1 > min_lim);
+          const bool kin = key < I.kv_hi;
+          if (!mbar_wait(bar(ms.s_full[sb]), (g / C::kSBufs) & 1, abort_flag, ptr.err)) bad = true;
+          tc_fence_after();
+          bool p_free = false, o_free = false;  // the waits before P is written / O is rescaled are done
+#pragma unroll
+          for (int cb = 0; cb < kCols; cb += 16) {
+            const int cc = c0 + cb;  // 16 rows
+            const bool active = cc < n16;  // the same in the row group's four warps
+            const uint32_t s_addr = tmem + lane_addr + C::kColS + sb * kN + cc;
+            float t[16];
+            bool rescale = false;
+            if (active) {
+              tmem_ld16(s_addr, t);
+              tmem_wait_ld();
+              // x = s c - m + sigma: the exponent of P
+              float xmax = -INFINITY;
+#pragma unroll
+              for (int n = 0; n < 16; n += 4) {
+                const float4 o4 = *reinterpret_cast<const float4*>(&ms.mo[pi][cc + n]);
+                const float4 s4 = *reinterpret_cast<const float4*>(&ms.cs[pi][cc + n]);
+                t[n] = fmaf(t[n], s4.x, o4.x);
+                t[n + 1] = fmaf(t[n + 1], s4.y, o4.y);
+                t[n + 2] = fmaf(t[n + 2], s4.z, o4.z);
+                t[n + 3] = fmaf(t[n + 3], s4.w, o4.w);
+              }
+              if (need_mask) {
+#pragma unroll
+                for (int n = 0; n < 16; n += 4) {
+                  const int4 l4 = *reinterpret_cast<const int4*>(&ms.lim[pi][cc + n]);
+                  if (!(kin && key <= l4.x)) t[n] = -INFINITY;
+                  if (!(kin && key <= l4.y)) t[n + 1] = -INFINITY;
+                  if (!(kin && key <= l4.z)) t[n + 2] = -INFINITY;
+                  if (!(kin && key <= l4.w)) t[n + 3] = -INFINITY;
+                }
+              }
+#pragma unroll
+              for (int n = 0; n < 16; n += 2) xmax = max3f(xmax, t[n], t[n + 1]);
+              // does any score of the row group exceed its row's reference by more than 2^kTau?
+              rescale = barrier_or(group_bar, 128, xmax > kTau + kSigma);
+              if (rescale) {
+                // The raw scores again (x may have lost s against a -1e30 reference): the exact
+                // tile maximum of s c per row, then the new reference.
+                tmem_ld16(s_addr, t);
+                tmem_wait_ld();
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                  const bool vis = !need_mask || (kin && key <= ms.lim[pi][cc + n]);
+                  t[n] = vis ? t[n] * ms.cs[pi][cc + n] : -INFINITY;
+                  const float r = warp_max(t[n]);
+                  if (lane == n) ms.red[q4][cc + n] = r;
+                }
+                named_barrier(group_bar, 128);
+                if (q4 == 0 && lane < 16) {
+                  const int n = cc + lane;
+                  const float mt = fmaxf(fmaxf(ms.red[0][n], ms.red[1][n]), fmaxf(ms.red[2][n], ms.red[3][n]));
+                  const float m_old = ms.m[pi][n];
+                  const float mn = fmaxf(m_old, mt);
+                  ms.alpha[n] = ex2(m_old - mn);
+                  ms.m[pi][n] = mn;
+                  ms.mo[pi][n] = kSigma - mn;
+                }
+                named_barrier(group_bar, 128);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                  t[n] += ms.mo[pi][cc + n];
+                  l[cb + n] *= ms.alpha[cc + n];
+                }
+              }
+            }
+            if (cb + 16 == kCols) {  // S is read for the last time above
+              tc_fence_before();
+              mbar_arrive(bar(ms.s_free[sb]));
+            }
+            uint32_t pk[8];
+            if (active) {
+#pragma unroll
+              for (int n = 0; n < 16; n += 2) {
+                const float a = ex2(t[n]), b = ex2(t[n + 1]);
+                l[cb + n] += a;
+                l[cb + n + 1] += b;
+                pk[n / 2] = pack_f16x2(a, b);
+              }
+            }
+            // P buffer g & 1 is free once P.V(g-2) has completed; O^T may be rescaled once
+            // P.V(g-1) has. Each barrier's next phase needs a P these threads have not written
+            // yet, so a late parity wait cannot mistake it for the phase it waits for.
+            if (!p_free) {
+              if (g >= 2 && !mbar_wait(bar(ms.pv_done[pb]), ((g >> 1) - 1) & 1, abort_flag, ptr.err)) bad = true;
+              p_free = true;
+            }
+            if (rescale && j > 0) {
+              if (!o_free && !mbar_wait(bar(ms.pv_done[pb ^ 1]), ((g - 1) >> 1) & 1, abort_flag, ptr.err)) bad = true;
+              o_free = true;
+              tc_fence_after();
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                float v[16];
+                const uint32_t a = tmem + lane_addr + C::kColO + h * kN + cc;
+                tmem_ld16(a, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= ms.alpha[cc + i];
+                tmem_st16(a, v);
+              }
+              tmem_wait_st();
+            }
+            if (active) {
+              // P^T row of key ti (128-byte swizzle): this thread's 16 rows
+              uint8_t* row = smem + C::kOffP + pb * C::kPBuf + (cc >> 6) * C::kPBlock + ti * 128;
+              const int ch = (cc & 63) >> 3;
+              *reinterpret_cast<uint4*>(row + ((ch ^ (ti & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (ti & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            }
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          mbar_arrive(bar(ms.p_full[pb]));
+        }
+        // Q of the next item while this item's last P.V runs
+        if (it + 1 < item_end) q_prep(load_item<kN, kFused>(p, cp, ptr, ms, it + 1), ii + 1);
+
+        // ---------------------------------------------------------- epilogue
+        if (!mbar_wait(bar(ms.o_ready), ii & 1, abort_flag, ptr.err)) bad = true;
+        tc_fence_after();
+        // row sums over the 128 key lanes: warp reduce-scatter, then across the quarters
+#pragma unroll
+        for (int cb = 0; cb < kCols; cb += 16) {
+          float v[16];
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            v[n] = l[cb + n];
+            l[cb + n] = 0.f;
+          }
+#pragma unroll
+          for (int w = 8, o = 16; o >= 2; w >>= 1, o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int i = 0; i < w; ++i) {
+              const float send = up ? v[i] : v[i + w];
+              const float keep = up ? v[i + w] : v[i];
+              v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+          }
+          v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+          // lanes 2r and 2r + 1 now hold row c0 + cb + r
+          if ((lane & 1) == 0) ms.red[q4][c0 + cb + (lane >> 1)] = v[0];
+        }
+        named_barrier(1, kSoftThreads);
+        const bool split = I.nsplit > 1;
+        const int slot = I.slot_base + I.split;
+        // 1 / (row sum), times v_descale unless this is a split piece (the merge applies it then);
+        // and a split piece's log2-sum-exp
+        if (gi < kN) {
+          const float lr = ms.red[0][gi] + ms.red[1][gi] + ms.red[2][gi] + ms.red[3][gi];
+          ms.alpha[gi] = lr > 0.f ? __fdividef(split ? 1.f : p.out_scale, lr) : lr == 0.f ? 0.f : lr;  // NaN stays
+          if (split) ms.lse_stage[gi] = lr > 0.f ? ms.m[pi][gi] - kSigma + log2f(lr) : lr == 0.f ? -INFINITY : lr;
+        }
+        named_barrier(1, kSoftThreads);  // (the next item's barrier keeps its rescales off red and alpha)
+#pragma unroll 1
+        for (int cb = 0; cb < kCols; cb += 16) {
+          const int cc = c0 + cb;
+          if (cc >= I.nrows) break;  // warp-uniform
+          float v[16], w[16];
+          tmem_ld16(tmem + lane_addr + C::kColO + cc, v);
+          tmem_ld16(tmem + lane_addr + C::kColO + kN + cc, w);
+          tmem_wait_ld();
+          if (split) {
+            uint32_t* stage = reinterpret_cast<uint32_t*>(smem + C::kOffP);  // rows of 128 f16 pairs
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float inv = ms.alpha[cc + i];
+              stage[(cc + i) * (kHeadDim / 2) + ti] = pack_f16x2(v[i] * inv, w[i] * inv);
+            }
+          } else {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(ptr.out) + 2 * ti;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (cc + i < I.nrows) {
+                const float inv = ms.alpha[cc + i];
+                *reinterpret_cast<uint32_t*>(out + ms.out_off[pi][cc + i]) = pack_bf16x2(v[i] * inv, w[i] * inv);
+              }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bar(ms.o_free));
+        if (split) {
+          // The f16 partial and its log2-sum-exp leave through the P buffers (every P.V of the
+          // item has completed) by two bulk stores from one thread, before the counter moves.
+          fence_proxy_async_smem();
+          named_barrier(1, kSoftThreads);
+          if (gi == 0) {
+            const unsigned long long seen = split_peek(cp.counters + I.block);
+            bulk_store(slot_o(cp, slot), sbase + C::kOffP, (uint32_t)I.nrows * kHeadDim * 2u);
+            bulk_store(slot_lse(cp, slot), smem_u32(ms.lse_stage), kN * 4u);
+            bulk_commit();
+            bulk_wait_all();  // the partial is in global memory before the split counter moves
+            fence_proxy_async_global();
+            fence_acq_rel_gpu();
+            ms.merge_flag = split_arrive_from(cp.counters + I.block, seen, I.nsplit, ctag);
+            fence_acq_rel_gpu();
+          }
+          named_barrier(1, kSoftThreads);  // the stage is reused by the next item's P; merge_flag
+          if (ms.merge_flag) {
+            if (it + 1 == item_end && I.nsplit <= kMergeMaxSplits) {
+              // The CTA's last item: its buffers are idle (every tile consumed, every MMA
+              // complete), so the pieces' partials are bulk-loaded into them.
+              const int ns = I.nsplit;
+              constexpr uint32_t kRegion = C::kOffMisc - C::kOffQ;
+              constexpr uint32_t kRowBytes = kHeadDim * 2;  // f16
+              const int rpp = min(kN, (int)(kRegion / (ns * kRowBytes)) / 8 * 8);  // rows per pass
+              for (int r0 = 0; r0 < I.nrows; r0 += rpp) {
+                const int nr = min(rpp, I.nrows - r0);
+                if (gi == 0) {
+                  fence_proxy_async_global();  // the partials are read by the async proxy
+                  fence_proxy_async_smem();    // after the generic accesses to these buffers
+                  mbar_expect_tx(bar(ms.merge_full), (uint32_t)(ns * nr) * kRowBytes);
+                  for (int i = 0; i < ns; ++i)
+                    bulk_load(sbase + C::kOffQ + (uint32_t)(i * rpp) * kRowBytes,
+                              slot_o(cp, I.slot_base + i) + (size_t)r0 * kHeadDim, (uint32_t)nr * kRowBytes,
+                              bar(ms.merge_full));
+                }
+                if (r0 == 0) {
+                  // per-row weights 2^(lse_i - M) / sum while the partials load
+                  for (int r = gi; r < I.nrows; r += kSoftThreads) {
+                    float M = -INFINITY, sum = 0.f;
+                    for (int i = 0; i < ns; ++i) M = fmaxf(M, __ldcg(slot_lse(cp, I.slot_base + i) + r));
+                    for (int i = 0; i < ns; ++i) {
+                      const float lse = __ldcg(slot_lse(cp, I.slot_base + i) + r);
+                      const float wt = lse == -INFINITY ? 0.f : exp2f(lse - M);
+                      ms.merge_w[i * kSlotRows + r] = wt;
+                      sum += wt;
+                    }
+                    const float inv_sum = sum == 0.f ? 0.f : p.out_scale / sum;
+                    for (int i = 0; i < ns; ++i) ms.merge_w[i * kSlotRows + r] *= inv_sum;
+                  }
+                  named_barrier(2, kSoftThreads);
+                }
+                // the bulk loads are this CTA's own: wait for them even after an abort
+                if (!mbar_drain(bar(ms.merge_full), merge_phase & 1, abort_flag, ptr.err)) bad = true;
+                ++merge_phase;
+                for (int idx = gi; idx < nr * (kHeadDim / 4); idx += kSoftThreads) {
+                  const int r = idx / (kHeadDim / 4), d = (idx % (kHeadDim / 4)) * 4;
+                  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                  for (int i = 0; i < ns; ++i) {
+                    const float wt = ms.merge_w[i * kSlotRows + r0 + r];
+                    const uint2 h = *reinterpret_cast<const uint2*>(smem + C::kOffQ + (size_t)(i * rpp + r) * kRowBytes + d * 2);
+                    const float2 o01 = unpack_f16x2(h.x), o23 = unpack_f16x2(h.y);
+                    acc.x += wt * o01.x;
+                    acc.y += wt * o01.y;
+                    acc.z += wt * o23.x;
+                    acc.w += wt * o23.y;
+                  }
+                  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(ptr.out) + ms.out_off[pi][r0 + r] + d) =
+                      make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+                }
+                named_barrier(2, kSoftThreads);  // the buffers are reused by the next pass
+              }
+            } else {
+              // a piece that is not its CTA's last item (or one of more than kMergeMaxSplits)
+              RowBlock rb;
+              rb.seq = I.seq;
+              rb.kvh = I.kvh;
+              rb.row0 = I.row0;
+              rb.nrows = I.nrows;
+              rb.nsplit = I.nsplit;
+              rb.slot_base = I.slot_base;
+              merge_split_block(p, ptr, cp, rb, gi, kSoftThreads, 2, ms.merge_w);
+            }
+          }
+        }
+      }
+    }  // !stalled
+    (void)bad;
+  } else if (wg == 5 || wg == 6) {
+    if constexpr (C::kWideRegs > kLaunchRegs)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
+    // ------------------------------------------------------------ widening: packed tiles to TMEM
+    const int q4 = warp & 3, half = (warp - kWideWarp0) >> 2;
+    const int ti = q4 * 32 + lane;  // TMEM lane
+    const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
+    uint32_t ring = 0;  // ring position of the next chunk
+    bool ok = true;
+    // the next chunk's buffer, free: its TMEM address
+    auto claim = [&](uint32_t& addr) -> bool {
+      const uint32_t b = ring % C::kRing, u = ring / C::kRing;
+      if (u >= 1 && !mbar_wait(bar(ms.a_free[b]), (u - 1) & 1, abort_flag, ptr.err)) return false;
+      tc_fence_after();
+      addr = tmem + lane_addr + C::kColA + b * kChunkCols;
+      return true;
+    };
+    auto publish = [&](uint64_t* full) {
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive_warp(bar(full[ring % C::kRing]), lane);
+      ++ring;
+    };
+    // K of tile g: this thread's key, d 128 h + 64 half + [0, 64) for chunk h
+    auto widen_k = [&](uint32_t g) -> bool {
+      const uint32_t st = g % C::kKStages;
+      if (!mbar_wait(bar(ms.k_full[st]), (g / C::kKStages) & 1, abort_flag, ptr.err)) return false;
+      const uint8_t* row = smem + C::kOffK + st * kTile + ti * kFp4Row;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4* src = reinterpret_cast<const uint4*>(row + 64 * h + 32 * half);
+        const uint4 x[2] = {src[0], src[1]};
+        const uint32_t sc = *reinterpret_cast<const uint32_t*>(row + kFp4Codes + 8 * h + 4 * half);
+        uint32_t dst;
+        if (!claim(dst)) return false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // 32 values: two groups
+          const uint32_t s2 = fp4::scales2(i ? sc >> 16 : sc);
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t o[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t hh[4];
+            fp4::codes4(w[k], hh);
+            const uint32_t s = __byte_perm(s2, s2, k < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) o[4 * k + b] = fp4::mul_f16x2(hh[b], s);
+          }
+          tmem_st16u(dst + 32 * half + 16 * i, o);
+        }
+        if (h == 1) mbar_arrive_warp(bar(ms.k_empty[st]), lane);
+        publish(ms.ak_full);
+      }
+      return true;
+    };
+    // V of tile g: code byte ti (d = 2 ti, 2 ti + 1) of keys 64 j + 32 half + [0, 32) for
+    // chunk j; keys from n_keys on (stale slots, or never copied) become zeros
+    auto widen_v = [&](uint32_t g, int n_keys) -> bool {
+      const uint32_t st = g % C::kVStages;
+      if (!mbar_wait(bar(ms.v_full[st]), (g / C::kVStages) & 1, abort_flag, ptr.err)) return false;
+      const uint8_t* tile = smem + C::kOffV + st * kTile;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t dst = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int blk = 4 * j + 2 * half + i;
+          const uint8_t* src = tile + blk * kFp4BlockBytes;
+          const uint4 x = *reinterpret_cast<const uint4*>(src + ti * 16);
+          uint4 sc = *reinterpret_cast<const uint4*>(src + kFp4BlockScales + (ti >> 3) * 16);
+          if (n_keys < kTileKeys) {
+            const int n = n_keys - blk * kFp4Block;
+            sc.x &= token_mask(n, 0);
+            sc.y &= token_mask(n, 1);
+            sc.z &= token_mask(n, 2);
+            sc.w &= token_mask(n, 3);
+          }
+          if (i == 0 && !claim(dst)) return false;
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w}, sw[4] = {sc.x, sc.y, sc.z, sc.w};
+          uint32_t lo[8], hi[8];  // tiles 0 and 1: key pairs
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t hh[4];
+            fp4::codes4(w[k], hh);
+            const uint32_t s01 = fp4::scales2(sw[k]), s23 = fp4::scales2(sw[k] >> 16);
+            lo[2 * k] = fp4::mul_f16x2(__byte_perm(hh[0], hh[1], 0x5410), s01);
+            lo[2 * k + 1] = fp4::mul_f16x2(__byte_perm(hh[2], hh[3], 0x5410), s23);
+            hi[2 * k] = fp4::mul_f16x2(__byte_perm(hh[0], hh[1], 0x7632), s01);
+            hi[2 * k + 1] = fp4::mul_f16x2(__byte_perm(hh[2], hh[3], 0x7632), s23);
+          }
+          tmem_st8u(dst + 16 * half + 8 * i, lo);
+          tmem_st8u(dst + 32 + 16 * half + 8 * i, hi);
+        }
+        if (j == 1) mbar_arrive_warp(bar(ms.v_empty[st]), lane);
+        publish(ms.av_full);
+      }
+      return true;
+    };
+    // K(0) K(1) V(0) K(2) V(1) .. V(last): V a tile behind K, over the CTA's whole range
+    uint32_t g = 0;
+    int prev_keys = 0;  // keys of tile g - 1 that are there
+    for (int it = item_begin; it < item_end && ok; ++it) {
+      const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
+      for (int j = 0; j < I.ntiles && ok; ++j, ++g) {
+        ok = widen_k(g);
+        if (ok && g >= 1) ok = widen_v(g - 1, prev_keys);
+        prev_keys = I.kv_hi - (I.tile_begin + j) * kTileKeys;
+      }
+    }
+    if (ok) widen_v(g - 1, prev_keys);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 0 || warp == 1) {
+      // ------------------------------------------------------------ MMA issuers
+      if (lane == 0) {
+        const bool is_s = warp == 0;
+        uint32_t g = 0;
+        int ii = 0;
+        bool ok = true;
+        for (int it = item_begin; it < item_end && ok; ++it, ++ii) {
+          const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
+          const uint32_t n16 = (uint32_t)(I.nrows + 15) & ~15u;
+          const uint32_t idesc = is_s ? idesc_f16(128, 0, false, false) | (n16 >> 3 << 17)
+                                      : idesc_f16(128, 0, false, true) | (n16 >> 3 << 17);
+          for (int j = 0; j < I.ntiles && ok; ++j, ++g) {
+            const bool last = it + 1 == item_end && j + 1 == I.ntiles;
+            if (is_s) {
+              const uint32_t sb = g % C::kSBufs, su = g / C::kSBufs;
+              if (j == 0 && !(ok = mbar_wait(bar(ms.q_full), ii & 1, abort_flag, ptr.err))) break;
+              if (su >= 1 && !(ok = mbar_wait(bar(ms.s_free[sb]), (su - 1) & 1, abort_flag, ptr.err))) break;
+              const Place kp = k_place<kN>(g);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t b = kp.buf + h;
+                if (!(ok = mbar_wait(bar(ms.ak_full[b]), kp.phase & 1, abort_flag, ptr.err))) break;
+                tc_fence_after();
+                const uint32_t a = tmem + C::kColA + b * kChunkCols;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {  // 16 d (8 columns of A) per instruction
+                  const uint64_t q = smem_desc(sbase + C::kOffQ + (2 * h + (i >> 2)) * C::kQQuarter, 16, 1024, kSw128);
+                  mma_f16_ts(tmem + C::kColS + sb * kN, a + i * 8, q + (((i & 3) * 32) >> 4), idesc, (h | i) ? 1u : 0u);
+                }
+                mma_commit(bar(ms.a_free[b]));
+              }
+              if (!ok) break;
+              mma_commit(bar(ms.s_full[sb]));
+              if (j == I.ntiles - 1) mma_commit(bar(ms.q_free));
+            } else {
+              // the first P.V of an item overwrites O^T: the previous epilogue must be done
+              if (j == 0 && ii >= 1 && !(ok = mbar_wait(bar(ms.o_free), (ii - 1) & 1, abort_flag, ptr.err))) break;
+              if (!(ok = mbar_wait(bar(ms.p_full[g & 1]), (g >> 1) & 1, abort_flag, ptr.err))) break;
+              const Place vp = v_place<kN>(g, last);
+#pragma unroll
+              for (int c64 = 0; c64 < 2; ++c64) {
+                const uint32_t b = vp.buf + c64;
+                if (!(ok = mbar_wait(bar(ms.av_full[b]), vp.phase & 1, abort_flag, ptr.err))) break;
+                tc_fence_after();
+                const uint32_t a = tmem + C::kColA + b * kChunkCols;
+                // P as an MN-major operand: 64-row blocks kPBlock apart, 8-key groups 1 KB apart,
+                // 16 keys (2 KB) per instruction
+                const uint64_t pd = smem_desc(sbase + C::kOffP + (g & 1) * C::kPBuf + c64 * 8192, C::kPBlock, 1024, kSw128);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    mma_f16_ts(tmem + C::kColO + h * kN, a + h * 32 + kk * 8, pd + ((kk * 2048) >> 4), idesc,
+                               (j == 0 && c64 == 0 && kk == 0) ? 0u : 1u);
+                mma_commit(bar(ms.a_free[b]));
+              }
+              if (!ok) break;
+              mma_commit(bar(ms.pv_done[g & 1]));
+              if (j == I.ntiles - 1) mma_commit(bar(ms.o_ready));
+            }
+          }
+        }
+        // Every MMA this thread issued has completed before the CTA may release TMEM.
+        uint64_t& drain = is_s ? ms.drain[0] : ms.drain[1];
+        mma_commit(bar(drain));
+        mbar_drain(bar(drain), 0, abort_flag, ptr.err);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ bulk copies of pages
+      // K and V have their own warps, kProdPerOp each: producer i takes the pages whose index
+      // in the tile is i modulo kProdPerOp.
+      const bool is_k = warp == 2 || warp == 28 || warp == 29;
+      const int pi = is_k ? (warp == 2 ? 0 : warp - 27) : (warp == 3 ? 0 : warp - 29);
+      const int nst = is_k ? C::kKStages : C::kVStages;
+      const uint32_t region = sbase + (is_k ? C::kOffK : C::kOffV);
+      uint64_t* full = is_k ? ms.k_full : ms.v_full;
+      uint64_t* empty = is_k ? ms.k_empty : ms.v_empty;
+      const uint8_t* cache = static_cast<const uint8_t*>(is_k ? ptr.k : ptr.v);
+      const long long sb = is_k ? p.k_sb : p.v_sb, sh = is_k ? p.k_sh : p.v_sh;
+      // verify: every page is read once; prefill: the row blocks of a sequence read it again
+      const uint64_t policy = kN == 64 ? policy_evict_first() : policy_evict_last();
+      const int ppt = kTileKeys / p.P;  // pages per tile (1, 2, 4 or 8); 32 is a multiple
+      uint32_t g = 0;
+      uint32_t issued[C::kVStages > C::kKStages ? C::kVStages : C::kKStages] = {};
+      bool stop = false;
+      for (int it = item_begin; it < item_end && !stop; ++it) {
+        const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
+        const int32_t* bt_row = ptr.block_table + (size_t)I.seq * p.bt_stride;
+        const uint8_t* head = cache + (long long)I.kvh * sh;
+        const int page0 = I.tile_begin * ppt;                 // first page of the piece
+        const int npages = (I.kv_hi + p.P - 1) / p.P - page0; // pages the piece reads
+        // a window of 32 block-table entries, one per lane, and the next one in flight; the index
+        // is clamped to the row, and an entry is checked, or dropped past the piece's pages,
+        // when it is used
+        auto fetch_raw = [&](int w) -> int { return bt_row[min(page0 + w * 32 + lane, p.W - 1)]; };
+        auto check = [&](int w, int raw) -> int {
+          if (w * 32 + lane >= npages) return -1;
+          if (raw < 0 || raw >= p.NB) {
+            atomicOr(ptr.err, kErrPage);
+            return 0;
+          }
+          return raw;
+        };
+        const int raw0 = fetch_raw(0), raw1 = fetch_raw(1);
+        int cur = check(0, raw0), nxt = check(1, raw1);
+        if (is_k && pi == 0) {
+          // the softmax warps read this item's Q soon: bring its rows into L2
+          for (int r = lane; r < I.nrows; r += 32) {
+            const RowMap m = map_row(I.row0 + r, p.G, I.kvh);
+            const uint8_t* row = static_cast<const uint8_t*>(ptr.q) + ((long long)(I.q0 + m.t) * p.q_st + (long long)m.h * p.q_sh) * 2;
+#pragma unroll
+            for (int c = 0; c < 512; c += 128) prefetch_l2(row + c);
+          }
+        }
+        int cur_w = 0;
+        for (int j = 0; j < I.ntiles; ++j, ++g) {
+          const int first = j * ppt;  // page of this tile, relative to the piece
+          if (first / 32 != cur_w) {
+            cur = nxt;
+            cur_w = first / 32;
+            nxt = check(cur_w + 1, fetch_raw(cur_w + 1));
+          }
+          const int tile_pages = min(ppt, npages - first);
+          // tokens to copy of page pg: all of them, but of the piece's last page the 16-token
+          // blocks that hold keys
+          auto tokens = [&](int pg) -> int {
+            return min(p.P, (I.kv_hi - (page0 + first + pg) * p.P + kFp4Block - 1) & ~(kFp4Block - 1));
+          };
+          uint32_t bytes = 0;
+          for (int pg = pi; pg < tile_pages; pg += kProdPerOp) bytes += (uint32_t)tokens(pg) * kFp4Row;
+          const uint32_t st = g % nst, ph = (g / nst) & 1;
+          int ok = 1;
+          if (lane == 0) {
+            ok = mbar_wait(bar(empty[st]), ph ^ 1, abort_flag, ptr.err);
+            if (ok) mbar_expect_tx(bar(full[st]), bytes);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) {
+            stop = true;
+            break;
+          }
+          for (int pg = pi; pg < tile_pages; pg += kProdPerOp) {
+            const int blk = __shfl_sync(0xffffffffu, cur, (first + pg) & 31);
+            if (lane == 0)
+              bulk_load_hint(region + st * kTile + (uint32_t)pg * p.P * kFp4Row, head + (long long)blk * sb,
+                             (uint32_t)tokens(pg) * kFp4Row, bar(full[st]), policy);
+          }
+          issued[st] = g / nst + 1;
+        }
+      }
+      // Every issued copy has landed before the CTA may exit.
+      if (lane == 0) {
+        for (int s = 0; s < nst; ++s)
+          if (issued[s]) mbar_drain(bar(full[s]), (issued[s] - 1) & 1, abort_flag, ptr.err);
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+namespace {
+
+template <int kN, bool kFused>
+int launch(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStream_t stream, bool dependent) {
+  auto kern = fp4_tc_kernel<kN, kFused>;
+  constexpr size_t smem = smem_bytes<kN, kFused>();
+  static bool done[64] = {};  // one per instance of this template
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e;
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) {
+      char buf[160];
+      snprintf(buf, sizeof buf, "cudaFuncSetAttribute(4-bit attention): %s", cudaGetErrorString(e));
+      set_tc_error(buf);
+      return -1;
+    }
+    // setmaxnreg.inc waits until the registers it asks for are free; the split adds up only
+    // if the kernel starts with exactly kLaunchRegs per thread, so never launch otherwise.
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess || fa.numRegs != kLaunchRegs) {
+      char buf[160];
+      snprintf(buf, sizeof buf, "4-bit attention kernel built with %d registers per thread; its warpgroup split needs %d",
+               e == cudaSuccess ? fa.numRegs : -1, kLaunchRegs);
+      set_tc_error(buf);
+      return -1;
+    }
+    if (dev >= 0 && dev < 64) done[dev] = true;
+  }
+  e = launch_pdl(dependent, kern, cp.num_ctas, kThreads, smem, stream, p, ptr, cp);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    char buf[160];
+    snprintf(buf, sizeof buf, "4-bit attention kernel launch: %s", cudaGetErrorString(e));
+    set_tc_error(buf);
+    return -1;
+  }
+  return 1;
+}
+
+}  // namespace
+
+int launch_fp4_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, int cls, cudaStream_t stream,
+                  bool dependent) {
+  if (cls == 1) return launch<128, false>(p, ptr, cp, stream, dependent);
+  return p.fused_verify ? launch<64, true>(p, ptr, cp, stream, dependent) : launch<64, false>(p, ptr, cp, stream, dependent);
+}
+
+}  // namespace pgqa

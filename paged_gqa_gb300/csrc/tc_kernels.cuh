@@ -24,6 +24,10 @@ int launch_prefill_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp
 // verify-class launch of a call with Problem::fused_verify (its CTAs plan the class).
 int launch_bf16_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, const pg_tensor* k,
                    const pg_tensor* v, cudaStream_t stream, bool dependent, bool self_planned);
+// 4-bit caches, class cls (0 = verify, 1 = prefill) (fp4_tc.cu); Problem::fused_verify: the
+// verify class is planned by this launch's own CTAs. 1, or -1 on a launch error.
+int launch_fp4_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, int cls, cudaStream_t stream,
+                  bool dependent);
 const char* tc_last_error();
 void set_tc_error(const char* msg);
 // TMA map over an e4m3 or bf16 cache [NB, P, Hkv, 256] (128 bytes of d of one page per box).

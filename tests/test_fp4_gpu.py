@@ -178,6 +178,20 @@ def test_attention_matches_the_oracle(i, path):
     fu.check(c, out, name)
 
 
+@pytest.mark.parametrize("seqs,hq,hkv,page", [
+    ([(2000, 9000)], 8, 1, 64),                                       # every CTA walks many tiles of many blocks
+    ([(611, 9001), (4, 8800), (574, 8900), (1, 777), (537, 5000)] + [(3, 3000)] * 9, 24, 2, 64),
+    ([(1500, 1500), (1, 12000)], 5, 5, 16),
+])
+def test_long_chunks_on_sampled_rows(seqs, hq, hkv, page):
+    c = fu.make(seqs, hq, hkv, page, seed=99)
+    rows = np.unique(np.concatenate([np.random.default_rng(7).integers(0, c.T * hq, 1500), np.arange(hq), c.T * hq - 1 - np.arange(hq)]))
+    for _ in range(3):
+        out = _attn(c)
+        _ok()
+        fu.check(c, out, "long chunks", rows=rows)
+
+
 def test_large_and_small_scores():
     """Scores of hundreds (one key takes the whole row) and queries of very different sizes in one block."""
     c = fu.make([(4, 500), (1, 300)], 16, 1, 16, seed=100, size=4.0, kd=0.05)
