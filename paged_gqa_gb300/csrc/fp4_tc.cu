@@ -25,9 +25,10 @@
 // row sums take it before that rounding. The softmax, its lazy rescale, the split-KV pieces and
 // their merge follow the FP8 verify kernel (verify_tc.cu): keys on lanes, rows on columns.
 //
-// Warp roles (1024 threads): warp 0 S issuer (+ TMEM owner), warp 1 P.V issuer, warps 2, 28,
-// 29 K copies, warps 3, 30, 31 V copies, warps 4-19 softmax and epilogue (row group (w - 4) / 4
-// owns kN / 4 rows), warps 20-27 widening (lane quarter w % 4, half (w - 20) / 4 of a chunk).
+// Warp roles: warp 0 S issuer (+ TMEM owner), warp 1 P.V issuer, warp 2 K copies, warp 3 V
+// copies, then the softmax and epilogue warps (four per 32 rows, one per TMEM lane quarter),
+// eight widening warps (lane quarter w % 4, one half of a chunk each) and, in the verify kernel,
+// four more copying warps (one thread issues page-sized copies too slowly to keep HBM busy).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,26 +49,28 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 1024;
-constexpr int kSoftWarps = 16, kSoftWarp0 = 4;
-constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kWideWarps = 8, kWideWarp0 = 20;
-constexpr int kProdPerOp = 3;
+constexpr int kWideWarps = 8, kSoftWarp0 = 4;
+constexpr int kCols = 32;           // rows per softmax thread
 constexpr float kTau = 4.f;         // rescale when a score exceeds the reference by 2^kTau
 constexpr float kSigma = 4.f;       // P is scaled by 2^kSigma (at most 2^8; f16 holds 2^-24)
-constexpr float kMInit = -1.0e30f;  // reference of a row before its first key
-
-// Registers: 1024 threads start with 64 each; the warpgroups' shares below add up to that.
-constexpr int kLaunchRegs = 64, kOtherRegs = 40;
+constexpr float kMInit = -3.0e38f;  // reference of a row before its first key
 
 constexpr uint32_t kTile = kTileKeys * kFp4Row;  // packed bytes of a tile of K or V (18 KB)
 constexpr uint32_t kChunkCols = 64;              // TMEM columns of a ring buffer
 
 template <int kN>
 struct Cfg {
-  static constexpr int kCols = kN / 4;              // rows per softmax thread
-  static constexpr int kSoftRegs = kN == 64 ? 72 : 80, kWideRegs = kN == 64 ? 72 : 56;
-  static_assert(4 * kSoftRegs + 2 * kWideRegs + 2 * kOtherRegs == 8 * kLaunchRegs, "register split");
+  static constexpr int kSoftWarps = kN / kCols * 4, kSoftThreads = kSoftWarps * 32;
+  static constexpr int kWideWarp0 = kSoftWarp0 + kSoftWarps;
+  static constexpr int kProdPerOp = kN == 64 ? 3 : 1;  // copying warps per operand
+  static constexpr int kCopyWarp0 = kWideWarp0 + kWideWarps;  // the further ones: K's, then V's
+  static constexpr int kWarps = kCopyWarp0 + (kN == 64 ? 4 : 0), kThreads = kWarps * 32;
+  // Registers: what the launch gives every thread, and the warpgroups' shares of that.
+  static constexpr int kLaunchRegs = kN == 64 ? 80 : 72;
+  static constexpr int kSoftRegs = kN == 64 ? 104 : 88, kWideRegs = kN == 64 ? 80 : 56, kOtherRegs = kN == 64 ? 56 : 40;
+  static_assert(kLaunchRegs == 65536 / kThreads / 8 * 8, "launch registers");
+  static_assert(kSoftWarps * kSoftRegs + kWideWarps * kWideRegs + (kWarps - kSoftWarps - kWideWarps) * kOtherRegs ==
+                kWarps * kLaunchRegs, "register split");
   static constexpr int kKStages = kN == 64 ? 3 : 2, kVStages = kN == 64 ? 4 : 2;
   static constexpr int kSBufs = kN == 64 ? 2 : 1;
   static constexpr int kRing = kN == 64 ? 4 : 2;    // TMEM ring buffers
@@ -193,10 +196,11 @@ __device__ __forceinline__ uint32_t token_mask(int n, int w) {
 }  // namespace
 
 template <int kN, bool kFused>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
 fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   using C = Cfg<kN>;
-  constexpr int kCols = C::kCols;
+  constexpr int kSoftWarps = C::kSoftWarps, kSoftThreads = C::kSoftThreads, kWideWarp0 = C::kWideWarp0;
+  constexpr int kProdPerOp = C::kProdPerOp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Misc<kN, kFused>& ms = *reinterpret_cast<Misc<kN, kFused>*>(smem + C::kOffMisc);
@@ -267,11 +271,11 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int wg = warp >> 2;
-  if (wg >= 1 && wg <= 4) {
+  if (wg >= 1 && wg < kWideWarp0 / 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     // ------------------------------------------------------------ softmax + epilogue
-    const int sw = warp - kSoftWarp0;      // 0..15
-    const int gi = sw * 32 + lane;         // 0..511
+    const int sw = warp - kSoftWarp0;
+    const int gi = sw * 32 + lane;
     const int q4 = warp & 3;               // TMEM lane quarter
     const int rg = sw >> 2;                // row group
     const int c0 = rg * kCols;             // first row (column) this thread owns
@@ -334,151 +338,58 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             const int qd = lane >> 3, cc = lane & 7;
             *reinterpret_cast<uint4*>(smem + C::kOffQ + qd * C::kQQuarter + r * 128 + ((cc ^ (r & 7)) << 4)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
-            if (lane == 0) ms.cs[pi][r] = ldexpf(p.score_scale_log2, e - 141);
+            if (lane == 0)  // times 2^(e - 141)
+              ms.cs[pi][r] = p.score_scale_log2 * __uint_as_float(e > 14 ? (uint32_t)(e - 14) << 23 : 0x00400000u);
           }
         }
         fence_proxy_async_smem();
         mbar_arrive(bar(ms.q_full));
       };
 
-      int ii = 0;
-      uint32_t g = 0;
-      q_prep(load_item<kN, kFused>(p, cp, ptr, ms, item_begin), 0);
-      for (int it = item_begin; it < item_end; ++it, ++ii) {
-        const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
-        const int pi = ii & 1;
-        named_barrier(1, kSoftThreads);  // q_prep's shared writes are visible
-        const int n16 = (I.nrows + 15) & ~15;
-        const int min_lim = I.L - I.qn + map_row(I.row0, p.G, I.kvh).t;
-        // A failed wait (timeout or abort) does not leave the loops: every later wait then
-        // fails fast, so all softmax warps still pass the same barriers and finish.
-        for (int j = 0; j < I.ntiles; ++j, ++g) {
-          const int sb = g % C::kSBufs, pb = g & 1;
-          const int key0 = (I.tile_begin + j) * kTileKeys;
-          const int key = key0 + ti;
-          const bool need_mask = (key0 + kTileKeys > I.kv_hi) || (key0 + kTileKeys - 1 > min_lim);
-          const bool kin = key < I.kv_hi;
-          if (!mbar_wait(bar(ms.s_full[sb]), (g / C::kSBufs) & 1, abort_flag, ptr.err)) bad = true;
-          tc_fence_after();
-          bool p_free = false, o_free = false;  // the waits before P is written / O is rescaled are done
-#pragma unroll
-          for (int cb = 0; cb < kCols; cb += 16) {
-            const int cc = c0 + cb;  // 16 rows
-            const bool active = cc < n16;  // the same in the row group's four warps
-            const uint32_t s_addr = tmem + lane_addr + C::kColS + sb * kN + cc;
-            float t[16];
-            bool rescale = false;
-            if (active) {
-              tmem_ld16(s_addr, t);
-              tmem_wait_ld();
-              // x = s c - m + sigma: the exponent of P
-              float xmax = -INFINITY;
-#pragma unroll
-              for (int n = 0; n < 16; n += 4) {
-                const float4 o4 = *reinterpret_cast<const float4*>(&ms.mo[pi][cc + n]);
-                const float4 s4 = *reinterpret_cast<const float4*>(&ms.cs[pi][cc + n]);
-                t[n] = fmaf(t[n], s4.x, o4.x);
-                t[n + 1] = fmaf(t[n + 1], s4.y, o4.y);
-                t[n + 2] = fmaf(t[n + 2], s4.z, o4.z);
-                t[n + 3] = fmaf(t[n + 3], s4.w, o4.w);
-              }
-              if (need_mask) {
-#pragma unroll
-                for (int n = 0; n < 16; n += 4) {
-                  const int4 l4 = *reinterpret_cast<const int4*>(&ms.lim[pi][cc + n]);
-                  if (!(kin && key <= l4.x)) t[n] = -INFINITY;
-                  if (!(kin && key <= l4.y)) t[n + 1] = -INFINITY;
-                  if (!(kin && key <= l4.z)) t[n + 2] = -INFINITY;
-                  if (!(kin && key <= l4.w)) t[n + 3] = -INFINITY;
-                }
-              }
-#pragma unroll
-              for (int n = 0; n < 16; n += 2) xmax = max3f(xmax, t[n], t[n + 1]);
-              // does any score of the row group exceed its row's reference by more than 2^kTau?
-              rescale = barrier_or(group_bar, 128, xmax > kTau + kSigma);
-              if (rescale) {
-                // The raw scores again (x may have lost s against a -1e30 reference): the exact
-                // tile maximum of s c per row, then the new reference.
-                tmem_ld16(s_addr, t);
-                tmem_wait_ld();
-#pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                  const bool vis = !need_mask || (kin && key <= ms.lim[pi][cc + n]);
-                  t[n] = vis ? t[n] * ms.cs[pi][cc + n] : -INFINITY;
-                  const float r = warp_max(t[n]);
-                  if (lane == n) ms.red[q4][cc + n] = r;
-                }
-                named_barrier(group_bar, 128);
-                if (q4 == 0 && lane < 16) {
-                  const int n = cc + lane;
-                  const float mt = fmaxf(fmaxf(ms.red[0][n], ms.red[1][n]), fmaxf(ms.red[2][n], ms.red[3][n]));
-                  const float m_old = ms.m[pi][n];
-                  const float mn = fmaxf(m_old, mt);
-                  ms.alpha[n] = ex2(m_old - mn);
-                  ms.m[pi][n] = mn;
-                  ms.mo[pi][n] = kSigma - mn;
-                }
-                named_barrier(group_bar, 128);
-#pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                  t[n] += ms.mo[pi][cc + n];
-                  l[cb + n] *= ms.alpha[cc + n];
-                }
-              }
-            }
-            if (cb + 16 == kCols) {  // S is read for the last time above
-              tc_fence_before();
-              mbar_arrive(bar(ms.s_free[sb]));
-            }
-            uint32_t pk[8];
-            if (active) {
-#pragma unroll
-              for (int n = 0; n < 16; n += 2) {
-                const float a = ex2(t[n]), b = ex2(t[n + 1]);
-                l[cb + n] += a;
-                l[cb + n + 1] += b;
-                pk[n / 2] = pack_f16x2(a, b);
-              }
-            }
-            // P buffer g & 1 is free once P.V(g-2) has completed; O^T may be rescaled once
-            // P.V(g-1) has. Each barrier's next phase needs a P these threads have not written
-            // yet, so a late parity wait cannot mistake it for the phase it waits for.
-            if (!p_free) {
-              if (g >= 2 && !mbar_wait(bar(ms.pv_done[pb]), ((g >> 1) - 1) & 1, abort_flag, ptr.err)) bad = true;
-              p_free = true;
-            }
-            if (rescale && j > 0) {
-              if (!o_free && !mbar_wait(bar(ms.pv_done[pb ^ 1]), ((g - 1) >> 1) & 1, abort_flag, ptr.err)) bad = true;
-              o_free = true;
-              tc_fence_after();
+      // Rows cc .. cc + 15 of S buffer sb hold a score above the reference by more than 2^kTau: the
+      // exact tile maximum of s c per row becomes the new reference, and O^T follows it (from the
+      // item's second tile on). Called by the row group's four warps together; rare, so that it
+      // trades speed for registers: a column at a time.
+      auto new_reference = [&](int cc, int pi, uint32_t sb, bool have_o, uint32_t g, bool need_mask, int key, int kv_hi) {
+        float r = -INFINITY;  // lane n: the warp's maximum of row cc + n
 #pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                float v[16];
-                const uint32_t a = tmem + lane_addr + C::kColO + h * kN + cc;
-                tmem_ld16(a, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] *= ms.alpha[cc + i];
-                tmem_st16(a, v);
-              }
-              tmem_wait_st();
-            }
-            if (active) {
-              // P^T row of key ti (128-byte swizzle): this thread's 16 rows
-              uint8_t* row = smem + C::kOffP + pb * C::kPBuf + (cc >> 6) * C::kPBlock + ti * 128;
-              const int ch = (cc & 63) >> 3;
-              *reinterpret_cast<uint4*>(row + ((ch ^ (ti & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-              *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (ti & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-            }
-          }
-          fence_proxy_async_smem();
-          tc_fence_before();
-          mbar_arrive(bar(ms.p_full[pb]));
+        for (int n = 0; n < 16; ++n) {
+          float x = tmem_ld1(tmem + lane_addr + C::kColS + sb * kN + cc + n);
+          tmem_wait_ld();
+          const bool vis = !need_mask || (key < kv_hi && key <= ms.lim[pi][cc + n]);
+          x = warp_max(vis ? x * ms.cs[pi][cc + n] : -INFINITY);
+          if (lane == n) r = x;
         }
-        // Q of the next item while this item's last P.V runs
-        if (it + 1 < item_end) q_prep(load_item<kN, kFused>(p, cp, ptr, ms, it + 1), ii + 1);
+        if (lane < 16) ms.red[q4][cc + lane] = r;
+        named_barrier(group_bar, 128);
+        if (q4 == 0 && lane < 16) {
+          const int n = cc + lane;
+          const float mt = fmaxf(fmaxf(ms.red[0][n], ms.red[1][n]), fmaxf(ms.red[2][n], ms.red[3][n]));
+          const float m_old = ms.m[pi][n];
+          const float mn = fmaxf(m_old, mt);
+          ms.alpha[n] = ex2(m_old - mn);
+          ms.m[pi][n] = mn;
+          ms.mo[pi][n] = kSigma - mn;
+        }
+        named_barrier(group_bar, 128);
+        if (have_o) {
+          if (!mbar_wait(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, ptr.err)) bad = true;
+          tc_fence_after();
+#pragma unroll 1
+          for (int n = 0; n < 32; ++n) {
+            const uint32_t a = tmem + lane_addr + C::kColO + (n >> 4) * kN + cc + (n & 15);
+            const float x = tmem_ld1(a);
+            tmem_wait_ld();
+            tmem_st1(a, x * ms.alpha[cc + (n & 15)]);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+      };
 
-        // ---------------------------------------------------------- epilogue
+      auto epilogue = [&](int it) {
+        const int ii = it - item_begin, pi = ii & 1;
+        const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
         if (!mbar_wait(bar(ms.o_ready), ii & 1, abort_flag, ptr.err)) bad = true;
         tc_fence_after();
         // row sums over the 128 key lanes: warp reduce-scatter, then across the quarters
@@ -627,11 +538,111 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             }
           }
         }
+      };
+
+      uint32_t g = 0;
+      // Per step: Q of item `it` (while the last P.V of the item before it runs), the epilogue of
+      // the item before it, the tiles of item `it`.
+      for (int it = item_begin;; ++it) {
+        const int ii = it - item_begin;
+        if (it < item_end) q_prep(load_item<kN, kFused>(p, cp, ptr, ms, it), ii);
+        if (it > item_begin) {
+          epilogue(it - 1);
+          if (it == item_end) break;
+        }
+        const int pi = ii & 1;
+        named_barrier(1, kSoftThreads);  // q_prep's shared writes are visible
+        int ntiles, key0, kv_hi, n16, min_lim;
+        {
+          const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
+          ntiles = I.ntiles;
+          key0 = I.tile_begin * kTileKeys;
+          kv_hi = I.kv_hi;
+          n16 = (I.nrows + 15) & ~15;
+          min_lim = I.L - I.qn + map_row(I.row0, p.G, I.kvh).t;
+        }
+        // A failed wait (timeout or abort) does not leave the loops: every later wait then
+        // fails fast, so all softmax warps still pass the same barriers and finish.
+        for (int j = 0; j < ntiles; ++j, ++g, key0 += kTileKeys) {
+          const uint32_t sb = g % C::kSBufs, pb = g & 1;
+          const int key = key0 + ti;
+          const bool need_mask = (key0 + kTileKeys > kv_hi) || (key0 + kTileKeys - 1 > min_lim);
+          if (!mbar_wait(bar(ms.s_full[sb]), (g / C::kSBufs) & 1, abort_flag, ptr.err)) bad = true;
+          tc_fence_after();
+#pragma unroll
+          for (int cb = 0; cb < kCols; cb += 16) {
+            const int cc = c0 + cb;        // 16 rows
+            const bool active = cc < n16;  // the same in the row group's four warps
+            float t[16];
+            if (active) {
+              while (true) {
+                tmem_ld16(tmem + lane_addr + C::kColS + sb * kN + cc, t);
+                tmem_wait_ld();
+                // x = s c - m + sigma: the exponent of P
+#pragma unroll
+                for (int n = 0; n < 16; n += 4) {
+                  const float4 o4 = *reinterpret_cast<const float4*>(&ms.mo[pi][cc + n]);
+                  const float4 s4 = *reinterpret_cast<const float4*>(&ms.cs[pi][cc + n]);
+                  t[n] = fmaf(t[n], s4.x, o4.x);
+                  t[n + 1] = fmaf(t[n + 1], s4.y, o4.y);
+                  t[n + 2] = fmaf(t[n + 2], s4.z, o4.z);
+                  t[n + 3] = fmaf(t[n + 3], s4.w, o4.w);
+                }
+                if (need_mask) {
+                  const int seen = key < kv_hi ? key : 0x7fffffff;
+#pragma unroll
+                  for (int n = 0; n < 16; n += 4) {
+                    const int4 l4 = *reinterpret_cast<const int4*>(&ms.lim[pi][cc + n]);
+                    t[n] = seen <= l4.x ? t[n] : -INFINITY;
+                    t[n + 1] = seen <= l4.y ? t[n + 1] : -INFINITY;
+                    t[n + 2] = seen <= l4.z ? t[n + 2] : -INFINITY;
+                    t[n + 3] = seen <= l4.w ? t[n + 3] : -INFINITY;
+                  }
+                }
+                float xmax = max3f(t[0], t[1], t[2]);
+#pragma unroll
+                for (int n = 3; n < 15; n += 2) xmax = max3f(xmax, t[n], t[n + 1]);
+                xmax = fmaxf(xmax, t[15]);
+                // does any score of these 16 rows exceed its row's reference by more than 2^kTau?
+                if (!barrier_or(group_bar, 128, xmax > kTau + kSigma)) break;
+                new_reference(cc, pi, sb, j > 0, g, need_mask, key, kv_hi);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) l[cb + n] *= ms.alpha[cc + n];
+              }
+            }
+            if (cb + 16 == kCols) {  // S is read for the last time above
+              tc_fence_before();
+              mbar_arrive(bar(ms.s_free[sb]));
+            }
+            // P buffer g & 1 is free once P.V(g-2) has completed (the barrier's next phase needs a
+            // P these threads have not written yet, so a late parity wait cannot miss it)
+            if (cb == 0 && g >= 2 && !mbar_wait(bar(ms.pv_done[pb]), ((g >> 1) - 1) & 1, abort_flag, ptr.err)) bad = true;
+            if (active) {
+              // P^T row of key ti (128-byte swizzle): this thread's 16 rows
+              uint8_t* row = smem + C::kOffP + pb * C::kPBuf + (cc >> 6) * C::kPBlock + ti * 128;
+#pragma unroll
+              for (int n = 0; n < 16; n += 8) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float a = ex2(t[n + 2 * k]), b = ex2(t[n + 2 * k + 1]);
+                  l[cb + n + 2 * k] += a;
+                  l[cb + n + 2 * k + 1] += b;
+                  pk[k] = pack_f16x2(a, b);
+                }
+                *reinterpret_cast<uint4*>(row + ((((cc & 63) + n) >> 3 ^ (ti & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          mbar_arrive(bar(ms.p_full[pb]));
+        }
       }
     }  // !stalled
     (void)bad;
-  } else if (wg == 5 || wg == 6) {
-    if constexpr (C::kWideRegs > kLaunchRegs)
+  } else if (wg >= kWideWarp0 / 4 && wg < C::kCopyWarp0 / 4) {
+    if constexpr (C::kWideRegs > C::kLaunchRegs)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
@@ -640,7 +651,6 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     const int ti = q4 * 32 + lane;  // TMEM lane
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
     uint32_t ring = 0;  // ring position of the next chunk
-    bool ok = true;
     // the next chunk's buffer, free: its TMEM address
     auto claim = [&](uint32_t& addr) -> bool {
       const uint32_t b = ring % C::kRing, u = ring / C::kRing;
@@ -660,7 +670,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       const uint32_t st = g % C::kKStages;
       if (!mbar_wait(bar(ms.k_full[st]), (g / C::kKStages) & 1, abort_flag, ptr.err)) return false;
       const uint8_t* row = smem + C::kOffK + st * kTile + ti * kFp4Row;
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         const uint4* src = reinterpret_cast<const uint4*>(row + 64 * h + 32 * half);
         const uint4 x[2] = {src[0], src[1]};
@@ -693,7 +703,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       const uint32_t st = g % C::kVStages;
       if (!mbar_wait(bar(ms.v_full[st]), (g / C::kVStages) & 1, abort_flag, ptr.err)) return false;
       const uint8_t* tile = smem + C::kOffV + st * kTile;
-#pragma unroll
+#pragma unroll 1
       for (int j = 0; j < 2; ++j) {
         uint32_t dst = 0;
 #pragma unroll
@@ -731,31 +741,43 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       return true;
     };
     // K(0) K(1) V(0) K(2) V(1) .. V(last): V a tile behind K, over the CTA's whole range
-    uint32_t g = 0;
-    int prev_keys = 0;  // keys of tile g - 1 that are there
-    for (int it = item_begin; it < item_end && ok; ++it) {
-      const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
-      for (int j = 0; j < I.ntiles && ok; ++j, ++g) {
-        ok = widen_k(g);
-        if (ok && g >= 1) ok = widen_v(g - 1, prev_keys);
-        prev_keys = I.kv_hi - (I.tile_begin + j) * kTileKeys;
+    int it = item_begin, j = 0, ntiles = 0, key_left = 0, prev_left = 0;
+    for (uint32_t g = 0;; ++g) {
+      const bool more = it < item_end;
+      if (more) {
+        if (j == 0) {
+          const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
+          ntiles = I.ntiles;
+          key_left = I.kv_hi - I.tile_begin * kTileKeys;  // keys from tile j on that are there
+        }
+        if (!widen_k(g)) break;
+      }
+      if (g >= 1 && !widen_v(g - 1, prev_left)) break;
+      if (!more) break;
+      prev_left = key_left;
+      key_left -= kTileKeys;
+      if (++j == ntiles) {
+        j = 0;
+        ++it;
       }
     }
-    if (ok) widen_v(g - 1, prev_keys);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == 0 || warp == 1) {
       // ------------------------------------------------------------ MMA issuers
       if (lane == 0) {
         const bool is_s = warp == 0;
+        // B: Q (K-major, 64-d quarters) or P (MN-major: 64-row blocks kPBlock apart, 8-key groups
+        // 1 KB apart, 16 keys or 2 KB per instruction)
+        const uint64_t bdesc = is_s ? smem_desc(sbase + C::kOffQ, 16, 1024, kSw128)
+                                    : smem_desc(sbase + C::kOffP, C::kPBlock, 1024, kSw128);
         uint32_t g = 0;
         int ii = 0;
         bool ok = true;
         for (int it = item_begin; it < item_end && ok; ++it, ++ii) {
           const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
           const uint32_t n16 = (uint32_t)(I.nrows + 15) & ~15u;
-          const uint32_t idesc = is_s ? idesc_f16(128, 0, false, false) | (n16 >> 3 << 17)
-                                      : idesc_f16(128, 0, false, true) | (n16 >> 3 << 17);
+          const uint32_t idesc = idesc_f16(128, 0, false, !is_s) | (n16 >> 3 << 17);
           for (int j = 0; j < I.ntiles && ok; ++j, ++g) {
             const bool last = it + 1 == item_end && j + 1 == I.ntiles;
             if (is_s) {
@@ -763,17 +785,16 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
               if (j == 0 && !(ok = mbar_wait(bar(ms.q_full), ii & 1, abort_flag, ptr.err))) break;
               if (su >= 1 && !(ok = mbar_wait(bar(ms.s_free[sb]), (su - 1) & 1, abort_flag, ptr.err))) break;
               const Place kp = k_place<kN>(g);
-#pragma unroll
+#pragma unroll 1
               for (int h = 0; h < 2; ++h) {
                 const uint32_t b = kp.buf + h;
                 if (!(ok = mbar_wait(bar(ms.ak_full[b]), kp.phase & 1, abort_flag, ptr.err))) break;
                 tc_fence_after();
                 const uint32_t a = tmem + C::kColA + b * kChunkCols;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {  // 16 d (8 columns of A) per instruction
-                  const uint64_t q = smem_desc(sbase + C::kOffQ + (2 * h + (i >> 2)) * C::kQQuarter, 16, 1024, kSw128);
-                  mma_f16_ts(tmem + C::kColS + sb * kN, a + i * 8, q + (((i & 3) * 32) >> 4), idesc, (h | i) ? 1u : 0u);
-                }
+                for (int i = 0; i < 8; ++i)  // 16 d (8 columns of A) per instruction
+                  mma_f16_ts(tmem + C::kColS + sb * kN, a + i * 8,
+                             bdesc + (((2 * h + (i >> 2)) * C::kQQuarter + (i & 3) * 32) >> 4), idesc, (h | i) ? 1u : 0u);
                 mma_commit(bar(ms.a_free[b]));
               }
               if (!ok) break;
@@ -784,15 +805,13 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
               if (j == 0 && ii >= 1 && !(ok = mbar_wait(bar(ms.o_free), (ii - 1) & 1, abort_flag, ptr.err))) break;
               if (!(ok = mbar_wait(bar(ms.p_full[g & 1]), (g >> 1) & 1, abort_flag, ptr.err))) break;
               const Place vp = v_place<kN>(g, last);
-#pragma unroll
+#pragma unroll 1
               for (int c64 = 0; c64 < 2; ++c64) {
                 const uint32_t b = vp.buf + c64;
                 if (!(ok = mbar_wait(bar(ms.av_full[b]), vp.phase & 1, abort_flag, ptr.err))) break;
                 tc_fence_after();
                 const uint32_t a = tmem + C::kColA + b * kChunkCols;
-                // P as an MN-major operand: 64-row blocks kPBlock apart, 8-key groups 1 KB apart,
-                // 16 keys (2 KB) per instruction
-                const uint64_t pd = smem_desc(sbase + C::kOffP + (g & 1) * C::kPBuf + c64 * 8192, C::kPBlock, 1024, kSw128);
+                const uint64_t pd = bdesc + (((g & 1) * C::kPBuf + c64 * 8192) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -817,9 +836,10 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       // ------------------------------------------------------------ bulk copies of pages
       // K and V have their own warps, kProdPerOp each: producer i takes the pages whose index
       // in the tile is i modulo kProdPerOp.
-      const bool is_k = warp == 2 || warp == 28 || warp == 29;
-      const int pi = is_k ? (warp == 2 ? 0 : warp - 27) : (warp == 3 ? 0 : warp - 29);
-      const int nst = is_k ? C::kKStages : C::kVStages;
+      const int cw = warp - C::kCopyWarp0;  // 0, 1: K's further warps, 2, 3: V's
+      const bool is_k = cw < 0 ? warp == 2 : cw < 2;
+      const int pi = cw < 0 ? 0 : (cw & 1) + 1;
+      const uint32_t nst = is_k ? C::kKStages : C::kVStages;
       const uint32_t region = sbase + (is_k ? C::kOffK : C::kOffV);
       uint64_t* full = is_k ? ms.k_full : ms.v_full;
       uint64_t* empty = is_k ? ms.k_empty : ms.v_empty;
@@ -829,7 +849,6 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       const uint64_t policy = kN == 64 ? policy_evict_first() : policy_evict_last();
       const int ppt = kTileKeys / p.P;  // pages per tile (1, 2, 4 or 8); 32 is a multiple
       uint32_t g = 0;
-      uint32_t issued[C::kVStages > C::kKStages ? C::kVStages : C::kKStages] = {};
       bool stop = false;
       for (int it = item_begin; it < item_end && !stop; ++it) {
         const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
@@ -893,13 +912,12 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
               bulk_load_hint(region + st * kTile + (uint32_t)pg * p.P * kFp4Row, head + (long long)blk * sb,
                              (uint32_t)tokens(pg) * kFp4Row, bar(full[st]), policy);
           }
-          issued[st] = g / nst + 1;
         }
       }
       // Every issued copy has landed before the CTA may exit.
       if (lane == 0) {
-        for (int s = 0; s < nst; ++s)
-          if (issued[s]) mbar_drain(bar(full[s]), (issued[s] - 1) & 1, abort_flag, ptr.err);
+        for (uint32_t t = g > nst ? g - nst : 0; t < g; ++t)  // the last tile of each stage
+          mbar_drain(bar(full[t % nst]), (t / nst) & 1, abort_flag, ptr.err);
       }
       __syncwarp();
     }
@@ -932,19 +950,19 @@ int launch(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStrea
       return -1;
     }
     // setmaxnreg.inc waits until the registers it asks for are free; the split adds up only
-    // if the kernel starts with exactly kLaunchRegs per thread, so never launch otherwise.
+    // if the kernel starts with exactly kLaunchRegs registers per thread, so never launch otherwise.
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kern);
-    if (e != cudaSuccess || fa.numRegs != kLaunchRegs) {
+    if (e != cudaSuccess || fa.numRegs != Cfg<kN>::kLaunchRegs) {
       char buf[160];
       snprintf(buf, sizeof buf, "4-bit attention kernel built with %d registers per thread; its warpgroup split needs %d",
-               e == cudaSuccess ? fa.numRegs : -1, kLaunchRegs);
+               e == cudaSuccess ? fa.numRegs : -1, Cfg<kN>::kLaunchRegs);
       set_tc_error(buf);
       return -1;
     }
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
-  e = launch_pdl(dependent, kern, cp.num_ctas, kThreads, smem, stream, p, ptr, cp);
+  e = launch_pdl(dependent, kern, cp.num_ctas, Cfg<kN>::kThreads, smem, stream, p, ptr, cp);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     char buf[160];
