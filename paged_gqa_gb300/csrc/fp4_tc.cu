@@ -14,10 +14,10 @@
 // tile for K (its row's bytes are d pairs, K's order), code byte t of every key for V, i.e. d =
 // 2t for tile 0 and 2t + 1 for tile 1; a V page's blocks hold 16 keys of a byte contiguously.
 //
-// The widened operand passes through a ring of 64-column TMEM buffers in chunks that one of
-// the MMA issuers frees as a whole: 128 d of the 128 keys for K, 64 keys of both tiles for V, in
-// the order K(0) K(1) V(0) K(2) V(1) ..: while the softmax works on S(g), the tensor core has
-// K(g + 1) to multiply and the widening warps V(g) to fetch.
+// The widening runs a tile ahead for K: K(0) K(1) V(0) K(2) V(1) .., so that while the softmax
+// works on S(g) the tensor core has K(g + 1) to multiply and the widening warps V(g) to fetch. With
+// 64 rows K and V have 128 TMEM columns each; with 128 rows (S and O^T take 384) they share 128
+// columns and go by halves: 128 d of the 128 keys of K, 64 keys of both tiles of V.
 //
 // Q is staged in f16 with a power of two per row (its largest value to [2^14, 2^15)): a bf16
 // value has 8 significant bits, so everything within 2^-28 of the row's largest is exact, and
@@ -26,9 +26,8 @@
 // their merge follow the FP8 verify kernel (verify_tc.cu): keys on lanes, rows on columns.
 //
 // Warp roles: warp 0 S issuer (+ TMEM owner), warp 1 P.V issuer, warp 2 K copies, warp 3 V
-// copies, then the softmax and epilogue warps (four per 32 rows, one per TMEM lane quarter),
-// eight widening warps (lane quarter w % 4, one half of a chunk each) and, in the verify kernel,
-// four more copying warps (one thread issues page-sized copies too slowly to keep HBM busy).
+// copies, then the softmax and epilogue warps (four per 32 rows, one per TMEM lane quarter) and
+// eight widening warps (lane quarter w % 4; half (w - first) / 4 of the d or keys).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -56,26 +55,26 @@ constexpr float kSigma = 4.f;       // P is scaled by 2^kSigma (at most 2^8; f16
 constexpr float kMInit = -3.0e38f;  // reference of a row before its first key
 
 constexpr uint32_t kTile = kTileKeys * kFp4Row;  // packed bytes of a tile of K or V (18 KB)
-constexpr uint32_t kChunkCols = 64;              // TMEM columns of a ring buffer
+constexpr uint32_t kChunkCols = 64;              // TMEM columns of half a tile of K or V
 
 template <int kN>
 struct Cfg {
   static constexpr int kSoftWarps = kN / kCols * 4, kSoftThreads = kSoftWarps * 32;
   static constexpr int kWideWarp0 = kSoftWarp0 + kSoftWarps;
-  static constexpr int kProdPerOp = kN == 64 ? 3 : 1;  // copying warps per operand
-  static constexpr int kCopyWarp0 = kWideWarp0 + kWideWarps;  // the further ones: K's, then V's
-  static constexpr int kWarps = kCopyWarp0 + (kN == 64 ? 4 : 0), kThreads = kWarps * 32;
+  static constexpr int kWarps = kWideWarp0 + kWideWarps, kThreads = kWarps * 32;
   // Registers: what the launch gives every thread, and the warpgroups' shares of that.
-  static constexpr int kLaunchRegs = kN == 64 ? 80 : 72;
-  static constexpr int kSoftRegs = kN == 64 ? 104 : 88, kWideRegs = kN == 64 ? 80 : 56, kOtherRegs = kN == 64 ? 56 : 40;
-  static_assert(kLaunchRegs == 65536 / kThreads / 8 * 8, "launch registers");
-  static_assert(kSoftWarps * kSoftRegs + kWideWarps * kWideRegs + (kWarps - kSoftWarps - kWideWarps) * kOtherRegs ==
-                kWarps * kLaunchRegs, "register split");
+  static constexpr int kLaunchRegs = kN == 64 ? 96 : 72;
+  static constexpr int kSoftRegs = kN == 64 ? 112 : 88, kWideRegs = kN == 64 ? 96 : 56, kOtherRegs = kN == 64 ? 64 : 40;
+  static_assert(kThreads * kLaunchRegs <= 65536, "launch registers");
+  static_assert(kSoftWarps * kSoftRegs + kWideWarps * kWideRegs + kSoftWarp0 * kOtherRegs == kWarps * kLaunchRegs,
+                "register split");
   static constexpr int kKStages = kN == 64 ? 3 : 2, kVStages = kN == 64 ? 4 : 2;
   static constexpr int kSBufs = kN == 64 ? 2 : 1;
-  static constexpr int kRing = kN == 64 ? 4 : 2;    // TMEM ring buffers
-  static constexpr uint32_t kColS = 0, kColO = 128, kColA = 128 + 2 * kN;
-  static_assert(kSBufs * kN <= 128 && kColA + kRing * kChunkCols <= 512, "TMEM columns");
+  // The widened operands in TMEM: with 64 rows K and V have 128 columns each, filled and freed as
+  // a whole; with 128 rows they share 128 columns, half a tile at a time.
+  static constexpr int kSteps = kN == 64 ? 1 : 2;
+  static constexpr uint32_t kColS = 0, kColO = 128, kColK = 128 + 2 * kN, kColV = kColK + (kN == 64 ? 128 : 0);
+  static_assert(kSBufs * kN <= 128 && kColV + 128 <= 512, "TMEM columns");
   static constexpr uint32_t kQQuarter = kN * 128;   // [kN rows][64 d] f16, 128-byte swizzle
   static constexpr uint32_t kPBlock = kTileKeys * 128;       // [128 keys][64 rows] f16
   static constexpr uint32_t kPBuf = kPBlock * (kN / 64);
@@ -97,12 +96,11 @@ struct Misc {
   alignas(16) float alpha[kN];
   alignas(16) int lim[2][kN];
   alignas(16) long long out_off[2][kN];
-  alignas(16) float merge_w[kMergeMaxSplits * kSlotRows];
   alignas(16) float lse_stage[kN];
   alignas(8) uint64_t k_full[C::kKStages], k_empty[C::kKStages], v_full[C::kVStages], v_empty[C::kVStages];
-  uint64_t ak_full[C::kRing], av_full[C::kRing], a_free[C::kRing];
+  uint64_t ak_full[2], av_full[2], ak_free[2], av_free[2];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
-  uint64_t q_full, q_free, o_ready, o_free, drain[2], merge_full;
+  uint64_t q_full, q_free, o_ready, o_free, drain[2];
   uint64_t never;  // no thread ever arrives (the failure-path test waits on it)
   uint32_t tmem_base;
   int abort_flag;
@@ -167,26 +165,6 @@ __device__ __forceinline__ Item load_item(const Problem& p, const ClassPlan& cp,
   return r;
 }
 
-// Where the first chunk of K(g) and of V(g) lies in the ring (the second one in the buffer after
-// it), g counting a CTA's tiles, and which phase of its barrier that is. The order K(0) K(1)
-// V(0) K(2) V(1) .. makes K(0) and the last V exceptions where the ring has four buffers. K and V
-// have a barrier each per buffer: an issuer has to wait for every phase of a barrier in turn (a
-// parity wait cannot tell a phase from the one two before it), and it only follows its own
-// operand.
-struct Place {
-  uint32_t buf, phase;
-};
-template <int kN>
-__device__ __forceinline__ Place k_place(uint32_t g) {
-  if (Cfg<kN>::kRing == 2) return Place{0, g};
-  return g ? Place{2, g - 1} : Place{0, 0};
-}
-template <int kN>
-__device__ __forceinline__ Place v_place(uint32_t g, bool last) {
-  if (Cfg<kN>::kRing == 2) return Place{0, g};
-  return last ? Place{2, 0} : Place{0, g};
-}
-
 // Byte mask of tokens 4w .. 4w + 3 of a 16-token block whose first n tokens are there.
 __device__ __forceinline__ uint32_t token_mask(int n, int w) {
   const int k = n - 4 * w;
@@ -200,7 +178,6 @@ __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
 fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   using C = Cfg<kN>;
   constexpr int kSoftWarps = C::kSoftWarps, kSoftThreads = C::kSoftThreads, kWideWarp0 = C::kWideWarp0;
-  constexpr int kProdPerOp = C::kProdPerOp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Misc<kN, kFused>& ms = *reinterpret_cast<Misc<kN, kFused>*>(smem + C::kOffMisc);
@@ -220,19 +197,18 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kKStages; ++s) {
-      mbar_init(bar(ms.k_full[s]), kProdPerOp);
+      mbar_init(bar(ms.k_full[s]), 1);
       mbar_init(bar(ms.k_empty[s]), kWideWarps);
     }
     for (int s = 0; s < C::kVStages; ++s) {
-      mbar_init(bar(ms.v_full[s]), kProdPerOp);
+      mbar_init(bar(ms.v_full[s]), 1);
       mbar_init(bar(ms.v_empty[s]), kWideWarps);
     }
-    for (int b = 0; b < C::kRing; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(bar(ms.ak_full[b]), kWideWarps);
       mbar_init(bar(ms.av_full[b]), kWideWarps);
-      mbar_init(bar(ms.a_free[b]), 1);
-    }
-    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar(ms.ak_free[b]), 1);
+      mbar_init(bar(ms.av_free[b]), 1);
       mbar_init(bar(ms.s_full[b]), 1);
       mbar_init(bar(ms.s_free[b]), kSoftThreads);
       mbar_init(bar(ms.p_full[b]), kSoftThreads);
@@ -244,7 +220,6 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     mbar_init(bar(ms.o_free), kSoftThreads);
     mbar_init(bar(ms.drain[0]), 1);
     mbar_init(bar(ms.drain[1]), 1);
-    mbar_init(bar(ms.merge_full), 1);
     mbar_init(bar(ms.never), 1);
     ms.abort_flag = 0;
     fence_mbar_init();
@@ -282,11 +257,10 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     const int group_bar = 3 + rg;          // named barrier of the row group's four warps
     const int ti = q4 * 32 + lane;         // TMEM lane: key of the tile; for O^T, d = 2 ti and 2 ti + 1
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
-    float l[kCols];
+    float2 l[kCols / 2];  // row sums over this thread's keys, two rows each
 #pragma unroll
-    for (int n = 0; n < kCols; ++n) l[n] = 0.f;
+    for (int n = 0; n < kCols / 2; ++n) l[n] = make_float2(0.f, 0.f);
     bool bad = false;
-    uint32_t merge_phase = 0;
     // Failure-path test: every softmax thread's bounded wait on a barrier nothing arrives on
     // runs out; they skip the items, no Q is published, and every other role gives up and
     // drains what it has in flight.
@@ -296,7 +270,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
 
       auto q_prep = [&](const Item& I, int ii) {
         const int pi = ii & 1;
-        if (ii >= 1 && !mbar_wait(bar(ms.q_free), (ii - 1) & 1, abort_flag, ptr.err)) bad = true;
+        if (ii >= 1 && !mbar_wait_polls(bar(ms.q_free), (ii - 1) & 1, abort_flag, ptr.err)) bad = true;
         if (gi < kN) {
           const int n = gi;
           const bool real = n < I.nrows;
@@ -373,7 +347,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         }
         named_barrier(group_bar, 128);
         if (have_o) {
-          if (!mbar_wait(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, ptr.err)) bad = true;
+          if (!mbar_wait_polls(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, ptr.err)) bad = true;
           tc_fence_after();
 #pragma unroll 1
           for (int n = 0; n < 32; ++n) {
@@ -387,10 +361,50 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         }
       };
 
+      // The block's last piece joins all of them: w_i = 2^(lse_i - M) / sum_j 2^(lse_j - M), M the
+      // largest, out = v_descale sum_i w_i o_i. A warp takes whole rows, 16 bytes a lane.
+      auto merge = [&](const Item& I, int pi) {
+        const int ns = I.nsplit;
+        const float* lse = slot_lse(cp, I.slot_base);
+        const uint16_t* part = slot_o(cp, I.slot_base);
+        for (int r = gi; r < I.nrows; r += kSoftThreads) {
+          float M = -INFINITY, sum = 0.f;
+#pragma unroll 1
+          for (int i = 0; i < ns; ++i) M = fmaxf(M, __ldcg(lse + i * kN + r));
+#pragma unroll 1
+          for (int i = 0; i < ns; ++i) sum += ex2(__ldcg(lse + i * kN + r) - M);
+          ms.red[0][r] = M;
+          ms.red[1][r] = p.out_scale / sum;
+        }
+        named_barrier(2, kSoftThreads);
+#pragma unroll 1
+        for (int r = sw; r < I.nrows; r += kSoftWarps) {
+          const float M = ms.red[0][r];
+          float acc[8] = {};
+#pragma unroll 4
+          for (int i = 0; i < ns; ++i) {
+            const float w = ex2(__ldcg(lse + i * kN + r) - M);
+            const uint4 h = __ldcg(reinterpret_cast<const uint4*>(part + ((size_t)i * kN + r) * kHeadDim) + lane);
+            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 o = unpack_f16x2(hw[k]);
+              acc[2 * k] += w * o.x;
+              acc[2 * k + 1] += w * o.y;
+            }
+          }
+          const float inv = ms.red[1][r];
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(ptr.out) + ms.out_off[pi][r] + lane * 8) =
+              make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                         pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+        }
+        named_barrier(2, kSoftThreads);  // red is used again by the next item
+      };
+
       auto epilogue = [&](int it) {
         const int ii = it - item_begin, pi = ii & 1;
         const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
-        if (!mbar_wait(bar(ms.o_ready), ii & 1, abort_flag, ptr.err)) bad = true;
+        if (!mbar_wait_polls(bar(ms.o_ready), ii & 1, abort_flag, ptr.err)) bad = true;
         tc_fence_after();
         // row sums over the 128 key lanes: warp reduce-scatter, then across the quarters
 #pragma unroll
@@ -398,9 +412,10 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           float v[16];
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
-            v[n] = l[cb + n];
-            l[cb + n] = 0.f;
+            v[n] = n & 1 ? l[(cb + n) / 2].y : l[(cb + n) / 2].x;
           }
+#pragma unroll
+          for (int n = 0; n < 8; ++n) l[cb / 2 + n] = make_float2(0.f, 0.f);
 #pragma unroll
           for (int w = 8, o = 16; o >= 2; w >>= 1, o >>= 1) {
             const bool up = lane & o;
@@ -470,73 +485,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             fence_acq_rel_gpu();
           }
           named_barrier(1, kSoftThreads);  // the stage is reused by the next item's P; merge_flag
-          if (ms.merge_flag) {
-            if (it + 1 == item_end && I.nsplit <= kMergeMaxSplits) {
-              // The CTA's last item: its buffers are idle (every tile consumed, every MMA
-              // complete), so the pieces' partials are bulk-loaded into them.
-              const int ns = I.nsplit;
-              constexpr uint32_t kRegion = C::kOffMisc - C::kOffQ;
-              constexpr uint32_t kRowBytes = kHeadDim * 2;  // f16
-              const int rpp = min(kN, (int)(kRegion / (ns * kRowBytes)) / 8 * 8);  // rows per pass
-              for (int r0 = 0; r0 < I.nrows; r0 += rpp) {
-                const int nr = min(rpp, I.nrows - r0);
-                if (gi == 0) {
-                  fence_proxy_async_global();  // the partials are read by the async proxy
-                  fence_proxy_async_smem();    // after the generic accesses to these buffers
-                  mbar_expect_tx(bar(ms.merge_full), (uint32_t)(ns * nr) * kRowBytes);
-                  for (int i = 0; i < ns; ++i)
-                    bulk_load(sbase + C::kOffQ + (uint32_t)(i * rpp) * kRowBytes,
-                              slot_o(cp, I.slot_base + i) + (size_t)r0 * kHeadDim, (uint32_t)nr * kRowBytes,
-                              bar(ms.merge_full));
-                }
-                if (r0 == 0) {
-                  // per-row weights 2^(lse_i - M) / sum while the partials load
-                  for (int r = gi; r < I.nrows; r += kSoftThreads) {
-                    float M = -INFINITY, sum = 0.f;
-                    for (int i = 0; i < ns; ++i) M = fmaxf(M, __ldcg(slot_lse(cp, I.slot_base + i) + r));
-                    for (int i = 0; i < ns; ++i) {
-                      const float lse = __ldcg(slot_lse(cp, I.slot_base + i) + r);
-                      const float wt = lse == -INFINITY ? 0.f : exp2f(lse - M);
-                      ms.merge_w[i * kSlotRows + r] = wt;
-                      sum += wt;
-                    }
-                    const float inv_sum = sum == 0.f ? 0.f : p.out_scale / sum;
-                    for (int i = 0; i < ns; ++i) ms.merge_w[i * kSlotRows + r] *= inv_sum;
-                  }
-                  named_barrier(2, kSoftThreads);
-                }
-                // the bulk loads are this CTA's own: wait for them even after an abort
-                if (!mbar_drain(bar(ms.merge_full), merge_phase & 1, abort_flag, ptr.err)) bad = true;
-                ++merge_phase;
-                for (int idx = gi; idx < nr * (kHeadDim / 4); idx += kSoftThreads) {
-                  const int r = idx / (kHeadDim / 4), d = (idx % (kHeadDim / 4)) * 4;
-                  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                  for (int i = 0; i < ns; ++i) {
-                    const float wt = ms.merge_w[i * kSlotRows + r0 + r];
-                    const uint2 h = *reinterpret_cast<const uint2*>(smem + C::kOffQ + (size_t)(i * rpp + r) * kRowBytes + d * 2);
-                    const float2 o01 = unpack_f16x2(h.x), o23 = unpack_f16x2(h.y);
-                    acc.x += wt * o01.x;
-                    acc.y += wt * o01.y;
-                    acc.z += wt * o23.x;
-                    acc.w += wt * o23.y;
-                  }
-                  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(ptr.out) + ms.out_off[pi][r0 + r] + d) =
-                      make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-                }
-                named_barrier(2, kSoftThreads);  // the buffers are reused by the next pass
-              }
-            } else {
-              // a piece that is not its CTA's last item (or one of more than kMergeMaxSplits)
-              RowBlock rb;
-              rb.seq = I.seq;
-              rb.kvh = I.kvh;
-              rb.row0 = I.row0;
-              rb.nrows = I.nrows;
-              rb.nsplit = I.nsplit;
-              rb.slot_base = I.slot_base;
-              merge_split_block(p, ptr, cp, rb, gi, kSoftThreads, 2, ms.merge_w);
-            }
-          }
+          if (ms.merge_flag) merge(I, pi);
         }
       };
 
@@ -567,7 +516,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           const uint32_t sb = g % C::kSBufs, pb = g & 1;
           const int key = key0 + ti;
           const bool need_mask = (key0 + kTileKeys > kv_hi) || (key0 + kTileKeys - 1 > min_lim);
-          if (!mbar_wait(bar(ms.s_full[sb]), (g / C::kSBufs) & 1, abort_flag, ptr.err)) bad = true;
+          if (!mbar_wait_polls(bar(ms.s_full[sb]), (g / C::kSBufs) & 1, abort_flag, ptr.err)) bad = true;
           tc_fence_after();
 #pragma unroll
           for (int cb = 0; cb < kCols; cb += 16) {
@@ -583,10 +532,12 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
                 for (int n = 0; n < 16; n += 4) {
                   const float4 o4 = *reinterpret_cast<const float4*>(&ms.mo[pi][cc + n]);
                   const float4 s4 = *reinterpret_cast<const float4*>(&ms.cs[pi][cc + n]);
-                  t[n] = fmaf(t[n], s4.x, o4.x);
-                  t[n + 1] = fmaf(t[n + 1], s4.y, o4.y);
-                  t[n + 2] = fmaf(t[n + 2], s4.z, o4.z);
-                  t[n + 3] = fmaf(t[n + 3], s4.w, o4.w);
+                  const float2 a = fma2(make_float2(t[n], t[n + 1]), make_float2(s4.x, s4.y), make_float2(o4.x, o4.y));
+                  const float2 b = fma2(make_float2(t[n + 2], t[n + 3]), make_float2(s4.z, s4.w), make_float2(o4.z, o4.w));
+                  t[n] = a.x;
+                  t[n + 1] = a.y;
+                  t[n + 2] = b.x;
+                  t[n + 3] = b.y;
                 }
                 if (need_mask) {
                   const int seen = key < kv_hi ? key : 0x7fffffff;
@@ -607,7 +558,10 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
                 if (!barrier_or(group_bar, 128, xmax > kTau + kSigma)) break;
                 new_reference(cc, pi, sb, j > 0, g, need_mask, key, kv_hi);
 #pragma unroll
-                for (int n = 0; n < 16; ++n) l[cb + n] *= ms.alpha[cc + n];
+                for (int n = 0; n < 8; ++n) {
+                  l[cb / 2 + n].x *= ms.alpha[cc + 2 * n];
+                  l[cb / 2 + n].y *= ms.alpha[cc + 2 * n + 1];
+                }
               }
             }
             if (cb + 16 == kCols) {  // S is read for the last time above
@@ -616,7 +570,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             }
             // P buffer g & 1 is free once P.V(g-2) has completed (the barrier's next phase needs a
             // P these threads have not written yet, so a late parity wait cannot miss it)
-            if (cb == 0 && g >= 2 && !mbar_wait(bar(ms.pv_done[pb]), ((g >> 1) - 1) & 1, abort_flag, ptr.err)) bad = true;
+            if (cb == 0 && g >= 2 && !mbar_wait_polls(bar(ms.pv_done[pb]), ((g >> 1) - 1) & 1, abort_flag, ptr.err)) bad = true;
             if (active) {
               // P^T row of key ti (128-byte swizzle): this thread's 16 rows
               uint8_t* row = smem + C::kOffP + pb * C::kPBuf + (cc >> 6) * C::kPBlock + ti * 128;
@@ -625,10 +579,9 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
                 uint32_t pk[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const float a = ex2(t[n + 2 * k]), b = ex2(t[n + 2 * k + 1]);
-                  l[cb + n + 2 * k] += a;
-                  l[cb + n + 2 * k + 1] += b;
-                  pk[k] = pack_f16x2(a, b);
+                  const float2 e = make_float2(ex2(t[n + 2 * k]), ex2(t[n + 2 * k + 1]));
+                  l[(cb + n) / 2 + k] = add2(l[(cb + n) / 2 + k], e);
+                  pk[k] = pack_f16x2(e.x, e.y);
                 }
                 *reinterpret_cast<uint4*>(row + ((((cc & 63) + n) >> 3 ^ (ti & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
               }
@@ -641,7 +594,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       }
     }  // !stalled
     (void)bad;
-  } else if (wg >= kWideWarp0 / 4 && wg < C::kCopyWarp0 / 4) {
+  } else if (wg >= kWideWarp0 / 4) {
     if constexpr (C::kWideRegs > C::kLaunchRegs)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
     else
@@ -650,33 +603,41 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     const int q4 = warp & 3, half = (warp - kWideWarp0) >> 2;
     const int ti = q4 * 32 + lane;  // TMEM lane
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
-    uint32_t ring = 0;  // ring position of the next chunk
-    // the next chunk's buffer, free: its TMEM address
-    auto claim = [&](uint32_t& addr) -> bool {
-      const uint32_t b = ring % C::kRing, u = ring / C::kRing;
-      if (u >= 1 && !mbar_wait(bar(ms.a_free[b]), (u - 1) & 1, abort_flag, ptr.err)) return false;
-      tc_fence_after();
-      addr = tmem + lane_addr + C::kColA + b * kChunkCols;
-      return true;
+    // Before half h of tile g's K or V is written: its columns are free. With two steps K and V
+    // share them, in the order K(0) K(1) V(0) K(2) V(1) ..: what was there last is V(g - 2) before
+    // K(g), and K(g + 1), or K(g) if that is the last tile, before V(g).
+    auto k_cols_free = [&](uint32_t g, int h) -> bool {
+      if (C::kSteps == 1) return g < 1 || mbar_wait_polls(bar(ms.ak_free[0]), (g - 1) & 1, abort_flag, ptr.err);
+      if (g == 1) return mbar_wait_polls(bar(ms.ak_free[h]), 0, abort_flag, ptr.err);
+      return g < 1 || mbar_wait_polls(bar(ms.av_free[h]), g & 1, abort_flag, ptr.err);
     };
-    auto publish = [&](uint64_t* full) {
+    auto v_cols_free = [&](uint32_t g, bool last, int h) -> bool {
+      if (C::kSteps == 1) return g < 1 || mbar_wait_polls(bar(ms.av_free[0]), (g - 1) & 1, abort_flag, ptr.err);
+      // K(g + 1) overwrote V(g - 1), so the order of these phases is one wait each, in turn
+      return last ? (g < 1 ? mbar_wait_polls(bar(ms.ak_free[h]), 0, abort_flag, ptr.err)
+                           : mbar_wait_polls(bar(ms.av_free[h]), (g - 1) & 1, abort_flag, ptr.err))
+                  : mbar_wait_polls(bar(ms.ak_free[h]), (g + 1) & 1, abort_flag, ptr.err);
+    };
+    auto publish = [&](uint64_t& full) {
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive_warp(bar(full[ring % C::kRing]), lane);
-      ++ring;
+      mbar_arrive_warp(bar(full), lane);
     };
-    // K of tile g: this thread's key, d 128 h + 64 half + [0, 64) for chunk h
+    // K of tile g: this thread's key, d 128 h + 64 half + [0, 64) of half h
     auto widen_k = [&](uint32_t g) -> bool {
       const uint32_t st = g % C::kKStages;
-      if (!mbar_wait(bar(ms.k_full[st]), (g / C::kKStages) & 1, abort_flag, ptr.err)) return false;
+      if (!mbar_wait_polls(bar(ms.k_full[st]), (g / C::kKStages) & 1, abort_flag, ptr.err)) return false;
       const uint8_t* row = smem + C::kOffK + st * kTile + ti * kFp4Row;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         const uint4* src = reinterpret_cast<const uint4*>(row + 64 * h + 32 * half);
         const uint4 x[2] = {src[0], src[1]};
         const uint32_t sc = *reinterpret_cast<const uint32_t*>(row + kFp4Codes + 8 * h + 4 * half);
-        uint32_t dst;
-        if (!claim(dst)) return false;
+        if (C::kSteps == 2 || h == 0) {
+          if (!k_cols_free(g, h)) return false;
+          tc_fence_after();
+        }
+        const uint32_t dst = tmem + lane_addr + C::kColK + h * kChunkCols + 32 * half;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // 32 values: two groups
           const uint32_t s2 = fp4::scales2(i ? sc >> 16 : sc);
@@ -690,22 +651,27 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) o[4 * k + b] = fp4::mul_f16x2(hh[b], s);
           }
-          tmem_st16u(dst + 32 * half + 16 * i, o);
+          tmem_st16u(dst + 16 * i, o);
         }
-        if (h == 1) mbar_arrive_warp(bar(ms.k_empty[st]), lane);
-        publish(ms.ak_full);
+        if (C::kSteps == 2) publish(ms.ak_full[h]);
       }
+      mbar_arrive_warp(bar(ms.k_empty[st]), lane);
+      if (C::kSteps == 1) publish(ms.ak_full[0]);
       return true;
     };
-    // V of tile g: code byte ti (d = 2 ti, 2 ti + 1) of keys 64 j + 32 half + [0, 32) for
-    // chunk j; keys from n_keys on (stale slots, or never copied) become zeros
-    auto widen_v = [&](uint32_t g, int n_keys) -> bool {
+    // V of tile g: code byte ti (d = 2 ti, 2 ti + 1) of keys 64 j + 32 half + [0, 32) of half j;
+    // keys from n_keys on (stale slots, or never copied) become zeros
+    auto widen_v = [&](uint32_t g, bool last, int n_keys) -> bool {
       const uint32_t st = g % C::kVStages;
-      if (!mbar_wait(bar(ms.v_full[st]), (g / C::kVStages) & 1, abort_flag, ptr.err)) return false;
+      if (!mbar_wait_polls(bar(ms.v_full[st]), (g / C::kVStages) & 1, abort_flag, ptr.err)) return false;
       const uint8_t* tile = smem + C::kOffV + st * kTile;
 #pragma unroll 1
       for (int j = 0; j < 2; ++j) {
-        uint32_t dst = 0;
+        if (C::kSteps == 2 || j == 0) {
+          if (!v_cols_free(g, last, j)) return false;
+          tc_fence_after();
+        }
+        const uint32_t dst = tmem + lane_addr + C::kColV + j * kChunkCols + 16 * half;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int blk = 4 * j + 2 * half + i;
@@ -719,7 +685,6 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             sc.z &= token_mask(n, 2);
             sc.w &= token_mask(n, 3);
           }
-          if (i == 0 && !claim(dst)) return false;
           const uint32_t w[4] = {x.x, x.y, x.z, x.w}, sw[4] = {sc.x, sc.y, sc.z, sc.w};
           uint32_t lo[8], hi[8];  // tiles 0 and 1: key pairs
 #pragma unroll
@@ -732,12 +697,13 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             hi[2 * k] = fp4::mul_f16x2(__byte_perm(hh[0], hh[1], 0x7632), s01);
             hi[2 * k + 1] = fp4::mul_f16x2(__byte_perm(hh[2], hh[3], 0x7632), s23);
           }
-          tmem_st8u(dst + 16 * half + 8 * i, lo);
-          tmem_st8u(dst + 32 + 16 * half + 8 * i, hi);
+          tmem_st8u(dst + 8 * i, lo);
+          tmem_st8u(dst + 32 + 8 * i, hi);
         }
-        if (j == 1) mbar_arrive_warp(bar(ms.v_empty[st]), lane);
-        publish(ms.av_full);
+        if (C::kSteps == 2) publish(ms.av_full[j]);
       }
+      mbar_arrive_warp(bar(ms.v_empty[st]), lane);
+      if (C::kSteps == 1) publish(ms.av_full[0]);
       return true;
     };
     // K(0) K(1) V(0) K(2) V(1) .. V(last): V a tile behind K, over the CTA's whole range
@@ -752,7 +718,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         }
         if (!widen_k(g)) break;
       }
-      if (g >= 1 && !widen_v(g - 1, prev_left)) break;
+      if (g >= 1 && !widen_v(g - 1, !more, prev_left)) break;
       if (!more) break;
       prev_left = key_left;
       key_left -= kTileKeys;
@@ -765,68 +731,82 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == 0 || warp == 1) {
       // ------------------------------------------------------------ MMA issuers
-      if (lane == 0) {
-        const bool is_s = warp == 0;
-        // B: Q (K-major, 64-d quarters) or P (MN-major: 64-row blocks kPBlock apart, 8-key groups
-        // 1 KB apart, 16 keys or 2 KB per instruction)
-        const uint64_t bdesc = is_s ? smem_desc(sbase + C::kOffQ, 16, 1024, kSw128)
-                                    : smem_desc(sbase + C::kOffP, C::kPBlock, 1024, kSw128);
-        uint32_t g = 0;
-        int ii = 0;
-        bool ok = true;
-        for (int it = item_begin; it < item_end && ok; ++it, ++ii) {
-          const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
-          const uint32_t n16 = (uint32_t)(I.nrows + 15) & ~15u;
-          const uint32_t idesc = idesc_f16(128, 0, false, !is_s) | (n16 >> 3 << 17);
-          for (int j = 0; j < I.ntiles && ok; ++j, ++g) {
-            const bool last = it + 1 == item_end && j + 1 == I.ntiles;
-            if (is_s) {
-              const uint32_t sb = g % C::kSBufs, su = g / C::kSBufs;
-              if (j == 0 && !(ok = mbar_wait(bar(ms.q_full), ii & 1, abort_flag, ptr.err))) break;
-              if (su >= 1 && !(ok = mbar_wait(bar(ms.s_free[sb]), (su - 1) & 1, abort_flag, ptr.err))) break;
-              const Place kp = k_place<kN>(g);
+      // The whole warp walks the tiles and waits; one elected lane issues. With uniform control
+      // flow the descriptors live in uniform registers, which tcgen05.mma takes: issued from a
+      // one-lane loop, each instruction first moved its operands there.
+      const bool is_s = warp == 0;
+      const bool lead = elect_one();
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm0 = __shfl_sync(0xffffffffu, sbase, 0);
+      // B: Q (K-major, 64-d quarters) or P (MN-major: 64-row blocks kPBlock apart, 8-key groups
+      // 1 KB apart, 16 keys or 2 KB per instruction)
+      const uint64_t bdesc = is_s ? smem_desc(sm0 + C::kOffQ, 16, 1024, kSw128)
+                                  : smem_desc(sm0 + C::kOffP, C::kPBlock, 1024, kSw128);
+      uint32_t g = 0;
+      int ii = 0;
+      bool ok = true;
+      for (int it = item_begin; it < item_end && ok; ++it, ++ii) {
+        const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
+        const uint32_t n16 = (uint32_t)(__shfl_sync(0xffffffffu, I.nrows, 0) + 15) & ~15u;
+        const int ntiles = __shfl_sync(0xffffffffu, I.ntiles, 0);
+        const uint32_t idesc = idesc_f16(128, 0, false, !is_s) | (n16 >> 3 << 17);
+        for (int j = 0; j < ntiles; ++j, ++g) {
+          if (is_s) {
+            const uint32_t sb = g % C::kSBufs, su = g / C::kSBufs;
+            if (j == 0 && !(ok = mbar_wait_polls(bar(ms.q_full), ii & 1, abort_flag, ptr.err))) break;
+            if (su >= 1 && !(ok = mbar_wait_polls(bar(ms.s_free[sb]), (su - 1) & 1, abort_flag, ptr.err))) break;
 #pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t b = kp.buf + h;
-                if (!(ok = mbar_wait(bar(ms.ak_full[b]), kp.phase & 1, abort_flag, ptr.err))) break;
+            for (int h = 0; h < 2; ++h) {
+              if (C::kSteps == 2 || h == 0) {
+                if (!(ok = mbar_wait_polls(bar(ms.ak_full[h]), g & 1, abort_flag, ptr.err))) break;
                 tc_fence_after();
-                const uint32_t a = tmem + C::kColA + b * kChunkCols;
+              }
+              if (lead) {
+                const uint32_t a = tm + C::kColK + h * kChunkCols, d = tm + C::kColS + sb * kN;
+                const uint64_t q = bdesc + ((2 * h * C::kQQuarter) >> 4);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)  // 16 d (8 columns of A) per instruction
-                  mma_f16_ts(tmem + C::kColS + sb * kN, a + i * 8,
-                             bdesc + (((2 * h + (i >> 2)) * C::kQQuarter + (i & 3) * 32) >> 4), idesc, (h | i) ? 1u : 0u);
-                mma_commit(bar(ms.a_free[b]));
+                  mma_f16_ts(d, a + i * 8, q + (((i >> 2) * C::kQQuarter + (i & 3) * 32) >> 4), idesc, (h | i) ? 1u : 0u);
+                if (C::kSteps == 2 || h == 1) mma_commit(bar(ms.ak_free[C::kSteps == 2 ? h : 0]));
+                if (h == 1) {
+                  mma_commit(bar(ms.s_full[sb]));
+                  if (j == ntiles - 1) mma_commit(bar(ms.q_free));
+                }
               }
-              if (!ok) break;
-              mma_commit(bar(ms.s_full[sb]));
-              if (j == I.ntiles - 1) mma_commit(bar(ms.q_free));
-            } else {
-              // the first P.V of an item overwrites O^T: the previous epilogue must be done
-              if (j == 0 && ii >= 1 && !(ok = mbar_wait(bar(ms.o_free), (ii - 1) & 1, abort_flag, ptr.err))) break;
-              if (!(ok = mbar_wait(bar(ms.p_full[g & 1]), (g >> 1) & 1, abort_flag, ptr.err))) break;
-              const Place vp = v_place<kN>(g, last);
+              __syncwarp();
+            }
+          } else {
+            // the first P.V of an item overwrites O^T: the previous epilogue must be done
+            if (j == 0 && ii >= 1 && !(ok = mbar_wait_polls(bar(ms.o_free), (ii - 1) & 1, abort_flag, ptr.err))) break;
+            if (!(ok = mbar_wait_polls(bar(ms.p_full[g & 1]), (g >> 1) & 1, abort_flag, ptr.err))) break;
 #pragma unroll 1
-              for (int c64 = 0; c64 < 2; ++c64) {
-                const uint32_t b = vp.buf + c64;
-                if (!(ok = mbar_wait(bar(ms.av_full[b]), vp.phase & 1, abort_flag, ptr.err))) break;
+            for (int c64 = 0; c64 < 2; ++c64) {
+              if (C::kSteps == 2 || c64 == 0) {
+                if (!(ok = mbar_wait_polls(bar(ms.av_full[c64]), g & 1, abort_flag, ptr.err))) break;
                 tc_fence_after();
-                const uint32_t a = tmem + C::kColA + b * kChunkCols;
+              }
+              if (lead) {
+                const uint32_t a = tm + C::kColV + c64 * kChunkCols, d = tm + C::kColO;
                 const uint64_t pd = bdesc + (((g & 1) * C::kPBuf + c64 * 8192) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                   for (int h = 0; h < 2; ++h)
-                    mma_f16_ts(tmem + C::kColO + h * kN, a + h * 32 + kk * 8, pd + ((kk * 2048) >> 4), idesc,
+                    mma_f16_ts(d + h * kN, a + h * 32 + kk * 8, pd + ((kk * 2048) >> 4), idesc,
                                (j == 0 && c64 == 0 && kk == 0) ? 0u : 1u);
-                mma_commit(bar(ms.a_free[b]));
+                if (C::kSteps == 2 || c64 == 1) mma_commit(bar(ms.av_free[C::kSteps == 2 ? c64 : 0]));
+                if (c64 == 1) {
+                  mma_commit(bar(ms.pv_done[g & 1]));
+                  if (j == ntiles - 1) mma_commit(bar(ms.o_ready));
+                }
               }
-              if (!ok) break;
-              mma_commit(bar(ms.pv_done[g & 1]));
-              if (j == I.ntiles - 1) mma_commit(bar(ms.o_ready));
+              __syncwarp();
             }
           }
+          if (!ok) break;
         }
-        // Every MMA this thread issued has completed before the CTA may release TMEM.
+      }
+      // Every MMA this warp's leader issued has completed before the CTA may release TMEM.
+      if (lead) {
         uint64_t& drain = is_s ? ms.drain[0] : ms.drain[1];
         mma_commit(bar(drain));
         mbar_drain(bar(drain), 0, abort_flag, ptr.err);
@@ -834,11 +814,8 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       __syncwarp();
     } else {
       // ------------------------------------------------------------ bulk copies of pages
-      // K and V have their own warps, kProdPerOp each: producer i takes the pages whose index
-      // in the tile is i modulo kProdPerOp.
-      const int cw = warp - C::kCopyWarp0;  // 0, 1: K's further warps, 2, 3: V's
-      const bool is_k = cw < 0 ? warp == 2 : cw < 2;
-      const int pi = cw < 0 ? 0 : (cw & 1) + 1;
+      // One warp for K, one for V; lane i copies page i of a tile (up to 8 pages).
+      const bool is_k = warp == 2;
       const uint32_t nst = is_k ? C::kKStages : C::kVStages;
       const uint32_t region = sbase + (is_k ? C::kOffK : C::kOffV);
       uint64_t* full = is_k ? ms.k_full : ms.v_full;
@@ -847,30 +824,21 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       const long long sb = is_k ? p.k_sb : p.v_sb, sh = is_k ? p.k_sh : p.v_sh;
       // verify: every page is read once; prefill: the row blocks of a sequence read it again
       const uint64_t policy = kN == 64 ? policy_evict_first() : policy_evict_last();
-      const int ppt = kTileKeys / p.P;  // pages per tile (1, 2, 4 or 8); 32 is a multiple
+      const int ppt = kTileKeys / p.P;  // pages per tile (1, 2, 4 or 8)
       uint32_t g = 0;
-      bool stop = false;
-      for (int it = item_begin; it < item_end && !stop; ++it) {
+      bool ok = true;
+      for (int it = item_begin; it < item_end && ok; ++it) {
         const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
         const int32_t* bt_row = ptr.block_table + (size_t)I.seq * p.bt_stride;
         const uint8_t* head = cache + (long long)I.kvh * sh;
-        const int page0 = I.tile_begin * ppt;                 // first page of the piece
-        const int npages = (I.kv_hi + p.P - 1) / p.P - page0; // pages the piece reads
-        // a window of 32 block-table entries, one per lane, and the next one in flight; the index
-        // is clamped to the row, and an entry is checked, or dropped past the piece's pages,
-        // when it is used
-        auto fetch_raw = [&](int w) -> int { return bt_row[min(page0 + w * 32 + lane, p.W - 1)]; };
-        auto check = [&](int w, int raw) -> int {
-          if (w * 32 + lane >= npages) return -1;
-          if (raw < 0 || raw >= p.NB) {
-            atomicOr(ptr.err, kErrPage);
-            return 0;
-          }
-          return raw;
-        };
-        const int raw0 = fetch_raw(0), raw1 = fetch_raw(1);
-        int cur = check(0, raw0), nxt = check(1, raw1);
-        if (is_k && pi == 0) {
+        int left = I.kv_hi - I.tile_begin * kTileKeys - lane * p.P;  // keys from this lane's page on
+        if (lane >= ppt) left = 0;
+        // a window of 32 block-table entries, one per lane, and the next one in flight; an index
+        // past the row is clamped, and such an entry is not used
+        int at = I.tile_begin * ppt + lane;
+        int cur = bt_row[min(at, p.W - 1)], next = bt_row[min(at + 32, p.W - 1)];
+        int first = 0;  // of the tile's pages in the window
+        if (is_k) {
           // the softmax warps read this item's Q soon: bring its rows into L2
           for (int r = lane; r < I.nrows; r += 32) {
             const RowMap m = map_row(I.row0 + r, p.G, I.kvh);
@@ -879,39 +847,37 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             for (int c = 0; c < 512; c += 128) prefetch_l2(row + c);
           }
         }
-        int cur_w = 0;
+#pragma unroll 1
         for (int j = 0; j < I.ntiles; ++j, ++g) {
-          const int first = j * ppt;  // page of this tile, relative to the piece
-          if (first / 32 != cur_w) {
-            cur = nxt;
-            cur_w = first / 32;
-            nxt = check(cur_w + 1, fetch_raw(cur_w + 1));
+          int blk = __shfl_sync(0xffffffffu, cur, (first + lane) & 31);
+          first += ppt;
+          if (first == 32) {
+            first = 0;
+            at += 32;
+            cur = next;
+            next = bt_row[min(at + 32, p.W - 1)];
           }
-          const int tile_pages = min(ppt, npages - first);
-          // tokens to copy of page pg: all of them, but of the piece's last page the 16-token
-          // blocks that hold keys
-          auto tokens = [&](int pg) -> int {
-            return min(p.P, (I.kv_hi - (page0 + first + pg) * p.P + kFp4Block - 1) & ~(kFp4Block - 1));
-          };
-          uint32_t bytes = 0;
-          for (int pg = pi; pg < tile_pages; pg += kProdPerOp) bytes += (uint32_t)tokens(pg) * kFp4Row;
-          const uint32_t st = g % nst, ph = (g / nst) & 1;
-          int ok = 1;
+          // tokens to copy: all of a page, but of the piece's last one the 16-token blocks with keys
+          const int tokens = min(p.P, (left + kFp4Block - 1) & ~(kFp4Block - 1));
+          const uint32_t st = g % nst;
           if (lane == 0) {
-            ok = mbar_wait(bar(empty[st]), ph ^ 1, abort_flag, ptr.err);
+            // what all lanes copy: the tile's keys, rounded up to whole blocks
+            const uint32_t bytes = (uint32_t)min(kTileKeys, (left + kFp4Block - 1) & ~(kFp4Block - 1)) * kFp4Row;
+            ok = mbar_wait_polls(bar(empty[st]), ((g / nst) & 1) ^ 1, abort_flag, ptr.err);
             if (ok) mbar_expect_tx(bar(full[st]), bytes);
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) {
-            stop = true;
-            break;
+          if (!ok) break;
+          __syncwarp();  // the other lanes' copies come after lane 0's wait
+          if (tokens > 0) {
+            if (blk < 0 || blk >= p.NB) {
+              atomicOr(ptr.err, kErrPage);
+              blk = 0;
+            }
+            bulk_load_hint(region + st * kTile + (uint32_t)(lane * p.P) * kFp4Row, head + (long long)blk * sb,
+                           (uint32_t)tokens * kFp4Row, bar(full[st]), policy);
           }
-          for (int pg = pi; pg < tile_pages; pg += kProdPerOp) {
-            const int blk = __shfl_sync(0xffffffffu, cur, (first + pg) & 31);
-            if (lane == 0)
-              bulk_load_hint(region + st * kTile + (uint32_t)pg * p.P * kFp4Row, head + (long long)blk * sb,
-                             (uint32_t)tokens(pg) * kFp4Row, bar(full[st]), policy);
-          }
+          left -= lane < ppt ? kTileKeys : 0;
         }
       }
       // Every issued copy has landed before the CTA may exit.

@@ -65,6 +65,27 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return false;
 }
 
+// mbar_wait in few instructions, for kernels whose code has to stay in the instruction caches:
+// polls that each suspend the thread (the try_wait's time hint, in ns) and a limit on their
+// number instead of a clock (a poll takes 30 ns at least, so the limit is 60 ms or more).
+constexpr uint32_t kSuspendNs = 2000, kMaxPolls = 1u << 21;
+__device__ __forceinline__ bool mbar_wait_polls(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kMaxPolls; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.b32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+  }
+  atomicOr(err, kErrTimeout);
+  *abort_flag = 1;
+  return false;
+}
+
 // mbar_wait by one lane of a converged warp while the other lanes wait at __syncwarp (which
 // orders their later accesses after lane 0's acquire): one poller per warp instead of 32, so
 // warps that wait do not flood the shared-memory pipe that other warps' copies, shuffles and
@@ -171,6 +192,12 @@ __device__ __forceinline__ uint64_t policy_evict_last() {
 }
 
 // ---------------------------------------------------------------- tcgen05 --
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
                : "memory");
@@ -313,6 +340,23 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 operations in one instruction (sm_100 and later).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 // The largest / smallest of three (max.f32 / min.f32 with three inputs, sm_100 and later):
 // one instruction where two-input ones take two dependent steps. Same NaN rule as fmaxf.
