@@ -59,9 +59,26 @@ __device__ __forceinline__ uint32_t encode8(const float (&x)[8]) {
       : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return w;
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+// An f16 pair times the low (high) half of another.
+__device__ __forceinline__ uint32_t mul_f16x2_lo(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __low2half2(*reinterpret_cast<const __half2*>(&s)));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t mul_f16x2_hi(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), __high2half2(*reinterpret_cast<const __half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// {lo(a) * lo(s), lo(b) * hi(t)} and {hi(a) * lo(s), hi(b) * hi(t)} for s = {x, 0}, t = {0, y}: two
+// f16 pairs of codes (one key each) to two pairs of keys, times their scales, exact. Selecting by
+// zeros keeps the work on the FMA pipes; byte permutes would share the ALU pipe with the codes'
+// conversions, which is the fuller one.
+__device__ __forceinline__ void pair_keys(uint32_t a, uint32_t b, uint32_t s, uint32_t t, uint32_t& lo, uint32_t& hi) {
+  const __half2 ha = *reinterpret_cast<const __half2*>(&a), hb = *reinterpret_cast<const __half2*>(&b);
+  const __half2 hs = *reinterpret_cast<const __half2*>(&s), ht = *reinterpret_cast<const __half2*>(&t);
+  const __half2 l = __hfma2(__low2half2(hb), ht, __hmul2(__low2half2(ha), hs));
+  const __half2 h = __hfma2(__high2half2(hb), ht, __hmul2(__high2half2(ha), hs));
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // 4 x 4 bytes transposed: byte k of r[j] = byte j of w[k].

@@ -48,27 +48,33 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWideWarps = 8, kSoftWarp0 = 4;
-constexpr int kCols = 32;           // rows per softmax thread
+constexpr int kSoftWarp0 = 4, kSoftWarps = 16, kSoftThreads = kSoftWarps * 32;
+constexpr int kWideWarp0 = kSoftWarp0 + kSoftWarps;
+constexpr int kVWarps = 8;          // that widen V
 constexpr float kTau = 4.f;         // rescale when a score exceeds the reference by 2^kTau
 constexpr float kSigma = 4.f;       // P is scaled by 2^kSigma (at most 2^8; f16 holds 2^-24)
 constexpr float kMInit = -3.0e38f;  // reference of a row before its first key
 
 constexpr uint32_t kTile = kTileKeys * kFp4Row;  // packed bytes of a tile of K or V (18 KB)
+// V's scales of a tile, as widen_v multiplies by them: per 16-token block and group 16 words, f16
+// {scale, 0} of even tokens and {0, scale} of odd ones.
+constexpr uint32_t kScaleBuf = kTileKeys * 16 * 4;  // 8 KB
 constexpr uint32_t kChunkCols = 64;              // TMEM columns of half a tile of K or V
 
 template <int kN>
 struct Cfg {
-  static constexpr int kSoftWarps = kN / kCols * 4, kSoftThreads = kSoftWarps * 32;
-  static constexpr int kWideWarp0 = kSoftWarp0 + kSoftWarps;
-  static constexpr int kWarps = kWideWarp0 + kWideWarps, kThreads = kWarps * 32;
+  static constexpr int kCols = kN / 4;  // rows per softmax thread
+  // With 64 rows K has four widening warps and V eight; with 128 rows the same eight do both.
+  static constexpr int kKWarps = kN == 64 ? 4 : 8, kVWarp0 = kN == 64 ? 4 : 0;
+  static constexpr int kWideAll = kVWarp0 + kVWarps;
+  static constexpr int kWarps = kWideWarp0 + kWideAll, kThreads = kWarps * 32;
   // Registers: what the launch gives every thread, and the warpgroups' shares of that.
-  static constexpr int kLaunchRegs = kN == 64 ? 96 : 72;
-  static constexpr int kSoftRegs = kN == 64 ? 112 : 88, kWideRegs = kN == 64 ? 96 : 56, kOtherRegs = kN == 64 ? 64 : 40;
+  static constexpr int kLaunchRegs = kN == 64 ? 64 : 72;
+  static constexpr int kSoftRegs = kN == 64 ? 72 : 88, kWideRegs = 56, kOtherRegs = kN == 64 ? 56 : 40;
   static_assert(kThreads * kLaunchRegs <= 65536, "launch registers");
-  static_assert(kSoftWarps * kSoftRegs + kWideWarps * kWideRegs + kSoftWarp0 * kOtherRegs == kWarps * kLaunchRegs,
+  static_assert(kSoftWarps * kSoftRegs + kWideAll * kWideRegs + kSoftWarp0 * kOtherRegs == kWarps * kLaunchRegs,
                 "register split");
-  static constexpr int kKStages = kN == 64 ? 3 : 2, kVStages = kN == 64 ? 4 : 2;
+  static constexpr int kKStages = kN == 64 ? 3 : 2, kVStages = kN == 64 ? 3 : 2;
   static constexpr int kSBufs = kN == 64 ? 2 : 1;
   // The widened operands in TMEM: with 64 rows K and V have 128 columns each, filled and freed as
   // a whole; with 128 rows they share 128 columns, half a tile at a time.
@@ -82,7 +88,8 @@ struct Cfg {
   static constexpr uint32_t kOffP = kOffQ + 4 * kQQuarter;
   static constexpr uint32_t kOffK = kOffP + 2 * kPBuf;
   static constexpr uint32_t kOffV = kOffK + kKStages * kTile;
-  static constexpr uint32_t kOffMisc = kOffV + kVStages * kTile;
+  static constexpr uint32_t kOffScale = kOffV + kVStages * kTile;  // two tiles' V scales, kScaleBuf each
+  static constexpr uint32_t kOffMisc = kOffScale + 2 * kScaleBuf;
   static_assert(2 * kPBuf >= kN * kHeadDim * 2, "a split piece's f16 partial fits the P buffers");
 };
 
@@ -177,7 +184,7 @@ template <int kN, bool kFused>
 __global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
 fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   using C = Cfg<kN>;
-  constexpr int kSoftWarps = C::kSoftWarps, kSoftThreads = C::kSoftThreads, kWideWarp0 = C::kWideWarp0;
+  constexpr int kCols = C::kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Misc<kN, kFused>& ms = *reinterpret_cast<Misc<kN, kFused>*>(smem + C::kOffMisc);
@@ -198,15 +205,15 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kKStages; ++s) {
       mbar_init(bar(ms.k_full[s]), 1);
-      mbar_init(bar(ms.k_empty[s]), kWideWarps);
+      mbar_init(bar(ms.k_empty[s]), C::kKWarps);
     }
     for (int s = 0; s < C::kVStages; ++s) {
       mbar_init(bar(ms.v_full[s]), 1);
-      mbar_init(bar(ms.v_empty[s]), kWideWarps);
+      mbar_init(bar(ms.v_empty[s]), kVWarps);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(bar(ms.ak_full[b]), kWideWarps);
-      mbar_init(bar(ms.av_full[b]), kWideWarps);
+      mbar_init(bar(ms.ak_full[b]), C::kKWarps);
+      mbar_init(bar(ms.av_full[b]), kVWarps);
       mbar_init(bar(ms.ak_free[b]), 1);
       mbar_init(bar(ms.av_free[b]), 1);
       mbar_init(bar(ms.s_full[b]), 1);
@@ -247,7 +254,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
 
   const int wg = warp >> 2;
   if (wg >= 1 && wg < kWideWarp0 / 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
+    if constexpr (C::kSoftRegs != C::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     // ------------------------------------------------------------ softmax + epilogue
     const int sw = warp - kSoftWarp0;
     const int gi = sw * 32 + lane;
@@ -257,9 +264,9 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     const int group_bar = 3 + rg;          // named barrier of the row group's four warps
     const int ti = q4 * 32 + lane;         // TMEM lane: key of the tile; for O^T, d = 2 ti and 2 ti + 1
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
-    float2 l[kCols / 2];  // row sums over this thread's keys, two rows each
+    uint64_t l[kCols / 2];  // row sums over this thread's keys, fp32, two rows each
 #pragma unroll
-    for (int n = 0; n < kCols / 2; ++n) l[n] = make_float2(0.f, 0.f);
+    for (int n = 0; n < kCols / 2; ++n) l[n] = 0;
     bool bad = false;
     // Failure-path test: every softmax thread's bounded wait on a barrier nothing arrives on
     // runs out; they skip the items, no Q is published, and every other role gives up and
@@ -411,11 +418,12 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         for (int cb = 0; cb < kCols; cb += 16) {
           float v[16];
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            v[n] = n & 1 ? l[(cb + n) / 2].y : l[(cb + n) / 2].x;
+          for (int n = 0; n < 8; ++n) {
+            const float2 x = unpack2(l[cb / 2 + n]);
+            v[2 * n] = x.x;
+            v[2 * n + 1] = x.y;
+            l[cb / 2 + n] = 0;
           }
-#pragma unroll
-          for (int n = 0; n < 8; ++n) l[cb / 2 + n] = make_float2(0.f, 0.f);
 #pragma unroll
           for (int w = 8, o = 16; o >= 2; w >>= 1, o >>= 1) {
             const bool up = lane & o;
@@ -501,13 +509,14 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         }
         const int pi = ii & 1;
         named_barrier(1, kSoftThreads);  // q_prep's shared writes are visible
-        int ntiles, key0, kv_hi, n16, min_lim;
+        int ntiles, key0, kv_hi, min_lim;
+        int nc;  // of this thread's rows (the same in the row group's four warps), a multiple of 16
         {
           const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
           ntiles = I.ntiles;
           key0 = I.tile_begin * kTileKeys;
           kv_hi = I.kv_hi;
-          n16 = (I.nrows + 15) & ~15;
+          nc = min(((I.nrows + 15) & ~15) - c0, kCols);
           min_lim = I.L - I.qn + map_row(I.row0, p.G, I.kvh).t;
         }
         // A failed wait (timeout or abort) does not leave the loops: every later wait then
@@ -520,51 +529,44 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           tc_fence_after();
 #pragma unroll
           for (int cb = 0; cb < kCols; cb += 16) {
-            const int cc = c0 + cb;        // 16 rows
-            const bool active = cc < n16;  // the same in the row group's four warps
-            float t[16];
+            const bool active = cb < nc;
+            uint64_t x[8];
             if (active) {
               while (true) {
-                tmem_ld16(tmem + lane_addr + C::kColS + sb * kN + cc, t);
+                tmem_ld16(tmem + lane_addr + C::kColS + sb * kN + c0 + cb, x);
                 tmem_wait_ld();
                 // x = s c - m + sigma: the exponent of P
 #pragma unroll
                 for (int n = 0; n < 16; n += 4) {
-                  const float4 o4 = *reinterpret_cast<const float4*>(&ms.mo[pi][cc + n]);
-                  const float4 s4 = *reinterpret_cast<const float4*>(&ms.cs[pi][cc + n]);
-                  const float2 a = fma2(make_float2(t[n], t[n + 1]), make_float2(s4.x, s4.y), make_float2(o4.x, o4.y));
-                  const float2 b = fma2(make_float2(t[n + 2], t[n + 3]), make_float2(s4.z, s4.w), make_float2(o4.z, o4.w));
-                  t[n] = a.x;
-                  t[n + 1] = a.y;
-                  t[n + 2] = b.x;
-                  t[n + 3] = b.y;
+                  const ulonglong2 o4 = *reinterpret_cast<const ulonglong2*>(&ms.mo[pi][c0 + cb + n]);
+                  const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(&ms.cs[pi][c0 + cb + n]);
+                  x[n / 2] = fma2(x[n / 2], s4.x, o4.x);
+                  x[n / 2 + 1] = fma2(x[n / 2 + 1], s4.y, o4.y);
                 }
                 if (need_mask) {
                   const int seen = key < kv_hi ? key : 0x7fffffff;
 #pragma unroll
-                  for (int n = 0; n < 16; n += 4) {
-                    const int4 l4 = *reinterpret_cast<const int4*>(&ms.lim[pi][cc + n]);
-                    t[n] = seen <= l4.x ? t[n] : -INFINITY;
-                    t[n + 1] = seen <= l4.y ? t[n + 1] : -INFINITY;
-                    t[n + 2] = seen <= l4.z ? t[n + 2] : -INFINITY;
-                    t[n + 3] = seen <= l4.w ? t[n + 3] : -INFINITY;
+                  for (int n = 0; n < 16; n += 2) {
+                    const int2 l2 = *reinterpret_cast<const int2*>(&ms.lim[pi][c0 + cb + n]);
+                    const float2 v = unpack2(x[n / 2]);
+                    x[n / 2] = pack2(seen <= l2.x ? v.x : -INFINITY, seen <= l2.y ? v.y : -INFINITY);
                   }
                 }
-                float xmax = max3f(t[0], t[1], t[2]);
-#pragma unroll
-                for (int n = 3; n < 15; n += 2) xmax = max3f(xmax, t[n], t[n + 1]);
-                xmax = fmaxf(xmax, t[15]);
-                // does any score of these 16 rows exceed its row's reference by more than 2^kTau?
-                if (!barrier_or(group_bar, 128, xmax > kTau + kSigma)) break;
-                new_reference(cc, pi, sb, j > 0, g, need_mask, key, kv_hi);
+                float xmax = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
-                  l[cb / 2 + n].x *= ms.alpha[cc + 2 * n];
-                  l[cb / 2 + n].y *= ms.alpha[cc + 2 * n + 1];
+                  const float2 v = unpack2(x[n]);
+                  xmax = max3f(xmax, v.x, v.y);
                 }
+                // does any score of these 16 rows exceed its row's reference by more than 2^kTau?
+                if (!barrier_or(group_bar, 128, xmax > kTau + kSigma)) break;
+                new_reference(c0 + cb, pi, sb, j > 0, g, need_mask, key, kv_hi);
+#pragma unroll
+                for (int n = 0; n < 16; n += 2)
+                  l[(cb + n) / 2] = mul2(l[(cb + n) / 2], *reinterpret_cast<const uint64_t*>(&ms.alpha[c0 + cb + n]));
               }
             }
-            if (cb + 16 == kCols) {  // S is read for the last time above
+            if (cb + 16 == kCols) {  // S has been read for the last time
               tc_fence_before();
               mbar_arrive(bar(ms.s_free[sb]));
             }
@@ -572,18 +574,19 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             // P these threads have not written yet, so a late parity wait cannot miss it)
             if (cb == 0 && g >= 2 && !mbar_wait_polls(bar(ms.pv_done[pb]), ((g >> 1) - 1) & 1, abort_flag, ptr.err)) bad = true;
             if (active) {
-              // P^T row of key ti (128-byte swizzle): this thread's 16 rows
-              uint8_t* row = smem + C::kOffP + pb * C::kPBuf + (cc >> 6) * C::kPBlock + ti * 128;
+              // P^T row of key ti (128-byte swizzle): 16 of this thread's rows
+              const uint32_t row = sbase + C::kOffP + pb * C::kPBuf + (c0 >> 6) * C::kPBlock + ti * 128;
 #pragma unroll
               for (int n = 0; n < 16; n += 8) {
                 uint32_t pk[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const float2 e = make_float2(ex2(t[n + 2 * k]), ex2(t[n + 2 * k + 1]));
-                  l[(cb + n) / 2 + k] = add2(l[(cb + n) / 2 + k], e);
-                  pk[k] = pack_f16x2(e.x, e.y);
+                  const float2 v = unpack2(x[n / 2 + k]);
+                  const float e0 = ex2(v.x), e1 = ex2(v.y);
+                  l[(cb + n) / 2 + k] = add2(l[(cb + n) / 2 + k], pack2(e0, e1));
+                  pk[k] = pack_f16x2(e0, e1);
                 }
-                *reinterpret_cast<uint4*>(row + ((((cc & 63) + n) >> 3 ^ (ti & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                st_shared_v4(row + (((((c0 & 63) + cb + n) >> 3) ^ (ti & 7)) << 4), pk);
               }
             }
           }
@@ -595,49 +598,51 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     }  // !stalled
     (void)bad;
   } else if (wg >= kWideWarp0 / 4) {
-    if constexpr (C::kWideRegs > C::kLaunchRegs)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
+    if constexpr (C::kWideRegs != C::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
     // ------------------------------------------------------------ widening: packed tiles to TMEM
-    const int q4 = warp & 3, half = (warp - kWideWarp0) >> 2;
+    const int ww = warp - kWideWarp0;
+    const int q4 = warp & 3, half = ((ww - C::kVWarp0) >> 2) & 1;  // of eight warps: which four
     const int ti = q4 * 32 + lane;  // TMEM lane
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
     // Before half h of tile g's K or V is written: its columns are free. With two steps K and V
     // share them, in the order K(0) K(1) V(0) K(2) V(1) ..: what was there last is V(g - 2) before
-    // K(g), and K(g + 1), or K(g) if that is the last tile, before V(g).
-    auto k_cols_free = [&](uint32_t g, int h) -> bool {
-      if (C::kSteps == 1) return g < 1 || mbar_wait_polls(bar(ms.ak_free[0]), (g - 1) & 1, abort_flag, ptr.err);
-      if (g == 1) return mbar_wait_polls(bar(ms.ak_free[h]), 0, abort_flag, ptr.err);
-      return g < 1 || mbar_wait_polls(bar(ms.av_free[h]), g & 1, abort_flag, ptr.err);
+    // K(g), and K(g + 1), or V(g - 1) if g is the last tile, before V(g). Every phase of a barrier
+    // is waited for in turn (a parity wait cannot tell a phase from the one two before it).
+    // A failed wait (timeout or abort) does not leave the loops: these warps share a barrier, and
+    // every later wait then fails fast.
+    auto wait = [&](uint32_t b, uint32_t parity) { mbar_wait_polls(b, parity & 1, abort_flag, ptr.err); };
+    auto k_cols_free = [&](uint32_t g, int h) {
+      if (g < 1) return;
+      if (C::kSteps == 1) wait(bar(ms.ak_free[0]), g - 1);
+      else wait(g == 1 ? bar(ms.ak_free[h]) : bar(ms.av_free[h]), g == 1 ? 0 : g);
     };
-    auto v_cols_free = [&](uint32_t g, bool last, int h) -> bool {
-      if (C::kSteps == 1) return g < 1 || mbar_wait_polls(bar(ms.av_free[0]), (g - 1) & 1, abort_flag, ptr.err);
-      // K(g + 1) overwrote V(g - 1), so the order of these phases is one wait each, in turn
-      return last ? (g < 1 ? mbar_wait_polls(bar(ms.ak_free[h]), 0, abort_flag, ptr.err)
-                           : mbar_wait_polls(bar(ms.av_free[h]), (g - 1) & 1, abort_flag, ptr.err))
-                  : mbar_wait_polls(bar(ms.ak_free[h]), (g + 1) & 1, abort_flag, ptr.err);
+    auto v_cols_free = [&](uint32_t g, bool last, int h) {
+      if (C::kSteps == 1) {
+        if (g >= 1) wait(bar(ms.av_free[0]), g - 1);
+      } else {
+        wait(last && g >= 1 ? bar(ms.av_free[h]) : bar(ms.ak_free[h]), !last ? g + 1 : g >= 1 ? g - 1 : 0);
+      }
     };
     auto publish = [&](uint64_t& full) {
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive_warp(bar(full), lane);
     };
-    // K of tile g: this thread's key, d 128 h + 64 half + [0, 64) of half h
-    auto widen_k = [&](uint32_t g) -> bool {
-      const uint32_t st = g % C::kKStages;
-      if (!mbar_wait_polls(bar(ms.k_full[st]), (g / C::kKStages) & 1, abort_flag, ptr.err)) return false;
-      const uint8_t* row = smem + C::kOffK + st * kTile + ti * kFp4Row;
+    // K of tile g: this thread's key, 64 d at a time
+    uint32_t kst = 0, kph = 0;  // stage and its phase
+    auto widen_k = [&](uint32_t g) {
+      wait(bar(ms.k_full[0]) + 8 * kst, kph);
+      const uint8_t* row = smem + C::kOffK + kst * kTile + ti * kFp4Row;
 #pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        const uint4* src = reinterpret_cast<const uint4*>(row + 64 * h + 32 * half);
+      for (int seg = C::kKWarps == 4 ? 0 : half; seg < 4; seg += C::kKWarps / 4) {
+        const uint4* src = reinterpret_cast<const uint4*>(row + 32 * seg);
         const uint4 x[2] = {src[0], src[1]};
-        const uint32_t sc = *reinterpret_cast<const uint32_t*>(row + kFp4Codes + 8 * h + 4 * half);
-        if (C::kSteps == 2 || h == 0) {
-          if (!k_cols_free(g, h)) return false;
+        const uint32_t sc = *reinterpret_cast<const uint32_t*>(row + kFp4Codes + 4 * seg);
+        if (C::kSteps == 2 || seg == 0) {
+          k_cols_free(g, seg >> 1);
           tc_fence_after();
         }
-        const uint32_t dst = tmem + lane_addr + C::kColK + h * kChunkCols + 32 * half;
+        const uint32_t dst = tmem + lane_addr + C::kColK + 32 * seg;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // 32 values: two groups
           const uint32_t s2 = fp4::scales2(i ? sc >> 16 : sc);
@@ -647,80 +652,98 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           for (int k = 0; k < 4; ++k) {
             uint32_t hh[4];
             fp4::codes4(w[k], hh);
-            const uint32_t s = __byte_perm(s2, s2, k < 2 ? 0x1010 : 0x3232);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) o[4 * k + b] = fp4::mul_f16x2(hh[b], s);
+            for (int b = 0; b < 4; ++b) o[4 * k + b] = k < 2 ? fp4::mul_f16x2_lo(hh[b], s2) : fp4::mul_f16x2_hi(hh[b], s2);
           }
           tmem_st16u(dst + 16 * i, o);
         }
-        if (C::kSteps == 2) publish(ms.ak_full[h]);
+        if (C::kSteps == 2) publish(ms.ak_full[seg >> 1]);
       }
-      mbar_arrive_warp(bar(ms.k_empty[st]), lane);
+      mbar_arrive_warp(bar(ms.k_empty[0]) + 8 * kst, lane);
       if (C::kSteps == 1) publish(ms.ak_full[0]);
-      return true;
+      if (++kst == C::kKStages) {
+        kst = 0;
+        kph ^= 1;
+      }
     };
-    // V of tile g: code byte ti (d = 2 ti, 2 ti + 1) of keys 64 j + 32 half + [0, 32) of half j;
-    // keys from n_keys on (stale slots, or never copied) become zeros
-    auto widen_v = [&](uint32_t g, bool last, int n_keys) -> bool {
-      const uint32_t st = g % C::kVStages;
-      if (!mbar_wait_polls(bar(ms.v_full[st]), (g / C::kVStages) & 1, abort_flag, ptr.err)) return false;
-      const uint8_t* tile = smem + C::kOffV + st * kTile;
+    // V of tile g: code byte ti (d = 2 ti, 2 ti + 1) of keys 64 j + 32 half + [0, 32) of half j.
+    // First these warps' threads widen the tile's scales once for all (8 bytes each), keys from
+    // n_keys on (stale slots, or never copied) to zeros.
+    uint32_t vst = 0, vph = 0;
+    const int vt = (ww - C::kVWarp0) * 32 + lane;  // 0..255
+    auto widen_v = [&](uint32_t g, bool last, int n_keys) {
+      wait(bar(ms.v_full[0]) + 8 * vst, vph);
+      const uint8_t* tile = smem + C::kOffV + vst * kTile;
+      uint8_t* scales = smem + C::kOffScale + (g & 1) * kScaleBuf;
+      {
+        const int blk = vt >> 5, grp = (vt & 31) >> 1, t8 = (vt & 1) * 8;
+        uint2 w = *reinterpret_cast<const uint2*>(tile + blk * kFp4BlockBytes + kFp4BlockScales + grp * 16 + t8);
+        if (n_keys < kTileKeys) {
+          const int n = n_keys - blk * kFp4Block - t8;
+          w.x &= token_mask(n, 0);
+          w.y &= token_mask(n, 1);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(scales + (blk * 16 + grp) * 64 + t8 * 4);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t x = k ? w.y : w.x, e = x & 0x00ff00ffu, o = x & 0xff00ff00u;
+          dst[k] = make_uint4(fp4::scales2(e), fp4::scales2(o), fp4::scales2(e >> 16), fp4::scales2(o >> 16));
+        }
+      }
+      named_barrier(8, kVWarps * 32);
 #pragma unroll 1
       for (int j = 0; j < 2; ++j) {
         if (C::kSteps == 2 || j == 0) {
-          if (!v_cols_free(g, last, j)) return false;
+          v_cols_free(g, last, j);
           tc_fence_after();
         }
         const uint32_t dst = tmem + lane_addr + C::kColV + j * kChunkCols + 16 * half;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
           const int blk = 4 * j + 2 * half + i;
-          const uint8_t* src = tile + blk * kFp4BlockBytes;
-          const uint4 x = *reinterpret_cast<const uint4*>(src + ti * 16);
-          uint4 sc = *reinterpret_cast<const uint4*>(src + kFp4BlockScales + (ti >> 3) * 16);
-          if (n_keys < kTileKeys) {
-            const int n = n_keys - blk * kFp4Block;
-            sc.x &= token_mask(n, 0);
-            sc.y &= token_mask(n, 1);
-            sc.z &= token_mask(n, 2);
-            sc.w &= token_mask(n, 3);
-          }
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w}, sw[4] = {sc.x, sc.y, sc.z, sc.w};
+          const uint4 x = *reinterpret_cast<const uint4*>(tile + blk * kFp4BlockBytes + ti * 16);
+          const uint4* sc = reinterpret_cast<const uint4*>(scales + (blk * 16 + (ti >> 3)) * 64);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
           uint32_t lo[8], hi[8];  // tiles 0 and 1: key pairs
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t hh[4];
             fp4::codes4(w[k], hh);
-            const uint32_t s01 = fp4::scales2(sw[k]), s23 = fp4::scales2(sw[k] >> 16);
-            lo[2 * k] = fp4::mul_f16x2(__byte_perm(hh[0], hh[1], 0x5410), s01);
-            lo[2 * k + 1] = fp4::mul_f16x2(__byte_perm(hh[2], hh[3], 0x5410), s23);
-            hi[2 * k] = fp4::mul_f16x2(__byte_perm(hh[0], hh[1], 0x7632), s01);
-            hi[2 * k + 1] = fp4::mul_f16x2(__byte_perm(hh[2], hh[3], 0x7632), s23);
+            const uint4 s = sc[k];
+            fp4::pair_keys(hh[0], hh[1], s.x, s.y, lo[2 * k], hi[2 * k]);
+            fp4::pair_keys(hh[2], hh[3], s.z, s.w, lo[2 * k + 1], hi[2 * k + 1]);
           }
           tmem_st8u(dst + 8 * i, lo);
           tmem_st8u(dst + 32 + 8 * i, hi);
         }
         if (C::kSteps == 2) publish(ms.av_full[j]);
       }
-      mbar_arrive_warp(bar(ms.v_empty[st]), lane);
+      mbar_arrive_warp(bar(ms.v_empty[0]) + 8 * vst, lane);
       if (C::kSteps == 1) publish(ms.av_full[0]);
-      return true;
+      if (++vst == C::kVStages) {
+        vst = 0;
+        vph ^= 1;
+      }
     };
-    // K(0) K(1) V(0) K(2) V(1) .. V(last): V a tile behind K, over the CTA's whole range
-    int it = item_begin, j = 0, ntiles = 0, key_left = 0, prev_left = 0;
+    // Both operands: K(0) K(1) V(0) K(2) V(1) .. V(last), V a tile behind K over the CTA's range.
+    const bool do_k = C::kSteps == 2 || ww < C::kKWarps, do_v = C::kSteps == 2 || ww >= C::kVWarp0;
+    const uint32_t lag = C::kSteps == 2 ? 1 : 0;
+    int it = item_begin, j = 0, ntiles = 0, key_left = 0, v_left = 0;
     for (uint32_t g = 0;; ++g) {
       const bool more = it < item_end;
+      if (!more && lag == 0) break;
       if (more) {
         if (j == 0) {
           const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
           ntiles = I.ntiles;
           key_left = I.kv_hi - I.tile_begin * kTileKeys;  // keys from tile j on that are there
         }
-        if (!widen_k(g)) break;
+        if (do_k) widen_k(g);
+        if (lag == 0) v_left = key_left;
       }
-      if (g >= 1 && !widen_v(g - 1, !more, prev_left)) break;
+      if (do_v && (lag == 0 || g >= 1)) widen_v(g - lag, !more, v_left);
       if (!more) break;
-      prev_left = key_left;
+      v_left = key_left;
       key_left -= kTileKeys;
       if (++j == ntiles) {
         j = 0;
@@ -728,7 +751,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    if constexpr (C::kOtherRegs != C::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == 0 || warp == 1) {
       // ------------------------------------------------------------ MMA issuers
       // The whole warp walks the tiles and waits; one elected lane issues. With uniform control
