@@ -14,10 +14,10 @@
 // tile for K (its row's bytes are d pairs, K's order), code byte t of every key for V, i.e. d =
 // 2t for tile 0 and 2t + 1 for tile 1; a V page's blocks hold 16 keys of a byte contiguously.
 //
-// The widening runs a tile ahead for K: K(0) K(1) V(0) K(2) V(1) .., so that while the softmax
-// works on S(g) the tensor core has K(g + 1) to multiply and the widening warps V(g) to fetch. With
-// 64 rows K and V have 128 TMEM columns each; with 128 rows (S and O^T take 384) they share 128
-// columns and go by halves: 128 d of the 128 keys of K, 64 keys of both tiles of V.
+// Widening goes by halves of a tile (128 d of the 128 keys of K, 64 keys of both tiles of V: 64
+// TMEM columns), each published to the MMA issuers and freed by them on its own, so a half is
+// multiplied while the other is widened. With 64 rows K and V have two such halves each; with 128
+// rows (S and O^T take 384 columns) they share two, K a tile ahead: K(0) K(1) V(0) K(2) V(1) ..
 //
 // Q is staged in f16 with a power of two per row (its largest value to [2^14, 2^15)): a bf16
 // value has 8 significant bits, so everything within 2^-28 of the row's largest is exact, and
@@ -25,9 +25,9 @@
 // row sums take it before that rounding. The softmax, its lazy rescale, the split-KV pieces and
 // their merge follow the FP8 verify kernel (verify_tc.cu): keys on lanes, rows on columns.
 //
-// Warp roles: warp 0 S issuer (+ TMEM owner), warp 1 P.V issuer, warp 2 K copies, warp 3 V
-// copies, then the softmax and epilogue warps (four per 32 rows, one per TMEM lane quarter) and
-// eight widening warps (lane quarter w % 4; half (w - first) / 4 of the d or keys).
+// Warp roles (1024 threads): warp 0 S issuer (+ TMEM owner), warp 1 P.V issuer, warp 2 K copies,
+// warp 3 V copies, warps 4-19 softmax and epilogue (row group (w - 4) / 4 owns kN / 4 rows, lane
+// quarter w % 4), warps 20-23 widen K, warps 24-31 V (lane quarter w % 4).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -50,7 +50,11 @@ using namespace tc;
 
 constexpr int kSoftWarp0 = 4, kSoftWarps = 16, kSoftThreads = kSoftWarps * 32;
 constexpr int kWideWarp0 = kSoftWarp0 + kSoftWarps;
-constexpr int kVWarps = 8;          // that widen V
+constexpr int kKWarps = 4, kVWarps = 8;  // that widen K, V
+constexpr int kVWarp0 = kWideWarp0 + kKWarps;
+constexpr int kWarps = kVWarp0 + kVWarps, kThreads = kWarps * 32;
+constexpr int kLaunchRegs = 64;
+static_assert(kThreads == 1024 && kThreads * kLaunchRegs == 65536, "one CTA fills the register file");
 constexpr float kTau = 4.f;         // rescale when a score exceeds the reference by 2^kTau
 constexpr float kSigma = 4.f;       // P is scaled by 2^kSigma (at most 2^8; f16 holds 2^-24)
 constexpr float kMInit = -3.0e38f;  // reference of a row before its first key
@@ -64,21 +68,15 @@ constexpr uint32_t kChunkCols = 64;              // TMEM columns of half a tile 
 template <int kN>
 struct Cfg {
   static constexpr int kCols = kN / 4;  // rows per softmax thread
-  // With 64 rows K has four widening warps and V eight; with 128 rows the same eight do both.
-  static constexpr int kKWarps = kN == 64 ? 4 : 8, kVWarp0 = kN == 64 ? 4 : 0;
-  static constexpr int kWideAll = kVWarp0 + kVWarps;
-  static constexpr int kWarps = kWideWarp0 + kWideAll, kThreads = kWarps * 32;
-  // Registers: what the launch gives every thread, and the warpgroups' shares of that.
-  static constexpr int kLaunchRegs = kN == 64 ? 64 : 72;
-  static constexpr int kSoftRegs = kN == 64 ? 72 : 88, kWideRegs = 56, kOtherRegs = kN == 64 ? 56 : 40;
-  static_assert(kThreads * kLaunchRegs <= 65536, "launch registers");
-  static_assert(kSoftWarps * kSoftRegs + kWideAll * kWideRegs + kSoftWarp0 * kOtherRegs == kWarps * kLaunchRegs,
+  // Registers of the warpgroups (their sum is what the launch gives: kLaunchRegs a thread).
+  static constexpr int kSoftRegs = kN == 64 ? 72 : 88, kWideRegs = kN == 64 ? 56 : 40, kOtherRegs = kN == 64 ? 56 : 40;
+  static_assert(kSoftWarps * kSoftRegs + (kKWarps + kVWarps) * kWideRegs + kSoftWarp0 * kOtherRegs == kWarps * kLaunchRegs,
                 "register split");
   static constexpr int kKStages = kN == 64 ? 3 : 2, kVStages = kN == 64 ? 3 : 2;
   static constexpr int kSBufs = kN == 64 ? 2 : 1;
-  // The widened operands in TMEM: with 64 rows K and V have 128 columns each, filled and freed as
-  // a whole; with 128 rows they share 128 columns, half a tile at a time.
-  static constexpr int kSteps = kN == 64 ? 1 : 2;
+  // The widened operands in TMEM go by halves of 64 columns: 128 d of the 128 keys of K, 64 keys
+  // of both tiles of V. With 64 rows K and V have two each; with 128 rows they share two.
+  static constexpr bool kShared = kN == 128;
   static constexpr uint32_t kColS = 0, kColO = 128, kColK = 128 + 2 * kN, kColV = kColK + (kN == 64 ? 128 : 0);
   static_assert(kSBufs * kN <= 128 && kColV + 128 <= 512, "TMEM columns");
   static constexpr uint32_t kQQuarter = kN * 128;   // [kN rows][64 d] f16, 128-byte swizzle
@@ -105,7 +103,7 @@ struct Misc {
   alignas(16) long long out_off[2][kN];
   alignas(16) float lse_stage[kN];
   alignas(8) uint64_t k_full[C::kKStages], k_empty[C::kKStages], v_full[C::kVStages], v_empty[C::kVStages];
-  uint64_t ak_full[2], av_full[2], ak_free[2], av_free[2];
+  uint64_t ak_full[2], av_full[2], ak_free[2], av_free[2], av_go[2];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t q_full, q_free, o_ready, o_free, drain[2];
   uint64_t never;  // no thread ever arrives (the failure-path test waits on it)
@@ -181,7 +179,7 @@ __device__ __forceinline__ uint32_t token_mask(int n, int w) {
 }  // namespace
 
 template <int kN, bool kFused>
-__global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   using C = Cfg<kN>;
   constexpr int kCols = C::kCols;
@@ -205,17 +203,18 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kKStages; ++s) {
       mbar_init(bar(ms.k_full[s]), 1);
-      mbar_init(bar(ms.k_empty[s]), C::kKWarps);
+      mbar_init(bar(ms.k_empty[s]), kKWarps);
     }
     for (int s = 0; s < C::kVStages; ++s) {
       mbar_init(bar(ms.v_full[s]), 1);
       mbar_init(bar(ms.v_empty[s]), kVWarps);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(bar(ms.ak_full[b]), C::kKWarps);
+      mbar_init(bar(ms.ak_full[b]), kKWarps);
       mbar_init(bar(ms.av_full[b]), kVWarps);
       mbar_init(bar(ms.ak_free[b]), 1);
       mbar_init(bar(ms.av_free[b]), 1);
+      mbar_init(bar(ms.av_go[b]), 1);
       mbar_init(bar(ms.s_full[b]), 1);
       mbar_init(bar(ms.s_free[b]), kSoftThreads);
       mbar_init(bar(ms.p_full[b]), kSoftThreads);
@@ -231,6 +230,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     ms.abort_flag = 0;
     fence_mbar_init();
   }
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(smem_u32(&ms.tmem_base), 512);
     tmem_relinquish();
@@ -254,7 +254,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
 
   const int wg = warp >> 2;
   if (wg >= 1 && wg < kWideWarp0 / 4) {
-    if constexpr (C::kSoftRegs != C::kLaunchRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     // ------------------------------------------------------------ softmax + epilogue
     const int sw = warp - kSoftWarp0;
     const int gi = sw * 32 + lane;
@@ -355,6 +355,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         named_barrier(group_bar, 128);
         if (have_o) {
           if (!mbar_wait_polls(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, ptr.err)) bad = true;
+          __syncwarp();
           tc_fence_after();
 #pragma unroll 1
           for (int n = 0; n < 32; ++n) {
@@ -412,6 +413,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         const int ii = it - item_begin, pi = ii & 1;
         const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
         if (!mbar_wait_polls(bar(ms.o_ready), ii & 1, abort_flag, ptr.err)) bad = true;
+        __syncwarp();
         tc_fence_after();
         // row sums over the 128 key lanes: warp reduce-scatter, then across the quarters
 #pragma unroll
@@ -526,6 +528,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           const int key = key0 + ti;
           const bool need_mask = (key0 + kTileKeys > kv_hi) || (key0 + kTileKeys - 1 > min_lim);
           if (!mbar_wait_polls(bar(ms.s_full[sb]), (g / C::kSBufs) & 1, abort_flag, ptr.err)) bad = true;
+          __syncwarp();  // the TMEM loads are warp-wide
           tc_fence_after();
 #pragma unroll
           for (int cb = 0; cb < kCols; cb += 16) {
@@ -598,35 +601,48 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     }  // !stalled
     (void)bad;
   } else if (wg >= kWideWarp0 / 4) {
-    if constexpr (C::kWideRegs != C::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
     // ------------------------------------------------------------ widening: packed tiles to TMEM
-    const int ww = warp - kWideWarp0;
-    const int q4 = warp & 3, half = ((ww - C::kVWarp0) >> 2) & 1;  // of eight warps: which four
+    const int q4 = warp & 3;
     const int ti = q4 * 32 + lane;  // TMEM lane
     const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
-    // Before half h of tile g's K or V is written: its columns are free. With two steps K and V
-    // share them, in the order K(0) K(1) V(0) K(2) V(1) ..: what was there last is V(g - 2) before
-    // K(g), and K(g + 1), or V(g - 1) if g is the last tile, before V(g). Every phase of a barrier
-    // is waited for in turn (a parity wait cannot tell a phase from the one two before it).
-    // A failed wait (timeout or abort) does not leave the loops: these warps share a barrier, and
+    // A failed wait (timeout or abort) does not leave the loops: the V warps share a barrier, and
     // every later wait then fails fast.
-    auto wait = [&](uint32_t b, uint32_t parity) { mbar_wait_polls(b, parity & 1, abort_flag, ptr.err); };
+    // The warp is converged after a wait and after an arrival: the tcgen05.st that follow are
+    // warp-wide instructions, and neither a poll's exit nor a one-lane arrival brings the lanes
+    // together by itself.
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      mbar_wait_polls(b, parity & 1, abort_flag, ptr.err);
+      __syncwarp();
+    };
+    auto arrive = [&](uint32_t b) {
+      mbar_arrive_warp(b, lane);
+      __syncwarp();
+    };
+    // Before half h of tile g's K or V is written: its columns are free. Shared columns are used
+    // in the order K(0) K(1) V(0) K(2) V(1) .. V(last): what was there last is K(0) before K(1), then
+    // V(g - 2) before K(g), and K(g + 1), or V(g - 1) if g is the last tile, before V(g). Every
+    // barrier here has one set of waiters that waits for its phases in turn, none of them more
+    // than one ahead of the waiters (a parity wait cannot tell a phase from the one two before
+    // it): so QK(0) arrives at ak_free for K(1), every later QK(g + 1) at av_go for V(g).
     auto k_cols_free = [&](uint32_t g, int h) {
       if (g < 1) return;
-      if (C::kSteps == 1) wait(bar(ms.ak_free[0]), g - 1);
-      else wait(g == 1 ? bar(ms.ak_free[h]) : bar(ms.av_free[h]), g == 1 ? 0 : g);
+      if (!C::kShared || g == 1) wait(bar(ms.ak_free[0]) + 8 * h, g - 1);
+      else wait(bar(ms.av_free[0]) + 8 * h, g);
     };
     auto v_cols_free = [&](uint32_t g, bool last, int h) {
-      if (C::kSteps == 1) {
-        if (g >= 1) wait(bar(ms.av_free[0]), g - 1);
+      if (!C::kShared) {
+        if (g >= 1) wait(bar(ms.av_free[0]) + 8 * h, g - 1);
+      } else if (last && g >= 1) {
+        wait(bar(ms.av_free[0]) + 8 * h, g - 1);
       } else {
-        wait(last && g >= 1 ? bar(ms.av_free[h]) : bar(ms.ak_free[h]), !last ? g + 1 : g >= 1 ? g - 1 : 0);
+        wait(bar(ms.av_go[0]) + 8 * h, g);
       }
     };
-    auto publish = [&](uint64_t& full) {
+    auto publish = [&](uint32_t full) {
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive_warp(bar(full), lane);
+      arrive(full);
     };
     // K of tile g: this thread's key, 64 d at a time
     uint32_t kst = 0, kph = 0;  // stage and its phase
@@ -634,33 +650,33 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       wait(bar(ms.k_full[0]) + 8 * kst, kph);
       const uint8_t* row = smem + C::kOffK + kst * kTile + ti * kFp4Row;
 #pragma unroll 1
-      for (int seg = C::kKWarps == 4 ? 0 : half; seg < 4; seg += C::kKWarps / 4) {
-        const uint4* src = reinterpret_cast<const uint4*>(row + 32 * seg);
-        const uint4 x[2] = {src[0], src[1]};
-        const uint32_t sc = *reinterpret_cast<const uint32_t*>(row + kFp4Codes + 4 * seg);
-        if (C::kSteps == 2 || seg == 0) {
-          k_cols_free(g, seg >> 1);
-          tc_fence_after();
-        }
-        const uint32_t dst = tmem + lane_addr + C::kColK + 32 * seg;
+      for (int h = 0; h < 2; ++h) {
+        k_cols_free(g, h);
+        tc_fence_after();
+#pragma unroll 1
+        for (int seg = 2 * h; seg < 2 * h + 2; ++seg) {
+          const uint4* src = reinterpret_cast<const uint4*>(row + 32 * seg);
+          const uint4 x[2] = {src[0], src[1]};
+          const uint32_t sc = *reinterpret_cast<const uint32_t*>(row + kFp4Codes + 4 * seg);
+          const uint32_t dst = tmem + lane_addr + C::kColK + 32 * seg;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // 32 values: two groups
-          const uint32_t s2 = fp4::scales2(i ? sc >> 16 : sc);
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          uint32_t o[16];
+          for (int i = 0; i < 2; ++i) {  // 32 values: two groups
+            const uint32_t s2 = fp4::scales2(i ? sc >> 16 : sc);
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t o[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t hh[4];
-            fp4::codes4(w[k], hh);
+            for (int k = 0; k < 4; ++k) {
+              uint32_t hh[4];
+              fp4::codes4(w[k], hh);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) o[4 * k + b] = k < 2 ? fp4::mul_f16x2_lo(hh[b], s2) : fp4::mul_f16x2_hi(hh[b], s2);
+              for (int b = 0; b < 4; ++b) o[4 * k + b] = k < 2 ? fp4::mul_f16x2_lo(hh[b], s2) : fp4::mul_f16x2_hi(hh[b], s2);
+            }
+            tmem_st16u(dst + 16 * i, o);
           }
-          tmem_st16u(dst + 16 * i, o);
         }
-        if (C::kSteps == 2) publish(ms.ak_full[seg >> 1]);
+        publish(bar(ms.ak_full[0]) + 8 * h);
       }
-      mbar_arrive_warp(bar(ms.k_empty[0]) + 8 * kst, lane);
-      if (C::kSteps == 1) publish(ms.ak_full[0]);
+      arrive(bar(ms.k_empty[0]) + 8 * kst);
       if (++kst == C::kKStages) {
         kst = 0;
         kph ^= 1;
@@ -670,7 +686,8 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     // First these warps' threads widen the tile's scales once for all (8 bytes each), keys from
     // n_keys on (stale slots, or never copied) to zeros.
     uint32_t vst = 0, vph = 0;
-    const int vt = (ww - C::kVWarp0) * 32 + lane;  // 0..255
+    const int vt = (warp - kVWarp0) * 32 + lane;  // 0..255
+    const int half = (vt >> 7) & 1;               // which 32 keys of a half tile
     auto widen_v = [&](uint32_t g, bool last, int n_keys) {
       wait(bar(ms.v_full[0]) + 8 * vst, vph);
       const uint8_t* tile = smem + C::kOffV + vst * kTile;
@@ -693,10 +710,8 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       named_barrier(8, kVWarps * 32);
 #pragma unroll 1
       for (int j = 0; j < 2; ++j) {
-        if (C::kSteps == 2 || j == 0) {
-          v_cols_free(g, last, j);
-          tc_fence_after();
-        }
+        v_cols_free(g, last, j);
+        tc_fence_after();
         const uint32_t dst = tmem + lane_addr + C::kColV + j * kChunkCols + 16 * half;
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
@@ -716,47 +731,38 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           tmem_st8u(dst + 8 * i, lo);
           tmem_st8u(dst + 32 + 8 * i, hi);
         }
-        if (C::kSteps == 2) publish(ms.av_full[j]);
+        publish(bar(ms.av_full[0]) + 8 * j);
       }
-      mbar_arrive_warp(bar(ms.v_empty[0]) + 8 * vst, lane);
-      if (C::kSteps == 1) publish(ms.av_full[0]);
+      arrive(bar(ms.v_empty[0]) + 8 * vst);
       if (++vst == C::kVStages) {
         vst = 0;
         vph ^= 1;
       }
     };
-    // Both operands: K(0) K(1) V(0) K(2) V(1) .. V(last), V a tile behind K over the CTA's range.
-    const bool do_k = C::kSteps == 2 || ww < C::kKWarps, do_v = C::kSteps == 2 || ww >= C::kVWarp0;
-    const uint32_t lag = C::kSteps == 2 ? 1 : 0;
-    int it = item_begin, j = 0, ntiles = 0, key_left = 0, v_left = 0;
-    for (uint32_t g = 0;; ++g) {
-      const bool more = it < item_end;
-      if (!more && lag == 0) break;
-      if (more) {
-        if (j == 0) {
-          const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
-          ntiles = I.ntiles;
-          key_left = I.kv_hi - I.tile_begin * kTileKeys;  // keys from tile j on that are there
-        }
-        if (do_k) widen_k(g);
-        if (lag == 0) v_left = key_left;
-      }
-      if (do_v && (lag == 0 || g >= 1)) widen_v(g - lag, !more, v_left);
-      if (!more) break;
-      v_left = key_left;
-      key_left -= kTileKeys;
-      if (++j == ntiles) {
-        j = 0;
-        ++it;
+    // the CTA's tiles
+    const bool is_k = warp < kVWarp0;
+    uint32_t g = 0;
+    for (int it = item_begin; it < item_end; ++it) {
+      const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
+      int left = I.kv_hi - I.tile_begin * kTileKeys;  // keys from tile j on that are there
+#pragma unroll 1
+      for (int j = 0; j < I.ntiles; ++j, ++g, left -= kTileKeys) {
+        if (is_k) widen_k(g);
+        else widen_v(g, it + 1 == item_end && j + 1 == I.ntiles, left);
       }
     }
   } else {
-    if constexpr (C::kOtherRegs != C::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == 0 || warp == 1) {
       // ------------------------------------------------------------ MMA issuers
       // The whole warp walks the tiles and waits; one elected lane issues. With uniform control
       // flow the descriptors live in uniform registers, which tcgen05.mma takes: issued from a
-      // one-lane loop, each instruction first moved its operands there.
+      // one-lane loop, each instruction first moved its operands there. The lanes have to leave
+      // every wait together for that (the vote): a suspended poll ends lane by lane, and uniform
+      // registers belong to the warp, not to a part of it that runs ahead.
+      auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_polls(b, parity & 1, abort_flag, ptr.err));
+      };
       const bool is_s = warp == 0;
       const bool lead = elect_one();
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sm0 = __shfl_sync(0xffffffffu, sbase, 0);
@@ -775,21 +781,20 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         for (int j = 0; j < ntiles; ++j, ++g) {
           if (is_s) {
             const uint32_t sb = g % C::kSBufs, su = g / C::kSBufs;
-            if (j == 0 && !(ok = mbar_wait_polls(bar(ms.q_full), ii & 1, abort_flag, ptr.err))) break;
-            if (su >= 1 && !(ok = mbar_wait_polls(bar(ms.s_free[sb]), (su - 1) & 1, abort_flag, ptr.err))) break;
+            const bool last = it + 1 == item_end && j + 1 == ntiles;
+            if (j == 0 && !(ok = wait(bar(ms.q_full), ii))) break;
+            if (su >= 1 && !(ok = wait(bar(ms.s_free[sb]), su - 1))) break;
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-              if (C::kSteps == 2 || h == 0) {
-                if (!(ok = mbar_wait_polls(bar(ms.ak_full[h]), g & 1, abort_flag, ptr.err))) break;
-                tc_fence_after();
-              }
+              if (!(ok = wait(bar(ms.ak_full[0]) + 8 * h, g))) break;
+              tc_fence_after();
               if (lead) {
                 const uint32_t a = tm + C::kColK + h * kChunkCols, d = tm + C::kColS + sb * kN;
                 const uint64_t q = bdesc + ((2 * h * C::kQQuarter) >> 4);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)  // 16 d (8 columns of A) per instruction
                   mma_f16_ts(d, a + i * 8, q + (((i >> 2) * C::kQQuarter + (i & 3) * 32) >> 4), idesc, (h | i) ? 1u : 0u);
-                if (C::kSteps == 2 || h == 1) mma_commit(bar(ms.ak_free[C::kSteps == 2 ? h : 0]));
+                mma_commit((!C::kShared || (g == 0 && !last) ? bar(ms.ak_free[0]) : bar(ms.av_go[0])) + 8 * h);
                 if (h == 1) {
                   mma_commit(bar(ms.s_full[sb]));
                   if (j == ntiles - 1) mma_commit(bar(ms.q_free));
@@ -799,14 +804,12 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             }
           } else {
             // the first P.V of an item overwrites O^T: the previous epilogue must be done
-            if (j == 0 && ii >= 1 && !(ok = mbar_wait_polls(bar(ms.o_free), (ii - 1) & 1, abort_flag, ptr.err))) break;
-            if (!(ok = mbar_wait_polls(bar(ms.p_full[g & 1]), (g >> 1) & 1, abort_flag, ptr.err))) break;
+            if (j == 0 && ii >= 1 && !(ok = wait(bar(ms.o_free), ii - 1))) break;
+            if (!(ok = wait(bar(ms.p_full[g & 1]), g >> 1))) break;
 #pragma unroll 1
             for (int c64 = 0; c64 < 2; ++c64) {
-              if (C::kSteps == 2 || c64 == 0) {
-                if (!(ok = mbar_wait_polls(bar(ms.av_full[c64]), g & 1, abort_flag, ptr.err))) break;
-                tc_fence_after();
-              }
+              if (!(ok = wait(bar(ms.av_full[0]) + 8 * c64, g))) break;
+              tc_fence_after();
               if (lead) {
                 const uint32_t a = tm + C::kColV + c64 * kChunkCols, d = tm + C::kColO;
                 const uint64_t pd = bdesc + (((g & 1) * C::kPBuf + c64 * 8192) >> 4);
@@ -816,7 +819,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
                   for (int h = 0; h < 2; ++h)
                     mma_f16_ts(d + h * kN, a + h * 32 + kk * 8, pd + ((kk * 2048) >> 4), idesc,
                                (j == 0 && c64 == 0 && kk == 0) ? 0u : 1u);
-                if (C::kSteps == 2 || c64 == 1) mma_commit(bar(ms.av_free[C::kSteps == 2 ? c64 : 0]));
+                mma_commit(bar(ms.av_free[0]) + 8 * c64);
                 if (c64 == 1) {
                   mma_commit(bar(ms.pv_done[g & 1]));
                   if (j == ntiles - 1) mma_commit(bar(ms.o_ready));
@@ -942,16 +945,16 @@ int launch(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStrea
     // if the kernel starts with exactly kLaunchRegs registers per thread, so never launch otherwise.
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kern);
-    if (e != cudaSuccess || fa.numRegs != Cfg<kN>::kLaunchRegs) {
+    if (e != cudaSuccess || fa.numRegs != kLaunchRegs) {
       char buf[160];
       snprintf(buf, sizeof buf, "4-bit attention kernel built with %d registers per thread; its warpgroup split needs %d",
-               e == cudaSuccess ? fa.numRegs : -1, Cfg<kN>::kLaunchRegs);
+               e == cudaSuccess ? fa.numRegs : -1, kLaunchRegs);
       set_tc_error(buf);
       return -1;
     }
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
-  e = launch_pdl(dependent, kern, cp.num_ctas, Cfg<kN>::kThreads, smem, stream, p, ptr, cp);
+  e = launch_pdl(dependent, kern, cp.num_ctas, kThreads, smem, stream, p, ptr, cp);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     char buf[160];
