@@ -354,7 +354,8 @@ int paged_gqa_check_device_errors(pg_stream_t stream);
  *       and warp-level MMA otherwise; sparse calls use the warp-level kernel (measured the
  *       faster of the two on the sparse workloads)
  *   1 = warp-level MMA (mma.sync) kernel for every tile
- *   2 = as 0, but sparse calls with lists of 64 or more entries use the tcgen05 kernel
+ *   2 = as 0, but sparse calls with lists of 64 or more entries use the tcgen05 kernel, and
+ *       4-bit attention uses it for batches of single tokens too
  *   3 = as 0, but the verify class is always planned by the plan kernel before its
  *       kernel runs (under 0 the tcgen05 verify kernel plans it itself when
  *       num_seqs x num_kv_heads <= 512; results are identical)
@@ -379,7 +380,7 @@ int paged_gqa_set_stall_test(uint32_t wait_ns);
  * Host-side launch summary of the last successful call on this host thread, for
  * tests and the benchmark. out8 receives {verify CTAs, prefill CTAs, kernels
  * launched, path bits (2: tcgen05 verify, 4: tcgen05 prefill, 8: warp-MMA verify,
- * 16: warp-MMA prefill, 32: tcgen05 sparse, 64: warp-MMA sparse), verify block bound,
+ * 16: warp-MMA prefill, 32: tcgen05 sparse, 64: warp-MMA sparse, 128: 4-bit decode), verify block bound,
  * prefill block bound, workspace bytes, 1 if the verify kernel planned its own class}.
  * A sparse call sets only the launch count and the path bits.
  */

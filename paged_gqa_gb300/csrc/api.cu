@@ -612,6 +612,10 @@ int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, 
   const bool single_prefill = p.num_seqs == 1 && (long long)p.T * p.G > kVerifyRows;
   p.fused_verify = tc && path != 3 && !single_prefill && (long long)p.num_seqs * p.Hkv <= kFusedMaxBlocks &&
                    max_tiles < (1 << 16) && (long long)p.num_seqs * p.Hkv * (max_tiles + fixed_cost(0)) < (1LL << 31);
+  // Single tokens (no more tokens than sequences) of groups of at most 16 heads go to the
+  // warp-level decode kernel: a sequence with more rows is served in passes, correctly but with
+  // its keys read once per 16 rows.
+  const bool decode = tc && path != 2 && p.T <= p.num_seqs && p.G <= 16;
   int launched = 0, used = 0;
   cudaError_t e;
   for (int c = 0; c < kNumClasses; ++c) {
@@ -624,7 +628,11 @@ int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, 
     }
     // no sequence of at most kVerifyRows rows in all can be of the prefill class
     if (c == 1 && (long long)p.T * p.G <= kVerifyRows) break;
-    if (tc) {
+    if (c == 0 && decode) {
+      if (launch_fp4_decode(p, ptr, cp[c], stream) < 0)
+        return fail(PG_ERR_CUDA, "4-bit decode launch failed: %s", tc_last_error());
+      used |= 128;
+    } else if (tc) {
       if (launch_fp4_tc(p, ptr, cp[c], c, stream, c == 1) < 0)
         return fail(PG_ERR_CUDA, "tcgen05 4-bit launch failed: %s", tc_last_error());
       used |= 2 << c;

@@ -28,6 +28,9 @@ int launch_bf16_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, c
 // verify class is planned by this launch's own CTAs. 1, or -1 on a launch error.
 int launch_fp4_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, int cls, cudaStream_t stream,
                   bool dependent);
+// The verify class of a batch of single tokens over 4-bit caches (fp4_decode.cu), groups of at
+// most 16 heads. 1, or -1 on a launch error.
+int launch_fp4_decode(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStream_t stream);
 const char* tc_last_error();
 void set_tc_error(const char* msg);
 // TMA map over an e4m3 or bf16 cache [NB, P, Hkv, 256] (128 bytes of d of one page per box).

@@ -161,10 +161,14 @@ ATTN = [
     ("mixed", [(4, 300), (129, 700), (1, 50), (0, 20), (33, 33), (2, 1000)], 24, 2, 64),
     ("empty sequences", [(0, 0), (2, 40), (0, 100), (1, 9)], 16, 1, 16),
     ("long", [(4, 20000), (1, 9999)], 16, 1, 16),
+    ("single tokens, long", [(1, 30000), (1, 7777), (1, 16), (1, 17), (1, 31)], 16, 1, 32),
+    ("single tokens, groups of eight", [(1, 5000), (1, 1), (1, 640), (1, 129)], 16, 2, 128),
+    ("single tokens, small groups", [(1, 1000), (1, 33), (1, 257)], 12, 4, 16),
+    ("as many tokens as sequences, unevenly", [(0, 40), (3, 700), (0, 0), (1, 300), (4, 129), (0, 9), (0, 8), (1, 5), (0, 3)], 16, 1, 16),
 ]
 
 
-@pytest.mark.parametrize("path", [1, 0, 3])
+@pytest.mark.parametrize("path", [1, 0, 2, 3])
 @pytest.mark.parametrize("i", range(len(ATTN)), ids=[a[0] for a in ATTN])
 def test_attention_matches_the_oracle(i, path):
     name, seqs, hq, hkv, page = ATTN[i]
