@@ -612,10 +612,11 @@ int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, 
   const bool single_prefill = p.num_seqs == 1 && (long long)p.T * p.G > kVerifyRows;
   p.fused_verify = tc && path != 3 && !single_prefill && (long long)p.num_seqs * p.Hkv <= kFusedMaxBlocks &&
                    max_tiles < (1 << 16) && (long long)p.num_seqs * p.Hkv * (max_tiles + fixed_cost(0)) < (1LL << 31);
-  // Single tokens (no more tokens than sequences) of groups of at most 16 heads go to the
-  // warp-level decode kernel: a sequence with more rows is served in passes, correctly but with
-  // its keys read once per 16 rows.
-  const bool decode = tc && path != 2 && p.T <= p.num_seqs && p.G <= 16;
+  // Single tokens (no more tokens than sequences) of groups of at most 8 heads go to the warp-level
+  // decode kernel: 37.0 us against 43.7 for the tcgen05 kernel at 32 sequences of 9000 keys and 8 heads,
+  // 150 against 189 at 256 of 8192. At 16 heads the warp-level kernel took 65 against 44. (A
+  // sequence with more rows is served in passes, correctly but with its keys read once per 8 rows.)
+  const bool decode = tc && path != 2 && p.T <= p.num_seqs && p.G <= 8;
   int launched = 0, used = 0;
   cudaError_t e;
   for (int c = 0; c < kNumClasses; ++c) {

@@ -1,14 +1,19 @@
 // fp4_decode.cu -- warp-level attention kernel over a 4-bit paged KV cache (fp4.cuh), bf16 Q, for
-// batches of single tokens: the verify class's blocks, 8 or 16 of their rows at a time.
+// batches of single tokens of at most 8 heads per kv head: the verify class's blocks, 8 rows at a time.
 //
-// With 16 query rows or fewer the tcgen05 kernel (fp4_tc.cu) spends most of its instructions on
-// handing widened tiles from warp to warp. Here no tile changes hands: each of the CTA's eight
-// warps takes every eighth 16-key block of the item, copies it into its own ring of shared-memory
-// stages (one bulk copy of 2304 bytes each for K and V), widens it straight into the A fragments
-// of mma.sync m16n8k16, and keeps its own running maxima, sums and O^T; the warps meet once per
-// item. The legacy tensor path does 1024 multiply-adds a cycle (8.25 cycles per m16n8k16 and
-// scheduler, measured): 1056 cycles per 128 keys at 16 rows, below the ~1600 that the keys take to
-// arrive from HBM.
+// With so few rows the tcgen05 kernel (fp4_tc.cu) spends most of its instructions on handing widened
+// tiles from warp to warp. Here no tile changes hands: each of the CTA's 16 warps takes every
+// 16th 16-key block of the item, copies it into its own ring of shared-memory stages (one bulk copy of
+// 2304 bytes each for K and V), widens it straight into the A fragments of mma.sync m16n8k16, and
+// keeps its own running maxima, sums and O^T; the warps meet once per item. What bounds it is widening:
+// a block takes 128 conversions, 64 permutes and 128 products in f16x2, of which the first two
+// share a pipe at 2.07 cycles a warp instruction (measured): ~1000 cycles per 128 keys and SM, below the
+// ~1600 that those keys take to arrive from HBM; ~2250 are measured, the rest waiting (four warps
+// per scheduler hide only part of the chain load, convert, multiply, MMA).
+// Time (graph replays, 8 heads): 14.5 us for one sequence of 600 keys, 36.2 for 32 of 9000 (12.2 at the
+// HBM rate), 150 for 256 of 8192 (89). The tcgen05 kernel: 17.0, 43.7, 189. With 8 warps of twice the registers
+// this kernel took twice as long per key; with 16 rows a pass (12 warps, O^T of 128 registers, spills) 65 us
+// against the tcgen05 kernel's 44 at 32 x 9000 keys, so groups of more than 8 heads go there.
 //
 //   S^T[16 keys, rows] = K Q^T    A = K: lane (g, t) = (lane / 4, lane % 4) holds fragment rows g and
 //       g + 8 and widens 32 code bytes of each of those two keys: k-step s takes bytes 32t + 2s, 2s + 1, so
@@ -40,14 +45,19 @@ namespace {
 
 using namespace tc;
 
-constexpr int kDWarps = 8, kDThreads = kDWarps * 32;
-constexpr int kDStages = 4;
 constexpr uint32_t kDStage = 2 * kFp4BlockBytes;  // a 16-key block of K, then of V
-constexpr int kDRows = 16;                        // rows of a pass, at most
+constexpr int kDRows = 8;                         // rows of a pass
 constexpr float kDTau = 4.f, kDSigma = 4.f, kDMInit = -3.0e38f;
 // A staged Q row: its 16-byte chunk (t, j) of d 64 t + 8 j .. + 7 at 64 j + 16 t, so that the four lanes of
 // a fragment row read 64 contiguous bytes; the pitch puts the next row in the other 16 banks.
 constexpr uint32_t kQPitch = kHeadDim * 2 + 64;
+
+// Two stages: a warp's next block is in flight while it works on one (16 x 2 x 4608 bytes in all).
+constexpr int kDWarps = 16, kDThreads = kDWarps * 32, kDStages = 2;
+constexpr uint32_t kOffQ = kDWarps * kDStages * kDStage;
+constexpr uint32_t kOffMisc = kOffQ + kDRows * kQPitch;
+static_assert(kDWarps * 16 * 32 * sizeof(float4) <= kOffQ, "the warps' O^T meets in the stages");
+static_assert(sizeof(self_plan::Scratch) <= kOffQ, "the self-plan scratch fits the stages");
 
 template <bool kFused>
 struct DMisc {
@@ -56,18 +66,12 @@ struct DMisc {
   alignas(16) float cs[kDRows];
   alignas(16) int lim[kDRows];
   alignas(16) long long out_off[kDRows];
-  alignas(16) float lse[kDRows];
   alignas(8) uint64_t full[kDWarps][kDStages];
   uint64_t never;
   int abort_flag, merge_flag, fcount;
   int4 fitem[kFused ? kFusedMaxBlocks : 1];
   int4 fseq[kFused ? kFusedMaxBlocks : 1];
 };
-constexpr uint32_t kDOffQ = kDWarps * kDStages * kDStage;
-constexpr uint32_t kDOffMisc = kDOffQ + kDRows * kQPitch;
-static_assert(sizeof(self_plan::Scratch) <= kDOffQ, "the self-plan scratch fits the stages");
-// the warps' O^T meet in the stages, one quarter of the fragments at a time
-static_assert(kDWarps * 4 * 2 * 4 * 32 * 4 <= kDOffQ, "a quarter of the warps' fragments fits the stages");
 
 struct DItem {
   int block, seq, kvh, nrows, nsplit, split, slot_base, key0, kv_hi, q0, qn, L;
@@ -125,13 +129,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 
 }  // namespace
 
-// kNT: 8-row groups of a pass.
-template <int kNT, bool kFused>
+template <bool kFused>
 __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Pointers ptr, ClassPlan cp) {
-  constexpr int kPassRows = 8 * kNT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  DMisc<kFused>& ms = *reinterpret_cast<DMisc<kFused>*>(smem + kDOffMisc);
+  DMisc<kFused>& ms = *reinterpret_cast<DMisc<kFused>*>(smem + kOffMisc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   volatile int* abort_flag = &ms.abort_flag;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -173,8 +175,8 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
     const int32_t* bt_row = ptr.block_table + (size_t)I.seq * p.bt_stride;
     const uint8_t* khead = static_cast<const uint8_t*>(ptr.k) + (long long)I.kvh * p.k_sh;
     const uint8_t* vhead = static_cast<const uint8_t*>(ptr.v) + (long long)I.kvh * p.v_sh;
-    for (int row0 = 0; row0 < I.nrows; row0 += kPassRows) {
-      const int rows = min(kPassRows, I.nrows - row0);
+    for (int row0 = 0; row0 < I.nrows; row0 += kDRows) {
+      const int rows = min(kDRows, I.nrows - row0);
       // ---- copies: this warp's i-th block of the piece goes to stage (used + i) % kDStages. Lane
       // (i % 32) holds its page, the next 32 are read when these run out.
       int page = -1, window = -1;
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
       for (int i = 0; i < min(mine, kDStages); ++i) issue(i);
 
       // ---- Q rows to shared memory in f16, each times a power of two (to [2^14, 2^15))
-      for (int r = warp; r < kPassRows; r += kDWarps) {
+      for (int r = warp; r < kDRows; r += kDWarps) {
         uint4 v = make_uint4(0, 0, 0, 0);
         const RowMap m = map_row(row0 + r, p.G, I.kvh);
         if (r < rows)
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
-        *reinterpret_cast<uint4*>(smem + kDOffQ + r * kQPitch + (lane & 7) * 64 + (lane >> 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(smem + kOffQ + r * kQPitch + (lane & 7) * 64 + (lane >> 3) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         if (lane == 0) {
           ms.cs[r] = p.score_scale_log2 * __uint_as_float(e > 14 ? (uint32_t)(e - 14) << 23 : 0x00400000u);
           ms.lim[r] = r < rows ? I.L - I.qn + m.t : -1;
@@ -226,24 +228,20 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
       }
       __syncthreads();
 
-      // ---- this lane's rows 2t, 2t + 1 of each 8-row group
-      float c[kNT][2], ref[kNT][2], sum[kNT][2];
-      int lim[kNT][2];
+      // ---- this lane's rows 2t, 2t + 1
+      float c[2], ref[2], sum[2];
+      int lim[2];
       const int min_lim = I.L - I.qn + map_row(row0, p.G, I.kvh).t;
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+      for (int b = 0; b < 2; ++b) {
+        c[b] = ms.cs[2 * t + b];
+        lim[b] = ms.lim[2 * t + b];
+        ref[b] = 2 * t + b < rows ? kDMInit : 0.f;  // padding rows never ask for a new one
+        sum[b] = 0.f;
+      }
+      float o[16][4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          c[n][b] = ms.cs[8 * n + 2 * t + b];
-          lim[n][b] = ms.lim[8 * n + 2 * t + b];
-          ref[n][b] = 8 * n + 2 * t + b < rows ? kDMInit : 0.f;  // padding rows never ask for a new one
-          sum[n][b] = 0.f;
-        }
-      float o[16][kNT][4];
-#pragma unroll
-      for (int m = 0; m < 16; ++m)
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
+      for (int m = 0; m < 16; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
 
 #pragma unroll 1
       for (int i = 0; i < mine; ++i) {
@@ -255,17 +253,17 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
         const uint8_t* vb = kb + kFp4BlockBytes;
         const int key0 = I.key0 + (i * kDWarps + warp) * kFp4Block;
         // S^T = K Q^T
-        float s[kNT][4];
+        float s[4], s1[4];  // two chains of products, added up after
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        for (int e = 0; e < 4; ++e) s[e] = s1[e] = 0.f;
         const uint32_t sc0 = *reinterpret_cast<const uint32_t*>(kb + tok0 * kFp4Row + kFp4Codes + 4 * t);
         const uint32_t sc1 = *reinterpret_cast<const uint32_t*>(kb + (tok0 + 2) * kFp4Row + kFp4Codes + 4 * t);
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {  // 16 of this lane's code bytes: 8 k-steps
           const uint4 x0 = *reinterpret_cast<const uint4*>(kb + tok0 * kFp4Row + 32 * t + 16 * h);
           const uint4 x1 = *reinterpret_cast<const uint4*>(kb + (tok0 + 2) * kFp4Row + 32 * t + 16 * h);
           const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
-          const uint32_t s0 = fp4::scales2(h ? sc0 >> 16 : sc0), s1 = fp4::scales2(h ? sc1 >> 16 : sc1);
+          const uint32_t f0 = fp4::scales2(h ? sc0 >> 16 : sc0), f1 = fp4::scales2(h ? sc1 >> 16 : sc1);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // a word of codes: two k-steps
             uint32_t h0[4], h1[4];
@@ -273,67 +271,57 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
             fp4::codes4(w1[k], h1);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-              h0[b] = k < 2 ? fp4::mul_f16x2_lo(h0[b], s0) : fp4::mul_f16x2_hi(h0[b], s0);
-              h1[b] = k < 2 ? fp4::mul_f16x2_lo(h1[b], s1) : fp4::mul_f16x2_hi(h1[b], s1);
+              h0[b] = k < 2 ? fp4::mul_f16x2_lo(h0[b], f0) : fp4::mul_f16x2_hi(h0[b], f0);
+              h1[b] = k < 2 ? fp4::mul_f16x2_lo(h1[b], f1) : fp4::mul_f16x2_hi(h1[b], f1);
             }
             const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-              // d = 64 t + 32 h + 8 k + 0 .. 7 of row 8 n + g
-              const uint4 q = *reinterpret_cast<const uint4*>(smem + kDOffQ + (8 * n + g) * kQPitch + (4 * h + k) * 64 + t * 16);
-              mma_f16_sync(s[n], a0, q.x, q.y);
-              mma_f16_sync(s[n], a1, q.z, q.w);
-            }
+            // d = 64 t + 32 h + 8 k + 0 .. 7 of row g
+            const uint4 q = *reinterpret_cast<const uint4*>(smem + kOffQ + g * kQPitch + (4 * h + k) * 64 + t * 16);
+            mma_f16_sync(s, a0, q.x, q.y);
+            mma_f16_sync(s1, a1, q.z, q.w);
           }
         }
-        // x = s c - m + sigma; keys of this lane: tok0 (s[..][0], s[..][1]) and tok0 + 2
+        // x = s c - m + sigma; keys of this lane: tok0 (s[0], s[1]) and tok0 + 2
         const int ka = key0 + tok0, kc = ka + 2;
         const bool need_mask = key0 + kFp4Block > I.kv_hi || key0 + kFp4Block - 1 > min_lim;
         float top = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            s[n][b] *= c[n][b];
-            s[n][2 + b] *= c[n][b];
-            if (need_mask) {
-              if (ka >= I.kv_hi || ka > lim[n][b]) s[n][b] = -INFINITY;
-              if (kc >= I.kv_hi || kc > lim[n][b]) s[n][2 + b] = -INFINITY;
-            }
-            top = max3f(top, s[n][b] - ref[n][b], s[n][2 + b] - ref[n][b]);
+        for (int b = 0; b < 2; ++b) {
+          s[b] = (s[b] + s1[b]) * c[b];
+          s[2 + b] = (s[2 + b] + s1[2 + b]) * c[b];
+          if (need_mask) {
+            if (ka >= I.kv_hi || ka > lim[b]) s[b] = -INFINITY;
+            if (kc >= I.kv_hi || kc > lim[b]) s[2 + b] = -INFINITY;
           }
+          top = max3f(top, s[b] - ref[b], s[2 + b] - ref[b]);
+        }
         if (__any_sync(0xffffffffu, top > kDTau)) {
           // new references: the exact maxima of this block's scores
 #pragma unroll
-          for (int n = 0; n < kNT; ++n)
+          for (int b = 0; b < 2; ++b) {
+            float mx = fmaxf(s[b], s[2 + b]);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              float mx = fmaxf(s[n][b], s[n][2 + b]);
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(ref[b], mx);
+            const float alpha = ex2(ref[b] - mn);
+            ref[b] = mn;
+            sum[b] *= alpha;
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-              const float mn = fmaxf(ref[n][b], mx);
-              const float alpha = ex2(ref[n][b] - mn);
-              ref[n][b] = mn;
-              sum[n][b] *= alpha;
-#pragma unroll
-              for (int m = 0; m < 16; ++m) {
-                o[m][n][b] *= alpha;
-                o[m][n][2 + b] *= alpha;
-              }
+            for (int m = 0; m < 16; ++m) {
+              o[m][b] *= alpha;
+              o[m][2 + b] *= alpha;
             }
-        }
-        uint32_t pb[kNT][2];
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          float e[4];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            e[b] = ex2(s[n][b] - ref[n][b & 1] + kDSigma);
-            sum[n][b & 1] += e[b];
           }
-          pb[n][0] = transpose8(pack_f16x2(e[0], e[1]));
-          pb[n][1] = transpose8(pack_f16x2(e[2], e[3]));
         }
+        uint32_t pb[2];
+        float e[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          e[b] = ex2(s[b] - ref[b & 1] + kDSigma);
+          sum[b & 1] += e[b];
+        }
+        pb[0] = transpose8(pack_f16x2(e[0], e[1]));
+        pb[1] = transpose8(pack_f16x2(e[2], e[3]));
         // O^T += V^T P^T; tokens past the piece's end (stale slots) get zero scales
         const uint32_t live = 4 * t + 4 <= I.kv_hi - key0 ? 0xffffffffu
                               : 4 * t >= I.kv_hi - key0   ? 0u
@@ -349,8 +337,7 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
                                  fp4::mul_f16x2(__byte_perm(h[0], h[1], 0x7632), s01),
                                  fp4::mul_f16x2(__byte_perm(h[2], h[3], 0x5410), s23),
                                  fp4::mul_f16x2(__byte_perm(h[2], h[3], 0x7632), s23)};
-#pragma unroll
-          for (int n = 0; n < kNT; ++n) mma_f16_sync(o[m][n], a, pb[n][0], pb[n][1]);
+          mma_f16_sync(o[m], a, pb[0], pb[1]);
         }
         __syncwarp();  // every lane has read the stage
         if (i + kDStages < mine) issue(i + kDStages);
@@ -359,74 +346,60 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
 
       // ---- the warps meet: references, sums, O^T
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+      for (int b = 0; b < 2; ++b) {
+        float l = sum[b];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float l = sum[n][b];
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-          if (g == 0) {
-            ms.m[warp][8 * n + 2 * t + b] = ref[n][b];
-            ms.l[warp][8 * n + 2 * t + b] = l;
-          }
+        for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (g == 0) {
+          ms.m[warp][2 * t + b] = ref[b];
+          ms.l[warp][2 * t + b] = l;
         }
+      }
       __syncthreads();  // (also: every warp's stages are consumed)
       const bool split = I.nsplit > 1;
       const int slot = I.slot_base + I.split;
-      float mine_w[kNT][2], inv[kNT][2];
+      float mine_w[2], inv[2];
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+      for (int b = 0; b < 2; ++b) {
+        const int r = 2 * t + b;
+        float M = kDMInit, L = 0.f;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int r = 8 * n + 2 * t + b;
-          float M = kDMInit, L = 0.f;
+        for (int w = 0; w < kDWarps; ++w) M = fmaxf(M, ms.m[w][r]);
 #pragma unroll
-          for (int w = 0; w < kDWarps; ++w) M = fmaxf(M, ms.m[w][r]);
-#pragma unroll
-          for (int w = 0; w < kDWarps; ++w) L += ms.l[w][r] * ex2(ms.m[w][r] - M);
-          mine_w[n][b] = ex2(ref[n][b] - M);
-          inv[n][b] = L > 0.f ? __fdividef(split ? 1.f : p.out_scale, L) : L == 0.f ? 0.f : L;  // NaN stays
-          if (split && warp == 0 && g == 0) {
-            const float lse = L > 0.f ? M - kDSigma + log2f(L) : L == 0.f ? -INFINITY : L;
-            if (r < rows) slot_lse(cp, slot)[row0 + r] = lse;
-          }
+        for (int w = 0; w < kDWarps; ++w) L += ms.l[w][r] * ex2(ms.m[w][r] - M);
+        mine_w[b] = ex2(ref[b] - M);
+        inv[b] = L > 0.f ? __fdividef(split ? 1.f : p.out_scale, L) : L == 0.f ? 0.f : L;  // NaN stays
+        if (split && warp == 0 && g == 0) {
+          const float lse = L > 0.f ? M - kDSigma + log2f(L) : L == 0.f ? -INFINITY : L;
+          if (r < rows) slot_lse(cp, slot)[row0 + r] = lse;
         }
-      // A quarter of the fragments at a time through shared memory: warp w adds up fragment
-      // 4 q + w / 2, 8-row group w % 2 (or, with one group, warps 0 .. 3 fragment 4 q + w).
-      float* meet = reinterpret_cast<float*>(smem);  // [warp][fragment of 4][group][4][32 lanes]
-      constexpr int kFrag = kNT * 4 * 32;
+      }
+      // Through shared memory: warp m adds up fragment m of all warps.
+      static_assert(kDWarps == 16, "a warp to each fragment of O^T");
+      float4* meet = reinterpret_cast<float4*>(smem) + lane;  // [warp][fragment][32 lanes]
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int m = 0; m < 16; ++m)
+        meet[(warp * 16 + m) * 32] =
+            make_float4(o[m][0] * mine_w[0], o[m][1] * mine_w[1], o[m][2] * mine_w[0], o[m][3] * mine_w[1]);
+      __syncthreads();
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+      for (int w = 0; w < kDWarps; ++w) {
+        const float4 x = meet[(w * 16 + warp) * 32];
+        acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
+      }
+      const int byte = 8 * warp + g;  // d = 2 byte (acc[0], acc[1]) and 2 byte + 1
 #pragma unroll
-          for (int n = 0; n < kNT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              meet[(warp * 4 + m) * kFrag + (n * 4 + e) * 32 + lane] = o[4 * q + m][n][e] * mine_w[n][e & 1];
-        __syncthreads();
-        const int fm = kNT == 2 ? warp >> 1 : warp, n = kNT == 2 ? warp & 1 : 0;
-        if (fm < 4) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int w = 0; w < kDWarps; ++w)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] += meet[(w * 4 + fm) * kFrag + (n * 4 + e) * 32 + lane];
-          const int byte = 8 * (4 * q + fm) + g;  // d = 2 byte (acc[0], acc[1]) and 2 byte + 1
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int r = 8 * n + 2 * t + b;
-            const float k = kNT == 2 && n ? inv[kNT - 1][b] : inv[0][b];
-            if (r < rows) {
-              if (split)
-                reinterpret_cast<uint32_t*>(slot_o(cp, slot))[(row0 + r) * (kHeadDim / 2) + byte] = pack_f16x2(acc[b] * k, acc[2 + b] * k);
-              else
-                *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(ptr.out) + ms.out_off[r] + 2 * byte) =
-                    pack_bf16x2(acc[b] * k, acc[2 + b] * k);
-            }
-          }
+      for (int b = 0; b < 2; ++b) {
+        const int r = 2 * t + b;
+        if (r < rows) {
+          if (split)
+            reinterpret_cast<uint32_t*>(slot_o(cp, slot))[(row0 + r) * (kHeadDim / 2) + byte] =
+                pack_f16x2(acc[b] * inv[b], acc[2 + b] * inv[b]);
+          else
+            *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(ptr.out) + ms.out_off[r] + 2 * byte) =
+                pack_bf16x2(acc[b] * inv[b], acc[2 + b] * inv[b]);
         }
-        __syncthreads();
       }
       fence_proxy_async_smem();  // the stages were written by these threads: the next copies come after
       __syncthreads();
@@ -487,10 +460,10 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
 
 namespace {
 
-template <int kNT, bool kFused>
+template <bool kFused>
 int launch(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStream_t stream) {
-  auto kern = fp4_decode_kernel<kNT, kFused>;
-  constexpr size_t smem = kDOffMisc + sizeof(DMisc<kFused>) + 128;
+  auto kern = fp4_decode_kernel<kFused>;
+  constexpr size_t smem = kOffMisc + sizeof(DMisc<kFused>) + 128;
   static_assert(smem <= 232448, "shared memory of one CTA");
   static bool done[64] = {};  // one per instance of this template
   int dev = 0;
@@ -514,8 +487,7 @@ int launch(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStrea
 }  // namespace
 
 int launch_fp4_decode(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStream_t stream) {
-  if (p.G <= 8) return p.fused_verify ? launch<1, true>(p, ptr, cp, stream) : launch<1, false>(p, ptr, cp, stream);
-  return p.fused_verify ? launch<2, true>(p, ptr, cp, stream) : launch<2, false>(p, ptr, cp, stream);
+  return p.fused_verify ? launch<true>(p, ptr, cp, stream) : launch<false>(p, ptr, cp, stream);
 }
 
 }  // namespace pgqa

@@ -29,7 +29,7 @@ int launch_bf16_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, c
 int launch_fp4_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, int cls, cudaStream_t stream,
                   bool dependent);
 // The verify class of a batch of single tokens over 4-bit caches (fp4_decode.cu), groups of at
-// most 16 heads. 1, or -1 on a launch error.
+// most 8 heads. 1, or -1 on a launch error.
 int launch_fp4_decode(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStream_t stream);
 const char* tc_last_error();
 void set_tc_error(const char* msg);
