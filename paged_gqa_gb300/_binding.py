@@ -41,9 +41,11 @@ _lock = threading.Lock()
 _lib = None
 
 # Descriptors are packed into a per-thread array of pg_tensor and passed by address: one
-# struct.pack_into per tensor instead of a ctypes Structure built field by field.
-_DESC_FMT = struct.Struct("=Qii4q4q")
-assert ctypes.sizeof(PgTensor) == _DESC_FMT.size == 80
+# struct.pack_into per tensor, by its number of dims, instead of a ctypes Structure built field
+# by field.
+_DESC_FMT = [struct.Struct(f"=Qii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x") for n in range(5)]
+assert all(ctypes.sizeof(PgTensor) == f.size == 80 for f in _DESC_FMT)
+_PACK_INTO = [f.pack_into for f in _DESC_FMT]
 _tls = threading.local()
 
 
@@ -51,7 +53,8 @@ def _desc_buf():
     b = getattr(_tls, "buf", None)
     if b is None:
         arr = (PgTensor * 10)()
-        b = _tls.buf = (arr, ctypes.addressof(arr), memoryview(arr).cast("B"))
+        base = ctypes.addressof(arr)
+        b = _tls.buf = (arr, [base + 80 * i for i in range(10)], memoryview(arr).cast("B"))
     return b
 
 
@@ -117,6 +120,7 @@ _DTYPES = {torch.bfloat16: PG_BF16, torch.float16: PG_F16, torch.int32: PG_I32, 
            torch.uint8: PG_E4M3}
 if hasattr(torch, "float8_e4m3fn"):
     _DTYPES[torch.float8_e4m3fn] = PG_E4M3
+_DTYPES_FP4 = {**_DTYPES, torch.uint8: PG_FP4}  # in the 4-bit calls uint8 is a 4-bit cache
 
 
 def _desc(t: Optional[torch.Tensor], dtype: Optional[int] = None) -> PgTensor:
@@ -135,24 +139,20 @@ def _desc(t: Optional[torch.Tensor], dtype: Optional[int] = None) -> PgTensor:
     return d
 
 
-def _pack(*tensors):
+def _pack(*tensors, dtypes=_DTYPES):
     """Addresses of pg_tensor descriptors of the given tensors, valid until the next call
     from this thread (the library copies what it needs before it returns)."""
-    arr, base, mv = _desc_buf()
-    pack, dt = _DESC_FMT.pack_into, _DTYPES
-    out = []
-    for i, t in enumerate(tensors):
-        off = 80 * i
-        n = t.dim()
+    _, addresses, mv = _desc_buf()
+    off = 0
+    for t in tensors:
+        sh = t.shape
+        n = len(sh)
         if n > 4:
             raise ValueError("at most 4 dims")
-        sh, st = tuple(t.shape), t.stride()
-        if n < 4:
-            sh = sh + (0,) * (4 - n)
-            st = st + (0,) * (4 - n)
-        pack(mv, off, t.data_ptr() if t.numel() > 0 else 0, dt[t.dtype], n, *sh, *st)
-        out.append(base + off)
-    return out
+        # (the data pointer of a tensor without elements is 0)
+        _PACK_INTO[n](mv, off, t.data_ptr(), dtypes[t.dtype], n, *sh, *t.stride())
+        off += 80
+    return addresses[:len(tensors)]
 
 
 def _stream(stream) -> int:
@@ -220,20 +220,16 @@ def _on_device(*tensors) -> None:
     """The tensors are on the current CUDA device (the library launches there)."""
     cur = torch.cuda.current_device()
     for t in tensors:
-        d = t.device
-        if d.type != "cuda" or d.index != cur:
-            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{cur}), got one on {d}")
+        if t.get_device() != cur:  # (-1 on the CPU)
+            raise ValueError(f"every tensor must be on the current CUDA device (cuda:{cur}), got one on {t.device}")
 
 
 def _pack_fp4(first_cache: int, *tensors):
     """_pack with tensors[first_cache] and the next one as 4-bit caches (uint8 rows of 144 bytes)."""
     for t in tensors[first_cache:first_cache + 2]:
-        if t.dtype != torch.uint8:
+        if t.dtype is not torch.uint8:
             raise ValueError(f"4-bit caches are uint8 tensors, got {t.dtype}")
-    out = _pack(*tensors)
-    arr = _desc_buf()[0]
-    arr[first_cache].dtype = arr[first_cache + 1].dtype = PG_FP4
-    return out
+    return _pack(*tensors, dtypes=_DTYPES_FP4)
 
 
 def paged_gqa_cache_write_fp4(k_new, v_new, k_cache, v_cache, block_table, seq_lens, query_start_loc,
