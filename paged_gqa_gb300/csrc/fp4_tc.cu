@@ -50,11 +50,6 @@ using namespace tc;
 
 constexpr int kSoftWarp0 = 4, kSoftWarps = 16, kSoftThreads = kSoftWarps * 32;
 constexpr int kWideWarp0 = kSoftWarp0 + kSoftWarps;
-constexpr int kKWarps = 4, kVWarps = 8;  // that widen K, V
-constexpr int kVWarp0 = kWideWarp0 + kKWarps;
-constexpr int kWarps = kVWarp0 + kVWarps, kThreads = kWarps * 32;
-constexpr int kLaunchRegs = 64;
-static_assert(kThreads == 1024 && kThreads * kLaunchRegs == 65536, "one CTA fills the register file");
 constexpr float kTau = 4.f;         // rescale when a score exceeds the reference by 2^kTau
 constexpr float kSigma = 4.f;       // P is scaled by 2^kSigma (at most 2^8; f16 holds 2^-24)
 constexpr float kMInit = -3.0e38f;  // reference of a row before its first key
@@ -68,15 +63,21 @@ constexpr uint32_t kChunkCols = 64;              // TMEM columns of half a tile 
 template <int kN>
 struct Cfg {
   static constexpr int kCols = kN / 4;  // rows per softmax thread
-  // Registers of the warpgroups (their sum is what the launch gives: kLaunchRegs a thread).
-  static constexpr int kSoftRegs = kN == 64 ? 72 : 88, kWideRegs = kN == 64 ? 56 : 40, kOtherRegs = kN == 64 ? 56 : 40;
-  static_assert(kSoftWarps * kSoftRegs + (kKWarps + kVWarps) * kWideRegs + kSoftWarp0 * kOtherRegs == kWarps * kLaunchRegs,
-                "register split");
-  static constexpr int kKStages = kN == 64 ? 3 : 2, kVStages = kN == 64 ? 3 : 2;
-  static constexpr int kSBufs = kN == 64 ? 2 : 1;
   // The widened operands in TMEM go by halves of 64 columns: 128 d of the 128 keys of K, 64 keys
   // of both tiles of V. With 64 rows K and V have two each; with 128 rows they share two.
   static constexpr bool kShared = kN == 128;
+  // Warps that widen: 4 K and 8 V side by side, or, where the columns allow only one at a time,
+  // the same 8 both in turn.
+  static constexpr int kKWarps = kShared ? 8 : 4, kVWarps = 8;
+  static constexpr int kVWarp0 = kWideWarp0 + (kShared ? 0 : kKWarps);
+  static constexpr int kWarps = kVWarp0 + kVWarps, kThreads = kWarps * 32;
+  // Registers of the warpgroups (their sum is what the launch gives: kLaunchRegs a thread).
+  static constexpr int kLaunchRegs = kShared ? 72 : 64;
+  static constexpr int kSoftRegs = kShared ? 96 : 72, kWideRegs = kShared ? 40 : 56, kOtherRegs = kShared ? 40 : 56;
+  static_assert(kSoftWarps * kSoftRegs + (kWarps - kWideWarp0) * kWideRegs + kSoftWarp0 * kOtherRegs == kWarps * kLaunchRegs &&
+                    kThreads * kLaunchRegs <= 65536, "register split");
+  static constexpr int kKStages = kN == 64 ? 3 : 2, kVStages = kN == 64 ? 3 : 2;
+  static constexpr int kSBufs = kN == 64 ? 2 : 1;
   static constexpr uint32_t kColS = 0, kColO = 128, kColK = 128 + 2 * kN, kColV = kColK + (kN == 64 ? 128 : 0);
   static_assert(kSBufs * kN <= 128 && kColV + 128 <= 512, "TMEM columns");
   static constexpr uint32_t kQQuarter = kN * 128;   // [kN rows][64 d] f16, 128-byte swizzle
@@ -179,7 +180,7 @@ __device__ __forceinline__ uint32_t token_mask(int n, int w) {
 }  // namespace
 
 template <int kN, bool kFused>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<kN>::kThreads, 1)
 fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   using C = Cfg<kN>;
   constexpr int kCols = C::kCols;
@@ -203,15 +204,15 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kKStages; ++s) {
       mbar_init(bar(ms.k_full[s]), 1);
-      mbar_init(bar(ms.k_empty[s]), kKWarps);
+      mbar_init(bar(ms.k_empty[s]), C::kKWarps);
     }
     for (int s = 0; s < C::kVStages; ++s) {
       mbar_init(bar(ms.v_full[s]), 1);
-      mbar_init(bar(ms.v_empty[s]), kVWarps);
+      mbar_init(bar(ms.v_empty[s]), C::kVWarps);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(bar(ms.ak_full[b]), kKWarps);
-      mbar_init(bar(ms.av_full[b]), kVWarps);
+      mbar_init(bar(ms.ak_full[b]), C::kKWarps);
+      mbar_init(bar(ms.av_full[b]), C::kVWarps);
       mbar_init(bar(ms.ak_free[b]), 1);
       mbar_init(bar(ms.av_free[b]), 1);
       mbar_init(bar(ms.av_go[b]), 1);
@@ -644,8 +645,9 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       tc_fence_before();
       arrive(full);
     };
-    // K of tile g: this thread's key, 64 d at a time
+    // K of tile g: this thread's key, 64 d at a time (of both segments of a half, or of one)
     uint32_t kst = 0, kph = 0;  // stage and its phase
+    const int kseg0 = C::kShared ? (warp - kWideWarp0) >> 2 : 0;  // of a half's two 64-d segments
     auto widen_k = [&](uint32_t g) {
       wait(bar(ms.k_full[0]) + 8 * kst, kph);
       const uint8_t* row = smem + C::kOffK + kst * kTile + ti * kFp4Row;
@@ -654,7 +656,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         k_cols_free(g, h);
         tc_fence_after();
 #pragma unroll 1
-        for (int seg = 2 * h; seg < 2 * h + 2; ++seg) {
+        for (int seg = 2 * h + kseg0; seg < 2 * h + (C::kShared ? kseg0 + 1 : 2); ++seg) {
           const uint4* src = reinterpret_cast<const uint4*>(row + 32 * seg);
           const uint4 x[2] = {src[0], src[1]};
           const uint32_t sc = *reinterpret_cast<const uint32_t*>(row + kFp4Codes + 4 * seg);
@@ -686,7 +688,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     // First these warps' threads widen the tile's scales once for all (8 bytes each), keys from
     // n_keys on (stale slots, or never copied) to zeros.
     uint32_t vst = 0, vph = 0;
-    const int vt = (warp - kVWarp0) * 32 + lane;  // 0..255
+    const int vt = (warp - C::kVWarp0) * 32 + lane;  // 0..255
     const int half = (vt >> 7) & 1;               // which 32 keys of a half tile
     auto widen_v = [&](uint32_t g, bool last, int n_keys) {
       wait(bar(ms.v_full[0]) + 8 * vst, vph);
@@ -707,7 +709,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           dst[k] = make_uint4(fp4::scales2(e), fp4::scales2(o), fp4::scales2(e >> 16), fp4::scales2(o >> 16));
         }
       }
-      named_barrier(8, kVWarps * 32);
+      named_barrier(8, C::kVWarps * 32);
 #pragma unroll 1
       for (int j = 0; j < 2; ++j) {
         v_cols_free(g, last, j);
@@ -740,15 +742,19 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       }
     };
     // the CTA's tiles
-    const bool is_k = warp < kVWarp0;
+    const bool is_k = warp < C::kVWarp0, is_v = warp >= C::kVWarp0;
     uint32_t g = 0;
     for (int it = item_begin; it < item_end; ++it) {
       const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
       int left = I.kv_hi - I.tile_begin * kTileKeys;  // keys from tile j on that are there
 #pragma unroll 1
       for (int j = 0; j < I.ntiles; ++j, ++g, left -= kTileKeys) {
-        if (is_k) widen_k(g);
-        else widen_v(g, it + 1 == item_end && j + 1 == I.ntiles, left);
+        const bool last = it + 1 == item_end && j + 1 == I.ntiles;
+        // one after the other: K a tile ahead
+        const uint32_t k_end = C::kShared ? g + (last ? 1 : 2) : is_k ? g + 1 : g;
+#pragma unroll 1
+        for (uint32_t kg = C::kShared && g > 0 ? g + 1 : g; kg < k_end; ++kg) widen_k(kg);
+        if (is_v) widen_v(g, last, left);
       }
     }
   } else {
@@ -945,16 +951,16 @@ int launch(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStrea
     // if the kernel starts with exactly kLaunchRegs registers per thread, so never launch otherwise.
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kern);
-    if (e != cudaSuccess || fa.numRegs != kLaunchRegs) {
+    if (e != cudaSuccess || fa.numRegs != Cfg<kN>::kLaunchRegs) {
       char buf[160];
       snprintf(buf, sizeof buf, "4-bit attention kernel built with %d registers per thread; its warpgroup split needs %d",
-               e == cudaSuccess ? fa.numRegs : -1, kLaunchRegs);
+               e == cudaSuccess ? fa.numRegs : -1, Cfg<kN>::kLaunchRegs);
       set_tc_error(buf);
       return -1;
     }
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
-  e = launch_pdl(dependent, kern, cp.num_ctas, kThreads, smem, stream, p, ptr, cp);
+  e = launch_pdl(dependent, kern, cp.num_ctas, Cfg<kN>::kThreads, smem, stream, p, ptr, cp);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {
     char buf[160];
