@@ -98,7 +98,6 @@ struct DeviceState {
   void* ws4 = nullptr;
   size_t ws4_bytes = 0;
   cudaEvent_t ws4_done = nullptr;
-  cudaStream_t ws4_stream = nullptr;
   bool ws4_used = false;
 };
 DeviceState g_dev[kMaxDevices];
@@ -745,9 +744,9 @@ int attn_fp4(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
       e = cudaMemsetAsync(ds->ws4, 0, want, stream);
       if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace)");
     }
-    // One workspace, any streams: a call on another stream than the last one's waits for that
-    // one (the per-thread default stream's handle names another stream in every thread).
-    if (ds->ws4_used && (ds->ws4_stream != stream || stream == cudaStreamPerThread)) {
+    // One workspace, any streams: a call waits for the last one, whose stream may be another (also
+    // under the same handle, which a destroyed stream or another thread's default one can have had).
+    if (ds->ws4_used) {
       e = cudaStreamWaitEvent(stream, ds->ws4_done, 0);
       if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
     }
@@ -755,7 +754,6 @@ int attn_fp4(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
     // also after a failed launch: what was launched before it may be running
     e = cudaEventRecord(ds->ws4_done, stream);
     if (e != cudaSuccess && st == PG_OK) return cuda_fail(e, "cudaEventRecord");
-    ds->ws4_stream = stream;
     ds->ws4_used = true;
   }
   if (st == PG_OK) t_last_error.clear();

@@ -165,6 +165,10 @@ ATTN = [
     ("single tokens, groups of eight", [(1, 5000), (1, 1), (1, 640), (1, 129)], 16, 2, 128),
     ("single tokens, small groups", [(1, 1000), (1, 33), (1, 257)], 12, 4, 16),
     ("as many tokens as sequences, unevenly", [(0, 40), (3, 700), (0, 0), (1, 300), (4, 129), (0, 9), (0, 8), (1, 5), (0, 3)], 16, 1, 16),
+    ("the same in groups of eight", [(0, 40), (3, 700), (0, 0), (1, 300), (4, 129), (0, 9), (0, 8), (1, 5), (0, 3)], 8, 1, 16),
+    ("single tokens and a prefill chunk of idle sequences' tokens", [(12, 2000)] + [(0, 30 + i) for i in range(11)] + [(1, 77)], 8, 1, 16),
+    ("more blocks than a self-planned launch takes", [(1, 1 + 5 * (i % 40)) for i in range(180)], 24, 3, 16),
+    ("as many of verify steps", [(1 + i % 3, 4 + 7 * (i % 40)) for i in range(180)], 24, 3, 16),
 ]
 
 
@@ -180,6 +184,50 @@ def test_attention_matches_the_oracle(i, path):
         pg.paged_gqa_set_path(prev)
     _ok()
     fu.check(c, out, name)
+
+
+PATHS = [
+    # seqs, q heads, kv heads, path: bits of the kernels that run (2 tcgen05 verify, 4 tcgen05 prefill, 128 decode)
+    ([(1, 300)] * 3, 8, 1, 0, 128),
+    ([(1, 300)] * 3, 8, 1, 2, 2),
+    ([(1, 300)] * 3, 9, 1, 0, 2),
+    ([(2, 300)], 8, 1, 0, 2),
+    ([(9, 300)], 8, 1, 0, 2 | 4),
+    ([(1, 300)] * 9, 8, 1, 0, 128 | 4),
+]
+
+
+@pytest.mark.parametrize("i", range(len(PATHS)))
+def test_kernel_of_a_batch(i):
+    seqs, hq, hkv, path, bits = PATHS[i]
+    c = fu.make(seqs, hq, hkv, 16, seed=170 + i)
+    prev = pg.paged_gqa_set_path(path)
+    try:
+        out = _attn(c)
+    finally:
+        pg.paged_gqa_set_path(prev)
+    _ok()
+    assert pg.paged_gqa_last_plan()["path_bits"] == bits
+    fu.check(c, out, "kernel of a batch")
+
+
+@pytest.mark.parametrize("name,seqs,hq", [
+    ("decode", [(1, 3000), (1, 129), (1, 5)], 8),
+    ("verify", [(4, 3000), (2, 700), (3, 129)], 16),
+    ("prefill", [(150, 400), (4, 9000), (40, 300)], 8),
+])
+def test_a_wait_that_runs_out_reports_timeout_and_the_next_call_is_correct(name, seqs, hq):
+    c = fu.make(seqs, hq, 1, 16, seed=180)
+    prev = pg.paged_gqa_set_stall_test(200_000)  # 200 us
+    try:
+        _attn(c)
+        st = pg.paged_gqa_check_device_errors()
+    finally:
+        pg.paged_gqa_set_stall_test(prev)
+    assert st == TIMEOUT, pg.paged_gqa_last_error()
+    out = _attn(c)
+    _ok()
+    fu.check(c, out, f"after a timeout ({name})")
 
 
 @pytest.mark.parametrize("seqs,hq,hkv,page", [
@@ -242,6 +290,22 @@ def test_rows_of_no_sequence_stay_as_they_were_and_views_work():
     _ok()
     fu.check(c, wide_out[:, 1:9], "views")
     assert bool((wide_out[:, [0, 9]] == 5.0).all())
+
+
+def test_invalid_single_token_sequences_are_zeroed_and_flagged():
+    c = fu.make([(1, 100), (1, 60), (1, 400)], 8, 1, 16, seed=106)
+    lens, table = c.lens.clone(), c.table.clone()
+    lens[1] = 0                       # fewer than its new tokens
+    out = torch.full(c.q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    pg.paged_gqa_attn_fp4(c.q, c.k, c.v, c.table, lens, c.qsl, c.kd, c.vd, c.scale, out)
+    assert pg.paged_gqa_check_device_errors() == BOUNDS
+    assert bool((out[1] == 0).all())
+    rows = np.array([r for r in range(24) if not 8 <= r < 16])
+    fu.check(c, out, "valid single tokens", rows=rows)
+    table[0, 2], table[2, 20] = -7, c.k.shape[0]
+    pg.paged_gqa_attn_fp4(c.q, c.k, c.v, table, c.lens, c.qsl, c.kd, c.vd, c.scale, out)
+    assert pg.paged_gqa_check_device_errors() == BOUNDS
+    fu.check(c, out, "the sequence with good pages", rows=np.arange(8, 16))
 
 
 def test_invalid_sequences_are_zeroed_and_flagged():
