@@ -595,7 +595,7 @@ int fp4_cache_call(bool write, const pg_tensor* kx, const pg_tensor* vx, const p
   return PG_OK;
 }
 
-int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, cudaStream_t stream) {
+int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, bool captured, cudaStream_t stream) {
   Problem p = val.p;
   Pointers ptr = val.ptr;
   ptr.err = ds->err;
@@ -616,18 +616,22 @@ int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, 
   // 150 against 189 at 256 of 8192. At 16 heads the warp-level kernel took 65 against 44. (A
   // sequence with more rows is served in passes, correctly but with its keys read once per 8 rows.)
   const bool decode = tc && path != 2 && p.T <= p.num_seqs && p.G <= 8;
+  // No sequence of at most kVerifyRows rows in all can be of the prefill class. Then a self-planned
+  // verify kernel is the whole call, unless it is captured: the plan kernel counts the workspace's
+  // epoch on, which tells a captured call's replays apart (other calls differ in their tags).
+  const bool no_prefill = (long long)p.T * p.G <= kVerifyRows;
+  p.unplanned = no_prefill && p.fused_verify && !captured;
   int launched = 0, used = 0;
   cudaError_t e;
   for (int c = 0; c < kNumClasses; ++c) {
     // the plan kernel goes before the verify class, or after it where that plans itself
     const bool plan_here = c == (p.fused_verify ? 1 : 0);
-    if (plan_here) {
+    if (plan_here && !p.unplanned) {
       e = launch_plan(p, ptr, cp[0], cp[1], !p.fused_verify, p.fused_verify, stream);
       if (e != cudaSuccess) return cuda_fail(e, "plan launch");
       ++launched;
     }
-    // no sequence of at most kVerifyRows rows in all can be of the prefill class
-    if (c == 1 && (long long)p.T * p.G <= kVerifyRows) break;
+    if (c == 1 && no_prefill) break;
     if (c == 0 && decode) {
       if (launch_fp4_decode(p, ptr, cp[c], stream) < 0)
         return fail(PG_ERR_CUDA, "4-bit decode launch failed: %s", tc_last_error());
@@ -709,19 +713,18 @@ int attn_fp4(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
   DeviceState* ds = nullptr;
   if ((st = current_device(&ds))) return st;
   const WsLayout L = make_layout(p.num_seqs, p.T, p.Hq, p.Hkv, ds->sms);
-  cudaError_t e;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
   if (use_user_ws) {
     if (!user_ws || (reinterpret_cast<uintptr_t>(user_ws) & 255u))
       return fail(PG_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
     if (user_ws_bytes < L.total)
       return fail(PG_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", user_ws_bytes, L.total);
-    st = run_fp4(val, user_ws, L, ds, stream);
+    st = run_fp4(val, user_ws, L, ds, cap != cudaStreamCaptureStatusNone, stream);
   } else {
     // A graph would keep the library's workspace, which may grow (and move) or serve another
     // stream while the graph replays.
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    e = cudaStreamIsCapturing(stream, &cap);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
     if (cap != cudaStreamCaptureStatusNone)
       return fail(PG_ERR_WORKSPACE, "a captured call needs its own workspace: paged_gqa_attn_fp4_ex");
     std::lock_guard<std::mutex> lk(ds->mu);
@@ -750,7 +753,7 @@ int attn_fp4(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
       e = cudaStreamWaitEvent(stream, ds->ws4_done, 0);
       if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
     }
-    st = run_fp4(val, ds->ws4, L, ds, stream);
+    st = run_fp4(val, ds->ws4, L, ds, false, stream);
     // also after a failed launch: what was launched before it may be running
     e = cudaEventRecord(ds->ws4_done, stream);
     if (e != cudaSuccess && st == PG_OK) return cuda_fail(e, "cudaEventRecord");

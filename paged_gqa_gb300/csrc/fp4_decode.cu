@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
   if (kFused) {
     self_plan::Scratch& fs = *reinterpret_cast<self_plan::Scratch*>(smem);
     self_plan::load(p, ptr, fs);
+    if (p.unplanned && blockIdx.x == 0) self_plan::flag_invalid(p, ptr, fs);
     __syncthreads();
     if (warp == 1) self_plan::plan_warp(p, fs, cp.num_ctas, lane, ms.fitem, ms.fseq, &ms.fcount);
   } else {

@@ -196,6 +196,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   self_plan::Scratch& fs = *reinterpret_cast<self_plan::Scratch*>(smem + C::kOffK);
   if (kFused) {
     self_plan::load(p, ptr, fs);  // the set-up below overlaps these reads
+    if (p.unplanned && blockIdx.x == 0) self_plan::flag_invalid(p, ptr, fs);
   } else {
     item_begin = cp.cta_item_begin[blockIdx.x];
     item_end = cp.cta_item_begin[blockIdx.x + 1];

@@ -63,6 +63,26 @@ __device__ __forceinline__ void load(const Problem& p, const Pointers& ptr, Scra
   }
 }
 
+// What the plan kernel does for invalid sequences, for calls without one: by the threads that staged
+// them, flags them and zeroes their rows.
+__device__ __forceinline__ void flag_invalid(const Problem& p, const Pointers& ptr, const Scratch& fs) {
+  if (threadIdx.x == 0 && (ptr.qsl[0] != 0 || ptr.qsl[p.num_seqs] != p.T)) atomicOr(ptr.err, kErrBounds);
+#pragma unroll 1
+  for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
+    const int4 i = fs.seq[s];
+    if (i.y >= 0 && i.x >= 0 && i.x + i.y <= p.T && i.y <= i.z && (long long)i.z <= (long long)p.W * p.P) continue;
+    atomicOr(ptr.err, kErrBounds);
+    const int t0 = max(0, i.x), t1 = min(p.T, max(t0, i.x + max(i.y, 0)));
+    uint16_t* o = static_cast<uint16_t*>(ptr.out);
+#pragma unroll 1
+    for (int t = t0; t < t1; ++t)
+#pragma unroll 1
+      for (int h = 0; h < p.Hq; ++h)
+#pragma unroll 1
+        for (int d = 0; d < kHeadDim; ++d) o[t * p.o_st + h * p.o_sh + d] = 0;
+  }
+}
+
 // Step 2, one warp, after a CTA barrier: the scan over sequences (each lane a contiguous
 // run of them), this CTA's range and items. Packed item (fitem, at most kFusedMaxBlocks):
 // x = block, y = sequence, z = first tile | tiles << 16, w = piece index | pieces << 15 |

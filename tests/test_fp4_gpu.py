@@ -380,6 +380,29 @@ def test_capture_needs_the_callers_workspace():
         pg.paged_gqa_attn_fp4_ex(c.q, c.k, c.v, c.table, c.lens, c.qsl, c.kd, c.vd, c.scale, out, None)
 
 
+@pytest.mark.parametrize("seqs,hq", [([(1, 30000)], 8), ([(4, 30000)], 16), ([(1, 20000)] * 4, 8), ([(1, 9000), (4, 5000), (30, 700)], 16)])
+def test_replays_and_direct_calls_share_a_workspace(seqs, hq):
+    """Split sequences, replayed with new queries and called directly in between, in one workspace of any contents."""
+    c = fu.make(seqs, hq, 1, 16, seed=131)
+    ws = _workspace(c).fill_(255)
+    out = torch.full(c.q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    call = lambda: pg.paged_gqa_attn_fp4_ex(c.q, c.k, c.v, c.table, c.lens, c.qsl, c.kd, c.vd, c.scale, out, ws)
+    call()
+    fu.check(c, out, "first")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for r in range(3):
+        c.q.copy_(c.q * -0.75 + 0.25)
+        out.fill_(float("nan"))
+        graph.replay()
+        fu.check(c, out, f"replay {r}")
+        out.fill_(float("nan"))
+        call()
+        fu.check(c, out, f"call {r}")
+    _ok()
+
+
 def _step(c, x, ws, buf):
     """One decoding step: rotary, cache write, attention; and the new tokens read back."""
     pg.paged_gqa_rope(x["q"], x["k"], x["pos"], x["inv"], [16, 8, 8], buf["q"], buf["k"], interleaved=True)
