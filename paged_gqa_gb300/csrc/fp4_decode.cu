@@ -35,6 +35,7 @@
 #include "common.cuh"
 #include "device_util.cuh"
 #include "fp4.cuh"
+#include "fp4_merge.cuh"
 #include "self_plan.cuh"
 #include "tc_kernels.cuh"
 #include "tc_util.cuh"
@@ -422,31 +423,14 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
       }
       __syncthreads();
       if (ms.merge_flag) {
-        // The block's last piece joins all of them: w_i = 2^(lse_i - M) / sum_j 2^(lse_j - M). A warp
-        // takes whole rows, 16 bytes a lane.
+        // The block's last piece joins all of them. A warp takes whole rows, 16 bytes a lane.
         __threadfence();
         const float* lse = slot_lse(cp, I.slot_base);
         const uint16_t* part = slot_o(cp, I.slot_base);
         for (int r = warp; r < I.nrows; r += kDWarps) {
-          float M = -INFINITY, S = 0.f;
-          for (int i = lane; i < I.nsplit; i += 32) M = fmaxf(M, __ldcg(lse + i * kVerifyRows + r));
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-          float acc[8] = {};
-#pragma unroll 4
-          for (int i = 0; i < I.nsplit; ++i) {
-            const float w = ex2(__ldcg(lse + i * kVerifyRows + r) - M);
-            const uint4 h = __ldcg(reinterpret_cast<const uint4*>(part + ((size_t)i * kVerifyRows + r) * kHeadDim) + lane);
-            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-            S += w;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 v = unpack_f16x2(hw[k]);
-              acc[2 * k] += w * v.x;
-              acc[2 * k + 1] += w * v.y;
-            }
-          }
-          const float k = p.out_scale / S;
+          float acc[8];
+          const float k = p.out_scale /
+                          merge_row<8>(lse + r, kVerifyRows, part + r * kHeadDim, kVerifyRows * kHeadDim, I.nsplit, lane, acc);
           const RowMap m = map_row(r, p.G, I.kvh);
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(ptr.out) + (long long)(I.q0 + m.t) * p.o_st +
                                     (long long)m.h * p.o_sh + lane * 8) =

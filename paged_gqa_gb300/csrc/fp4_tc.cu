@@ -38,6 +38,7 @@
 #include "common.cuh"
 #include "device_util.cuh"
 #include "fp4.cuh"
+#include "fp4_merge.cuh"
 #include "self_plan.cuh"
 #include "tc_kernels.cuh"
 #include "tc_util.cuh"
@@ -374,41 +375,16 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       // The block's last piece joins all of them: w_i = 2^(lse_i - M) / sum_j 2^(lse_j - M), M the
       // largest, out = v_descale sum_i w_i o_i. A warp takes whole rows, 16 bytes a lane.
       auto merge = [&](const Item& I, int pi) {
-        const int ns = I.nsplit;
         const float* lse = slot_lse(cp, I.slot_base);
         const uint16_t* part = slot_o(cp, I.slot_base);
-        for (int r = gi; r < I.nrows; r += kSoftThreads) {
-          float M = -INFINITY, sum = 0.f;
-#pragma unroll 1
-          for (int i = 0; i < ns; ++i) M = fmaxf(M, __ldcg(lse + i * kN + r));
-#pragma unroll 1
-          for (int i = 0; i < ns; ++i) sum += ex2(__ldcg(lse + i * kN + r) - M);
-          ms.red[0][r] = M;
-          ms.red[1][r] = p.out_scale / sum;
-        }
-        named_barrier(2, kSoftThreads);
 #pragma unroll 1
         for (int r = sw; r < I.nrows; r += kSoftWarps) {
-          const float M = ms.red[0][r];
-          float acc[8] = {};
-#pragma unroll 4
-          for (int i = 0; i < ns; ++i) {
-            const float w = ex2(__ldcg(lse + i * kN + r) - M);
-            const uint4 h = __ldcg(reinterpret_cast<const uint4*>(part + ((size_t)i * kN + r) * kHeadDim) + lane);
-            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 o = unpack_f16x2(hw[k]);
-              acc[2 * k] += w * o.x;
-              acc[2 * k + 1] += w * o.y;
-            }
-          }
-          const float inv = ms.red[1][r];
+          float acc[8];
+          const float inv = p.out_scale / merge_row<4>(lse + r, kN, part + r * kHeadDim, kN * kHeadDim, I.nsplit, lane, acc);
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(ptr.out) + ms.out_off[pi][r] + lane * 8) =
               make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
                          pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
         }
-        named_barrier(2, kSoftThreads);  // red is used again by the next item
       };
 
       auto epilogue = [&](int it) {
