@@ -261,7 +261,7 @@ int paged_gqa_cache_write(const pg_tensor* k_new, const pg_tensor* v_new, const 
  * A group with a NaN gets a NaN scale, so its values read back as NaN; infinities saturate.
  * A descale near amax / (6 * 448) of the tensor uses the scales' whole range.
  * Nothing else in the caches changes. k_new and v_new need 16-byte aligned rows; the caches'
- * (page, head) blocks must not overlap. Descales must be finite, positive and have a finite
+ * (page, head) blocks must not overlap, nor the two caches each other. Descales must be finite, positive and have a finite
  * reciprocal. Errors as paged_gqa_cache_write (a bad position or page: that row is skipped).
  * Allocates nothing.
  */
@@ -276,7 +276,8 @@ int paged_gqa_cache_write_fp4(const pg_tensor* k_new, const pg_tensor* v_new, co
  * query_start_loc[s] positions of each sequence (its whole context, where that is
  * seq_lens[s]), rounded to bf16 once; with a power-of-two descale they are exact. For moving
  * a prefix to another cache, or a kernel that wants bf16. A bad position or page is flagged
- * and its rows are zeros. Arguments otherwise as paged_gqa_cache_write_fp4. Allocates nothing.
+ * and its rows are zeros. k_out and v_out must not overlap. Arguments otherwise as
+ * paged_gqa_cache_write_fp4. Allocates nothing.
  */
 int paged_gqa_cache_read_fp4(const pg_tensor* k_cache, const pg_tensor* v_cache, const pg_tensor* block_table,
                              const pg_tensor* seq_lens, const pg_tensor* query_start_loc, float k_descale,
@@ -287,7 +288,9 @@ int paged_gqa_cache_read_fp4(const pg_tensor* k_cache, const pg_tensor* v_cache,
  * prefill chunks in one batch. q and out are bf16 [T, Hq, 256]; the other arguments, the mask,
  * the errors and what is left untouched are those of paged_gqa_attn. K and V enter the
  * products exactly (code * scale has 6 significant bits); scores, sums and outputs are held
- * in fp32. A new call and an older one on another stream are ordered by the library (they
+ * in fp32. out and q must not overlap. A NaN in V (a NaN scale) reaches the new tokens that see
+ * its key, and may reach the others of that sequence that share a block of rows with one.
+ * A new call and an older one on another stream are ordered by the library (they
  * share its workspace), so such calls do not overlap; in a stream capture the call returns
  * PG_ERR_WORKSPACE: use paged_gqa_attn_fp4_ex there, with a workspace of
  * paged_gqa_workspace_size(...) bytes, 256-byte aligned, that no overlapping call uses (two
@@ -317,7 +320,8 @@ int paged_gqa_attn_fp4_ex(const pg_tensor* q, const pg_tensor* k_cache, const pg
  *   adjacent      0: pair i is (i, i + R / 2); 1: (2i, 2i + 1)
  *   q_out, k_out  bf16, shapes of q and k, rows disjoint; each may be its input (same data
  *                 and strides: then only the rotated values are touched) and must otherwise
- *                 not overlap any input
+ *                 overlap no input, nor each other (refused; rows of one allocation with the
+ *                 same token stride are told apart)
  *
  * Pair (u, w) becomes (u cos a - w sin a, w cos a + u sin a), a = position * inv_freq[i], in
  * fp32, rounded once. The angle keeps its phase for every 32-bit position (negative ones turn

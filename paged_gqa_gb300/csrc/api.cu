@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -530,6 +531,41 @@ int check_rows(const pg_tensor* t, const char* name, bool written) {
   return PG_OK;
 }
 
+// Do two checked bf16 [T, H, 256] tensors share bytes? Rows of one allocation with equal token strides
+// (slices of a projection's output) are told apart exactly; otherwise intersecting address
+// ranges count as shared.
+bool rows_overlap(const pg_tensor* a, const pg_tensor* b) {
+  if (!a->data || !b->data || !a->shape[0] || !b->shape[0] || !a->shape[1] || !b->shape[1]) return false;
+  long long ext[2], st[2], sh[2];
+  const pg_tensor* t[2] = {a, b};
+  for (int i = 0; i < 2; ++i) {
+    const pg_tensor* other = t[1 - i];
+    st[i] = t[i]->shape[0] > 1 ? t[i]->stride[0] : other->shape[0] > 1 ? other->stride[0] : 0;
+    sh[i] = t[i]->shape[1] > 1 ? t[i]->stride[1] : 0;
+    if (st[i] < 0 || sh[i] < 0) return true;
+    ext[i] = (t[i]->shape[0] - 1) * st[i] + (t[i]->shape[1] - 1) * sh[i] + kHeadDim;
+  }
+  // b's first value after a's, in elements (rows are 16-byte aligned)
+  const long long delta = ((long long)reinterpret_cast<intptr_t>(b->data) - (long long)reinterpret_cast<intptr_t>(a->data)) / 2;
+  if (delta >= ext[0] || -delta >= ext[1]) return false;
+  if (st[0] != st[1] || a->shape[1] * b->shape[1] > 1 << 16) return true;
+  // is a row of b at less than a row's length from one of a: |delta + hb sh_b - ha sh_a + n st| < 256,
+  // -T_a < n < T_b?
+  const long long S = st[0], lo = 1 - a->shape[0], hi = b->shape[0] - 1;
+  for (long long ha = 0; ha < a->shape[1]; ++ha)
+    for (long long hb = 0; hb < b->shape[1]; ++hb) {
+      const long long d = delta + hb * sh[1] - ha * sh[0];
+      long long n = S > 0 ? -d / S : 0;
+      for (long long c = std::max(lo, n - 1); c <= std::min(hi, n + 1); ++c)
+        if (std::llabs(d + c * S) < kHeadDim) return true;
+      if (n - 1 > hi || n + 1 < lo) {  // the nearest n is out of range: the range's end is the closest
+        const long long c = n > hi ? hi : lo;
+        if (std::llabs(d + c * S) < kHeadDim) return true;
+      }
+    }
+  return false;
+}
+
 int current_device(DeviceState** ds) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -560,6 +596,8 @@ int fp4_cache_call(bool write, const pg_tensor* kx, const pg_tensor* vx, const p
     t_last_error.clear();
     return PG_OK;
   }
+  if (write ? kc->data && kc->data == vc->data : rows_overlap(kx, vx))
+    return fail(PG_ERR_INVALID_ARG, write ? "k_cache and v_cache are the same memory" : "k_out and v_out overlap");
   DeviceState* ds = nullptr;
   if ((st = current_device(&ds))) return st;
   Fp4CacheArgs a;
@@ -680,6 +718,7 @@ int attn_fp4(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
     return PG_OK;
   }
   if (k->shape[0] == 0 || W == 0) return fail(PG_ERR_INVALID_ARG, "new tokens without pages");
+  if (rows_overlap(q, out)) return fail(PG_ERR_INVALID_ARG, "out overlaps q");
   Validated val{};
   Problem& p = val.p;
   p.num_seqs = (int)S;
@@ -1120,6 +1159,12 @@ int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* posi
     for (int x = 1; x < A; ++x)
       if (sections[x] > 0 && (long long)(sections[x] - 1) * A + x >= half)
         return fail(PG_ERR_INVALID_ARG, "interleaved sections: axis %d has no %d-th entry", x, sections[x]);
+  for (int i = 0; i < 2; ++i) {
+    if (!a.in_place[i] && rows_overlap(out[i], in[i]))
+      return fail(PG_ERR_INVALID_ARG, "%s overlaps %s without being in place of it", names[i][1], names[i][0]);
+    if (rows_overlap(out[i], in[1 - i])) return fail(PG_ERR_INVALID_ARG, "%s overlaps %s", names[i][1], names[1 - i][0]);
+  }
+  if (rows_overlap(q_out, k_out)) return fail(PG_ERR_INVALID_ARG, "q_out overlaps k_out");
   a.pos = static_cast<const int32_t*>(positions->data);
   a.pos_sa = positions->stride[0];
   a.inv_freq = static_cast<const float*>(inv_freq->data);

@@ -166,3 +166,38 @@ def test_marshalling_refuses_caches_of_another_type():
     k = FakeTensor(CACHE, torch.float8_e4m3fn)
     with pytest.raises(ValueError, match="uint8"):
         B._pack_fp4(0, k, k)
+
+
+def _at(shape, offset, stride=None):
+    return FakeTensor(shape, BF, ptr=(1 << 24) + 2 * offset, stride=stride)
+
+
+ROW = 20 * 256  # a token of a projection's output: 16 query heads, 2 key heads, 2 value heads
+
+
+@pytest.mark.parametrize("over,msg", [
+    # q_out where k is; q_out half over q; the outputs at one place; a token apart
+    (dict(q=_at((8, 2, 256), 0), k=_at((8, 2, 256), 1 << 20), qo=_at((8, 2, 256), 1 << 20), ko=_at((8, 2, 256), 1 << 21)), "q_out overlaps k"),
+    (dict(q=_at((8, 16, 256), 0), qo=_at((8, 16, 256), 8 * 256)), "q_out overlaps q without"),
+    (dict(k=_at((8, 2, 256), 1 << 20), ko=_at((8, 2, 256), (1 << 20) + 3 * 512)), "k_out overlaps k without"),
+    (dict(qo=_at((8, 16, 256), 1 << 20), ko=_at((8, 2, 256), (1 << 20) + 7 * 16 * 256)), "q_out overlaps k_out"),
+    (dict(q=_at((8, 16, 256), 0, [ROW, 256, 1]), qo=_at((8, 16, 256), 0, [ROW, 256, 1]),
+          k=_at((8, 2, 256), 15 * 256, [ROW, 256, 1]), ko=_at((8, 2, 256), 1 << 20)), "q_out overlaps k"),
+    (dict(q=_at((8, 16, 256), 0, [ROW, 256, 1]), qo=_at((8, 16, 256), 0, [ROW, 256, 1]),
+          k=_at((8, 2, 256), 1 << 20), ko=_at((8, 2, 256), 5 * ROW + 17 * 256 - 3 * ROW - 2 * 256, [ROW, 256, 1])), "k_out overlaps q"),
+])
+def test_rope_refuses_overlapping_tensors(over, msg):
+    a = dict(q=_at((8, 16, 256), 0), k=_at((8, 2, 256), 1 << 18), qo=_at((8, 16, 256), 1 << 19), ko=_at((8, 2, 256), 3 << 18))
+    a.update(over)
+    assert _rope(**a) == -1 and msg in pg.paged_gqa_last_error(), pg.paged_gqa_last_error()
+
+
+def test_write_and_read_refuse_one_memory_for_two_tensors():
+    far = dict(k=FakeTensor(CACHE, U8, ptr=1 << 22), kn=_at((8, 2, 256), 0), vn=_at((8, 2, 256), 1 << 20))
+    assert _write(_args(**dict(far, v=FakeTensor(CACHE, U8, ptr=1 << 22)))) == -1 and "same memory" in pg.paged_gqa_last_error()
+    assert _read(_args(**dict(far, vn=_at((8, 2, 256), 256)))) == -1 and "k_out and v_out overlap" in pg.paged_gqa_last_error()
+
+
+def test_attention_refuses_an_output_over_its_queries():
+    assert _attn(_args(q=_at((8, 16, 256), 0), out=_at((8, 16, 256), 256 * 16))) == -1
+    assert "out overlaps q" in pg.paged_gqa_last_error()
