@@ -59,8 +59,8 @@ __host__ __device__ constexpr int fixed_cost(int cls) { return cls == 0 ? 6 : 2;
 // everywhere (8 x q4 with L 2-5.5k: 38 us per call, against 96 us when every CTA took a
 // range), and the 64- and 256-sequence workloads did not change.
 constexpr int kMinRangeUnits = 6;
-__host__ __device__ __forceinline__ int cut_ctas(long long U, int num_ctas) {
-  const long long c = U / kMinRangeUnits;
+__host__ __device__ __forceinline__ int cut_ctas(long long U, int num_ctas, int min_units) {
+  const long long c = U / min_units;
   return (int)(c < 1 ? (U > 0 ? 1 : 0) : (c < num_ctas ? c : num_ctas));
 }
 // CTA whose range holds unit u.
@@ -128,6 +128,16 @@ struct Problem {
   // No plan kernel runs in this call (4-bit caches): the verify kernel flags invalid sequences.
   int unplanned;
 };
+
+// Units a range of the cut has at least (kMinRangeUnits). 4-bit caches: a tile takes longer, and
+// the last piece merges row by row, so the rows of a block decide. Graph replays over 6, 4, 3, 2, 1: one sequence of 1200 keys, 8 rows: 19.7, 15.7, 15.4,
+// 13.6, 13.2 us; 16 rows: 24.3, 18.1, 18.4, 15.9, 16.4; 64 rows: 31.3, 24.1, 24.6, 23.3, 25.8; one of 16384 keys,
+// 16 rows: 26.3, 24.4, 25.4, 25.2, 35.1; 64 rows: 40.5, 40.9, 47.6, 53.6, 91.9 (as many pieces as
+// tiles to merge for every row). Batches that fill the SMs do not change.
+__host__ __device__ __forceinline__ int min_range_units(const Problem& p) {
+  if (!p.kv_is_fp4) return kMinRangeUnits;
+  return (long long)p.T * p.G <= 16ll * p.num_seqs ? 2 : 4;
+}
 
 struct Pointers {
   const void* q;
