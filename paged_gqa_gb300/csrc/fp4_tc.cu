@@ -7,7 +7,7 @@
 //   O^T[d, row] += V^T P^T         A = V^T [256 d, 128 keys], as two 128-lane tiles
 // so the MMA's 128 lanes are full however few rows a block has, its cost follows the rows
 // (N = rows rounded up to 16), and A can come from TMEM: the packed pages (144 bytes per key)
-// go from HBM to shared memory by bulk copies, eight warps widen them to f16 (code * scale,
+// go from HBM to shared memory by bulk copies, eight to twelve warps widen them to f16 (code * scale,
 // exact) and store them with tcgen05.st, and no widened value ever passes through shared memory.
 // (Through it, 1 KB per key written and read again would cost 16 of the ~12 cycles per key
 // that a CTA has at full HBM bandwidth.) Widening thread t owns TMEM lane t: key t of the
@@ -25,9 +25,22 @@
 // row sums take it before that rounding. The softmax, its lazy rescale, the split-KV pieces and
 // their merge follow the FP8 verify kernel (verify_tc.cu): keys on lanes, rows on columns.
 //
-// Warp roles (1024 threads): warp 0 S issuer (+ TMEM owner), warp 1 P.V issuer, warp 2 K copies,
-// warp 3 V copies, warps 4-19 softmax and epilogue (row group (w - 4) / 4 owns kN / 4 rows, lane
-// quarter w % 4), warps 20-23 widen K, warps 24-31 V (lane quarter w % 4).
+// Warp roles: warp 0 S issuer (+ TMEM owner), warp 1 P.V issuer, warp 2 K copies, warp 3 V
+// copies, warps 4-19 softmax and epilogue (row group (w - 4) / 4 owns kN / 4 rows, lane quarter w % 4);
+// with 64 rows (1024 threads) warps 20-23 widen K and 24-31 V, side by side; with 128 rows (896 threads) warps
+// 20-27 widen both in turn, since the shared columns hold one at a time (2228 us for a 8192-token
+// chunk on 32768 keys with the two groups of warps there, 2175 so).
+//
+// What bounds it. A 128-key tile takes about 10.2k warp instructions at 48-64 rows: ~3.2k widen, ~1.9k
+// softmax, the rest hands tiles from role to role; issue slots are 63 % busy, the ALU pipe (conversions at
+// half rate) 44 %, tensor cores 25 %, HBM 31 %. With either half of the work taken out (timing only): neither
+// widening nor softmax 248 us, no widening 275, no softmax 337, all of it 431 (256 sequences of
+// 8192 keys, 2-4 tokens, 32/2 heads: 1233 MB, 182 us at the HBM rate). 64 sequences of 1k-32k keys,
+// 4 tokens, 16/1 heads: 130 us (46). With 128 rows widening and the products alternate in the shared
+// columns, and a tile takes ~4700 cycles where the products alone take 2230: 2170 us, 887 TFLOP/s.
+// Tried and slower: operands in quarters instead of halves (2910 us, a hand-over costs ~400
+// cycles), both row halves of the softmax in registers (2370, spills), byte permutes for half of
+// V's pairs (2337), one barrier arrival per softmax warp instead of per thread (2204, verify 439).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
