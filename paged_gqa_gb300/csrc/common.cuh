@@ -134,8 +134,10 @@ struct Problem {
 // 13.6, 13.2 us; 16 rows: 24.3, 18.1, 18.4, 15.9, 16.4; 64 rows: 31.3, 24.1, 24.6, 23.3, 25.8; one of 16384 keys,
 // 16 rows: 26.3, 24.4, 25.4, 25.2, 35.1; 64 rows: 40.5, 40.9, 47.6, 53.6, 91.9 (as many pieces as
 // tiles to merge for every row). Batches that fill the SMs do not change.
-__host__ __device__ __forceinline__ int min_range_units(const Problem& p) {
+__host__ __device__ __forceinline__ int min_range_units(const Problem& p, int cls) {
   if (!p.kv_is_fp4) return kMinRangeUnits;
+  constexpr int kX = 4;
+  if (cls == 1) return kX;
   return (long long)p.T * p.G <= 16ll * p.num_seqs ? 2 : 4;
 }
 

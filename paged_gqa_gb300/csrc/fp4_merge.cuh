@@ -7,6 +7,17 @@
 
 namespace pgqa {
 
+// acc += w times the eight f16 of h.
+__device__ __forceinline__ void merge_add(float (&acc)[8], const uint4& h, float w) {
+  const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 o = unpack_f16x2(hw[k]);
+    acc[2 * k] += w * o.x;
+    acc[2 * k + 1] += w * o.y;
+  }
+}
+
 // One row of a split block by one warp: with M the largest log2-sum-exp of its pieces and
 // w_i = 2^(lse_i - M), the lane's 8 columns of sum_i w_i o_i in acc; returns sum_i w_i. lse and part point at
 // the row in the block's first piece, the others follow at the given pitches (elements). The lanes read
@@ -36,16 +47,7 @@ __device__ __forceinline__ float merge_row(const float* lse, int lse_pitch, cons
       for (int b = 0; b < kBatch; ++b)
         h[b] = i + b < n ? __ldcg(reinterpret_cast<const uint4*>(src + (size_t)(i + b) * part_pitch)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const float wb = __shfl_sync(0xffffffffu, w, i + b);
-        const uint32_t hw[4] = {h[b].x, h[b].y, h[b].z, h[b].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 o = unpack_f16x2(hw[k]);
-          acc[2 * k] += wb * o.x;
-          acc[2 * k + 1] += wb * o.y;
-        }
-      }
+      for (int b = 0; b < kBatch; ++b) merge_add(acc, h[b], __shfl_sync(0xffffffffu, w, i + b));
     }
   }
 #pragma unroll

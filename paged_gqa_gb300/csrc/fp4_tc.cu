@@ -304,13 +304,13 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           ms.m[pi][n] = real ? kMInit : 0.f;
           ms.mo[pi][n] = kSigma - ms.m[pi][n];
         }
-        // A warp takes whole rows (32 lanes of 16 bytes), four at a time.
-#pragma unroll 1
-        for (int k0 = 0; k0 < kN / kSoftWarps; k0 += 4) {
-          uint4 v[4];
+        // A warp takes whole rows (32 lanes of 16 bytes), all of its rows at once.
+        {
+          constexpr int kRows = kN / kSoftWarps;
+          uint4 v[kRows];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = (k0 + k) * kSoftWarps + sw;
+          for (int k = 0; k < kRows; ++k) {
+            const int r = k * kSoftWarps + sw;
             v[k] = make_uint4(0, 0, 0, 0);
             if (r < I.nrows) {
               const RowMap m = map_row(I.row0 + r, p.G, I.kvh);
@@ -319,8 +319,8 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             }
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = (k0 + k) * kSoftWarps + sw;
+          for (int k = 0; k < kRows; ++k) {
+            const int r = k * kSoftWarps + sw;
             uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
             uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                                     __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
@@ -350,12 +350,16 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       auto new_reference = [&](int cc, int pi, uint32_t sb, bool have_o, uint32_t g, bool need_mask, int key, int kv_hi) {
         float r = -INFINITY;  // lane n: the warp's maximum of row cc + n
 #pragma unroll 1
-        for (int n = 0; n < 16; ++n) {
-          float x = tmem_ld1(tmem + lane_addr + C::kColS + sb * kN + cc + n);
+        for (int n = 0; n < 16; n += 4) {
+          float v[4];
+          tmem_ld4f(tmem + lane_addr + C::kColS + sb * kN + cc + n, v);
           tmem_wait_ld();
-          const bool vis = !need_mask || (key < kv_hi && key <= ms.lim[pi][cc + n]);
-          x = warp_max(vis ? x * ms.cs[pi][cc + n] : -INFINITY);
-          if (lane == n) r = x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool vis = !need_mask || (key < kv_hi && key <= ms.lim[pi][cc + n + i]);
+            const float x = warp_max(vis ? v[i] * ms.cs[pi][cc + n + i] : -INFINITY);
+            if (lane == n + i) r = x;
+          }
         }
         if (lane < 16) ms.red[q4][cc + lane] = r;
         named_barrier(group_bar, 128);
@@ -374,11 +378,14 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
-          for (int n = 0; n < 32; ++n) {
+          for (int n = 0; n < 32; n += 4) {
             const uint32_t a = tmem + lane_addr + C::kColO + (n >> 4) * kN + cc + (n & 15);
-            const float x = tmem_ld1(a);
+            float v[4];
+            tmem_ld4f(a, v);
             tmem_wait_ld();
-            tmem_st1(a, x * ms.alpha[cc + (n & 15)]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] *= ms.alpha[cc + (n & 15) + i];
+            tmem_st4f(a, v);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -390,13 +397,46 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       auto merge = [&](const Item& I, int pi) {
         const float* lse = slot_lse(cp, I.slot_base);
         const uint16_t* part = slot_o(cp, I.slot_base);
-#pragma unroll 1
-        for (int r = sw; r < I.nrows; r += kSoftWarps) {
-          float acc[8];
-          const float inv = p.out_scale / merge_row<4>(lse + r, kN, part + r * kHeadDim, kN * kHeadDim, I.nsplit, lane, acc);
+        auto store_row = [&](int r, const float (&acc)[8], float k) {
           *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(ptr.out) + ms.out_off[pi][r] + lane * 8) =
-              make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
-                         pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+              make_uint4(pack_bf16x2(acc[0] * k, acc[1] * k), pack_bf16x2(acc[2] * k, acc[3] * k),
+                         pack_bf16x2(acc[4] * k, acc[5] * k), pack_bf16x2(acc[6] * k, acc[7] * k));
+        };
+        if (I.nsplit <= 4) {
+          // few pieces: the loads of all of them, for two rows at a time
+#pragma unroll 1
+          for (int r = sw; r < I.nrows; r += 2 * kSoftWarps) {
+            float w[2][4];
+            uint4 h[2][4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int rb = min(r + b * kSoftWarps, I.nrows - 1);
+                w[b][i] = i < I.nsplit ? __ldcg(lse + i * kN + rb) : -INFINITY;
+                h[b][i] = i < I.nsplit ? __ldcg(reinterpret_cast<const uint4*>(part + (i * kN + rb) * kHeadDim) + lane) : make_uint4(0, 0, 0, 0);
+              }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              if (r + b * kSoftWarps >= I.nrows) break;
+              const float M = fmaxf(fmaxf(w[b][0], w[b][1]), fmaxf(w[b][2], w[b][3]));
+              float sum = 0.f, acc[8] = {};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float wi = ex2(w[b][i] - M);
+                sum += wi;
+                merge_add(acc, h[b][i], wi);
+              }
+              store_row(r + b * kSoftWarps, acc, p.out_scale / sum);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int r = sw; r < I.nrows; r += kSoftWarps) {
+            float acc[8];
+            const float sum = merge_row<4>(lse + r, kN, part + r * kHeadDim, kN * kHeadDim, I.nsplit, lane, acc);
+            store_row(r, acc, p.out_scale / sum);
+          }
         }
       };
 

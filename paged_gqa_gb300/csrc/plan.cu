@@ -209,7 +209,7 @@ __device__ __forceinline__ void plan_class(const Problem& p, const Pointers& ptr
   }
   const long long U = tbase;
   // At most U ranges, none empty in units (a range may hold no tile: that CTA has no item).
-  const int C = cut_ctas(U, cp.num_ctas, min_range_units(p));
+  const int C = cut_ctas(U, cp.num_ctas, min_range_units(p, cls));
 
   // ---- per-block split count and partial slots (split_slot_base: no scan); block containing
   // the start of each range

@@ -104,7 +104,7 @@ __device__ __forceinline__ void plan_warp(const Problem& p, Scratch& fs, int num
   }
   const long long total = __shfl_sync(0xffffffffu, x, 31);
   const int U = (int)(total >> 16);
-  const int C = cut_ctas(U, num_ctas, min_range_units(p));
+  const int C = cut_ctas(U, num_ctas, min_range_units(p, 0));
   const int c = blockIdx.x;
   if (c >= C) {  // warp-uniform: no range (C = 0: no verify block at all)
     if (lane == 0) *fcount = 0;
