@@ -34,10 +34,12 @@
 // What bounds it. A 128-key tile takes about 10.2k warp instructions at 48-64 rows: ~3.2k widen, ~1.9k
 // softmax, the rest hands tiles from role to role; issue slots are 63 % busy, the ALU pipe (conversions at
 // half rate) 44 %, tensor cores 25 %, HBM 31 %. With either half of the work taken out (timing only): neither
-// widening nor softmax 248 us, no widening 275, no softmax 337, all of it 431 (256 sequences of
+// widening nor softmax 248 us, no widening 275, no softmax 337, all of it 431 then, 424 now (256 sequences of
 // 8192 keys, 2-4 tokens, 32/2 heads: 1233 MB, 182 us at the HBM rate). 64 sequences of 1k-32k keys,
-// 4 tokens, 16/1 heads: 130 us (46). With 128 rows widening and the products alternate in the shared
-// columns, and a tile takes ~4700 cycles where the products alone take 2230: 2170 us, 887 TFLOP/s.
+// 4 tokens, 16/1 heads: 127 us (46). With 128 rows widening and the products alternate in the shared
+// columns, and a tile takes ~4700 cycles where the products alone take 2230: 2140 us, 899 TFLOP/s.
+// A call's least time is the chain of cold steps (cycles, prefill): plan and item 2-4k, rows of Q 4k, first tile
+// 8k of which the first references 3k, epilogue 4k, its store and count 4k, merge of two pieces 8k.
 // Tried and slower: operands in quarters instead of halves (2910 us, a hand-over costs ~400
 // cycles), both row halves of the softmax in registers (2370, spills), byte permutes for half of
 // V's pairs (2337), one barrier arrival per softmax warp instead of per thread (2204, verify 439).
