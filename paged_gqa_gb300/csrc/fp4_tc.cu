@@ -38,8 +38,10 @@
 // 8192 keys, 2-4 tokens, 32/2 heads: 1233 MB, 182 us at the HBM rate). 64 sequences of 1k-32k keys,
 // 4 tokens, 16/1 heads: 127 us (46). With 128 rows widening and the products alternate in the shared
 // columns, and a tile takes ~4700 cycles where the products alone take 2230: 2140 us, 899 TFLOP/s.
-// A call's least time is the chain of cold steps (cycles, prefill): plan and item 2-4k, rows of Q 4k, first tile
-// 8k of which the first references 3k, epilogue 4k, its store and count 4k, merge of two pieces 8k.
+// A small call is a chain of cold steps. One CTA of a 128-row block, in cycles: set-up 1.7k, the item and its
+// rows of Q 9k, the first S 2.4k, its softmax 10k (first references: 2.7k for each 16 rows; code
+// fetched for the first time), each further tile 5k, epilogue 5.5k, the partial's store and count 6k, a merge of two
+// pieces 11k: ~30 us, where the products take 2.
 // Tried and slower: operands in quarters instead of halves (2910 us, a hand-over costs ~400
 // cycles), both row halves of the softmax in registers (2370, spills), byte permutes for half of
 // V's pairs (2337), one barrier arrival per softmax warp instead of per thread (2204, verify 439).
