@@ -297,6 +297,11 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
 
       auto q_prep = [&](const Item& I, int ii) {
         const int pi = ii & 1;
+        // 128 rows: (token of the block << 16 | head) of each, worked out once (the division per load
+        // makes a small call 1-2 us longer, and code to fetch); the epilogue's first barrier comes
+        // before lse_stage is written
+        uint32_t* where = reinterpret_cast<uint32_t*>(ms.lse_stage);
+        const int t0 = I.row0 / p.G;
         if (ii >= 1 && !mbar_wait_polls(bar(ms.q_free), (ii - 1) & 1, abort_flag, ptr.err)) bad = true;
         if (gi < kN) {
           const int n = gi;
@@ -304,27 +309,35 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           const RowMap m = map_row(I.row0 + n, p.G, I.kvh);
           ms.lim[pi][n] = real ? I.L - I.qn + m.t : -1;
           ms.out_off[pi][n] = real ? (long long)(I.q0 + m.t) * p.o_st + (long long)m.h * p.o_sh : 0;
+          if (kN == 128) where[n] = (uint32_t)(m.t - t0) << 16 | (uint32_t)m.h;
           // padding rows: a finite reference, so their (discarded) scores never vote
           ms.m[pi][n] = real ? kMInit : 0.f;
           ms.mo[pi][n] = kSigma - ms.m[pi][n];
         }
-        // A warp takes whole rows (32 lanes of 16 bytes), all of its rows at once.
-        {
-          constexpr int kRows = kN / kSoftWarps;
-          uint4 v[kRows];
+        if (kN == 128) named_barrier(1, kSoftThreads);
+        // A warp takes whole rows (32 lanes of 16 bytes), four at a time.
+#pragma unroll 1
+        for (int k0 = 0; k0 < kN / kSoftWarps; k0 += 4) {
+          uint4 v[4];
 #pragma unroll
-          for (int k = 0; k < kRows; ++k) {
-            const int r = k * kSoftWarps + sw;
+          for (int k = 0; k < 4; ++k) {
+            const int r = (k0 + k) * kSoftWarps + sw;
             v[k] = make_uint4(0, 0, 0, 0);
             if (r < I.nrows) {
-              const RowMap m = map_row(I.row0 + r, p.G, I.kvh);
+              RowMap m;
+              if (kN == 128) {
+                m.t = t0 + (int)(where[r] >> 16);
+                m.h = (int)(where[r] & 0xffffu);
+              } else {
+                m = map_row(I.row0 + r, p.G, I.kvh);
+              }
               v[k] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(ptr.q) +
                                                      (long long)(I.q0 + m.t) * p.q_st + (long long)m.h * p.q_sh + lane * 8);
             }
           }
 #pragma unroll
-          for (int k = 0; k < kRows; ++k) {
-            const int r = k * kSoftWarps + sw;
+          for (int k = 0; k < 4; ++k) {
+            const int r = (k0 + k) * kSoftWarps + sw;
             uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
             uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                                     __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
