@@ -37,7 +37,7 @@
 // widening nor softmax 248 us, no widening 275, no softmax 337, all of it 431 then, 424 now (256 sequences of
 // 8192 keys, 2-4 tokens, 32/2 heads: 1233 MB, 182 us at the HBM rate). 64 sequences of 1k-32k keys,
 // 4 tokens, 16/1 heads: 127 us (46). With 128 rows widening and the products alternate in the shared
-// columns, and a tile takes ~4700 cycles where the products alone take 2230: 2140 us, 899 TFLOP/s.
+// columns, and a tile takes ~4700 cycles where the products alone take 2230: 2131 us, 903 TFLOP/s.
 // A small call is a chain of cold steps. One CTA of a 128-row block, in cycles: set-up 1.7k, the item and its
 // rows of Q 9k, the first S 2.4k, its softmax 10k (first references: 2.7k for each 16 rows; code
 // fetched for the first time), each further tile 5k, epilogue 5.5k, the partial's store and count 6k, a merge of two

@@ -12,7 +12,9 @@
 // the kv tile is loaded once and reused by all q_len x G rows of the kv head).
 // Online softmax per row with quad shuffles; split pieces write partial results that
 // the last piece merges. The kFp4 instance gathers 4-bit K/V (code times scale is exact in
-// tf32 too): the simplest form of that attention, and the cross-check of its tcgen05 kernel.
+// tf32 too): the simplest form of that attention, and the cross-check of its faster kernels. It widens
+// byte by byte with plain loads: 1072 us for 64 sequences of 4 tokens and 1k-32k keys, 16/1
+// heads, where the tcgen05 kernel takes 127.
 #include "common.cuh"
 #include "device_util.cuh"
 #include "fp4.cuh"
