@@ -1,4 +1,6 @@
 """The 4-bit paged cache on the GPU: write, read, attention, and a decoding step of all of them."""
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
@@ -351,6 +353,91 @@ def test_calls_on_other_streams_and_growing_batches():
     _ok()
     for c, out in outs:
         fu.check(c, out, "streams")
+
+
+def test_two_threads_at_once():
+    """Calls of two host threads, each on its own stream, in the library's workspace and in one of each thread's."""
+    import threading
+    cases = [fu.make([(1, 9000), (4, 700)], 16, 1, 16, seed=140), fu.make([(1, 2000)] * 6, 8, 1, 64, seed=141)]
+    want = [_attn(c) for c in cases]
+    torch.cuda.synchronize()
+    wrong, streams = [], [torch.cuda.Stream() for _ in cases]
+
+    def run(c, w, stream):
+        with torch.cuda.stream(stream):
+            ws = _workspace(c)
+            for i in range(40):
+                out = torch.full(c.q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+                if i % 2:
+                    _attn(c, out)
+                else:
+                    pg.paged_gqa_attn_fp4_ex(c.q, c.k, c.v, c.table, c.lens, c.qsl, c.kd, c.vd, c.scale, out, ws)
+                if not bool((out == w).all()):
+                    wrong.append(i)
+    threads = [threading.Thread(target=run, args=a) for a in zip(cases, want, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _ok()
+    assert not wrong
+    for c, w in zip(cases, want):
+        fu.check(c, w, "threads")
+
+
+def _far(t, step):
+    """t's values in a view whose first axis steps far: `step` elements."""
+    buf = torch.empty(step * (t.shape[0] - 1) + t[0].numel(), dtype=t.dtype, device="cuda")
+    v = buf.as_strided(t.shape, (step, *t[0].contiguous().stride()))
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("seqs,hq", [([(4, 50), (1, 33)], 16), ([(1, 60), (1, 20)], 8), ([(70, 75)], 8)])
+def test_offsets_beyond_32_bits(seqs, hq):
+    """Pages a gigabyte apart, query rows more than 2^32 bytes apart from first to last: the whole step."""
+    c = fu.make(seqs, hq, 1, 16, seed=150)
+    gap = (5 * 2 ** 30 // (c.k.shape[0] - 1) + 15) // 16 * 16
+    c.k, c.v = _far(c.k, gap), _far(c.v, gap)
+    gap = (2 ** 32 // 2 // (c.T - 1) + 256) // 8 * 8 + 256 * hq
+    kn, vn = (_far(x, gap) for x in _new(c.T, 1, 151))
+    want = fp4.write(kn.float().cpu().numpy(), vn.float().cpu().numpy(), c.k.contiguous().cpu().numpy(), c.v.contiguous().cpu().numpy(),
+                     c.table.cpu().numpy(), c.lens.cpu().numpy(), c.qsl.cpu().numpy(), c.kd, c.vd)
+    pg.paged_gqa_cache_write_fp4(kn, vn, c.k, c.v, c.table, c.lens, c.qsl, c.kd, c.vd)
+    _ok()
+    assert (c.k.contiguous().cpu().numpy() == want[0]).all() and (c.v.contiguous().cpu().numpy() == want[1]).all()
+    pg.paged_gqa_cache_read_fp4(c.k, c.v, c.table, c.lens, c.qsl, c.kd, c.vd, kn, vn)
+    back = fp4.read(*want, c.table.cpu().numpy(), c.lens.cpu().numpy(), c.qsl.cpu().numpy(), c.kd, c.vd)
+    for x, w in ((kn, back[0]), (vn, back[1])):
+        assert (np.abs(x.double().cpu().numpy() - w) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(w)).all()
+    c.q = _far(c.q, gap)
+    out = _far(torch.full(c.q.shape, float("nan"), dtype=torch.bfloat16, device="cuda"), gap)
+    pos = torch.arange(c.T, dtype=torch.int32, device="cuda")[None]
+    inv = (10000.0 ** (-torch.arange(0, 64, 2) / 64)).float().cuda()
+    q0 = c.q.double().cpu().numpy()
+    pg.paged_gqa_rope(c.q, kn, pos, inv, [32], c.q, torch.empty(c.T, 1, 256, dtype=torch.bfloat16, device="cuda"))
+    ref = ro.rope(q0, pos.cpu().numpy(), inv.cpu().numpy(), [32], False, False)
+    assert (np.abs(c.q.double().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * np.abs(q0).max()).all()
+    for path in (0, 1):
+        out.fill_(float("nan"))
+        prev = pg.paged_gqa_set_path(path)
+        try:
+            _attn(c, out)
+        finally:
+            pg.paged_gqa_set_path(prev)
+        _ok()
+        fu.check(dataclasses.replace(c, q=c.q.contiguous(), k=c.k.contiguous(), v=c.v.contiguous()), out, "far apart")
+
+
+def test_sequences_that_share_pages():
+    """Three sequences on one prefix (the same pages in every table row), each with its own last page."""
+    c = fu.make([(2, 700), (2, 700), (1, 690)], 16, 1, 32, seed=142)
+    c.table[1:, :20] = c.table[0, :20]
+    _ok()
+    fu.check(c, _attn(c), "shared prefix")
+    c.table[2] = c.table[1]  # and two of them in all of them
+    fu.check(c, _attn(c), "shared pages")
+    _ok()
 
 
 def test_results_repeat_bit_for_bit():
