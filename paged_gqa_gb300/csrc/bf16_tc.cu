@@ -76,7 +76,9 @@ struct Misc {
   alignas(16) float merge_w[kMergeMaxSplits * kSlotRows];
   alignas(8) uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
   uint64_t s_full[2], pv_done[2];
-  uint64_t p_full, q_full, q_free, o_ready, o_free, drain[2];
+  // P of even and of odd sub-tiles: a softmax warp can publish P(g + 1) before another one of the CTA
+  // has published P(g), and on one barrier its arrival would count for P(g).
+  uint64_t p_full[2], q_full, q_free, o_ready, o_free, drain[2];
   uint64_t never;  // no thread ever arrives (the failure-path test waits on it)
   uint32_t tmem_base;
   int abort_flag;
@@ -184,7 +186,8 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
       mbar_init(bar(ms.s_full[b]), 1);
       mbar_init(bar(ms.pv_done[b]), 1);
     }
-    mbar_init(bar(ms.p_full), kSoftThreads);
+    mbar_init(bar(ms.p_full[0]), kSoftThreads);
+    mbar_init(bar(ms.p_full[1]), kSoftThreads);
     mbar_init(bar(ms.q_full), kSoftThreads);
     mbar_init(bar(ms.q_free), 1);
     mbar_init(bar(ms.o_ready), 1);
@@ -326,7 +329,7 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
           } else {
             // the first P.V of an item overwrites O: the previous epilogue must be done
             if (j == 0 && ii >= 1 && !(ok = mbar_wait(bar(ms.o_free), (ii - 1) & 1, abort_flag, ptr.err))) break;
-            if (!(ok = mbar_wait(bar(ms.p_full), g & 1, abort_flag, ptr.err))) break;
+            if (!(ok = mbar_wait(bar(ms.p_full[b]), (g >> 1) & 1, abort_flag, ptr.err))) break;
             const uint32_t st = g % kVStages;
             if (!(ok = mbar_wait(bar(ms.v_full[st]), (g / kVStages) & 1, abort_flag, ptr.err))) break;
             tc_fence_after();
@@ -509,7 +512,7 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
         tmem_wait_st();
         fence_proxy_async_smem();  // zeroed V rows, if any
         tc_fence_before();
-        mbar_arrive(bar(ms.p_full));
+        mbar_arrive(bar(ms.p_full[b]));
         // P.V(g-1) has a barrier of its own (its S buffer's), whose next phase needs P(g+1):
         // the wait cannot mistake a later phase for this one, however late it runs.
         if (!warp_rescale && g >= 1 &&
