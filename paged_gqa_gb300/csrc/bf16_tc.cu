@@ -205,6 +205,7 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
   if (kFused) {
     __syncthreads();  // the sequences are staged
     if (warp == 0) self_plan::plan_warp(p, fs, cp.num_ctas, lane, ms.fitem, ms.fseq, &ms.fcount);
+    fence_proxy_async_smem();  // the scratch lies where the copies go
   }
   tc_fence_before();
   __syncthreads();

@@ -95,7 +95,7 @@ __device__ __forceinline__ void load32_fp4(float* dst, const uint8_t* page, int 
   const int tok = slot % kFp4Block;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const int byte = seg * 16 + i, grp = seg * 2 + i / 8;
+    const int byte = seg * 16 + i, grp = 2 * byte / kFp4Group;
     const uint32_t code = is_v ? blk[byte * kFp4Block + tok] : page[slot * kFp4Row + byte];
     const uint32_t sc = is_v ? blk[kFp4BlockScales + grp * kFp4Block + tok] : page[slot * kFp4Row + kFp4Codes + grp];
     const float2 x = fp4::code_pair(code);
