@@ -287,6 +287,7 @@ int validate(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
   p.q_is_fp8 = q->dtype == PG_E4M3;
   p.kv_is_fp8 = k->dtype == PG_E4M3;
   p.kv_is_fp4 = 0;
+  p.zero2 = 0;
   p.q_cast = q_cast ? 1 : 0;
   p.q_amax_parts = 0;
   p.q_st = q->stride[0];
@@ -730,6 +731,7 @@ int attn_fp4(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
   p.W = (int)W;
   p.NB = (int)k->shape[0];
   p.kv_is_fp4 = 1;
+  p.zero2 = 0;
   p.q_st = q->stride[0];
   p.q_sh = q->stride[1];
   p.k_sb = k->stride[0];

@@ -127,6 +127,8 @@ struct Problem {
   int fused_verify;
   // No plan kernel runs in this call (4-bit caches): the verify kernel flags invalid sequences.
   int unplanned;
+  // Two fp32 zeros: an addend that keeps the compiler from fusing a product with a sum (4-bit caches).
+  unsigned long long zero2;
 };
 
 // Units a range of the cut has at least (kMinRangeUnits). 4-bit caches: a tile takes longer, and

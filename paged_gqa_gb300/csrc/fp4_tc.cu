@@ -375,7 +375,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const bool vis = !need_mask || (key < kv_hi && key <= ms.lim[pi][cc + n + i]);
-            const float x = warp_max(vis ? v[i] * ms.cs[pi][cc + n + i] : -INFINITY);
+            const float x = warp_max(vis ? __fmul_rn(v[i], ms.cs[pi][cc + n + i]) : -INFINITY);
             if (lane == n + i) r = x;
           }
         }
@@ -584,16 +584,28 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             const bool active = cb < nc;
             uint64_t x[8];
             if (active) {
-              while (true) {
+              // At most two passes: the one after a new reference asks for no other. With 64 rows it
+              // leaves before the vote, with 128 the limit of the vote is out of reach then (the other way
+              // round 436 for 428 us and 2205 for 2125 us: registers).
+              float limit = kTau + kSigma;
+              bool moved = false;
+#pragma unroll 1
+              for (;;) {
                 tmem_ld16(tmem + lane_addr + C::kColS + sb * kN + c0 + cb, x);
                 tmem_wait_ld();
-                // x = s c - m + sigma: the exponent of P
+                // x = s c - m + sigma, the exponent of P, from the rounded product that new_reference
+                // takes its maxima of: with m >= s c, x is at most rn(m + rn(sigma - m)) <= kTau + kSigma
+                // whatever the size of m (sigma - m is off by up to 4 where m is about 2^26 and is -m
+                // beyond), so P fits f16, and equal scores weigh the same in every tile. A product fused
+                // with the sum would be off from m by up to half a step of it, 64 for scores of 2^30
+                // (256 sequences: 424 us so, 428 with rounded ones). The compiler fuses mul.rn.f32x2
+                // with add.rn.f32x2 (measured), but cannot fuse an fma whose zero it does not know.
 #pragma unroll
                 for (int n = 0; n < 16; n += 4) {
                   const ulonglong2 o4 = *reinterpret_cast<const ulonglong2*>(&ms.mo[pi][c0 + cb + n]);
                   const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(&ms.cs[pi][c0 + cb + n]);
-                  x[n / 2] = fma2(x[n / 2], s4.x, o4.x);
-                  x[n / 2 + 1] = fma2(x[n / 2 + 1], s4.y, o4.y);
+                  x[n / 2] = add2(fma2(x[n / 2], s4.x, p.zero2), o4.x);
+                  x[n / 2 + 1] = add2(fma2(x[n / 2 + 1], s4.y, p.zero2), o4.y);
                 }
                 if (need_mask) {
                   const int seen = key < kv_hi ? key : 0x7fffffff;
@@ -604,6 +616,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
                     x[n / 2] = pack2(seen <= l2.x ? v.x : -INFINITY, seen <= l2.y ? v.y : -INFINITY);
                   }
                 }
+                if (kN == 64 && moved) break;
                 float xmax = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
@@ -611,11 +624,13 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
                   xmax = max3f(xmax, v.x, v.y);
                 }
                 // does any score of these 16 rows exceed its row's reference by more than 2^kTau?
-                if (!barrier_or(group_bar, 128, xmax > kTau + kSigma)) break;
+                if (!barrier_or(group_bar, 128, xmax > (kN == 128 ? limit : kTau + kSigma))) break;
                 new_reference(c0 + cb, pi, sb, j > 0, g, need_mask, key, kv_hi);
 #pragma unroll
                 for (int n = 0; n < 16; n += 2)
                   l[(cb + n) / 2] = mul2(l[(cb + n) / 2], *reinterpret_cast<const uint64_t*>(&ms.alpha[c0 + cb + n]));
+                if (kN == 128) limit = INFINITY;
+                else moved = true;
               }
             }
             if (cb + 16 == kCols) {  // S has been read for the last time
