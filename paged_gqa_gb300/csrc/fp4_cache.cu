@@ -52,9 +52,10 @@ __device__ __forceinline__ void for_each_unit(const Fp4CacheArgs& a, int t, int 
       q1 = __ldg(a.qsl + s + 1);
       L = __ldg(a.seq_lens + s);
     }
-    const int qn = q1 - q0;
-    const long long pos = (long long)L - qn + (t - q0);
-    if (t < q0 || t >= q1 || qn > L || pos < 0 || (pos >> a.p_shift) >= a.W) {
+    // As in the attention, a sequence whose tokens do not lie in [0, T) has no valid token: its
+    // units are cut at q1, and so end by T.
+    const long long qn = (long long)q1 - q0, pos = L - qn + (t - q0);
+    if (q0 < 0 || q1 > a.T || t < q0 || t >= q1 || qn > L || pos < 0 || (pos >> a.p_shift) >= a.W) {
       if (lane == 0) atomicOr(a.err, kErrBounds);
       fn(t, 1, 0, -1);  // a token without a place
       ++t;
