@@ -289,8 +289,10 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
         float top = -INFINITY;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          s[b] = (s[b] + s1[b]) * c[b];
-          s[2 + b] = (s[2 + b] + s1[2 + b]) * c[b];
+          // rounded before anything is taken from it, as the references are: fused with that, a score of
+          // 2^30 would be off from its own maximum by up to 64
+          s[b] = __fmul_rn(s[b] + s1[b], c[b]);
+          s[2 + b] = __fmul_rn(s[2 + b] + s1[2 + b], c[b]);
           if (need_mask) {
             if (ka >= I.kv_hi || ka > lim[b]) s[b] = -INFINITY;
             if (kc >= I.kv_hi || kc > lim[b]) s[2 + b] = -INFINITY;
