@@ -567,6 +567,18 @@ bool rows_overlap(const pg_tensor* a, const pg_tensor* b) {
   return false;
 }
 
+// Do a checked bf16 [T, H, 256] tensor's addresses, first to last, meet the n bytes at p?
+bool rows_meet(const pg_tensor* t, const void* p, long long n) {
+  if (!t->data || !t->shape[0] || !t->shape[1] || n <= 0) return false;
+  long long lo = 0, hi = kHeadDim;  // elements, relative to data
+  for (int i = 0; i < 2; ++i) {
+    const long long last = t->shape[i] > 1 ? (t->shape[i] - 1) * t->stride[i] : 0;
+    (last < 0 ? lo : hi) += last;
+  }
+  const intptr_t base = reinterpret_cast<intptr_t>(t->data), q = reinterpret_cast<intptr_t>(p);
+  return base + 2 * lo < q + n && q < base + 2 * hi;
+}
+
 int current_device(DeviceState** ds) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1167,6 +1179,12 @@ int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* posi
     if (rows_overlap(out[i], in[1 - i])) return fail(PG_ERR_INVALID_ARG, "%s overlaps %s", names[i][1], names[1 - i][0]);
   }
   if (rows_overlap(q_out, k_out)) return fail(PG_ERR_INVALID_ARG, "q_out overlaps k_out");
+  for (int i = 0; i < 2; ++i) {
+    for (int x = 0; x < A; ++x)
+      if (rows_meet(out[i], static_cast<const int32_t*>(positions->data) + x * positions->stride[0], T * 4))
+        return fail(PG_ERR_INVALID_ARG, "%s overlaps positions", names[i][1]);
+    if (rows_meet(out[i], inv_freq->data, half * 4)) return fail(PG_ERR_INVALID_ARG, "%s overlaps inv_freq", names[i][1]);
+  }
   a.pos = static_cast<const int32_t*>(positions->data);
   a.pos_sa = positions->stride[0];
   a.inv_freq = static_cast<const float*>(inv_freq->data);
