@@ -261,7 +261,8 @@ int paged_gqa_cache_write(const pg_tensor* k_new, const pg_tensor* v_new, const 
  * A group with a NaN gets a NaN scale, so its values read back as NaN; infinities saturate.
  * A descale near amax / (6 * 448) of the tensor uses the scales' whole range.
  * Nothing else in the caches changes. k_new and v_new need 16-byte aligned rows; the caches'
- * (page, head) blocks must not overlap, nor the two caches each other. Descales must be finite, positive and have a finite
+ * (page, head) blocks must not overlap, nor the two caches each other (refused; caches of one
+ * allocation with the same page stride are told apart). Descales must be finite, positive and have a finite
  * reciprocal. Errors as paged_gqa_cache_write (a bad position or page: that row is skipped; a sequence
  * whose tokens do not lie in [0, T): all of its rows).
  * Allocates nothing.

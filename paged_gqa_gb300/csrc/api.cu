@@ -532,10 +532,11 @@ int check_rows(const pg_tensor* t, const char* name, bool written) {
   return PG_OK;
 }
 
-// Do two checked bf16 [T, H, 256] tensors share bytes? Rows of one allocation with equal token strides
-// (slices of a projection's output) are told apart exactly; otherwise intersecting address
-// ranges count as shared.
-bool rows_overlap(const pg_tensor* a, const pg_tensor* b) {
+// Do two tensors share bytes, whose first two dims index runs of `span` contiguous elements of `size` bytes
+// (rows of bf16 [T, H, 256], pages of 4-bit caches)? Runs of one allocation with equal strides of the first dim
+// (slices of a projection's output) are told apart exactly; otherwise intersecting address ranges
+// count as shared.
+bool runs_overlap(const pg_tensor* a, const pg_tensor* b, long long span, int size) {
   if (!a->data || !b->data || !a->shape[0] || !b->shape[0] || !a->shape[1] || !b->shape[1]) return false;
   long long ext[2], st[2], sh[2];
   const pg_tensor* t[2] = {a, b};
@@ -544,13 +545,14 @@ bool rows_overlap(const pg_tensor* a, const pg_tensor* b) {
     st[i] = t[i]->shape[0] > 1 ? t[i]->stride[0] : other->shape[0] > 1 ? other->stride[0] : 0;
     sh[i] = t[i]->shape[1] > 1 ? t[i]->stride[1] : 0;
     if (st[i] < 0 || sh[i] < 0) return true;
-    ext[i] = (t[i]->shape[0] - 1) * st[i] + (t[i]->shape[1] - 1) * sh[i] + kHeadDim;
+    ext[i] = (t[i]->shape[0] - 1) * st[i] + (t[i]->shape[1] - 1) * sh[i] + span;
   }
-  // b's first value after a's, in elements (rows are 16-byte aligned)
-  const long long delta = ((long long)reinterpret_cast<intptr_t>(b->data) - (long long)reinterpret_cast<intptr_t>(a->data)) / 2;
+  // b's first value after a's, in elements (runs are 16-byte aligned)
+  const long long delta =
+      ((long long)reinterpret_cast<intptr_t>(b->data) - (long long)reinterpret_cast<intptr_t>(a->data)) / size;
   if (delta >= ext[0] || -delta >= ext[1]) return false;
   if (st[0] != st[1] || a->shape[1] * b->shape[1] > 1 << 16) return true;
-  // is a row of b at less than a row's length from one of a: |delta + hb sh_b - ha sh_a + n st| < 256,
+  // is a run of b at less than a run's length from one of a: |delta + hb sh_b - ha sh_a + n st| < span,
   // -T_a < n < T_b?
   const long long S = st[0], lo = 1 - a->shape[0], hi = b->shape[0] - 1;
   for (long long ha = 0; ha < a->shape[1]; ++ha)
@@ -558,14 +560,15 @@ bool rows_overlap(const pg_tensor* a, const pg_tensor* b) {
       const long long d = delta + hb * sh[1] - ha * sh[0];
       long long n = S > 0 ? -d / S : 0;
       for (long long c = std::max(lo, n - 1); c <= std::min(hi, n + 1); ++c)
-        if (std::llabs(d + c * S) < kHeadDim) return true;
+        if (std::llabs(d + c * S) < span) return true;
       if (n - 1 > hi || n + 1 < lo) {  // the nearest n is out of range: the range's end is the closest
         const long long c = n > hi ? hi : lo;
-        if (std::llabs(d + c * S) < kHeadDim) return true;
+        if (std::llabs(d + c * S) < span) return true;
       }
     }
   return false;
 }
+bool rows_overlap(const pg_tensor* a, const pg_tensor* b) { return runs_overlap(a, b, kHeadDim, 2); }
 
 // Do a checked bf16 [T, H, 256] tensor's addresses, first to last, meet the n bytes at p?
 bool rows_meet(const pg_tensor* t, const void* p, long long n) {
@@ -609,8 +612,10 @@ int fp4_cache_call(bool write, const pg_tensor* kx, const pg_tensor* vx, const p
     t_last_error.clear();
     return PG_OK;
   }
-  if (write ? kc->data && kc->data == vc->data : rows_overlap(kx, vx))
-    return fail(PG_ERR_INVALID_ARG, write ? "k_cache and v_cache are the same memory" : "k_out and v_out overlap");
+  if (write && kc->data && kc->data == vc->data)
+    return fail(PG_ERR_INVALID_ARG, "k_cache and v_cache are the same memory");
+  if (write && runs_overlap(kc, vc, kc->shape[2] * kFp4Row, 1)) return fail(PG_ERR_INVALID_ARG, "k_cache and v_cache overlap");
+  if (!write && rows_overlap(kx, vx)) return fail(PG_ERR_INVALID_ARG, "k_out and v_out overlap");
   DeviceState* ds = nullptr;
   if ((st = current_device(&ds))) return st;
   Fp4CacheArgs a;

@@ -57,3 +57,48 @@ def test_neighbours_of_the_outputs_are_no_overlap():
     f.copy_(inv)
     pg.paged_gqa_rope(q, k, pos, f, [16, 8, 8], out, k_out)
     assert bool((out == want).all())
+
+
+def _cache(offset, shape=ab.CACHE, stride=None):
+    return FakeTensor(shape, ab.U8, ptr=(1 << 26) + offset, stride=stride)
+
+
+PAGE = 16 * 144          # of one head; CACHE has 2 heads
+BOTH = [4 * PAGE, PAGE, 144, 1]          # the strides of one half of [pages, 2, heads, 16, 144]
+INNER = [4 * PAGE, 2 * PAGE, 144, 1]     # and of [pages, heads, 2, 16, 144]
+
+
+@pytest.mark.parametrize("k,v", [
+    (_cache(0), _cache(16)),
+    (_cache(0), _cache(9 * 2 * PAGE)),                       # k's last page is v's first
+    (_cache(0, stride=BOTH), _cache(PAGE, stride=BOTH)),     # k's second head is v's first
+    (_cache(0, stride=BOTH), _cache(2 * PAGE - 16, stride=BOTH)),
+    (_cache(0, stride=BOTH), _cache(4 * PAGE, stride=BOTH)),  # v's pages are k's next ones
+    (_cache(0, stride=INNER), _cache(2 * PAGE, stride=INNER)),
+    (_cache(0, stride=INNER), _cache(PAGE, stride=BOTH)),    # the same page stride, other heads
+])
+def test_write_refuses_caches_that_overlap(k, v):
+    for a, b in ((k, v), (v, k)):
+        far = dict(k=a, v=b, kn=ab._at((8, 2, 256), 0), vn=ab._at((8, 2, 256), 1 << 20))
+        assert ab._write(ab._args(**far)) == -1 and "k_cache and v_cache overlap" in pg.paged_gqa_last_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("layout", ["[2, pages, heads]", "[pages, 2, heads]", "[pages, heads, 2]", "[heads, pages, 2]"])
+def test_caches_of_one_allocation_are_no_overlap(layout):
+    NB, H, P, T = 6, 2, 16, 40
+    order = {"[2, pages, heads]": (2, NB, H), "[pages, 2, heads]": (NB, 2, H), "[pages, heads, 2]": (NB, H, 2),
+             "[heads, pages, 2]": (H, NB, 2)}[layout]
+    whole = torch.zeros(*order, P, 144, dtype=torch.uint8, device="cuda")
+    axis = layout.strip("[]").split(", ").index("2")
+    k, v = whole.select(axis, 0), whole.select(axis, 1)
+    if layout.startswith("[heads"):
+        k, v = k.transpose(0, 1), v.transpose(0, 1)
+    kn, vn = (torch.randn(T, H, 256).bfloat16().cuda() for _ in range(2))
+    table = torch.tensor([[3, 0, 5, 1]], dtype=torch.int32, device="cuda")
+    lens, qsl = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([50], [0, T]))
+    pg.paged_gqa_cache_write_fp4(kn, vn, k, v, table, lens, qsl, 0.01, 0.02)
+    want = [torch.zeros(NB, H, P, 144, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pg.paged_gqa_cache_write_fp4(kn, vn, *want, table, lens, qsl, 0.01, 0.02)
+    assert pg.paged_gqa_check_device_errors() == 0, pg.paged_gqa_last_error()
+    assert bool((k == want[0]).all()) and bool((v == want[1]).all())
