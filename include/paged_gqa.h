@@ -393,9 +393,10 @@ int paged_gqa_set_stall_test(uint32_t wait_ns);
 int paged_gqa_last_plan(int64_t* out8);
 
 /*
- * Profiling hook (process-wide): while set, every call records `start` on its stream
- * immediately before the attention kernel of class `cls` (0 = verify blocks,
- * 1 = prefill blocks) and `stop` immediately after it. Both are cudaEvent_t handles
+ * Profiling hook (process-wide): while set, every dense call (not sparse attention) records `start`
+ * on its stream immediately before the attention kernel of class `cls` (0 = verify blocks,
+ * 1 = prefill blocks) and `stop` immediately after it; a 4-bit call of at most 64 rows
+ * (T * Hq / Hkv) has no kernel of class 1. Both are cudaEvent_t handles
  * owned by the caller; pass NULLs to stop recording. Returns PG_OK or
  * PG_ERR_INVALID_ARG.
  */

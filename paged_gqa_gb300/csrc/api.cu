@@ -679,21 +679,25 @@ int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, 
   p.unplanned = no_prefill && p.fused_verify && !captured;
   int launched = 0, used = 0;
   cudaError_t e;
+  bool prev_ev = false;  // an event was recorded after the previous class's kernel: no programmatic launch behind it
   for (int c = 0; c < kNumClasses; ++c) {
     // the plan kernel goes before the verify class, or after it where that plans itself
     const bool plan_here = c == (p.fused_verify ? 1 : 0);
     if (plan_here && !p.unplanned) {
-      e = launch_plan(p, ptr, cp[0], cp[1], !p.fused_verify, p.fused_verify, stream);
+      e = launch_plan(p, ptr, cp[0], cp[1], !p.fused_verify, p.fused_verify && !prev_ev, stream);
       if (e != cudaSuccess) return cuda_fail(e, "plan launch");
       ++launched;
+      prev_ev = false;
     }
     if (c == 1 && no_prefill) break;
+    cudaEvent_t ev0 = g_ev_start[c].load(), ev1 = g_ev_stop[c].load();
+    if (ev0 && (e = cudaEventRecord(ev0, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
     if (c == 0 && decode) {
       if (launch_fp4_decode(p, ptr, cp[c], stream) < 0)
         return fail(PG_ERR_CUDA, "4-bit decode launch failed: %s", tc_last_error());
       used |= 128;
     } else if (tc) {
-      if (launch_fp4_tc(p, ptr, cp[c], c, stream, c == 1) < 0)
+      if (launch_fp4_tc(p, ptr, cp[c], c, stream, c == 1 && !ev0 && !prev_ev) < 0)
         return fail(PG_ERR_CUDA, "tcgen05 4-bit launch failed: %s", tc_last_error());
       used |= 2 << c;
     } else {
@@ -702,6 +706,8 @@ int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, 
       used |= 8 << c;
     }
     ++launched;
+    if (ev1 && (e = cudaEventRecord(ev1, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
+    prev_ev = ev1 != nullptr;
   }
   plan_info[0] = cp[0].num_ctas;
   plan_info[1] = cp[1].num_ctas;
