@@ -289,8 +289,10 @@ int paged_gqa_cache_read_fp4(const pg_tensor* k_cache, const pg_tensor* v_cache,
  * paged_gqa_attn_fp4 -- paged_gqa_attn on 4-bit caches: single new tokens, verify steps and
  * prefill chunks in one batch. q and out are bf16 [T, Hq, 256]; the other arguments, the mask,
  * the errors and what is left untouched are those of paged_gqa_attn. K and V enter the
- * products exactly (code * scale has 6 significant bits); scores, sums and outputs are held
- * in fp32. out and q must not overlap. A NaN in V (a NaN scale) reaches the new tokens that see
+ * products exactly (code * scale has 6 significant bits), Q exactly within 2^-28 of its row's largest
+ * value. Scores, the softmax's references and sums and the sums of P.V are held in fp32; two things
+ * are rounded to f16 (2^-11) on the way: P before P.V, and the normalised output of a sequence's piece
+ * where it is split over SMs. out and q must not overlap (refused). A NaN in V (a NaN scale) reaches the new tokens that see
  * its key, and may reach the others of that sequence that share a block of rows with one.
  * A new call and an older one on another stream are ordered by the library (they
  * share its workspace), so such calls do not overlap; in a stream capture the call returns

@@ -131,16 +131,24 @@ struct Problem {
   unsigned long long zero2;
 };
 
-// Units a range of the cut has at least (kMinRangeUnits). 4-bit caches: a tile takes longer, and
-// the last piece merges row by row, so the rows of a block decide. Graph replays over 6, 4, 3, 2, 1: one sequence of 1200 keys, 8 rows: 19.7, 15.7, 15.4,
-// 13.6, 13.2 us; 16 rows: 24.3, 18.1, 18.4, 15.9, 16.4; 64 rows: 31.3, 24.1, 24.6, 23.3, 25.8; one of 16384 keys,
-// 16 rows: 26.3, 24.4, 25.4, 25.2, 35.1; 64 rows: 40.5, 40.9, 47.6, 53.6, 91.9 (as many pieces as
-// tiles to merge for every row). Batches that fill the SMs do not change.
+// Units a range of the cut has at least (kMinRangeUnits). 4-bit caches: a tile takes longer, and the
+// last piece merges row by row, so the rows of a block decide. Graph replays, us:
+//   verify class, one sequence, over 6, 4, 3, 2, 1 units
+//     1200 keys    8 rows 19.7, 15.7, 15.4, 13.6, 13.2   16 rows 24.3, 18.1, 18.4, 15.9, 16.4
+//                  64 rows 31.3, 24.1, 24.6, 23.3, 25.8
+//     16384 keys   16 rows 26.3, 24.4, 25.4, 25.2, 35.1   64 rows 40.5, 40.9, 47.6, 53.6, 91.9 (as many
+//                  pieces as tiles to merge for every row)
+//   prefill class, over 6, 4, 3, 2 units (8 rows a token)
+//     one chunk    16 tokens on 4096 keys 53, 47, 47, 46; on 16384 64, 64, 73, 84; 512 on 2048 55, 62, 65, 65;
+//                  1024 on as many 58, 53, 40, 39; 128 on 8192 57, 57, 58, 58
+//     two chunks   of 116-134 tokens on 787-4084 keys 59, 57, 47, 49
+// For prefill no value is the best everywhere: 4 is within 5 % of the best at contexts of 4096 and more (2:
+// 31 %), and loses up to 34 % at short ones. Batches that fill the SMs do not change.
+constexpr int kMinFewRows = 2, kMinVerify = 4, kMinPrefill = 4;
 __host__ __device__ __forceinline__ int min_range_units(const Problem& p, int cls) {
   if (!p.kv_is_fp4) return kMinRangeUnits;
-  constexpr int kX = 4;
-  if (cls == 1) return kX;
-  return (long long)p.T * p.G <= 16ll * p.num_seqs ? 2 : 4;
+  if (cls == 1) return kMinPrefill;
+  return (long long)p.T * p.G <= 16ll * p.num_seqs ? kMinFewRows : kMinVerify;
 }
 
 struct Pointers {
@@ -168,8 +176,10 @@ struct ClassPlan {
   // changes on every call, CUDA-graph replays included) and a workspace needs no zeroing.
   unsigned long long* counters;
   unsigned long long* epoch;  // [1] workspace word the plan kernel advances once per call
-  uint16_t* part_o;        // [max_slots][slot_rows][kHeadDim] f16: O / l in cache-code units
-                           // (v_descale is applied by the merge; |O / l| <= 448 fits f16)
+  uint16_t* part_o;        // [max_slots][slot_rows][kHeadDim] f16: O / l in cache-code units (v_descale is
+                           // applied by the merge; |O / l| is at most 448, in 4-bit caches 6 * 448, and
+                           // fits f16). Half the bytes of fp32 to write and to read back, for a rounding
+                           // of 2^-11 where the output's is 2^-8.
   float* part_lse;         // [max_slots][slot_rows] (log2 units)
   int num_ctas;
   int max_blocks, max_items, max_slots;

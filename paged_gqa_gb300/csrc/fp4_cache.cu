@@ -15,8 +15,9 @@
 // one warp, lane l holding values 8l .. 8l + 7, i.e. code bytes 4l .. 4l + 3. A whole block
 // of V leaves as 64 contiguous bytes per lane; a part of one as single bytes (16 apart).
 // Measured: writing 8 chunks of 8001-8192 tokens, 2 heads, and reading them back 67 us (339 MB, 5.0 TB/s; 50 us
-// at the copy rate); reading 6 prefixes of up to 16384 tokens, 2 heads, 31 us (158 MB, 5.1 TB/s; 23 us). A step's
-// 256 tokens take 6 us to write and as many to read: launch and two dependent reads (table, row).
+// at the copy rate); alone, from a graph, the write takes 40 us (25 at the copy rate) and the read 31 (25).
+// Reading 6 prefixes of up to 16384 tokens, 2 heads: 31 us (158 MB, 5.1 TB/s; 23 us). A step's 256 tokens take
+// 3.7 us to write and 3.3 to read, from a graph: launch and two dependent reads (table, row).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,8 +36,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kBatch = 4;       // tokens whose rows are in flight at once in a warp
-constexpr int kWarpsPerSm = 16; // a call with fewer (token, head) rows than this many warps per SM
-                                // gives each warp one token, a larger one up to a block's 16
+constexpr int kWarpsPerSm = 16; // A call with fewer (token, head) rows than this many warps per SM launches a
+                                // warp for each; only those whose token starts a block of 16 or a sequence
+                                // have a unit to move, the others look their sequence up and leave. A
+                                // larger call gives a warp a window of up to 16 tokens.
 
 // The units of the warps' windows: every unit belongs to the window that holds its first
 // token. fn(t, n, slot, page): tokens [t, t + n) lie in slots [slot, slot + n) of `page`

@@ -23,7 +23,7 @@
 //       fragment when the block's tokens are ordered 4t, 4t + 1 | 4t + 2, 4t + 3 along k. K's fragment
 //       rows take the same order, so P^T only needs its 8 x 8 blocks transposed (movmatrix).
 // Everything is exact as in fp4_tc.cu: widened values in f16, Q in f16 with a power of two per row,
-// P = 2^(s - m + 4) rounded to f16, fp32 sums. A warp's reference m moves when one of its scores
+// P = 2^(s - m + 4) rounded to f16 and a split piece's O (2^-11 each, the output's rounding is 2^-8), fp32 sums. A warp's reference m moves when one of its scores
 // exceeds it by more than 2^4.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -410,13 +410,6 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
     }
     if (I.nsplit > 1) {
       __threadfence();
-      RowBlock rb;
-      rb.seq = I.seq;
-      rb.kvh = I.kvh;
-      rb.row0 = 0;
-      rb.nrows = I.nrows;
-      rb.nsplit = I.nsplit;
-      rb.slot_base = I.slot_base;
       __syncthreads();
       if (threadIdx.x == 0) {
         fence_acq_rel_gpu();

@@ -22,7 +22,8 @@
 // Q is staged in f16 with a power of two per row (its largest value to [2^14, 2^15)): a bf16
 // value has 8 significant bits, so everything within 2^-28 of the row's largest is exact, and
 // the power goes into the row's score scale. P = 2^(s - m + 4) is rounded to f16 (2^-11), the
-// row sums take it before that rounding. The softmax, its lazy rescale, the split-KV pieces and
+// row sums take it before that rounding: half the bytes and the rate of the f16 product, below the
+// output's own rounding of 2^-8 (so is a split piece's f16 partial). The softmax, its lazy rescale, the split-KV pieces and
 // their merge follow the FP8 verify kernel (verify_tc.cu): keys on lanes, rows on columns.
 //
 // Warp roles: warp 0 S issuer (+ TMEM owner), warp 1 P.V issuer, warp 2 K copies, warp 3 V
@@ -34,10 +35,10 @@
 // What bounds it. A 128-key tile takes about 10.2k warp instructions at 48-64 rows: ~3.2k widen, ~1.9k
 // softmax, the rest hands tiles from role to role; issue slots are 63 % busy, the ALU pipe (conversions at
 // half rate) 44 %, tensor cores 25 %, HBM 31 %. With either half of the work taken out (timing only): neither
-// widening nor softmax 248 us, no widening 275, no softmax 337, all of it 431 then, 424 now (256 sequences of
+// widening nor softmax 248 us, no widening 275, no softmax 337, all of it 431 then, 428 now (256 sequences of
 // 8192 keys, 2-4 tokens, 32/2 heads: 1233 MB, 182 us at the HBM rate). 64 sequences of 1k-32k keys,
-// 4 tokens, 16/1 heads: 127 us (46). With 128 rows widening and the products alternate in the shared
-// columns, and a tile takes ~4700 cycles where the products alone take 2230: 2131 us, 903 TFLOP/s.
+// 4 tokens, 16/1 heads: 128 us (46). With 128 rows widening and the products alternate in the shared
+// columns, and a tile takes ~4700 cycles where the products alone take 2230: 2125 us, 905 TFLOP/s.
 // A small call is a chain of cold steps. One CTA of a 128-row block, in cycles: set-up 1.7k, the item and its
 // rows of Q 9k, the first S 2.4k, its softmax 10k (first references: 2.7k for each 16 rows; code
 // fetched for the first time), each further tile 5k, epilogue 5.5k, the partial's store and count 6k, a merge of two
@@ -288,7 +289,6 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     uint64_t l[kCols / 2];  // row sums over this thread's keys, fp32, two rows each
 #pragma unroll
     for (int n = 0; n < kCols / 2; ++n) l[n] = 0;
-    bool bad = false;
     // Failure-path test: every softmax thread's bounded wait on a barrier nothing arrives on
     // runs out; they skip the items, no Q is published, and every other role gives up and
     // drains what it has in flight.
@@ -303,7 +303,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         // before lse_stage is written
         uint32_t* where = reinterpret_cast<uint32_t*>(ms.lse_stage);
         const int t0 = I.row0 / p.G;
-        if (ii >= 1 && !mbar_wait_polls(bar(ms.q_free), (ii - 1) & 1, abort_flag, ptr.err)) bad = true;
+        if (ii >= 1) mbar_wait_polls(bar(ms.q_free), (ii - 1) & 1, abort_flag, ptr.err);
         if (gi < kN) {
           const int n = gi;
           const bool real = n < I.nrows;
@@ -392,7 +392,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         }
         named_barrier(group_bar, 128);
         if (have_o) {
-          if (!mbar_wait_polls(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, ptr.err)) bad = true;
+          mbar_wait_polls(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, ptr.err);
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
@@ -461,7 +461,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
       auto epilogue = [&](int it) {
         const int ii = it - item_begin, pi = ii & 1;
         const Item I = load_item<kN, kFused>(p, cp, ptr, ms, it);
-        if (!mbar_wait_polls(bar(ms.o_ready), ii & 1, abort_flag, ptr.err)) bad = true;
+        mbar_wait_polls(bar(ms.o_ready), ii & 1, abort_flag, ptr.err);
         __syncwarp();
         tc_fence_after();
         // row sums over the 128 key lanes: warp reduce-scatter, then across the quarters
@@ -576,7 +576,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
           const uint32_t sb = g % C::kSBufs, pb = g & 1;
           const int key = key0 + ti;
           const bool need_mask = (key0 + kTileKeys > kv_hi) || (key0 + kTileKeys - 1 > min_lim);
-          if (!mbar_wait_polls(bar(ms.s_full[sb]), (g / C::kSBufs) & 1, abort_flag, ptr.err)) bad = true;
+          mbar_wait_polls(bar(ms.s_full[sb]), (g / C::kSBufs) & 1, abort_flag, ptr.err);
           __syncwarp();  // the TMEM loads are warp-wide
           tc_fence_after();
 #pragma unroll
@@ -639,7 +639,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
             }
             // P buffer g & 1 is free once P.V(g-2) has completed (the barrier's next phase needs a
             // P these threads have not written yet, so a late parity wait cannot miss it)
-            if (cb == 0 && g >= 2 && !mbar_wait_polls(bar(ms.pv_done[pb]), ((g >> 1) - 1) & 1, abort_flag, ptr.err)) bad = true;
+            if (cb == 0 && g >= 2) mbar_wait_polls(bar(ms.pv_done[pb]), ((g >> 1) - 1) & 1, abort_flag, ptr.err);
             if (active) {
               // P^T row of key ti (128-byte swizzle): 16 of this thread's rows
               const uint32_t row = sbase + C::kOffP + pb * C::kPBuf + (c0 >> 6) * C::kPBlock + ti * 128;
@@ -663,7 +663,6 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         }
       }
     }  // !stalled
-    (void)bad;
   } else if (wg >= kWideWarp0 / 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kWideRegs));
     // ------------------------------------------------------------ widening: packed tiles to TMEM

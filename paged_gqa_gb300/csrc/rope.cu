@@ -20,10 +20,11 @@
 // 8c .. 8c + 7 and rot / 2 + 8c .. of the halves order, 16c .. 16c + 15 of the adjacent one, so
 // a lane holds both values of its 8 pairs and its 8 angles serve every head of a token.
 // A half-warp loads four rows before it works out the angles and stores any (an in-place store keeps the
-// compiler from moving later loads up): 16384 tokens of 26 heads, 256 values, 78 us (5.6 TB/s of
-// reads and writes; 64 us at the measured copy rate); row by row 98, two rows 81, six 77 but more
-// registers. 16 warps an SM, 4 KB in flight each: with 24 warps the registers spill (92 us). A decoding
-// step's 256 tokens of 17 heads take 8 us on the GPU, less than the call's host time.
+// compiler from moving later loads up): 16384 tokens of 26 heads, 256 values, 76 us (5.75 TB/s of
+// reads and writes; 64 us at the measured copy rate); when that was 78, row by row 98, two rows 81, six 77
+// but more registers. 16 warps an SM, 4 KB in flight each: with 24 warps the registers spill (92 us). A decoding
+// step's 256 tokens of 17 heads take 7.1 us from a graph, one token 5.7 (an empty kernel 1.1): a chain of
+// frequencies, positions, rows and eight sines and cosines per lane, in code fetched for the first time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
