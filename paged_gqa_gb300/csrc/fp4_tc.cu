@@ -32,9 +32,9 @@
 // 20-27 widen both in turn, since the shared columns hold one at a time (2228 us for a 8192-token
 // chunk on 32768 keys with the two groups of warps there, 2175 so).
 //
-// What bounds it. A 128-key tile takes about 10.2k warp instructions at 48-64 rows: ~3.2k widen, ~1.9k
-// softmax, the rest hands tiles from role to role; issue slots are 63 % busy, the ALU pipe (conversions at
-// half rate) 44 %, tensor cores 25 %, HBM 31 %. With either half of the work taken out (timing only): neither
+// What bounds it. A 128-key tile takes about 10.4k warp instructions at 48-64 rows: ~3.2k widen, ~2.0k
+// softmax, the rest hands tiles from role to role; issue slots are 65 % busy, the ALU pipe (conversions at
+// half rate) 46 %, tensor cores 25 %, HBM 31 %. With either half of the work taken out (timing only): neither
 // widening nor softmax 248 us, no widening 275, no softmax 337, all of it 431 then, 428 now (256 sequences of
 // 8192 keys, 2-4 tokens, 32/2 heads: 1233 MB, 182 us at the HBM rate). 64 sequences of 1k-32k keys,
 // 4 tokens, 16/1 heads: 128 us (46). With 128 rows widening and the products alternate in the shared
