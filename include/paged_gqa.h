@@ -292,8 +292,9 @@ int paged_gqa_cache_read_fp4(const pg_tensor* k_cache, const pg_tensor* v_cache,
  * products exactly (code * scale has 6 significant bits), Q exactly within 2^-28 of its row's largest
  * value. Scores, the softmax's references and sums and the sums of P.V are held in fp32; two things
  * are rounded to f16 (2^-11) on the way: P before P.V, and the normalised output of a sequence's piece
- * where it is split over SMs. out and q must not overlap (refused). A NaN in V (a NaN scale) reaches the new tokens that see
- * its key, and may reach the others of that sequence that share a block of rows with one.
+ * where it is split over SMs. out and q must not overlap (refused). A NaN in V (a NaN scale) reaches
+ * the new tokens that see its key, and may reach the others of that sequence that share a block of
+ * rows with one.
  * A new call and an older one on another stream are ordered by the library (they
  * share its workspace), so such calls do not overlap; in a stream capture the call returns
  * PG_ERR_WORKSPACE: use paged_gqa_attn_fp4_ex there, with a workspace of

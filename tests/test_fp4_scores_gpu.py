@@ -87,3 +87,13 @@ def test_equal_keys_share_a_row_evenly_however_large_their_score(name, seqs, hq,
     c.k[:] = c.k[int(c.table[0, 0]), 0, 3].clone()
     c.q = (c.q.float() * 2.0 ** bits).bfloat16()
     fu.check(c, _run(c, path, bit), name)
+
+
+@pytest.mark.parametrize("scale,kd", [(0.0, 0.01), (-1.0 / 16, 0.01), (0.4, 0.01), (1.0 / 16, -0.02), (2.0 ** -40, 2.0 ** 30), (1e-30, 0.01)])
+@pytest.mark.parametrize("i", range(len(KERNELS)), ids=[k[0] for k in KERNELS])
+def test_other_scales(i, scale, kd):
+    """A scale of zero (the mean of the V seen), negative ones, scales far from one."""
+    name, seqs, hq, path, bit = KERNELS[i]
+    c = fu.make(seqs, hq, 1, 16, seed=350 + i)
+    c.scale, c.kd = scale, kd
+    fu.check(c, _run(c, path, bit), name)
