@@ -58,7 +58,7 @@ typedef struct CUstream_st* pg_stream_t;
 
 typedef enum {
   PG_BF16 = 1,
-  PG_F16 = 2,   /* accepted by no entry point today; reserved */
+  PG_F16 = 2,   /* paged_gqa_attn_prompt only */
   PG_E4M3 = 3,  /* OCP FP8 e4m3fn (max 448, no inf, 0x7F/0xFF are NaN) */
   PG_I32 = 4,
   PG_F32 = 5,
@@ -336,6 +336,141 @@ int paged_gqa_attn_fp4_ex(const pg_tensor* q, const pg_tensor* k_cache, const pg
 int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* positions, const pg_tensor* inv_freq,
                    const int32_t* sections, int interleaved, int adjacent, pg_tensor* q_out, pg_tensor* k_out,
                    pg_stream_t stream);
+
+/*
+ * paged_gqa_build_tables -- what every call above is given, made on the GPU from the requests'
+ * lengths: the batch's block table, seq_lens and query_start_loc, and each new token's slot.
+ *
+ * The pages of all requests lie in a pool: row r of `pages` lists those of one request in order,
+ * page_counts[r] of them; `free_pages` is a stack of the others, num_free[0] high. A step names a
+ * row for each of its S requests:
+ *
+ *   q_lens     [S]       int32  new tokens; -1: the request has ended and gives its pages back
+ *   ctx_lens   [S]       int32  tokens it has in the cache already (not read where it has ended)
+ *   rows       [S]       int32  its row of the pool; -1: no request (padding: then q_lens is <= 0)
+ *   page_size            16, 32, 64 or 128 (P)
+ *   pages      [R, Wp]   int32  in place: entries [page_counts[r], ..) of a row are filled as needed
+ *   page_counts [R]      int32  read; page_counts_out [R] gets the new counts (may be the same tensor)
+ *   free_pages [F]       int32  in place: pages given back are put on top
+ *   num_free   [1]       int32  read; num_free_out [1] gets the new height (may be the same tensor)
+ *   block_table [S, W]   int32  the first ceil(seq_lens[s] / P) pages of each request, then -1
+ *   seq_lens   [S]       int32  ctx_lens + q_lens, 0 for ended requests and padding
+ *   query_start_loc [S + 1]     prefix sums of the new tokens (none of ended requests and padding)
+ *   slot_map   [T]       int32  page * P + slot of each new token; -1 behind the last one
+ *
+ * First the ended requests put their pages on the stack, in the batch's order; then, in that order
+ * too, each of the others takes the pages it is missing from the top, page by page. Pages beyond
+ * what it needs stay with a request (tokens that were rejected leave such). The answer does not
+ * depend on the order of execution. A request that cannot be served gets seq_lens 0, a table row of
+ * -1 and slots of -1, keeps its pages and its place among the tokens, and sets
+ * PG_ERR_DEVICE_BOUNDS: a row outside [-1, R), a row that an earlier request of the batch names, a
+ * count outside [0, Wp], q_lens below -1, ctx_lens below 0, more pages than W or Wp, not enough
+ * free pages (then the requests behind it get none either). So does a q_lens > 0 without a row, a
+ * num_free outside [0, F] (taken as the nearer end), a stack that would pass F (that request keeps its
+ * pages) and more new tokens than T (those from T on have no slot). A taken page id that is negative
+ * or whose slots pass 2^31 - 1 has slots of -1 and sets it too. Apart from the two named pairs no
+ * written tensor may share memory with another (refused). Allocates nothing; two launches.
+ * (The pages describe no allocator.)
+ */
+int paged_gqa_build_tables(const pg_tensor* q_lens, const pg_tensor* ctx_lens, const pg_tensor* rows, int page_size,
+                           const pg_tensor* pages, const pg_tensor* page_counts, const pg_tensor* free_pages,
+                           const pg_tensor* num_free, pg_tensor* block_table, pg_tensor* seq_lens,
+                           pg_tensor* query_start_loc, pg_tensor* slot_map, pg_tensor* page_counts_out,
+                           pg_tensor* num_free_out, pg_stream_t stream);
+
+/*
+ * Token trees: paged_gqa_tree_masks, paged_gqa_attn_tree, paged_gqa_cache_keep.
+ *
+ * A drafted tree's tokens are the new tokens of their sequence, parents before children. They are
+ * written to the cache like any others (token t of a sequence at position seq_lens - q_len + t),
+ * attend the context and their own ancestors, and once some path has been accepted its K and V
+ * move to the positions behind the context. A token's mask is a row of `words` 32-bit words
+ * (1 to 32 of them): bit i % 32 of word i / 32 is set where it sees new token i of its sequence.
+ * (The pages verify chains of drafted tokens only.)
+ */
+
+/*
+ * paged_gqa_tree_masks -- masks and positions from the trees' parents.
+ *
+ *   parents    [T]       int32  each new token's parent, as its number among the sequence's new
+ *                               tokens; -1: it hangs on the context
+ *   seq_lens, query_start_loc   as in paged_gqa_attn
+ *   masks      [T, words]       int32, the token itself and its ancestors
+ *   positions  [A, T]           int32, 1 <= A <= 4: seq_lens - q_len + its depth, the same on each
+ *                               axis (what paged_gqa_rope takes)
+ *
+ * A parent that is not before its child is flagged (PG_ERR_DEVICE_BOUNDS) and taken as -1. A sequence
+ * with bad bounds (as in paged_gqa_attn) or more than 32 * words new tokens is flagged, its masks and
+ * positions are 0. Rows behind query_start_loc[num_seqs] are left as they were. Allocates nothing.
+ */
+int paged_gqa_tree_masks(const pg_tensor* parents, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                         pg_tensor* masks, pg_tensor* positions, pg_stream_t stream);
+
+/*
+ * paged_gqa_attn_tree -- paged_gqa_attn where new token t of a sequence attends the context (keys
+ * 0 .. L - q_len - 1) and those of the new tokens 0 .. t whose bit of its mask is set, itself
+ * among them (bits from t + 1 on are not used; any masks do, a tree's or not). A row that sees no
+ * key is zeros. masks is int32 [T, words], rows any distance apart; a sequence of more than 32 * words
+ * new tokens is flagged like other bad bounds, its rows are zeros. q is bf16, the caches bf16 or
+ * e4m3; everything else is as in paged_gqa_attn, out and q must not overlap (refused). A NaN or
+ * infinity in V of a key reaches the tokens that see it, and may reach others of its sequence
+ * that share a block of rows with one. Slots behind seq_lens and other pages do not matter. With bf16
+ * caches |V| must not pass 65504 (the pieces of a split sequence are held in f16, as in paged_gqa_attn).
+ *
+ * Calls are ordered by the library as those of paged_gqa_attn_fp4 (one workspace); in a stream
+ * capture use paged_gqa_attn_tree_ex, under the terms of paged_gqa_attn_fp4_ex and with a workspace of
+ * paged_gqa_workspace_size(...) bytes.
+ */
+int paged_gqa_attn_tree(const pg_tensor* q, const pg_tensor* k_cache, const pg_tensor* v_cache,
+                        const pg_tensor* block_table, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                        const pg_tensor* masks, float k_descale, float v_descale, float softmax_scale, pg_tensor* out,
+                        pg_stream_t stream);
+int paged_gqa_attn_tree_ex(const pg_tensor* q, const pg_tensor* k_cache, const pg_tensor* v_cache,
+                           const pg_tensor* block_table, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                           const pg_tensor* masks, float k_descale, float v_descale, float softmax_scale,
+                           pg_tensor* out, void* workspace, size_t workspace_bytes, pg_stream_t stream);
+
+/*
+ * paged_gqa_cache_keep -- after verification: the accepted new tokens' K and V move to the positions
+ * right behind the context, in place, and the sequences get their new lengths.
+ *
+ *   k_cache, v_cache  [NB, P, Hkv, 256]  e4m3 or bf16, as in paged_gqa_cache_write
+ *   block_table, seq_lens, query_start_loc  as in paged_gqa_attn
+ *   kept       [S, D]    int32  the accepted tokens' numbers among the sequence's new ones, increasing
+ *   num_kept   [S]       int32  how many of them count, 0 .. min(D, q_len)
+ *   seq_lens_out [S]     int32  seq_lens - q_len + num_kept; shares memory with no other argument
+ *
+ * Token kept[s, k] moves from position seq_lens - q_len + kept[s, k] to seq_lens - q_len + k; the
+ * rest of the caches is left as it was. Sequences must not share the pages of their new tokens.
+ * A sequence whose kept tokens do not increase, or lie outside its new ones, is flagged
+ * (PG_ERR_DEVICE_BOUNDS): nothing of it moves and nothing is kept. One with bad bounds is flagged and
+ * keeps its length; a page id out of range is flagged and that token does not move. Allocates nothing.
+ */
+int paged_gqa_cache_keep(const pg_tensor* k_cache, const pg_tensor* v_cache, const pg_tensor* block_table,
+                         const pg_tensor* seq_lens, const pg_tensor* query_start_loc, const pg_tensor* kept,
+                         const pg_tensor* num_kept, pg_tensor* seq_lens_out, pg_stream_t stream);
+
+/*
+ * paged_gqa_attn_prompt -- causal attention over whole prompts packed behind one another, before there
+ * is a cache: token t of a prompt attends its tokens 0 .. t.
+ *
+ *   q          [T, Hq, 256]    bf16 or f16; at most 128 q heads per kv head
+ *   k, v       [T, Hkv, 256]   of q's type; rows of all three 16-byte aligned, any such strides
+ *                              (slices of one projection's output do)
+ *   query_start_loc [S + 1]    int32, [0] == 0, non-decreasing, at most T; prompts may be empty
+ *   softmax_scale              multiplies q . k
+ *   out        [T, Hq, 256]    of q's type, rows disjoint; overlaps no input (refused)
+ *   lse        [T, Hq]         float32 or NULL: natural logarithm of each row's sum of exp(scores), which
+ *                              merges this attention with one over other keys
+ *
+ * Scores, the softmax's statistics and the sums of P.V are held in fp32; P is rounded to the inputs'
+ * type before P.V. Rows behind query_start_loc[S] are left as they were. A sequence that does not lie in
+ * [0, T) is flagged (PG_ERR_DEVICE_BOUNDS) and its rows are left as they were. A NaN or infinity in V
+ * reaches the tokens that see it, and may reach earlier ones of its prompt that share a block of rows
+ * with one; no other prompt.
+ */
+int paged_gqa_attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* query_start_loc,
+                          float softmax_scale, pg_tensor* out, pg_tensor* lse, pg_stream_t stream);
 
 /*
  * Workspace bytes for a call with these host-known sizes on `device`

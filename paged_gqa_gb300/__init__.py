@@ -22,6 +22,12 @@ from ._binding import (  # noqa: F401
     paged_gqa_attn_fp4,
     paged_gqa_attn_fp4_ex,
     paged_gqa_rope,
+    paged_gqa_build_tables,
+    paged_gqa_tree_masks,
+    paged_gqa_attn_tree,
+    paged_gqa_attn_tree_ex,
+    paged_gqa_cache_keep,
+    paged_gqa_attn_prompt,
     paged_gqa_check_device_errors,
     paged_gqa_last_error,
     paged_gqa_last_plan,

@@ -20,6 +20,8 @@ EXPORTED = ("paged_gqa_attn", "paged_gqa_attn_ex", "paged_gqa_attn_noalloc", "pa
             "paged_gqa_sparse_attn", "paged_gqa_cache_write",
             "paged_gqa_cache_write_fp4", "paged_gqa_cache_read_fp4", "paged_gqa_attn_fp4", "paged_gqa_attn_fp4_ex",
             "paged_gqa_rope",
+            "paged_gqa_build_tables", "paged_gqa_tree_masks", "paged_gqa_attn_tree", "paged_gqa_attn_tree_ex",
+            "paged_gqa_cache_keep", "paged_gqa_attn_prompt",
             "paged_gqa_workspace_size",
             "paged_gqa_last_error",
             "paged_gqa_check_device_errors", "paged_gqa_set_path", "paged_gqa_set_stall_test", "paged_gqa_last_plan",
@@ -52,9 +54,9 @@ _tls = threading.local()
 def _desc_buf():
     b = getattr(_tls, "buf", None)
     if b is None:
-        arr = (PgTensor * 10)()
+        arr = (PgTensor * 13)()
         base = ctypes.addressof(arr)
-        b = _tls.buf = (arr, [base + 80 * i for i in range(10)], memoryview(arr).cast("B"))
+        b = _tls.buf = (arr, [base + 80 * i for i in range(13)], memoryview(arr).cast("B"))
     return b
 
 
@@ -91,7 +93,14 @@ def load(build_if_missing: bool = True):
             lib.paged_gqa_attn_fp4.argtypes = [P, P, P, P, P, P, f, f, f, P, c_vp]
             lib.paged_gqa_attn_fp4_ex.argtypes = [P, P, P, P, P, P, f, f, f, P, c_vp, ctypes.c_size_t, c_vp]
             lib.paged_gqa_rope.argtypes = [P, P, P, P, ctypes.POINTER(ctypes.c_int32), ctypes.c_int, ctypes.c_int, P, P, c_vp]
-            for name in ("cache_write_fp4", "cache_read_fp4", "attn_fp4", "attn_fp4_ex", "rope"):
+            lib.paged_gqa_build_tables.argtypes = [P, P, P, ctypes.c_int] + [P] * 10 + [c_vp]
+            lib.paged_gqa_tree_masks.argtypes = [P, P, P, P, P, c_vp]
+            lib.paged_gqa_attn_tree.argtypes = [P, P, P, P, P, P, P, f, f, f, P, c_vp]
+            lib.paged_gqa_attn_tree_ex.argtypes = [P, P, P, P, P, P, P, f, f, f, P, c_vp, ctypes.c_size_t, c_vp]
+            lib.paged_gqa_cache_keep.argtypes = [P, P, P, P, P, P, P, P, c_vp]
+            lib.paged_gqa_attn_prompt.argtypes = [P, P, P, P, f, P, P, c_vp]
+            for name in ("cache_write_fp4", "cache_read_fp4", "attn_fp4", "attn_fp4_ex", "rope", "build_tables", "tree_masks",
+                         "attn_tree", "attn_tree_ex", "cache_keep", "attn_prompt"):
                 getattr(lib, "paged_gqa_" + name).restype = ctypes.c_int
             lib.paged_gqa_workspace_size.argtypes = [ctypes.c_int] * 7
             lib.paged_gqa_workspace_size.restype = ctypes.c_size_t
@@ -230,6 +239,16 @@ def _on_device(*tensors) -> None:
             raise ValueError(f"every tensor must be on the current CUDA device (cuda:{cur}), got one on {t.device}")
 
 
+def _workspace(workspace):
+    """(address, bytes) of a workspace tensor."""
+    if workspace is None:
+        return None, 0
+    _on_device(workspace)
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return workspace.data_ptr() or None, workspace.numel() * workspace.element_size()
+
+
 def _pack_fp4(first_cache: int, *tensors):
     """_pack with tensors[first_cache] and the next one as 4-bit caches (uint8 rows of 144 bytes)."""
     for t in tensors[first_cache:first_cache + 2]:
@@ -272,14 +291,8 @@ def paged_gqa_attn_fp4_ex(q, k_cache, v_cache, block_table, seq_lens, query_star
     lib = load()
     _on_device(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, out)
     d = _pack_fp4(1, q, k_cache, v_cache, block_table, seq_lens, query_start_loc, out)
-    ptr = nbytes = 0
-    if workspace is not None:
-        _on_device(workspace)
-        if not workspace.is_contiguous():
-            raise ValueError("the workspace must be contiguous")
-        ptr, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(lib.paged_gqa_attn_fp4_ex(*d[:6], float(k_descale), float(v_descale), float(softmax_scale), d[6],
-                                     ptr or None, nbytes, _stream(stream)))
+                                     *_workspace(workspace), _stream(stream)))
 
 
 def paged_gqa_rope(q, k, positions, inv_freq, sections, q_out=None, k_out=None, interleaved: bool = False,
@@ -296,6 +309,67 @@ def paged_gqa_rope(q, k, positions, inv_freq, sections, q_out=None, k_out=None, 
     d = _pack(q, k, positions, inv_freq, q_out, k_out)
     _check(lib.paged_gqa_rope(*d[:4], (ctypes.c_int32 * len(sections))(*sections), int(interleaved), int(adjacent),
                               d[4], d[5], _stream(stream)))
+
+
+def paged_gqa_build_tables(q_lens, ctx_lens, rows, page_size: int, pages, page_counts, free_pages, num_free, block_table,
+                           seq_lens, query_start_loc, slot_map, page_counts_out=None, num_free_out=None,
+                           stream=None) -> None:
+    """Block table, seq_lens, query_start_loc and slots of a step, from its requests' lengths (int32 tensors).
+
+    page_counts and num_free are updated in place where no output is given."""
+    lib = load()
+    t = (q_lens, ctx_lens, rows, pages, page_counts, free_pages, num_free, block_table, seq_lens, query_start_loc, slot_map,
+         page_counts if page_counts_out is None else page_counts_out, num_free if num_free_out is None else num_free_out)
+    _on_device(*t)
+    d = _pack(*t)
+    _check(lib.paged_gqa_build_tables(*d[:3], int(page_size), *d[3:], _stream(stream)))
+
+
+def paged_gqa_tree_masks(parents, seq_lens, query_start_loc, masks, positions, stream=None) -> None:
+    """Ancestor masks (int32 [T, words]) and positions (int32 [A, T]) of token trees from their parents."""
+    lib = load()
+    _on_device(parents, seq_lens, query_start_loc, masks, positions)
+    d = _pack(parents, seq_lens, query_start_loc, masks, positions)
+    _check(lib.paged_gqa_tree_masks(*d, _stream(stream)))
+
+
+def paged_gqa_attn_tree(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks, k_descale: float,
+                        v_descale: float, softmax_scale: float, out, stream=None) -> None:
+    """paged_gqa_attn where the new tokens see each other by masks (int32 [T, words]); q is bf16."""
+    lib = load()
+    _on_device(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks, out)
+    d = _pack(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks, out)
+    _check(lib.paged_gqa_attn_tree(*d[:7], float(k_descale), float(v_descale), float(softmax_scale), d[7],
+                                   _stream(stream)))
+
+
+def paged_gqa_attn_tree_ex(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks, k_descale: float,
+                           v_descale: float, softmax_scale: float, out, workspace, stream=None) -> None:
+    """paged_gqa_attn_tree with a caller-owned workspace tensor (for stream capture)."""
+    lib = load()
+    _on_device(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks, out)
+    d = _pack(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks, out)
+    _check(lib.paged_gqa_attn_tree_ex(*d[:7], float(k_descale), float(v_descale), float(softmax_scale), d[7],
+                                      *_workspace(workspace), _stream(stream)))
+
+
+def paged_gqa_cache_keep(k_cache, v_cache, block_table, seq_lens, query_start_loc, kept, num_kept, seq_lens_out,
+                         stream=None) -> None:
+    """Move the accepted new tokens' K and V (kept: int32 [S, D], num_kept of them) right behind the context."""
+    lib = load()
+    _on_device(k_cache, v_cache, block_table, seq_lens, query_start_loc, kept, num_kept, seq_lens_out)
+    d = _pack(k_cache, v_cache, block_table, seq_lens, query_start_loc, kept, num_kept, seq_lens_out)
+    _check(lib.paged_gqa_cache_keep(*d, _stream(stream)))
+
+
+def paged_gqa_attn_prompt(q, k, v, query_start_loc, softmax_scale: float, out, lse=None, stream=None) -> None:
+    """Causal attention over whole packed prompts: q [T, Hq, 256], k and v [T, Hkv, 256] in bf16 or f16."""
+    lib = load()
+    t = (q, k, v, query_start_loc, out) + (() if lse is None else (lse,))
+    _on_device(*t)
+    d = _pack(*t)
+    _check(lib.paged_gqa_attn_prompt(*d[:4], float(softmax_scale), d[4], d[5] if lse is not None else None,
+                                     _stream(stream)))
 
 
 def paged_gqa_workspace_size(num_seqs: int, total_q: int, num_q_heads: int, num_kv_heads: int,

@@ -20,6 +20,8 @@
 #include "../../include/paged_gqa.h"
 #include "common.cuh"
 #include "plan.cuh"
+#include "prompt.cuh"
+#include "step.cuh"
 #include "tc_kernels.cuh"
 
 namespace pgqa {
@@ -95,7 +97,7 @@ struct DeviceState {
   uint32_t* err = nullptr;   // address of g_error_word on this device
   void* ws = nullptr;        // library-owned workspace
   size_t ws_bytes = 0;
-  // The 4-bit attention's own one; a call on another stream than the last waits for its event.
+  // The one of the 4-bit and the tree attention; a call waits for the last one's event.
   void* ws4 = nullptr;
   size_t ws4_bytes = 0;
   cudaEvent_t ws4_done = nullptr;
@@ -288,6 +290,8 @@ int validate(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
   p.kv_is_fp8 = k->dtype == PG_E4M3;
   p.kv_is_fp4 = 0;
   p.zero2 = 0;
+  p.mask_words = 0;
+  p.mask_st = 0;
   p.q_cast = q_cast ? 1 : 0;
   p.q_amax_parts = 0;
   p.q_st = q->stride[0];
@@ -314,6 +318,7 @@ int validate(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
   ptr.out = out->data;
   ptr.err = nullptr;
   ptr.q_amax = nullptr;
+  ptr.masks = nullptr;
   return PG_OK;
 }
 
@@ -514,11 +519,11 @@ int check_tables(const pg_tensor* bt, const pg_tensor* sl, const pg_tensor* qsl,
   return PG_OK;
 }
 
-// bf16 [T, H, 256] rows with 16-byte aligned (token, head) rows.
-int check_rows(const pg_tensor* t, const char* name, bool written) {
+// bf16 (or f16) [T, H, 256] rows with 16-byte aligned (token, head) rows.
+int check_rows(const pg_tensor* t, const char* name, bool written, int dtype = PG_BF16) {
   int st;
   if ((st = check_tensor(t, name, 3))) return st;
-  if (t->dtype != PG_BF16) return fail(PG_ERR_UNSUPPORTED, "%s must be bf16", name);
+  if (t->dtype != dtype) return fail(PG_ERR_UNSUPPORTED, "%s must be %s", name, dtype == PG_F16 ? "f16" : "bf16");
   if (t->shape[2] != kHeadDim) return fail(PG_ERR_UNSUPPORTED, "%s: head_dim must be 256", name);
   if (t->shape[0] > INT32_MAX / 2 || t->shape[1] > 65535)
     return fail(PG_ERR_UNSUPPORTED, "sizes beyond the supported range");
@@ -651,6 +656,110 @@ int fp4_cache_call(bool write, const pg_tensor* kx, const pg_tensor* vx, const p
   return PG_OK;
 }
 
+// An int32 tensor of one or two dims whose last dim is contiguous; its rows are disjoint if written.
+int check_ints(const pg_tensor* t, const char* name, int ndim, bool written) {
+  int st;
+  if ((st = check_tensor(t, name, ndim))) return st;
+  if (t->dtype != PG_I32) return fail(PG_ERR_INVALID_ARG, "%s must be int32", name);
+  long long n = 1;
+  for (int i = 0; i < ndim; ++i) {
+    if (t->shape[i] > INT32_MAX / 2) return fail(PG_ERR_UNSUPPORTED, "%s: sizes beyond the supported range", name);
+    n *= t->shape[i];
+  }
+  if (t->shape[ndim - 1] > 1 && t->stride[ndim - 1] != 1) return fail(PG_ERR_INVALID_ARG, "%s: the last axis must be contiguous", name);
+  if (n > 0 && !t->data) return fail(PG_ERR_INVALID_ARG, "%s: null data pointer", name);
+  if (reinterpret_cast<uintptr_t>(t->data) & 3u) return fail(PG_ERR_INVALID_ARG, "%s must be 4-byte aligned", name);
+  if (written && ndim == 2 && n > 0 && !rows_disjoint(t, 1, t->shape[1])) return fail(PG_ERR_INVALID_ARG, "%s strides make rows overlap", name);
+  return PG_OK;
+}
+
+// Do the addresses, first to last, of two tensors of 4-byte values meet?
+bool ints_meet(const pg_tensor* a, const pg_tensor* b) {
+  const pg_tensor* t[2] = {a, b};
+  long long lo[2], hi[2];
+  for (int i = 0; i < 2; ++i) {
+    lo[i] = hi[i] = (long long)reinterpret_cast<intptr_t>(t[i]->data);
+    hi[i] += 4;
+    for (int d = 0; d < t[i]->ndim; ++d) {
+      if (t[i]->shape[d] == 0) return false;
+      const long long last = t[i]->shape[d] > 1 ? 4 * (t[i]->shape[d] - 1) * t[i]->stride[d] : 0;
+      (last < 0 ? lo[i] : hi[i]) += last;
+    }
+  }
+  return lo[0] < hi[1] && lo[1] < hi[0];
+}
+
+struct Named {
+  const pg_tensor* t;
+  const char* name;
+};
+// No written tensor of the list (its first `written` ones) shares memory with another of it.
+template <int N>
+int check_apart(const Named (&t)[N], int written) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < N; ++j)
+      if (ints_meet(t[i].t, t[j].t)) return fail(PG_ERR_INVALID_ARG, "%s overlaps %s", t[i].name, t[j].name);
+  return PG_OK;
+}
+
+bool bad_page_size(long long P) { return P != 16 && P != 32 && P != 64 && P != 128; }
+
+// Runs a call on its workspace of `bytes` bytes: the caller's, or the library's, which calls that do not
+// overlap share. `ex`: the entry point for captures. run(workspace, captured) issues the launches.
+template <typename Run>
+int with_workspace(DeviceState* ds, size_t bytes, void* user_ws, size_t user_ws_bytes, bool use_user_ws, const char* ex,
+                   cudaStream_t stream, Run run) {
+  int st;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  if (use_user_ws) {
+    if (!user_ws || (reinterpret_cast<uintptr_t>(user_ws) & 255u))
+      return fail(PG_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
+    if (user_ws_bytes < bytes)
+      return fail(PG_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", user_ws_bytes, bytes);
+    st = run(user_ws, cap != cudaStreamCaptureStatusNone);
+  } else {
+    // A graph would keep the library's workspace, which may grow (and move) or serve another
+    // stream while the graph replays.
+    if (cap != cudaStreamCaptureStatusNone)
+      return fail(PG_ERR_WORKSPACE, "a captured call needs its own workspace: %s", ex);
+    std::lock_guard<std::mutex> lk(ds->mu);
+    if (!ds->ws4_done && (e = cudaEventCreateWithFlags(&ds->ws4_done, cudaEventDisableTiming)) != cudaSuccess)
+      return cuda_fail(e, "cudaEventCreate");
+    if (ds->ws4_bytes < bytes) {
+      if (ds->ws4) {
+        e = cudaDeviceSynchronize();  // work already queued may still use the old buffer
+        if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize before workspace growth");
+        cudaFree(ds->ws4);
+        ds->ws4 = nullptr;
+        ds->ws4_bytes = 0;
+        ds->ws4_used = false;
+      }
+      const size_t want = bytes + bytes / 4;
+      e = cudaMalloc(&ds->ws4, want);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
+      ds->ws4_bytes = want;
+      // the counters are tagged per call and need no clearing; defined contents all the same
+      e = cudaMemsetAsync(ds->ws4, 0, want, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace)");
+    }
+    // One workspace, any streams: a call waits for the last one, whose stream may be another (also
+    // under the same handle, which a destroyed stream or another thread's default one can have had).
+    if (ds->ws4_used) {
+      e = cudaStreamWaitEvent(stream, ds->ws4_done, 0);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
+    }
+    st = run(ds->ws4, false);
+    // also after a failed launch: what was launched before it may be running
+    e = cudaEventRecord(ds->ws4_done, stream);
+    if (e != cudaSuccess && st == PG_OK) return cuda_fail(e, "cudaEventRecord");
+    ds->ws4_used = true;
+  }
+  if (st == PG_OK) t_last_error.clear();
+  return st;
+}
+
 int run_fp4(const Validated& val, void* ws, const WsLayout& L, DeviceState* ds, bool captured, cudaStream_t stream) {
   Problem p = val.p;
   Pointers ptr = val.ptr;
@@ -777,54 +886,116 @@ int attn_fp4(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const p
   DeviceState* ds = nullptr;
   if ((st = current_device(&ds))) return st;
   const WsLayout L = make_layout(p.num_seqs, p.T, p.Hq, p.Hkv, ds->sms);
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(stream, &cap);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-  if (use_user_ws) {
-    if (!user_ws || (reinterpret_cast<uintptr_t>(user_ws) & 255u))
-      return fail(PG_ERR_WORKSPACE, "workspace must be non-null and 256-byte aligned");
-    if (user_ws_bytes < L.total)
-      return fail(PG_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", user_ws_bytes, L.total);
-    st = run_fp4(val, user_ws, L, ds, cap != cudaStreamCaptureStatusNone, stream);
-  } else {
-    // A graph would keep the library's workspace, which may grow (and move) or serve another
-    // stream while the graph replays.
-    if (cap != cudaStreamCaptureStatusNone)
-      return fail(PG_ERR_WORKSPACE, "a captured call needs its own workspace: paged_gqa_attn_fp4_ex");
-    std::lock_guard<std::mutex> lk(ds->mu);
-    if (!ds->ws4_done && (e = cudaEventCreateWithFlags(&ds->ws4_done, cudaEventDisableTiming)) != cudaSuccess)
-      return cuda_fail(e, "cudaEventCreate");
-    if (ds->ws4_bytes < L.total) {
-      if (ds->ws4) {
-        e = cudaDeviceSynchronize();  // work already queued may still use the old buffer
-        if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize before workspace growth");
-        cudaFree(ds->ws4);
-        ds->ws4 = nullptr;
-        ds->ws4_bytes = 0;
-        ds->ws4_used = false;
-      }
-      const size_t want = L.total + L.total / 4;
-      e = cudaMalloc(&ds->ws4, want);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
-      ds->ws4_bytes = want;
-      // the counters are tagged per call and need no clearing; defined contents all the same
-      e = cudaMemsetAsync(ds->ws4, 0, want, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace)");
-    }
-    // One workspace, any streams: a call waits for the last one, whose stream may be another (also
-    // under the same handle, which a destroyed stream or another thread's default one can have had).
-    if (ds->ws4_used) {
-      e = cudaStreamWaitEvent(stream, ds->ws4_done, 0);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaStreamWaitEvent");
-    }
-    st = run_fp4(val, ds->ws4, L, ds, false, stream);
-    // also after a failed launch: what was launched before it may be running
-    e = cudaEventRecord(ds->ws4_done, stream);
-    if (e != cudaSuccess && st == PG_OK) return cuda_fail(e, "cudaEventRecord");
-    ds->ws4_used = true;
+  return with_workspace(ds, L.total, user_ws, user_ws_bytes, use_user_ws, "paged_gqa_attn_fp4_ex", stream,
+                        [&](void* ws, bool captured) { return run_fp4(val, ws, L, ds, captured, stream); });
+}
+
+// ---------------------------------------------------------------- token trees, prompts --
+
+int attn_tree(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* bt, const pg_tensor* sl,
+              const pg_tensor* qsl, const pg_tensor* masks, float k_descale, float v_descale, float softmax_scale,
+              const pg_tensor* out, void* user_ws, size_t user_ws_bytes, bool use_user_ws, cudaStream_t stream) {
+  Validated val;
+  int st;
+  long long W = 0;
+  if ((st = validate(q, k, v, bt, sl, qsl, 1.f, k_descale, v_descale, softmax_scale, out, false, &val)) ||
+      (st = check_tables(bt, sl, qsl, &W)))
+    return st;
+  if (q->dtype != PG_BF16) return fail(PG_ERR_UNSUPPORTED, "tree attention takes a bf16 q");
+  if ((st = check_ints(masks, "masks", 2, false))) return st;
+  const long long T = q->shape[0], words = masks->shape[1];
+  if (masks->shape[0] != T) return fail(PG_ERR_INVALID_ARG, "masks must be [T, words]");
+  if (words < 1 || words > kMaxMaskWords) return fail(PG_ERR_UNSUPPORTED, "masks must have 1 to %d words", kMaxMaskWords);
+  if (!std::isfinite(val.p.score_scale_log2)) return fail(PG_ERR_INVALID_ARG, "softmax_scale * k_descale must fit fp32");
+  if (val.p.num_seqs == 0 || T == 0) {
+    t_last_error.clear();
+    return PG_OK;
   }
-  if (st == PG_OK) t_last_error.clear();
-  return st;
+  if (k->shape[0] == 0 || W == 0) return fail(PG_ERR_INVALID_ARG, "new tokens without pages");
+  if (rows_overlap(q, out)) return fail(PG_ERR_INVALID_ARG, "out overlaps q");
+  val.p.mask_words = (int)words;
+  val.p.mask_st = T > 1 ? masks->stride[0] : 0;
+  val.ptr.masks = static_cast<const int32_t*>(masks->data);
+  DeviceState* ds = nullptr;
+  if ((st = current_device(&ds))) return st;
+  const WsLayout L = make_layout(val.p.num_seqs, val.p.T, val.p.Hq, val.p.Hkv, ds->sms);
+  return with_workspace(ds, L.total, user_ws, user_ws_bytes, use_user_ws, "paged_gqa_attn_tree_ex", stream,
+                        [&](void* ws, bool) { return run(val, k, v, ws, L.total, L, ds, stream); });
+}
+
+int attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* qsl, float softmax_scale,
+                const pg_tensor* out, const pg_tensor* lse, cudaStream_t stream) {
+  int st;
+  if (!q || (q->dtype != PG_BF16 && q->dtype != PG_F16)) return fail(q ? PG_ERR_UNSUPPORTED : PG_ERR_INVALID_ARG, "q must be bf16 or f16");
+  if ((st = check_rows(q, "q", false, q->dtype)) || (st = check_rows(k, "k", false, q->dtype)) ||
+      (st = check_rows(v, "v", false, q->dtype)) || (st = check_ints(qsl, "query_start_loc", 1, false)) ||
+      (st = check_rows(out, "out", true, q->dtype)))
+    return st;
+  const long long T = q->shape[0], Hq = q->shape[1], Hkv = k->shape[1], S = qsl->shape[0] - 1;
+  if (S < 0) return fail(PG_ERR_INVALID_ARG, "query_start_loc must have an entry more than there are sequences");
+  if (k->shape[0] != T || v->shape[0] != T || v->shape[1] != Hkv) return fail(PG_ERR_INVALID_ARG, "k and v must be [T, num_kv_heads, 256]");
+  if (out->shape[0] != T || out->shape[1] != Hq) return fail(PG_ERR_INVALID_ARG, "out shape must equal q shape");
+  if (Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0)
+    return fail(PG_ERR_INVALID_ARG, "num_q_heads (%lld) must be a positive multiple of num_kv_heads (%lld)", Hq, Hkv);
+  const long long G = Hq / Hkv;
+  if (G > 128) return fail(PG_ERR_UNSUPPORTED, "at most 128 q heads per kv head (got %lld)", G);
+  if (T * G > INT32_MAX / 2) return fail(PG_ERR_UNSUPPORTED, "sizes beyond the supported range");
+  const double score = (double)softmax_scale * 1.4426950408889634;
+  if (!std::isfinite(softmax_scale) || !(std::fabs(score) <= 3.4e38)) return fail(PG_ERR_INVALID_ARG, "softmax_scale must be finite");
+  if (lse) {
+    if ((st = check_tensor(lse, "lse", 2))) return st;
+    if (lse->dtype != PG_F32) return fail(PG_ERR_INVALID_ARG, "lse must be float32");
+    if (lse->shape[0] != T || lse->shape[1] != Hq) return fail(PG_ERR_INVALID_ARG, "lse must be [T, num_q_heads]");
+    if ((T > 0 && !lse->data) || (reinterpret_cast<uintptr_t>(lse->data) & 3u))
+      return fail(PG_ERR_INVALID_ARG, "lse must be non-null and 4-byte aligned");
+    if (!rows_disjoint(lse, 2, 1)) return fail(PG_ERR_INVALID_ARG, "lse strides make entries overlap");
+  }
+  const Named in[3] = {{q, "q"}, {k, "k"}, {v, "v"}};
+  for (const Named& x : in)
+    if (rows_overlap(out, x.t)) return fail(PG_ERR_INVALID_ARG, "out overlaps %s", x.name);
+  if (rows_meet(out, qsl->data, qsl->shape[0] * 4)) return fail(PG_ERR_INVALID_ARG, "out overlaps query_start_loc");
+  if (lse && T > 0) {
+    if (ints_meet(lse, qsl)) return fail(PG_ERR_INVALID_ARG, "lse overlaps query_start_loc");
+    const long long bytes = 4 * ((T - 1) * (T > 1 ? lse->stride[0] : 0) + (Hq - 1) * (Hq > 1 ? lse->stride[1] : 0) + 1);
+    if (rows_meet(out, lse->data, bytes)) return fail(PG_ERR_INVALID_ARG, "lse overlaps out");
+    for (const Named& x : in)
+      if (rows_meet(x.t, lse->data, bytes)) return fail(PG_ERR_INVALID_ARG, "lse overlaps %s", x.name);
+  }
+  if (S == 0 || T == 0) {
+    t_last_error.clear();
+    return PG_OK;
+  }
+  DeviceState* ds = nullptr;
+  if ((st = current_device(&ds))) return st;
+  PromptArgs a;
+  a.q = static_cast<const uint16_t*>(q->data);
+  a.k = static_cast<const uint16_t*>(k->data);
+  a.v = static_cast<const uint16_t*>(v->data);
+  a.out = static_cast<uint16_t*>(out->data);
+  a.lse = lse ? static_cast<float*>(lse->data) : nullptr;
+  a.q_st = q->stride[0];
+  a.q_sh = q->stride[1];
+  a.k_st = k->stride[0];
+  a.k_sh = k->stride[1];
+  a.v_st = v->stride[0];
+  a.v_sh = v->stride[1];
+  a.o_st = out->stride[0];
+  a.o_sh = out->stride[1];
+  a.lse_st = lse ? lse->stride[0] : 0;
+  a.lse_sh = lse ? lse->stride[1] : 0;
+  a.qsl = static_cast<const int32_t*>(qsl->data);
+  a.num_seqs = (int)S;
+  a.T = (int)T;
+  a.Hq = (int)Hq;
+  a.Hkv = (int)Hkv;
+  a.G = (int)G;
+  a.f16 = q->dtype == PG_F16;
+  a.score_scale_log2 = (float)score;
+  a.err = ds->err;
+  const cudaError_t e = launch_prompt_mma(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+  t_last_error.clear();
+  return PG_OK;
 }
 
 }  // namespace
@@ -1214,6 +1385,207 @@ int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* posi
   if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
   t_last_error.clear();
   return PG_OK;
+}
+
+int paged_gqa_build_tables(const pg_tensor* q_lens, const pg_tensor* ctx_lens, const pg_tensor* rows, int page_size,
+                           const pg_tensor* pages, const pg_tensor* page_counts, const pg_tensor* free_pages,
+                           const pg_tensor* num_free, pg_tensor* block_table, pg_tensor* seq_lens,
+                           pg_tensor* query_start_loc, pg_tensor* slot_map, pg_tensor* page_counts_out,
+                           pg_tensor* num_free_out, pg_stream_t stream) {
+  int st;
+  if ((st = check_ints(q_lens, "q_lens", 1, false)) || (st = check_ints(ctx_lens, "ctx_lens", 1, false)) ||
+      (st = check_ints(rows, "rows", 1, false)) || (st = check_ints(pages, "pages", 2, true)) ||
+      (st = check_ints(page_counts, "page_counts", 1, false)) || (st = check_ints(free_pages, "free_pages", 1, true)) ||
+      (st = check_ints(num_free, "num_free", 1, false)) || (st = check_ints(block_table, "block_table", 2, true)) ||
+      (st = check_ints(seq_lens, "seq_lens", 1, true)) || (st = check_ints(query_start_loc, "query_start_loc", 1, true)) ||
+      (st = check_ints(slot_map, "slot_map", 1, true)) || (st = check_ints(page_counts_out, "page_counts_out", 1, true)) ||
+      (st = check_ints(num_free_out, "num_free_out", 1, true)))
+    return st;
+  if (bad_page_size(page_size)) return fail(PG_ERR_UNSUPPORTED, "page size %d not in {16, 32, 64, 128}", page_size);
+  const long long S = q_lens->shape[0], R = pages->shape[0], W = block_table->shape[1];
+  if (ctx_lens->shape[0] != S || rows->shape[0] != S || block_table->shape[0] != S || seq_lens->shape[0] != S ||
+      query_start_loc->shape[0] != S + 1)
+    return fail(PG_ERR_INVALID_ARG, "ctx_lens, rows, block_table, seq_lens and query_start_loc must match q_lens");
+  if (page_counts->shape[0] != R || page_counts_out->shape[0] != R)
+    return fail(PG_ERR_INVALID_ARG, "page_counts and page_counts_out must have an entry per row of pages");
+  if (num_free->shape[0] != 1 || num_free_out->shape[0] != 1)
+    return fail(PG_ERR_INVALID_ARG, "num_free and num_free_out must have one entry");
+  if (S * ((W + 511) / 512 + 1) > INT32_MAX) return fail(PG_ERR_UNSUPPORTED, "sizes beyond the supported range");
+  // in place: the very same entries
+  const bool counts_same = page_counts_out->data == page_counts->data, free_same = num_free_out->data == num_free->data;
+  const pg_tensor none = {nullptr, PG_I32, 1, {0}, {1}};
+  const Named all[] = {{pages, "pages"}, {free_pages, "free_pages"}, {block_table, "block_table"}, {seq_lens, "seq_lens"},
+                       {query_start_loc, "query_start_loc"}, {slot_map, "slot_map"}, {page_counts_out, "page_counts_out"},
+                       {num_free_out, "num_free_out"}, {q_lens, "q_lens"}, {ctx_lens, "ctx_lens"}, {rows, "rows"},
+                       {counts_same ? &none : page_counts, "page_counts"}, {free_same ? &none : num_free, "num_free"}};
+  if ((st = check_apart(all, 8))) return st;
+  DeviceState* ds = nullptr;
+  if ((st = current_device(&ds))) return st;
+  TableArgs a;
+  a.q_lens = static_cast<const int32_t*>(q_lens->data);
+  a.ctx_lens = static_cast<const int32_t*>(ctx_lens->data);
+  a.rows = static_cast<const int32_t*>(rows->data);
+  a.pages = static_cast<int32_t*>(pages->data);
+  a.pages_st = pages->stride[0];
+  a.counts = static_cast<const int32_t*>(page_counts->data);
+  a.free_pages = static_cast<int32_t*>(free_pages->data);
+  a.num_free = static_cast<const int32_t*>(num_free->data);
+  a.table = static_cast<int32_t*>(block_table->data);
+  a.table_st = block_table->stride[0];
+  a.seq_lens = static_cast<int32_t*>(seq_lens->data);
+  a.qsl = static_cast<int32_t*>(query_start_loc->data);
+  a.slots = static_cast<int32_t*>(slot_map->data);
+  a.counts_out = static_cast<int32_t*>(page_counts_out->data);
+  a.num_free_out = static_cast<int32_t*>(num_free_out->data);
+  a.S = (int)S;
+  a.R = (int)R;
+  a.Wp = (int)pages->shape[1];
+  a.F = (int)free_pages->shape[0];
+  a.W = (int)W;
+  a.T = (int)slot_map->shape[0];
+  a.P = page_size;
+  a.p_shift = __builtin_ctz((unsigned)page_size);
+  a.err = ds->err;
+  const cudaError_t e = launch_build_tables(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "block table launch");
+  t_last_error.clear();
+  return PG_OK;
+}
+
+int paged_gqa_tree_masks(const pg_tensor* parents, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                         pg_tensor* masks, pg_tensor* positions, pg_stream_t stream) {
+  int st;
+  if ((st = check_ints(parents, "parents", 1, false)) || (st = check_ints(seq_lens, "seq_lens", 1, false)) ||
+      (st = check_ints(query_start_loc, "query_start_loc", 1, false)) || (st = check_ints(masks, "masks", 2, true)) ||
+      (st = check_ints(positions, "positions", 2, true)))
+    return st;
+  const long long T = parents->shape[0], S = seq_lens->shape[0];
+  if (query_start_loc->shape[0] != S + 1) return fail(PG_ERR_INVALID_ARG, "query_start_loc length must match seq_lens");
+  if (masks->shape[0] != T) return fail(PG_ERR_INVALID_ARG, "masks must be [T, words]");
+  if (masks->shape[1] < 1 || masks->shape[1] > kMaxMaskWords)
+    return fail(PG_ERR_UNSUPPORTED, "masks must have 1 to %d words", kMaxMaskWords);
+  if (positions->shape[1] != T) return fail(PG_ERR_INVALID_ARG, "positions must be [axes, T]");
+  if (positions->shape[0] < 1 || positions->shape[0] > kRopeMaxAxes)
+    return fail(PG_ERR_UNSUPPORTED, "positions must have 1 to %d axes", kRopeMaxAxes);
+  const Named all[] = {{masks, "masks"}, {positions, "positions"}, {parents, "parents"}, {seq_lens, "seq_lens"},
+                       {query_start_loc, "query_start_loc"}};
+  if ((st = check_apart(all, 2))) return st;
+  if (S == 0 || T == 0) {
+    t_last_error.clear();
+    return PG_OK;
+  }
+  DeviceState* ds = nullptr;
+  if ((st = current_device(&ds))) return st;
+  TreeMaskArgs a;
+  a.parents = static_cast<const int32_t*>(parents->data);
+  a.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+  a.qsl = static_cast<const int32_t*>(query_start_loc->data);
+  a.masks = static_cast<int32_t*>(masks->data);
+  a.masks_st = masks->stride[0];
+  a.positions = static_cast<int32_t*>(positions->data);
+  a.positions_sa = positions->stride[0];
+  a.S = (int)S;
+  a.T = (int)T;
+  a.words = (int)masks->shape[1];
+  a.axes = (int)positions->shape[0];
+  a.err = ds->err;
+  const cudaError_t e = launch_tree_masks(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "tree mask launch");
+  t_last_error.clear();
+  return PG_OK;
+}
+
+int paged_gqa_attn_tree(const pg_tensor* q, const pg_tensor* k_cache, const pg_tensor* v_cache,
+                        const pg_tensor* block_table, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                        const pg_tensor* masks, float k_descale, float v_descale, float softmax_scale, pg_tensor* out,
+                        pg_stream_t stream) {
+  return attn_tree(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks, k_descale, v_descale,
+                   softmax_scale, out, nullptr, 0, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int paged_gqa_attn_tree_ex(const pg_tensor* q, const pg_tensor* k_cache, const pg_tensor* v_cache,
+                           const pg_tensor* block_table, const pg_tensor* seq_lens, const pg_tensor* query_start_loc,
+                           const pg_tensor* masks, float k_descale, float v_descale, float softmax_scale,
+                           pg_tensor* out, void* workspace, size_t workspace_bytes, pg_stream_t stream) {
+  return attn_tree(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, masks, k_descale, v_descale,
+                   softmax_scale, out, workspace, workspace_bytes, true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int paged_gqa_cache_keep(const pg_tensor* k_cache, const pg_tensor* v_cache, const pg_tensor* block_table,
+                         const pg_tensor* seq_lens, const pg_tensor* query_start_loc, const pg_tensor* kept,
+                         const pg_tensor* num_kept, pg_tensor* seq_lens_out, pg_stream_t stream) {
+  int st;
+  long long W = 0;
+  if ((st = check_tensor(k_cache, "k_cache", 4)) || (st = check_tensor(v_cache, "v_cache", 4)) ||
+      (st = check_tables(block_table, seq_lens, query_start_loc, &W)) || (st = check_ints(kept, "kept", 2, false)) ||
+      (st = check_ints(num_kept, "num_kept", 1, false)) || (st = check_ints(seq_lens_out, "seq_lens_out", 1, true)))
+    return st;
+  if (k_cache->dtype != PG_E4M3 && k_cache->dtype != PG_BF16)
+    return fail(PG_ERR_UNSUPPORTED, "cache dtype must be bf16 or e4m3");
+  if (v_cache->dtype != k_cache->dtype) return fail(PG_ERR_INVALID_ARG, "k_cache and v_cache dtypes differ");
+  for (int i = 0; i < 4; ++i)
+    if (k_cache->shape[i] != v_cache->shape[i]) return fail(PG_ERR_INVALID_ARG, "k_cache and v_cache shapes differ");
+  const long long NB = k_cache->shape[0], P = k_cache->shape[1], Hkv = k_cache->shape[2], S = seq_lens->shape[0];
+  if (k_cache->shape[3] != kHeadDim) return fail(PG_ERR_UNSUPPORTED, "head_dim must be 256");
+  if (bad_page_size(P)) return fail(PG_ERR_UNSUPPORTED, "page size %lld not in {16, 32, 64, 128}", P);
+  const int size = k_cache->dtype == PG_BF16 ? 2 : 1;
+  for (const pg_tensor* t : {k_cache, v_cache}) {
+    if (t->stride[3] != 1) return fail(PG_ERR_INVALID_ARG, "the head_dim axis must be contiguous");
+    if (!aligned16(t->data)) return fail(PG_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
+    for (int i = 0; i < 3; ++i)
+      if ((t->stride[i] * size) % 16) return fail(PG_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes");
+    if (!rows_disjoint(t, 3)) return fail(PG_ERR_INVALID_ARG, "cache strides make (page, slot, head) rows overlap");
+    if (NB > 0 && Hkv > 0 && !t->data) return fail(PG_ERR_INVALID_ARG, "null data pointer");
+  }
+  if (NB > INT32_MAX || Hkv > 65535 || 2 * S * Hkv > INT32_MAX) return fail(PG_ERR_UNSUPPORTED, "sizes beyond the supported range");
+  if (kept->shape[0] != S || num_kept->shape[0] != S || seq_lens_out->shape[0] != S)
+    return fail(PG_ERR_INVALID_ARG, "kept, num_kept and seq_lens_out must match seq_lens");
+  const Named all[] = {{seq_lens_out, "seq_lens_out"}, {block_table, "block_table"}, {seq_lens, "seq_lens"},
+                       {query_start_loc, "query_start_loc"}, {kept, "kept"}, {num_kept, "num_kept"}};
+  if ((st = check_apart(all, 1))) return st;
+  if (Hkv < 1) return fail(PG_ERR_INVALID_ARG, "the caches have no kv head");
+  if (k_cache->data && k_cache->data == v_cache->data)
+    return fail(PG_ERR_INVALID_ARG, "k_cache and v_cache are the same memory");
+  if (S == 0) {
+    t_last_error.clear();
+    return PG_OK;
+  }
+  DeviceState* ds = nullptr;
+  if ((st = current_device(&ds))) return st;
+  KeepArgs a;
+  const pg_tensor* caches[2] = {k_cache, v_cache};
+  for (int i = 0; i < 2; ++i) {
+    a.cache[i] = static_cast<uint8_t*>(caches[i]->data);
+    a.sb[i] = caches[i]->stride[0] * size;
+    a.sp[i] = caches[i]->stride[1] * size;
+    a.sh[i] = caches[i]->stride[2] * size;
+  }
+  a.bt = static_cast<const int32_t*>(block_table->data);
+  a.bt_stride = block_table->stride[0];
+  a.seq_lens = static_cast<const int32_t*>(seq_lens->data);
+  a.qsl = static_cast<const int32_t*>(query_start_loc->data);
+  a.kept = static_cast<const int32_t*>(kept->data);
+  a.kept_st = kept->stride[0];
+  a.num_kept = static_cast<const int32_t*>(num_kept->data);
+  a.lens_out = static_cast<int32_t*>(seq_lens_out->data);
+  a.S = (int)S;
+  a.Hkv = (int)Hkv;
+  a.D = (int)kept->shape[1];
+  a.P = (int)P;
+  a.p_shift = __builtin_ctz((unsigned)P);
+  a.W = (int)W;
+  a.NB = (int)NB;
+  a.row_bytes = kHeadDim * size;
+  a.err = ds->err;
+  const cudaError_t e = launch_cache_keep(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache keep launch");
+  t_last_error.clear();
+  return PG_OK;
+}
+
+int paged_gqa_attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* query_start_loc,
+                          float softmax_scale, pg_tensor* out, pg_tensor* lse, pg_stream_t stream) {
+  return attn_prompt(q, k, v, query_start_loc, softmax_scale, out, lse, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int paged_gqa_version(void) { return 100; }

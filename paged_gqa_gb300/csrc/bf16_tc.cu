@@ -149,7 +149,8 @@ __device__ __forceinline__ Item load_item(const Problem& p, const ClassPlan& cp,
 
 }  // namespace
 
-template <bool kFused>
+// kTree: the new tokens see each other by the call's masks (Problem::mask_words) instead of causally.
+template <bool kFused, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                Problem p, Pointers ptr, ClassPlan cp) {
@@ -426,6 +427,8 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
       l = 0.f;
       const int kv_hi = I.kv_hi, key_begin = I.tile_begin * kTileKeys;
       const int hi_key = min(kv_hi - 1, lim);  // keys <= hi_key are visible to this row
+      const int ctx = I.L - I.qn, tok = lim - ctx;  // kTree: this row's new token
+      const int32_t* mask = kTree && row < I.nrows ? ptr.masks + (long long)(I.q0 + tok) * p.mask_st : nullptr;
       // A failed wait (timeout or abort) does not leave the loop: every later wait then
       // fails fast, so all softmax warps still pass the same barriers and finish.
       for (int j = 0; j < I.nsub; ++j, ++g) {
@@ -444,9 +447,16 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
         }
         tmem_wait_ld();
         // scaled scores, masked past the row's causal limit and the piece's end
-        const bool need_mask = (key0 + kSub > kv_hi) || (key0 + kSub - 1 > min_lim);
+        const bool need_mask = (key0 + kSub > kv_hi) || (key0 + kSub > (kTree ? ctx : min_lim + 1));
+        if (kTree) {
+          uint32_t see = 0xffffffffu;  // this thread's 32 keys
+          if (need_mask) see = mask ? tree_bits(p, mask, tok, kbase - ctx) & low_bits(kv_hi - kbase) : 0u;
 #pragma unroll
-        for (int i = 0; i < kHalfKeys; ++i) t[i] = (!need_mask || kbase + i <= hi_key) ? t[i] * c : -INFINITY;
+          for (int i = 0; i < kHalfKeys; ++i) t[i] = (see >> i & 1u) ? t[i] * c : -INFINITY;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kHalfKeys; ++i) t[i] = (!need_mask || kbase + i <= hi_key) ? t[i] * c : -INFINITY;
+        }
         const float mx = extreme_of<true>(t);
         // the row's maximum over both key halves (partner: same lane, the other warp)
         ms.red[g & 1][kh][row] = mx;
@@ -595,8 +605,10 @@ int launch_bf16_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, c
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t e;
-  auto kern = self_planned ? bf16_tc_kernel<true> : bf16_tc_kernel<false>;
-  const int which = self_planned ? 2 : 1;
+  const bool tree = p.mask_words > 0;
+  auto kern = tree ? (self_planned ? bf16_tc_kernel<true, true> : bf16_tc_kernel<false, true>)
+                   : (self_planned ? bf16_tc_kernel<true, false> : bf16_tc_kernel<false, false>);
+  const int which = (self_planned ? 2 : 1) << (tree ? 2 : 0);
   if (dev >= 0 && dev < 64 && !(attr_done[dev] & which)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) {

@@ -105,6 +105,10 @@ struct Problem {
   int num_seqs, T, Hq, Hkv, G, P, W, NB;
   int q_is_fp8, kv_is_fp8;
   int kv_is_fp4;           // 4-bit caches: the k_ / v_ strides are bytes and *_sp is unused
+  // Token trees: 32-bit words of a token's mask, 0 for plain causal calls. New token t of a
+  // sequence sees its context and those new tokens i <= t whose bit of the mask is set.
+  int mask_words;
+  long long mask_st;       // elements between the masks of two tokens
   int q_cast;              // bf16 Q quantised per tensor inside the call (kQCast)
   int q_amax_parts;        // entries of Pointers::q_amax (q_cast only)
   // strides in elements
@@ -130,6 +134,11 @@ struct Problem {
   // Two fp32 zeros: an addend that keeps the compiler from fusing a product with a sum (4-bit caches).
   unsigned long long zero2;
 };
+
+// Does a token's mask have a bit for each of qn new tokens?
+__host__ __device__ __forceinline__ bool mask_holds(const Problem& p, int qn) {
+  return p.mask_words == 0 || qn <= 32 * p.mask_words;
+}
 
 // Units a range of the cut has at least (kMinRangeUnits). 4-bit caches: a tile takes longer, and the
 // last piece merges row by row, so the rows of a block decide. Graph replays, us:
@@ -161,6 +170,7 @@ struct Pointers {
   void* out;               // bf16
   uint32_t* err;           // device error word
   const float* q_amax;     // per-CTA maxima of |q| from the amax kernel (q_cast only)
+  const int32_t* masks;    // [T, mask_words] (token trees only)
 };
 
 // Plan output in the workspace, one instance per class.

@@ -59,6 +59,22 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// Bits 0 .. 31 of a token tree's visibility from new token `first` on, for new token t with the given
+// mask row: ones for tokens of the context (negative numbers), the mask's bits up to t, zeros behind.
+__device__ __forceinline__ uint32_t tree_word(const Problem& p, const int32_t* row, int t, int w) {
+  if (w < 0) return 0xffffffffu;
+  const int keep = t - 32 * w;  // the last bit that counts
+  if (keep < 0 || w >= p.mask_words) return 0u;
+  const uint32_t x = (uint32_t)__ldg(row + w);
+  return keep >= 31 ? x : x & ((2u << keep) - 1u);
+}
+__device__ __forceinline__ uint32_t tree_bits(const Problem& p, const int32_t* row, int t, int first) {
+  const int w = first >> 5;
+  return __funnelshift_r(tree_word(p, row, t, w), tree_word(p, row, t, w + 1), first & 31);
+}
+// The low n bits (all from 32 on, none from 0 down).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // Partial result slot of (block, split): f16 rows of O / l in cache-code units.
 __device__ __forceinline__ uint16_t* slot_o(const ClassPlan& cp, int slot) {
   return cp.part_o + (size_t)slot * cp.slot_rows * kHeadDim;

@@ -60,7 +60,7 @@ __device__ SeqInfo seq_info(const Problem& p, const Pointers& ptr, int s) {
   r.qn = q1 - r.q0;
   r.L = ptr.seq_lens[s];
   r.ok = (r.qn >= 0) && (r.q0 >= 0) && (q1 <= p.T) && (r.qn <= r.L) &&
-         ((long long)r.L <= (long long)p.W * p.P);
+         ((long long)r.L <= (long long)p.W * p.P) && mask_holds(p, r.qn);
   return r;
 }
 

@@ -150,6 +150,10 @@ portable_attn_kernel(Problem p, Pointers ptr, ClassPlan cp) {
     const int lim0 = lr0 < rb.nrows ? L - qn + (rb.row0 + lr0) / p.G : -1;
     const int lim1 = lr1 < rb.nrows ? L - qn + (rb.row0 + lr1) / p.G : -1;
     const bool warp_active = warp * 16 < rb.nrows;
+    // token trees: the masks of the two rows' tokens, which are L - qn below their limits
+    const int ctx = L - qn;
+    const int32_t* mask0 = p.mask_words && lim0 >= 0 ? ptr.masks + (long long)(seq_q0 + lim0 - ctx) * p.mask_st : nullptr;
+    const int32_t* mask1 = p.mask_words && lim1 >= 0 ? ptr.masks + (long long)(seq_q0 + lim1 - ctx) * p.mask_st : nullptr;
 
     float o[32][4];
 #pragma unroll
@@ -219,7 +223,10 @@ portable_attn_kernel(Problem p, Pointers ptr, ClassPlan cp) {
         for (int e = 0; e < 4; ++e) {
           const int key = k0 + n * 8 + 2 * tq + (e & 1);
           const int lim = min(key_hi - 1, (e < 2) ? lim0 : lim1);
-          const float v = key <= lim ? s[n][e] * p.score_scale_log2 : -INFINITY;
+          bool seen = key <= lim;
+          if (p.mask_words && seen && key >= ctx)
+            seen = tree_bits(p, e < 2 ? mask0 : mask1, (e < 2 ? lim0 : lim1) - ctx, key - ctx) & 1u;
+          const float v = seen ? s[n][e] * p.score_scale_log2 : -INFINITY;
           s[n][e] = v;
           if (e < 2) mx0 = fmaxf(mx0, v); else mx1 = fmaxf(mx1, v);
         }

@@ -143,7 +143,8 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
 
 }  // namespace
 
-template <int kQM>
+// kTree: the new tokens see each other by the call's masks (Problem::mask_words) instead of causally.
+template <int kQM, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   Problem p, Pointers ptr, ClassPlan cp) {
@@ -484,6 +485,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       const int kv_hi = I.kv_hi, tile_begin = I.tile_begin, ntiles = I.ntiles;
       const int hi_key = min(kv_hi - 1, lim);  // keys <= hi_key are visible to this row
       const bool c_pos = c >= 0.f;
+      const int ctx = I.L - I.qn, tok = lim - ctx;  // kTree: this row's new token
+      const int32_t* mask = kTree && row < I.nrows ? ptr.masks + (long long)(I.q0 + tok) * p.mask_st : nullptr;
       // A failed wait (timeout or abort) does not leave the loop: every later wait then
       // fails fast, so all softmax warps still pass the same barriers and finish.
       for (int j = 0; j < ntiles; ++j, ++g) {
@@ -505,9 +508,19 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         mbar_arrive(bar(ms.s_free));  // S(g+1) may overwrite S now
         // masked tiles hold scaled scores; unmasked tiles keep raw scores and take the
         // scale in the exponent's FFMA
-        const bool need_mask = (key0 + kTileKeys > kv_hi) || (key0 + kTileKeys - 1 > min_lim);
+        const bool need_mask = (key0 + kTileKeys > kv_hi) || (key0 + kTileKeys > (kTree ? ctx : min_lim + 1));
         float mx;
-        if (need_mask) {
+        if (need_mask && kTree) {
+          uint32_t see[2] = {0u, 0u};  // this thread's 64 keys
+          if (mask) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              see[w] = tree_bits(p, mask, tok, kbase + 32 * w - ctx) & low_bits(kv_hi - (kbase + 32 * w));
+          }
+#pragma unroll
+          for (int i = 0; i < kHalfKeys; ++i) t[i] = (see[i >> 5] >> (i & 31) & 1u) ? t[i] * c : -INFINITY;
+          mx = extreme_of<true>(t);
+        } else if (need_mask) {
 #pragma unroll
           for (int i = 0; i < kHalfKeys; ++i) t[i] = (kbase + i <= hi_key) ? t[i] * c : -INFINITY;
           mx = extreme_of<true>(t);
@@ -668,9 +681,13 @@ int launch_prefill_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp
   cudaGetDevice(&dev);
   cudaError_t e;
   const int mode = p.q_cast ? kQCast : p.q_is_fp8 ? kQGiven : kQSplit;
-  auto kern = mode == kQCast ? prefill_tc_kernel<kQCast> : mode == kQGiven ? prefill_tc_kernel<kQGiven> : prefill_tc_kernel<kQSplit>;
+  const bool tree = p.mask_words > 0;  // (with a bf16 q only)
+  if (tree && mode != kQSplit) return 0;
+  auto kern = tree ? prefill_tc_kernel<kQSplit, true>
+              : mode == kQCast ? prefill_tc_kernel<kQCast, false>
+              : mode == kQGiven ? prefill_tc_kernel<kQGiven, false> : prefill_tc_kernel<kQSplit, false>;
   const size_t bytes = mode != kQSplit ? smem_bytes<true>() : smem_bytes<false>();
-  const int which = 1 << mode;
+  const int which = 1 << (tree ? 3 : mode);
   if (dev >= 0 && dev < 64 && !(attr_done[dev] & which)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) {

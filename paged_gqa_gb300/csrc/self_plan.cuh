@@ -52,7 +52,7 @@ __device__ __forceinline__ void load(const Problem& p, const Pointers& ptr, Scra
     long long v = 0;
     int tiles = 0;
     // the plan kernel's validity test; invalid sequences are flagged and zeroed there
-    const bool ok = qn >= 0 && q0 >= 0 && q1 <= p.T && qn <= L && (long long)L <= (long long)p.W * p.P;
+    const bool ok = qn >= 0 && q0 >= 0 && q1 <= p.T && qn <= L && (long long)L <= (long long)p.W * p.P && mask_holds(p, qn);
     if (ok && qn > 0 && (long long)qn * p.G <= kVerifyRows) {
       tiles = (L + kTileKeys - 1) / kTileKeys;
       v = ((long long)p.Hkv * (tiles + kE) << 16) | 1;

@@ -112,6 +112,7 @@ struct Misc {
   alignas(16) float red[4][kVN];
   alignas(16) float alpha[kVN];
   alignas(16) int lim[2][kVN];
+  alignas(16) uint32_t tree[2][2][kVN];  // [item parity][word][row]: the new tokens a row's token sees (kTree)
   alignas(16) long long out_off[2][kVN];
   alignas(16) float merge_w[kMergeMaxSplits * kSlotRows];
   alignas(16) float lse_stage[kVN];  // a split piece's log2-sum-exp per row, for its bulk store
@@ -196,7 +197,8 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
 
 }  // namespace
 
-template <int kQM, bool kFused>
+// kTree: the new tokens see each other by the call's masks (Problem::mask_words) instead of causally.
+template <int kQM, bool kFused, bool kTree>
 __global__ void __launch_bounds__(kVThreads, 1)
 verify_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                  Problem p, Pointers ptr, ClassPlan cp) {
@@ -317,9 +319,15 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           const RowMap m = map_row(I.row0 + n, p.G, I.kvh);
           ms.lim[pi][n] = I.L - I.qn + m.t;
           ms.out_off[pi][n] = (long long)(I.q0 + m.t) * p.o_st + (long long)m.h * p.o_sh;
+          if (kTree) {  // at most 64 tokens: two words
+            const int32_t* mask = ptr.masks + (long long)(I.q0 + m.t) * p.mask_st;
+            ms.tree[pi][0][n] = tree_word(p, mask, m.t, 0);
+            ms.tree[pi][1][n] = tree_word(p, mask, m.t, 1);
+          }
         } else {
           ms.lim[pi][n] = -1;
           ms.out_off[pi][n] = 0;
+          if (kTree) ms.tree[pi][0][n] = ms.tree[pi][1][n] = 0u;
         }
         // padding rows: a finite reference, so their (discarded) scores never vote
         ms.m[pi][n] = n < I.nrows ? kMInit : 0.f;
@@ -460,9 +468,26 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         load_s(b, t);
         tmem_wait_ld();
         // x = s c - m + sigma: the exponent of P, one FFMA per score
-        const bool need_mask = (key0 + kTileKeys > I.kv_hi) || (key0 + kTileKeys - 1 > min_lim);
+        // (a token of a tree may not even see itself: its masks begin with the first new token)
+        const bool need_mask = (key0 + kTileKeys > I.kv_hi) || (key0 + kTileKeys - 1 > (kTree ? min_lim - 1 : min_lim));
         float xmax = -INFINITY;
-        if (need_mask) {
+        // kTree: this thread's key is bit tree_bit of a row's word tree_w, or of the context
+        const int new_key = key - (I.L - I.qn);
+        const int tree_w = (new_key >> 5) & 1, tree_bit = new_key & 31;
+        if (need_mask && kTree) {
+          const bool kin = key < I.kv_hi;
+#pragma unroll
+          for (int n = 0; n < kCols; n += 4) {
+            const float4 o4 = *reinterpret_cast<const float4*>(&ms.mo[pi][c0 + n]);
+            uint4 w4 = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+            if (new_key >= 0) w4 = *reinterpret_cast<const uint4*>(&ms.tree[pi][tree_w][c0 + n]);
+            t[n] = (kin && (w4.x >> tree_bit & 1u)) ? fmaf(t[n], c, o4.x) : -INFINITY;
+            t[n + 1] = (kin && (w4.y >> tree_bit & 1u)) ? fmaf(t[n + 1], c, o4.y) : -INFINITY;
+            t[n + 2] = (kin && (w4.z >> tree_bit & 1u)) ? fmaf(t[n + 2], c, o4.z) : -INFINITY;
+            t[n + 3] = (kin && (w4.w >> tree_bit & 1u)) ? fmaf(t[n + 3], c, o4.w) : -INFINITY;
+            xmax = fmaxf(xmax, fmaxf(fmaxf(t[n], t[n + 1]), fmaxf(t[n + 2], t[n + 3])));
+          }
+        } else if (need_mask) {
           const bool kin = key < I.kv_hi;
 #pragma unroll
           for (int n = 0; n < kCols; n += 4) {
@@ -499,7 +524,8 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           const bool kin = key < I.kv_hi;
 #pragma unroll
           for (int n = 0; n < kCols; ++n) {
-            const bool vis = !need_mask || (kin && key <= ms.lim[pi][c0 + n]);
+            const bool vis = !need_mask || (kin && (kTree ? new_key < 0 || (ms.tree[pi][tree_w][c0 + n] >> tree_bit & 1u)
+                                                          : key <= ms.lim[pi][c0 + n]));
             t[n] = vis ? t[n] * c : -INFINITY;  // s c, masked
             const float r = warp_max(t[n]);
             if (lane == n) ms.red[q4][c0 + n] = r;
@@ -957,12 +983,15 @@ int launch_verify_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp,
   cudaGetDevice(&dev);
   cudaError_t e;
   const int mode = p.q_cast ? kQCast : p.q_is_fp8 ? kQGiven : kQSplit;
-  auto kern = p.fused_verify
-                  ? (mode == kQCast ? verify_tc_kernel<kQCast, true>
-                                    : mode == kQGiven ? verify_tc_kernel<kQGiven, true> : verify_tc_kernel<kQSplit, true>)
-                  : (mode == kQCast ? verify_tc_kernel<kQCast, false>
-                                    : mode == kQGiven ? verify_tc_kernel<kQGiven, false> : verify_tc_kernel<kQSplit, false>);
-  const int which = 1 << (mode + (p.fused_verify ? 3 : 0));
+  const bool tree = p.mask_words > 0;  // (with a bf16 q only)
+  if (tree && mode != kQSplit) return 0;
+  auto kern = tree ? (p.fused_verify ? verify_tc_kernel<kQSplit, true, true> : verify_tc_kernel<kQSplit, false, true>)
+              : p.fused_verify
+                  ? (mode == kQCast ? verify_tc_kernel<kQCast, true, false>
+                                    : mode == kQGiven ? verify_tc_kernel<kQGiven, true, false> : verify_tc_kernel<kQSplit, true, false>)
+                  : (mode == kQCast ? verify_tc_kernel<kQCast, false, false>
+                                    : mode == kQGiven ? verify_tc_kernel<kQGiven, false, false> : verify_tc_kernel<kQSplit, false, false>);
+  const int which = 1 << ((tree ? 6 : mode) + (p.fused_verify ? 3 : 0));
   if (dev >= 0 && dev < 64 && !(attr_done[dev] & which)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) {
