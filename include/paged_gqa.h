@@ -468,9 +468,17 @@ int paged_gqa_cache_keep(const pg_tensor* k_cache, const pg_tensor* v_cache, con
  * [0, T) is flagged (PG_ERR_DEVICE_BOUNDS) and its rows are left as they were. A NaN or infinity in V
  * reaches the tokens that see it, and may reach earlier ones of its prompt that share a block of rows
  * with one; no other prompt.
+ *
+ * Calls are ordered by the library as those of paged_gqa_attn_fp4 (they share its workspace); in a stream
+ * capture use paged_gqa_attn_prompt_ex, under the terms of paged_gqa_attn_fp4_ex and with a workspace of
+ * paged_gqa_prompt_workspace_size(...) bytes (0 on invalid sizes).
  */
 int paged_gqa_attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* query_start_loc,
                           float softmax_scale, pg_tensor* out, pg_tensor* lse, pg_stream_t stream);
+int paged_gqa_attn_prompt_ex(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* query_start_loc,
+                             float softmax_scale, pg_tensor* out, pg_tensor* lse, void* workspace, size_t workspace_bytes,
+                             pg_stream_t stream);
+size_t paged_gqa_prompt_workspace_size(int num_seqs, int total_tokens, int num_q_heads, int num_kv_heads, int device);
 
 /*
  * Workspace bytes for a call with these host-known sizes on `device`
@@ -524,7 +532,8 @@ int paged_gqa_set_stall_test(uint32_t wait_ns);
  * Host-side launch summary of the last successful call on this host thread, for
  * tests and the benchmark. out8 receives {verify CTAs, prefill CTAs, kernels
  * launched, path bits (2: tcgen05 verify, 4: tcgen05 prefill, 8: warp-MMA verify,
- * 16: warp-MMA prefill, 32: tcgen05 sparse, 64: warp-MMA sparse, 128: 4-bit decode), verify block bound,
+ * 16: warp-MMA prefill, 32: tcgen05 sparse, 64: warp-MMA sparse, 128: 4-bit decode, 256: tcgen05 prompt (its
+ * CTAs stand for the verify CTAs), 512: warp-MMA prompt), verify block bound,
  * prefill block bound, workspace bytes, 1 if the verify kernel planned its own class}.
  * A sparse call sets only the launch count and the path bits.
  */

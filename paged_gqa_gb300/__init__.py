@@ -28,6 +28,8 @@ from ._binding import (  # noqa: F401
     paged_gqa_attn_tree_ex,
     paged_gqa_cache_keep,
     paged_gqa_attn_prompt,
+    paged_gqa_attn_prompt_ex,
+    paged_gqa_prompt_workspace_size,
     paged_gqa_check_device_errors,
     paged_gqa_last_error,
     paged_gqa_last_plan,

@@ -21,7 +21,8 @@ EXPORTED = ("paged_gqa_attn", "paged_gqa_attn_ex", "paged_gqa_attn_noalloc", "pa
             "paged_gqa_cache_write_fp4", "paged_gqa_cache_read_fp4", "paged_gqa_attn_fp4", "paged_gqa_attn_fp4_ex",
             "paged_gqa_rope",
             "paged_gqa_build_tables", "paged_gqa_tree_masks", "paged_gqa_attn_tree", "paged_gqa_attn_tree_ex",
-            "paged_gqa_cache_keep", "paged_gqa_attn_prompt",
+            "paged_gqa_cache_keep", "paged_gqa_attn_prompt", "paged_gqa_attn_prompt_ex",
+            "paged_gqa_prompt_workspace_size",
             "paged_gqa_workspace_size",
             "paged_gqa_last_error",
             "paged_gqa_check_device_errors", "paged_gqa_set_path", "paged_gqa_set_stall_test", "paged_gqa_last_plan",
@@ -99,8 +100,11 @@ def load(build_if_missing: bool = True):
             lib.paged_gqa_attn_tree_ex.argtypes = [P, P, P, P, P, P, P, f, f, f, P, c_vp, ctypes.c_size_t, c_vp]
             lib.paged_gqa_cache_keep.argtypes = [P, P, P, P, P, P, P, P, c_vp]
             lib.paged_gqa_attn_prompt.argtypes = [P, P, P, P, f, P, P, c_vp]
+            lib.paged_gqa_attn_prompt_ex.argtypes = [P, P, P, P, f, P, P, c_vp, ctypes.c_size_t, c_vp]
+            lib.paged_gqa_prompt_workspace_size.argtypes = [ctypes.c_int] * 5
+            lib.paged_gqa_prompt_workspace_size.restype = ctypes.c_size_t
             for name in ("cache_write_fp4", "cache_read_fp4", "attn_fp4", "attn_fp4_ex", "rope", "build_tables", "tree_masks",
-                         "attn_tree", "attn_tree_ex", "cache_keep", "attn_prompt"):
+                         "attn_tree", "attn_tree_ex", "cache_keep", "attn_prompt", "attn_prompt_ex"):
                 getattr(lib, "paged_gqa_" + name).restype = ctypes.c_int
             lib.paged_gqa_workspace_size.argtypes = [ctypes.c_int] * 7
             lib.paged_gqa_workspace_size.restype = ctypes.c_size_t
@@ -370,6 +374,20 @@ def paged_gqa_attn_prompt(q, k, v, query_start_loc, softmax_scale: float, out, l
     d = _pack(*t)
     _check(lib.paged_gqa_attn_prompt(*d[:4], float(softmax_scale), d[4], d[5] if lse is not None else None,
                                      _stream(stream)))
+
+
+def paged_gqa_attn_prompt_ex(q, k, v, query_start_loc, softmax_scale: float, out, lse, workspace, stream=None) -> None:
+    """paged_gqa_attn_prompt with a caller-owned workspace tensor (for stream capture); lse may be None."""
+    lib = load()
+    t = (q, k, v, query_start_loc, out) + (() if lse is None else (lse,))
+    _on_device(*t)
+    d = _pack(*t)
+    _check(lib.paged_gqa_attn_prompt_ex(*d[:4], float(softmax_scale), d[4], d[5] if lse is not None else None,
+                                        *_workspace(workspace), _stream(stream)))
+
+
+def paged_gqa_prompt_workspace_size(num_seqs: int, total_tokens: int, num_q_heads: int, num_kv_heads: int, device: int = 0) -> int:
+    return int(load().paged_gqa_prompt_workspace_size(num_seqs, total_tokens, num_q_heads, num_kv_heads, device))
 
 
 def paged_gqa_workspace_size(num_seqs: int, total_q: int, num_q_heads: int, num_kv_heads: int,

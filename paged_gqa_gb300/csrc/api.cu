@@ -97,7 +97,7 @@ struct DeviceState {
   uint32_t* err = nullptr;   // address of g_error_word on this device
   void* ws = nullptr;        // library-owned workspace
   size_t ws_bytes = 0;
-  // The one of the 4-bit and the tree attention; a call waits for the last one's event.
+  // The one of the 4-bit, the tree and the prompt attention; a call waits for the last one's event.
   void* ws4 = nullptr;
   size_t ws4_bytes = 0;
   cudaEvent_t ws4_done = nullptr;
@@ -923,8 +923,32 @@ int attn_tree(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const 
                         [&](void* ws, bool) { return run(val, k, v, ws, L.total, L, ds, stream); });
 }
 
+// Workspace of the prompt attention.
+size_t prompt_layout(int clusters, char* base, PromptScratch* ws) {
+  const size_t slots = 4 * (size_t)clusters;
+  size_t at = 0;
+  auto part = [&](size_t bytes) {
+    const size_t o = at;
+    at += align256(bytes);
+    return base + o;
+  };
+  char* o = part(slots * 128 * kHeadDim * sizeof(float));
+  char* l = part(slots * 128 * sizeof(float));
+  char* c = part(slots * sizeof(unsigned long long));
+  char* e = part(sizeof(unsigned long long));
+  if (ws) {
+    ws->part_o = reinterpret_cast<float*>(o);
+    ws->part_lse = reinterpret_cast<float*>(l);
+    ws->counters = reinterpret_cast<unsigned long long*>(c);
+    ws->epoch = reinterpret_cast<unsigned long long*>(e);
+    ws->call_tag = next_call_tag();
+  }
+  return at;
+}
+
 int attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* qsl, float softmax_scale,
-                const pg_tensor* out, const pg_tensor* lse, cudaStream_t stream) {
+                const pg_tensor* out, const pg_tensor* lse, void* user_ws, size_t user_ws_bytes, bool use_user_ws,
+                cudaStream_t stream) {
   int st;
   if (!q || (q->dtype != PG_BF16 && q->dtype != PG_F16)) return fail(q ? PG_ERR_UNSUPPORTED : PG_ERR_INVALID_ARG, "q must be bf16 or f16");
   if ((st = check_rows(q, "q", false, q->dtype)) || (st = check_rows(k, "k", false, q->dtype)) ||
@@ -992,10 +1016,25 @@ int attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, cons
   a.f16 = q->dtype == PG_F16;
   a.score_scale_log2 = (float)score;
   a.err = ds->err;
-  const cudaError_t e = launch_prompt_mma(a, stream);
-  if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
-  t_last_error.clear();
-  return PG_OK;
+  a.stall_test_ns = g_stall_test_ns.load();
+  const int clusters = prompt_clusters(T, (int)S, (int)Hkv, (int)G, ds->sms);
+  return with_workspace(ds, prompt_layout(clusters, nullptr, nullptr), user_ws, user_ws_bytes, use_user_ws,
+                        "paged_gqa_attn_prompt_ex", stream, [&](void* ws, bool captured) -> int {
+    PromptScratch scratch;
+    prompt_layout(clusters, static_cast<char*>(ws), &scratch);
+    int64_t plan_info[8] = {2 * clusters, 0, 1, 256, 0, 0, (int64_t)prompt_layout(clusters, nullptr, nullptr), 0};
+    int r = 0;
+    if (g_path.load() != 1 && (r = launch_prompt_tc(a, scratch, clusters, captured, stream)) < 0)
+      return fail(PG_ERR_CUDA, "tcgen05 prompt launch failed: %s", tc_last_error());
+    if (r == 0) {
+      const cudaError_t e = launch_prompt_mma(a, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+      plan_info[0] = 0;
+      plan_info[3] = 512;
+    }
+    memcpy(t_last_plan, plan_info, sizeof plan_info);
+    return PG_OK;
+  });
 }
 
 }  // namespace
@@ -1585,7 +1624,24 @@ int paged_gqa_cache_keep(const pg_tensor* k_cache, const pg_tensor* v_cache, con
 
 int paged_gqa_attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* query_start_loc,
                           float softmax_scale, pg_tensor* out, pg_tensor* lse, pg_stream_t stream) {
-  return attn_prompt(q, k, v, query_start_loc, softmax_scale, out, lse, reinterpret_cast<cudaStream_t>(stream));
+  return attn_prompt(q, k, v, query_start_loc, softmax_scale, out, lse, nullptr, 0, false,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+int paged_gqa_attn_prompt_ex(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* query_start_loc,
+                             float softmax_scale, pg_tensor* out, pg_tensor* lse, void* workspace, size_t workspace_bytes,
+                             pg_stream_t stream) {
+  return attn_prompt(q, k, v, query_start_loc, softmax_scale, out, lse, workspace, workspace_bytes, true,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t paged_gqa_prompt_workspace_size(int num_seqs, int total_tokens, int num_q_heads, int num_kv_heads, int device) {
+  if (num_seqs < 0 || total_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > 128)
+    return 0;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0) return 0;
+  return prompt_layout(prompt_clusters(total_tokens, num_seqs, num_kv_heads, num_q_heads / num_kv_heads, sms), nullptr, nullptr);
 }
 
 int paged_gqa_version(void) { return 100; }

@@ -1,0 +1,769 @@
+// prompt_tc.cu -- tcgen05 (TMEM, TMA) kernel of causal attention over whole packed prompts.
+//
+// The formula: out = softmax(scale q K^T + causal) V per (token, head), head_dim 256, grouped heads;
+// 4 * 256 flops per visible (row, key) pair, K and V re-read from L2 by every block of rows. It is bound by
+// the matrix products, and next by L2: 128 rows against 1024 bytes of K and V per key are 128 flops a byte,
+// which at 2 PFLOP/s would be 16 TB/s. So two SMs share a block:
+//
+//   * a cluster of two CTAs (cta_group::2) serves 256 rows of a prompt and kv head. A CTA holds 128 / G tokens,
+//     row t * G + g of its half being token t, head g (one TMA box per 128-byte d-quarter of Q). Each CTA
+//     loads half of every tile of 128 keys: 64 keys of K, half of d of V; the instruction reads both
+//     halves. That halves the bytes from L2 and the shared memory a tile takes (Q 64 KB, two stages of K
+//     and of V of 32 KB each per CTA);
+//   * S = Q K^T: M = 256, N = 128, 16 instructions of K = 16 per tile; O += P V: M = 256, N = 256, 8
+//     instructions, P (the inputs' type) from TMEM. S takes 128 columns, P two buffers of 64, O 256: all 512;
+//   * S(g + 1) is issued once the softmax has loaded S(g), and P(g) is written once P.V(g - 2) is done, so the
+//     tensor pipe always has the next product queued: a tile's softmax (8 warps, two threads per
+//     row) has the time of two products;
+//   * online softmax, fp32, one row per TMEM lane; the reference of a row moves, and its O is rescaled, only
+//     when a score exceeds it by 2^8;
+//   * the even CTA issues the products. The odd CTA's copies are announced to it by a relaying warp, the
+//     softmax warps of both arrive on its barriers, and its commits arrive in both CTAs;
+//   * the work is cut into equal ranges over the clusters, worked out by each CTA for itself: block b of a
+//     prompt costs a fixed part and (b + 1) tokens' worth of keys, a closed form whose prefix sums need no pass
+//     over blocks. A block cut across clusters is merged by its last piece (fp32 partials, counters
+//     tagged per call).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdio>
+
+#include "common.cuh"
+#include "device_util.cuh"
+#include "prompt.cuh"
+#include "tc_kernels.cuh"
+#include "tc_util.cuh"
+
+namespace pgqa {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;                   // rows of a CTA
+constexpr int kKeys = 128;                   // keys of a tile
+constexpr int kSoftWarp0 = 4, kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
+constexpr int kThreads = kSoftWarp0 * 32 + kSoftThreads;
+constexpr int kStages = 2;                   // of K, and of V
+constexpr int kRing = 2;                     // items known in advance
+constexpr float kTau = 8.f;                  // a row's reference moves when a score exceeds it by this (log2)
+constexpr float kMInit = -1.0e30f;
+
+constexpr uint32_t kQQuarter = kRows * 128;  // [128 rows][64 d]
+constexpr uint32_t kKQuarter = 64 * 128;     // [64 keys][64 d], four of them
+constexpr uint32_t kVQuarter = kKeys * 128;  // [128 keys][64 d], two of them
+constexpr uint32_t kTile = 32768;            // a CTA's half of a tile of K or V
+constexpr uint32_t kOffQ = 0, kOffK = 4 * kQQuarter, kOffV = kOffK + kStages * kTile, kOffMisc = kOffV + kStages * kTile;
+constexpr uint32_t kTmemCols = 512, kColS = 0, kColP = 128, kPBufCols = 64, kColO = 256;
+
+// The cut, in keys: what a block costs a cluster beyond its keys (Q, first softmax, epilogue), the least of a
+// range, and the least tiles of a piece (a shorter one costs more in its merge than it saves).
+constexpr int kFixed = 320, kMinRange = 384, kMinPiece = 2;
+
+struct Item {
+  int q0, n;             // first token of the prompt, its length
+  int tok0;              // the block's first token in the prompt
+  int kvh, kv_end;       // keys [0, kv_end) are seen by the block's last token
+  int t0, t1;            // tiles of this piece
+  int split, nsplit;
+  int slot, slot0, slot1;  // partial slots: this piece's, the first piece's, the second's (the others follow it by 2)
+};
+
+struct Misc {
+  alignas(16) float red[2][2][kRows];  // [tile parity][key half][row] partial maxima
+  alignas(16) float lsum[2][kRows];
+  alignas(16) Item item[kRing];
+  alignas(8) uint64_t item_full[kRing], item_empty[kRing];
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t q_full, q_empty, s_full, s_free, p_full[2], pv_done[2], o_ready, o_free, drain, never;
+  long long scan[kThreads / 32];
+  long long total;
+  long long start_off;   // units before the prompt the range starts in
+  int start_seq;
+  uint32_t tmem_base;
+  int abort_flag, merge_flag;
+};
+constexpr size_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+
+// ------------------------------------------------------------------ cluster-wide instructions --
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of a shared variable of the cluster's CTA 0.
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void arrive_leader(uint32_t leader_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
+}
+// Bounded wait (as mbar_wait) that also acquires what the other CTA's threads released.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((i & 63u) == 0u) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_timer_ns();
+      if (i == 0) t0 = now;
+      else if (now - t0 > kWaitLimitNs) break;
+    }
+  }
+  atomicOr(err, kErrTimeout);
+  *abort_flag = 1;
+  return false;
+}
+__device__ __forceinline__ void alloc2(uint32_t dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc2(uint32_t taddr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on `bar` in both CTAs once the products issued so far are done.
+__device__ __forceinline__ void commit2(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// ------------------------------------------------------------------------------------ the cut --
+struct Shape {
+  int tb;      // tokens of a block (both CTAs)
+  int blocks;  // of a prompt and kv head
+};
+__device__ __forceinline__ int blocks_of(int n, int tb) { return (n + tb - 1) / tb; }
+// Units of a prompt's first b blocks (of one kv head).
+__device__ __forceinline__ long long units(long long b, int tb) { return b * kFixed + tb * (b * (b + 1) / 2); }
+
+// Length of prompt s; one that does not lie in [0, T) has none and is flagged by the first CTA.
+__device__ __forceinline__ int prompt_len(const PromptArgs& a, int s, int* q0) {
+  const int x = a.qsl[s], y = a.qsl[s + 1];
+  *q0 = x;
+  if (x < 0 || y < x || y > a.T) {
+    if (blockIdx.x == 0) atomicOr(a.err, kErrBounds);
+    return 0;
+  }
+  return y - x;
+}
+
+// First tile of the range that begins at unit x of a block's span (x < 0: the whole block is later).
+__device__ __forceinline__ int cut_tile(long long x, int tiles) {
+  if (x <= kFixed) return 0;
+  const long long t = (x - kFixed + kKeys / 2) / kKeys;
+  return t < kMinPiece ? 0 : t > tiles - kMinPiece ? tiles : (int)t;
+}
+
+}  // namespace
+
+template <bool kF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                 const __grid_constant__ CUtensorMap tmap_v, PromptArgs a, PromptScratch ws) {
+  constexpr float kSigma = kF16 ? 4.f : 0.f;  // P is stored times 2^kSigma (f16 has few small values; at most 2^12)
+  constexpr uint32_t kIdescS = kF16 ? idesc_f16(256, 128, false, false) : idesc_bf16(256, 128, false, false);
+  constexpr uint32_t kIdescO = kF16 ? idesc_f16(256, 256, false, true) : idesc_bf16(256, 256, false, true);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Misc& ms = *reinterpret_cast<Misc*>(smem + kOffMisc);
+  const uint32_t sbase = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cta_rank(), cluster = (int)(blockIdx.x >> 1);
+  volatile int* abort_flag = &ms.abort_flag;
+  auto bar = [&](const uint64_t& b) { return smem_u32(&b); };
+  const int tpc = kRows / a.G, tb = 2 * tpc;  // tokens of a CTA, of a block
+  const int used = tpc * a.G;                 // rows of a CTA that hold tokens
+
+  if (tid == 0) {
+    const int both = rank == 0 ? 2 : 1;  // the leader's Q and K are full once the other CTA's are, too
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(bar(ms.item_full[i]), 1);
+      mbar_init(bar(ms.item_empty[i]), kSoftWarps + 3);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(ms.k_full[i]), both);
+      mbar_init(bar(ms.k_empty[i]), 1);
+      mbar_init(bar(ms.v_full[i]), 1);
+      mbar_init(bar(ms.v_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(ms.p_full[i]), 2 * kSoftWarps);
+      mbar_init(bar(ms.pv_done[i]), 1);
+    }
+    mbar_init(bar(ms.q_full), both);
+    mbar_init(bar(ms.q_empty), 1);
+    mbar_init(bar(ms.s_full), 1);
+    mbar_init(bar(ms.s_free), 2 * kSoftWarps);
+    mbar_init(bar(ms.o_ready), 1);
+    mbar_init(bar(ms.o_free), 2 * kSoftWarps);
+    mbar_init(bar(ms.drain), 1);
+    mbar_init(bar(ms.never), 1);
+    ms.abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  if (warp == 0) alloc2(smem_u32(&ms.tmem_base), kTmemCols);
+  // rows of Q that no token has: zeros, once
+  for (int i = tid; i < (kRows - used) * 32; i += kThreads) {
+    const int qd = i & 3, c = (i >> 2) & 7, r = used + (i >> 5);
+    *reinterpret_cast<uint4*>(smem + kOffQ + qd * kQQuarter + r * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  // the units of all prompts, and the prompt this cluster's range starts in: each thread a run of prompts
+  const int per = (a.num_seqs + kThreads - 1) / kThreads;
+  const int s0 = min(tid * per, a.num_seqs), s1 = min(s0 + per, a.num_seqs);
+  long long sum = 0;
+  for (int s = s0; s < s1; ++s) {
+    int q0;
+    sum += a.Hkv * units(blocks_of(prompt_len(a, s, &q0), tb), tb);
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) ms.scan[warp] = incl;
+  if (tid == 0) ms.start_seq = -1;
+  tc_fence_before();
+  __syncthreads();
+  long long before = incl - sum, U = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += ms.scan[w];
+    U += ms.scan[w];
+  }
+  const int C = (int)max(1LL, min((long long)(gridDim.x >> 1), U / kMinRange));
+  const bool work = cluster < C && U > 0;
+  const long long u0 = work ? range_begin(cluster, U, C) : 0, u1 = work ? range_begin(cluster + 1, U, C) : 0;
+  if (work && before <= u0 && u0 < before + sum) {
+    for (int s = s0; s < s1; ++s) {
+      int q0;
+      const long long c = a.Hkv * units(blocks_of(prompt_len(a, s, &q0), tb), tb);
+      if (u0 < before + c) {
+        ms.start_seq = s;
+        ms.start_off = before;
+        break;
+      }
+      before += c;
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // barriers, TMEM and the start are there in both CTAs
+  tc_fence_after();
+  const uint32_t tmem = ms.tmem_base;
+
+  if (work) {
+    // The ring: consumers read item i from entry i % kRing.
+    auto take = [&](int i, Item& I) -> bool {
+      const bool ok = mbar_wait(bar(ms.item_full[i % kRing]), (i / kRing) & 1, abort_flag, a.err);
+      I = ms.item[i % kRing];
+      return ok;
+    };
+    auto give = [&](int i) { mbar_arrive(bar(ms.item_empty[i % kRing])); };
+
+    if (warp == 2) {
+      // ------------------------------------------------------------ the items, and their Q
+      if (lane == 0) {
+        tma_prefetch_desc(&tmap_q);
+        const uint64_t policy = policy_evict_first();
+        int s = ms.start_seq, q0, n = prompt_len(a, s, &q0), nb = blocks_of(n, tb);
+        long long off = u0 - ms.start_off;
+        const long long head_units = units(nb, tb);
+        int kvh = (int)(off / head_units), b = 0;
+        off -= kvh * head_units;
+        for (int step = 1 << 30; step; step >>= 1)  // the last block that begins at or before off
+          if (b + step < nb && units(b + step, tb) <= off) b += step;
+        long long u = u0 - off + units(b, tb);  // the block's first unit
+        int i = 0;
+        bool ok = true;
+        while (ok && u < u1) {
+          const int kv_end = min(n, (b + 1) * tb), tiles = (kv_end + kKeys - 1) / kKeys;
+          const long long next = u + kFixed + (long long)(b + 1) * tb;
+          auto first_tile = [&](int c) { return cut_tile(range_begin(c, U, C) - u, tiles); };
+          Item I;
+          I.t0 = u < u0 ? first_tile(cluster) : 0;
+          I.t1 = next > u1 ? first_tile(cluster + 1) : tiles;
+          if (I.t0 < I.t1) {
+            int c0 = cta_of(u, U, C), c1 = cta_of(next - 1, U, C);
+            while (c0 < c1 && first_tile(c0 + 1) == 0) ++c0;
+            while (c1 > c0 && first_tile(c1) == tiles) --c1;
+            I.q0 = q0;
+            I.n = n;
+            I.tok0 = b * tb;
+            I.kvh = kvh;
+            I.kv_end = kv_end;
+            I.split = cluster - c0;
+            I.nsplit = c1 - c0 + 1;
+            // a cluster has at most one piece that continues a block (slot 2c) and one that begins one (2c + 1)
+            I.slot0 = 2 * c0 + (range_begin(c0, U, C) <= u ? 1 : 0);
+            I.slot1 = 2 * (c0 + 1);
+            I.slot = I.split == 0 ? I.slot0 : I.slot1 + 2 * (I.split - 1);
+            if (i >= kRing) ok = mbar_wait(bar(ms.item_empty[i % kRing]), ((i / kRing) - 1) & 1, abort_flag, a.err);
+            if (!ok) break;
+            ms.item[i % kRing] = I;
+            mbar_arrive(bar(ms.item_full[i % kRing]));
+            if (i >= 1) ok = mbar_wait(bar(ms.q_empty), (i - 1) & 1, abort_flag, a.err);
+            if (!ok) break;
+            mbar_expect_tx(bar(ms.q_full), (uint32_t)used * 512u);
+            for (int qd = 0; qd < 4; ++qd)
+              tma_load_3d(sbase + kOffQ + qd * kQQuarter, &tmap_q, qd * 64, kvh * a.G, q0 + I.tok0 + rank * tpc, bar(ms.q_full), policy);
+            ++i;
+          }
+          u = next;
+          if (++b == nb) {
+            b = 0;
+            if (++kvh == a.Hkv) {
+              kvh = 0;
+              do {
+                if (++s >= a.num_seqs) break;
+                n = prompt_len(a, s, &q0);
+                nb = blocks_of(n, tb);
+              } while (n == 0);
+              if (s >= a.num_seqs) break;
+            }
+          }
+        }
+        // the end of the items
+        if (ok && i >= kRing) ok = mbar_wait(bar(ms.item_empty[i % kRing]), ((i / kRing) - 1) & 1, abort_flag, a.err);
+        if (ok) {
+          ms.item[i % kRing].nsplit = 0;
+          mbar_arrive(bar(ms.item_full[i % kRing]));
+        }
+        // the copies have landed before the CTA may exit (the leader's barrier waits for the other CTA's too;
+        // it gives up when that one has)
+        if (i >= 1) mbar_drain(bar(ms.q_full), (i - 1) & 1, abort_flag, a.err);
+      }
+    } else if (warp == 0 || warp == 1) {
+      // ------------------------------------------------------------ K (warp 0) and V (warp 1)
+      if (lane == 0) {
+        const bool is_k = warp == 0;
+        const CUtensorMap* tmap = is_k ? &tmap_k : &tmap_v;
+        uint64_t* full = is_k ? ms.k_full : ms.v_full;
+        uint64_t* empty = is_k ? ms.k_empty : ms.v_empty;
+        const uint32_t region = sbase + (is_k ? kOffK : kOffV);
+        tma_prefetch_desc(tmap);
+        const uint64_t policy = policy_evict_last();  // every block of a prompt reads them again
+        uint32_t g = 0;
+        bool ok = true;
+        Item I;
+        for (int i = 0; ok; ++i) {
+          if (!(ok = take(i, I)) || I.nsplit == 0) break;
+          for (int t = I.t0; t < I.t1; ++t, ++g) {
+            const uint32_t st = g % kStages;
+            if (g >= kStages && !(ok = mbar_wait(bar(empty[st]), ((g / kStages) - 1) & 1, abort_flag, a.err))) break;
+            mbar_expect_tx(bar(full[st]), kTile);
+            const uint32_t dst = region + st * kTile;
+            const int key = I.q0 + t * kKeys;
+            if (is_k) {
+              for (int qd = 0; qd < 4; ++qd)
+                tma_load_3d(dst + qd * kKQuarter, tmap, qd * 64, I.kvh, key + rank * 64, bar(full[st]), policy);
+            } else {
+              for (int qd = 0; qd < 2; ++qd)
+                tma_load_3d(dst + qd * kVQuarter, tmap, rank * 128 + qd * 64, I.kvh, key, bar(full[st]), policy);
+            }
+          }
+          if (ok) give(i);
+        }
+        for (uint32_t st = 0; st < kStages; ++st) {  // every copy has landed before the CTA may exit
+          if (g <= st) continue;
+          const uint32_t last = (g - 1 - st) / kStages;  // the last use of the stage
+          mbar_drain(bar(full[st]), last & 1, abort_flag, a.err);
+        }
+      }
+    } else if (warp == 3 && rank != 0) {
+      // ------------------------------------------------------------ the other CTA's relay
+      if (lane == 0) {
+        const uint32_t q_leader = in_leader(bar(ms.q_full));
+        uint32_t k_leader[kStages];
+        for (int st = 0; st < kStages; ++st) k_leader[st] = in_leader(bar(ms.k_full[st]));
+        uint32_t g = 0;
+        bool ok = true;
+        Item I;
+        for (int i = 0; ok; ++i) {
+          if (!(ok = take(i, I)) || I.nsplit == 0) break;
+          if (!(ok = mbar_wait(bar(ms.q_full), i & 1, abort_flag, a.err))) break;
+          arrive_leader(q_leader);
+          for (int t = I.t0; t < I.t1; ++t, ++g) {
+            const uint32_t st = g % kStages;
+            if (!(ok = mbar_wait(bar(ms.k_full[st]), (g / kStages) & 1, abort_flag, a.err))) break;
+            arrive_leader(k_leader[st]);
+          }
+          if (ok) give(i);
+        }
+      }
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ the leader's products
+      // The lanes of the warp agree on every wait: the ones that see an abort and those that do not must not part.
+      uint32_t g = 0;
+      bool ok = true;
+      Item I;
+      auto waited = [&](const uint64_t& b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait_cluster(bar(b), parity, abort_flag, a.err));
+      };
+      auto pv = [&](uint32_t gg, bool first, bool last, int i) -> bool {
+        const uint32_t st = gg % kStages, b = gg & 1;
+        // the first P.V of an item overwrites O: both CTAs' epilogues of the one before must be done
+        if (first && i >= 1 && !waited(ms.o_free, (i - 1) & 1)) return false;
+        if (!waited(ms.p_full[b], (gg >> 1) & 1)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          // V as one N = 256 MN-major operand, 128 of d in each CTA: 64-element atoms 16 KB apart, 8-key
+          // groups 1 KB apart, 16 keys (2 KB) per instruction
+          const uint64_t v0 = smem_desc(sbase + kOffV + st * kTile, kVQuarter, 1024, kSw128);
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma2_ts(tmem + kColO, tmem + kColP + b * kPBufCols + kk * 8, v0 + ((kk * 2048) >> 4), kIdescO, first && kk == 0 ? 0u : 1u);
+          commit2(bar(ms.v_empty[st]));
+          commit2(bar(ms.pv_done[b]));
+          if (last) commit2(bar(ms.o_ready));
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int i = 0; ok; ++i) {
+        if (!(ok = __all_sync(0xffffffffu, take(i, I))) || I.nsplit == 0) break;
+        const int nt = I.t1 - I.t0;
+        for (int j = 0; j < nt && ok; ++j, ++g) {
+          const uint32_t st = g % kStages;
+          if (j == 0 && !(ok = waited(ms.q_full, i & 1))) break;
+          if (!(ok = waited(ms.k_full[st], (g / kStages) & 1))) break;
+          if (g >= 1 && !(ok = waited(ms.s_free, (g - 1) & 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int qd = 0; qd < 4; ++qd) {
+              const uint64_t q0 = smem_desc(sbase + kOffQ + qd * kQQuarter, 16, 1024, kSw128);
+              const uint64_t k0 = smem_desc(sbase + kOffK + st * kTile + qd * kKQuarter, 16, 1024, kSw128);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)  // 16 values (32 bytes) of d per instruction
+                mma2(tmem + kColS, q0 + ((k * 32) >> 4), k0 + ((k * 32) >> 4), kIdescS, (qd | k) ? 1u : 0u);
+            }
+            commit2(bar(ms.s_full));
+            commit2(bar(ms.k_empty[st]));
+            if (j == nt - 1) commit2(bar(ms.q_empty));
+          }
+          __syncwarp();
+          if (j >= 1) ok = pv(g - 1, j == 1, false, i);
+        }
+        if (ok) ok = pv(g - 1, nt == 1, true, i);
+        if (ok && lane == 0) give(i);
+      }
+      // every product has completed before either CTA may give its TMEM back
+      if (elect_one()) commit2(bar(ms.drain));
+      __syncwarp();
+    } else if (warp >= kSoftWarp0) {
+      // ------------------------------------------------------------ softmax and epilogue
+      const int sw = warp - kSoftWarp0, gi = sw * 32 + lane;
+      const int q4 = warp & 3, kh = sw >> 2;  // TMEM lane quarter; key half of the tile, d half of O
+      const int row = q4 * 32 + lane;
+      const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
+      const int pair_bar = 1 + q4;            // named barrier of the two warps that share these rows
+      const uint32_t s_free = in_leader(bar(ms.s_free)), o_free = in_leader(bar(ms.o_free));
+      const uint32_t p_full[2] = {in_leader(bar(ms.p_full[0])), in_leader(bar(ms.p_full[1]))};
+      const float c = a.score_scale_log2;
+      const bool c_pos = c >= 0.f;
+      const int my_t = row / a.G, my_g = row - my_t * a.G;
+      uint32_t g = 0;
+      // failure-path test: a bounded wait on a barrier nothing arrives on
+      const bool stalled = a.stall_test_ns && !mbar_wait(bar(ms.never), 0, abort_flag, a.err, a.stall_test_ns);
+      // This call's counter tag (thread 0 uses it).
+      const unsigned long long tag = (__ldcg(ws.epoch) ^ ((unsigned long long)ws.call_tag * 0x9E3779B97F4A7C15ull)) & kSplitTagMask;
+      Item I;
+      for (int i = 0; !stalled; ++i) {
+        // All softmax threads leave together (they meet at barriers). A failed wait inside an item does not
+        // leave it: the later ones then fail at once.
+        if (barrier_or(10, kSoftThreads, !take(i, I)) || I.nsplit == 0) break;
+        const int first_tok = I.tok0 + rank * tpc;
+        const int tok = first_tok + my_t;                 // this row's token
+        const bool valid = row < used && tok < I.n;
+        float m_ref = kMInit, l = 0.f;
+        const int nt = I.t1 - I.t0;
+        for (int j = 0; j < nt; ++j, ++g) {
+          const uint32_t b = g & 1, st = g % kStages;
+          const int key0 = (I.t0 + j) * kKeys, kbase = key0 + kh * 64;
+          float t[64];
+          mbar_wait(bar(ms.s_full), g & 1, abort_flag, a.err);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 64; k += 16) {
+            float v[16];
+            tmem_ld16(tmem + lane_addr + kColS + kh * 64 + k, v);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) t[k + x] = v[x];
+          }
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader(s_free);  // S may be overwritten
+          const bool need_mask = key0 + kKeys - 1 > first_tok;
+          float mx;
+          if (need_mask) {
+#pragma unroll
+            for (int x = 0; x < 64; ++x) t[x] = kbase + x <= tok ? t[x] * c : -INFINITY;
+            mx = extreme_of<true>(t);
+          } else {
+            mx = (c_pos ? extreme_of<true>(t) : extreme_of<false>(t)) * c;
+          }
+          ms.red[b][kh][row] = mx;
+          named_barrier(pair_bar, 64);
+          const float mt = fmaxf(mx, ms.red[b][kh ^ 1][row]);
+          float alpha = 1.f;
+          const bool rescale = mt > m_ref + kTau;
+          if (rescale) {
+            alpha = ex2(m_ref - mt);
+            m_ref = mt;
+            l *= alpha;
+          }
+          const float off = m_ref - kSigma, sc = need_mask ? 1.f : c;
+          uint32_t pk[32];
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            const float p0 = ex2(fmaf(t[x], sc, -off)), p1 = ex2(fmaf(t[x + 1], sc, -off));
+            ls[(x >> 1) & 3] += p0 + p1;  // (the sums take P before its rounding: lse needs more than P.V does)
+            pk[x / 2] = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+          // tcgen05.ld/st are warp-wide: a warp rescales if any of its rows must
+          if (__any_sync(0xffffffffu, rescale && j > 0)) {
+            mbar_wait(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, a.err);
+            tc_fence_after();
+            if (!rescale) alpha = 1.f;
+#pragma unroll 1
+            for (int k = 0; k < 128; k += 16) {  // this thread's half of its row of O
+              float v[16];
+              const uint32_t at = tmem + lane_addr + kColO + kh * 128 + k;
+              tmem_ld16(at, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) v[x] *= alpha;
+              tmem_st16(at, v);
+            }
+            tmem_wait_st();
+          }
+          // P.V(g - 2) has read P buffer b; its next phase needs P(g)
+          if (g >= 2) mbar_wait(bar(ms.pv_done[b]), ((g >> 1) - 1) & 1, abort_flag, a.err);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t w[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) w[x] = pk[16 * k + x];
+            tmem_st16u(tmem + lane_addr + kColP + b * kPBufCols + kh * 32 + 16 * k, w);
+          }
+          // This CTA's half of V has landed: P's arrival tells the leader so.
+          mbar_wait(bar(ms.v_full[st]), (g / kStages) & 1, abort_flag, a.err);
+          if (key0 + row >= I.kv_end) {
+            // keys behind the block's last token (other prompts', later ones'): their V becomes zeros;
+            // thread (kh, row) zeroes d-quarter kh of key `row`
+            uint4* dst = reinterpret_cast<uint4*>(smem + kOffV + st * kTile + kh * kVQuarter + row * 128);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) dst[x] = make_uint4(0, 0, 0, 0);
+          }
+          tmem_wait_st();
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader(p_full[b]);
+        }
+        // ---------------------------------------------------------- epilogue
+        mbar_wait(bar(ms.o_ready), i & 1, abort_flag, a.err);
+        tc_fence_after();
+        ms.lsum[kh][row] = l;
+        named_barrier(pair_bar, 64);
+        const float lr = l + ms.lsum[kh ^ 1][row];
+        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        const float lse = lr > 0.f ? m_ref - kSigma + log2f(lr) : -INFINITY;
+        const bool split = I.nsplit > 1;
+        const int head = I.kvh * a.G + my_g;
+        uint16_t* dst = a.out + (long long)(I.q0 + tok) * a.o_st + (long long)head * a.o_sh + kh * 128;
+        float* part = ws.part_o + ((size_t)(2 * I.slot + rank) * kRows + row) * kHeadDim + kh * 128;
+#pragma unroll 1
+        for (int k = 0; k < 128; k += 16) {
+          float v[16];
+          tmem_ld16(tmem + lane_addr + kColO + kh * 128 + k, v);
+          tmem_wait_ld();
+          if (!valid) continue;
+#pragma unroll
+          for (int x = 0; x < 16; ++x) v[x] *= inv;
+          if (split) {
+#pragma unroll
+            for (int x = 0; x < 16; x += 4) *reinterpret_cast<float4*>(part + k + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16; x += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = kF16 ? pack_f16x2(v[x + 2 * y], v[x + 2 * y + 1]) : pack_bf16x2(v[x + 2 * y], v[x + 2 * y + 1]);
+              *reinterpret_cast<uint4*>(dst + k + x) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(o_free);
+        if (!split) {
+          if (a.lse && valid && kh == 0)
+            a.lse[(long long)(I.q0 + tok) * a.lse_st + (long long)head * a.lse_sh] = lse * 0.6931471805599453f;
+        } else {
+          if (valid && kh == 0) ws.part_lse[(size_t)(2 * I.slot + rank) * kRows + row] = lse;
+          __threadfence();
+          named_barrier(9, kSoftThreads);
+          if (gi == 0) {
+            __threadfence();
+            ms.merge_flag = split_arrive(ws.counters + 2 * I.slot0 + rank, I.nsplit, tag);
+            __threadfence();
+          }
+          named_barrier(9, kSoftThreads);
+          if (ms.merge_flag) {
+            // out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M), a warp per row
+            __threadfence();
+            const int rows = min(used, (I.n - first_tok) * a.G);
+            for (int r = sw; r < rows; r += kSoftWarps) {
+              float M = -INFINITY;
+              for (int x = 0; x < I.nsplit; ++x)
+                M = fmaxf(M, __ldcg(ws.part_lse + (size_t)(2 * (x ? I.slot1 + 2 * (x - 1) : I.slot0) + rank) * kRows + r));
+              float total = 0.f, acc[8] = {};
+              for (int x = 0; x < I.nsplit; ++x) {
+                const size_t at = (size_t)(2 * (x ? I.slot1 + 2 * (x - 1) : I.slot0) + rank) * kRows + r;
+                const float w = exp2f(__ldcg(ws.part_lse + at) - M);
+                const float4* o = reinterpret_cast<const float4*>(ws.part_o + at * kHeadDim + lane * 8);
+                const float4 lo = __ldcg(o), hi = __ldcg(o + 1);
+                total += w;
+                acc[0] += w * lo.x;
+                acc[1] += w * lo.y;
+                acc[2] += w * lo.z;
+                acc[3] += w * lo.w;
+                acc[4] += w * hi.x;
+                acc[5] += w * hi.y;
+                acc[6] += w * hi.z;
+                acc[7] += w * hi.w;
+              }
+              const float scale = 1.f / total;  // (a token sees itself: some piece has weight 1)
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = kF16 ? pack_f16x2(acc[2 * y] * scale, acc[2 * y + 1] * scale) : pack_bf16x2(acc[2 * y] * scale, acc[2 * y + 1] * scale);
+              const int t = r / a.G, h = I.kvh * a.G + r - t * a.G;
+              const long long token = I.q0 + first_tok + t;
+              *reinterpret_cast<uint4*>(a.out + token * a.o_st + (long long)h * a.o_sh + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+              if (a.lse && lane == 0) a.lse[token * a.lse_st + (long long)h * a.lse_sh] = (M + log2f(total)) * 0.6931471805599453f;
+            }
+            named_barrier(9, kSoftThreads);
+          }
+        }
+        if (lane == 0) give(i);
+      }
+    }
+    // both CTAs wait for the leader's products (also after an abort)
+    __syncwarp();
+    if (warp == kSoftWarp0 && lane == 0) mbar_drain(bar(ms.drain), 0, abort_flag, a.err);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while the other may still arrive on its barriers
+  if (warp == 0) {
+    tc_fence_after();
+    dealloc2(tmem, kTmemCols);
+  }
+}
+
+namespace {
+
+__global__ void prompt_epoch_kernel(unsigned long long* epoch) { *epoch += 1ull; }
+
+bool encode(CUtensorMap* m, const void* data, bool f16, int heads, int T, long long sh, long long st, int box_heads, int box_tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)T};
+  // (a dim of one entry has no stride that matters)
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? sh * 2 : 512), (cuuint64_t)(T > 1 ? st * 2 : 512)};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  return encode_tmap(m, f16, 3, data, dims, strides, box);
+}
+
+}  // namespace
+
+int launch_prompt_tc(const PromptArgs& a, const PromptScratch& ws, int clusters, bool captured, cudaStream_t stream) {
+  const long long strides[6] = {a.Hq > 1 ? a.q_sh : 1, a.T > 1 ? a.q_st : 1, a.Hkv > 1 ? a.k_sh : 1,
+                                a.T > 1 ? a.k_st : 1, a.Hkv > 1 ? a.v_sh : 1, a.T > 1 ? a.v_st : 1};
+  for (long long s : strides)
+    if (s <= 0 || s >= 1LL << 38) return 0;  // what a tensor map cannot say (2^40 bytes): the warp-level kernel
+  CUtensorMap q, k, v;
+  const int tpc = kRows / a.G;
+  if (!encode(&q, a.q, a.f16, a.Hq, a.T, a.q_sh, a.q_st, a.G, tpc) || !encode(&k, a.k, a.f16, a.Hkv, a.T, a.k_sh, a.k_st, 1, 64) ||
+      !encode(&v, a.v, a.f16, a.Hkv, a.T, a.v_sh, a.v_st, 1, kKeys))
+    return -1;
+  auto kern = a.f16 ? prompt_tc_kernel<true> : prompt_tc_kernel<false>;
+  static int attr_done[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e = cudaSuccess;
+  const int which = a.f16 ? 2 : 1;
+  if (dev < 0 || dev >= 64 || !(attr_done[dev] & which)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) attr_done[dev] |= which;
+  }
+  // A graph replays its captured tag: the workspace's epoch word tells the replays apart.
+  if (e == cudaSuccess && captured) {
+    prompt_epoch_kernel<<<1, 1, 0, stream>>>(ws.epoch);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = launch_pdl(false, kern, 2 * clusters, kThreads, kSmemBytes, stream, q, k, v, a, ws);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    char buf[160];
+    snprintf(buf, sizeof buf, "prompt kernel: %s", cudaGetErrorString(e));
+    set_tc_error(buf);
+    return -1;
+  }
+  return 1;
+}
+
+// Clusters that a call of these sizes can use: its units, were all tokens one prompt's, over the least range.
+int prompt_clusters(long long T, int num_seqs, int Hkv, int G, int sms) {
+  const int tb = 2 * (kRows / G);
+  const double b = (double)((T + tb - 1) / tb) + num_seqs;
+  const double most = Hkv * (b * kFixed + tb * b * (b + 1) / 2) / kMinRange;
+  const int all = sms / 2;
+  return most < 1 ? 1 : most < all ? (int)most : all;
+}
+
+}  // namespace pgqa

@@ -75,6 +75,26 @@ bool encode_cache_tmap(CUtensorMap* m, const pg_tensor* t, int P);
 
 }  // namespace
 
+bool encode_tmap(CUtensorMap* m, bool f16, int rank, const void* data, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) {
+    set_tc_error("cuTensorMapEncodeTiled unavailable");
+    return false;
+  }
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+                        const_cast<void*>(data), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char buf[96];
+    snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    set_tc_error(buf);
+    return false;
+  }
+  return true;
+}
+
 // 4-D map over a cache [NB, P, Hkv, 256] (see encode_cache_tmap), from the cache of
 // recent maps when the same tensor view was seen before.
 bool make_cache_tmap(CUtensorMap* m, const pg_tensor* t, int P) {

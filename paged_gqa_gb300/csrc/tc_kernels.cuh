@@ -33,6 +33,9 @@ int launch_fp4_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, in
 int launch_fp4_decode(const Problem& p, const Pointers& ptr, const ClassPlan& cp, cudaStream_t stream);
 const char* tc_last_error();
 void set_tc_error(const char* msg);
+// TMA map of bf16 or f16 values, 128-byte swizzle; strides in bytes, of all dims but the first.
+bool encode_tmap(CUtensorMap* m, bool f16, int rank, const void* data, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box);
 // TMA map over an e4m3 or bf16 cache [NB, P, Hkv, 256] (128 bytes of d of one page per box).
 bool make_cache_tmap(CUtensorMap* m, const pg_tensor* t, int P);
 

@@ -22,8 +22,10 @@ def test_prompts(path, case, dtype):
     prev = pg.paged_gqa_set_path(path)
     try:
         out, lse = x.run()
+        bits = pg.paged_gqa_last_plan()["path_bits"]
     finally:
         pg.paged_gqa_set_path(prev)
+    assert bits == (512 if path == 1 else 256)
     x.check(out, lse)
 
 
@@ -68,3 +70,107 @@ def test_bad_starts_are_flagged():
     x.qsl_t = torch.tensor([0, 60, 50], dtype=torch.int32, device="cuda")
     x.run(check=False)
     assert pg.paged_gqa_check_device_errors() == -5
+
+
+def test_tokens_that_share_their_memory():
+    """k and v of one token for all (stride 0, no tensor map for that): the warp-level kernel."""
+    x = su.Prompt([40], 4, 1, seed=9, fused=False)
+    x.k, x.v = x.k[:1].expand(40, 1, 256), x.v[:1].expand(40, 1, 256)
+    out, lse = x.run()
+    assert pg.paged_gqa_last_plan()["path_bits"] == 512
+    x.check(out, lse)
+
+
+def test_heads_before_tokens():
+    x = su.Prompt([150, 70], 6, 3, seed=10, fused=False)
+    x.q, x.k, x.v = (t.transpose(0, 1).contiguous().transpose(0, 1) for t in (x.q, x.k, x.v))
+    out, lse = x.run()
+    assert pg.paged_gqa_last_plan()["path_bits"] == 256
+    x.check(out, lse)
+
+
+def test_values_beyond_f16_in_split_prompts():
+    x = su.Prompt([3000], 8, 1, seed=12, fused=False)
+    x.v = (x.v.float() * 1e30).bfloat16()
+    out, lse = x.run()
+    x.check(out, lse, rows={0: [0, 500, 1500, 2999]})
+
+
+def test_the_same_bits_again():
+    x = su.Prompt([1900, 700, 33], 8, 2, seed=11)
+    first, lse = x.run()
+    for _ in range(60):
+        out, ls = x.run(check=False)
+        assert torch.equal(out, first) and torch.equal(ls, lse)
+    assert pg.paged_gqa_check_device_errors() == 0
+
+
+def test_two_captured_graphs_with_a_workspace_each():
+    xs = [su.Prompt([1500 + 200 * i, 40], 8, 1, seed=20 + i) for i in range(2)]
+    runs = []
+    for x in xs:
+        ws = torch.empty(pg.paged_gqa_prompt_workspace_size(2, x.T, 8, 1), dtype=torch.uint8, device="cuda")
+        out = torch.empty(x.T, 8, 256, dtype=torch.bfloat16, device="cuda")
+        st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            pg.paged_gqa_attn_prompt_ex(x.q, x.k, x.v, x.qsl_t, x.scale, out, None, ws)
+            st.synchronize()
+            with torch.cuda.graph(g, stream=st):
+                pg.paged_gqa_attn_prompt_ex(x.q, x.k, x.v, x.qsl_t, x.scale, out, None, ws)
+        runs.append((x, g, st, out, ws))
+    for _ in range(5):
+        for _, _, _, out, _ in runs:
+            out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _, g, st, _, _ in runs:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+    for x, _, _, out, _ in runs:
+        x.check(out, None, rows={0: [0, 300, 1499], 1: [0, 39]})
+    assert pg.paged_gqa_check_device_errors() == 0
+
+
+def test_refused_in_a_capture_without_a_workspace():
+    x = su.Prompt([40], 8, 1)
+    out = torch.empty(40, 8, 256, dtype=torch.bfloat16, device="cuda")
+    st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(st), torch.cuda.graph(g, stream=st):
+        with pytest.raises(pg.PagedGQAError, match="paged_gqa_attn_prompt_ex"):
+            pg.paged_gqa_attn_prompt(x.q, x.k, x.v, x.qsl_t, x.scale, out)
+    with pytest.raises(pg.PagedGQAError, match="too small"):
+        pg.paged_gqa_attn_prompt_ex(x.q, x.k, x.v, x.qsl_t, x.scale, out, None, torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def test_two_streams_and_other_calls_share_the_workspace_in_turn():
+    xs = [su.Prompt([2000 - 300 * i, 9], 8, 1, seed=30 + i) for i in range(2)]
+    tree = su.Tree([(13, 4000), (5, 900)], 16, 1, 16, seed=3)
+    outs = [torch.empty(x.T, 8, 256, dtype=torch.bfloat16, device="cuda") for x in xs]
+    tree_out = torch.empty_like(tree.q)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(10):
+        for x, o, st in zip(xs, outs, streams):
+            with torch.cuda.stream(st):
+                pg.paged_gqa_attn_prompt(x.q, x.k, x.v, x.qsl_t, x.scale, o)
+        with torch.cuda.stream(streams[2]):
+            pg.paged_gqa_attn_tree(*tree.args(), tree_out)
+    torch.cuda.synchronize()
+    for x, o in zip(xs, outs):
+        x.check(o, None, rows={0: [0, 1000, 1699], 1: [8]})
+    su.compare(tree_out, tree.reference(), "tree")
+    assert pg.paged_gqa_check_device_errors() == 0
+
+
+def test_a_wait_that_runs_out_reports_timeout_and_the_next_call_is_correct():
+    x = su.Prompt([700, 50], 8, 1, seed=40)
+    prev = pg.paged_gqa_set_stall_test(200_000)
+    try:
+        x.run(check=False)
+        status = pg.paged_gqa_check_device_errors()
+    finally:
+        pg.paged_gqa_set_stall_test(prev)
+    assert status == -4, pg.paged_gqa_last_error()
+    out, lse = x.run()
+    x.check(out, lse)
