@@ -98,6 +98,14 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
 // The address of a shared variable of the cluster's CTA 0.
 __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
   uint32_t r;
@@ -106,6 +114,11 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
 }
 __device__ __forceinline__ void arrive_leader(uint32_t leader_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
+}
+// As arrive_leader for what only TMEM accesses come before (the tcgen05 fences order those): a release at
+// cluster scope waits for the thread's memory accesses, which stalled the softmax warps more than anything else.
+__device__ __forceinline__ void signal_leader(uint32_t leader_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
 }
 // Bounded wait (as mbar_wait) that also acquires what the other CTA's threads released.
 __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
@@ -213,15 +226,16 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
   const int used = tpc * a.G;                 // rows of a CTA that hold tokens
 
   if (tid == 0) {
-    const int both = rank == 0 ? 2 : 1;  // the leader's Q and K are full once the other CTA's are, too
+    const int both = rank == 0 ? 2 : 1;  // the leader's Q, K and V are full once the other CTA's are, too
+    const int relays = rank == 0 ? 1 : 2;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(ms.item_full[i]), 1);
-      mbar_init(bar(ms.item_empty[i]), kSoftWarps + 3);
+      mbar_init(bar(ms.item_empty[i]), kSoftWarps + 2 + relays);  // softmax, K, V, and the products or both relays
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(ms.k_full[i]), both);
       mbar_init(bar(ms.k_empty[i]), 1);
-      mbar_init(bar(ms.v_full[i]), 1);
+      mbar_init(bar(ms.v_full[i]), both);
       mbar_init(bar(ms.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -410,23 +424,54 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       }
     } else if (warp == 3 && rank != 0) {
       // ------------------------------------------------------------ the other CTA's relay
+      // One thread polls what it waits for in turn: K (with each item's Q in front) and V land at their own
+      // times, and neither may hold up the other. (K behind V cost 1100 cycles a tile.)
       if (lane == 0) {
+        struct Stream {
+          int i, left;   // the item, and what of it is still to come (0: the item itself is)
+          uint32_t g;
+          bool q, done;
+        } x[2] = {{0, 0, 0, false, false}, {0, 0, 0, false, false}};
         const uint32_t q_leader = in_leader(bar(ms.q_full));
-        uint32_t k_leader[kStages];
-        for (int st = 0; st < kStages; ++st) k_leader[st] = in_leader(bar(ms.k_full[st]));
-        uint32_t g = 0;
-        bool ok = true;
-        Item I;
-        for (int i = 0; ok; ++i) {
-          if (!(ok = take(i, I)) || I.nsplit == 0) break;
-          if (!(ok = mbar_wait(bar(ms.q_full), i & 1, abort_flag, a.err))) break;
-          arrive_leader(q_leader);
-          for (int t = I.t0; t < I.t1; ++t, ++g) {
-            const uint32_t st = g % kStages;
-            if (!(ok = mbar_wait(bar(ms.k_full[st]), (g / kStages) & 1, abort_flag, a.err))) break;
-            arrive_leader(k_leader[st]);
+        uint64_t t0 = 0;
+        for (uint32_t polls = 0; !(x[0].done && x[1].done); ++polls) {
+          bool moved = false;
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            Stream& r = x[which];
+            if (r.done) continue;
+            uint64_t* full = which == 0 ? ms.k_full : ms.v_full;
+            const uint32_t st = r.g % kStages;
+            if (r.left == 0) {
+              if (!mbar_test(bar(ms.item_full[r.i % kRing]), (r.i / kRing) & 1)) continue;
+              const Item& I = ms.item[r.i % kRing];
+              r.done = I.nsplit == 0;
+              r.left = I.t1 - I.t0;
+              r.q = which == 0;
+            } else if (r.q) {
+              if (!mbar_test(bar(ms.q_full), r.i & 1)) continue;
+              arrive_leader(q_leader);
+              r.q = false;
+            } else {
+              if (!mbar_test(bar(full[st]), (r.g / kStages) & 1)) continue;
+              arrive_leader(in_leader(bar(full[st])));
+              ++r.g;
+              if (--r.left == 0) give(r.i++);
+            }
+            moved = true;
           }
-          if (ok) give(i);
+          if (moved || polls == 0) {
+            t0 = 0;
+          } else if ((polls & 63u) == 0u) {  // bounded, as every wait
+            if (*abort_flag) break;
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
+              atomicOr(a.err, kErrTimeout);
+              *abort_flag = 1;
+              break;
+            }
+          }
         }
       }
     } else if (warp == 3) {
@@ -442,7 +487,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         const uint32_t st = gg % kStages, b = gg & 1;
         // the first P.V of an item overwrites O: both CTAs' epilogues of the one before must be done
         if (first && i >= 1 && !waited(ms.o_free, (i - 1) & 1)) return false;
-        if (!waited(ms.p_full[b], (gg >> 1) & 1)) return false;
+        if (!waited(ms.p_full[b], (gg >> 1) & 1) || !waited(ms.v_full[st], (gg / kStages) & 1)) return false;
         tc_fence_after();
         if (elect_one()) {
           // V as one N = 256 MN-major operand, 128 of d in each CTA: 64-element atoms 16 KB apart, 8-key
@@ -532,7 +577,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_leader(s_free);  // S may be overwritten
+          if (lane == 0) signal_leader(s_free);  // S may be overwritten
           const bool need_mask = key0 + kKeys - 1 > first_tok;
           float mx;
           if (need_mask) {
@@ -589,20 +634,26 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             for (int x = 0; x < 16; ++x) w[x] = pk[16 * k + x];
             tmem_st16u(tmem + lane_addr + kColP + b * kPBufCols + kh * 32 + 16 * k, w);
           }
-          // This CTA's half of V has landed: P's arrival tells the leader so.
-          mbar_wait(bar(ms.v_full[st]), (g / kStages) & 1, abort_flag, a.err);
-          if (key0 + row >= I.kv_end) {
+          const bool tail = key0 + kKeys > I.kv_end;
+          if (tail) {
             // keys behind the block's last token (other prompts', later ones'): their V becomes zeros;
-            // thread (kh, row) zeroes d-quarter kh of key `row`
-            uint4* dst = reinterpret_cast<uint4*>(smem + kOffV + st * kTile + kh * kVQuarter + row * 128);
+            // thread (kh, row) zeroes d-quarter kh of key `row`. This wait skips the phases of other tiles:
+            // V(g - 2) has landed (P.V(g - 2) is done), V(g + 2) comes after P.V(g).
+            mbar_wait(bar(ms.v_full[st]), (g / kStages) & 1, abort_flag, a.err);
+            if (key0 + row >= I.kv_end) {
+              uint4* dst = reinterpret_cast<uint4*>(smem + kOffV + st * kTile + kh * kVQuarter + row * 128);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) dst[x] = make_uint4(0, 0, 0, 0);
+              for (int x = 0; x < 8; ++x) dst[x] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
           }
           tmem_wait_st();
-          fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_leader(p_full[b]);
+          if (lane == 0) {
+            if (tail) arrive_leader(p_full[b]);
+            else signal_leader(p_full[b]);
+          }
         }
         // ---------------------------------------------------------- epilogue
         mbar_wait(bar(ms.o_ready), i & 1, abort_flag, a.err);
@@ -640,7 +691,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader(o_free);
+        if (lane == 0) signal_leader(o_free);
         if (!split) {
           if (a.lse && valid && kh == 0)
             a.lse[(long long)(I.q0 + tok) * a.lse_st + (long long)head * a.lse_sh] = lse * 0.6931471805599453f;
