@@ -22,7 +22,8 @@ struct PromptArgs {
 // Workspace of the tcgen05 kernel: for each cluster two slots (a piece that continues a block, one that begins
 // one) of both CTAs' rows, and the counters of the blocks whose first piece has the slot.
 struct PromptScratch {
-  float* part_o;                // [2 clusters][2][128][256] normalised, fp32 (V may be beyond f16)
+  float* part_o;                // [2 clusters][2][64][128][4]: columns 4 c .. 4 c + 3 of each row, normalised, fp32 (V
+                                // may be beyond f16)
   float* part_lse;              // [2 clusters][2][128], log2 units
   unsigned long long* counters; // [2 clusters][2] (tag << 16) | pieces arrived (see ClassPlan::counters)
   unsigned long long* epoch;

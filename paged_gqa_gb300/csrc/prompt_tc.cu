@@ -78,7 +78,7 @@ struct Misc {
   alignas(16) Item item[kRing];
   alignas(8) uint64_t item_full[kRing], item_empty[kRing];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t q_full, q_empty, s_full, s_free, p_full[2], pv_done[2], o_ready, o_free, drain, never;
+  uint64_t q_full, q_empty, s_full, s_free, p_full[2][2], pv_done[2], o_ready, o_free, drain, never;
   long long scan[kThreads / 32];
   long long total;
   long long start_off;   // units before the prompt the range starts in
@@ -112,35 +112,16 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
+// Between the CTAs of a pair nothing goes through memory that a thread reads: P, S and O lie in TMEM (the tcgen05
+// fences order those), K, V and Q have landed in the shared memory of the SM whose tensor core reads them before
+// their arrival is sent on, and so have the zeros of a tail (proxy fence). So the signals need no order at cluster
+// scope. It is far from free: a release at that scope took 1040 cycles, an acquire 500 to 700 even if the phase
+// had long completed, more than anything else in the kernel.
 __device__ __forceinline__ void arrive_leader(uint32_t leader_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
 }
-// As arrive_leader for what only TMEM accesses come before (the tcgen05 fences order those): a release at
-// cluster scope waits for the thread's memory accesses, which stalled the softmax warps more than anything else.
 __device__ __forceinline__ void signal_leader(uint32_t leader_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
-}
-// Bounded wait (as mbar_wait) that also acquires what the other CTA's threads released.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 0;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 63u) == 0u) {
-      if (*abort_flag) return false;
-      const uint64_t now = global_timer_ns();
-      if (i == 0) t0 = now;
-      else if (now - t0 > kWaitLimitNs) break;
-    }
-  }
-  atomicOr(err, kErrTimeout);
-  *abort_flag = 1;
-  return false;
 }
 __device__ __forceinline__ void alloc2(uint32_t dst, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
@@ -239,7 +220,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       mbar_init(bar(ms.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(ms.p_full[i]), 2 * kSoftWarps);
+      mbar_init(bar(ms.p_full[i][0]), 2 * kSoftWarps);
+      mbar_init(bar(ms.p_full[i][1]), 2 * kSoftWarps);
       mbar_init(bar(ms.pv_done[i]), 1);
     }
     mbar_init(bar(ms.q_full), both);
@@ -481,26 +463,35 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       bool ok = true;
       Item I;
       auto waited = [&](const uint64_t& b, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, wait_cluster(bar(b), parity, abort_flag, a.err));
+        return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, a.err));
       };
       auto pv = [&](uint32_t gg, bool first, bool last, int i) -> bool {
         const uint32_t st = gg % kStages, b = gg & 1;
         // the first P.V of an item overwrites O: both CTAs' epilogues of the one before must be done
         if (first && i >= 1 && !waited(ms.o_free, (i - 1) & 1)) return false;
-        if (!waited(ms.p_full[b], (gg >> 1) & 1) || !waited(ms.v_full[st], (gg / kStages) & 1)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          // V as one N = 256 MN-major operand, 128 of d in each CTA: 64-element atoms 16 KB apart, 8-key
-          // groups 1 KB apart, 16 keys (2 KB) per instruction
-          const uint64_t v0 = smem_desc(sbase + kOffV + st * kTile, kVQuarter, 1024, kSw128);
+        if (!waited(ms.v_full[st], (gg / kStages) & 1)) return false;
+        // P comes in two parts, keys 0-31 and 64-95 of the tile and then the others
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma2_ts(tmem + kColO, tmem + kColP + b * kPBufCols + kk * 8, v0 + ((kk * 2048) >> 4), kIdescO, first && kk == 0 ? 0u : 1u);
-          commit2(bar(ms.v_empty[st]));
-          commit2(bar(ms.pv_done[b]));
-          if (last) commit2(bar(ms.o_ready));
+        for (int h = 0; h < 2; ++h) {
+          if (!waited(ms.p_full[b][h], (gg >> 1) & 1)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            // V as one N = 256 MN-major operand, 128 of d in each CTA: 64-element atoms 16 KB apart, 8-key
+            // groups 1 KB apart, 16 keys (2 KB) per instruction
+            const uint64_t v0 = smem_desc(sbase + kOffV + st * kTile, kVQuarter, 1024, kSw128);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int kk = 2 * h + (x & 1) + (x >> 1) * 4;
+              mma2_ts(tmem + kColO, tmem + kColP + b * kPBufCols + kk * 8, v0 + ((kk * 2048) >> 4), kIdescO, first && kk == 0 ? 0u : 1u);
+            }
+            if (h == 1) {
+              commit2(bar(ms.v_empty[st]));
+              commit2(bar(ms.pv_done[b]));
+              if (last) commit2(bar(ms.o_ready));
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
         return true;
       };
       for (int i = 0; ok; ++i) {
@@ -542,7 +533,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
       const int pair_bar = 1 + q4;            // named barrier of the two warps that share these rows
       const uint32_t s_free = in_leader(bar(ms.s_free)), o_free = in_leader(bar(ms.o_free));
-      const uint32_t p_full[2] = {in_leader(bar(ms.p_full[0])), in_leader(bar(ms.p_full[1]))};
+      const uint32_t p_full = in_leader(bar(ms.p_full[0][0]));  // (the four barriers lie in a row)
       const float c = a.score_scale_log2;
       const bool c_pos = c >= 0.f;
       const int my_t = row / a.G, my_g = row - my_t * a.G;
@@ -574,6 +565,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
 #pragma unroll
             for (int x = 0; x < 16; ++x) t[k + x] = v[x];
           }
+          // P.V(g - 2) has read P buffer b (its barrier's next phase needs P(g)); long since, so the wait costs
+          // nothing but its own latency, which the load above hides
+          if (g >= 2) mbar_wait(bar(ms.pv_done[b]), ((g >> 1) - 1) & 1, abort_flag, a.err);
           tmem_wait_ld();
           tc_fence_before();
           __syncwarp();
@@ -597,16 +591,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             m_ref = mt;
             l *= alpha;
           }
-          const float off = m_ref - kSigma, sc = need_mask ? 1.f : c;
-          uint32_t pk[32];
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int x = 0; x < 64; x += 2) {
-            const float p0 = ex2(fmaf(t[x], sc, -off)), p1 = ex2(fmaf(t[x + 1], sc, -off));
-            ls[(x >> 1) & 3] += p0 + p1;  // (the sums take P before its rounding: lse needs more than P.V does)
-            pk[x / 2] = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-          }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
           // tcgen05.ld/st are warp-wide: a warp rescales if any of its rows must
           if (__any_sync(0xffffffffu, rescale && j > 0)) {
             mbar_wait(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, a.err);
@@ -624,16 +608,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             }
             tmem_wait_st();
           }
-          // P.V(g - 2) has read P buffer b; its next phase needs P(g)
-          if (g >= 2) mbar_wait(bar(ms.pv_done[b]), ((g >> 1) - 1) & 1, abort_flag, a.err);
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t w[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) w[x] = pk[16 * k + x];
-            tmem_st16u(tmem + lane_addr + kColP + b * kPBufCols + kh * 32 + 16 * k, w);
-          }
           const bool tail = key0 + kKeys > I.kv_end;
           if (tail) {
             // keys behind the block's last token (other prompts', later ones'): their V becomes zeros;
@@ -647,12 +621,29 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             }
             fence_proxy_async_smem();
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (tail) arrive_leader(p_full[b]);
-            else signal_leader(p_full[b]);
+          // P = 2^(s c - m + sigma), 32 keys at a time: P.V of the first begins while the second are computed
+          tc_fence_after();
+          const float off = m_ref - kSigma, sc = need_mask ? 1.f : c;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const float p0 = ex2(fmaf(t[32 * h + x], sc, -off)), p1 = ex2(fmaf(t[32 * h + x + 1], sc, -off));
+              ls[(x >> 1) & 3] += p0 + p1;  // (the sums take P before its rounding: lse needs more than P.V does)
+              pk[x / 2] = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            tmem_st16u(tmem + lane_addr + kColP + b * kPBufCols + kh * 32 + 16 * h, pk);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              const uint32_t full = p_full + (2 * b + h) * 8;
+              if (tail) arrive_leader(full);
+              else signal_leader(full);
+            }
           }
         }
         // ---------------------------------------------------------- epilogue
@@ -666,7 +657,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         const bool split = I.nsplit > 1;
         const int head = I.kvh * a.G + my_g;
         uint16_t* dst = a.out + (long long)(I.q0 + tok) * a.o_st + (long long)head * a.o_sh + kh * 128;
-        float* part = ws.part_o + ((size_t)(2 * I.slot + rank) * kRows + row) * kHeadDim + kh * 128;
+        auto part_of = [&](int slot) {  // this thread's half row of a partial: four values every kRows * 4
+          return reinterpret_cast<float4*>(ws.part_o) + (size_t)(2 * slot + rank) * (kHeadDim / 4) * kRows + kh * 32 * kRows + row;
+        };
+        float4* part = part_of(I.slot);
 #pragma unroll 1
         for (int k = 0; k < 128; k += 16) {
           float v[16];
@@ -677,7 +671,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           for (int x = 0; x < 16; ++x) v[x] *= inv;
           if (split) {
 #pragma unroll
-            for (int x = 0; x < 16; x += 4) *reinterpret_cast<float4*>(part + k + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+            for (int x = 0; x < 16; x += 4) part[(k + x) / 4 * kRows] = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
           } else {
 #pragma unroll
             for (int x = 0; x < 16; x += 8) {
@@ -706,38 +700,47 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           }
           named_barrier(9, kSoftThreads);
           if (ms.merge_flag) {
-            // out = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M), a warp per row
+            // out = sum_x 2^(lse_x - M) o_x / sum_x 2^(lse_x - M): each thread its half row, whose values
+            // of 32 lanes lie side by side, 32 columns of two pieces in flight
             __threadfence();
-            const int rows = min(used, (I.n - first_tok) * a.G);
-            for (int r = sw; r < rows; r += kSoftWarps) {
-              float M = -INFINITY;
-              for (int x = 0; x < I.nsplit; ++x)
-                M = fmaxf(M, __ldcg(ws.part_lse + (size_t)(2 * (x ? I.slot1 + 2 * (x - 1) : I.slot0) + rank) * kRows + r));
-              float total = 0.f, acc[8] = {};
-              for (int x = 0; x < I.nsplit; ++x) {
-                const size_t at = (size_t)(2 * (x ? I.slot1 + 2 * (x - 1) : I.slot0) + rank) * kRows + r;
-                const float w = exp2f(__ldcg(ws.part_lse + at) - M);
-                const float4* o = reinterpret_cast<const float4*>(ws.part_o + at * kHeadDim + lane * 8);
-                const float4 lo = __ldcg(o), hi = __ldcg(o + 1);
-                total += w;
-                acc[0] += w * lo.x;
-                acc[1] += w * lo.y;
-                acc[2] += w * lo.z;
-                acc[3] += w * lo.w;
-                acc[4] += w * hi.x;
-                acc[5] += w * hi.y;
-                acc[6] += w * hi.z;
-                acc[7] += w * hi.w;
-              }
+            auto slot_of = [&](int x) { return x == 0 ? I.slot0 : I.slot1 + 2 * (x - 1); };
+            auto lse_of = [&](int x) { return __ldcg(ws.part_lse + (size_t)(2 * slot_of(x) + rank) * kRows + row); };
+            float M = -INFINITY, total = 0.f;
+#pragma unroll 2
+            for (int x = 0; x < I.nsplit; ++x) M = fmaxf(M, lse_of(x));
+#pragma unroll 2
+            for (int x = 0; x < I.nsplit; ++x) total += exp2f(lse_of(x) - M);
+            if (valid) {
               const float scale = 1.f / total;  // (a token sees itself: some piece has weight 1)
-              uint32_t w[4];
+              if (a.lse && kh == 0)
+                a.lse[(long long)(I.q0 + tok) * a.lse_st + (long long)head * a.lse_sh] = (M + log2f(total)) * 0.6931471805599453f;
+#pragma unroll 1
+              for (int k = 0; k < 32; k += 8) {
+                float acc[32] = {};
+#pragma unroll 2
+                for (int x = 0; x < I.nsplit; ++x) {
+                  const float w = exp2f(lse_of(x) - M) * scale;
+                  const float4* o = part_of(slot_of(x)) + k * kRows;
+                  float4 v[8];
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                w[y] = kF16 ? pack_f16x2(acc[2 * y] * scale, acc[2 * y + 1] * scale) : pack_bf16x2(acc[2 * y] * scale, acc[2 * y + 1] * scale);
-              const int t = r / a.G, h = I.kvh * a.G + r - t * a.G;
-              const long long token = I.q0 + first_tok + t;
-              *reinterpret_cast<uint4*>(a.out + token * a.o_st + (long long)h * a.o_sh + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-              if (a.lse && lane == 0) a.lse[token * a.lse_st + (long long)h * a.lse_sh] = (M + log2f(total)) * 0.6931471805599453f;
+                  for (int y = 0; y < 8; ++y) v[y] = __ldcg(o + y * kRows);
+#pragma unroll
+                  for (int y = 0; y < 8; ++y) {
+                    acc[4 * y] += w * v[y].x;
+                    acc[4 * y + 1] += w * v[y].y;
+                    acc[4 * y + 2] += w * v[y].z;
+                    acc[4 * y + 3] += w * v[y].w;
+                  }
+                }
+#pragma unroll
+                for (int y = 0; y < 32; y += 8) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int z = 0; z < 4; ++z)
+                    w[z] = kF16 ? pack_f16x2(acc[y + 2 * z], acc[y + 2 * z + 1]) : pack_bf16x2(acc[y + 2 * z], acc[y + 2 * z + 1]);
+                  *reinterpret_cast<uint4*>(dst + 4 * k + y) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
             }
             named_barrier(9, kSoftThreads);
           }
