@@ -48,7 +48,7 @@ constexpr int kKeys = 128;                   // keys of a tile
 constexpr int kSoftWarp0 = 4, kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
 constexpr int kThreads = kSoftWarp0 * 32 + kSoftThreads;
 constexpr int kStages = 2;                   // of K, and of V
-constexpr int kRing = 2;                     // items known in advance
+constexpr int kRing = 3;                     // items known at a time: one whose epilogue is to come, one at work, the next
 constexpr float kTau = 8.f;                  // a row's reference moves when a score exceeds it by this (log2)
 constexpr float kMInit = -1.0e30f;
 
@@ -86,7 +86,8 @@ struct Misc {
   uint32_t tmem_base;
   int abort_flag, merge_flag;
 };
-constexpr size_t kSmemBytes = kOffMisc + sizeof(Misc) + 1024;
+constexpr uint32_t kOffStage = kOffMisc + (uint32_t)((sizeof(Misc) + 127) / 128 * 128);  // 2 KB per softmax warp
+constexpr size_t kSmemBytes = kOffStage + kSoftWarps * 2048 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // ------------------------------------------------------------------ cluster-wide instructions --
@@ -494,10 +495,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         }
         return true;
       };
+      // The order: S of the next tile, also of the next item, goes before P.V of this one.
+      int nt_before = 0;  // tiles of the item before
       for (int i = 0; ok; ++i) {
-        if (!(ok = __all_sync(0xffffffffu, take(i, I))) || I.nsplit == 0) break;
-        const int nt = I.t1 - I.t0;
-        for (int j = 0; j < nt && ok; ++j, ++g) {
+        if (!(ok = __all_sync(0xffffffffu, take(i, I)))) break;
+        const int nt = I.nsplit == 0 ? 0 : I.t1 - I.t0;
+        for (int j = 0; j < nt; ++j, ++g) {
           const uint32_t st = g % kStages;
           if (j == 0 && !(ok = waited(ms.q_full, i & 1))) break;
           if (!(ok = waited(ms.k_full[st], (g / kStages) & 1))) break;
@@ -518,8 +521,14 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           }
           __syncwarp();
           if (j >= 1) ok = pv(g - 1, j == 1, false, i);
+          else if (i >= 1) ok = pv(g - 1, nt_before == 1, true, i - 1);
+          if (!ok) break;
         }
-        if (ok) ok = pv(g - 1, nt == 1, true, i);
+        if (nt == 0) {  // the end: the last item's last P.V
+          if (i >= 1) ok = pv(g - 1, nt_before == 1, true, i - 1);
+          break;
+        }
+        nt_before = nt;
         if (ok && lane == 0) give(i);
       }
       // every product has completed before either CTA may give its TMEM back
@@ -542,210 +551,239 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
       const bool stalled = a.stall_test_ns && !mbar_wait(bar(ms.never), 0, abort_flag, a.err, a.stall_test_ns);
       // This call's counter tag (thread 0 uses it).
       const unsigned long long tag = (__ldcg(ws.epoch) ^ ((unsigned long long)ws.call_tag * 0x9E3779B97F4A7C15ull)) & kSplitTagMask;
-      Item I;
+      // An item's epilogue comes after the first tile of the next one: its last P.V then runs while these
+      // warps are at work, and the tensor pipe has a product to go on with during the epilogue. What the epilogue
+      // needs of the item is in the ring still; the row's statistics are kept here.
+      float m_ref = kMInit, l = 0.f, m_done = 0.f, l_done = 0.f;
       for (int i = 0; !stalled; ++i) {
         // All softmax threads leave together (they meet at barriers). A failed wait inside an item does not
         // leave it: the later ones then fail at once.
-        if (barrier_or(10, kSoftThreads, !take(i, I)) || I.nsplit == 0) break;
-        const int first_tok = I.tok0 + rank * tpc;
-        const int tok = first_tok + my_t;                 // this row's token
-        const bool valid = row < used && tok < I.n;
-        float m_ref = kMInit, l = 0.f;
-        const int nt = I.t1 - I.t0;
-        for (int j = 0; j < nt; ++j, ++g) {
-          const uint32_t b = g & 1, st = g % kStages;
-          const int key0 = (I.t0 + j) * kKeys, kbase = key0 + kh * 64;
-          float t[64];
-          mbar_wait(bar(ms.s_full), g & 1, abort_flag, a.err);
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 64; k += 16) {
-            float v[16];
-            tmem_ld16(tmem + lane_addr + kColS + kh * 64 + k, v);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) t[k + x] = v[x];
-          }
-          // P.V(g - 2) has read P buffer b (its barrier's next phase needs P(g)); long since, so the wait costs
-          // nothing but its own latency, which the load above hides
-          if (g >= 2) mbar_wait(bar(ms.pv_done[b]), ((g >> 1) - 1) & 1, abort_flag, a.err);
-          tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) signal_leader(s_free);  // S may be overwritten
-          const bool need_mask = key0 + kKeys - 1 > first_tok;
-          float mx;
-          if (need_mask) {
-#pragma unroll
-            for (int x = 0; x < 64; ++x) t[x] = kbase + x <= tok ? t[x] * c : -INFINITY;
-            mx = extreme_of<true>(t);
-          } else {
-            mx = (c_pos ? extreme_of<true>(t) : extreme_of<false>(t)) * c;
-          }
-          ms.red[b][kh][row] = mx;
-          named_barrier(pair_bar, 64);
-          const float mt = fmaxf(mx, ms.red[b][kh ^ 1][row]);
-          float alpha = 1.f;
-          const bool rescale = mt > m_ref + kTau;
-          if (rescale) {
-            alpha = ex2(m_ref - mt);
-            m_ref = mt;
-            l *= alpha;
-          }
-          // tcgen05.ld/st are warp-wide: a warp rescales if any of its rows must
-          if (__any_sync(0xffffffffu, rescale && j > 0)) {
-            mbar_wait(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, a.err);
+        Item I;
+        if (barrier_or(10, kSoftThreads, !take(i, I))) break;
+        const bool end = I.nsplit == 0;
+        const int tok = I.tok0 + rank * tpc + my_t;  // this row's token
+        const int nt = end ? 0 : I.t1 - I.t0;
+        m_ref = kMInit;
+        l = 0.f;
+        for (int j = 0; j < max(nt, 1); ++j) {
+          if (!end) {
+            const uint32_t b = g & 1, st = g % kStages;
+            const int key0 = (I.t0 + j) * kKeys, kbase = key0 + kh * 64;
+            float t[64];
+            mbar_wait(bar(ms.s_full), g & 1, abort_flag, a.err);
             tc_fence_after();
-            if (!rescale) alpha = 1.f;
-#pragma unroll 1
-            for (int k = 0; k < 128; k += 16) {  // this thread's half of its row of O
+#pragma unroll
+            for (int k = 0; k < 64; k += 16) {
               float v[16];
-              const uint32_t at = tmem + lane_addr + kColO + kh * 128 + k;
-              tmem_ld16(at, v);
-              tmem_wait_ld();
+              tmem_ld16(tmem + lane_addr + kColS + kh * 64 + k, v);
 #pragma unroll
-              for (int x = 0; x < 16; ++x) v[x] *= alpha;
-              tmem_st16(at, v);
+              for (int x = 0; x < 16; ++x) t[k + x] = v[x];
             }
-            tmem_wait_st();
-          }
-          const bool tail = key0 + kKeys > I.kv_end;
-          if (tail) {
-            // keys behind the block's last token (other prompts', later ones'): their V becomes zeros;
-            // thread (kh, row) zeroes d-quarter kh of key `row`. This wait skips the phases of other tiles:
-            // V(g - 2) has landed (P.V(g - 2) is done), V(g + 2) comes after P.V(g).
-            mbar_wait(bar(ms.v_full[st]), (g / kStages) & 1, abort_flag, a.err);
-            if (key0 + row >= I.kv_end) {
-              uint4* dst = reinterpret_cast<uint4*>(smem + kOffV + st * kTile + kh * kVQuarter + row * 128);
-#pragma unroll
-              for (int x = 0; x < 8; ++x) dst[x] = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-          // P = 2^(s c - m + sigma), 32 keys at a time: P.V of the first begins while the second are computed
-          tc_fence_after();
-          const float off = m_ref - kSigma, sc = need_mask ? 1.f : c;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[16];
-            float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-              const float p0 = ex2(fmaf(t[32 * h + x], sc, -off)), p1 = ex2(fmaf(t[32 * h + x + 1], sc, -off));
-              ls[(x >> 1) & 3] += p0 + p1;  // (the sums take P before its rounding: lse needs more than P.V does)
-              pk[x / 2] = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-            }
-            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-            tmem_st16u(tmem + lane_addr + kColP + b * kPBufCols + kh * 32 + 16 * h, pk);
-            tmem_wait_st();
+            // P.V(g - 2) has read P buffer b (its barrier's next phase needs P(g)); long since, so the wait costs
+            // nothing but its own latency, which the load above hides
+            if (g >= 2) mbar_wait(bar(ms.pv_done[b]), ((g >> 1) - 1) & 1, abort_flag, a.err);
+            tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-              const uint32_t full = p_full + (2 * b + h) * 8;
-              if (tail) arrive_leader(full);
-              else signal_leader(full);
+            if (lane == 0) signal_leader(s_free);  // S may be overwritten
+            const bool need_mask = key0 + kKeys - 1 > I.tok0 + rank * tpc;
+            float mx;
+            if (need_mask) {
+#pragma unroll
+              for (int x = 0; x < 64; ++x) t[x] = kbase + x <= tok ? t[x] * c : -INFINITY;
+              mx = extreme_of<true>(t);
+            } else {
+              mx = (c_pos ? extreme_of<true>(t) : extreme_of<false>(t)) * c;
             }
-          }
-        }
-        // ---------------------------------------------------------- epilogue
-        mbar_wait(bar(ms.o_ready), i & 1, abort_flag, a.err);
-        tc_fence_after();
-        ms.lsum[kh][row] = l;
-        named_barrier(pair_bar, 64);
-        const float lr = l + ms.lsum[kh ^ 1][row];
-        const float inv = lr > 0.f ? 1.f / lr : 0.f;
-        const float lse = lr > 0.f ? m_ref - kSigma + log2f(lr) : -INFINITY;
-        const bool split = I.nsplit > 1;
-        const int head = I.kvh * a.G + my_g;
-        uint16_t* dst = a.out + (long long)(I.q0 + tok) * a.o_st + (long long)head * a.o_sh + kh * 128;
-        auto part_of = [&](int slot) {  // this thread's half row of a partial: four values every kRows * 4
-          return reinterpret_cast<float4*>(ws.part_o) + (size_t)(2 * slot + rank) * (kHeadDim / 4) * kRows + kh * 32 * kRows + row;
-        };
-        float4* part = part_of(I.slot);
+            ms.red[b][kh][row] = mx;
+            named_barrier(pair_bar, 64);
+            const float mt = fmaxf(mx, ms.red[b][kh ^ 1][row]);
+            float alpha = 1.f;
+            const bool rescale = mt > m_ref + kTau;
+            if (rescale) {
+              alpha = ex2(m_ref - mt);
+              m_ref = mt;
+              l *= alpha;
+            }
+            // tcgen05.ld/st are warp-wide: a warp rescales if any of its rows must
+            if (__any_sync(0xffffffffu, rescale && j > 0)) {
+              mbar_wait(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, a.err);
+              tc_fence_after();
+              if (!rescale) alpha = 1.f;
 #pragma unroll 1
-        for (int k = 0; k < 128; k += 16) {
-          float v[16];
-          tmem_ld16(tmem + lane_addr + kColO + kh * 128 + k, v);
-          tmem_wait_ld();
-          if (!valid) continue;
+              for (int k = 0; k < 128; k += 16) {  // this thread's half of its row of O
+                float v[16];
+                const uint32_t at = tmem + lane_addr + kColO + kh * 128 + k;
+                tmem_ld16(at, v);
+                tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] *= inv;
-          if (split) {
-#pragma unroll
-            for (int x = 0; x < 16; x += 4) part[(k + x) / 4 * kRows] = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 16; x += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                w[y] = kF16 ? pack_f16x2(v[x + 2 * y], v[x + 2 * y + 1]) : pack_bf16x2(v[x + 2 * y], v[x + 2 * y + 1]);
-              *reinterpret_cast<uint4*>(dst + k + x) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int x = 0; x < 16; ++x) v[x] *= alpha;
+                tmem_st16(at, v);
+              }
+              tmem_wait_st();
             }
+            const bool tail = key0 + kKeys > I.kv_end;
+            if (tail) {
+              // keys behind the block's last token (other prompts', later ones'): their V becomes zeros;
+              // thread (kh, row) zeroes d-quarter kh of key `row`, each lane of eight beginning with another
+              // 16 bytes (another bank). This wait skips the phases of other tiles: V(g - 2) has landed
+              // (P.V(g - 2) is done), V(g + 2) comes after P.V(g).
+              mbar_wait(bar(ms.v_full[st]), (g / kStages) & 1, abort_flag, a.err);
+              if (key0 + row >= I.kv_end) {
+                uint4* dst = reinterpret_cast<uint4*>(smem + kOffV + st * kTile + kh * kVQuarter + row * 128);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) dst[(x + lane) & 7] = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+            }
+            // P = 2^(s c - m + sigma), 32 keys at a time: P.V of the first begins while the second are computed
+            tc_fence_after();
+            const float off = m_ref - kSigma, sc = need_mask ? 1.f : c;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pk[16];
+              float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int x = 0; x < 32; x += 2) {
+                const float p0 = ex2(fmaf(t[32 * h + x], sc, -off)), p1 = ex2(fmaf(t[32 * h + x + 1], sc, -off));
+                ls[(x >> 1) & 3] += p0 + p1;  // (the sums take P before its rounding: lse needs more than P.V does)
+                pk[x / 2] = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+              }
+              l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+              tmem_st16u(tmem + lane_addr + kColP + b * kPBufCols + kh * 32 + 16 * h, pk);
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                const uint32_t full = p_full + (2 * b + h) * 8;
+                if (tail) arrive_leader(full);
+                else signal_leader(full);
+              }
+            }
+            ++g;
           }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) signal_leader(o_free);
-        if (!split) {
-          if (a.lse && valid && kh == 0)
-            a.lse[(long long)(I.q0 + tok) * a.lse_st + (long long)head * a.lse_sh] = lse * 0.6931471805599453f;
-        } else {
-          if (valid && kh == 0) ws.part_lse[(size_t)(2 * I.slot + rank) * kRows + row] = lse;
-          __threadfence();
-          named_barrier(9, kSoftThreads);
-          if (gi == 0) {
+          if (j > 0 || i == 0) continue;
+          // -------------------------------------------------------- epilogue of item i - 1
+          const Item& E = ms.item[(i - 1) % kRing];
+          const int e_tok = E.tok0 + rank * tpc + my_t;
+          const bool valid = row < used && e_tok < E.n;
+          ms.lsum[kh][row] = l_done;
+          mbar_wait(bar(ms.o_ready), (i - 1) & 1, abort_flag, a.err);
+          tc_fence_after();
+          named_barrier(pair_bar, 64);
+          const float lr = l_done + ms.lsum[kh ^ 1][row];
+          const float inv = lr > 0.f ? 1.f / lr : 0.f;
+          const float lse = lr > 0.f ? m_done - kSigma + log2f(lr) : -INFINITY;
+          const int head = E.kvh * a.G + my_g;
+          // this thread's half row of the output (-1: no row), and of lse
+          const long long out_at = valid ? (long long)(E.q0 + e_tok) * a.o_st + (long long)head * a.o_sh + kh * 128 : -1;
+          const long long lse_at = (long long)(E.q0 + e_tok) * a.lse_st + (long long)head * a.lse_sh;
+          // 32 columns of each of the warp's rows: through shared memory, so that four lanes store 64 bytes of a
+          // row side by side (16 bytes of 32 rows a store took 6300 cycles for the 64 KB, LSU-bound)
+          auto store32 = [&](const uint32_t* w, int col) {
+            uint8_t* stage = smem + kOffStage + sw * 2048;
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int r = 8 * x + (lane >> 2), ch = lane & 3;
+              const long long at = __shfl_sync(0xffffffffu, out_at, r);
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+              if (at >= 0) *reinterpret_cast<uint4*>(a.out + at + col + ch * 8) = v;
+            }
+          };
+          if (E.nsplit == 1) {
+            uint32_t w[64];
+#pragma unroll
+            for (int k = 0; k < 128; k += 16) {
+              float v[16];
+              tmem_ld16(tmem + lane_addr + kColO + kh * 128 + k, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                w[k / 2 + x] = kF16 ? pack_f16x2(v[2 * x] * inv, v[2 * x + 1] * inv) : pack_bf16x2(v[2 * x] * inv, v[2 * x + 1] * inv);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) signal_leader(o_free);  // the next P.V may overwrite O
+#pragma unroll
+            for (int k = 0; k < 4; ++k) store32(w + 16 * k, 32 * k);
+            if (a.lse && valid && kh == 0) a.lse[lse_at] = lse * 0.6931471805599453f;
+          } else {
+            auto part_of = [&](int slot) {  // this thread's half row of a partial: four values every kRows * 4
+              return reinterpret_cast<float4*>(ws.part_o) + (size_t)(2 * slot + rank) * (kHeadDim / 4) * kRows + kh * 32 * kRows + row;
+            };
+            float4* part = part_of(E.slot);
+#pragma unroll 1
+            for (int k = 0; k < 128; k += 16) {
+              float v[16];
+              tmem_ld16(tmem + lane_addr + kColO + kh * 128 + k, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; x += 4)
+                part[(k + x) / 4 * kRows] = make_float4(v[x] * inv, v[x + 1] * inv, v[x + 2] * inv, v[x + 3] * inv);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) signal_leader(o_free);
+            if (kh == 0) ws.part_lse[(size_t)(2 * E.slot + rank) * kRows + row] = lse;
             __threadfence();
-            ms.merge_flag = split_arrive(ws.counters + 2 * I.slot0 + rank, I.nsplit, tag);
-            __threadfence();
-          }
-          named_barrier(9, kSoftThreads);
-          if (ms.merge_flag) {
-            // out = sum_x 2^(lse_x - M) o_x / sum_x 2^(lse_x - M): each thread its half row, whose values
-            // of 32 lanes lie side by side, 32 columns of two pieces in flight
-            __threadfence();
-            auto slot_of = [&](int x) { return x == 0 ? I.slot0 : I.slot1 + 2 * (x - 1); };
-            auto lse_of = [&](int x) { return __ldcg(ws.part_lse + (size_t)(2 * slot_of(x) + rank) * kRows + row); };
-            float M = -INFINITY, total = 0.f;
+            named_barrier(9, kSoftThreads);
+            if (gi == 0) {
+              __threadfence();
+              ms.merge_flag = split_arrive(ws.counters + 2 * E.slot0 + rank, E.nsplit, tag);
+              __threadfence();
+            }
+            named_barrier(9, kSoftThreads);
+            if (ms.merge_flag) {
+              // out = sum_x 2^(lse_x - M) o_x / sum_x 2^(lse_x - M): each thread its half row, whose values
+              // of 32 lanes lie side by side, 32 columns of two pieces in flight
+              __threadfence();
+              auto slot_of = [&](int x) { return x == 0 ? E.slot0 : E.slot1 + 2 * (x - 1); };
+              auto lse_of = [&](int x) { return __ldcg(ws.part_lse + (size_t)(2 * slot_of(x) + rank) * kRows + row); };
+              float M = -INFINITY, total = 0.f;
 #pragma unroll 2
-            for (int x = 0; x < I.nsplit; ++x) M = fmaxf(M, lse_of(x));
+              for (int x = 0; x < E.nsplit; ++x) M = fmaxf(M, lse_of(x));
 #pragma unroll 2
-            for (int x = 0; x < I.nsplit; ++x) total += exp2f(lse_of(x) - M);
-            if (valid) {
+              for (int x = 0; x < E.nsplit; ++x) total += exp2f(lse_of(x) - M);
               const float scale = 1.f / total;  // (a token sees itself: some piece has weight 1)
-              if (a.lse && kh == 0)
-                a.lse[(long long)(I.q0 + tok) * a.lse_st + (long long)head * a.lse_sh] = (M + log2f(total)) * 0.6931471805599453f;
+              if (a.lse && valid && kh == 0) a.lse[lse_at] = (M + log2f(total)) * 0.6931471805599453f;
 #pragma unroll 1
               for (int k = 0; k < 32; k += 8) {
                 float acc[32] = {};
 #pragma unroll 2
-                for (int x = 0; x < I.nsplit; ++x) {
-                  const float w = exp2f(lse_of(x) - M) * scale;
+                for (int x = 0; x < E.nsplit; ++x) {
+                  const float wx = exp2f(lse_of(x) - M) * scale;
                   const float4* o = part_of(slot_of(x)) + k * kRows;
                   float4 v[8];
 #pragma unroll
                   for (int y = 0; y < 8; ++y) v[y] = __ldcg(o + y * kRows);
 #pragma unroll
                   for (int y = 0; y < 8; ++y) {
-                    acc[4 * y] += w * v[y].x;
-                    acc[4 * y + 1] += w * v[y].y;
-                    acc[4 * y + 2] += w * v[y].z;
-                    acc[4 * y + 3] += w * v[y].w;
+                    acc[4 * y] += wx * v[y].x;
+                    acc[4 * y + 1] += wx * v[y].y;
+                    acc[4 * y + 2] += wx * v[y].z;
+                    acc[4 * y + 3] += wx * v[y].w;
                   }
                 }
+                uint32_t w[16];
 #pragma unroll
-                for (int y = 0; y < 32; y += 8) {
-                  uint32_t w[4];
-#pragma unroll
-                  for (int z = 0; z < 4; ++z)
-                    w[z] = kF16 ? pack_f16x2(acc[y + 2 * z], acc[y + 2 * z + 1]) : pack_bf16x2(acc[y + 2 * z], acc[y + 2 * z + 1]);
-                  *reinterpret_cast<uint4*>(dst + 4 * k + y) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                for (int y = 0; y < 16; ++y)
+                  w[y] = kF16 ? pack_f16x2(acc[2 * y], acc[2 * y + 1]) : pack_bf16x2(acc[2 * y], acc[2 * y + 1]);
+                store32(w, 4 * k);
               }
+              named_barrier(9, kSoftThreads);
             }
-            named_barrier(9, kSoftThreads);
           }
+          __syncwarp();
+          if (lane == 0) give(i - 1);
         }
-        if (lane == 0) give(i);
+        if (end) break;
+        m_done = m_ref;
+        l_done = l;
       }
     }
     // both CTAs wait for the leader's products (also after an abort)
