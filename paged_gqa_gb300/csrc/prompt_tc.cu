@@ -30,6 +30,7 @@
 
 #include <cstddef>
 #include <cstdio>
+#include <type_traits>
 
 #include "common.cuh"
 #include "device_util.cuh"
@@ -45,10 +46,15 @@ using namespace tc;
 
 constexpr int kRows = 128;                   // rows of a CTA
 constexpr int kKeys = 128;                   // keys of a tile
+// Warps 0-3: K and V copies, items and Q, products or relay; 4-11: softmax; 12-15: epilogue. The kernel starts with
+// 128 registers a thread, which the warpgroups then share out among themselves (setmaxnreg).
 constexpr int kSoftWarp0 = 4, kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
-constexpr int kThreads = kSoftWarp0 * 32 + kSoftThreads;
+constexpr int kEpiWarp0 = kSoftWarp0 + kSoftWarps, kEpiWarps = 4, kEpiThreads = kEpiWarps * 32;
+constexpr int kThreads = kEpiWarp0 * 32 + kEpiThreads;
+constexpr int kLaunchRegs = 128, kSoftRegs = 144, kEpiRegs = 160, kOtherRegs = 64;
+static_assert(kThreads * kLaunchRegs == 65536 && 256 * kSoftRegs + 128 * kEpiRegs + 128 * kOtherRegs == 65536, "register split");
 constexpr int kStages = 2;                   // of K, and of V
-constexpr int kRing = 3;                     // items known at a time: one whose epilogue is to come, one at work, the next
+constexpr int kRing = 3;                     // items known at a time: one in its epilogue, one at work, the next
 constexpr float kTau = 8.f;                  // a row's reference moves when a score exceeds it by this (log2)
 constexpr float kMInit = -1.0e30f;
 
@@ -74,9 +80,10 @@ struct Item {
 
 struct Misc {
   alignas(16) float red[2][2][kRows];  // [tile parity][key half][row] partial maxima
-  alignas(16) float lsum[2][kRows];
+  alignas(16) float stat_l[kRing][2][kRows];  // a finished item's row sums (of each key half) and references
+  alignas(16) float stat_m[kRing][kRows];
   alignas(16) Item item[kRing];
-  alignas(8) uint64_t item_full[kRing], item_empty[kRing];
+  alignas(8) uint64_t item_full[kRing], item_empty[kRing], stat_full[kRing];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full, q_empty, s_full, s_free, p_full[2][2], pv_done[2], o_ready, o_free, drain, never;
   long long scan[kThreads / 32];
@@ -86,8 +93,10 @@ struct Misc {
   uint32_t tmem_base;
   int abort_flag, merge_flag;
 };
-constexpr uint32_t kOffStage = kOffMisc + (uint32_t)((sizeof(Misc) + 127) / 128 * 128);  // 2 KB per softmax warp
-constexpr size_t kSmemBytes = kOffStage + kSoftWarps * 2048 + 1024;
+// The epilogue's stage: 96 columns of each row, rows 13 chunks of 16 bytes apart (an odd number: no bank conflicts).
+constexpr int kStageCols = 96, kStagePitch = 208;
+constexpr uint32_t kOffStage = kOffMisc + (uint32_t)((sizeof(Misc) + 127) / 128 * 128);
+constexpr size_t kSmemBytes = kOffStage + kRows * kStagePitch + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // ------------------------------------------------------------------ cluster-wide instructions --
@@ -212,7 +221,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     const int relays = rank == 0 ? 1 : 2;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(ms.item_full[i]), 1);
-      mbar_init(bar(ms.item_empty[i]), kSoftWarps + 2 + relays);  // softmax, K, V, and the products or both relays
+      mbar_init(bar(ms.item_empty[i]), kSoftWarps + kEpiWarps + 2 + relays);  // + K, V, and the products or both relays
+      mbar_init(bar(ms.stat_full[i]), kSoftWarps);
     }
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(ms.k_full[i]), both);
@@ -230,7 +240,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     mbar_init(bar(ms.s_full), 1);
     mbar_init(bar(ms.s_free), 2 * kSoftWarps);
     mbar_init(bar(ms.o_ready), 1);
-    mbar_init(bar(ms.o_free), 2 * kSoftWarps);
+    mbar_init(bar(ms.o_free), 2 * kEpiWarps);
     mbar_init(bar(ms.drain), 1);
     mbar_init(bar(ms.never), 1);
     ms.abort_flag = 0;
@@ -296,494 +306,537 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     };
     auto give = [&](int i) { mbar_arrive(bar(ms.item_empty[i % kRing])); };
 
-    if (warp == 2) {
-      // ------------------------------------------------------------ the items, and their Q
-      if (lane == 0) {
-        tma_prefetch_desc(&tmap_q);
-        const uint64_t policy = policy_evict_first();
-        int s = ms.start_seq, q0, n = prompt_len(a, s, &q0), nb = blocks_of(n, tb);
-        long long off = u0 - ms.start_off;
-        const long long head_units = units(nb, tb);
-        int kvh = (int)(off / head_units), b = 0;
-        off -= kvh * head_units;
-        for (int step = 1 << 30; step; step >>= 1)  // the last block that begins at or before off
-          if (b + step < nb && units(b + step, tb) <= off) b += step;
-        long long u = u0 - off + units(b, tb);  // the block's first unit
-        int i = 0;
-        bool ok = true;
-        while (ok && u < u1) {
-          const int kv_end = min(n, (b + 1) * tb), tiles = (kv_end + kKeys - 1) / kKeys;
-          const long long next = u + kFixed + (long long)(b + 1) * tb;
-          auto first_tile = [&](int c) { return cut_tile(range_begin(c, U, C) - u, tiles); };
-          Item I;
-          I.t0 = u < u0 ? first_tile(cluster) : 0;
-          I.t1 = next > u1 ? first_tile(cluster + 1) : tiles;
-          if (I.t0 < I.t1) {
-            int c0 = cta_of(u, U, C), c1 = cta_of(next - 1, U, C);
-            while (c0 < c1 && first_tile(c0 + 1) == 0) ++c0;
-            while (c1 > c0 && first_tile(c1) == tiles) --c1;
-            I.q0 = q0;
-            I.n = n;
-            I.tok0 = b * tb;
-            I.kvh = kvh;
-            I.kv_end = kv_end;
-            I.split = cluster - c0;
-            I.nsplit = c1 - c0 + 1;
-            // a cluster has at most one piece that continues a block (slot 2c) and one that begins one (2c + 1)
-            I.slot0 = 2 * c0 + (range_begin(c0, U, C) <= u ? 1 : 0);
-            I.slot1 = 2 * (c0 + 1);
-            I.slot = I.split == 0 ? I.slot0 : I.slot1 + 2 * (I.split - 1);
-            if (i >= kRing) ok = mbar_wait(bar(ms.item_empty[i % kRing]), ((i / kRing) - 1) & 1, abort_flag, a.err);
-            if (!ok) break;
-            ms.item[i % kRing] = I;
-            mbar_arrive(bar(ms.item_full[i % kRing]));
-            if (i >= 1) ok = mbar_wait(bar(ms.q_empty), (i - 1) & 1, abort_flag, a.err);
-            if (!ok) break;
-            mbar_expect_tx(bar(ms.q_full), (uint32_t)used * 512u);
-            for (int qd = 0; qd < 4; ++qd)
-              tma_load_3d(sbase + kOffQ + qd * kQQuarter, &tmap_q, qd * 64, kvh * a.G, q0 + I.tok0 + rank * tpc, bar(ms.q_full), policy);
-            ++i;
+    // (a warpgroup's four warps execute its setmaxnreg together, first thing in their branch)
+    if (warp < kSoftWarp0) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+      if (warp == 2) {
+        // ------------------------------------------------------------ the items, and their Q
+        if (lane == 0) {
+          tma_prefetch_desc(&tmap_q);
+          const uint64_t policy = policy_evict_first();
+          int s = ms.start_seq, q0, n = prompt_len(a, s, &q0), nb = blocks_of(n, tb);
+          long long off = u0 - ms.start_off;
+          const long long head_units = units(nb, tb);
+          int kvh = (int)(off / head_units), b = 0;
+          off -= kvh * head_units;
+          for (int step = 1 << 30; step; step >>= 1)  // the last block that begins at or before off
+            if (b + step < nb && units(b + step, tb) <= off) b += step;
+          long long u = u0 - off + units(b, tb);  // the block's first unit
+          int i = 0;
+          bool ok = true;
+          while (ok && u < u1) {
+            const int kv_end = min(n, (b + 1) * tb), tiles = (kv_end + kKeys - 1) / kKeys;
+            const long long next = u + kFixed + (long long)(b + 1) * tb;
+            auto first_tile = [&](int c) { return cut_tile(range_begin(c, U, C) - u, tiles); };
+            Item I;
+            I.t0 = u < u0 ? first_tile(cluster) : 0;
+            I.t1 = next > u1 ? first_tile(cluster + 1) : tiles;
+            if (I.t0 < I.t1) {
+              int c0 = cta_of(u, U, C), c1 = cta_of(next - 1, U, C);
+              while (c0 < c1 && first_tile(c0 + 1) == 0) ++c0;
+              while (c1 > c0 && first_tile(c1) == tiles) --c1;
+              I.q0 = q0;
+              I.n = n;
+              I.tok0 = b * tb;
+              I.kvh = kvh;
+              I.kv_end = kv_end;
+              I.split = cluster - c0;
+              I.nsplit = c1 - c0 + 1;
+              // a cluster has at most one piece that continues a block (slot 2c) and one that begins one (2c + 1)
+              I.slot0 = 2 * c0 + (range_begin(c0, U, C) <= u ? 1 : 0);
+              I.slot1 = 2 * (c0 + 1);
+              I.slot = I.split == 0 ? I.slot0 : I.slot1 + 2 * (I.split - 1);
+              if (i >= kRing) ok = mbar_wait(bar(ms.item_empty[i % kRing]), ((i / kRing) - 1) & 1, abort_flag, a.err);
+              if (!ok) break;
+              ms.item[i % kRing] = I;
+              mbar_arrive(bar(ms.item_full[i % kRing]));
+              if (i >= 1) ok = mbar_wait(bar(ms.q_empty), (i - 1) & 1, abort_flag, a.err);
+              if (!ok) break;
+              mbar_expect_tx(bar(ms.q_full), (uint32_t)used * 512u);
+              for (int qd = 0; qd < 4; ++qd)
+                tma_load_3d(sbase + kOffQ + qd * kQQuarter, &tmap_q, qd * 64, kvh * a.G, q0 + I.tok0 + rank * tpc, bar(ms.q_full), policy);
+              ++i;
+            }
+            u = next;
+            if (++b == nb) {
+              b = 0;
+              if (++kvh == a.Hkv) {
+                kvh = 0;
+                do {
+                  if (++s >= a.num_seqs) break;
+                  n = prompt_len(a, s, &q0);
+                  nb = blocks_of(n, tb);
+                } while (n == 0);
+                if (s >= a.num_seqs) break;
+              }
+            }
           }
-          u = next;
-          if (++b == nb) {
-            b = 0;
-            if (++kvh == a.Hkv) {
-              kvh = 0;
-              do {
-                if (++s >= a.num_seqs) break;
-                n = prompt_len(a, s, &q0);
-                nb = blocks_of(n, tb);
-              } while (n == 0);
-              if (s >= a.num_seqs) break;
+          // the end of the items
+          if (ok && i >= kRing) ok = mbar_wait(bar(ms.item_empty[i % kRing]), ((i / kRing) - 1) & 1, abort_flag, a.err);
+          if (ok) {
+            ms.item[i % kRing].nsplit = 0;
+            mbar_arrive(bar(ms.item_full[i % kRing]));
+          }
+          // the copies have landed before the CTA may exit (the leader's barrier waits for the other CTA's too;
+          // it gives up when that one has)
+          if (i >= 1) mbar_drain(bar(ms.q_full), (i - 1) & 1, abort_flag, a.err);
+        }
+      } else if (warp == 0 || warp == 1) {
+        // ------------------------------------------------------------ K (warp 0) and V (warp 1)
+        if (lane == 0) {
+          const bool is_k = warp == 0;
+          const CUtensorMap* tmap = is_k ? &tmap_k : &tmap_v;
+          uint64_t* full = is_k ? ms.k_full : ms.v_full;
+          uint64_t* empty = is_k ? ms.k_empty : ms.v_empty;
+          const uint32_t region = sbase + (is_k ? kOffK : kOffV);
+          tma_prefetch_desc(tmap);
+          const uint64_t policy = policy_evict_last();  // every block of a prompt reads them again
+          uint32_t g = 0;
+          bool ok = true;
+          Item I;
+          for (int i = 0; ok; ++i) {
+            if (!(ok = take(i, I)) || I.nsplit == 0) break;
+            for (int t = I.t0; t < I.t1; ++t, ++g) {
+              const uint32_t st = g % kStages;
+              if (g >= kStages && !(ok = mbar_wait(bar(empty[st]), ((g / kStages) - 1) & 1, abort_flag, a.err))) break;
+              mbar_expect_tx(bar(full[st]), kTile);
+              const uint32_t dst = region + st * kTile;
+              const int key = I.q0 + t * kKeys;
+              if (is_k) {
+                for (int qd = 0; qd < 4; ++qd)
+                  tma_load_3d(dst + qd * kKQuarter, tmap, qd * 64, I.kvh, key + rank * 64, bar(full[st]), policy);
+              } else {
+                for (int qd = 0; qd < 2; ++qd)
+                  tma_load_3d(dst + qd * kVQuarter, tmap, rank * 128 + qd * 64, I.kvh, key, bar(full[st]), policy);
+              }
+            }
+            if (ok) give(i);
+          }
+          for (uint32_t st = 0; st < kStages; ++st) {  // every copy has landed before the CTA may exit
+            if (g <= st) continue;
+            const uint32_t last = (g - 1 - st) / kStages;  // the last use of the stage
+            mbar_drain(bar(full[st]), last & 1, abort_flag, a.err);
+          }
+        }
+      } else if (warp == 3 && rank != 0) {
+        // ------------------------------------------------------------ the other CTA's relay
+        // One thread polls what it waits for in turn: K (with each item's Q in front) and V land at their own
+        // times, and neither may hold up the other. (K behind V cost 1100 cycles a tile.)
+        if (lane == 0) {
+          struct Stream {
+            int i, left;   // the item, and what of it is still to come (0: the item itself is)
+            uint32_t g;
+            bool q, done;
+          } x[2] = {{0, 0, 0, false, false}, {0, 0, 0, false, false}};
+          const uint32_t q_leader = in_leader(bar(ms.q_full));
+          uint64_t t0 = 0;
+          for (uint32_t polls = 0; !(x[0].done && x[1].done); ++polls) {
+            bool moved = false;
+  #pragma unroll
+            for (int which = 0; which < 2; ++which) {
+              Stream& r = x[which];
+              if (r.done) continue;
+              uint64_t* full = which == 0 ? ms.k_full : ms.v_full;
+              const uint32_t st = r.g % kStages;
+              if (r.left == 0) {
+                if (!mbar_test(bar(ms.item_full[r.i % kRing]), (r.i / kRing) & 1)) continue;
+                const Item& I = ms.item[r.i % kRing];
+                r.done = I.nsplit == 0;
+                r.left = I.t1 - I.t0;
+                r.q = which == 0;
+              } else if (r.q) {
+                if (!mbar_test(bar(ms.q_full), r.i & 1)) continue;
+                arrive_leader(q_leader);
+                r.q = false;
+              } else {
+                if (!mbar_test(bar(full[st]), (r.g / kStages) & 1)) continue;
+                arrive_leader(in_leader(bar(full[st])));
+                ++r.g;
+                if (--r.left == 0) give(r.i++);
+              }
+              moved = true;
+            }
+            if (moved || polls == 0) {
+              t0 = 0;
+            } else if ((polls & 63u) == 0u) {  // bounded, as every wait
+              if (*abort_flag) break;
+              const uint64_t now = global_timer_ns();
+              if (t0 == 0) t0 = now;
+              if (now - t0 > kWaitLimitNs) {
+                atomicOr(a.err, kErrTimeout);
+                *abort_flag = 1;
+                break;
+              }
             }
           }
         }
-        // the end of the items
-        if (ok && i >= kRing) ok = mbar_wait(bar(ms.item_empty[i % kRing]), ((i / kRing) - 1) & 1, abort_flag, a.err);
-        if (ok) {
-          ms.item[i % kRing].nsplit = 0;
-          mbar_arrive(bar(ms.item_full[i % kRing]));
-        }
-        // the copies have landed before the CTA may exit (the leader's barrier waits for the other CTA's too;
-        // it gives up when that one has)
-        if (i >= 1) mbar_drain(bar(ms.q_full), (i - 1) & 1, abort_flag, a.err);
-      }
-    } else if (warp == 0 || warp == 1) {
-      // ------------------------------------------------------------ K (warp 0) and V (warp 1)
-      if (lane == 0) {
-        const bool is_k = warp == 0;
-        const CUtensorMap* tmap = is_k ? &tmap_k : &tmap_v;
-        uint64_t* full = is_k ? ms.k_full : ms.v_full;
-        uint64_t* empty = is_k ? ms.k_empty : ms.v_empty;
-        const uint32_t region = sbase + (is_k ? kOffK : kOffV);
-        tma_prefetch_desc(tmap);
-        const uint64_t policy = policy_evict_last();  // every block of a prompt reads them again
+      } else if (warp == 3) {
+        // ------------------------------------------------------------ the leader's products
+        // The lanes of the warp agree on every wait: the ones that see an abort and those that do not must not part.
         uint32_t g = 0;
         bool ok = true;
         Item I;
+        auto waited = [&](const uint64_t& b, uint32_t parity) -> bool {
+          return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, a.err));
+        };
+        auto pv = [&](uint32_t gg, bool first, bool last, int i) -> bool {
+          const uint32_t st = gg % kStages, b = gg & 1;
+          // the first P.V of an item overwrites O: both CTAs' epilogues of the one before must be done
+          if (first && i >= 1 && !waited(ms.o_free, (i - 1) & 1)) return false;
+          if (!waited(ms.v_full[st], (gg / kStages) & 1)) return false;
+          // P comes in two parts, keys 0-31 and 64-95 of the tile and then the others
+  #pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!waited(ms.p_full[b][h], (gg >> 1) & 1)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+              // V as one N = 256 MN-major operand, 128 of d in each CTA: 64-element atoms 16 KB apart, 8-key
+              // groups 1 KB apart, 16 keys (2 KB) per instruction
+              const uint64_t v0 = smem_desc(sbase + kOffV + st * kTile, kVQuarter, 1024, kSw128);
+  #pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int kk = 2 * h + (x & 1) + (x >> 1) * 4;
+                mma2_ts(tmem + kColO, tmem + kColP + b * kPBufCols + kk * 8, v0 + ((kk * 2048) >> 4), kIdescO, first && kk == 0 ? 0u : 1u);
+              }
+              if (h == 1) {
+                commit2(bar(ms.v_empty[st]));
+                commit2(bar(ms.pv_done[b]));
+                if (last) commit2(bar(ms.o_ready));
+              }
+            }
+            __syncwarp();
+          }
+          return true;
+        };
+        // The order: S of the next tile, also of the next item, goes before P.V of this one.
+        int nt_before = 0;  // tiles of the item before
         for (int i = 0; ok; ++i) {
-          if (!(ok = take(i, I)) || I.nsplit == 0) break;
-          for (int t = I.t0; t < I.t1; ++t, ++g) {
+          if (!(ok = __all_sync(0xffffffffu, take(i, I)))) break;
+          const int nt = I.nsplit == 0 ? 0 : I.t1 - I.t0;
+          for (int j = 0; j < nt; ++j, ++g) {
             const uint32_t st = g % kStages;
-            if (g >= kStages && !(ok = mbar_wait(bar(empty[st]), ((g / kStages) - 1) & 1, abort_flag, a.err))) break;
-            mbar_expect_tx(bar(full[st]), kTile);
-            const uint32_t dst = region + st * kTile;
-            const int key = I.q0 + t * kKeys;
-            if (is_k) {
-              for (int qd = 0; qd < 4; ++qd)
-                tma_load_3d(dst + qd * kKQuarter, tmap, qd * 64, I.kvh, key + rank * 64, bar(full[st]), policy);
-            } else {
-              for (int qd = 0; qd < 2; ++qd)
-                tma_load_3d(dst + qd * kVQuarter, tmap, rank * 128 + qd * 64, I.kvh, key, bar(full[st]), policy);
+            if (j == 0 && !(ok = waited(ms.q_full, i & 1))) break;
+            if (!(ok = waited(ms.k_full[st], (g / kStages) & 1))) break;
+            if (g >= 1 && !(ok = waited(ms.s_free, (g - 1) & 1))) break;
+            tc_fence_after();
+            if (elect_one()) {
+  #pragma unroll
+              for (int qd = 0; qd < 4; ++qd) {
+                const uint64_t q0 = smem_desc(sbase + kOffQ + qd * kQQuarter, 16, 1024, kSw128);
+                const uint64_t k0 = smem_desc(sbase + kOffK + st * kTile + qd * kKQuarter, 16, 1024, kSw128);
+  #pragma unroll
+                for (int k = 0; k < 4; ++k)  // 16 values (32 bytes) of d per instruction
+                  mma2(tmem + kColS, q0 + ((k * 32) >> 4), k0 + ((k * 32) >> 4), kIdescS, (qd | k) ? 1u : 0u);
+              }
+              commit2(bar(ms.s_full));
+              commit2(bar(ms.k_empty[st]));
+              if (j == nt - 1) commit2(bar(ms.q_empty));
             }
+            __syncwarp();
+            if (j >= 1) ok = pv(g - 1, j == 1, false, i);
+            else if (i >= 1) ok = pv(g - 1, nt_before == 1, true, i - 1);
+            if (!ok) break;
           }
-          if (ok) give(i);
+          if (nt == 0) {  // the end: the last item's last P.V
+            if (i >= 1) ok = pv(g - 1, nt_before == 1, true, i - 1);
+            break;
+          }
+          nt_before = nt;
+          if (ok && lane == 0) give(i);
         }
-        for (uint32_t st = 0; st < kStages; ++st) {  // every copy has landed before the CTA may exit
-          if (g <= st) continue;
-          const uint32_t last = (g - 1 - st) / kStages;  // the last use of the stage
-          mbar_drain(bar(full[st]), last & 1, abort_flag, a.err);
-        }
+        // every product has completed before either CTA may give its TMEM back
+        if (elect_one()) commit2(bar(ms.drain));
+        __syncwarp();
       }
-    } else if (warp == 3 && rank != 0) {
-      // ------------------------------------------------------------ the other CTA's relay
-      // One thread polls what it waits for in turn: K (with each item's Q in front) and V land at their own
-      // times, and neither may hold up the other. (K behind V cost 1100 cycles a tile.)
-      if (lane == 0) {
-        struct Stream {
-          int i, left;   // the item, and what of it is still to come (0: the item itself is)
-          uint32_t g;
-          bool q, done;
-        } x[2] = {{0, 0, 0, false, false}, {0, 0, 0, false, false}};
-        const uint32_t q_leader = in_leader(bar(ms.q_full));
-        uint64_t t0 = 0;
-        for (uint32_t polls = 0; !(x[0].done && x[1].done); ++polls) {
-          bool moved = false;
-#pragma unroll
-          for (int which = 0; which < 2; ++which) {
-            Stream& r = x[which];
-            if (r.done) continue;
-            uint64_t* full = which == 0 ? ms.k_full : ms.v_full;
-            const uint32_t st = r.g % kStages;
-            if (r.left == 0) {
-              if (!mbar_test(bar(ms.item_full[r.i % kRing]), (r.i / kRing) & 1)) continue;
-              const Item& I = ms.item[r.i % kRing];
-              r.done = I.nsplit == 0;
-              r.left = I.t1 - I.t0;
-              r.q = which == 0;
-            } else if (r.q) {
-              if (!mbar_test(bar(ms.q_full), r.i & 1)) continue;
-              arrive_leader(q_leader);
-              r.q = false;
-            } else {
-              if (!mbar_test(bar(full[st]), (r.g / kStages) & 1)) continue;
-              arrive_leader(in_leader(bar(full[st])));
-              ++r.g;
-              if (--r.left == 0) give(r.i++);
-            }
-            moved = true;
-          }
-          if (moved || polls == 0) {
-            t0 = 0;
-          } else if ((polls & 63u) == 0u) {  // bounded, as every wait
-            if (*abort_flag) break;
-            const uint64_t now = global_timer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitLimitNs) {
-              atomicOr(a.err, kErrTimeout);
-              *abort_flag = 1;
-              break;
-            }
-          }
-        }
-      }
-    } else if (warp == 3) {
-      // ------------------------------------------------------------ the leader's products
-      // The lanes of the warp agree on every wait: the ones that see an abort and those that do not must not part.
-      uint32_t g = 0;
-      bool ok = true;
-      Item I;
-      auto waited = [&](const uint64_t& b, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, a.err));
-      };
-      auto pv = [&](uint32_t gg, bool first, bool last, int i) -> bool {
-        const uint32_t st = gg % kStages, b = gg & 1;
-        // the first P.V of an item overwrites O: both CTAs' epilogues of the one before must be done
-        if (first && i >= 1 && !waited(ms.o_free, (i - 1) & 1)) return false;
-        if (!waited(ms.v_full[st], (gg / kStages) & 1)) return false;
-        // P comes in two parts, keys 0-31 and 64-95 of the tile and then the others
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!waited(ms.p_full[b][h], (gg >> 1) & 1)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-            // V as one N = 256 MN-major operand, 128 of d in each CTA: 64-element atoms 16 KB apart, 8-key
-            // groups 1 KB apart, 16 keys (2 KB) per instruction
-            const uint64_t v0 = smem_desc(sbase + kOffV + st * kTile, kVQuarter, 1024, kSw128);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int kk = 2 * h + (x & 1) + (x >> 1) * 4;
-              mma2_ts(tmem + kColO, tmem + kColP + b * kPBufCols + kk * 8, v0 + ((kk * 2048) >> 4), kIdescO, first && kk == 0 ? 0u : 1u);
-            }
-            if (h == 1) {
-              commit2(bar(ms.v_empty[st]));
-              commit2(bar(ms.pv_done[b]));
-              if (last) commit2(bar(ms.o_ready));
-            }
-          }
-          __syncwarp();
-        }
-        return true;
-      };
-      // The order: S of the next tile, also of the next item, goes before P.V of this one.
-      int nt_before = 0;  // tiles of the item before
-      for (int i = 0; ok; ++i) {
-        if (!(ok = __all_sync(0xffffffffu, take(i, I)))) break;
-        const int nt = I.nsplit == 0 ? 0 : I.t1 - I.t0;
-        for (int j = 0; j < nt; ++j, ++g) {
-          const uint32_t st = g % kStages;
-          if (j == 0 && !(ok = waited(ms.q_full, i & 1))) break;
-          if (!(ok = waited(ms.k_full[st], (g / kStages) & 1))) break;
-          if (g >= 1 && !(ok = waited(ms.s_free, (g - 1) & 1))) break;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int qd = 0; qd < 4; ++qd) {
-              const uint64_t q0 = smem_desc(sbase + kOffQ + qd * kQQuarter, 16, 1024, kSw128);
-              const uint64_t k0 = smem_desc(sbase + kOffK + st * kTile + qd * kKQuarter, 16, 1024, kSw128);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)  // 16 values (32 bytes) of d per instruction
-                mma2(tmem + kColS, q0 + ((k * 32) >> 4), k0 + ((k * 32) >> 4), kIdescS, (qd | k) ? 1u : 0u);
-            }
-            commit2(bar(ms.s_full));
-            commit2(bar(ms.k_empty[st]));
-            if (j == nt - 1) commit2(bar(ms.q_empty));
-          }
-          __syncwarp();
-          if (j >= 1) ok = pv(g - 1, j == 1, false, i);
-          else if (i >= 1) ok = pv(g - 1, nt_before == 1, true, i - 1);
-          if (!ok) break;
-        }
-        if (nt == 0) {  // the end: the last item's last P.V
-          if (i >= 1) ok = pv(g - 1, nt_before == 1, true, i - 1);
-          break;
-        }
-        nt_before = nt;
-        if (ok && lane == 0) give(i);
-      }
-      // every product has completed before either CTA may give its TMEM back
-      if (elect_one()) commit2(bar(ms.drain));
-      __syncwarp();
-    } else if (warp >= kSoftWarp0) {
-      // ------------------------------------------------------------ softmax and epilogue
-      const int sw = warp - kSoftWarp0, gi = sw * 32 + lane;
-      const int q4 = warp & 3, kh = sw >> 2;  // TMEM lane quarter; key half of the tile, d half of O
+    } else if (warp < kEpiWarp0) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+      // ------------------------------------------------------------ softmax
+      const int sw = warp - kSoftWarp0;
+      const int q4 = warp & 3, kh = sw >> 2;  // TMEM lane quarter; key half of the tile
       const int row = q4 * 32 + lane;
       const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
       const int pair_bar = 1 + q4;            // named barrier of the two warps that share these rows
-      const uint32_t s_free = in_leader(bar(ms.s_free)), o_free = in_leader(bar(ms.o_free));
+      const uint32_t s_free = in_leader(bar(ms.s_free));
       const uint32_t p_full = in_leader(bar(ms.p_full[0][0]));  // (the four barriers lie in a row)
       const float c = a.score_scale_log2;
       const bool c_pos = c >= 0.f;
-      const int my_t = row / a.G, my_g = row - my_t * a.G;
+      const int my_t = row / a.G;
       uint32_t g = 0;
       // failure-path test: a bounded wait on a barrier nothing arrives on
       const bool stalled = a.stall_test_ns && !mbar_wait(bar(ms.never), 0, abort_flag, a.err, a.stall_test_ns);
-      // This call's counter tag (thread 0 uses it).
-      const unsigned long long tag = (__ldcg(ws.epoch) ^ ((unsigned long long)ws.call_tag * 0x9E3779B97F4A7C15ull)) & kSplitTagMask;
-      // An item's epilogue comes after the first tile of the next one: its last P.V then runs while these
-      // warps are at work, and the tensor pipe has a product to go on with during the epilogue. What the epilogue
-      // needs of the item is in the ring still; the row's statistics are kept here.
-      float m_ref = kMInit, l = 0.f, m_done = 0.f, l_done = 0.f;
       for (int i = 0; !stalled; ++i) {
         // All softmax threads leave together (they meet at barriers). A failed wait inside an item does not
         // leave it: the later ones then fail at once.
         Item I;
-        if (barrier_or(10, kSoftThreads, !take(i, I))) break;
-        const bool end = I.nsplit == 0;
-        const int tok = I.tok0 + rank * tpc + my_t;  // this row's token
-        const int nt = end ? 0 : I.t1 - I.t0;
-        m_ref = kMInit;
-        l = 0.f;
-        for (int j = 0; j < max(nt, 1); ++j) {
-          if (!end) {
-            const uint32_t b = g & 1, st = g % kStages;
-            const int key0 = (I.t0 + j) * kKeys, kbase = key0 + kh * 64;
-            float t[64];
-            mbar_wait(bar(ms.s_full), g & 1, abort_flag, a.err);
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 64; k += 16) {
-              float v[16];
-              tmem_ld16(tmem + lane_addr + kColS + kh * 64 + k, v);
-#pragma unroll
-              for (int x = 0; x < 16; ++x) t[k + x] = v[x];
-            }
-            // P.V(g - 2) has read P buffer b (its barrier's next phase needs P(g)); long since, so the wait costs
-            // nothing but its own latency, which the load above hides
-            if (g >= 2) mbar_wait(bar(ms.pv_done[b]), ((g >> 1) - 1) & 1, abort_flag, a.err);
-            tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) signal_leader(s_free);  // S may be overwritten
-            const bool need_mask = key0 + kKeys - 1 > I.tok0 + rank * tpc;
-            float mx;
-            if (need_mask) {
-#pragma unroll
-              for (int x = 0; x < 64; ++x) t[x] = kbase + x <= tok ? t[x] * c : -INFINITY;
-              mx = extreme_of<true>(t);
-            } else {
-              mx = (c_pos ? extreme_of<true>(t) : extreme_of<false>(t)) * c;
-            }
-            ms.red[b][kh][row] = mx;
-            named_barrier(pair_bar, 64);
-            const float mt = fmaxf(mx, ms.red[b][kh ^ 1][row]);
-            float alpha = 1.f;
-            const bool rescale = mt > m_ref + kTau;
-            if (rescale) {
-              alpha = ex2(m_ref - mt);
-              m_ref = mt;
-              l *= alpha;
-            }
-            // tcgen05.ld/st are warp-wide: a warp rescales if any of its rows must
-            if (__any_sync(0xffffffffu, rescale && j > 0)) {
-              mbar_wait(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, a.err);
-              tc_fence_after();
-              if (!rescale) alpha = 1.f;
-#pragma unroll 1
-              for (int k = 0; k < 128; k += 16) {  // this thread's half of its row of O
-                float v[16];
-                const uint32_t at = tmem + lane_addr + kColO + kh * 128 + k;
-                tmem_ld16(at, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int x = 0; x < 16; ++x) v[x] *= alpha;
-                tmem_st16(at, v);
-              }
-              tmem_wait_st();
-            }
-            const bool tail = key0 + kKeys > I.kv_end;
-            if (tail) {
-              // keys behind the block's last token (other prompts', later ones'): their V becomes zeros;
-              // thread (kh, row) zeroes d-quarter kh of key `row`, each lane of eight beginning with another
-              // 16 bytes (another bank). This wait skips the phases of other tiles: V(g - 2) has landed
-              // (P.V(g - 2) is done), V(g + 2) comes after P.V(g).
-              mbar_wait(bar(ms.v_full[st]), (g / kStages) & 1, abort_flag, a.err);
-              if (key0 + row >= I.kv_end) {
-                uint4* dst = reinterpret_cast<uint4*>(smem + kOffV + st * kTile + kh * kVQuarter + row * 128);
-#pragma unroll
-                for (int x = 0; x < 8; ++x) dst[(x + lane) & 7] = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-            }
-            // P = 2^(s c - m + sigma), 32 keys at a time: P.V of the first begins while the second are computed
-            tc_fence_after();
-            const float off = m_ref - kSigma, sc = need_mask ? 1.f : c;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t pk[16];
-              float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int x = 0; x < 32; x += 2) {
-                const float p0 = ex2(fmaf(t[32 * h + x], sc, -off)), p1 = ex2(fmaf(t[32 * h + x + 1], sc, -off));
-                ls[(x >> 1) & 3] += p0 + p1;  // (the sums take P before its rounding: lse needs more than P.V does)
-                pk[x / 2] = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-              }
-              l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-              tmem_st16u(tmem + lane_addr + kColP + b * kPBufCols + kh * 32 + 16 * h, pk);
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                const uint32_t full = p_full + (2 * b + h) * 8;
-                if (tail) arrive_leader(full);
-                else signal_leader(full);
-              }
-            }
-            ++g;
-          }
-          if (j > 0 || i == 0) continue;
-          // -------------------------------------------------------- epilogue of item i - 1
-          const Item& E = ms.item[(i - 1) % kRing];
-          const int e_tok = E.tok0 + rank * tpc + my_t;
-          const bool valid = row < used && e_tok < E.n;
-          ms.lsum[kh][row] = l_done;
-          mbar_wait(bar(ms.o_ready), (i - 1) & 1, abort_flag, a.err);
+        if (barrier_or(10, kSoftThreads, !take(i, I)) || I.nsplit == 0) break;
+        const int first_tok = I.tok0 + rank * tpc, tok = first_tok + my_t;  // this CTA's first, this row's token
+        float m_ref = kMInit, l = 0.f;
+        const int nt = I.t1 - I.t0;
+        for (int j = 0; j < nt; ++j, ++g) {
+          const uint32_t b = g & 1, st = g % kStages;
+          const int key0 = (I.t0 + j) * kKeys, kbase = key0 + kh * 64;
+          float t[64];
+          mbar_wait(bar(ms.s_full), g & 1, abort_flag, a.err);
           tc_fence_after();
-          named_barrier(pair_bar, 64);
-          const float lr = l_done + ms.lsum[kh ^ 1][row];
-          const float inv = lr > 0.f ? 1.f / lr : 0.f;
-          const float lse = lr > 0.f ? m_done - kSigma + log2f(lr) : -INFINITY;
-          const int head = E.kvh * a.G + my_g;
-          // this thread's half row of the output (-1: no row), and of lse
-          const long long out_at = valid ? (long long)(E.q0 + e_tok) * a.o_st + (long long)head * a.o_sh + kh * 128 : -1;
-          const long long lse_at = (long long)(E.q0 + e_tok) * a.lse_st + (long long)head * a.lse_sh;
-          // 32 columns of each of the warp's rows: through shared memory, so that four lanes store 64 bytes of a
-          // row side by side (16 bytes of 32 rows a store took 6300 cycles for the 64 KB, LSU-bound)
-          auto store32 = [&](const uint32_t* w, int col) {
-            uint8_t* stage = smem + kOffStage + sw * 2048;
-            __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              *reinterpret_cast<uint4*>(stage + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-            __syncwarp();
+          for (int k = 0; k < 64; k += 16) {
+            float v[16];
+            tmem_ld16(tmem + lane_addr + kColS + kh * 64 + k, v);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int r = 8 * x + (lane >> 2), ch = lane & 3;
-              const long long at = __shfl_sync(0xffffffffu, out_at, r);
-              const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-              if (at >= 0) *reinterpret_cast<uint4*>(a.out + at + col + ch * 8) = v;
-            }
-          };
-          if (E.nsplit == 1) {
-            uint32_t w[64];
+            for (int x = 0; x < 16; ++x) t[k + x] = v[x];
+          }
+          // P.V(g - 2) has read P buffer b (its barrier's next phase needs P(g)); long since, so the wait costs
+          // nothing but its own latency, which the load above hides
+          if (g >= 2) mbar_wait(bar(ms.pv_done[b]), ((g >> 1) - 1) & 1, abort_flag, a.err);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) signal_leader(s_free);  // S may be overwritten
+          const bool need_mask = key0 + kKeys - 1 > first_tok;
+          float mx;
+          if (need_mask) {
 #pragma unroll
-            for (int k = 0; k < 128; k += 16) {
-              float v[16];
-              tmem_ld16(tmem + lane_addr + kColO + kh * 128 + k, v);
-              tmem_wait_ld();
-#pragma unroll
-              for (int x = 0; x < 8; ++x)
-                w[k / 2 + x] = kF16 ? pack_f16x2(v[2 * x] * inv, v[2 * x + 1] * inv) : pack_bf16x2(v[2 * x] * inv, v[2 * x + 1] * inv);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) signal_leader(o_free);  // the next P.V may overwrite O
-#pragma unroll
-            for (int k = 0; k < 4; ++k) store32(w + 16 * k, 32 * k);
-            if (a.lse && valid && kh == 0) a.lse[lse_at] = lse * 0.6931471805599453f;
+            for (int x = 0; x < 64; ++x) t[x] = kbase + x <= tok ? t[x] * c : -INFINITY;
+            mx = extreme_of<true>(t);
           } else {
-            auto part_of = [&](int slot) {  // this thread's half row of a partial: four values every kRows * 4
-              return reinterpret_cast<float4*>(ws.part_o) + (size_t)(2 * slot + rank) * (kHeadDim / 4) * kRows + kh * 32 * kRows + row;
-            };
-            float4* part = part_of(E.slot);
+            mx = (c_pos ? extreme_of<true>(t) : extreme_of<false>(t)) * c;
+          }
+          ms.red[b][kh][row] = mx;
+          named_barrier(pair_bar, 64);
+          const float mt = fmaxf(mx, ms.red[b][kh ^ 1][row]);
+          float alpha = 1.f;
+          const bool rescale = mt > m_ref + kTau;
+          if (rescale) {
+            alpha = ex2(m_ref - mt);
+            m_ref = mt;
+            l *= alpha;
+          }
+          // tcgen05.ld/st are warp-wide: a warp rescales if any of its rows must
+          if (__any_sync(0xffffffffu, rescale && j > 0)) {
+            mbar_wait(bar(ms.pv_done[(g - 1) & 1]), ((g - 1) >> 1) & 1, abort_flag, a.err);
+            tc_fence_after();
+            if (!rescale) alpha = 1.f;
 #pragma unroll 1
-            for (int k = 0; k < 128; k += 16) {
+            for (int k = 0; k < 128; k += 16) {  // this thread's half of its row of O
               float v[16];
-              tmem_ld16(tmem + lane_addr + kColO + kh * 128 + k, v);
+              const uint32_t at = tmem + lane_addr + kColO + kh * 128 + k;
+              tmem_ld16(at, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 16; x += 4)
-                part[(k + x) / 4 * kRows] = make_float4(v[x] * inv, v[x + 1] * inv, v[x + 2] * inv, v[x + 3] * inv);
+              for (int x = 0; x < 16; ++x) v[x] *= alpha;
+              tmem_st16(at, v);
             }
+            tmem_wait_st();
+          }
+          const bool tail = key0 + kKeys > I.kv_end;
+          if (tail) {
+            // keys behind the block's last token (other prompts', later ones'): their V becomes zeros;
+            // thread (kh, row) zeroes d-quarter kh of key `row`, each lane of eight beginning with another
+            // 16 bytes (another bank). This wait skips the phases of other tiles: V(g - 2) has landed
+            // (P.V(g - 2) is done), V(g + 2) comes after P.V(g).
+            mbar_wait(bar(ms.v_full[st]), (g / kStages) & 1, abort_flag, a.err);
+            if (key0 + row >= I.kv_end) {
+              uint4* dst = reinterpret_cast<uint4*>(smem + kOffV + st * kTile + kh * kVQuarter + row * 128);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) dst[(x + lane) & 7] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          // P = 2^(s c - m + sigma), 32 keys at a time: P.V of the first begins while the second are computed
+          tc_fence_after();
+          const float off = m_ref - kSigma, sc = need_mask ? 1.f : c;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[16];
+            float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const float p0 = ex2(fmaf(t[32 * h + x], sc, -off)), p1 = ex2(fmaf(t[32 * h + x + 1], sc, -off));
+              ls[(x >> 1) & 3] += p0 + p1;  // (the sums take P before its rounding: lse needs more than P.V does)
+              pk[x / 2] = kF16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            }
+            l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+            tmem_st16u(tmem + lane_addr + kColP + b * kPBufCols + kh * 32 + 16 * h, pk);
+            tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) signal_leader(o_free);
-            if (kh == 0) ws.part_lse[(size_t)(2 * E.slot + rank) * kRows + row] = lse;
-            __threadfence();
-            named_barrier(9, kSoftThreads);
-            if (gi == 0) {
-              __threadfence();
-              ms.merge_flag = split_arrive(ws.counters + 2 * E.slot0 + rank, E.nsplit, tag);
-              __threadfence();
+            if (lane == 0) {
+              const uint32_t full = p_full + (2 * b + h) * 8;
+              if (tail) arrive_leader(full);
+              else signal_leader(full);
             }
-            named_barrier(9, kSoftThreads);
-            if (ms.merge_flag) {
-              // out = sum_x 2^(lse_x - M) o_x / sum_x 2^(lse_x - M): each thread its half row, whose values
-              // of 32 lanes lie side by side, 32 columns of two pieces in flight
-              __threadfence();
-              auto slot_of = [&](int x) { return x == 0 ? E.slot0 : E.slot1 + 2 * (x - 1); };
-              auto lse_of = [&](int x) { return __ldcg(ws.part_lse + (size_t)(2 * slot_of(x) + rank) * kRows + row); };
-              float M = -INFINITY, total = 0.f;
-#pragma unroll 2
-              for (int x = 0; x < E.nsplit; ++x) M = fmaxf(M, lse_of(x));
-#pragma unroll 2
-              for (int x = 0; x < E.nsplit; ++x) total += exp2f(lse_of(x) - M);
-              const float scale = 1.f / total;  // (a token sees itself: some piece has weight 1)
-              if (a.lse && valid && kh == 0) a.lse[lse_at] = (M + log2f(total)) * 0.6931471805599453f;
-#pragma unroll 1
-              for (int k = 0; k < 32; k += 8) {
-                float acc[32] = {};
-#pragma unroll 2
-                for (int x = 0; x < E.nsplit; ++x) {
-                  const float wx = exp2f(lse_of(x) - M) * scale;
-                  const float4* o = part_of(slot_of(x)) + k * kRows;
-                  float4 v[8];
+          }
+        }
+        ms.stat_l[i % kRing][kh][row] = l;
+        if (kh == 0) ms.stat_m[i % kRing][row] = m_ref;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(ms.stat_full[i % kRing]));
+          give(i);
+        }
+      }
+    } else {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+      // ------------------------------------------------------------ epilogue
+      const int q4 = warp & 3, row = q4 * 32 + lane, gi = row;
+      const uint32_t o_addr = tmem + ((uint32_t)(q4 * 32) << 16) + kColO;
+      const uint32_t o_free = in_leader(bar(ms.o_free));
+      const int my_t = row / a.G, my_g = row - my_t * a.G;
+      // This call's counter tag (thread 0 uses it).
+      const unsigned long long tag = (__ldcg(ws.epoch) ^ ((unsigned long long)ws.call_tag * 0x9E3779B97F4A7C15ull)) & kSplitTagMask;
+      for (int i = 0;; ++i) {
+        Item I;
+        if (barrier_or(11, kEpiThreads, !take(i, I)) || I.nsplit == 0) break;
+        const int tok = I.tok0 + rank * tpc + my_t;
+        const bool valid = row < used && tok < I.n;
+        mbar_wait(bar(ms.stat_full[i % kRing]), (i / kRing) & 1, abort_flag, a.err);
+        const float lr = ms.stat_l[i % kRing][0][row] + ms.stat_l[i % kRing][1][row];
+        const float inv = lr > 0.f ? 1.f / lr : 0.f;
+        const float lse = lr > 0.f ? ms.stat_m[i % kRing][row] - kSigma + log2f(lr) : -INFINITY;
+        const int head = I.kvh * a.G + my_g;
+        const long long out_at = valid ? (long long)(I.q0 + tok) * a.o_st + (long long)head * a.o_sh : -1;  // this row (-1: none)
+        const long long lse_at = (long long)(I.q0 + tok) * a.lse_st + (long long)head * a.lse_sh;
+        uint8_t* stage = smem + kOffStage + q4 * 32 * kStagePitch;
+        // Chunks of 8 columns of each of the warp's rows, packed, go through shared memory, so that lanes side by
+        // side store the bytes of a row (16 bytes of 32 rows a store were bound by the LSU): put() and flush().
+        auto put = [&](const uint32_t* w, int chunk, int n) {
 #pragma unroll
-                  for (int y = 0; y < 8; ++y) v[y] = __ldcg(o + y * kRows);
+          for (int x = 0; x < n; ++x)
+            *reinterpret_cast<uint4*>(stage + lane * kStagePitch + (chunk + x) * 16) = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        };
+        auto flush = [&](auto chunks, int col) {
+          constexpr int kN = decltype(chunks)::value;
+          __syncwarp();
 #pragma unroll
-                  for (int y = 0; y < 8; ++y) {
-                    acc[4 * y] += wx * v[y].x;
-                    acc[4 * y + 1] += wx * v[y].y;
-                    acc[4 * y + 2] += wx * v[y].z;
-                    acc[4 * y + 3] += wx * v[y].w;
-                  }
-                }
-                uint32_t w[16];
-#pragma unroll
-                for (int y = 0; y < 16; ++y)
-                  w[y] = kF16 ? pack_f16x2(acc[2 * y], acc[2 * y + 1]) : pack_bf16x2(acc[2 * y], acc[2 * y + 1]);
-                store32(w, 4 * k);
-              }
-              named_barrier(9, kSoftThreads);
-            }
+          for (int x = 0; x < kN; ++x) {
+            const int idx = x * 32 + lane, r = idx / kN, ch = idx - r * kN;
+            const long long at = __shfl_sync(0xffffffffu, out_at, r);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kStagePitch + ch * 16);
+            if (at >= 0) *reinterpret_cast<uint4*>(a.out + at + col + ch * 8) = v;
           }
           __syncwarp();
-          if (lane == 0) give(i - 1);
+        };
+        auto load16 = [&](int col, float (&v)[16]) {
+          tmem_ld16(o_addr + col, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) v[x] *= inv;
+        };
+        auto pack = [&](float x, float y) { return kF16 ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
+        mbar_wait(bar(ms.o_ready), i & 1, abort_flag, a.err);
+        tc_fence_after();
+        if (I.nsplit == 1) {
+          // O leaves TMEM at once, part of it to the stage and the rest to registers, so that the next P.V may
+          // overwrite it while the stores are still to come
+          uint32_t w[80];
+#pragma unroll
+          for (int k = 0; k < kHeadDim; k += 16) {
+            float v[16];
+            load16(k, v);
+            uint32_t x8[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) x8[x] = pack(v[2 * x], v[2 * x + 1]);
+            if (k < kStageCols) {
+              put(x8, k / 8, 2);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) w[(k - kStageCols) / 2 + x] = x8[x];
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) signal_leader(o_free);
+          flush(std::integral_constant<int, 12>(), 0);
+          put(w, 0, 12);
+          flush(std::integral_constant<int, 12>(), kStageCols);
+          put(w + 48, 0, 8);
+          flush(std::integral_constant<int, 8>(), 2 * kStageCols);
+          if (a.lse && valid) a.lse[lse_at] = lse * 0.6931471805599453f;
+        } else {
+          // A piece whose block's other pieces have all arrived merges them with its own O at once. Any other
+          // piece leaves its partial behind; should the others have arrived meanwhile, it merges too.
+          auto slot_of = [&](int x) { return x == 0 ? I.slot0 : I.slot1 + 2 * (x - 1); };
+          auto lse_of = [&](int x) { return ws.part_lse + (size_t)(2 * slot_of(x) + rank) * kRows + row; };
+          auto part_of = [&](int x) {  // this row of a partial: four values every kRows * 4
+            return reinterpret_cast<float4*>(ws.part_o) + (size_t)(2 * slot_of(x) + rank) * (kHeadDim / 4) * kRows + row;
+          };
+          unsigned long long* counter = ws.counters + 2 * I.slot0 + rank;
+          if (gi == 0) {
+            ms.merge_flag = split_peek(counter) == (tag << 16 | (unsigned)(I.nsplit - 1));
+            __threadfence();
+          }
+          named_barrier(9, kEpiThreads);
+          bool last = ms.merge_flag;
+          if (!last) {
+            float4* part = part_of(I.split);
+#pragma unroll 1
+            for (int k = 0; k < kHeadDim; k += 16) {
+              float v[16];
+              load16(k, v);
+#pragma unroll
+              for (int x = 0; x < 16; x += 4) part[(k + x) / 4 * kRows] = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+            }
+            *lse_of(I.split) = lse;
+            __threadfence();
+            named_barrier(9, kEpiThreads);
+            if (gi == 0) {
+              __threadfence();
+              ms.merge_flag = split_arrive(counter, I.nsplit, tag);
+              __threadfence();
+            }
+            named_barrier(9, kEpiThreads);
+            last = ms.merge_flag;
+          }
+          if (last) {
+            // out = sum_x 2^(lse_x - M) o_x / sum_x 2^(lse_x - M), in the order of the pieces: the same bits
+            // whichever came last
+            __threadfence();
+            float M = -INFINITY, total = 0.f;
+            for (int x = 0; x < I.nsplit; ++x) M = fmaxf(M, x == I.split ? lse : __ldcg(lse_of(x)));
+            for (int x = 0; x < I.nsplit; ++x) total += exp2f((x == I.split ? lse : __ldcg(lse_of(x))) - M);
+            const float scale = 1.f / total;  // (a token sees itself: some piece has weight 1)
+            if (a.lse && valid) a.lse[lse_at] = (M + log2f(total)) * 0.6931471805599453f;
+#pragma unroll 1
+            for (int k = 0; k < kHeadDim; k += 32) {
+              float acc[32] = {};
+              for (int x = 0; x < I.nsplit; ++x) {
+                const float wx = exp2f((x == I.split ? lse : __ldcg(lse_of(x))) - M) * scale;
+                float v[32];
+                if (x == I.split) {
+#pragma unroll
+                  for (int y = 0; y < 32; y += 16) {
+                    float o[16];
+                    load16(k + y, o);
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) v[y + z] = o[z];
+                  }
+                } else {
+                  const float4* o = part_of(x) + k / 4 * kRows;
+#pragma unroll
+                  for (int y = 0; y < 8; ++y) {
+                    const float4 f = __ldcg(o + y * kRows);
+                    v[4 * y] = f.x;
+                    v[4 * y + 1] = f.y;
+                    v[4 * y + 2] = f.z;
+                    v[4 * y + 3] = f.w;
+                  }
+                }
+#pragma unroll
+                for (int y = 0; y < 32; ++y) acc[y] = fmaf(wx, v[y], acc[y]);
+              }
+              uint32_t w[16];
+#pragma unroll
+              for (int y = 0; y < 16; ++y) w[y] = pack(acc[2 * y], acc[2 * y + 1]);
+              put(w, 0, 4);
+              flush(std::integral_constant<int, 4>(), k);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) signal_leader(o_free);
         }
-        if (end) break;
-        m_done = m_ref;
-        l_done = l;
+        __syncwarp();
+        if (lane == 0) give(i);
       }
     }
     // both CTAs wait for the leader's products (also after an abort)
@@ -831,6 +884,15 @@ int launch_prompt_tc(const PromptArgs& a, const PromptScratch& ws, int clusters,
   const int which = a.f16 ? 2 : 1;
   if (dev < 0 || dev >= 64 || !(attr_done[dev] & which)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    // setmaxnreg.inc waits for registers that are free: never launch a build whose split does not add up
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e == cudaSuccess && fa.numRegs != kLaunchRegs) {
+      char buf[160];
+      snprintf(buf, sizeof buf, "prompt kernel built with %d registers per thread; its warpgroup split needs %d", fa.numRegs, kLaunchRegs);
+      set_tc_error(buf);
+      return -1;
+    }
     if (e == cudaSuccess && dev >= 0 && dev < 64) attr_done[dev] |= which;
   }
   // A graph replays its captured tag: the workspace's epoch word tells the replays apart.
