@@ -65,9 +65,10 @@ constexpr uint32_t kTile = 32768;            // a CTA's half of a tile of K or V
 constexpr uint32_t kOffQ = 0, kOffK = 4 * kQQuarter, kOffV = kOffK + kStages * kTile, kOffMisc = kOffV + kStages * kTile;
 constexpr uint32_t kTmemCols = 512, kColS = 0, kColP = 128, kPBufCols = 64, kColO = 256;
 
-// The cut, in keys: what a block costs a cluster beyond its keys (Q, first softmax, epilogue), the least of a
-// range, and the least tiles of a piece (a shorter one costs more in its merge than it saves).
-constexpr int kFixed = 320, kMinRange = 384, kMinPiece = 2;
+// The cut, in keys: what a block costs a cluster beyond its keys (Q, first and last softmax), and the least of a
+// range. A piece has at least kMinPiece tiles: writing and merging partials costs a cluster about what six tiles do.
+// There are as many ranges as blocks where those are small.
+constexpr int kFixed = 320, kMinPiece = 8, kMinRange = kFixed + kMinPiece * kKeys;
 
 struct Item {
   int q0, n;             // first token of the prompt, its length
@@ -86,8 +87,7 @@ struct Misc {
   alignas(8) uint64_t item_full[kRing], item_empty[kRing], stat_full[kRing];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full, q_empty, s_full, s_free, p_full[2][2], pv_done[2], o_ready, o_free, drain, never;
-  long long scan[kThreads / 32];
-  long long total;
+  long long scan[2][kThreads / 32];  // units, blocks
   long long start_off;   // units before the prompt the range starts in
   int start_seq;
   uint32_t tmem_base;
@@ -167,6 +167,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
 }
 
 // ------------------------------------------------------------------------------------ the cut --
@@ -257,27 +263,35 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
   // the units of all prompts, and the prompt this cluster's range starts in: each thread a run of prompts
   const int per = (a.num_seqs + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, a.num_seqs), s1 = min(s0 + per, a.num_seqs);
-  long long sum = 0;
+  long long sum = 0, blocks = 0;
   for (int s = s0; s < s1; ++s) {
     int q0;
-    sum += a.Hkv * units(blocks_of(prompt_len(a, s, &q0), tb), tb);
+    const int nb = blocks_of(prompt_len(a, s, &q0), tb);
+    blocks += nb;
+    sum += a.Hkv * units(nb, tb);
   }
   long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
+    blocks += __shfl_xor_sync(0xffffffffu, blocks, o);
   }
-  if (lane == 31) ms.scan[warp] = incl;
+  if (lane == 31) {
+    ms.scan[0][warp] = incl;
+    ms.scan[1][warp] = blocks;
+  }
   if (tid == 0) ms.start_seq = -1;
   tc_fence_before();
   __syncthreads();
   long long before = incl - sum, U = 0;
+  blocks = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += ms.scan[w];
-    U += ms.scan[w];
+    if (w < warp) before += ms.scan[0][w];
+    U += ms.scan[0][w];
+    blocks += ms.scan[1][w];
   }
-  const int C = (int)max(1LL, min((long long)(gridDim.x >> 1), U / kMinRange));
+  const int C = (int)max(1LL, min((long long)(gridDim.x >> 1), max(a.Hkv * blocks, U / kMinRange)));
   const bool work = cluster < C && U > 0;
   const long long u0 = work ? range_begin(cluster, U, C) : 0, u1 = work ? range_begin(cluster + 1, U, C) : 0;
   if (work && before <= u0 && u0 < before + sum) {
@@ -350,6 +364,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
               if (!ok) break;
               ms.item[i % kRing] = I;
               mbar_arrive(bar(ms.item_full[i % kRing]));
+              // Q can only be loaded once the item before has done with its own: bring it to L2 meanwhile
+              for (int qd = 0; qd < 4; ++qd) tma_prefetch_3d(&tmap_q, qd * 64, kvh * a.G, q0 + I.tok0 + rank * tpc);
               if (i >= 1) ok = mbar_wait(bar(ms.q_empty), (i - 1) & 1, abort_flag, a.err);
               if (!ok) break;
               mbar_expect_tx(bar(ms.q_full), (uint32_t)used * 512u);
@@ -716,13 +732,27 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           }
           __syncwarp();
         };
-        auto load16 = [&](int col, float (&v)[16]) {
-          tmem_ld16(o_addr + col, v);
+        auto load32 = [&](int col, float (&v)[32]) {
+          float x0[16], x1[16];
+          tmem_ld16(o_addr + col, x0);
+          tmem_ld16(o_addr + col + 16, x1);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] *= inv;
+          for (int x = 0; x < 16; ++x) {
+            v[x] = x0[x] * inv;
+            v[16 + x] = x1[x] * inv;
+          }
         };
         auto pack = [&](float x, float y) { return kF16 ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
+        // Have the other pieces of a cut block all arrived?
+        unsigned long long* counter = ws.counters + 2 * I.slot0 + rank;
+        if (I.nsplit > 1) {
+          if (gi == 0) {
+            ms.merge_flag = split_peek(counter) == (tag << 16 | (unsigned)(I.nsplit - 1));
+            __threadfence();
+          }
+          named_barrier(9, kEpiThreads);
+        }
         mbar_wait(bar(ms.o_ready), i & 1, abort_flag, a.err);
         tc_fence_after();
         if (I.nsplit == 1) {
@@ -730,17 +760,17 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           // overwrite it while the stores are still to come
           uint32_t w[80];
 #pragma unroll
-          for (int k = 0; k < kHeadDim; k += 16) {
-            float v[16];
-            load16(k, v);
-            uint32_t x8[8];
+          for (int k = 0; k < kHeadDim; k += 32) {
+            float v[32];
+            load32(k, v);
+            uint32_t p[16];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) x8[x] = pack(v[2 * x], v[2 * x + 1]);
+            for (int x = 0; x < 16; ++x) p[x] = pack(v[2 * x], v[2 * x + 1]);
             if (k < kStageCols) {
-              put(x8, k / 8, 2);
+              put(p, k / 8, 4);
             } else {
 #pragma unroll
-              for (int x = 0; x < 8; ++x) w[(k - kStageCols) / 2 + x] = x8[x];
+              for (int x = 0; x < 16; ++x) w[(k - kStageCols) / 2 + x] = p[x];
             }
           }
           tc_fence_before();
@@ -760,21 +790,15 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           auto part_of = [&](int x) {  // this row of a partial: four values every kRows * 4
             return reinterpret_cast<float4*>(ws.part_o) + (size_t)(2 * slot_of(x) + rank) * (kHeadDim / 4) * kRows + row;
           };
-          unsigned long long* counter = ws.counters + 2 * I.slot0 + rank;
-          if (gi == 0) {
-            ms.merge_flag = split_peek(counter) == (tag << 16 | (unsigned)(I.nsplit - 1));
-            __threadfence();
-          }
-          named_barrier(9, kEpiThreads);
           bool last = ms.merge_flag;
           if (!last) {
             float4* part = part_of(I.split);
 #pragma unroll 1
-            for (int k = 0; k < kHeadDim; k += 16) {
-              float v[16];
-              load16(k, v);
+            for (int k = 0; k < kHeadDim; k += 32) {
+              float v[32];
+              load32(k, v);
 #pragma unroll
-              for (int x = 0; x < 16; x += 4) part[(k + x) / 4 * kRows] = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+              for (int x = 0; x < 32; x += 4) part[(k + x) / 4 * kRows] = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
             }
             *lse_of(I.split) = lse;
             __threadfence();
@@ -796,31 +820,41 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             for (int x = 0; x < I.nsplit; ++x) total += exp2f((x == I.split ? lse : __ldcg(lse_of(x))) - M);
             const float scale = 1.f / total;  // (a token sees itself: some piece has weight 1)
             if (a.lse && valid) a.lse[lse_at] = (M + log2f(total)) * 0.6931471805599453f;
+            // the next 32 columns of another piece are on their way while these are added up
+            const int fx0 = I.split == 0 ? 1 : 0;
+            int fx = fx0, fk = 0;
+            float4 next[8];
+            auto fetch = [&]() {
+              const float4* o = part_of(fx) + fk / 4 * kRows;
+#pragma unroll
+              for (int y = 0; y < 8; ++y) next[y] = __ldcg(o + y * kRows);
+              ++fx;
+              fx += fx == I.split;
+              if (fx >= I.nsplit) {
+                fx = fx0;
+                fk += 32;
+              }
+            };
+            fetch();
 #pragma unroll 1
             for (int k = 0; k < kHeadDim; k += 32) {
               float acc[32] = {};
+#pragma unroll 1
               for (int x = 0; x < I.nsplit; ++x) {
-                const float wx = exp2f((x == I.split ? lse : __ldcg(lse_of(x))) - M) * scale;
                 float v[32];
                 if (x == I.split) {
-#pragma unroll
-                  for (int y = 0; y < 32; y += 16) {
-                    float o[16];
-                    load16(k + y, o);
-#pragma unroll
-                    for (int z = 0; z < 16; ++z) v[y + z] = o[z];
-                  }
+                  load32(k, v);
                 } else {
-                  const float4* o = part_of(x) + k / 4 * kRows;
 #pragma unroll
                   for (int y = 0; y < 8; ++y) {
-                    const float4 f = __ldcg(o + y * kRows);
-                    v[4 * y] = f.x;
-                    v[4 * y + 1] = f.y;
-                    v[4 * y + 2] = f.z;
-                    v[4 * y + 3] = f.w;
+                    v[4 * y] = next[y].x;
+                    v[4 * y + 1] = next[y].y;
+                    v[4 * y + 2] = next[y].z;
+                    v[4 * y + 3] = next[y].w;
                   }
+                  if (fk < kHeadDim) fetch();
                 }
+                const float wx = exp2f((x == I.split ? lse : __ldcg(lse_of(x))) - M) * scale;
 #pragma unroll
                 for (int y = 0; y < 32; ++y) acc[y] = fmaf(wx, v[y], acc[y]);
               }
@@ -911,11 +945,12 @@ int launch_prompt_tc(const PromptArgs& a, const PromptScratch& ws, int clusters,
   return 1;
 }
 
-// Clusters that a call of these sizes can use: its units, were all tokens one prompt's, over the least range.
+// Clusters that a call of these sizes can use: its blocks, or its units over the least range were all tokens one prompt's.
 int prompt_clusters(long long T, int num_seqs, int Hkv, int G, int sms) {
   const int tb = 2 * (kRows / G);
   const double b = (double)((T + tb - 1) / tb) + num_seqs;
-  const double most = Hkv * (b * kFixed + tb * b * (b + 1) / 2) / kMinRange;
+  const double ranges = Hkv * (b * kFixed + tb * b * (b + 1) / 2) / kMinRange;
+  const double most = ranges > Hkv * b ? ranges : Hkv * b;
   const int all = sms / 2;
   return most < 1 ? 1 : most < all ? (int)most : all;
 }
