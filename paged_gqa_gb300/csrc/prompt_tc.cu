@@ -68,7 +68,7 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColP = 128, kPBufCols = 64, kCol
 // The cut, in keys: what a block costs a cluster beyond its keys (Q, first and last softmax), and the least of a
 // range. A piece has at least kMinPiece tiles: writing and merging partials costs a cluster about what six tiles do.
 // There are as many ranges as blocks where those are small.
-constexpr int kFixed = 320, kMinPiece = 8, kMinRange = kFixed + kMinPiece * kKeys;
+constexpr int kFixed = 384, kMinPiece = 8, kMinRange = kFixed + kMinPiece * kKeys;
 
 struct Item {
   int q0, n;             // first token of the prompt, its length
