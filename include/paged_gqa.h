@@ -343,7 +343,7 @@ int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* posi
  *
  * The pages of all requests lie in a pool: row r of `pages` lists those of one request in order,
  * page_counts[r] of them; `free_pages` is a stack of the others, num_free[0] high. A step names a
- * row for each of its S requests:
+ * row for each of its S requests (8192 at most):
  *
  *   q_lens     [S]       int32  new tokens; -1: the request has ended and gives its pages back
  *   ctx_lens   [S]       int32  tokens it has in the cache already (not read where it has ended)

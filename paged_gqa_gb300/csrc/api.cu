@@ -1449,6 +1449,7 @@ int paged_gqa_build_tables(const pg_tensor* q_lens, const pg_tensor* ctx_lens, c
     return fail(PG_ERR_INVALID_ARG, "page_counts and page_counts_out must have an entry per row of pages");
   if (num_free->shape[0] != 1 || num_free_out->shape[0] != 1)
     return fail(PG_ERR_INVALID_ARG, "num_free and num_free_out must have one entry");
+  if (S > kMaxRequests) return fail(PG_ERR_UNSUPPORTED, "at most %d requests (got %lld)", kMaxRequests, S);
   if (S * ((W + 511) / 512 + 1) > INT32_MAX) return fail(PG_ERR_UNSUPPORTED, "sizes beyond the supported range");
   // in place: the very same entries
   const bool counts_same = page_counts_out->data == page_counts->data, free_same = num_free_out->data == num_free->data;

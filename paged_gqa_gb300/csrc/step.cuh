@@ -8,6 +8,9 @@ namespace pgqa {
 // Most 32-bit words of a token's mask (new tokens of a sequence: 32 a word).
 constexpr int kMaxMaskWords = 32;
 
+// Most requests of a step's block tables.
+constexpr int kMaxRequests = 8192;
+
 // Block tables and slot maps (tables.cu); strides in elements.
 struct TableArgs {
   const int32_t* q_lens;     // [S]

@@ -9,10 +9,12 @@
 // execution. query_start_loc is the prefix sum of the new tokens, the slot of a token at
 // position p is page * P + p % P.
 //
-// Two launches. The first, one CTA, does what needs every request: the prefix sums, the pages
-// given back and taken, the counts. The second copies the pool's rows into the batch's block
-// table and writes the slots, over as many CTAs as there are table rows; it is the one that
-// moves bytes (4 W per request), and starts as a programmatic dependent.
+// Two launches. The first, one CTA, does what needs every request: who has which row, the prefix sums,
+// the pages given back and taken, the counts. It is a chain of dependent reads, so a thread keeps what it has
+// read of its requests in registers, rows are told apart by a hash table in shared memory, one scan carries
+// all three sums, and what is copied in bulk is shared out over the warps. The second copies the pool's
+// rows into the batch's block table and writes the slots, over as many CTAs as there are table rows; it is the
+// one that moves bytes (4 W per request), and is resident before the first one ends.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -29,187 +31,225 @@ namespace {
 constexpr int kPoolThreads = 1024;
 constexpr int kFillThreads = 128;
 constexpr int kSegment = 512;  // table columns per CTA of the second launch: four per thread
+static_assert(kMaxRequests % kPoolThreads == 0, "requests per thread of the first launch");
 
-// Exclusive block-wide prefix sums of two values; *ta and *tb get the sums.
-__device__ void scan2(long long& a, long long& b, long long* ta, long long* tb) {
-  __shared__ long long sa[32], sb[32];
+struct Sums {
+  long long given, taken, tokens;
+};
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) {
+  return Sums{a.given + b.given, a.taken + b.taken, a.tokens + b.tokens};
+}
+__device__ __forceinline__ Sums shfl_up(Sums a, int o) {
+  return Sums{__shfl_up_sync(0xffffffffu, a.given, o), __shfl_up_sync(0xffffffffu, a.taken, o),
+              __shfl_up_sync(0xffffffffu, a.tokens, o)};
+}
+// Block-wide exclusive prefix sums; *all gets the sums.
+__device__ __forceinline__ Sums scan(Sums v, Sums* warps, Sums* all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long a0 = a, b0 = b;
+  Sums x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-    if (lane >= o) {
-      a += x;
-      b += y;
-    }
+    const Sums y = shfl_up(x, o);
+    if (lane >= o) x = x + y;
   }
-  if (lane == 31) {
-    sa[warp] = a;
-    sb[warp] = b;
-  }
+  if (lane == 31) warps[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    long long x = sa[lane], y = sb[lane];
+    Sums w = warps[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) {
-        x += u;
-        y += v;
-      }
+      const Sums y = shfl_up(w, o);
+      if (lane >= o) w = w + y;
     }
-    sa[lane] = x;
-    sb[lane] = y;
+    warps[lane] = w;
   }
   __syncthreads();
-  a += (warp ? sa[warp - 1] : 0) - a0;
-  b += (warp ? sb[warp - 1] : 0) - b0;
-  *ta = sa[31];
-  *tb = sb[31];
-  __syncthreads();  // sa and sb may be written again
+  *all = warps[31];
+  const Sums before = warp ? warps[warp - 1] : Sums{0, 0, 0};
+  return Sums{before.given + x.given - v.given, before.taken + x.taken - v.taken, before.tokens + x.tokens - v.tokens};
 }
 
-// Calls f(lane's value of x, i) for i < n of every lane in turn, the lanes of the warp sharing the i.
-template <typename F>
-__device__ __forceinline__ void warp_each(int n, F f) {
-  unsigned todo = __ballot_sync(0xffffffffu, n > 0);
-  while (todo) {
-    const int j = __ffs(todo) - 1;
-    todo &= todo - 1;
-    f(j, __shfl_sync(0xffffffffu, n, j));
+// Copies of page ids between a row of the pool and the stack. A few are made by the request's own thread;
+// longer ones become jobs of kJob ids, which the warps share.
+constexpr int kFew = 4, kJob = 256, kMaxJobs = 1024;
+struct Job {
+  int row, at, n, stack;  // ids pages[row][at ..), stack[stack ..) upwards (back) or downwards (taken)
+};
+struct Jobs {
+  int count;
+  Job job[kMaxJobs];
+};
+__device__ __forceinline__ void copy_ids(const TableArgs& a, const Job& j, bool back, int from, int step) {
+  int32_t* row = a.pages + (long long)j.row * a.pages_st + j.at;
+  for (int i0 = from; i0 < j.n; i0 += step * 8) {
+    int32_t v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * step;
+      if (i < j.n) v[k] = back ? row[i] : a.free_pages[j.stack - i];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * step;
+      if (i < j.n) {
+        if (back) a.free_pages[j.stack + i] = v[k];
+        else row[i] = v[k];
+      }
+    }
   }
 }
+__device__ __forceinline__ void copy_or_queue(const TableArgs& a, Jobs& jobs, const Job& j, bool back) {
+  if (j.n <= kFew) {
+    copy_ids(a, j, back, 0, 1);
+    return;
+  }
+  for (int i = 0; i < j.n; i += kJob) {
+    const Job part = {j.row, j.at + i, min(kJob, j.n - i), back ? j.stack + i : j.stack - i};
+    const int at = atomicAdd(&jobs.count, 1);
+    if (at < kMaxJobs) jobs.job[at] = part;
+    else copy_ids(a, part, back, 0, 1);
+  }
+}
+__device__ __forceinline__ void do_jobs(const TableArgs& a, const Jobs& jobs, bool back) {
+  const int n = min(jobs.count, kMaxJobs);
+  for (int i = threadIdx.x >> 5; i < n; i += kPoolThreads / 32) copy_ids(a, jobs.job[i], back, threadIdx.x & 31, 32);
+}
+
+struct PoolSmem {
+  Sums warps[32];
+  int flag, given, taken;
+  Jobs back, take;
+};
 
 }  // namespace
 
-// Every thread serves the same requests in each phase. A request's held pages are kept in its
-// entry of seq_lens in between (-1: flagged), since page_counts may be page_counts_out.
-__global__ void __launch_bounds__(kPoolThreads, 1) pool_kernel(TableArgs a) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  __shared__ int s_flag, s_free, s_given, s_taken;
-  if (tid == 0) {
-    s_flag = s_given = s_taken = 0;
-    int nf = *a.num_free;
-    if (nf < 0 || nf > a.F) {  // no such stack: nothing can be given back or taken
-      s_flag = 1;
-      nf = nf < 0 ? 0 : a.F;
-    }
-    s_free = nf;
+// Thread t serves `per` requests from t * per on, at most kPer. `slots`: entries of the hash table, a power of two,
+// twice the requests at least.
+template <int kPer>
+__global__ void __launch_bounds__(kPoolThreads, 1) pool_kernel(TableArgs a, int per, int slots) {
+  extern __shared__ __align__(16) unsigned char pool_smem[];
+  PoolSmem& sm = *reinterpret_cast<PoolSmem*>(pool_smem);
+  int* key = reinterpret_cast<int*>(&sm + 1);  // row of the pool (-1: none yet)
+  int* owner = key + slots;                    // the first request that names it
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
+  if (tid == 0) sm.flag = sm.given = sm.taken = sm.back.count = sm.take.count = 0;
+  int nf = *a.num_free;
+  int row[kPer], q[kPer], ctx[kPer], held[kPer];  // held: -1 where the request cannot be served
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int s = tid * per + i;
+    const bool there = i < per && s < a.S;
+    row[i] = there ? a.rows[s] : -1;
+    q[i] = there ? a.q_lens[s] : 0;
+    ctx[i] = there ? a.ctx_lens[s] : 0;
   }
-  // 1. the rows' counts; a request whose row or lengths cannot be is flagged
-  for (int s = tid; s < a.S; s += kPoolThreads) {
-    const int row = a.rows[s];
-    int held = 0;
-    if (row >= 0 && row < a.R) {
-      held = a.counts[row];
-      if (held < 0 || held > a.Wp) held = -1;
-    } else if (row != -1) {
-      held = -1;
-    }
-    a.seq_lens[s] = held;
-  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) held[i] = row[i] >= 0 && row[i] < a.R ? a.counts[row[i]] : row[i] == -1 ? 0 : -1;
   if (a.counts_out != a.counts)
     for (int r = tid; r < a.R; r += kPoolThreads) a.counts_out[r] = a.counts[r];
-  __syncthreads();
-  // 2. a row that two requests name belongs to the first of them: each puts its number there, the
-  // largest of INT_MAX - s stays
-  for (int s = tid; s < a.S; s += kPoolThreads)
-    if (a.rows[s] >= 0 && a.seq_lens[s] >= 0) atomicMax(a.counts_out + a.rows[s], INT_MAX - s);
-  __syncthreads();
-  for (int s = tid; s < a.S; s += kPoolThreads)
-    if (a.rows[s] >= 0 && a.seq_lens[s] >= 0 &&
-        *const_cast<volatile int*>(a.counts_out + a.rows[s]) != INT_MAX - s)
-      a.seq_lens[s] = -1;
-  __syncthreads();
-  // 3. ended requests give their pages back, on top of the stack, in the batch's order
-  long long base = 0;
-  const int nf = s_free;
-  for (int s0 = 0; s0 < a.S; s0 += kPoolThreads) {
-    const int s = s0 + tid;
-    int n = 0, row = -1;
-    bool mine = false;
-    if (s < a.S && a.rows[s] >= 0 && a.seq_lens[s] >= 0) {
-      row = a.rows[s];
-      mine = a.q_lens[s] == -1;
-      n = mine ? a.seq_lens[s] : 0;
-    }
-    long long off = n, none = 0, total, total2;
-    scan2(off, none, &total, &total2);
-    off += base + nf;
-    const bool fits = off + n <= a.F;
-    if (mine) {
-      a.counts_out[row] = fits ? 0 : n;
-      if (!fits) s_flag = 1;
-    }
-    if (!fits) n = 0;
-    if (n) atomicMax(&s_given, (int)(off + n) - nf);
-    warp_each(n, [&](int j, int nj) {
-      const int rj = __shfl_sync(0xffffffffu, row, j);
-      const int to = (int)__shfl_sync(0xffffffffu, off, j);
-      for (int i = lane; i < nj; i += 32) a.free_pages[to + i] = a.pages[(long long)rj * a.pages_st + i];
-    });
-    base += total;
+  for (int i = tid; i < slots; i += kPoolThreads) {
+    key[i] = -1;
+    owner[i] = INT_MAX;
   }
   __syncthreads();
-  // 4. the others take theirs; the first token of each
-  const int avail = nf + s_given;
-  long long tokens = 0;
-  base = 0;
-  for (int s0 = 0; s0 < a.S; s0 += kPoolThreads) {
-    const int s = s0 + tid;
-    int q = 0, row = -1, held = 0, take = 0;
-    long long L = 0;
-    bool ok = false;
-    if (s < a.S) {
-      const int given = a.q_lens[s];
-      row = a.rows[s];
-      held = a.seq_lens[s];
-      if (row == -1) {
-        if (given > 0) s_flag = 1;  // tokens of no request
-      } else {
-        q = max(given, 0);
-        if (given < -1 || held < 0) {
-          s_flag = 1;
-        } else if (given >= 0) {
-          const int ctx = a.ctx_lens[s];
-          L = (long long)ctx + q;
-          const long long need = (L + a.P - 1) >> a.p_shift;
-          ok = ctx >= 0 && L <= INT_MAX && need <= min(a.W, a.Wp);
-          if (ok) take = max(0, (int)need - held);
-        }
+  // a row that two requests name belongs to the first of them
+  bool flag = false;
+  int slot[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (held[i] > a.Wp || held[i] < 0) held[i] = -1;
+    slot[i] = -1;
+    if (row[i] < 0 || held[i] < 0) continue;
+    int h = (int)(((unsigned)row[i] * 2654435761u) >> 8) & (slots - 1);
+    for (;;) {  // (at most half of the table is taken)
+      const int k = atomicCAS(key + h, -1, row[i]);
+      if (k == -1 || k == row[i]) break;
+      h = (h + 1) & (slots - 1);
+    }
+    atomicMin(owner + h, tid * per + i);
+    slot[i] = h;
+  }
+  __syncthreads();
+  if (nf < 0 || nf > a.F) {  // no such stack: taken as the nearer end
+    flag = true;
+    nf = nf < 0 ? 0 : a.F;
+  }
+  // what each request gives, needs and brings
+  Sums mine = {0, 0, 0};
+  int take[kPer], give[kPer], ok[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (slot[i] >= 0 && owner[slot[i]] != tid * per + i) held[i] = -1;
+    take[i] = give[i] = ok[i] = 0;
+    if (row[i] == -1) {
+      flag |= q[i] > 0;  // tokens of no request
+      q[i] = 0;
+      continue;
+    }
+    flag |= held[i] < 0 || q[i] < -1;
+    if (held[i] >= 0 && q[i] == -1) {
+      give[i] = held[i];
+    } else if (held[i] >= 0 && q[i] >= 0) {
+      const long long L = (long long)ctx[i] + q[i], need = (L + a.P - 1) >> a.p_shift;
+      ok[i] = ctx[i] >= 0 && L <= INT_MAX && need <= min(a.W, a.Wp);
+      if (ok[i]) take[i] = max(0, (int)need - held[i]);
+    }
+    mine = mine + Sums{give[i], take[i], max(q[i], 0)};
+  }
+  Sums all;
+  const Sums start = scan(mine, sm.warps, &all);
+  // ended requests give their pages back, on top of the stack
+  Sums at = start;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const long long to = nf + at.given;
+    at.given += give[i];
+    if (row[i] >= 0 && held[i] >= 0 && q[i] == -1) {
+      const bool fits = to + give[i] <= a.F;
+      if (fits && give[i]) {
+        atomicMax(&sm.given, (int)(to + give[i]) - nf);
+        copy_or_queue(a, sm.back, Job{row[i], 0, give[i], (int)to}, true);
       }
+      flag |= !fits;
+      a.counts_out[row[i]] = fits ? 0 : held[i];
     }
-    long long first = take, tok = q, total, total_q;
-    scan2(first, tok, &total, &total_q);
-    first += base;
-    tok += tokens;
-    const bool mine = s < a.S && row >= 0 && held >= 0 && a.q_lens[s] != -1;  // its entry holds the mark of step 2
-    if (take && first + take > avail) {  // out of pages: this request, and those behind it that need some
-      take = 0;
-      ok = false;
-    }
-    if (mine) {
-      if (!ok) s_flag = 1;
-      a.counts_out[row] = held + take;
-    }
-    if (take) atomicMax(&s_taken, (int)(first + take));
-    if (s < a.S) {
-      a.seq_lens[s] = ok ? (int)L : 0;
-      a.qsl[s + 1] = (int)min(tok + q, (long long)INT_MAX);
-    }
-    warp_each(take, [&](int j, int nj) {
-      const int rj = __shfl_sync(0xffffffffu, row, j), hj = __shfl_sync(0xffffffffu, held, j);
-      const int from = avail - 1 - (int)__shfl_sync(0xffffffffu, first, j);
-      for (int i = lane; i < nj; i += 32) a.pages[(long long)rj * a.pages_st + hj + i] = a.free_pages[from - i];
-    });
-    base += total;
-    tokens += total_q;
   }
   __syncthreads();
+  do_jobs(a, sm.back, true);
+  __syncthreads();
+  // the others take theirs from the top
+  const int avail = nf + sm.given;
+  at = start;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int s = tid * per + i;
+    if (i >= per || s >= a.S) break;
+    const long long first = at.taken;
+    at.taken += take[i];
+    at.tokens += max(q[i], 0);
+    if (take[i] && first + take[i] > avail) {  // out of pages: this request, and those behind it that need some
+      take[i] = 0;
+      ok[i] = 0;
+    }
+    if (row[i] >= 0 && held[i] >= 0 && q[i] >= 0) {
+      flag |= !ok[i];
+      a.counts_out[row[i]] = held[i] + take[i];
+    }
+    if (take[i]) {
+      atomicMax(&sm.taken, (int)(first + take[i]));
+      copy_or_queue(a, sm.take, Job{row[i], held[i], take[i], avail - 1 - (int)first}, false);
+    }
+    a.seq_lens[s] = ok[i] ? ctx[i] + q[i] : 0;
+    a.qsl[s + 1] = (int)min(at.tokens, (long long)INT_MAX);
+  }
+  if (flag) sm.flag = 1;
+  __syncthreads();
+  do_jobs(a, sm.take, false);
   if (tid == 0) {
     a.qsl[0] = 0;
-    *a.num_free_out = avail - s_taken;
-    if (s_flag || tokens > a.T) atomicOr(a.err, kErrBounds);
+    *a.num_free_out = avail - sm.taken;
+    if (sm.flag || all.tokens > a.T) atomicOr(a.err, kErrBounds);
   }
 }
 
@@ -246,7 +286,23 @@ __global__ void __launch_bounds__(kFillThreads) table_fill_kernel(TableArgs a, i
 }
 
 cudaError_t launch_build_tables(const TableArgs& a, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(false, pool_kernel, 1, kPoolThreads, 0, stream, a);
+  int slots = 64;
+  while (slots < 2 * a.S) slots *= 2;
+  const size_t smem = sizeof(PoolSmem) + 2 * sizeof(int) * (size_t)slots;
+  static_assert(sizeof(PoolSmem) + 2 * sizeof(int) * 2 * kMaxRequests <= 232448, "hash table of the most requests");
+  const bool one = a.S <= kPoolThreads;  // a request per thread
+  auto kern = one ? pool_kernel<1> : pool_kernel<kMaxRequests / kPoolThreads>;
+  static int attr_done[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e = cudaSuccess;
+  if (dev < 0 || dev >= 64 || !(attr_done[dev] & (one ? 1 : 2))) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(sizeof(PoolSmem) + 2 * sizeof(int) * 2 * kMaxRequests));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] |= one ? 1 : 2;
+  }
+  e = launch_pdl(false, kern, 1, kPoolThreads, smem, stream, a, (a.S + kPoolThreads - 1) / kPoolThreads, slots);
   if (e != cudaSuccess) return e;
   if (a.S == 0) return a.T > 0 ? cudaMemsetAsync(a.slots, 0xff, sizeof(int32_t) * (size_t)a.T, stream) : cudaGetLastError();
   const int segments = a.W > 0 ? (a.W + kSegment - 1) / kSegment : 1;

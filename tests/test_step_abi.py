@@ -50,6 +50,8 @@ def _tables(page=16, **over):
     (dict(counts_out=FakeTensor((9,), I32, ptr=(5 << 24) + 4)), -1, "page_counts_out overlaps page_counts"),
     (dict(q=ints(4, 1)), -1, "expected 1 dims"),
     (dict(slots=FakeTensor((7,), I32, ptr=0)), -1, "null"),
+    (dict(q=ints(8193), ctx=ints(8193, at=2), rows=ints(8193, at=3), table=ints(8193, 20, at=8), lens=ints(8193, at=9), qsl=ints(8194, at=10)),
+     -2, "8192 requests"),
 ])
 def test_table_refusals(over, code, msg):
     assert _tables(**over) == code

@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("S,P,W,q_hi,ctx_hi", [
     (1, 16, 40, 1, 300), (7, 16, 40, 5, 300), (33, 64, 9, 9, 500), (300, 32, 40, 4, 1200), (1025, 128, 5, 3, 600), (2500, 16, 20, 1, 300),
-    (20, 16, 1300, 3, 20000)])
+    (8192, 16, 6, 2, 60), (20, 16, 1300, 3, 20000), (40, 128, 300, 1, 30000)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_tables(S, P, W, q_hi, ctx_hi, in_place):
     x = su.requests(S, S, P, W, q_hi, ctx_hi)
