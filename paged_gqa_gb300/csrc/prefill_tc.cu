@@ -277,64 +277,78 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     // ------------------------------------------------------------ MMA issuers
     // One thread cannot issue tcgen05.mma faster than about one per 44 ns, below the tensor
     // pipe's rate, so S = Q K^T and O += P V come from two warps. S(g) waits for the softmax
-    // to have loaded S(g-1); P.V(g) waits for P(g) and V(g).
-    if (lane == 0) {
+    // to have loaded S(g-1); P.V(g) waits for P(g) and V(g). The whole warp waits and one elected lane issues,
+    // which takes fewer cycles an instruction than a lane by itself; the lanes agree on every wait, since those
+    // that see an abort and those that do not must not part.
+    {
       const bool is_s = warp == 1;
       uint32_t g = 0;
       int ii = 0;
       bool ok = true;
+      auto waited = [&](const uint64_t& b, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, ptr.err));
+      };
       for (int it = item_begin; it < item_end && ok; ++it, ++ii) {
         const Item I = load_item(cp, ptr, it);
         for (int j = 0; j < I.ntiles && ok; ++j, ++g) {
           const uint32_t b = g & 1;
           if (is_s) {
-            if (j == 0 && !(ok = mbar_wait(bar(ms.q_full), ii & 1, abort_flag, ptr.err))) break;
+            if (j == 0 && !(ok = waited(ms.q_full, ii & 1))) break;
             const uint32_t st = g % kKStages;
-            if (!(ok = mbar_wait(bar(ms.k_full[st]), (g / kKStages) & 1, abort_flag, ptr.err))) break;
-            if (g >= 1 && !(ok = mbar_wait(bar(ms.s_free), (g - 1) & 1, abort_flag, ptr.err))) break;
+            if (!(ok = waited(ms.k_full[st], (g / kKStages) & 1))) break;
+            if (g >= 1 && !(ok = waited(ms.s_free, (g - 1) & 1))) break;
             tc_fence_after();
-            const uint64_t k0 = smem_desc(sbase + LY::kOffK + st * kKVTile, 16, 1024, kSw128);
+            if (elect_one()) {
+              const uint64_t k0 = smem_desc(sbase + LY::kOffK + st * kKVTile, 16, 1024, kSw128);
 #pragma unroll
-            for (int part = 0; part < LY::kQParts; ++part) {
-              const uint64_t q0 = smem_desc(sbase + LY::kOffQ + part * kQPart, 16, 1024, kSw128);
+              for (int part = 0; part < LY::kQParts; ++part) {
+                const uint64_t q0 = smem_desc(sbase + LY::kOffQ + part * kQPart, 16, 1024, kSw128);
 #pragma unroll
-              for (int kb = 0; kb < 8; ++kb) {
-                const uint32_t qoff = (kb >> 2) * kQHalf + (kb & 3) * 32, koff = (kb >> 2) * kKVHalf + (kb & 3) * 32;
-                mma_e4m3(tmem + kColS, q0 + (qoff >> 4), k0 + (koff >> 4), kIdescS, (part | kb) ? 1u : 0u);
+                for (int kb = 0; kb < 8; ++kb) {
+                  const uint32_t qoff = (kb >> 2) * kQHalf + (kb & 3) * 32, koff = (kb >> 2) * kKVHalf + (kb & 3) * 32;
+                  mma_e4m3(tmem + kColS, q0 + (qoff >> 4), k0 + (koff >> 4), kIdescS, (part | kb) ? 1u : 0u);
+                }
               }
+              mma_commit(bar(ms.s_full));
+              mma_commit(bar(ms.k_empty[st]));
+              if (j == I.ntiles - 1) mma_commit(bar(ms.q_free));
             }
-            mma_commit(bar(ms.s_full));
-            mma_commit(bar(ms.k_empty[st]));
-            if (j == I.ntiles - 1) mma_commit(bar(ms.q_free));
+            __syncwarp();
           } else {
             // the first P.V of an item overwrites O: the previous epilogue must be done
-            if (j == 0 && ii >= 1 && !(ok = mbar_wait(bar(ms.o_free), (ii - 1) & 1, abort_flag, ptr.err))) break;
+            if (j == 0 && ii >= 1 && !(ok = waited(ms.o_free, (ii - 1) & 1))) break;
             // one barrier per P buffer: P(g + 2) waits for P.V(g), so the softmax is never two
             // publications ahead of this wait
-            if (!(ok = mbar_wait(bar(ms.p_full[b]), (g >> 1) & 1, abort_flag, ptr.err))) break;
+            if (!(ok = waited(ms.p_full[b], (g >> 1) & 1))) break;
             const uint32_t st = g % kVStages;
-            if (!(ok = mbar_wait(bar(ms.v_full[st]), (g / kVStages) & 1, abort_flag, ptr.err))) break;
+            if (!(ok = waited(ms.v_full[st], (g / kVStages) & 1))) break;
             tc_fence_after();
-            // V as one N = 256 MN-major operand: d-half 1 is the second 128-byte atom, 16 KB on
-            const uint64_t v0 = smem_desc(sbase + LY::kOffV + st * kKVTile, kKVHalf, 1024, kSw128);
-            const uint32_t p_cols = tmem + kColP + b * kPBufCols;  // P of this tile
+            if (elect_one()) {
+              // V as one N = 256 MN-major operand: d-half 1 is the second 128-byte atom, 16 KB on
+              const uint64_t v0 = smem_desc(sbase + LY::kOffV + st * kKVTile, kKVHalf, 1024, kSw128);
+              const uint32_t p_cols = tmem + kColP + b * kPBufCols;  // P of this tile
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
+              for (int part = 0; part < 2; ++part) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_e4m3_ts(tmem + kColO, p_cols + part * kPCols + kk * 8, v0 + ((kk * 4096) >> 4), kIdescO,
-                            (j == 0 && part == 0 && kk == 0) ? 0u : 1u);
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_e4m3_ts(tmem + kColO, p_cols + part * kPCols + kk * 8, v0 + ((kk * 4096) >> 4), kIdescO,
+                              (j == 0 && part == 0 && kk == 0) ? 0u : 1u);
+              }
+              mma_commit(bar(ms.v_empty[st]));
+              mma_commit(bar(ms.pv_done[b]));
+              if (j == I.ntiles - 1) mma_commit(bar(ms.o_ready));
             }
-            mma_commit(bar(ms.v_empty[st]));
-            mma_commit(bar(ms.pv_done[b]));
-            if (j == I.ntiles - 1) mma_commit(bar(ms.o_ready));
+            __syncwarp();
           }
         }
       }
-      // Every MMA this thread issued has completed before the CTA may release TMEM.
+      // Every MMA this warp issued (its elected lane is always the same one) has completed before the CTA may
+      // release TMEM.
       uint64_t& drain = is_s ? ms.drain[0] : ms.drain[1];
-      mma_commit(bar(drain));
-      mbar_drain(bar(drain), 0, abort_flag, ptr.err);
+      if (elect_one()) {
+        mma_commit(bar(drain));
+        mbar_drain(bar(drain), 0, abort_flag, ptr.err);
+      }
     }
     __syncwarp();
   } else if (warp >= 2 && warp < kVProducerWarp) {
@@ -420,18 +434,27 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         }
         if (gi == 0) ms.qscale[pi] = 1.f;
       } else {
-        float amax = 0.f;
+        // all of the thread's 16 loads at once, and kept: one after another, and again for the split, they took
+        // these warps 19,500 cycles an item
+        uint4 v[8][2];
+#pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int c = gi + k * kSoftThreads, r = c >> 4, ch = c & 15;
+          v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
           if (r < I.nrows) {
             const uint4* s = reinterpret_cast<const uint4*>(src_of(r, ch));
-            const uint4 a = s[0], b = s[1];
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            v[k][0] = s[0];
+            v[k][1] = s[1];
+          }
+        }
+        float amax = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 f = bf2(w[i]);
-              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = bf2(w[i]);
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         }
         amax = warp_max(amax);
@@ -445,24 +468,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         if (amax > 0.f && isfinite(amax)) sig = 7 - (int)((__float_as_uint(amax) >> 23) & 0xff) + 127;
         sig = max(-100, min(100, sig));
         const float scale = ldexpf(1.f, sig);
+#pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int c = gi + k * kSoftThreads, r = c >> 4, ch = c & 15;
-          uint4 hv = make_uint4(0, 0, 0, 0), lv = make_uint4(0, 0, 0, 0);
-          if (r < I.nrows) {
-            const uint4* s = reinterpret_cast<const uint4*>(src_of(r, ch));
-            const uint4 a = s[0], b = s[1];
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            uint32_t hw[4], lw[4];
+          const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+          uint32_t hw[4], lw[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f0 = bf2(w[2 * i]), f1 = bf2(w[2 * i + 1]);
-              split4(f0.x * scale, f0.y * scale, f1.x * scale, f1.y * scale, hw[i], lw[i]);
-            }
-            hv = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-            lv = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          for (int i = 0; i < 4; ++i) {
+            const float2 f0 = bf2(w[2 * i]), f1 = bf2(w[2 * i + 1]);
+            split4(f0.x * scale, f0.y * scale, f1.x * scale, f1.y * scale, hw[i], lw[i]);
           }
-          *reinterpret_cast<uint4*>(dst_of(0, r, ch)) = hv;
-          *reinterpret_cast<uint4*>(dst_of(1, r, ch)) = lv;
+          *reinterpret_cast<uint4*>(dst_of(0, r, ch)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+          *reinterpret_cast<uint4*>(dst_of(1, r, ch)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
         }
         if (gi == 0) ms.qscale[pi] = ldexpf(1.f, -sig);
       }
