@@ -581,7 +581,7 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
         rb.nrows = I.nrows;
         rb.nsplit = I.nsplit;
         rb.slot_base = I.slot_base;
-        finish_split_block(p, ptr, cp, I.block, rb, gi, kSoftThreads, 10, &ms.merge_flag, ms.merge_w);
+        finish_split_block<kFused ? 0 : 8>(p, ptr, cp, I.block, rb, gi, kSoftThreads, 10, &ms.merge_flag, ms.merge_w);
       }
     }
     }  // !stalled

@@ -154,11 +154,13 @@ __device__ __forceinline__ bool split_arrive(unsigned long long* counter, int ns
 // ("Optimize Qwen3.5 MTP unified attention on gfx950": split-KV segments reduced by
 // a second pass). s_w is shared scratch of kMergeMaxSplits * kSlotRows floats.
 // Returns after the merge (if any) is complete.
-// kAtOnce: chunks of four columns a thread has in flight (six registers each).
-template <int kAtOnce = 8>
+// kAtOnce: chunks of four columns a thread has in flight, six registers and some code each; 0: a loop that is
+// short in code, for kernels of few tiles (the verify kernels fetch their code cold).
+template <int kAtOnce = 0>
 __device__ inline void merge_split_block(const Problem& p, const Pointers& ptr, const ClassPlan& cp,
                                          const RowBlock& rb, int tid, int nthreads, int bar_id, float* s_w);
 
+template <int kAtOnce = 0>
 __device__ inline void finish_split_block(const Problem& p, const Pointers& ptr, const ClassPlan& cp,
                                           int block_index, const RowBlock& rb, int tid, int nthreads,
                                           int bar_id, int* s_flag, float* s_w) {
@@ -169,7 +171,7 @@ __device__ inline void finish_split_block(const Problem& p, const Pointers& ptr,
     __threadfence();
   }
   named_barrier(bar_id, nthreads);
-  if (*s_flag) merge_split_block(p, ptr, cp, rb, tid, nthreads, bar_id, s_w);
+  if (*s_flag) merge_split_block<kAtOnce>(p, ptr, cp, rb, tid, nthreads, bar_id, s_w);
 }
 
 // The merge of finish_split_block, for a caller that has arrived itself (its arriving thread
@@ -203,42 +205,65 @@ __device__ inline void merge_split_block(const Problem& p, const Pointers& ptr, 
         if (i < ns) s_w[i * kSlotRows + r] = lse[i] * inv;
     }
     named_barrier(bar_id, nthreads);
-    // kAtOnce chunks a thread at a time, a piece's loads of all of them in flight (one after another they
-    // took 25 us for 128 rows of two pieces)
-    const int chunks = rb.nrows * (kHeadDim / 4);
-    for (int idx0 = tid; idx0 < chunks; idx0 += kAtOnce * nthreads) {
-      float4 acc[kAtOnce];
+    if constexpr (kAtOnce == 0) {
+#pragma unroll 4
+      for (int idx = tid; idx < rb.nrows * (kHeadDim / 4); idx += nthreads) {
+        const int r = idx / (kHeadDim / 4);
+        const int d = (idx % (kHeadDim / 4)) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < ns; ++i) {
+          const float w = s_w[i * kSlotRows + r];
+          const uint2 h = __ldcg(reinterpret_cast<const uint2*>(slot_o(cp, rb.slot_base + i) +
+                                                                (size_t)r * kHeadDim + d));
+          const float2 o01 = unpack_f16x2(h.x), o23 = unpack_f16x2(h.y);
+          acc.x += w * o01.x;
+          acc.y += w * o01.y;
+          acc.z += w * o23.x;
+          acc.w += w * o23.y;
+        }
+        const RowMap m = map_row(rb.row0 + r, p.G, rb.kvh);
+        uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(ptr.out) +
+                                              (size_t)(seq_q0 + m.t) * p.o_st + (size_t)m.h * p.o_sh + d);
+        *dst = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+      }
+    } else {
+      // kAtOnce chunks a thread at a time, a piece's loads of all of them in flight (one after another they
+      // took 25 us for 128 rows of two pieces)
+      const int chunks = rb.nrows * (kHeadDim / 4);
+      for (int idx0 = tid; idx0 < chunks; idx0 += kAtOnce * nthreads) {
+        float4 acc[kAtOnce > 0 ? kAtOnce : 1];
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < ns; ++i) {
-        const uint16_t* o = slot_o(cp, rb.slot_base + i);
-        uint2 h[kAtOnce];
+        for (int u = 0; u < kAtOnce; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < ns; ++i) {
+          const uint16_t* o = slot_o(cp, rb.slot_base + i);
+          uint2 h[kAtOnce > 0 ? kAtOnce : 1];
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          const int idx = idx0 + u * nthreads;
-          if (idx < chunks) h[u] = __ldcg(reinterpret_cast<const uint2*>(o + (size_t)idx * 4));
+          for (int u = 0; u < kAtOnce; ++u) {
+            const int idx = idx0 + u * nthreads;
+            if (idx < chunks) h[u] = __ldcg(reinterpret_cast<const uint2*>(o + (size_t)idx * 4));
+          }
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u) {
+            const int idx = idx0 + u * nthreads;
+            if (idx >= chunks) break;
+            const float w = s_w[i * kSlotRows + idx / (kHeadDim / 4)];
+            const float2 o01 = unpack_f16x2(h[u].x), o23 = unpack_f16x2(h[u].y);
+            acc[u].x += w * o01.x;
+            acc[u].y += w * o01.y;
+            acc[u].z += w * o23.x;
+            acc[u].w += w * o23.y;
+          }
         }
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
           const int idx = idx0 + u * nthreads;
           if (idx >= chunks) break;
-          const float w = s_w[i * kSlotRows + idx / (kHeadDim / 4)];
-          const float2 o01 = unpack_f16x2(h[u].x), o23 = unpack_f16x2(h[u].y);
-          acc[u].x += w * o01.x;
-          acc[u].y += w * o01.y;
-          acc[u].z += w * o23.x;
-          acc[u].w += w * o23.y;
+          const int r = idx / (kHeadDim / 4), d = idx % (kHeadDim / 4) * 4;
+          const RowMap m = map_row(rb.row0 + r, p.G, rb.kvh);
+          uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(ptr.out) +
+                                                (size_t)(seq_q0 + m.t) * p.o_st + (size_t)m.h * p.o_sh + d);
+          *dst = make_uint2(pack_bf16x2(acc[u].x, acc[u].y), pack_bf16x2(acc[u].z, acc[u].w));
         }
-      }
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int idx = idx0 + u * nthreads;
-        if (idx >= chunks) break;
-        const int r = idx / (kHeadDim / 4), d = idx % (kHeadDim / 4) * 4;
-        const RowMap m = map_row(rb.row0 + r, p.G, rb.kvh);
-        uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(ptr.out) +
-                                              (size_t)(seq_q0 + m.t) * p.o_st + (size_t)m.h * p.o_sh + d);
-        *dst = make_uint2(pack_bf16x2(acc[u].x, acc[u].y), pack_bf16x2(acc[u].z, acc[u].w));
       }
     }
     named_barrier(bar_id, nthreads);  // s_w may be reused right after

@@ -137,6 +137,12 @@ __device__ __forceinline__ Item load_item(const ClassPlan& cp, const Pointers& p
   return r;
 }
 
+// 16 bytes of global memory into shared memory, zeros where `there` is false.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ float2 bf2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
@@ -434,23 +440,23 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         }
         if (gi == 0) ms.qscale[pi] = 1.f;
       } else {
-        // all of the thread's 16 loads at once, and kept: one after another, and again for the split, they took
-        // these warps 19,500 cycles an item
-        uint4 v[8][2];
-#pragma unroll
+        // A chunk's 32 bytes land where its hi and lo parts go (16 each), all of a thread's chunks in flight, and are
+        // split in place. (Loaded one after another, and again for the split, they took these warps 19,500 cycles an
+        // item; kept in registers, 10,000 and the code of eight chunks, which a first item fetches cold.)
         for (int k = 0; k < 8; ++k) {
           const int c = gi + k * kSoftThreads, r = c >> 4, ch = c & 15;
-          v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-          if (r < I.nrows) {
-            const uint4* s = reinterpret_cast<const uint4*>(src_of(r, ch));
-            v[k][0] = s[0];
-            v[k][1] = s[1];
-          }
+          const bool there = r < I.nrows;
+          const uint8_t* s = there ? src_of(r, ch) : static_cast<const uint8_t*>(ptr.q);
+          cp_async16(smem_u32(dst_of(0, r, ch)), s, there);
+          cp_async16(smem_u32(dst_of(1, r, ch)), s + 16, there);
         }
+        cp_async_wait_all();
         float amax = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 8; ++k) {
-          const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+          const int c = gi + k * kSoftThreads, r = c >> 4, ch = c & 15;
+          const uint4 a = *reinterpret_cast<const uint4*>(dst_of(0, r, ch)), b = *reinterpret_cast<const uint4*>(dst_of(1, r, ch));
+          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float2 f = bf2(w[i]);
@@ -468,10 +474,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         if (amax > 0.f && isfinite(amax)) sig = 7 - (int)((__float_as_uint(amax) >> 23) & 0xff) + 127;
         sig = max(-100, min(100, sig));
         const float scale = ldexpf(1.f, sig);
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 8; ++k) {
           const int c = gi + k * kSoftThreads, r = c >> 4, ch = c & 15;
-          const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+          const uint4 a = *reinterpret_cast<const uint4*>(dst_of(0, r, ch)), b = *reinterpret_cast<const uint4*>(dst_of(1, r, ch));
+          const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
           uint32_t hw[4], lw[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -672,7 +679,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         rb.nrows = I.nrows;
         rb.nsplit = I.nsplit;
         rb.slot_base = I.slot_base;
-        finish_split_block(p, ptr, cp, I.block, rb, gi, kSoftThreads, 10, &ms.merge_flag, ms.merge_w);
+        finish_split_block<8>(p, ptr, cp, I.block, rb, gi, kSoftThreads, 10, &ms.merge_flag, ms.merge_w);
       }
     }
     }  // !stalled

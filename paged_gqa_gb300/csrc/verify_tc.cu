@@ -797,7 +797,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
           rb.nrows = I.nrows;
           rb.nsplit = I.nsplit;
           rb.slot_base = I.slot_base;
-          merge_split_block<2>(p, ptr, cp, rb, gi, kSoftThreads, 2, ms.merge_w);
+          merge_split_block(p, ptr, cp, rb, gi, kSoftThreads, 2, ms.merge_w);
         }
       }
 #pragma unroll
