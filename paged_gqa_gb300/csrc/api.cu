@@ -366,10 +366,12 @@ int run(const Validated& val, const pg_tensor* k, const pg_tensor* v, void* ws, 
   }
   int used = 0;
   bool prev_ev = false;  // an event was recorded after the previous class's kernel
-  for (int c = 0; c < kNumClasses; ++c) {
+  // (one sequence that is all prefill has no verify class: a tree call leaves that launch out)
+  const bool no_verify = p.mask_words > 0 && single_prefill && (fast_ok || bf16_ok);
+  for (int c = no_verify ? 1 : 0; c < kNumClasses; ++c) {
     bool done = false;
     cudaEvent_t ev0 = g_ev_start[c].load(), ev1 = g_ev_stop[c].load();
-    bool after_plan = false;  // this class's kernel directly follows the plan kernel
+    bool after_plan = c == 1 && no_verify;  // this class's kernel directly follows the plan kernel
     if (c == 1 && p.fused_verify) {
       e = launch_plan(p, ptr, cp[0], cp[1], false, !prev_ev, stream);
       if (e != cudaSuccess) return cuda_fail(e, "plan launch");
@@ -401,6 +403,11 @@ int run(const Validated& val, const pg_tensor* k, const pg_tensor* v, void* ws, 
     ++launched;
     if (ev1 && (e = cudaEventRecord(ev1, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
     prev_ev = ev1 != nullptr;
+  }
+  if (p.mask_words > 0 && (used & 6)) {  // the pieces of split blocks are joined behind the attention kernels
+    e = launch_tree_merge(p, ptr, cp[0], cp[1], used >> 1 & 3, !prev_ev, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "tree merge launch");
+    ++launched;
   }
   plan_info[0] = cp[0].num_ctas;
   plan_info[1] = cp[1].num_ctas;

@@ -205,7 +205,7 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
   }
   if (kFused) {
     __syncthreads();  // the sequences are staged
-    if (warp == 0) self_plan::plan_warp(p, fs, cp.num_ctas, lane, ms.fitem, ms.fseq, &ms.fcount);
+    if (warp == 0) self_plan::plan_warp<kTree>(p, fs, cp, lane, ms.fitem, ms.fseq, &ms.fcount);
     fence_proxy_async_smem();  // the scratch lies where the copies go
   }
   tc_fence_before();
@@ -573,6 +573,7 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
       mbar_arrive(bar(ms.o_free));
       if (split) {
         if (kh == 0 && valid) slot_lse(cp, slot)[row] = lr > 0.f ? m_ref - kSigma + log2f(lr) : -INFINITY;
+        if (kTree) continue;  // the merge kernel joins the pieces
         __threadfence();
         RowBlock rb;
         rb.seq = I.seq;

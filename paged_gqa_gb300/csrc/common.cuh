@@ -153,8 +153,12 @@ __host__ __device__ __forceinline__ bool mask_holds(const Problem& p, int qn) {
 //     two chunks   of 116-134 tokens on 787-4084 keys 59, 57, 47, 49
 // For prefill no value is the best everywhere: 4 is within 5 % of the best at contexts of 4096 and more (2:
 // 31 %), and loses up to 34 % at short ones. Batches that fill the SMs do not change.
-constexpr int kMinFewRows = 2, kMinVerify = 4, kMinPrefill = 4;
+// Tree calls, whose pieces a kernel of its own joins over all SMs: over 6, 4, 3, 2 units, one sequence of 700 keys
+// and 13 tokens of 16 heads 33, 30, 28, 26; of 4000 keys 37, 32, 31, 27; four of 2000 keys 35, 33, 32, 30; batches
+// that fill the SMs within 2 %.
+constexpr int kMinFewRows = 2, kMinVerify = 4, kMinPrefill = 4, kMinTree = 2;
 __host__ __device__ __forceinline__ int min_range_units(const Problem& p, int cls) {
+  if (p.mask_words > 0) return kMinTree;
   if (!p.kv_is_fp4) return kMinRangeUnits;
   if (cls == 1) return kMinPrefill;
   return (long long)p.T * p.G <= 16ll * p.num_seqs ? kMinFewRows : kMinVerify;

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kDThreads, 1) fp4_decode_kernel(Problem p, Poi
     self_plan::load(p, ptr, fs);
     if (p.unplanned && blockIdx.x == 0) self_plan::flag_invalid(p, ptr, fs);
     __syncthreads();
-    if (warp == 1) self_plan::plan_warp(p, fs, cp.num_ctas, lane, ms.fitem, ms.fseq, &ms.fcount);
+    if (warp == 1) self_plan::plan_warp<false>(p, fs, cp, lane, ms.fitem, ms.fseq, &ms.fcount);
   } else {
     item_begin = cp.cta_item_begin[blockIdx.x];
     item_end = cp.cta_item_begin[blockIdx.x + 1];

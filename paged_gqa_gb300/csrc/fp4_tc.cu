@@ -258,7 +258,7 @@ fp4_tc_kernel(Problem p, Pointers ptr, ClassPlan cp) {
   }
   if (kFused) {
     __syncthreads();  // the sequences are staged
-    if (warp == 1) self_plan::plan_warp(p, fs, cp.num_ctas, lane, ms.fitem, ms.fseq, &ms.fcount);
+    if (warp == 1) self_plan::plan_warp<false>(p, fs, cp, lane, ms.fitem, ms.fseq, &ms.fcount);
     fence_proxy_async_smem();  // the scratch lies where the copies go
   }
   tc_fence_before();

@@ -100,6 +100,10 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs& a, int sms, cudaStream_t stream);
 
+// Joins the pieces of the split blocks of tree attention (tree_merge.cu), of the classes in the bit set.
+cudaError_t launch_tree_merge(const Problem& p, const Pointers& ptr, const ClassPlan& c0, const ClassPlan& c1, int classes,
+                              bool dependent, cudaStream_t stream);
+
 // Warp-level MMA (mma.sync, tf32) kernel for one class's items; any dtype mix.
 cudaError_t launch_portable(const Problem& p, const Pointers& ptr, const ClassPlan& cp,
                             int block_rows, cudaStream_t stream);

@@ -671,6 +671,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
       mbar_arrive(bar(ms.o_free));
       if (split) {
         if (kh == 0 && valid) slot_lse(cp, slot)[row] = lr > 0.f ? m_ref - kSigma + log2f(lr) : -INFINITY;
+        if (kTree) continue;  // the merge kernel joins the pieces
         __threadfence();
         RowBlock rb;
         rb.seq = I.seq;

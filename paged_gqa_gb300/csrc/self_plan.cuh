@@ -88,8 +88,10 @@ __device__ __forceinline__ void flag_invalid(const Problem& p, const Pointers& p
 // x = block, y = sequence, z = first tile | tiles << 16, w = piece index | pieces << 15 |
 // (1 << 30 if the block's first CTA's range starts in an earlier block); fseq gets the
 // item's sequence {first token, q_len, L, 0}, so that no item load reads global memory.
-// *fcount gets the number of items.
-__device__ __forceinline__ void plan_warp(const Problem& p, Scratch& fs, int num_ctas, int lane, int4* fitem,
+// *fcount gets the number of items. kRecord (tree calls): the class's blocks and their number are written to the
+// workspace for the merge kernel, each by the CTA of its first piece.
+template <bool kRecord>
+__device__ __forceinline__ void plan_warp(const Problem& p, Scratch& fs, const ClassPlan& cp, int lane, int4* fitem,
                                           int4* fseq, int* fcount) {
   const int n = p.num_seqs;
   const int per = (n + 31) / 32;
@@ -104,7 +106,8 @@ __device__ __forceinline__ void plan_warp(const Problem& p, Scratch& fs, int num
   }
   const long long total = __shfl_sync(0xffffffffu, x, 31);
   const int U = (int)(total >> 16);
-  const int C = cut_ctas(U, num_ctas, min_range_units(p, 0));
+  if (kRecord && blockIdx.x == 0 && lane == 0) *cp.n_blocks = (int)(total & 0xffff) * p.Hkv;
+  const int C = cut_ctas(U, cp.num_ctas, min_range_units(p, 0));
   const int c = blockIdx.x;
   if (c >= C) {  // warp-uniform: no range (C = 0: no verify block at all)
     if (lane == 0) *fcount = 0;
@@ -147,6 +150,15 @@ __device__ __forceinline__ void plan_warp(const Problem& p, Scratch& fs, int num
     const int later = cut_begin(k, c0) < off ? 1 : 0;
     fitem[t] = make_int4(b, fs.fv_seq[j], (lo - real) | ((hi - lo) << 16), (c - c0) | (nsplit << 15) | (later << 30));
     fseq[t] = fs.seq[fs.fv_seq[j]];
+    if (kRecord && c == c0) {
+      RowBlock r{};
+      r.seq = fs.fv_seq[j];
+      r.kvh = kvh;
+      r.nrows = fs.seq[r.seq].y * p.G;
+      r.nsplit = nsplit;
+      r.slot_base = split_slot_base(c0, later);
+      cp.blocks[b] = r;
+    }
   }
   if (lane == 0) *fcount = cnt;
 }

@@ -262,7 +262,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   }
   if (kFused) {
     __syncthreads();  // the sequences are staged
-    if (warp == 1) self_plan::plan_warp(p, fs, cp.num_ctas, lane, ms.fitem, ms.fseq, &ms.fcount);
+    if (warp == 1) self_plan::plan_warp<kTree>(p, fs, cp, lane, ms.fitem, ms.fseq, &ms.fcount);
     fence_proxy_async_smem();  // the scratch lies where the copies go
   }
   tc_fence_before();
@@ -681,7 +681,12 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         fence_proxy_async_smem();
         named_barrier(1, kSoftThreads);
-        if (gi == 0) {
+        if (kTree && gi == 0) {  // the merge kernel joins the pieces
+          bulk_store(slot_o(cp, slot), smem_u32(stage), (uint32_t)I.nrows * kHeadDim * 2u);
+          bulk_store(slot_lse(cp, slot), smem_u32(ms.lse_stage), kVN * 4u);
+          bulk_commit();
+          bulk_wait_all();
+        } else if (gi == 0) {
           // the counter's current word travels while the partial is written
           const unsigned long long seen = split_peek(cp.counters + I.block);
           bulk_store(slot_o(cp, slot), smem_u32(stage), (uint32_t)I.nrows * kHeadDim * 2u);
@@ -719,7 +724,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
       }
       tc_fence_before();
       mbar_arrive(bar(ms.o_free));
-      if (split) {
+      if (split && !kTree) {
         if (it + 1 == item_end && I.nsplit <= kMergeMaxSplits) {
           // The CTA's last item: its Q, K, V and P buffers are idle (every tile consumed,
           // every MMA complete), so if this piece is the block's last, the merge bulk-loads
