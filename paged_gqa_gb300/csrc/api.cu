@@ -356,7 +356,10 @@ int run(const Validated& val, const pg_tensor* k, const pg_tensor* v, void* ws, 
   // A single sequence whose q_len x G rows exceed a verify block is all prefill (its q_len is
   // T): then the plan kernel goes first, as the verify kernel would only find nothing to do.
   const bool single_prefill = p.num_seqs == 1 && (long long)p.T * p.G > kVerifyRows;
-  p.fused_verify = (fast_ok || bf16_ok) && path != 3 && !single_prefill && (long long)p.num_seqs * p.Hkv <= kFusedMaxBlocks &&
+  // Trees of more rows than a verify block holds, on average, are mostly prefill class too.
+  const bool wide_trees = p.mask_words > 0 && (long long)p.T * p.G > (long long)kVerifyRows * p.num_seqs;
+  p.fused_verify = (fast_ok || bf16_ok) && path != 3 && !single_prefill && !wide_trees &&
+                   (long long)p.num_seqs * p.Hkv <= kFusedMaxBlocks &&
                    max_tiles < (1 << 16) &&
                    (long long)p.num_seqs * p.Hkv * (max_tiles + fixed_cost(0)) < (1LL << 31);
   if (!p.fused_verify) {
