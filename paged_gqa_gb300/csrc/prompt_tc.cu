@@ -176,13 +176,33 @@ __device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int c0, int c1
 }
 
 // ------------------------------------------------------------------------------------ the cut --
-struct Shape {
-  int tb;      // tokens of a block (both CTAs)
-  int blocks;  // of a prompt and kv head
+// Range c of C begins at unit floor(c U / C) = c q + floor(c r / C), U = q C + r: one 64-bit division a CTA. (By one
+// thread, the scheduler's divisions and a binary search took a small prompt 4900 cycles.)
+struct Cut {
+  long long U, q;
+  int C, r;
+  __device__ __forceinline__ long long begin(int c) const { return c * q + c * r / C; }
+  // the range that holds unit u, from an estimate
+  __device__ __forceinline__ int of(long long u) const {
+    int c = min(max((int)((float)u * (float)C / (float)U), 0), C - 1);
+    while (c > 0 && begin(c) > u) --c;
+    while (c + 1 < C && begin(c + 1) <= u) ++c;
+    return c;
+  }
 };
 __device__ __forceinline__ int blocks_of(int n, int tb) { return (n + tb - 1) / tb; }
 // Units of a prompt's first b blocks (of one kv head).
 __device__ __forceinline__ long long units(long long b, int tb) { return b * kFixed + tb * (b * (b + 1) / 2); }
+
+// The last of n blocks that begins at or before unit `off` of its prompt and kv head: the quadratic's root, corrected.
+__device__ __forceinline__ int block_at(long long off, int n, int tb) {
+  const float h = kFixed + 0.5f * tb;
+  int b = (int)((sqrtf(h * h + 2.f * tb * (float)off) - h) / tb);
+  b = min(max(b, 0), n - 1);
+  while (b > 0 && units(b, tb) > off) --b;
+  while (b + 1 < n && units(b + 1, tb) <= off) ++b;
+  return b;
+}
 
 // Length of prompt s; one that does not lie in [0, T) has none and is flagged by the first CTA.
 __device__ __forceinline__ int prompt_len(const PromptArgs& a, int s, int* q0) {
@@ -292,8 +312,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
     blocks += ms.scan[1][w];
   }
   const int C = (int)max(1LL, min((long long)(gridDim.x >> 1), max(a.Hkv * blocks, U / kMinRange)));
+  const Cut cut = {U, U / C, C, (int)(U % C)};
   const bool work = cluster < C && U > 0;
-  const long long u0 = work ? range_begin(cluster, U, C) : 0, u1 = work ? range_begin(cluster + 1, U, C) : 0;
+  const long long u0 = work ? cut.begin(cluster) : 0, u1 = work ? cut.begin(cluster + 1) : 0;
   if (work && before <= u0 && u0 < before + sum) {
     for (int s = s0; s < s1; ++s) {
       int q0;
@@ -331,22 +352,21 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           int s = ms.start_seq, q0, n = prompt_len(a, s, &q0), nb = blocks_of(n, tb);
           long long off = u0 - ms.start_off;
           const long long head_units = units(nb, tb);
-          int kvh = (int)(off / head_units), b = 0;
-          off -= kvh * head_units;
-          for (int step = 1 << 30; step; step >>= 1)  // the last block that begins at or before off
-            if (b + step < nb && units(b + step, tb) <= off) b += step;
+          int kvh = 0;
+          for (; off >= head_units; ++kvh) off -= head_units;
+          int b = block_at(off, nb, tb);
           long long u = u0 - off + units(b, tb);  // the block's first unit
           int i = 0;
           bool ok = true;
           while (ok && u < u1) {
             const int kv_end = min(n, (b + 1) * tb), tiles = (kv_end + kKeys - 1) / kKeys;
             const long long next = u + kFixed + (long long)(b + 1) * tb;
-            auto first_tile = [&](int c) { return cut_tile(range_begin(c, U, C) - u, tiles); };
+            auto first_tile = [&](int c) { return cut_tile(cut.begin(c) - u, tiles); };
             Item I;
             I.t0 = u < u0 ? first_tile(cluster) : 0;
             I.t1 = next > u1 ? first_tile(cluster + 1) : tiles;
             if (I.t0 < I.t1) {
-              int c0 = cta_of(u, U, C), c1 = cta_of(next - 1, U, C);
+              int c0 = u >= u0 ? cluster : cut.of(u), c1 = next <= u1 ? cluster : cut.of(next - 1);
               while (c0 < c1 && first_tile(c0 + 1) == 0) ++c0;
               while (c1 > c0 && first_tile(c1) == tiles) --c1;
               I.q0 = q0;
@@ -357,7 +377,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
               I.split = cluster - c0;
               I.nsplit = c1 - c0 + 1;
               // a cluster has at most one piece that continues a block (slot 2c) and one that begins one (2c + 1)
-              I.slot0 = 2 * c0 + (range_begin(c0, U, C) <= u ? 1 : 0);
+              I.slot0 = 2 * c0 + (cut.begin(c0) <= u ? 1 : 0);
               I.slot1 = 2 * (c0 + 1);
               I.slot = I.split == 0 ? I.slot0 : I.slot1 + 2 * (I.split - 1);
               if (i >= kRing) ok = mbar_wait(bar(ms.item_empty[i % kRing]), ((i / kRing) - 1) & 1, abort_flag, a.err);
