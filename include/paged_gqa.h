@@ -355,7 +355,8 @@ int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* posi
  *   num_free   [1]       int32  read; num_free_out [1] gets the new height (may be the same tensor)
  *   block_table [S, W]   int32  the first ceil(seq_lens[s] / P) pages of each request, then -1
  *   seq_lens   [S]       int32  ctx_lens + q_lens, 0 for ended requests and padding
- *   query_start_loc [S + 1]     prefix sums of the new tokens (none of ended requests and padding)
+ *   query_start_loc [S + 1]     prefix sums of the new tokens (none of ended requests and padding), 2^31 - 1
+ *                               at most
  *   slot_map   [T]       int32  page * P + slot of each new token; -1 behind the last one
  *
  * First the ended requests put their pages on the stack, in the batch's order; then, in that order
@@ -368,8 +369,8 @@ int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* posi
  * free pages (then the requests behind it get none either). So does a q_lens > 0 without a row, a
  * num_free outside [0, F] (taken as the nearer end), a stack that would pass F (that request keeps its
  * pages) and more new tokens than T (those from T on have no slot). A taken page id that is negative
- * or whose slots pass 2^31 - 1 has slots of -1 and sets it too. Apart from the two named pairs no
- * written tensor may share memory with another (refused). Allocates nothing; two launches.
+ * or whose slots pass 2^31 - 1 has slots of -1 and sets it too. Apart from the two named pairs the
+ * addresses of a written tensor, first to last, may meet no other's (refused). Allocates nothing; two launches.
  * (The pages describe no allocator.)
  */
 int paged_gqa_build_tables(const pg_tensor* q_lens, const pg_tensor* ctx_lens, const pg_tensor* rows, int page_size,
@@ -434,7 +435,8 @@ int paged_gqa_attn_tree_ex(const pg_tensor* q, const pg_tensor* k_cache, const p
  * paged_gqa_cache_keep -- after verification: the accepted new tokens' K and V move to the positions
  * right behind the context, in place, and the sequences get their new lengths.
  *
- *   k_cache, v_cache  [NB, P, Hkv, 256]  e4m3 or bf16, as in paged_gqa_cache_write
+ *   k_cache, v_cache  [NB, P, Hkv, 256]  e4m3 or bf16, rows as in paged_gqa_cache_write; they share no memory
+ *                              (refused; of two interleaved ones with unequal strides that is assumed)
  *   block_table, seq_lens, query_start_loc  as in paged_gqa_attn
  *   kept       [S, D]    int32  the accepted tokens' numbers among the sequence's new ones, increasing
  *   num_kept   [S]       int32  how many of them count, 0 .. min(D, q_len)
@@ -464,7 +466,8 @@ int paged_gqa_cache_keep(const pg_tensor* k_cache, const pg_tensor* v_cache, con
  *                              merges this attention with one over other keys
  *
  * Scores, the softmax's statistics and the sums of P.V are held in fp32; P is rounded to the inputs'
- * type before P.V. Rows behind query_start_loc[S] are left as they were. A sequence that does not lie in
+ * type before P.V. |softmax_scale q . k| may reach 2^25 (there an fp32 score is off by 2 itself; a row beyond it
+ * may be anything). Rows behind query_start_loc[S] are left as they were. A sequence that does not lie in
  * [0, T) is flagged (PG_ERR_DEVICE_BOUNDS) and its rows are left as they were. A NaN or infinity in V
  * reaches the tokens that see it, and may reach earlier ones of its prompt that share a block of rows
  * with one; no other prompt.
@@ -543,7 +546,8 @@ int paged_gqa_last_plan(int64_t* out8);
  * Profiling hook (process-wide): while set, every dense call (not sparse attention) records `start`
  * on its stream immediately before the attention kernel of class `cls` (0 = verify blocks,
  * 1 = prefill blocks) and `stop` immediately after it; a 4-bit call of at most 64 rows
- * (T * Hq / Hkv) has no kernel of class 1. Both are cudaEvent_t handles
+ * (T * Hq / Hkv) has no kernel of class 1, a tree call of one sequence of more than 64 rows none of
+ * class 0, and a call on whole prompts none of either. Both are cudaEvent_t handles
  * owned by the caller; pass NULLs to stop recording. Returns PG_OK or
  * PG_ERR_INVALID_ARG.
  */

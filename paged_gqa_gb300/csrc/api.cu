@@ -597,6 +597,48 @@ bool rows_meet(const pg_tensor* t, const void* p, long long n) {
   return base + 2 * lo < q + n && q < base + 2 * hi;
 }
 
+// Do two caches of one shape, each of disjoint (page, slot, head) rows, share bytes? Caches of one allocation with equal
+// strides (K and V interleaved at any level) are told apart exactly; otherwise intersecting ranges count as shared.
+bool caches_overlap(const pg_tensor* a, const pg_tensor* b, int size) {
+  long long str[3], last[3], ext[2] = {kHeadDim, kHeadDim};
+  int n = 0;
+  bool equal = true;
+  for (int i = 0; i < 3; ++i) {
+    if (a->shape[i] == 0) return false;
+    if (a->shape[i] == 1) continue;
+    equal &= a->stride[i] == b->stride[i];
+    ext[0] += (a->shape[i] - 1) * a->stride[i];
+    ext[1] += (a->shape[i] - 1) * b->stride[i];
+    int j = n++;
+    for (; j > 0 && str[j - 1] < a->stride[i]; --j) {  // from the largest stride down
+      str[j] = str[j - 1];
+      last[j] = last[j - 1];
+    }
+    str[j] = a->stride[i];
+    last[j] = a->shape[i] - 1;
+  }
+  const long long delta =
+      ((long long)reinterpret_cast<intptr_t>(b->data) - (long long)reinterpret_cast<intptr_t>(a->data)) / size;
+  if (delta >= ext[0] || -delta >= ext[1]) return false;
+  if (!equal) return true;
+  // is |delta + sum_i c_i str_i| < 256 for some -last_i <= c_i <= last_i? The strides nest, so at each level only the
+  // nearest multiples can be.
+  long long left[27] = {delta};
+  int count = 1;
+  for (int i = 0; i < n; ++i) {
+    long long next[27];
+    int m = 0;
+    for (int x = 0; x < count; ++x)
+      for (long long c = -left[x] / str[i] - 1, k = 0; k < 3; ++c, ++k)
+        if (c >= -last[i] && c <= last[i]) next[m++] = left[x] + c * str[i];
+    std::copy(next, next + m, left);
+    count = m;
+  }
+  for (int x = 0; x < count; ++x)
+    if (std::llabs(left[x]) < kHeadDim) return true;
+  return false;
+}
+
 int current_device(DeviceState** ds) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1594,8 +1636,7 @@ int paged_gqa_cache_keep(const pg_tensor* k_cache, const pg_tensor* v_cache, con
                        {query_start_loc, "query_start_loc"}, {kept, "kept"}, {num_kept, "num_kept"}};
   if ((st = check_apart(all, 1))) return st;
   if (Hkv < 1) return fail(PG_ERR_INVALID_ARG, "the caches have no kv head");
-  if (k_cache->data && k_cache->data == v_cache->data)
-    return fail(PG_ERR_INVALID_ARG, "k_cache and v_cache are the same memory");
+  if (caches_overlap(k_cache, v_cache, size)) return fail(PG_ERR_INVALID_ARG, "k_cache and v_cache overlap");
   if (S == 0) {
     t_last_error.clear();
     return PG_OK;

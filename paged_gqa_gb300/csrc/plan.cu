@@ -57,7 +57,7 @@ __device__ SeqInfo seq_info(const Problem& p, const Pointers& ptr, int s) {
   SeqInfo r;
   r.q0 = ptr.qsl[s];
   int q1 = ptr.qsl[s + 1];
-  r.qn = q1 - r.q0;
+  r.qn = q1 >= r.q0 ? q1 - r.q0 : -1;  // (a difference of any two ints could wrap to a small one)
   r.L = ptr.seq_lens[s];
   r.ok = (r.qn >= 0) && (r.q0 >= 0) && (q1 <= p.T) && (r.qn <= r.L) &&
          ((long long)r.L <= (long long)p.W * p.P) && mask_holds(p, r.qn);

@@ -59,6 +59,7 @@ constexpr int kKStages = 2;
 constexpr float kTau = 4.f;
 constexpr float kSigma = 4.f;
 constexpr float kMInit = -1.0e30f;
+constexpr float kExact = 1 << 20;  // scores up to here go unrounded into a tree call's exponents
 
 constexpr uint32_t kQHalf = kRows * 128;        // [128 rows][128 B]
 constexpr uint32_t kQPart = 2 * kQHalf;         // 32 KB
@@ -533,24 +534,30 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         // masked tiles hold scaled scores; unmasked tiles keep raw scores and take the
         // scale in the exponent's FFMA
         const bool need_mask = (key0 + kTileKeys > kv_hi) || (key0 + kTileKeys > (kTree ? ctx : min_lim + 1));
+        // (tree calls: large scores too, since P's exponent takes s c as it is and the reference takes it rounded: at
+        // 2^24 that is off by one, and P at the end of e4m3)
+        bool scaled = need_mask;
         float mx;
-        if (need_mask && kTree) {
-          uint32_t see[2] = {0u, 0u};  // this thread's 64 keys
-          if (mask) {
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-              see[w] = tree_bits(p, mask, tok, kbase + 32 * w - ctx) & low_bits(kv_hi - (kbase + 32 * w));
-          }
-#pragma unroll
-          for (int i = 0; i < kHalfKeys; ++i) t[i] = (see[i >> 5] >> (i & 31) & 1u) ? t[i] * c : -INFINITY;
-          mx = extreme_of<true>(t);
-        } else if (need_mask) {
-#pragma unroll
-          for (int i = 0; i < kHalfKeys; ++i) t[i] = (kbase + i <= hi_key) ? t[i] * c : -INFINITY;
-          mx = extreme_of<true>(t);
-        } else {
+        if (!need_mask) {
           // max of s c = c max(s) for c >= 0, c min(s) for c < 0
           mx = (c_pos ? extreme_of<true>(t) : extreme_of<false>(t)) * c;
+          if (kTree) scaled = __any_sync(0xffffffffu, fabsf(mx) > kExact);
+        }
+        if (scaled) {
+          if (kTree) {
+            uint32_t see[2] = {0u, 0u};  // this thread's 64 keys
+            if (mask) {
+#pragma unroll
+              for (int w = 0; w < 2; ++w)
+                see[w] = tree_bits(p, mask, tok, kbase + 32 * w - ctx) & low_bits(kv_hi - (kbase + 32 * w));
+            }
+#pragma unroll
+            for (int i = 0; i < kHalfKeys; ++i) t[i] = (see[i >> 5] >> (i & 31) & 1u) ? t[i] * c : -INFINITY;
+          } else {
+#pragma unroll
+            for (int i = 0; i < kHalfKeys; ++i) t[i] = (kbase + i <= hi_key) ? t[i] * c : -INFINITY;
+          }
+          mx = extreme_of<true>(t);
         }
         // the row's maximum over both key halves (partner: same lane, the other warp)
         ms.red[g & 1][kh][row] = mx;
@@ -566,7 +573,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         // P = 2^(s c - m + sigma) in f16, split into e4m3 hi + lo, 4 keys per word
         uint32_t ph[kHalfKeys / 4], pl[kHalfKeys / 4];
         const float off = m_ref - kSigma;
-        const float sc = need_mask ? 1.f : c;
+        const float sc = scaled ? 1.f : c;
         __half2 acc[4] = {__float2half2_rn(0.f), __float2half2_rn(0.f), __float2half2_rn(0.f),
                           __float2half2_rn(0.f)};
 #pragma unroll

@@ -58,8 +58,9 @@ __global__ void __launch_bounds__(kThreads) prompt_mma_kernel(PromptArgs a) {
     int start = 0, n = 0;
     if (s < a.num_seqs) {
       start = a.qsl[s];
-      n = a.qsl[s + 1] - start;
-      if (start < 0 || n < 0 || start + n > a.T) {
+      const int end = a.qsl[s + 1];
+      n = end - start;
+      if (start < 0 || end < start || end > a.T) {
         if (blockIdx.x == 0 && kvh == 0 && warp == 0) atomicOr(a.err, kErrBounds);
         n = 0;
       }

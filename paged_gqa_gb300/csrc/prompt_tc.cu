@@ -56,7 +56,7 @@ static_assert(kThreads * kLaunchRegs == 65536 && 256 * kSoftRegs + 128 * kEpiReg
 constexpr int kStages = 2;                   // of K, and of V
 constexpr int kRing = 3;                     // items known at a time: one in its epilogue, one at work, the next
 constexpr float kTau = 8.f;                  // a row's reference moves when a score exceeds it by this (log2)
-constexpr float kMInit = -1.0e30f;
+constexpr float kMInit = -3.0e38f;          // reference of a row before its first key
 
 constexpr uint32_t kQQuarter = kRows * 128;  // [128 rows][64 d]
 constexpr uint32_t kKQuarter = 64 * 128;     // [64 keys][64 d], four of them
@@ -678,7 +678,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             }
             fence_proxy_async_smem();
           }
-          // P = 2^(s c - m + sigma), 32 keys at a time: P.V of the first begins while the second are computed
+          // P = 2^(s c - m + sigma), 32 keys at a time: P.V of the first begins while the second are computed. m is a
+          // rounded s c, so P's largest value is off by 2^(m 2^-24), which cancels in the sums, but ends f16's range from
+          // |m| = 2^26 on (rounding s c first too, where m is large, cost 1.5 % in every form tried).
           tc_fence_after();
           const float off = m_ref - kSigma, sc = need_mask ? 1.f : c;
 #pragma unroll

@@ -48,7 +48,7 @@ struct Scratch {
 __device__ __forceinline__ void load(const Problem& p, const Pointers& ptr, Scratch& fs) {
   for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
     const int q0 = ptr.qsl[s], q1 = ptr.qsl[s + 1], L = ptr.seq_lens[s];
-    const int qn = q1 - q0;
+    const int qn = q1 >= q0 ? q1 - q0 : -1;
     long long v = 0;
     int tiles = 0;
     // the plan kernel's validity test; invalid sequences are flagged and zeroed there

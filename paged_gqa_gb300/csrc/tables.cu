@@ -268,12 +268,12 @@ __global__ void __launch_bounds__(kFillThreads) table_fill_kernel(TableArgs a, i
     const int c = seg * kSegment + i * kFillThreads + tid;
     if (c < a.W) dst[c] = c < need ? src[c] : -1;
   }
-  const int t0 = a.qsl[s], t1 = min(a.qsl[s + 1], a.T);
-  const int n = a.qsl[s + 1] - t0, ctx = L - n;
+  // (query_start_loc may pass T, up to 2^31 - 1: no token is counted from there)
+  const int t0 = min(a.qsl[s], a.T), t1 = min(a.qsl[s + 1], a.T), ctx = a.ctx_lens[s];
   for (int t = t0 + seg * kFillThreads + tid; t < t1; t += segments * kFillThreads) {
     int slot = -1;
     if (L > 0) {
-      const int pos = ctx + t - t0;
+      const int pos = ctx + (t - t0);
       const int page = src[pos >> a.p_shift];
       const long long x = (long long)page * a.P + (pos & (a.P - 1));
       if (page >= 0 && x <= INT_MAX) slot = (int)x;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kFillThreads) table_fill_kernel(TableArgs a, i
     a.slots[t] = slot;
   }
   if (s == a.S - 1)
-    for (int t = max(0, a.qsl[a.S]) + seg * kFillThreads + tid; t < a.T; t += segments * kFillThreads) a.slots[t] = -1;
+    for (int t = min(a.qsl[a.S], a.T) + seg * kFillThreads + tid; t < a.T; t += segments * kFillThreads) a.slots[t] = -1;
 }
 
 cudaError_t launch_build_tables(const TableArgs& a, cudaStream_t stream) {

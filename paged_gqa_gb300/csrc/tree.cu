@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(32 * kMaxMaskWords) tree_mask_kernel(TreeMaskA
   __shared__ int par[32 * kMaxMaskWords];
   const int s = blockIdx.x, t = threadIdx.x;
   const int q0 = a.qsl[s], q1 = a.qsl[s + 1], qn = q1 - q0, L = a.seq_lens[s];
-  if (q0 < 0 || qn < 0 || q1 > a.T || qn > L || qn > 32 * a.words) {
+  if (q0 < 0 || q1 < q0 || q1 > a.T || qn > L || qn > 32 * a.words) {
     if (t == 0) atomicOr(a.err, kErrBounds);
     for (int i = max(q0, 0) + t; i < min(q1, a.T); i += blockDim.x) {
       for (int w = 0; w < a.words; ++w) a.masks[(long long)i * a.masks_st + w] = 0;
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kKeepWarps * 32) cache_keep_kernel(KeepArgs a)
   const int which = part & 1, head = part >> 1;
   const int q0 = a.qsl[s], q1 = a.qsl[s + 1], qn = q1 - q0, L = a.seq_lens[s], n = a.num_kept[s];
   const bool first = part == 0 && lane == 0;
-  if (q0 < 0 || qn < 0 || qn > L || (long long)L > (long long)a.W * a.P) {
+  if (q0 < 0 || q1 < q0 || qn > L || (long long)L > (long long)a.W * a.P) {
     if (first) {
       atomicOr(a.err, kErrBounds);
       a.lens_out[s] = L;

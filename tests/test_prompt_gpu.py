@@ -174,3 +174,87 @@ def test_a_wait_that_runs_out_reports_timeout_and_the_next_call_is_correct():
     assert status == -4, pg.paged_gqa_last_error()
     out, lse = x.run()
     x.check(out, lse)
+
+
+def test_prompts_cut_into_many_pieces():
+    x = su.Prompt([9000, 3], 2, 1, seed=50)
+    out, lse = x.run()
+    x.check(out, lse, rows={0: [0, 127, 128, 255, 4097, 8191, 8448, 8999], 1: [0, 2]})
+    for _ in range(20):
+        again, ls = x.run(check=False)
+        assert torch.equal(again, out) and torch.equal(ls, lse)
+    assert pg.paged_gqa_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("path", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_of_2_to_the_25(path, dtype, sign):
+    """q and k are small whole numbers: scores are exact, and under a scale of 2^16 a row is V of its largest one's key."""
+    x = su.Prompt([600, 90], 8, 1, dtype, seed=60, fused=False)
+    gen = torch.Generator().manual_seed(60)
+    x.q, x.k = (torch.randint(-3, 4, t.shape, generator=gen).to(dtype).cuda() for t in (x.q, x.k))
+    x.scale = sign * 2.0 ** 16
+    prev = pg.paged_gqa_set_path(path)
+    try:
+        out, lse = x.run()
+    finally:
+        pg.paged_gqa_set_path(prev)
+    seen = 0
+    for s, n in enumerate(x.lens):
+        at = x.qsl[s]
+        for h in range(8):
+            score = sign * (x.q[at:at + n, h].double() @ x.k[at:at + n, 0].double().T)
+            score = score.masked_fill(torch.ones(n, n, device="cuda").triu(1).bool(), -1e9)
+            top = score.topk(min(n, 2), dim=1)
+            alone = top.values[:, 0] > top.values[:, 1]
+            seen += int(alone.sum())
+            # the row's one P is 2^x with |x| up to half a step of the reference, rounded once (u) over its unrounded self,
+            # times V, rounded once (u): in f16 two halves of V's values below 2^-14 as well
+            got, want = out[at:at + n, h][alone].double(), x.v[at:at + n, 0][top.indices[:, 0]][alone].double()
+            assert ((got - want).abs() <= 2.1 * su.U[dtype] * want.abs() + (2.0 ** -24 if dtype is torch.float16 else 0)).all()
+            # fp32 products and a rounding each: 2^-22 of the largest
+            want = top.values[:, 0] * 2.0 ** 16
+            assert ((lse[at:at + n, h].double() - want).abs() <= 2.0 ** -22 * want.abs() + 2.0).all()
+    assert seen > 8 * 500
+
+
+def test_rows_far_apart():
+    """Tokens 2^28 elements apart: offsets of more than 32 bits, beyond 2^31 elements."""
+    dtype, T = torch.bfloat16, 12
+    x = su.Prompt([9, 3], 4, 2, dtype, seed=61, fused=False)
+    step = 2 ** 28
+    space = torch.empty((T - 1) * step + 4096, dtype=dtype, device="cuda")
+    far = [space[i * 1024:].as_strided((T, h, 256), (step, 256, 1)) for i, h in enumerate((4, 2, 2, 4))]
+    for f, t in zip(far, (x.q, x.k, x.v)):
+        f.copy_(t)
+    x.q, x.k, x.v = far[:3]
+    out, lse = x.run(out=far[3])
+    assert pg.paged_gqa_last_plan()["path_bits"] == 256
+    x.check(out, lse)
+    prev = pg.paged_gqa_set_path(1)
+    try:
+        out, lse = x.run(out=far[3].zero_())
+    finally:
+        pg.paged_gqa_set_path(prev)
+    x.check(out, lse)
+
+
+@pytest.mark.parametrize("qsl", [[0, 2 ** 31 - 1, -2 ** 31], [-2 ** 31, 2 ** 31 - 1, 2 ** 31 - 1], [0, 41, 40], [-1, 0, 0]])
+@pytest.mark.parametrize("path", [0, 1])
+def test_starts_from_nowhere_are_flagged(path, qsl):
+    x = su.Prompt([20, 20], 8, 1, seed=62)
+    x.qsl_t = torch.tensor(qsl, dtype=torch.int32, device="cuda")
+    prev = pg.paged_gqa_set_path(path)
+    try:
+        out, _ = x.run(check=False)
+    finally:
+        pg.paged_gqa_set_path(prev)
+    assert pg.paged_gqa_check_device_errors() == -5
+    assert torch.isnan(out).all()
+
+
+def test_no_prompt_at_all():
+    x = su.Prompt([0, 0, 0], 8, 1, behind=30)
+    out, lse = x.run()
+    assert torch.isnan(out).all() and torch.isnan(lse).all()

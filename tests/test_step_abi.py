@@ -129,7 +129,7 @@ def _keep(**over):
     (dict(k=FakeTensor((10, 20, 2, 256), U8), v=FakeTensor((10, 20, 2, 256), U8, ptr=1 << 30)), -2, "page size"),
     (dict(k=FakeTensor((10, 16, 2, 256), U8, stride=[8192, 512, 0, 1])), -1, "overlap"),
     (dict(k=FakeTensor((10, 16, 2, 256), U8, stride=[8200, 512, 256, 1])), -1, "16 bytes"),
-    (dict(v=FakeTensor((10, 16, 2, 256), U8, ptr=1 << 20)), -1, "same memory"),
+    (dict(v=FakeTensor((10, 16, 2, 256), U8, ptr=1 << 20)), -1, "k_cache and v_cache overlap"),
     (dict(kept=ints(3, 4, at=4)), -1, "must match seq_lens"),
     (dict(num=ints(3, at=5)), -1, "must match seq_lens"),
     (dict(lens_out=ints(2, at=2)), -1, "seq_lens_out overlaps seq_lens"),
@@ -185,3 +185,37 @@ def test_empty_batches_are_no_ops():
     assert _keep(bt=ints(0, 5), lens=z, qsl=one, kept=ints(0, 3), num=z, lens_out=z) == 0
     kv = FakeTensor((0, 2, 256), BF)
     assert _prompt(q=FakeTensor((0, 8, 256), BF), k=kv, v=kv, qsl=one, out=FakeTensor((0, 8, 256), BF), lse=None) == 0
+
+
+def _row_starts(ptr, strides, shape):
+    return {ptr + b * strides[0] + p * strides[1] + h * strides[2] for b in range(shape[0]) for p in range(shape[1]) for h in range(shape[2])}
+
+
+def test_keep_tells_interleaved_caches_from_overlapping_ones():
+    import itertools
+    import random
+    r = random.Random(1)
+    shape, base, seen = (3, 16, 2), 1 << 20, [0, 0]
+    for order in itertools.permutations(range(3)):  # which dim is outermost
+        for gap in (0, 256):
+            strides, at = [0, 0, 0], 256 + gap
+            for d in reversed(order):
+                strides[d] = at
+                at = at * shape[d] + r.choice([0, 256 + gap])
+            for delta in [256, 512, 16, strides[0], strides[1], strides[2], strides[1] - 256, at, at + 16, at - 256] + [
+                    16 * r.randrange(0, at // 16) for _ in range(12)]:
+                a, b = _row_starts(base, strides, shape), _row_starts(base + delta, strides, shape)
+                every = sorted([(x, 0) for x in a] + [(x, 1) for x in b])
+                want = any(y[0] - x[0] < 256 and x[1] != y[1] for x, y in zip(every, every[1:]))
+                st = strides + [1]
+                _keep(k=FakeTensor((*shape, 256), U8, ptr=base, stride=st), v=FakeTensor((*shape, 256), U8, ptr=base + delta, stride=st))
+                assert ("k_cache and v_cache overlap" in pg.paged_gqa_last_error()) == want, (order, gap, delta)
+                seen[want] += 1
+    assert min(seen) > 20
+
+
+def test_keep_refuses_caches_of_unequal_strides_in_one_range():
+    st = [8192 * 2, 512, 256, 1]
+    assert _keep(k=FakeTensor((10, 16, 2, 256), U8, ptr=1 << 20, stride=st),
+                 v=FakeTensor((10, 16, 2, 256), U8, ptr=(1 << 20) + 8192, stride=[8192 * 2, 256, 4096, 1])) == -1
+    assert "k_cache and v_cache overlap" in pg.paged_gqa_last_error()

@@ -389,3 +389,256 @@ def test_a_step_as_it_is_used():
     pg.paged_gqa_build_tables(i32([1] * S), new_lens, i32(rows), P, pages_t, counts_t, free_t, num_t, table, lens, qsl, slots)
     assert lens.tolist() == [n + 1 for n in new_lens.tolist()] and qsl.tolist() == list(range(S + 1))
     assert pg.paged_gqa_check_device_errors() == 0, pg.paged_gqa_last_error()
+
+
+# ------------------------------------------------------------------- what the calls above leave out --
+
+def test_tables_of_more_tokens_than_31_bits_count():
+    big = 2 ** 31 - 1
+    x = dict(q_lens=[4, big, big, 3], ctx_lens=[5, 0, 0, 14], rows=[3, 1, 2, 0], page_size=16,
+             pages=[[7], [-1], [-1], [5]], counts=[1, 0, 0, 1], free=[1, 2, 3], num_free=3)
+    for row in x["pages"]:
+        row += [-1]
+    got, status = su.run_tables(x, 2, 9)
+    assert status == -5
+    assert got["lens"] == [9, 0, 0, 17] and got["qsl"] == [0, 4, big, big, big]
+    assert got["slots"] == [5 * 16 + 5 + i for i in range(4)] + [-1] * 5
+    assert got["table"] == [[5, -1], [-1, -1], [-1, -1], [7, 3]] and got["num_free"] == [2]
+
+
+@pytest.mark.parametrize("qsl", [[2 ** 31 - 1, -2 ** 31], [-2 ** 31, 2 ** 31 - 1], [5, 2], [0, 2 ** 31 - 1], [-1, 0]])
+def test_starts_from_nowhere_are_flagged(qsl):
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    masks, pos = torch.full((6, 1), -7, dtype=torch.int32, device="cuda"), torch.full((1, 6), -7, dtype=torch.int32, device="cuda")
+    pg.paged_gqa_tree_masks(i32([-1] * 6), i32([2 ** 31 - 1]), i32(qsl), masks, pos)
+    assert pg.paged_gqa_check_device_errors() == -5
+    x = su.Tree([(5, 30)], 4, 1, 16, seed=2)
+    before = x.k.view(torch.uint8).clone()
+    x.qsl_t = i32(qsl)
+    assert _keep(x, [[1, 3]], [2], 2) == [30]
+    assert pg.paged_gqa_check_device_errors() == -5 and torch.equal(before, x.k.view(torch.uint8))
+    for path in (0, 3, 1):
+        prev = pg.paged_gqa_set_path(path)
+        try:
+            x.run(check=False)
+        finally:
+            pg.paged_gqa_set_path(prev)
+        assert pg.paged_gqa_check_device_errors() == -5
+
+
+# e4m3 and bf16 caches, rows of both classes; "many": more row blocks than the verify kernel plans by itself
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("seqs,hq,hkv", [([(0, 0), (5, 60), (0, 33), (3, 3), (0, 0)], 8, 1), ([(3, 70), (1, 1), (8, 20)] * 100, 8, 2),
+                                         ([(0, 9), (70, 600), (0, 1)], 4, 1)])
+def test_padded_and_many_sequences(seqs, hq, hkv, cache):
+    x = su.Tree(seqs, hq, hkv, 16, cache, seed=13)
+    ref = x.reference()
+    for path in (0, 3):
+        prev = pg.paged_gqa_set_path(path)
+        try:
+            su.compare(x.run(), ref, f"{cache} path {path}")
+        finally:
+            pg.paged_gqa_set_path(prev)
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("seqs,hq,hkv", [([(8, 40000)], 8, 1), ([(60, 12000)], 8, 1), ([(2, 30000), (33, 9000)], 16, 2)])
+def test_blocks_of_many_pieces_and_the_same_bits_again(seqs, hq, hkv, cache):
+    x = su.Tree(seqs, hq, hkv, 64, cache, seed=17)
+    first = x.run()
+    su.compare(first, x.reference(), cache)
+    for _ in range(40):
+        assert torch.equal(x.run(check=False), first)
+    assert pg.paged_gqa_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+@pytest.mark.parametrize("seqs", [[(40, 900)], [(5, 700), (3, 90)], [(40, 900), (5, 700)]])
+def test_a_tree_wait_that_runs_out_reports_timeout_and_the_next_call_is_correct(seqs, cache):
+    x = su.Tree(seqs, 8, 1, 16, cache, seed=21)
+    prev = pg.paged_gqa_set_stall_test(200_000)
+    try:
+        x.run(check=False)
+        status = pg.paged_gqa_check_device_errors()
+    finally:
+        pg.paged_gqa_set_stall_test(prev)
+    assert status == -4, pg.paged_gqa_last_error()
+    su.compare(x.run(), x.reference(), cache)
+
+
+def whole_numbers(x, gen):
+    """q and k as small whole numbers: scores are exact, and under a scale of 2^26 a row is V of its largest one's key."""
+    for name, t in (("q", x.q), ("k", x.k)):
+        setattr(x, name, torch.randint(-3, 4, t.shape, generator=gen).to(torch.bfloat16).to(t.dtype).to(t.device))
+    x.scale = 2.0 ** 26
+
+
+@pytest.mark.parametrize("path", [0, 1])
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_scores_of_2_to_the_34(path, cache):
+    x = su.Tree([(40, 600), (5, 400), (3, 300)], 8, 2, 16, cache, seed=23, masks="all")
+    nan = torch.isnan(x.k.float())
+    whole_numbers(x, torch.Generator().manual_seed(23))
+    k = x.k.float()
+    x.k = k.masked_fill(nan, float("nan")).to(x.k.dtype)
+    prev = pg.paged_gqa_set_path(path)
+    try:
+        out = x.run().float()
+    finally:
+        pg.paged_gqa_set_path(prev)
+    seen = 0
+    for s, (n, L) in enumerate(x.seqs):
+        ids = x.table[s, :-(-L // 16)].long()
+        for h in range(8):
+            ks, vs = (c.float()[ids, :, h // 4].reshape(-1, 256)[:L] for c in (x.k, x.v))
+            score = x.q[x.qsl[s]:x.qsl[s + 1], h].double() @ ks.double().T
+            score = score.masked_fill(torch.arange(L, device="cuda") > L - n + torch.arange(n, device="cuda")[:, None], -1e9)
+            top = score.topk(2, dim=1)
+            alone = top.values[:, 0] > top.values[:, 1]
+            seen += int(alone.sum())
+            got, want = out[x.qsl[s]:x.qsl[s + 1], h][alone], (vs[top.indices[:, 0]] * x.v_descale)[alone]
+            # V itself, except that the pieces of a split sequence are held in f16: exact from 2^-14 on (bf16 has 8
+            # bits, f16 11), below that off by 2^-25, and then rounded to bf16 by at most 2^-8 of 2^-14
+            small = want.abs() < 2.0 ** -14
+            assert torch.equal(got[~small], want[~small])
+            assert ((got - want)[small].abs() <= 2.0 ** -25 + 2.0 ** -22).all()
+    assert seen > 8 * 40
+
+
+def test_offsets_beyond_32_bits():
+    """Caches of 10 GB each, a table, masks and rows of more than 2^31 elements apart."""
+    P, hkv, NB = 128, 16, 20000
+    dev = "cuda"
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device=dev)  # noqa: E731
+    gen = torch.Generator().manual_seed(3)
+    n, L, hq = 9, 200, 16
+    ids = [19999, 19990]
+    space = torch.empty(2, NB, P, hkv, 256, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+    k, v = space[0], space[1]
+    rows = [torch.randn(2 * P, hkv, 256, generator=gen).to(torch.float8_e4m3fn).to(dev) for _ in range(2)]
+    for c, x in zip((k, v), rows):
+        c[ids] = x.view(2, P, hkv, 256)
+    far = torch.empty(2 * 2 ** 31 + 4096, dtype=torch.int32, device=dev)
+    table = far[:2 ** 31 + 4].as_strided((2, 2), (2 ** 31, 1))
+    table.copy_(i32([[0, 1], ids]))
+    masks = far[8:].as_strided((n, 1), (2 ** 28 + 2 ** 10, 1))
+    par = su.parents(random.Random(1), n)
+    lens, qsl = i32([0, L]), i32([0, 0, n])
+    pos = torch.empty(1, n, dtype=torch.int32, device=dev)
+    pg.paged_gqa_tree_masks(i32(par), lens, qsl, masks, pos)
+    want_masks, want_pos = step.tree_masks(par, [L], [0, n], 1)
+    assert masks.tolist() == want_masks and pos.tolist() == [want_pos]
+    q = torch.randn(n, hq, 256, generator=gen).bfloat16().to(dev)
+    out = torch.empty_like(q)
+    pg.paged_gqa_attn_tree(q, k, v, table, lens, qsl, masks, 1.0, 1.0, 1 / 16, out)
+    assert pg.paged_gqa_check_device_errors() == 0
+    seen = step.tree_seen(want_masks, n, L)
+    ref = np.zeros((n, hq, 256))
+    qd, kd, vd = q.double().cpu().numpy(), rows[0].double().cpu().numpy(), rows[1].double().cpu().numpy()
+    for h in range(hq):
+        ref[:, h] = step.attention(qd[:, h], kd[:L, h], vd[:L, h], seen, 1 / 16)[0]
+    su.compare(out, ref, "far")
+    kept = far[16:].as_strided((2, 3), (2 ** 31 + 64, 1))
+    kept.copy_(i32([[0, 0, 0], [1, 4, 8]]))
+    new = torch.empty(2, dtype=torch.int32, device=dev)
+    pg.paged_gqa_cache_keep(k, v, table, lens, qsl, kept, i32([0, 3]), new)
+    assert pg.paged_gqa_check_device_errors() == 0 and new.tolist() == [0, L - n + 3]
+    for c, x in zip((k, v), rows):
+        want = x.view(torch.uint8).clone()
+        for i, a in enumerate([1, 4, 8]):
+            want[L - n + i] = x.view(torch.uint8)[L - n + a]
+        assert torch.equal(c.view(torch.uint8)[ids].view(2 * P, hkv, 256), want)
+    # tables and a pool with rows that far apart
+    pages, table = far.as_strided((2, 3), (2 ** 31 + 8, 1)), far[2 ** 31 + 64:].as_strided((2, 3), (2 ** 31 + 8, 1))
+    pages.copy_(i32([[-1] * 3, [4, -1, -1]]))
+    counts, lens, qsl, slots = i32([0, 1]), i32([0, 0]), i32([0, 0, 0]), i32([0] * 5)
+    pg.paged_gqa_build_tables(i32([3, 2]), i32([0, 15]), i32([0, 1]), 16, pages, counts, i32([7, 8, 9]), i32([3]), table, lens, qsl, slots)
+    assert pg.paged_gqa_check_device_errors() == 0
+    assert table.tolist() == [[9, -1, -1], [4, 8, -1]] and pages.tolist() == [[9, -1, -1], [4, 8, -1]]
+    assert slots.tolist() == [144, 145, 146, 79, 128]
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_keep_in_interleaved_caches(cache):
+    r = random.Random(3)
+    x = su.Tree([(13, 300), (40, 41)], 8, 2, 16, cache, seed=31)
+    both = torch.stack([x.k.view(torch.uint8), x.v.view(torch.uint8)], dim=2).view(x.k.dtype)  # [NB, P, 2, Hkv, 256]
+    before = [c.view(torch.uint8).clone() for c in (x.k, x.v)]
+    x.k, x.v = both[:, :, 0], both[:, :, 1]
+    su.compare(x.run(), x.reference(), "interleaved")
+    kept = [sorted(r.sample(range(13), 6)), sorted(r.sample(range(40), 33))]
+    assert _keep(x, kept, [6, 33], 33) == [293, 34]
+    assert pg.paged_gqa_check_device_errors() == 0
+    _kept_reference(x, before, kept)
+    for got, want in zip((x.k, x.v), before):
+        assert torch.equal(got.contiguous().view(torch.uint8), want)
+
+
+def test_a_step_captured_and_replayed_against_the_eager_one():
+    """Masks, tree attention, keep and the next tables in one graph, replayed on new lengths and pages."""
+    x = su.Tree([(13, 300), (9, 40), (1, 1)], 8, 1, 16, seed=41)
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.empty(pg.paged_gqa_workspace_size(3, x.T, 8, 1, 16, x.table.shape[1]), dtype=torch.uint8, device="cuda")
+    masks, pos = torch.empty(x.T, 1, dtype=torch.int32, device="cuda"), torch.empty(3, x.T, dtype=torch.int32, device="cuda")
+    out, new, kept, num = torch.empty_like(x.q), i32([0] * 3), i32([[0, 1, 2], [0, 2, 5], [0, 0, 0]]), i32([3, 2, 1])
+    k, v = (c.view(torch.uint8).clone() for c in (x.k, x.v))
+
+    def run():
+        pg.paged_gqa_tree_masks(x.parents_t, x.lens_t, x.qsl_t, masks, pos)
+        pg.paged_gqa_attn_tree_ex(*x.args(masks=masks), out, ws)
+        pg.paged_gqa_cache_keep(x.k, x.v, x.table, x.lens_t, x.qsl_t, kept, num, new)
+
+    st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        run()
+        st.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            run()
+    for lens, num_kept in (([300, 40, 1], [3, 2, 1]), ([290, 39, 1], [0, 3, 0]), ([13, 9, 1], [1, 1, 1])):
+        x.seqs = [(n, L) for (n, _), L in zip(x.seqs, lens)]
+        x.lens_t.copy_(i32(lens))
+        num.copy_(i32(num_kept))
+        x.k.view(torch.uint8).copy_(k)
+        x.v.view(torch.uint8).copy_(v)
+        ref = x.reference()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        su.compare(out, ref, lens)
+        assert new.tolist() == [L - n + a for (n, L), a in zip(x.seqs, num_kept)]
+        assert pg.paged_gqa_check_device_errors() == 0
+
+
+def test_two_host_threads_at_once():
+    import threading
+    tree = su.Tree([(13, 4000), (70, 900)], 16, 2, 16, seed=51)
+    prompt = su.Prompt([1500, 33], 8, 1, seed=52)
+    tree_ref, failed = tree.reference(), []
+    torch.cuda.synchronize()
+
+    def work(which):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(25):
+                    if which:
+                        out = torch.full_like(tree.q, float("nan"))
+                        pg.paged_gqa_attn_tree(*tree.args(), out)
+                    else:
+                        out = torch.full(prompt.q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+                        pg.paged_gqa_attn_prompt(prompt.q, prompt.k, prompt.v, prompt.qsl_t, prompt.scale, out)
+                torch.cuda.current_stream().synchronize()
+            if which:
+                su.compare(out, tree_ref, "thread")
+            else:
+                prompt.check(out, None, rows={0: [0, 700, 1499], 1: [32]})
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i % 2,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    assert pg.paged_gqa_check_device_errors() == 0
