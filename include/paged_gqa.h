@@ -545,7 +545,7 @@ int paged_gqa_last_plan(int64_t* out8);
 /*
  * Profiling hook (process-wide): while set, every dense call (not sparse attention) records `start`
  * on its stream immediately before the attention kernel of class `cls` (0 = verify blocks,
- * 1 = prefill blocks) and `stop` immediately after it; a 4-bit call of at most 64 rows
+ * 1 = prefill blocks) and `stop` immediately after it; a 4-bit or tree call of at most 64 rows
  * (T * Hq / Hkv) has no kernel of class 1, a tree call of one sequence of more than 64 rows none of
  * class 0, and a call on whole prompts none of either. Both are cudaEvent_t handles
  * owned by the caller; pass NULLs to stop recording. Returns PG_OK or

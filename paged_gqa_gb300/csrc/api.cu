@@ -367,11 +367,15 @@ int run(const Validated& val, const pg_tensor* k, const pg_tensor* v, void* ws, 
     if (e != cudaSuccess) return cuda_fail(e, "plan launch");
     ++launched;
   }
+  // Tree calls without prefill class (at most kVerifyRows rows in all; the verify kernel then flags bad sequences by
+  // itself) or without verify class (one sequence of more rows) leave out the kernel that would find nothing to do.
+  const bool tc = fast_ok || bf16_ok;
+  const bool no_prefill = p.mask_words > 0 && p.fused_verify && (long long)p.T * p.G <= kVerifyRows;
+  const bool no_verify = p.mask_words > 0 && single_prefill && tc;
+  p.unplanned = no_prefill;
   int used = 0;
   bool prev_ev = false;  // an event was recorded after the previous class's kernel
-  // (one sequence that is all prefill has no verify class: a tree call leaves that launch out)
-  const bool no_verify = p.mask_words > 0 && single_prefill && (fast_ok || bf16_ok);
-  for (int c = no_verify ? 1 : 0; c < kNumClasses; ++c) {
+  for (int c = no_verify ? 1 : 0; c < (no_prefill ? 1 : kNumClasses); ++c) {
     bool done = false;
     cudaEvent_t ev0 = g_ev_start[c].load(), ev1 = g_ev_stop[c].load();
     bool after_plan = c == 1 && no_verify;  // this class's kernel directly follows the plan kernel
@@ -382,7 +386,7 @@ int run(const Validated& val, const pg_tensor* k, const pg_tensor* v, void* ws, 
       after_plan = true;
     }
     if (ev0 && (e = cudaEventRecord(ev0, stream)) != cudaSuccess) return cuda_fail(e, "cudaEventRecord");
-    if (fast_ok || bf16_ok) {
+    if (tc) {
       // the prefill-class kernel follows the verify-class one (or the plan kernel, when the
       // verify kernel planned itself) as a programmatic dependent, when that one is a
       // tcgen05 kernel too and no event sits between them

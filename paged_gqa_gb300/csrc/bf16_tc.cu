@@ -168,6 +168,7 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
   self_plan::Scratch& fs = *reinterpret_cast<self_plan::Scratch*>(smem + kOffK);
   if (kFused) {
     self_plan::load(p, ptr, fs);  // the set-up below overlaps these reads
+    if (kTree && p.unplanned && blockIdx.x == 0) self_plan::flag_invalid(p, ptr, fs);
   } else {
     item_begin = cp.cta_item_begin[blockIdx.x];
     item_end = cp.cta_item_begin[blockIdx.x + 1];

@@ -129,7 +129,7 @@ struct Problem {
   // The verify class is planned by its own kernel's CTAs (each works out its range from
   // query_start_loc and seq_lens in its prologue); the plan kernel then plans prefill only.
   int fused_verify;
-  // No plan kernel runs in this call (4-bit caches): the verify kernel flags invalid sequences.
+  // No plan kernel runs in this call (4-bit caches, small trees): the verify kernel flags invalid sequences.
   int unplanned;
   // Two fp32 zeros: an addend that keeps the compiler from fusing a product with a sum (4-bit caches).
   unsigned long long zero2;

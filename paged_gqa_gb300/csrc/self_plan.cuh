@@ -70,7 +70,9 @@ __device__ __forceinline__ void flag_invalid(const Problem& p, const Pointers& p
 #pragma unroll 1
   for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
     const int4 i = fs.seq[s];
-    if (i.y >= 0 && i.x >= 0 && i.x + i.y <= p.T && i.y <= i.z && (long long)i.z <= (long long)p.W * p.P) continue;
+    if (i.y >= 0 && i.x >= 0 && i.x + i.y <= p.T && i.y <= i.z && (long long)i.z <= (long long)p.W * p.P &&
+        mask_holds(p, i.y))
+      continue;
     atomicOr(ptr.err, kErrBounds);
     const int t0 = max(0, i.x), t1 = min(p.T, max(t0, i.x + max(i.y, 0)));
     uint16_t* o = static_cast<uint16_t*>(ptr.out);

@@ -222,6 +222,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
   if (kFused) {
     // The sequences' reads go out first; the set-up below overlaps them.
     self_plan::load(p, ptr, fs);
+    if (kTree && p.unplanned && blockIdx.x == 0) self_plan::flag_invalid(p, ptr, fs);
   } else {
     item_begin = cp.cta_item_begin[blockIdx.x];
     item_end = cp.cta_item_begin[blockIdx.x + 1];

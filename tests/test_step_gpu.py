@@ -642,3 +642,29 @@ def test_two_host_threads_at_once():
         t.join()
     assert not failed, failed
     assert pg.paged_gqa_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_calls_of_at_most_64_rows_flag_and_zero_bad_sequences_themselves(cache):
+    x = su.Tree([(3, 50), (9, 400), (4, 100)], 4, 1, 16, cache, seed=61)
+    ref = x.reference()
+    out = x.run()
+    assert pg.paged_gqa_last_plan()["path_bits"] == 2
+    su.compare(out, ref, cache)
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")  # noqa: E731
+    for lens, gone in (([50, 8, 100], 1), ([2, 400, 100], 0), ([50, 400, 10 ** 6], 2), ([-1, 400, 100], 0)):
+        x.lens_t = i32(lens)
+        out = x.run(check=False)
+        assert pg.paged_gqa_check_device_errors() == -5
+        for s in range(3):
+            rows = slice(x.qsl[s], x.qsl[s + 1])
+            if s == gone:
+                assert (out[rows] == 0).all()
+            else:
+                su.compare(out[rows], ref[rows], (cache, lens))
+    x = su.Tree([(40, 100)], 1, 1, 16, cache, seed=62)
+    out = x.run(check=False, masks=x.masks_t[:, :1].contiguous())  # 40 tokens, masks of 32
+    assert pg.paged_gqa_check_device_errors() == -5 and (out == 0).all()
+    x.qsl_t = i32([0, 39])  # not all of T
+    x.run(check=False)
+    assert pg.paged_gqa_check_device_errors() == -5
