@@ -19,10 +19,18 @@
 //     when a score exceeds it by 2^8;
 //   * the even CTA issues the products. The odd CTA's copies are announced to it by a relaying warp, the
 //     softmax warps of both arrive on its barriers, and its commits arrive in both CTAs;
+//   * an item's epilogue has a warpgroup of its own, O leaves TMEM at once (part to the stage, part to registers), and
+//     the next item's first S is issued before this one's last P.V, so items follow each other without a gap;
 //   * the work is cut into equal ranges over the clusters, worked out by each CTA for itself: block b of a
 //     prompt costs a fixed part and (b + 1) tokens' worth of keys, a closed form whose prefix sums need no pass
 //     over blocks. A block cut across clusters is merged by its last piece (fp32 partials, counters
 //     tagged per call).
+//
+// Measured (GB300, bf16, back to back, L2 warm): 16384 tokens, 16/2 heads 1100 us, 2000 TFLOP/s of visible pairs (a
+// cuBLAS bf16 product in a burst: 1930; under a power cap held for seconds 1250 us); 8192 tokens, 8/1 164 us, 1670;
+// 2048 tokens 35; 173 tokens 16 (latency: set-up 5, one item's chain of cold steps). Under ncu the tensor pipe is
+// busy 79 % of the cycles at 8192 tokens, DRAM 3 %, L2 hits 89 %. The other 21 % are the ends of ranges (tiles
+// on the diagonal, of which half is masked) and the softmax where it takes longer than two products.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -15,6 +15,11 @@
 // all three sums, and what is copied in bulk is shared out over the warps. The second copies the pool's
 // rows into the batch's block table and writes the slots, over as many CTAs as there are table rows; it is the
 // one that moves bytes (4 W per request), and is resident before the first one ends.
+//
+// Bound by latency and by the host: 250 requests of up to 2080 columns take 7.5 us from a graph (2.1 MB; 0.5 us at the
+// copy rate) and 17 as a call from Python (13 tensors described, two launches); 1500 requests of 160 columns, 41 of them
+// new with up to 64 pages each, 15.4 and 17. With the first launch written plainly (three scans, rows told apart in global
+// memory, each thread copying its own pages) the 250 requests took 17 us from a graph.
 #include <cuda_runtime.h>
 
 #include <climits>

