@@ -414,8 +414,7 @@ int paged_gqa_tree_masks(const pg_tensor* parents, const pg_tensor* seq_lens, co
  * key is zeros. masks is int32 [T, words], rows any distance apart; a sequence of more than 32 * words
  * new tokens is flagged like other bad bounds, its rows are zeros. q is bf16, the caches bf16 or
  * e4m3; everything else is as in paged_gqa_attn, out and q must not overlap (refused). A NaN or
- * infinity in V of a key reaches the tokens that see it, and may reach others of its sequence
- * that share a block of rows with one. Slots behind seq_lens and other pages do not matter. With bf16
+ * infinity in V of a key reaches the tokens that see it, and may reach others of its sequence. Slots behind seq_lens and other pages do not matter. With bf16
  * caches |V| must not pass 65504 (the pieces of a split sequence are held in f16, as in paged_gqa_attn).
  *
  * Calls are ordered by the library as those of paged_gqa_attn_fp4 (one workspace); in a stream
@@ -546,8 +545,8 @@ int paged_gqa_last_plan(int64_t* out8);
  * Profiling hook (process-wide): while set, every dense call (not sparse attention) records `start`
  * on its stream immediately before the attention kernel of class `cls` (0 = verify blocks,
  * 1 = prefill blocks) and `stop` immediately after it; a 4-bit or tree call of at most 64 rows
- * (T * Hq / Hkv) has no kernel of class 1, a tree call of one sequence of more than 64 rows none of
- * class 0, and a call on whole prompts none of either. Both are cudaEvent_t handles
+ * (T * Hq / Hkv) has no kernel of class 1, a tree call of more than 64 rows a sequence on average may have
+ * none of class 0, and a call on whole prompts none of either. Both are cudaEvent_t handles
  * owned by the caller; pass NULLs to stop recording. Returns PG_OK or
  * PG_ERR_INVALID_ARG.
  */

@@ -348,6 +348,7 @@ int run(const Validated& val, const pg_tensor* k, const pg_tensor* v, void* ws, 
     ++launched;
   }
   p.call_tag = next_call_tag();
+  const bool tc = fast_ok || bf16_ok;
   // The verify kernel (FP8 or bf16) plans its own class when its CTAs can hold one entry per verify block
   // (sequence x kv head), the class's units fit 31 bits and a block's tiles 16: it then runs
   // first, and the plan kernel (prefill only) and the prefill kernel follow it as
@@ -362,23 +363,25 @@ int run(const Validated& val, const pg_tensor* k, const pg_tensor* v, void* ws, 
                    (long long)p.num_seqs * p.Hkv <= kFusedMaxBlocks &&
                    max_tiles < (1 << 16) &&
                    (long long)p.num_seqs * p.Hkv * (max_tiles + fixed_cost(0)) < (1LL << 31);
-  if (!p.fused_verify) {
+  // Few of them need no plan kernel either: the prefill kernel's CTAs work out their items, for every sequence.
+  p.self_all = tc && path != 3 && p.mask_words > 0 && (single_prefill || wide_trees) &&
+               cp[1].max_blocks <= kSelfAllBlocks && max_tiles < (1 << 16);
+  if (!p.fused_verify && !p.self_all) {
     e = launch_plan(p, ptr, cp[0], cp[1], true, false, stream);
     if (e != cudaSuccess) return cuda_fail(e, "plan launch");
     ++launched;
   }
   // Tree calls without prefill class (at most kVerifyRows rows in all; the verify kernel then flags bad sequences by
   // itself) or without verify class (one sequence of more rows) leave out the kernel that would find nothing to do.
-  const bool tc = fast_ok || bf16_ok;
   const bool no_prefill = p.mask_words > 0 && p.fused_verify && (long long)p.T * p.G <= kVerifyRows;
-  const bool no_verify = p.mask_words > 0 && single_prefill && tc;
-  p.unplanned = no_prefill;
+  const bool no_verify = p.self_all || (p.mask_words > 0 && single_prefill && tc);
+  p.unplanned = no_prefill || p.self_all;
   int used = 0;
   bool prev_ev = false;  // an event was recorded after the previous class's kernel
   for (int c = no_verify ? 1 : 0; c < (no_prefill ? 1 : kNumClasses); ++c) {
     bool done = false;
     cudaEvent_t ev0 = g_ev_start[c].load(), ev1 = g_ev_stop[c].load();
-    bool after_plan = c == 1 && no_verify;  // this class's kernel directly follows the plan kernel
+    bool after_plan = c == 1 && no_verify && !p.self_all;  // this class's kernel directly follows the plan kernel
     if (c == 1 && p.fused_verify) {
       e = launch_plan(p, ptr, cp[0], cp[1], false, !prev_ev, stream);
       if (e != cudaSuccess) return cuda_fail(e, "plan launch");

@@ -102,15 +102,14 @@ struct Item {
 
 // A work item of the plan (128-key tiles) as 64-key sub-tiles that end at the piece's last
 // key: sub-tiles past it would read block-table entries the call does not define.
-template <bool kFused>
+template <int kFused>
 __device__ __forceinline__ Item load_item(const Problem& p, const ClassPlan& cp, const Pointers& ptr,
                                           const Misc& ms, int it) {
-  if (kFused) {  // a verify block of a self-planned CTA
+  if (kFused) {  // a block of a self-planned CTA
     const self_plan::Piece f = self_plan::unpack(p, ms.fitem[it]);
     Item r;
     r.block = f.block;
     r.seq = f.seq;
-    r.kvh = f.kvh;
     r.nsplit = f.nsplit;
     r.split = f.split;
     r.slot_base = f.slot_base;
@@ -119,8 +118,10 @@ __device__ __forceinline__ Item load_item(const Problem& p, const ClassPlan& cp,
     r.q0 = sq.x;
     r.qn = sq.y;
     r.L = sq.z;
-    r.row0 = 0;
-    r.nrows = r.qn * p.G;
+    const self_plan::RowsOf rows = kFused == 2 ? self_plan::rows_of(p, sq) : self_plan::RowsOf{f.kvh, 0, r.qn * p.G};
+    r.kvh = rows.kvh;
+    r.row0 = rows.row0;
+    r.nrows = rows.nrows;
     r.kv_end = r.L;  // the causal limit of the last row (token qn - 1) is L
     r.kv_hi = min((f.tile_begin + f.ntiles) * kTileKeys, r.kv_end);
     r.nsub = (r.kv_hi - f.tile_begin * kTileKeys + kSub - 1) / kSub;
@@ -151,8 +152,9 @@ __device__ __forceinline__ Item load_item(const Problem& p, const ClassPlan& cp,
 
 // kTree: the new tokens see each other by the call's masks (Problem::mask_words) instead of causally: a thread shifts its 32
 // keys' bits out of its row's words, on sub-tiles that hold new tokens. Pieces of split blocks stay in the workspace
-// (tree_merge.cu). 13 tokens on 700 keys, 16 heads: 24.5 us from a graph (plan 7.5, this kernel 11 behind it, merge 3): latency.
-template <bool kFused, bool kTree>
+// (tree_merge.cu). 13 tokens on 700 keys, 16 heads: 20.4 us from a graph (this kernel with its own plan 16, merge 3): latency.
+// kFused: 1: the CTAs plan the verify class, 2: every sequence (Problem::self_all), 0: the plan kernel's plan.
+template <int kFused, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                Problem p, Pointers ptr, ClassPlan cp) {
@@ -169,7 +171,7 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
   int item_begin = 0, item_end = 0;
   self_plan::Scratch& fs = *reinterpret_cast<self_plan::Scratch*>(smem + kOffK);
   if (kFused) {
-    self_plan::load(p, ptr, fs);  // the set-up below overlaps these reads
+    self_plan::load<kFused == 2>(p, ptr, fs);  // the set-up below overlaps these reads
     if (kTree && p.unplanned && blockIdx.x == 0) self_plan::flag_invalid(p, ptr, fs);
   } else {
     item_begin = cp.cta_item_begin[blockIdx.x];
@@ -208,7 +210,7 @@ bf16_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant
   }
   if (kFused) {
     __syncthreads();  // the sequences are staged
-    if (warp == 0) self_plan::plan_warp<kTree>(p, fs, cp, lane, ms.fitem, ms.fseq, &ms.fcount);
+    if (warp == 0) self_plan::plan_warp<kTree, kFused == 2>(p, fs, cp, lane, ms.fitem, ms.fseq, &ms.fcount, ptr.err);
     fence_proxy_async_smem();  // the scratch lies where the copies go
   }
   tc_fence_before();
@@ -610,9 +612,10 @@ int launch_bf16_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp, c
   cudaGetDevice(&dev);
   cudaError_t e;
   const bool tree = p.mask_words > 0;
-  auto kern = tree ? (self_planned ? bf16_tc_kernel<true, true> : bf16_tc_kernel<false, true>)
-                   : (self_planned ? bf16_tc_kernel<true, false> : bf16_tc_kernel<false, false>);
-  const int which = (self_planned ? 2 : 1) << (tree ? 2 : 0);
+  auto kern = p.self_all ? bf16_tc_kernel<2, true>
+              : tree ? (self_planned ? bf16_tc_kernel<1, true> : bf16_tc_kernel<0, true>)
+                     : (self_planned ? bf16_tc_kernel<1, false> : bf16_tc_kernel<0, false>);
+  const int which = p.self_all ? 16 : (self_planned ? 2 : 1) << (tree ? 2 : 0);
   if (dev >= 0 && dev < 64 && !(attr_done[dev] & which)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) {

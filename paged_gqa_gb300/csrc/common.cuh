@@ -74,6 +74,11 @@ constexpr unsigned long long kSplitTagMask = (1ull << 48) - 1;
 // Most verify blocks (sequences x kv heads) of a call whose verify kernel plans its own
 // class (its CTAs keep one entry per block they work on in shared memory).
 constexpr int kFusedMaxBlocks = 512;
+// Most row blocks of a tree call whose one attention kernel plans all of them (Problem::self_all): a CTA may have as
+// many items, and more do not fit beside the prefill kernel's tiles. Against the plan kernel, an (empty) verify kernel and the
+// prefill kernel, us: 13 tokens on 700 keys, 16 heads 24.8 to 20.4 (graph), 8 x 60 tokens on 1000 keys 42.7 to 34.6, 32 x 33-60 on
+// 2k-16k 233 to 219, 64 x 20-30 on 4k-8k 203 to 189, 8 x 90-100 on 20k-30k 144 to 131.
+constexpr int kSelfAllBlocks = 448;
 
 struct RowBlock {
   int seq, kvh;
@@ -131,6 +136,8 @@ struct Problem {
   int fused_verify;
   // No plan kernel runs in this call (4-bit caches, small trees): the verify kernel flags invalid sequences.
   int unplanned;
+  // Tree calls of few row blocks: the prefill (or bf16) kernel plans and serves every sequence by itself.
+  int self_all;
   // Two fp32 zeros: an addend that keeps the compiler from fusing a product with a sum (4-bit caches).
   unsigned long long zero2;
 };

@@ -36,6 +36,7 @@
 
 #include "common.cuh"
 #include "device_util.cuh"
+#include "self_plan.cuh"
 #include "tc_kernels.cuh"
 #include "tc_util.cuh"
 
@@ -104,11 +105,20 @@ struct Misc {
   int vote[2][kSoftWarps];
   int merge_flag;
 };
+// A CTA that plans its own items (Problem::self_all) keeps them behind that: packed by self_plan::plan_warp, each one's
+// sequence {first token, q_len, L, number among its blocks}, and their count.
+struct OwnItems {
+  alignas(16) int4 fitem[kSelfAllBlocks];
+  int4 fseq[kSelfAllBlocks];
+  int fcount;
+};
+constexpr uint32_t kOwnItemsOff = (sizeof(Misc) + 15) / 16 * 16;
 
-template <bool kQFp8>
+template <bool kQFp8, bool kSelf = false>
 constexpr size_t smem_bytes() {
-  return Layout<kQFp8>::kOffMisc + sizeof(Misc) + 1024;
+  return Layout<kQFp8>::kOffMisc + kOwnItemsOff + (kSelf ? sizeof(OwnItems) : 0) + 1024;
 }
+static_assert(smem_bytes<false, true>() <= 232448 && sizeof(self_plan::Scratch) <= kKStages * kKVTile, "shared memory of one CTA");
 
 struct Item {
   int block, seq, kvh, row0, nrows, kv_end, nsplit, split, slot_base;
@@ -116,7 +126,30 @@ struct Item {
   int q0, qn, L;
 };
 
-__device__ __forceinline__ Item load_item(const ClassPlan& cp, const Pointers& ptr, int it) {
+template <bool kSelf>
+__device__ __forceinline__ Item load_item(const Problem& p, const ClassPlan& cp, const Pointers& ptr, const OwnItems& own, int it) {
+  if (kSelf) {
+    const self_plan::Piece f = self_plan::unpack(p, own.fitem[it]);
+    const int4 sq = own.fseq[it];
+    const self_plan::RowsOf rows = self_plan::rows_of(p, sq);
+    Item r;
+    r.block = f.block;
+    r.seq = f.seq;
+    r.kvh = rows.kvh;
+    r.row0 = rows.row0;
+    r.nrows = rows.nrows;
+    r.kv_end = sq.z;
+    r.nsplit = f.nsplit;
+    r.split = f.split;
+    r.slot_base = f.slot_base;
+    r.tile_begin = f.tile_begin;
+    r.ntiles = f.ntiles;
+    r.kv_hi = min((f.tile_begin + f.ntiles) * kTileKeys, r.kv_end);
+    r.q0 = sq.x;
+    r.qn = sq.y;
+    r.L = sq.z;
+    return r;
+  }
   const WorkItem w = cp.items[it];
   const RowBlock b = cp.blocks[w.block];
   Item r;
@@ -152,11 +185,13 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
 
 // kTree: the new tokens see each other by the call's masks (Problem::mask_words) instead of causally: a thread shifts its 64
 // keys' bits out of its row's words, on tiles that hold new tokens. Pieces of split blocks stay in the workspace
-// (tree_merge.cu). 32 sequences of 33 to 60 tokens on 2k-16k keys, 16/2 heads, take 197 us (a call 235; 108 us of products at
+// (tree_merge.cu). 32 sequences of 33 to 60 tokens on 2k-16k keys, 16/2 heads, take 197 us (a call 219; 108 us of products at
 // the bf16 rate): the three or four row blocks of a sequence read its pages at different times, 880 MB from HBM where
-// 287 lie, and two stages of K hide no more than part of that (all sequences on the same pages, from L2: a call
-// 196 us); the tensor pipe is busy 59 %.
-template <int kQM, bool kTree>
+// 287 lie (all sequences on the same pages, from L2: a call takes 39 us less); the tensor pipe is busy 59 %. Blocks ordered so
+// that those of a sequence run side by side, where the cut allows, gained 5 % there and lost as much elsewhere;
+// prefetching tiles into L2 two ahead gained nothing.
+// kSelf: the CTAs plan every sequence's blocks by themselves (Problem::self_all).
+template <int kQM, bool kTree, bool kSelf>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                   Problem p, Pointers ptr, ClassPlan cp) {
@@ -174,9 +209,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
   // The plan is read once the previous grid (the plan kernel) has completed. A CTA with no
   // work (an empty class, or fewer items than CTAs) leaves before any set-up.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int item_begin = cp.cta_item_begin[blockIdx.x];
-  const int item_end = cp.cta_item_begin[blockIdx.x + 1];
-  if (item_begin >= item_end) return;
+  OwnItems& own = *reinterpret_cast<OwnItems*>(smem + LY::kOffMisc + kOwnItemsOff);
+  self_plan::Scratch& fs = *reinterpret_cast<self_plan::Scratch*>(smem + LY::kOffK);
+  int item_begin = 0, item_end = 0;
+  if (kSelf) {
+    self_plan::load<true>(p, ptr, fs);  // the set-up below overlaps these reads
+    if (blockIdx.x == 0) self_plan::flag_invalid(p, ptr, fs);
+  } else {
+    item_begin = cp.cta_item_begin[blockIdx.x];
+    item_end = cp.cta_item_begin[blockIdx.x + 1];
+    if (item_begin >= item_end) return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kKStages; ++s) {
@@ -208,10 +251,22 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     tmem_alloc(smem_u32(&ms.tmem_base), kTmemCols);
     tmem_relinquish();
   }
+  if (kSelf) {
+    __syncthreads();  // the sequences are staged
+    if (warp == 0) self_plan::plan_warp<true, true>(p, fs, cp, lane, own.fitem, own.fseq, &own.fcount, ptr.err);
+    fence_proxy_async_smem();  // the scratch lies where the copies go
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ms.tmem_base;
+  if (kSelf) {
+    item_end = own.fcount;
+    if (item_end == 0) {  // no range or no tile in it: give the columns back and leave
+      if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+      return;
+    }
+  }
   // The next kernel on the stream (the other class) may start its own checks now.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -231,7 +286,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     uint32_t issued[kVStages > kKStages ? kVStages : kKStages] = {};
     bool stop = false;
     for (int it = item_begin; it < item_end && !stop; ++it) {
-      const Item I = load_item(cp, ptr, it);
+      const Item I = load_item<kSelf>(p, cp, ptr, own, it);
       const int32_t* bt_row = ptr.block_table + (size_t)I.seq * p.bt_stride;
       const int page0 = I.tile_begin * ppt;
       const int npages = (I.kv_hi + p.P - 1) / p.P - page0;
@@ -301,7 +356,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, ptr.err));
       };
       for (int it = item_begin; it < item_end && ok; ++it, ++ii) {
-        const Item I = load_item(cp, ptr, it);
+        const Item I = load_item<kSelf>(p, cp, ptr, own, it);
         for (int j = 0; j < I.ntiles && ok; ++j, ++g) {
           const uint32_t b = g & 1;
           if (is_s) {
@@ -502,9 +557,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 
     int ii = 0;
     uint32_t g = 0;
-    if (item_end > item_begin) q_prep(load_item(cp, ptr, item_begin), 0);
+    if (item_end > item_begin) q_prep(load_item<kSelf>(p, cp, ptr, own, item_begin), 0);
     for (int it = item_begin; it < item_end; ++it, ++ii) {
-      const Item I = load_item(cp, ptr, it);
+      const Item I = load_item<kSelf>(p, cp, ptr, own, it);
       const int pi = ii & 1;
       named_barrier(9, kSoftThreads);  // q_prep's shared writes are visible
       const float c = p.score_scale_log2 * ms.qscale[pi];
@@ -640,7 +695,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         tc_fence_before();
         mbar_arrive(bar(ms.p_full[b]));
       }
-      if (it + 1 < item_end) q_prep(load_item(cp, ptr, it + 1), ii + 1);
+      if (it + 1 < item_end) q_prep(load_item<kSelf>(p, cp, ptr, own, it + 1), ii + 1);
 
       // ---------------------------------------------------------- epilogue
       if (!mbar_wait(bar(ms.o_ready), ii & 1, abort_flag, ptr.err)) bad = true;
@@ -720,11 +775,12 @@ int launch_prefill_tc(const Problem& p, const Pointers& ptr, const ClassPlan& cp
   const int mode = p.q_cast ? kQCast : p.q_is_fp8 ? kQGiven : kQSplit;
   const bool tree = p.mask_words > 0;  // (with a bf16 q only)
   if (tree && mode != kQSplit) return 0;
-  auto kern = tree ? prefill_tc_kernel<kQSplit, true>
-              : mode == kQCast ? prefill_tc_kernel<kQCast, false>
-              : mode == kQGiven ? prefill_tc_kernel<kQGiven, false> : prefill_tc_kernel<kQSplit, false>;
-  const size_t bytes = mode != kQSplit ? smem_bytes<true>() : smem_bytes<false>();
-  const int which = 1 << (tree ? 3 : mode);
+  auto kern = p.self_all ? prefill_tc_kernel<kQSplit, true, true>
+              : tree ? prefill_tc_kernel<kQSplit, true, false>
+              : mode == kQCast ? prefill_tc_kernel<kQCast, false, false>
+              : mode == kQGiven ? prefill_tc_kernel<kQGiven, false, false> : prefill_tc_kernel<kQSplit, false, false>;
+  const size_t bytes = p.self_all ? smem_bytes<false, true>() : mode != kQSplit ? smem_bytes<true>() : smem_bytes<false>();
+  const int which = 1 << (p.self_all ? 4 : tree ? 3 : mode);
   if (dev >= 0 && dev < 64 && !(attr_done[dev] & which)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess) {

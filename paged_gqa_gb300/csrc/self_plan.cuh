@@ -17,8 +17,6 @@
 namespace pgqa {
 namespace self_plan {
 
-constexpr int kE = fixed_cost(0);
-
 struct Cut {
   int U, C, q, r;
 };
@@ -34,17 +32,21 @@ __device__ __forceinline__ int cut_cta(const Cut& k, int u) {
   return c;
 }
 
-// Scratch of the prologue (20 KB), in shared memory no copy has touched yet.
+// Scratch of the prologue (22 KB), in shared memory no copy has touched yet.
 struct Scratch {
-  long long v[kFusedMaxBlocks];  // per sequence: (units << 16) | 1 for a verify sequence, else 0
+  long long v[kFusedMaxBlocks];  // per sequence: (units << 16) | 1 (kAll: row blocks) for one of the class, else 0
   int tiles[kFusedMaxBlocks];    // per sequence: key tiles of each of its blocks
   int4 seq[kFusedMaxBlocks];     // per sequence: {first token, q_len, L, 0} as read
   int fv_seq[kFusedMaxBlocks];   // per verify sequence j: its index,
   int fv_off[kFusedMaxBlocks];   // the first unit of its blocks,
   int fv_tiles[kFusedMaxBlocks]; // its tiles per block
+  int fv_first[kFusedMaxBlocks]; // kAll: the first entry of its sequence
 };
 
 // Step 1, every thread of the CTA: the sequences' reads and units, staged in the scratch.
+// kAll (tree calls with Problem::self_all): every sequence's blocks of 128 rows, which one kernel serves; a block has
+// the tiles of its sequence's last token's keys.
+template <bool kAll = false>
 __device__ __forceinline__ void load(const Problem& p, const Pointers& ptr, Scratch& fs) {
   for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
     const int q0 = ptr.qsl[s], q1 = ptr.qsl[s + 1], L = ptr.seq_lens[s];
@@ -53,9 +55,10 @@ __device__ __forceinline__ void load(const Problem& p, const Pointers& ptr, Scra
     int tiles = 0;
     // the plan kernel's validity test; invalid sequences are flagged and zeroed there
     const bool ok = qn >= 0 && q0 >= 0 && q1 <= p.T && qn <= L && (long long)L <= (long long)p.W * p.P && mask_holds(p, qn);
-    if (ok && qn > 0 && (long long)qn * p.G <= kVerifyRows) {
+    if (ok && qn > 0 && (kAll || (long long)qn * p.G <= kVerifyRows)) {
       tiles = (L + kTileKeys - 1) / kTileKeys;
-      v = ((long long)p.Hkv * (tiles + kE) << 16) | 1;
+      const int nrb = kAll ? (int)(((long long)qn * p.G + kPrefillRows - 1) / kPrefillRows) : 1;
+      v = ((long long)p.Hkv * nrb * (tiles + fixed_cost(kAll)) << 16) | nrb;
     }
     fs.v[s] = v;
     fs.tiles[s] = tiles;
@@ -85,6 +88,16 @@ __device__ __forceinline__ void flag_invalid(const Problem& p, const Pointers& p
   }
 }
 
+// The rows of a block (kAll), from its item's record {first token, q_len, L, number among the sequence's blocks}.
+struct RowsOf {
+  int kvh, row0, nrows;
+};
+__device__ __forceinline__ RowsOf rows_of(const Problem& p, int4 sq) {
+  const int rows = sq.y * p.G, nrb = (rows + kPrefillRows - 1) / kPrefillRows;
+  const int kvh = sq.w / nrb, row0 = (sq.w - kvh * nrb) * kPrefillRows;
+  return RowsOf{kvh, row0, min(kPrefillRows, rows - row0)};
+}
+
 // Step 2, one warp, after a CTA barrier: the scan over sequences (each lane a contiguous
 // run of them), this CTA's range and items. Packed item (fitem, at most kFusedMaxBlocks):
 // x = block, y = sequence, z = first tile | tiles << 16, w = piece index | pieces << 15 |
@@ -92,9 +105,11 @@ __device__ __forceinline__ void flag_invalid(const Problem& p, const Pointers& p
 // item's sequence {first token, q_len, L, 0}, so that no item load reads global memory.
 // *fcount gets the number of items. kRecord (tree calls): the class's blocks and their number are written to the
 // workspace for the merge kernel, each by the CTA of its first piece.
-template <bool kRecord>
+// kAll: the entries of a sequence's row blocks lie side by side in the arrays of Scratch, and an item's fseq.w is its
+// number among the sequence's blocks (kv heads major).
+template <bool kRecord, bool kAll = false>
 __device__ __forceinline__ void plan_warp(const Problem& p, Scratch& fs, const ClassPlan& cp, int lane, int4* fitem,
-                                          int4* fseq, int* fcount) {
+                                          int4* fseq, int* fcount, uint32_t* err = nullptr) {
   const int n = p.num_seqs;
   const int per = (n + 31) / 32;
   const int s0 = lane * per, s1 = min(n, s0 + per);
@@ -106,10 +121,23 @@ __device__ __forceinline__ void plan_warp(const Problem& p, Scratch& fs, const C
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
+  constexpr int kE = fixed_cost(kAll);
+  if (kAll) {  // (more blocks than the host counted on: sequences that share tokens)
+    int blocks = 0;
+    for (int s = s0; s < s1; ++s) blocks += (int)(fs.v[s] & 0xffff);
+    if (__reduce_add_sync(0xffffffffu, blocks) * p.Hkv > min(cp.max_blocks, kSelfAllBlocks)) {
+      if (lane == 0) *fcount = 0;
+      if (blockIdx.x == 0 && lane == 0) {
+        *cp.n_blocks = 0;
+        atomicOr(err, kErrBounds);
+      }
+      return;
+    }
+  }
   const long long total = __shfl_sync(0xffffffffu, x, 31);
   const int U = (int)(total >> 16);
   if (kRecord && blockIdx.x == 0 && lane == 0) *cp.n_blocks = (int)(total & 0xffff) * p.Hkv;
-  const int C = cut_ctas(U, cp.num_ctas, min_range_units(p, 0));
+  const int C = cut_ctas(U, cp.num_ctas, min_range_units(p, kAll));
   const int c = blockIdx.x;
   if (c >= C) {  // warp-uniform: no range (C = 0: no verify block at all)
     if (lane == 0) *fcount = 0;
@@ -125,9 +153,12 @@ __device__ __forceinline__ void plan_warp(const Problem& p, Scratch& fs, const C
     if (v) {
       const int j = (int)(pre & 0xffff), off = (int)(pre >> 16), units = (int)(v >> 16);
       const int tiles = fs.tiles[s], span = tiles + kE;
-      fs.fv_seq[j] = s;
-      fs.fv_off[j] = off;
-      fs.fv_tiles[j] = tiles;
+      for (int i = 0; i < (kAll ? (int)(v & 0xffff) : 1); ++i) {
+        fs.fv_seq[j + i] = s;
+        fs.fv_off[j + i] = off;
+        fs.fv_tiles[j + i] = tiles;
+        if (kAll) fs.fv_first[j + i] = j;
+      }
       if (u0 >= off && u0 < off + units) ib = j * p.Hkv + (u0 - off) / span;
       if (u1 - 1 >= off && u1 - 1 < off + units) {
         const int kvh = (u1 - 1 - off) / span;
@@ -143,20 +174,24 @@ __device__ __forceinline__ void plan_warp(const Problem& p, Scratch& fs, const C
   const int cnt = max(0, il - ib + 1);
   for (int t = lane; t < cnt; t += 32) {
     const int b = ib + t;
-    const int j = b / p.Hkv, kvh = b - j * p.Hkv;
+    const int j = b / p.Hkv, at = b - (kAll ? fs.fv_first[j] : j) * p.Hkv;  // at: the kv head (kAll: kv head, row block)
     const int tiles = fs.fv_tiles[j];
-    const int off = fs.fv_off[j] + kvh * (tiles + kE), real = off + kE;
+    const int off = fs.fv_off[j] + at * (tiles + kE), real = off + kE;
     const int lo = max(u0, real), hi = min(u1, real + tiles);
     const int c0 = cut_cta(k, real);
     const int nsplit = cut_cta(k, real + tiles - 1) - c0 + 1;
     const int later = cut_begin(k, c0) < off ? 1 : 0;
     fitem[t] = make_int4(b, fs.fv_seq[j], (lo - real) | ((hi - lo) << 16), (c - c0) | (nsplit << 15) | (later << 30));
-    fseq[t] = fs.seq[fs.fv_seq[j]];
+    int4 sq = fs.seq[fs.fv_seq[j]];
+    if (kAll) sq.w = at;
+    fseq[t] = sq;
     if (kRecord && c == c0) {
       RowBlock r{};
       r.seq = fs.fv_seq[j];
-      r.kvh = kvh;
-      r.nrows = fs.seq[r.seq].y * p.G;
+      const RowsOf rows = kAll ? rows_of(p, sq) : RowsOf{at, 0, sq.y * p.G};
+      r.kvh = rows.kvh;
+      r.row0 = rows.row0;
+      r.nrows = rows.nrows;
       r.nsplit = nsplit;
       r.slot_base = split_slot_base(c0, later);
       cp.blocks[b] = r;

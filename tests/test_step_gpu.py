@@ -668,3 +668,41 @@ def test_calls_of_at_most_64_rows_flag_and_zero_bad_sequences_themselves(cache):
     x.qsl_t = i32([0, 39])  # not all of T
     x.run(check=False)
     assert pg.paged_gqa_check_device_errors() == -5
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_wide_trees_around_the_most_blocks_that_a_kernel_plans_by_itself(cache):
+    for S in (1, 40, 64, 150, 230):  # 2 kv heads, 17 tokens of 4 heads: 68 rows, one block of each
+        x = su.Tree([(17, 17 + 3 * s) for s in range(S)], 8, 2, 16, cache, seed=S)
+        out = x.run()
+        su.compare(out, x.reference(), (cache, S))
+        prev = pg.paged_gqa_set_path(3)  # planned by the plan kernel
+        try:
+            su.compare(x.run(), x.reference(), (cache, S, "plan"))
+        finally:
+            pg.paged_gqa_set_path(prev)
+    x = su.Tree([(300, 900), (1, 40), (0, 5), (90, 90), (700, 700)], 16, 2, 32, cache, seed=3)  # several blocks each
+    su.compare(x.run(), x.reference(), cache)
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "bf16"])
+def test_wide_trees_flag_and_zero_bad_sequences(cache):
+    x = su.Tree([(30, 50), (9, 400), (40, 100)], 8, 1, 16, cache, seed=71)
+    ref = x.reference()
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")  # noqa: E731
+    for lens, gone in (([50, 8, 100], 1), ([29, 400, 100], 0), ([50, 400, 10 ** 6], 2), ([-1, 400, 100], 0)):
+        x.lens_t = i32(lens)
+        out = x.run(check=False)
+        assert pg.paged_gqa_check_device_errors() == -5
+        for s in range(3):
+            rows = slice(x.qsl[s], x.qsl[s + 1])
+            if s == gone:
+                assert (out[rows] == 0).all()
+            else:
+                su.compare(out[rows], ref[rows], (cache, lens))
+    # sequences that share their tokens: more blocks than tokens can have
+    S, T = 121, 79
+    x.lens_t, x.qsl_t = i32([100] * S), i32([0, T] * ((S + 1) // 2))
+    x.table = x.table[2:3].expand(S, -1).contiguous()
+    x.run(check=False)
+    assert pg.paged_gqa_check_device_errors() == -5
