@@ -183,13 +183,18 @@ def test_rows_that_see_nothing_are_zeros(cache):
 
 
 # (one tile each: tree calls cut longer contexts into other pieces; and the e4m3 prefill kernel rounds its exponents in
-# another order on masked tiles, of which there are more in a tree call)
+# another order on masked tiles, of which there are more in a tree call. Path 3: so few tiles would go to the prefill
+# kernel, whose P is rounded otherwise than the verify kernel's)
 @pytest.mark.parametrize("cache,chunk", [("e4m3", 8), ("bf16", 20)])
 def test_full_masks_are_the_causal_attention_bit_for_bit(cache, chunk):
     x = su.Tree([(4, 100), (chunk, 128), (1, 33)], 16, 2, 16, cache, masks="all")
     want = torch.empty_like(x.q)
-    pg.paged_gqa_attn(x.q, x.k, x.v, x.table, x.lens_t, x.qsl_t, x.k_descale, x.v_descale, x.scale, want)
-    assert torch.equal(x.run(), want)
+    prev = pg.paged_gqa_set_path(3)
+    try:
+        pg.paged_gqa_attn(x.q, x.k, x.v, x.table, x.lens_t, x.qsl_t, x.k_descale, x.v_descale, x.scale, want)
+        assert torch.equal(x.run(), want)
+    finally:
+        pg.paged_gqa_set_path(prev)
 
 
 def test_long_contexts_split_over_many_blocks():
@@ -706,3 +711,14 @@ def test_wide_trees_flag_and_zero_bad_sequences(cache):
     x.table = x.table[2:3].expand(S, -1).contiguous()
     x.run(check=False)
     assert pg.paged_gqa_check_device_errors() == -5
+
+
+def test_small_trees_and_wide_ones_in_one_call():
+    """e4m3 caches and more than a few pages: the verify kernel with its own plan, then plan and prefill kernel."""
+    x = su.Tree([(3, 9000)] * 3 + [(20, 5000)] + [(1, 8000), (2, 2), (0, 7), (8, 4000)], 8, 1, 16, seed=81)
+    out = x.run()
+    plan = pg.paged_gqa_last_plan()
+    assert plan["path_bits"] == 6 and plan["kernels_launched"] == 4
+    su.compare(out, x.reference(), "mixed")
+    for _ in range(20):
+        assert torch.equal(x.run(), out)
