@@ -322,11 +322,12 @@ def paged_gqa_build_tables(q_lens, ctx_lens, rows, page_size: int, pages, page_c
 
     page_counts and num_free are updated in place where no output is given."""
     lib = load()
-    t = (q_lens, ctx_lens, rows, pages, page_counts, free_pages, num_free, block_table, seq_lens, query_start_loc, slot_map,
-         page_counts if page_counts_out is None else page_counts_out, num_free if num_free_out is None else num_free_out)
+    t = (q_lens, ctx_lens, rows, pages, page_counts, free_pages, num_free, block_table, seq_lens, query_start_loc, slot_map)
+    t += tuple(x for x in (page_counts_out, num_free_out) if x is not None)
     _on_device(*t)
     d = _pack(*t)
-    _check(lib.paged_gqa_build_tables(*d[:3], int(page_size), *d[3:], _stream(stream)))
+    counts_out, num_out = d[4] if page_counts_out is None else d[11], d[6] if num_free_out is None else d[-1]
+    _check(lib.paged_gqa_build_tables(*d[:3], int(page_size), *d[3:11], counts_out, num_out, _stream(stream)))
 
 
 def paged_gqa_tree_masks(parents, seq_lens, query_start_loc, masks, positions, stream=None) -> None:

@@ -1,4 +1,5 @@
-// self_plan.cuh -- a verify-class kernel that plans its own class (Problem::fused_verify).
+// self_plan.cuh -- a verify-class kernel that plans its own class (Problem::fused_verify), or a tree call's one kernel
+// that plans every sequence (Problem::self_all, kAll below).
 //
 // Every CTA works out the plan kernel's cut of the verify blocks (one per verify sequence
 // and kv head, in sequence order, each fixed_cost(0) units and then its ceil(L / 128) key

@@ -31,6 +31,21 @@ def test_tables_of_one_request_without_anything():
     su.check_tables(x, 1, 3)
 
 
+@pytest.mark.parametrize("counts_too", [False, True])
+def test_tables_with_one_output_in_place(counts_too):
+    x = su.requests(5, 20, 16, 30)
+    i32 = lambda y: torch.tensor(y, dtype=torch.int32, device="cuda")  # noqa: E731
+    t = {n: i32(x[n] if n != "num_free" else [x[n]]) for n in ("q_lens", "ctx_lens", "rows", "pages", "counts", "free", "num_free")}
+    T = sum(n for n in x["q_lens"] if n > 0)
+    table, lens, qsl, slots = i32([[0] * 30] * 20), i32([0] * 20), i32([0] * 21), i32([0] * T)
+    counts, num = torch.zeros_like(t["counts"]), i32([0])
+    pg.paged_gqa_build_tables(t["q_lens"], t["ctx_lens"], t["rows"], 16, t["pages"], t["counts"], t["free"], t["num_free"], table, lens, qsl, slots,
+                              **({"page_counts_out": counts} if counts_too else {"num_free_out": num}))
+    want = step.build_tables(**x, width=30, tokens=T)
+    assert (counts if counts_too else t["counts"]).tolist() == want["counts"]
+    assert (t["num_free"] if counts_too else num).tolist() == want["num_free"] and table.tolist() == want["table"]
+
+
 def test_tables_without_requests():
     x = dict(q_lens=[], ctx_lens=[], rows=[], page_size=16, pages=[[5, 6]], counts=[1], free=[9], num_free=1)
     su.check_tables(x, 2, 4)
@@ -458,7 +473,8 @@ def test_blocks_of_many_pieces_and_the_same_bits_again(seqs, hq, hkv, cache):
 
 
 @pytest.mark.parametrize("cache", ["e4m3", "bf16"])
-@pytest.mark.parametrize("seqs", [[(40, 900)], [(5, 700), (3, 90)], [(40, 900), (5, 700)]])
+@pytest.mark.parametrize("seqs", [[(40, 900)], [(5, 700), (3, 90)], [(40, 900), (5, 700)], [(3, 9000)] * 3 + [(20, 5000), (1, 8000)],
+                                  [(17, 40)] * 460])
 def test_a_tree_wait_that_runs_out_reports_timeout_and_the_next_call_is_correct(seqs, cache):
     x = su.Tree(seqs, 8, 1, 16, cache, seed=21)
     prev = pg.paged_gqa_set_stall_test(200_000)
