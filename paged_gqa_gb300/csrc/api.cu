@@ -23,6 +23,7 @@
 #include "prompt.cuh"
 #include "step.cuh"
 #include "tc_kernels.cuh"
+#include "workspace.cuh"
 
 namespace pgqa {
 __device__ uint32_t g_error_word;
@@ -125,62 +126,6 @@ int device_state(int dev, DeviceState** out) {
 
 // ---------------------------------------------------------------- workspace layout --
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-struct ClassSizes {
-  int num_ctas, max_blocks, max_items, max_slots, slot_rows;
-};
-
-struct WsLayout {
-  ClassSizes cls[kNumClasses];
-  size_t off[kNumClasses][8];
-  size_t q_amax_off;  // per-CTA maxima of |q| (calls that quantise Q)
-  size_t epoch_off;   // the split counters' epoch word
-  size_t total;
-};
-
-WsLayout make_layout(int num_seqs, int T, int Hq, int Hkv, int sms) {
-  WsLayout L{};
-  const long long G = Hq / Hkv;
-  const long long rows_all = (long long)T * G;
-  // verify blocks: one per (sequence, kv head); prefill blocks: 128-row blocks
-  const long long vb = (long long)num_seqs * Hkv;
-  // a prefill block needs some sequence with q_len*G > 64, so none exist if T*G <= 64
-  const long long pb =
-      rows_all > kVerifyRows ? (long long)Hkv * ((rows_all + kPrefillRows - 1) / kPrefillRows + num_seqs) : 0;
-  const long long nb[2] = {vb, pb};
-  const int rows[2] = {kVerifyRows, kPrefillRows};
-  size_t at = 0;
-  for (int c = 0; c < kNumClasses; ++c) {
-    ClassSizes& s = L.cls[c];
-    s.num_ctas = sms;
-    s.max_blocks = (int)std::max<long long>(1, nb[c]);
-    s.max_items = s.max_blocks + s.num_ctas;
-    // Split pieces take slots by split_slot_base: below 2 per CTA.
-    s.max_slots = nb[c] == 0 ? 0 : 2 * s.num_ctas;
-    s.slot_rows = rows[c];
-    size_t sz[8] = {
-        256,                                                          // n_blocks, n_items, total_tiles
-        sizeof(int) * (size_t)(s.num_ctas + 1),                       // cta_item_begin
-        sizeof(RowBlock) * (size_t)s.max_blocks,                      // blocks
-        sizeof(WorkItem) * (size_t)s.max_items,                       // items
-        sizeof(unsigned long long) * (size_t)s.max_blocks,            // counters
-        sizeof(uint16_t) * (size_t)s.max_slots * s.slot_rows * kHeadDim, // part_o (f16)
-        sizeof(float) * (size_t)s.max_slots * s.slot_rows,            // part_lse
-        0};
-    for (int i = 0; i < 8; ++i) {
-      L.off[c][i] = at;
-      at += align256(sz[i]);
-    }
-  }
-  L.q_amax_off = at;
-  at += align256(sizeof(float) * (size_t)q_amax_parts(sms));
-  L.epoch_off = at;
-  at += 256;
-  L.total = at;
-  return L;
-}
-
 ClassPlan class_plan(const WsLayout& L, int c, char* base) {
   ClassPlan cp{};
   const size_t* o = L.off[c];
@@ -191,7 +136,7 @@ ClassPlan class_plan(const WsLayout& L, int c, char* base) {
   cp.blocks = reinterpret_cast<RowBlock*>(base + o[2]);
   cp.items = reinterpret_cast<WorkItem*>(base + o[3]);
   cp.counters = reinterpret_cast<unsigned long long*>(base + o[4]);
-  cp.epoch = reinterpret_cast<unsigned long long*>(base + L.epoch_off);
+  cp.epoch = reinterpret_cast<unsigned long long*>(base + kWsEpochOff);
   cp.part_o = reinterpret_cast<uint16_t*>(base + o[5]);
   cp.part_lse = reinterpret_cast<float*>(base + o[6]);
   cp.num_ctas = L.cls[c].num_ctas;
@@ -986,27 +931,14 @@ int attn_tree(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const 
                         [&](void* ws, bool) { return run(val, k, v, ws, L.total, L, ds, stream); });
 }
 
-// Workspace of the prompt attention.
-size_t prompt_layout(int clusters, char* base, PromptScratch* ws) {
-  const size_t slots = 4 * (size_t)clusters;
-  size_t at = 0;
-  auto part = [&](size_t bytes) {
-    const size_t o = at;
-    at += align256(bytes);
-    return base + o;
-  };
-  char* o = part(slots * 128 * kHeadDim * sizeof(float));
-  char* l = part(slots * 128 * sizeof(float));
-  char* c = part(slots * sizeof(unsigned long long));
-  char* e = part(sizeof(unsigned long long));
-  if (ws) {
-    ws->part_o = reinterpret_cast<float*>(o);
-    ws->part_lse = reinterpret_cast<float*>(l);
-    ws->counters = reinterpret_cast<unsigned long long*>(c);
-    ws->epoch = reinterpret_cast<unsigned long long*>(e);
-    ws->call_tag = next_call_tag();
-  }
-  return at;
+PromptScratch prompt_scratch(const PromptLayout& L, char* base) {
+  PromptScratch ws;
+  ws.part_o = reinterpret_cast<float*>(base + L.part_o);
+  ws.part_lse = reinterpret_cast<float*>(base + L.part_lse);
+  ws.counters = reinterpret_cast<unsigned long long*>(base + L.counters);
+  ws.epoch = reinterpret_cast<unsigned long long*>(base + kWsEpochOff);
+  ws.call_tag = next_call_tag();
+  return ws;
 }
 
 int attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const pg_tensor* qsl, float softmax_scale,
@@ -1081,11 +1013,11 @@ int attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, cons
   a.err = ds->err;
   a.stall_test_ns = g_stall_test_ns.load();
   const int clusters = prompt_clusters(T, (int)S, (int)Hkv, (int)G, ds->sms);
-  return with_workspace(ds, prompt_layout(clusters, nullptr, nullptr), user_ws, user_ws_bytes, use_user_ws,
-                        "paged_gqa_attn_prompt_ex", stream, [&](void* ws, bool captured) -> int {
-    PromptScratch scratch;
-    prompt_layout(clusters, static_cast<char*>(ws), &scratch);
-    int64_t plan_info[8] = {2 * clusters, 0, 1, 256, 0, 0, (int64_t)prompt_layout(clusters, nullptr, nullptr), 0};
+  const PromptLayout L = prompt_layout(clusters);
+  return with_workspace(ds, L.total, user_ws, user_ws_bytes, use_user_ws, "paged_gqa_attn_prompt_ex", stream,
+                        [&](void* ws, bool captured) -> int {
+    const PromptScratch scratch = prompt_scratch(L, static_cast<char*>(ws));
+    int64_t plan_info[8] = {2 * clusters, 0, 1, 256, 0, 0, (int64_t)L.total, 0};
     int r = 0;
     if (g_path.load() != 1 && (r = launch_prompt_tc(a, scratch, clusters, captured, stream)) < 0)
       return fail(PG_ERR_CUDA, "tcgen05 prompt launch failed: %s", tc_last_error());
@@ -1704,7 +1636,7 @@ size_t paged_gqa_prompt_workspace_size(int num_seqs, int total_tokens, int num_q
     return 0;
   int sms = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0) return 0;
-  return prompt_layout(prompt_clusters(total_tokens, num_seqs, num_kv_heads, num_q_heads / num_kv_heads, sms), nullptr, nullptr);
+  return prompt_layout(prompt_clusters(total_tokens, num_seqs, num_kv_heads, num_q_heads / num_kv_heads, sms)).total;
 }
 
 int paged_gqa_version(void) { return 100; }
