@@ -194,7 +194,8 @@ struct ClassPlan {
   WorkItem* items;         // [max_items]
   // [max_blocks] split counters: (48-bit tag << 16) | pieces arrived. A word whose tag is
   // not this call's counts as zero, so nothing has to clear them between calls (the tag
-  // changes on every call, CUDA-graph replays included) and a workspace needs no zeroing.
+  // changes on every call, CUDA-graph replays included) and a workspace needs no zeroing; a block's last
+  // piece clears its word.
   unsigned long long* counters;
   unsigned long long* epoch;  // [1] workspace word the plan kernel advances once per call
   uint16_t* part_o;        // [max_slots][slot_rows][kHeadDim] f16: O / l in cache-code units (v_descale is

@@ -126,11 +126,16 @@ __device__ __forceinline__ void fence_acq_rel_gpu() { asm volatile("fence.acq_re
 // counter word holds (tag << 16) | arrivals (nsplit < 2^16). Whoever finds another tag there puts
 // its own with no arrivals (one compare-and-swap of any number succeeds, and the others then see the
 // tag), and every piece adds one: pieces that arrive together need two round trips, where counting by
-// compare-and-swap took one after the other (152 pieces: 20 us).
+// compare-and-swap took one after the other (152 pieces: 20 us). The last piece clears the word (split_clear): a
+// finished call leaves no arrivals behind, whatever its tag, so a graph whose workspace another program writes between
+// replays, epoch word included, counts from none all the same.
 // split_peek reads the word for split_arrive_from, so that its round trip can overlap the
 // wait for the piece's partial; split_arrive reads it itself.
 __device__ __forceinline__ unsigned long long split_peek(const unsigned long long* counter) {
   return *reinterpret_cast<const volatile unsigned long long*>(counter);
+}
+__device__ __forceinline__ void split_clear(unsigned long long* counter) {
+  *reinterpret_cast<volatile unsigned long long*>(counter) = 0;
 }
 __device__ __forceinline__ bool split_arrive_from(unsigned long long* counter, unsigned long long old, int nsplit,
                                                   unsigned long long tag) {
@@ -139,7 +144,9 @@ __device__ __forceinline__ bool split_arrive_from(unsigned long long* counter, u
     if (seen == old) break;
     old = seen;
   }
-  return (unsigned)(atomicAdd(counter, 1ull) & 0xffffu) + 1u == (unsigned)nsplit;
+  const bool last = (unsigned)(atomicAdd(counter, 1ull) & 0xffffu) + 1u == (unsigned)nsplit;
+  if (last) split_clear(counter);
+  return last;
 }
 __device__ __forceinline__ bool split_arrive(unsigned long long* counter, int nsplit, unsigned long long tag) {
   return split_arrive_from(counter, split_peek(counter), nsplit, tag);

@@ -779,6 +779,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         if (I.nsplit > 1) {
           if (gi == 0) {
             ms.merge_flag = split_peek(counter) == (tag << 16 | (unsigned)(I.nsplit - 1));
+            if (ms.merge_flag) split_clear(counter);
             __threadfence();
           }
           named_barrier(9, kEpiThreads);

@@ -97,3 +97,21 @@ def test_two_shapes_of_one_call_captured_on_one_workspace():
     second = _capture(lambda: pg.paged_gqa_attn_ex(*a, 1.0, x.k_descale, x.v_descale, x.scale, wide, ws))
     graph = _capture(lambda: call(ws))
     _replay_and_compare(q, out, eager, graph, gen, lambda: (second.replay(), torch.cuda.synchronize()))
+
+
+def _prompt():
+    x = su.Prompt([9000, 700], 4, 1, seed=13, fused=False)
+    out = torch.empty_like(x.q)
+    need = pg.paged_gqa_prompt_workspace_size(2, x.T, 4, 1)
+    a = (x.q, x.k, x.v, x.qsl_t, x.scale)
+    return x.q, out, lambda o: pg.paged_gqa_attn_prompt(*a, o), lambda ws: pg.paged_gqa_attn_prompt_ex(*a, out, None, ws), need
+
+
+@pytest.mark.parametrize("which", [_verify, _fp4, _tree, _prompt])
+def test_a_program_that_uses_the_workspace_between_replays(which):
+    """It writes the same values over the first bytes each time; the rest stays as the last replay left it."""
+    gen = torch.Generator().manual_seed(9)
+    q, out, eager, call, need = which()
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graph = _capture(lambda: call(ws))
+    _replay_and_compare(q, out, eager, graph, gen, lambda: ws[:256].fill_(7))
