@@ -1,7 +1,8 @@
 // prompt_mma.cu -- causal attention over whole packed prompts in its simplest form: warp-level
 // mma.sync, one CTA per 64 rows (row r of a prompt and kv head: token r / G, head r % G), every
-// block by itself. It runs under paged_gqa_set_path(1), where the tests compare the tcgen05
-// kernel with it.
+// block by itself. It serves calls whose strides no tensor map can say (a token or head stride of q, k or v
+// that is not positive, or of 2^38 elements and more; tokens that share their K, for example), and runs under
+// paged_gqa_set_path(1), where the tests compare the tcgen05 kernel with it.
 //
 // A warp holds 16 rows: their Q as MMA fragments (64 registers), their O in fp32 (128). K and V
 // come 32 keys at a time into shared memory; S = Q K^T, the running maximum and sum of the
@@ -50,10 +51,11 @@ __global__ void __launch_bounds__(kThreads) prompt_mma_kernel(PromptArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, tq = lane & 3;
   const int kvh = blockIdx.y;
-  // the sequence that holds row block blockIdx.x of this kv head
+  // the sequence that holds row block blockIdx.x of this kv head; the first CTA goes through all of them, to flag bad ones
+  const bool flags = blockIdx.x == 0 && kvh == 0;
   int seq = -1, block = 0, q0 = 0, qn = 0;
   long long pre = 0;
-  for (int s0 = 0; s0 < a.num_seqs && seq < 0; s0 += 32) {
+  for (int s0 = 0; s0 < a.num_seqs && (seq < 0 || flags); s0 += 32) {
     const int s = s0 + lane;
     int start = 0, n = 0;
     if (s < a.num_seqs) {
@@ -61,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) prompt_mma_kernel(PromptArgs a) {
       const int end = a.qsl[s + 1];
       n = end - start;
       if (start < 0 || end < start || end > a.T) {
-        if (blockIdx.x == 0 && kvh == 0 && warp == 0) atomicOr(a.err, kErrBounds);
+        if (flags && warp == 0) atomicOr(a.err, kErrBounds);
         n = 0;
       }
     }
