@@ -335,13 +335,14 @@ plan_kernel(Problem p, Pointers ptr, ClassPlan c0, ClassPlan c1, int plan_verify
   }
   if (has_p) plan_class(p, ptr, c1, 1, sm); else empty_class(c1);
   if (threadIdx.x == 0 && s_overflow) {
-    // Host-side bounds make this unreachable; flag it rather than run a partial plan.
+    // More blocks than the host counted on (sequences that share their tokens): flagged, no partial plan runs. No
+    // blocks either, as the merge kernel of tree calls goes by their records.
     atomicOr(ptr.err, kErrBounds);
     if (plan_verify) {
-      *c0.n_items = 0;
+      *c0.n_blocks = *c0.n_items = 0;
       for (int c = 0; c <= c0.num_ctas; ++c) c0.cta_item_begin[c] = 0;
     }
-    *c1.n_items = 0;
+    *c1.n_blocks = *c1.n_items = 0;
     for (int c = 0; c <= c1.num_ctas; ++c) c1.cta_item_begin[c] = 0;
   }
   // New split-counter tag for the next call: every kernel of this call that reads the epoch
