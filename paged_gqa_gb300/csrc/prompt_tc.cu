@@ -737,8 +737,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         const bool valid = row < used && tok < I.n;
         mbar_wait(bar(ms.stat_full[i % kRing]), (i / kRing) & 1, abort_flag, a.err);
         const float lr = ms.stat_l[i % kRing][0][row] + ms.stat_l[i % kRing][1][row];
-        const float inv = lr > 0.f ? 1.f / lr : 0.f;
-        const float lse = lr > 0.f ? ms.stat_m[i % kRing][row] - kSigma + log2f(lr) : -INFINITY;
+        // (a piece of which a row sees nothing has the sum 0; a NaN is not that)
+        const float inv = lr == 0.f ? 0.f : 1.f / lr;
+        const float lse = lr == 0.f ? -INFINITY : ms.stat_m[i % kRing][row] - kSigma + log2f(lr);
         const int head = I.kvh * a.G + my_g;
         const long long out_at = valid ? (long long)(I.q0 + tok) * a.o_st + (long long)head * a.o_sh : -1;  // this row (-1: none)
         const long long lse_at = (long long)(I.q0 + tok) * a.lse_st + (long long)head * a.lse_sh;

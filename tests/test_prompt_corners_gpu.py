@@ -1,4 +1,4 @@
-"""Prompt attention on what its other tests leave out: many prompts of which one is bad."""
+"""Prompt attention on what its other tests leave out: many prompts of which one is bad, statistics of NaN rows."""
 import pytest
 import torch
 
@@ -27,3 +27,25 @@ def test_one_bad_prompt_among_many_is_flagged(path, lens, bad):
     assert torch.isnan(out[first:]).all()
     x.check(out, None, rows={s: list(range(n)) for s, n in enumerate(lens[:bad]) if n})
     assert good.isfinite().all()
+
+
+@pytest.mark.parametrize("path", [0, 1])
+@pytest.mark.parametrize("lens,hq", [([300, 40], 8), ([9000, 3], 2)])
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_statistics_of_rows_with_a_nan_are_nan(path, lens, hq, which):
+    x = su.Prompt(lens, hq, 1, seed=71, fused=False)
+    if which == "q":
+        x.q[[17, 250], 1] = float("nan")
+        rows = torch.zeros(x.T, hq, dtype=torch.bool, device="cuda")
+        rows[[17, 250], 1] = True
+    else:  # every token of the prompt from 200 on sees it
+        x.k[200, 0, 5] = float("nan")
+        rows = torch.zeros(x.T, hq, dtype=torch.bool, device="cuda")
+        rows[200:lens[0]] = True
+    prev = pg.paged_gqa_set_path(path)
+    try:
+        out, lse = x.run()
+    finally:
+        pg.paged_gqa_set_path(prev)
+    assert torch.isnan(out[rows]).all() and out[~rows].isfinite().all()
+    assert torch.isnan(lse[rows]).all() and lse[~rows].isfinite().all()
