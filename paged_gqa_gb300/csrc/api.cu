@@ -1026,6 +1026,8 @@ int attn_prompt(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, cons
       if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
       plan_info[0] = 0;
       plan_info[3] = 512;
+    } else if (captured) {
+      plan_info[2] = 2;  // the epoch word moves in a kernel of its own
     }
     memcpy(t_last_plan, plan_info, sizeof plan_info);
     return PG_OK;

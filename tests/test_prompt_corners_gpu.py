@@ -1,4 +1,4 @@
-"""Prompt attention on what its other tests leave out: many prompts of which one is bad, statistics of NaN rows."""
+"""Prompt attention on what its other tests leave out: many prompts of which one is bad, statistics of NaN rows, the launch summary."""
 import pytest
 import torch
 
@@ -49,3 +49,22 @@ def test_statistics_of_rows_with_a_nan_are_nan(path, lens, hq, which):
         pg.paged_gqa_set_path(prev)
     assert torch.isnan(out[rows]).all() and out[~rows].isfinite().all()
     assert torch.isnan(lse[rows]).all() and lse[~rows].isfinite().all()
+
+
+def test_the_launch_summary_counts_a_captured_calls_kernels():
+    x = su.Prompt([300], 8, 1, seed=72)
+    out = torch.empty_like(x.q)
+    ws = torch.empty(pg.paged_gqa_prompt_workspace_size(1, 300, 8, 1), dtype=torch.uint8, device="cuda")
+    call = lambda: pg.paged_gqa_attn_prompt_ex(x.q, x.k, x.v, x.qsl_t, x.scale, out, None, ws)  # noqa: E731
+    st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        call()
+        st.synchronize()
+        assert pg.paged_gqa_last_plan()["kernels_launched"] == 1
+        with torch.cuda.graph(g, stream=st):
+            call()
+        assert pg.paged_gqa_last_plan()["kernels_launched"] == 2  # the epoch word moves first
+        g.replay()
+        st.synchronize()
+    x.check(out, None)
