@@ -83,16 +83,19 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) tree_merge_kernel(Pro
                                                                  int classes) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const int first = blockIdx.x * kWarps + (threadIdx.x >> 5), warps = gridDim.x * kWarps;
+  const long long first = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int warps = gridDim.x * kWarps;
 #pragma unroll 1
   for (int c = 0; c < kNumClasses; ++c) {
     if (!(classes >> c & 1)) continue;
     const ClassPlan& cp = c ? c1 : c0;
-    const int rows = c ? kPrefillRows : kVerifyRows;
-    const int n = min(*cp.n_blocks, cp.max_blocks) * rows;
-    for (int u = first; u < n; u += warps) {
-      const RowBlock& b = cp.blocks[u / rows];
-      const int row = u % rows;
+    constexpr int kVShift = 6, kPShift = 7;
+    static_assert(1 << kVShift == kVerifyRows && 1 << kPShift == kPrefillRows, "rows of a block");
+    const int shift = c ? kPShift : kVShift;
+    const long long n = (long long)min(*cp.n_blocks, cp.max_blocks) << shift;  // (may pass 2^31)
+    for (long long u = first; u < n; u += warps) {
+      const RowBlock& b = cp.blocks[u >> shift];
+      const int row = (int)u & ((1 << shift) - 1);
       if (b.nsplit <= 1 || row >= b.nrows) continue;
       // (the plan's own bounds: a record that is none must not lead anywhere)
       if (b.slot_base < 0 || b.slot_base + b.nsplit > cp.max_slots || b.seq < 0 || b.seq >= p.num_seqs || b.kvh < 0 || b.kvh >= p.Hkv)

@@ -1,4 +1,4 @@
-"""Tree attention under each of its plans: calls whose plan does not fit."""
+"""Tree attention under each of its plans: calls whose plan does not fit, the largest number of blocks."""
 import pytest
 import torch
 
@@ -31,3 +31,26 @@ def test_a_plan_that_does_not_fit_leaves_out_as_it_was(path, cache):
     _on_path(path, lambda: x.run(out=out, check=False))
     assert pg.paged_gqa_check_device_errors() == -5
     assert (out == 5).all()
+
+
+def test_more_rows_of_blocks_than_31_bits_count():
+    """2^25 blocks of 64 rows: a million sequences of one token and 32 kv heads, all on the same pages."""
+    S, H, L, P = 2 ** 20, 32, 380, 128
+    dev = "cuda"
+    gen = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(3, P, H, 256, generator=gen).to(torch.float8_e4m3fn).to(dev) for _ in range(2))
+    q = torch.randn(1, H, 256, generator=gen).bfloat16().to(dev).expand(S, H, 256)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=dev).expand(S, 3)
+    lens = torch.full((S,), L, dtype=torch.int32, device=dev)
+    qsl = torch.arange(S + 1, dtype=torch.int32, device=dev)
+    masks = torch.ones(1, 1, dtype=torch.int32, device=dev).expand(S, 1)
+    out = torch.full((S, H, 256), float("nan"), dtype=torch.bfloat16, device=dev)
+    pg.paged_gqa_attn_tree(q, k, v, table, lens, qsl, masks, 1.0, 1.0, 1 / 16, out)
+    assert pg.paged_gqa_check_device_errors() == 0
+    ks, vs = (c.double()[[2, 0, 1]].reshape(-1, H, 256)[:L] for c in (k, v))
+    w = torch.softmax(torch.einsum("hd,khd->hk", q[0].double(), ks) / 16, 1)
+    want = torch.einsum("hk,khd->hd", w, vs)
+    su.compare(out[0], want.cpu().numpy(), "first")
+    for i in range(0, S, 2 ** 16):  # the others differ in the order of a split block's sums at most: a bf16 step
+        part = out[i:i + 2 ** 16].float()
+        assert ((part - out[0].float()).abs() <= 2.0 ** -7 * out[0].float().abs() + 2.0 ** -9).all(), i
