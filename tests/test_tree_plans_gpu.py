@@ -1,4 +1,4 @@
-"""Tree attention under each of its plans: calls whose plan does not fit, the largest number of blocks."""
+"""Tree attention under each of its plans: which kernels serve a call, calls whose plan does not fit, the largest number of blocks."""
 import pytest
 import torch
 
@@ -31,6 +31,58 @@ def test_a_plan_that_does_not_fit_leaves_out_as_it_was(path, cache):
     _on_path(path, lambda: x.run(out=out, check=False))
     assert pg.paged_gqa_check_device_errors() == -5
     assert (out == 5).all()
+
+
+WHICH = [  # (sequences, path, path bits, kernels): e4m3 caches, 8/2 heads
+    ([(16, 600)], 0, 2, 2),                                            # the verify kernel alone, and the merge
+    ([(5, 400), (3, 300), (8, 600)], 0, 2, 2),
+    ([(40, 600), (5, 400), (3, 300)], 3, 6, 4),                        # plan, verify, prefill, merge
+    ([(3, 9000)] * 3 + [(20, 5000)] + [(1, 8000), (2, 2), (0, 7), (8, 4000)], 0, 6, 4),  # the verify kernel plans its own class
+    ([(40, 600), (5, 400), (3, 300)], 0, 4, 2),                        # the prefill kernel plans every sequence
+]
+
+
+@pytest.mark.parametrize("case", range(len(WHICH)))
+def test_scores_of_2_to_the_34_in_every_kernel_of_e4m3_caches(case):
+    seqs, path, bits, kernels = WHICH[case]
+    x = su.Tree(seqs, 8, 2, 16, seed=23, masks="all")
+    nan = torch.isnan(x.k.float())
+    gen = torch.Generator().manual_seed(23)
+    x.q = torch.randint(-3, 4, x.q.shape, generator=gen).bfloat16().cuda()  # small whole numbers: scores are exact
+    x.k = torch.randint(-3, 4, x.k.shape, generator=gen).float().cuda().masked_fill(nan, float("nan")).to(x.k.dtype)
+    x.scale = 2.0 ** 26
+    out = _on_path(path, x.run).float()
+    plan = pg.paged_gqa_last_plan()
+    assert plan["path_bits"] == bits and plan["kernels_launched"] == kernels
+    seen = 0
+    for s, (n, L) in enumerate(x.seqs):
+        ids = x.table[s, :-(-L // 16)].long()
+        for h in range(8 if n else 0):
+            ks, vs = (c.float()[ids, :, h // 4].reshape(-1, 256)[:L] for c in (x.k, x.v))
+            score = x.q[x.qsl[s]:x.qsl[s + 1], h].double() @ ks.double().T
+            score = score.masked_fill(torch.arange(L, device="cuda") > L - n + torch.arange(n, device="cuda")[:, None], -1e9)
+            top = score.topk(2, dim=1)
+            alone = top.values[:, 0] > top.values[:, 1]
+            seen += int(alone.sum())
+            got, want = out[x.qsl[s]:x.qsl[s + 1], h][alone], (vs[top.indices[:, 0]] * x.v_descale)[alone]
+            # the largest score's V itself: an e4m3 value times a power of two is exact in f16 pieces and in bf16
+            assert torch.equal(got, want)
+    assert seen > 4 * sum(n for n, _ in seqs)
+
+
+@pytest.mark.parametrize("path,bits", [(0, 4), (3, 6)])
+def test_rows_that_see_nothing_are_zeros_under_each_plan(path, bits):
+    x = su.Tree([(5, 5), (3, 40), (130, 130), (2, 2)], 8, 2, 16, masks="none")
+    out = _on_path(path, x.run)
+    assert pg.paged_gqa_last_plan()["path_bits"] == bits
+    su.compare(out, x.reference(), path)
+    for s in (0, 2, 3):
+        assert (out[x.qsl[s]:x.qsl[s + 1]] == 0).all()
+    x = su.Tree([(5, 5), (2, 40), (1, 1)], 8, 1, 16, masks="none")  # at most 64 rows: the verify kernel alone
+    out = x.run()
+    assert pg.paged_gqa_last_plan()["path_bits"] == 2
+    su.compare(out, x.reference(), "verify")
+    assert (out[:5] == 0).all() and (out[7:] == 0).all()
 
 
 def test_more_rows_of_blocks_than_31_bits_count():
