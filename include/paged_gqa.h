@@ -413,8 +413,10 @@ int paged_gqa_tree_masks(const pg_tensor* parents, const pg_tensor* seq_lens, co
  * among them (bits from t + 1 on are not used; any masks do, a tree's or not). A row that sees no
  * key is zeros. masks is int32 [T, words], rows any distance apart; a sequence of more than 32 * words
  * new tokens is flagged like other bad bounds, its rows are zeros. q is bf16, the caches bf16 or
- * e4m3; everything else is as in paged_gqa_attn, out and q must not overlap (refused). A NaN or
- * infinity in V of a key reaches the tokens that see it, and may reach others of its sequence. Slots behind seq_lens and other pages do not matter. With bf16
+ * e4m3; everything else is as in paged_gqa_attn. out shares memory with no input (refused for q, and for masks,
+ * block_table, seq_lens and query_start_loc, whose addresses, first to last, its rows may not meet). A NaN or
+ * infinity in V of a key reaches the tokens that see it, and may reach others of its sequence. Slots behind seq_lens and
+ * other pages do not matter. With bf16
  * caches |V| must not pass 65504 (the pieces of a split sequence are held in f16, as in paged_gqa_attn).
  *
  * Calls are ordered by the library as those of paged_gqa_attn_fp4 (one workspace); in a stream

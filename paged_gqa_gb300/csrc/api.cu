@@ -697,6 +697,45 @@ bool ints_meet(const pg_tensor* a, const pg_tensor* b) {
   return lo[0] < hi[1] && lo[1] < hi[0];
 }
 
+// Does a run of `span` bytes at one of the places sum_i c_i str_i (0 <= c_i < ext_i; the strides, from the largest down, each
+// step past all that the smaller ones span) meet the bytes [lo, hi)?
+bool runs_meet(const long long* str, const long long* ext, int n, long long span, long long lo, long long hi) {
+  if (n == 0) return lo < span && hi > 0;
+  long long inner = span;
+  for (int i = 1; i < n; ++i) inner += (ext[i] - 1) * str[i];
+  // the indexes whose [c str, c str + inner) meets it
+  const long long first = lo < inner ? 0 : (lo - inner) / str[0] + 1;
+  const long long last = hi <= 0 ? -1 : std::min(ext[0] - 1, (hi - 1) / str[0]);
+  if (last - first >= 2) return true;  // the run that begins at one between them begins in [lo, hi)
+  for (long long c = first; c <= last; ++c)
+    if (runs_meet(str + 1, ext + 1, n - 1, span, lo - c * str[0], hi - c * str[0])) return true;
+  return false;
+}
+// Do the (disjoint) rows of kHeadDim values of `size` bytes of a tensor, indexed by its first nd dims, meet the addresses,
+// first to last, of an int32 tensor?
+bool rows_meet_ints(const pg_tensor* t, int nd, int size, const pg_tensor* ints) {
+  long long str[4], ext[4];
+  int n = 0;
+  for (int i = 0; i < nd; ++i) {
+    if (t->shape[i] == 0) return false;
+    if (t->shape[i] == 1) continue;
+    int j = n++;
+    for (; j > 0 && str[j - 1] < t->stride[i] * size; --j) {
+      str[j] = str[j - 1];
+      ext[j] = ext[j - 1];
+    }
+    str[j] = t->stride[i] * size;
+    ext[j] = t->shape[i];
+  }
+  long long lo = (long long)(reinterpret_cast<intptr_t>(ints->data) - reinterpret_cast<intptr_t>(t->data)), hi = lo + 4;
+  for (int d = 0; d < ints->ndim; ++d) {
+    if (ints->shape[d] == 0) return false;
+    const long long last = ints->shape[d] > 1 ? 4 * (ints->shape[d] - 1) * ints->stride[d] : 0;
+    (last < 0 ? lo : hi) += last;
+  }
+  return runs_meet(str, ext, n, (long long)kHeadDim * size, lo, hi);
+}
+
 struct Named {
   const pg_tensor* t;
   const char* name;
@@ -921,6 +960,9 @@ int attn_tree(const pg_tensor* q, const pg_tensor* k, const pg_tensor* v, const 
   }
   if (k->shape[0] == 0 || W == 0) return fail(PG_ERR_INVALID_ARG, "new tokens without pages");
   if (rows_overlap(q, out)) return fail(PG_ERR_INVALID_ARG, "out overlaps q");
+  const Named read[] = {{masks, "masks"}, {bt, "block_table"}, {sl, "seq_lens"}, {qsl, "query_start_loc"}};
+  for (const Named& x : read)  // other CTAs may still read them
+    if (rows_meet_ints(out, 2, 2, x.t)) return fail(PG_ERR_INVALID_ARG, "out overlaps %s", x.name);
   val.p.mask_words = (int)words;
   val.p.mask_st = T > 1 ? masks->stride[0] : 0;
   val.ptr.masks = static_cast<const int32_t*>(masks->data);
