@@ -441,7 +441,9 @@ int paged_gqa_attn_tree_ex(const pg_tensor* q, const pg_tensor* k_cache, const p
  *   block_table, seq_lens, query_start_loc  as in paged_gqa_attn
  *   kept       [S, D]    int32  the accepted tokens' numbers among the sequence's new ones, increasing
  *   num_kept   [S]       int32  how many of them count, 0 .. min(D, q_len)
- *   seq_lens_out [S]     int32  seq_lens - q_len + num_kept; shares memory with no other argument
+ *   seq_lens_out [S]     int32  seq_lens - q_len + num_kept
+ *   No integer tensor lies in a row of a cache, by its addresses from first to last, and seq_lens_out shares memory with none of
+ *   the others (refused).
  *
  * Token kept[s, k] moves from position seq_lens - q_len + kept[s, k] to seq_lens - q_len + k; the
  * rest of the caches is left as it was. Sequences must not share the pages of their new tokens.

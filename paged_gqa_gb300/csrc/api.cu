@@ -1624,6 +1624,10 @@ int paged_gqa_cache_keep(const pg_tensor* k_cache, const pg_tensor* v_cache, con
   if ((st = check_apart(all, 1))) return st;
   if (Hkv < 1) return fail(PG_ERR_INVALID_ARG, "the caches have no kv head");
   if (caches_overlap(k_cache, v_cache, size)) return fail(PG_ERR_INVALID_ARG, "k_cache and v_cache overlap");
+  // the caches are written too: nothing that is read as a number may lie in one, nor may the new lengths
+  for (const Named& x : all)
+    for (const pg_tensor* t : {k_cache, v_cache})
+      if (t->data && rows_meet_ints(t, 3, size, x.t)) return fail(PG_ERR_INVALID_ARG, "%s overlaps %s", x.name, t == k_cache ? "k_cache" : "v_cache");
   if (S == 0) {
     t_last_error.clear();
     return PG_OK;
