@@ -106,3 +106,26 @@ def test_more_rows_of_blocks_than_31_bits_count():
     for i in range(0, S, 2 ** 16):  # the others differ in the order of a split block's sums at most: a bf16 step
         part = out[i:i + 2 ** 16].float()
         assert ((part - out[0].float()).abs() <= 2.0 ** -7 * out[0].float().abs() + 2.0 ** -9).all(), i
+
+
+@pytest.mark.parametrize("tokens,path,bits", [(9, 0, 4), (9, 3, 4), (8, 0, 2), (8, 3, 6)])
+def test_row_sums_keep_what_is_small(tokens, path, bits):
+    """One key of weight 1 and 99 of 2^-12, in one tile: sum = 1 + 99 * 2^-12. V is 1 at the first key and 0 at the others,
+    scaled so that the output, 1.0031, lies 0.8e-3 below the middle of two bf16 values; sums that lose seven of the
+    99 (as additions in 11 bits to the first key's would) are 1.7e-3 too small, and give the other one."""
+    x = su.Tree([(tokens, 100 + tokens)], 8, 1, 16, seed=5, masks="none")
+    ids = x.table[0, :-(-x.lens[0] // 16)].long()
+    pos = torch.arange(ids.numel() * 16, device="cuda").view(-1, 16)
+    k, v = (torch.zeros(ids.numel(), 16, 1, 256, device="cuda") for _ in range(2))
+    k[..., 0, 0] = torch.where(pos == 0, 0.0, -1.0)
+    v[..., 0, :] = (pos == 0).float().unsqueeze(-1)
+    x.k[ids], x.v[ids] = k.to(x.k.dtype), v.to(x.v.dtype)
+    x.q = torch.zeros_like(x.q)
+    x.q[..., 0] = 1.0
+    x.k_descale, x.scale = 1.0, 12 * 0.6931471805599453
+    want = (1 + 2.0 ** -8) * (1 - 0.8e-3)
+    x.v_descale = want * (1 + 99 * 2.0 ** -12)
+    out = _on_path(path, x.run).double()
+    assert pg.paged_gqa_last_plan()["path_bits"] == bits
+    # its own rounding (half a step: 2^-8), fp32's in the scales, the weights and the sums
+    assert ((out - want).abs() <= 2.0 ** -8 + 2.0 ** -18).all(), (out.min(), out.max(), want)
