@@ -367,8 +367,8 @@ int paged_gqa_rope(const pg_tensor* q, const pg_tensor* k, const pg_tensor* posi
  * PG_ERR_DEVICE_BOUNDS: a row outside [-1, R), a row that an earlier request of the batch names, a
  * count outside [0, Wp], q_lens below -1, ctx_lens below 0, more pages than W or Wp, not enough
  * free pages (then the requests behind it get none either). So does a q_lens > 0 without a row, a
- * num_free outside [0, F] (taken as the nearer end), a stack that would pass F (that request keeps its
- * pages) and more new tokens than T (those from T on have no slot). A taken page id that is negative
+ * num_free outside [0, F] (taken as the nearer end), a stack that would pass F (that ended request and those behind it
+ * keep their pages) and more new tokens than T (those from T on have no slot). A taken page id that is negative
  * or whose slots pass 2^31 - 1 has slots of -1 and sets it too. Apart from the two named pairs the
  * addresses of a written tensor, first to last, may meet no other's (refused). Allocates nothing; two launches.
  * (The pages describe no allocator.)
@@ -416,8 +416,11 @@ int paged_gqa_tree_masks(const pg_tensor* parents, const pg_tensor* seq_lens, co
  * e4m3; everything else is as in paged_gqa_attn. out shares memory with no input (refused for q, and for masks,
  * block_table, seq_lens and query_start_loc, whose addresses, first to last, its rows may not meet). A NaN or
  * infinity in V of a key reaches the tokens that see it, and may reach others of its sequence. Slots behind seq_lens and
- * other pages do not matter. With bf16
- * caches |V| must not pass 65504 (the pieces of a split sequence are held in f16, as in paged_gqa_attn).
+ * other pages do not matter.
+ * Scores, the softmax's references and sums and the sums of P.V are held in fp32. Rounded on the way: with e4m3 caches q to the sum
+ * of two e4m3 values (exact from 2^-9 of the largest |q| of its block of rows on, off by 2^-17 of that at most below) and P to
+ * such a sum, by way of f16 (about 2^-8 of a value); with bf16 caches P to bf16 (2^-8); with both, where a sequence is split over
+ * SMs, the normalised output of a piece to f16 (2^-11): with bf16 caches |V| must not pass 65504, which is an infinity there.
  *
  * Calls are ordered by the library as those of paged_gqa_attn_fp4 (one workspace); in a stream
  * capture use paged_gqa_attn_tree_ex, under the terms of paged_gqa_attn_fp4_ex and with a workspace of

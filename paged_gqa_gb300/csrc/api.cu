@@ -305,9 +305,11 @@ int run(const Validated& val, const pg_tensor* k, const pg_tensor* v, void* ws, 
   // Trees of more rows than a verify block holds, on average, are mostly prefill class too.
   const bool wide_trees = p.mask_words > 0 && (long long)p.T * p.G > (long long)kVerifyRows * p.num_seqs;
   // Tree calls of few row blocks are one attention kernel, whose CTAs work out the items of every sequence: trees that are
-  // wide; with bf16 caches any (both classes are the same kernel there: 32 x 6 tokens on 6000 keys 57.7 to 52.2 us); with e4m3
+  // wide; with bf16 caches any (both classes are the same kernel there: 32 x 6 tokens on 6000 keys, 16/1 heads, 57.7 to 52.2 us); with e4m3
   // caches, where the verify kernel serves small trees faster, those of so few pages that launches decide (8 x 5 tokens on
-  // 1000 keys, 64 tiles: 19.1 to 16.7 us, 256 tiles 25.2 to 24.3, 384 22.2 to 21.8, 1024 29.2 to 32.0, 4032 64 to 80).
+  // 1000 keys, 64 tiles: 19.1 to 16.7 us, 256 tiles 25.2 to 24.3, 384 22.2 to 21.8, 1024 29.2 to 32.0, 4032 64 to 80). The host
+  // knows no lengths: max_tiles counts the table's columns, so a table as wide as the longest context allowed keeps small
+  // trees on the verify kernel (the 8 x 5 tokens then take the 19.1).
   const bool few_tiles = (long long)p.num_seqs * p.Hkv * max_tiles <= 3ll * cp[1].num_ctas;
   p.self_all = tc && path != 3 && p.mask_words > 0 && (long long)p.T * p.G > kVerifyRows &&
                (wide_trees || bf16_ok || few_tiles) && cp[1].max_blocks <= kSelfAllBlocks && max_tiles < (1 << 16);

@@ -122,7 +122,7 @@ __device__ __forceinline__ Item load_item(const Problem& p, const ClassPlan& cp,
     r.kvh = rows.kvh;
     r.row0 = rows.row0;
     r.nrows = rows.nrows;
-    r.kv_end = r.L;  // the causal limit of the last row (token qn - 1) is L
+    r.kv_end = r.L;  // the limit of token qn - 1 (kFused 2: of the sequence's last block; see self_plan::load)
     r.kv_hi = min((f.tile_begin + f.ntiles) * kTileKeys, r.kv_end);
     r.nsub = (r.kv_hi - f.tile_begin * kTileKeys + kSub - 1) / kSub;
     return r;

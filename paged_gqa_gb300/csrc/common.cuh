@@ -76,7 +76,7 @@ constexpr unsigned long long kSplitTagMask = (1ull << 48) - 1;
 constexpr int kFusedMaxBlocks = 512;
 // Most row blocks of a tree call whose one attention kernel plans all of them (Problem::self_all): a CTA may have as
 // many items, and more do not fit beside the prefill kernel's tiles. Against the plan kernel, an (empty) verify kernel and the
-// prefill kernel, us: 13 tokens on 700 keys, 16 heads 24.8 to 20.4 (graph), 8 x 60 tokens on 1000 keys 42.7 to 34.6, 32 x 33-60 on
+// prefill kernel, us from a graph: 13 tokens on 700 keys, 16 heads 24.8 to 20.4, 8 x 60 tokens on 1000 keys 42.7 to 34.6, 32 x 33-60 on
 // 2k-16k 233 to 219, 64 x 20-30 on 4k-8k 203 to 189, 8 x 90-100 on 20k-30k 144 to 131.
 constexpr int kSelfAllBlocks = 448;
 

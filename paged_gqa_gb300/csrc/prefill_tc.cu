@@ -185,9 +185,9 @@ __device__ __forceinline__ float2 bf2(uint32_t w) {
 
 // kTree: the new tokens see each other by the call's masks (Problem::mask_words) instead of causally: a thread shifts its 64
 // keys' bits out of its row's words, on tiles that hold new tokens. Pieces of split blocks stay in the workspace
-// (tree_merge.cu). 32 sequences of 33 to 60 tokens on 2k-16k keys, 16/2 heads, take 200 us (its own plan among them; a call 219; 108 us of products at
-// the bf16 rate): the three or four row blocks of a sequence read its pages at different times, 877 MB from HBM where
-// 287 lie (all sequences on the same pages, from L2: a call takes 39 us less); the tensor pipe is busy 59 %. Blocks ordered so
+// (tree_merge.cu). 32 sequences of 33 to 60 tokens on 2k-16k keys, 16/2 heads, take 203 us (its own plan among them; a call 222; 108 us of products at
+// the bf16 rate): the three or four row blocks of a sequence read its pages at different times, 867 MB from HBM where
+// 287 lie (all sequences on the same pages, from L2: a call takes 39 us less); the tensor pipe is busy 58 %. Blocks ordered so
 // that those of a sequence run side by side, where the cut allows, gained 5 % there and lost as much elsewhere;
 // prefetching tiles into L2 two ahead gained nothing.
 // kSelf: the CTAs plan every sequence's blocks by themselves (Problem::self_all).

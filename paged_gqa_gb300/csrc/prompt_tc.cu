@@ -132,8 +132,10 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
 }
 // Between the CTAs of a pair nothing goes through memory that a thread reads: P, S and O lie in TMEM (the tcgen05
 // fences order those), K, V and Q have landed in the shared memory of the SM whose tensor core reads them before
-// their arrival is sent on, and so have the zeros of a tail (proxy fence). So the signals need no order at cluster
-// scope. It is far from free: a release at that scope took 1040 cycles, an acquire 500 to 700 even if the phase
+// their arrival is sent on, and so have the zeros of a tail (proxy fence). So the signals take no order at cluster
+// scope. For what lies in TMEM the two tcgen05 fences around a relaxed arrival are that order; for what lies in the odd SM's shared
+// memory (its copies, relayed, and the zeros) it is an assumption about the chip, which the memory model does not
+// guarantee: the leader's thread learns of it at CTA scope only, and the reader is the odd SM's own tensor core. Order at cluster scope is far from free: a release at that scope took 1040 cycles, an acquire 500 to 700 even if the phase
 // had long completed, more than anything else in the kernel.
 __device__ __forceinline__ void arrive_leader(uint32_t leader_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");

@@ -45,8 +45,11 @@ struct Scratch {
 };
 
 // Step 1, every thread of the CTA: the sequences' reads and units, staged in the scratch.
-// kAll (tree calls with Problem::self_all): every sequence's blocks of 128 rows, which one kernel serves; a block has
-// the tiles of its sequence's last token's keys.
+// kAll (tree calls with Problem::self_all): every sequence's blocks of 128 rows, which one kernel serves; every block has
+// the tiles of all L keys, where the plan kernel's end with the block's last token. So a block's place in the cut is a
+// product, and blocks whose tokens come early visit tiles that are masked throughout. From a graph, 8/1 heads, e4m3, against the
+// plan kernel: trees of 520 tokens on their own keys alone 23.9 against 27.7 us, 4 of 640 47.4 against 50.7, one of 1024 36.8 against
+// 33.2, three of 1000 on 1300 keys 66.3 against 65.8, on 20,000 127.7 against 129.0.
 template <bool kAll = false>
 __device__ __forceinline__ void load(const Problem& p, const Pointers& ptr, Scratch& fs) {
   for (int s = threadIdx.x; s < p.num_seqs; s += blockDim.x) {
