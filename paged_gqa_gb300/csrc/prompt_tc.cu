@@ -17,8 +17,8 @@
 //     row) has the time of two products;
 //   * online softmax, fp32, one row per TMEM lane; the reference of a row moves, and its O is rescaled, only
 //     when a score exceeds it by 2^8;
-//   * the even CTA issues the products. The odd CTA's copies are announced to it by a relaying warp, the
-//     softmax warps of both arrive on its barriers, and its commits arrive in both CTAs;
+//   * the even CTA issues the products. The odd CTA's copies complete on its barriers, the
+//     softmax warps of both arrive on them, and its commits arrive in both CTAs;
 //   * an item's epilogue has a warpgroup of its own, O leaves TMEM at once (part to the stage, part to registers), and
 //     the next item's first S is issued before this one's last P.V, so items follow each other without a gap;
 //   * the work is cut into equal ranges over the clusters, worked out by each CTA for itself: block b of a
@@ -28,8 +28,8 @@
 //
 // Measured (GB300, bf16, back to back, L2 warm): 16384 tokens, 16/2 heads 1100 us, 2000 TFLOP/s of visible pairs (a
 // cuBLAS bf16 product in a burst: 1930; under a power cap held for seconds 1250 us); 8192 tokens, 8/1 164 us, 1670;
-// 2048 tokens 35; 173 tokens 16 (latency: set-up 5, one item's chain of cold steps). Under ncu the tensor pipe is
-// busy 79 % of the cycles at 8192 tokens, DRAM 3 %, L2 hits 89 %. The other 21 % are the ends of ranges (tiles
+// 2048 tokens 33; 173 tokens 17 (latency: set-up 5, one item's chain of cold steps). Under ncu the tensor pipe is
+// busy 78 % of the cycles at 8192 tokens, DRAM 4 %, L2 hits 88 %. The other 22 % are the ends of ranges (tiles
 // on the diagonal, of which half is masked) and the softmax where it takes longer than two products.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -54,7 +54,7 @@ using namespace tc;
 
 constexpr int kRows = 128;                   // rows of a CTA
 constexpr int kKeys = 128;                   // keys of a tile
-// Warps 0-3: K and V copies, items and Q, products or relay; 4-11: softmax; 12-15: epilogue. The kernel starts with
+// Warps 0-3: K and V copies, items and Q, products or (odd CTA) tails; 4-11: softmax; 12-15: epilogue. The kernel starts with
 // 128 registers a thread, which the warpgroups then share out among themselves (setmaxnreg).
 constexpr int kSoftWarp0 = 4, kSoftWarps = 8, kSoftThreads = kSoftWarps * 32;
 constexpr int kEpiWarp0 = kSoftWarp0 + kSoftWarps, kEpiWarps = 4, kEpiThreads = kEpiWarps * 32;
@@ -95,6 +95,9 @@ struct Misc {
   alignas(8) uint64_t item_full[kRing], item_empty[kRing], stat_full[kRing];
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full, q_empty, s_full, s_free, p_full[2][2], pv_done[2], o_ready, o_free, drain, never;
+  // A piece's last tile where it passes the block's keys, of stage g % kStages. Odd CTA: V has landed; even CTA: and its
+  // tail is zeroed.
+  uint64_t tail_v[kStages], tail_full[kStages];
   long long scan[2][kThreads / 32];  // units, blocks
   long long start_off;   // units before the prompt the range starts in
   int start_seq;
@@ -116,32 +119,45 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}\n"
-               : "=r"(ok)
-               : "r"(bar), "r"(parity)
-               : "memory");
-  return ok != 0;
-}
 // The address of a shared variable of the cluster's CTA 0.
 __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
-// Between the CTAs of a pair nothing goes through memory that a thread reads: P, S and O lie in TMEM (the tcgen05
-// fences order those), K, V and Q have landed in the shared memory of the SM whose tensor core reads them before
-// their arrival is sent on, and so have the zeros of a tail (proxy fence). So the signals take no order at cluster
-// scope. For what lies in TMEM the two tcgen05 fences around a relaxed arrival are that order; for what lies in the odd SM's shared
-// memory (its copies, relayed, and the zeros) it is an assumption about the chip, which the memory model does not
-// guarantee: the leader's thread learns of it at CTA scope only, and the reader is the odd SM's own tensor core. Order at cluster scope is far from free: a release at that scope took 1040 cycles, an acquire 500 to 700 even if the phase
-// had long completed, more than anything else in the kernel.
-__device__ __forceinline__ void arrive_leader(uint32_t leader_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
+// The order between the CTAs of a pair. P, S and O lie in TMEM: the tcgen05 fences on both sides of a relaxed arrival
+// order them. The odd CTA's copies of Q, K and V complete on the leader's barriers themselves (.cta_group::2). What
+// threads write, the zeros of a tail, takes a release and an acquire at cluster scope; a release costs its thread 1040 cycles
+// (an acquire next to nothing), so the odd CTA's warp 3, which has nothing else to do, writes them and releases early. (As
+// releases of the softmax warps they cost a call 2-5 %; a relay of landed copies by releases 14-18 %.)
+__device__ __forceinline__ void release_to_leader(uint32_t leader_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
 }
 __device__ __forceinline__ void signal_leader(uint32_t leader_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_bar) : "memory");
+}
+// mbar_wait that acquires at cluster scope.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if ((i & 63u) == 0u) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) break;
+    }
+  }
+  atomicOr(err, kErrTimeout);
+  *abort_flag = 1;
+  return false;
 }
 __device__ __forceinline__ void alloc2(uint32_t dst, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
@@ -171,12 +187,19 @@ __device__ __forceinline__ void commit2(uint32_t bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// `bar`: of either CTA of the pair (a shared::cluster address).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
       " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
+}
+// The odd CTA's copies complete where it cannot wait for them. The leader, which can, does before either CTA leaves; only
+// after an abort may it not have counted on all of them. They take microseconds: then a millisecond goes by.
+__device__ __forceinline__ void outlast_copies() {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < 1000000ull) __nanosleep(10000);
 }
 
 __device__ __forceinline__ void tma_prefetch_3d(const void* tmap, int c0, int c1, int c2) {
@@ -253,25 +276,25 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
   const int used = tpc * a.G;                 // rows of a CTA that hold tokens
 
   if (tid == 0) {
-    const int both = rank == 0 ? 2 : 1;  // the leader's Q, K and V are full once the other CTA's are, too
-    const int relays = rank == 0 ? 1 : 2;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(bar(ms.item_full[i]), 1);
-      mbar_init(bar(ms.item_empty[i]), kSoftWarps + kEpiWarps + 2 + relays);  // + K, V, and the products or both relays
+      mbar_init(bar(ms.item_empty[i]), kSoftWarps + kEpiWarps + 3);  // + K, V, and warp 3
       mbar_init(bar(ms.stat_full[i]), kSoftWarps);
     }
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(ms.k_full[i]), both);
+      mbar_init(bar(ms.k_full[i]), 1);  // (the leader's Q, K and V are full once the other CTA's are, too: twice the bytes)
       mbar_init(bar(ms.k_empty[i]), 1);
-      mbar_init(bar(ms.v_full[i]), both);
+      mbar_init(bar(ms.v_full[i]), 1);
       mbar_init(bar(ms.v_empty[i]), 1);
+      mbar_init(bar(ms.tail_v[i]), 1);
+      mbar_init(bar(ms.tail_full[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(ms.p_full[i][0]), 2 * kSoftWarps);
       mbar_init(bar(ms.p_full[i][1]), 2 * kSoftWarps);
       mbar_init(bar(ms.pv_done[i]), 1);
     }
-    mbar_init(bar(ms.q_full), both);
+    mbar_init(bar(ms.q_full), 1);
     mbar_init(bar(ms.q_empty), 1);
     mbar_init(bar(ms.s_full), 1);
     mbar_init(bar(ms.s_free), 2 * kSoftWarps);
@@ -359,6 +382,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         if (lane == 0) {
           tma_prefetch_desc(&tmap_q);
           const uint64_t policy = policy_evict_first();
+          const uint32_t q_full = in_leader(bar(ms.q_full));
           int s = ms.start_seq, q0, n = prompt_len(a, s, &q0), nb = blocks_of(n, tb);
           long long off = u0 - ms.start_off;
           const long long head_units = units(nb, tb);
@@ -398,9 +422,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
               for (int qd = 0; qd < 4; ++qd) tma_prefetch_3d(&tmap_q, qd * 64, kvh * a.G, q0 + I.tok0 + rank * tpc);
               if (i >= 1) ok = mbar_wait(bar(ms.q_empty), (i - 1) & 1, abort_flag, a.err);
               if (!ok) break;
-              mbar_expect_tx(bar(ms.q_full), (uint32_t)used * 512u);
+              if (rank == 0) mbar_expect_tx(bar(ms.q_full), 2u * (uint32_t)used * 512u);
               for (int qd = 0; qd < 4; ++qd)
-                tma_load_3d(sbase + kOffQ + qd * kQQuarter, &tmap_q, qd * 64, kvh * a.G, q0 + I.tok0 + rank * tpc, bar(ms.q_full), policy);
+                tma_load_3d(sbase + kOffQ + qd * kQQuarter, &tmap_q, qd * 64, kvh * a.G, q0 + I.tok0 + rank * tpc, q_full, policy);
               ++i;
             }
             u = next;
@@ -423,9 +447,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             ms.item[i % kRing].nsplit = 0;
             mbar_arrive(bar(ms.item_full[i % kRing]));
           }
-          // the copies have landed before the CTA may exit (the leader's barrier waits for the other CTA's too;
-          // it gives up when that one has)
-          if (i >= 1) mbar_drain(bar(ms.q_full), (i - 1) & 1, abort_flag, a.err);
+          // the copies, the other CTA's too, have landed before the leader lets either CTA exit
+          if (rank == 0 && i >= 1) mbar_drain(bar(ms.q_full), (i - 1) & 1, abort_flag, a.err);
+          if (rank != 0 && !ok) outlast_copies();
         }
       } else if (warp == 0 || warp == 1) {
         // ------------------------------------------------------------ K (warp 0) and V (warp 1)
@@ -435,6 +459,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
           uint64_t* full = is_k ? ms.k_full : ms.v_full;
           uint64_t* empty = is_k ? ms.k_empty : ms.v_empty;
           const uint32_t region = sbase + (is_k ? kOffK : kOffV);
+          const uint32_t leader_full = in_leader(bar(full[0]));
           tma_prefetch_desc(tmap);
           const uint64_t policy = policy_evict_last();  // every block of a prompt reads them again
           uint32_t g = 0;
@@ -445,76 +470,53 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             for (int t = I.t0; t < I.t1; ++t, ++g) {
               const uint32_t st = g % kStages;
               if (g >= kStages && !(ok = mbar_wait(bar(empty[st]), ((g / kStages) - 1) & 1, abort_flag, a.err))) break;
-              mbar_expect_tx(bar(full[st]), kTile);
+              // V of a tail: the odd CTA's threads write into it first, so it completes there
+              const bool tail = !is_k && t + 1 == I.t1 && (t + 1) * kKeys > I.kv_end;
+              if (rank == 0) mbar_expect_tx(bar(full[st]), tail ? kTile : 2 * kTile);
+              else if (tail) mbar_expect_tx(bar(ms.tail_v[st]), kTile);
+              const uint32_t done = rank != 0 && tail ? bar(ms.tail_v[st]) : leader_full + st * 8;
               const uint32_t dst = region + st * kTile;
               const int key = I.q0 + t * kKeys;
               if (is_k) {
                 for (int qd = 0; qd < 4; ++qd)
-                  tma_load_3d(dst + qd * kKQuarter, tmap, qd * 64, I.kvh, key + rank * 64, bar(full[st]), policy);
+                  tma_load_3d(dst + qd * kKQuarter, tmap, qd * 64, I.kvh, key + rank * 64, done, policy);
               } else {
                 for (int qd = 0; qd < 2; ++qd)
-                  tma_load_3d(dst + qd * kVQuarter, tmap, rank * 128 + qd * 64, I.kvh, key, bar(full[st]), policy);
+                  tma_load_3d(dst + qd * kVQuarter, tmap, rank * 128 + qd * 64, I.kvh, key, done, policy);
               }
             }
             if (ok) give(i);
           }
-          for (uint32_t st = 0; st < kStages; ++st) {  // every copy has landed before the CTA may exit
+          if (rank != 0 && !ok) outlast_copies();
+          for (uint32_t st = 0; rank == 0 && st < kStages; ++st) {  // every copy has landed before either CTA may exit
             if (g <= st) continue;
             const uint32_t last = (g - 1 - st) / kStages;  // the last use of the stage
             mbar_drain(bar(full[st]), last & 1, abort_flag, a.err);
           }
         }
       } else if (warp == 3 && rank != 0) {
-        // ------------------------------------------------------------ the other CTA's relay
-        // One thread polls what it waits for in turn: K (with each item's Q in front) and V land at their own
-        // times, and neither may hold up the other. (K behind V cost 1100 cycles a tile.)
-        if (lane == 0) {
-          struct Stream {
-            int i, left;   // the item, and what of it is still to come (0: the item itself is)
-            uint32_t g;
-            bool q, done;
-          } x[2] = {{0, 0, 0, false, false}, {0, 0, 0, false, false}};
-          const uint32_t q_leader = in_leader(bar(ms.q_full));
-          uint64_t t0 = 0;
-          for (uint32_t polls = 0; !(x[0].done && x[1].done); ++polls) {
-            bool moved = false;
-  #pragma unroll
-            for (int which = 0; which < 2; ++which) {
-              Stream& r = x[which];
-              if (r.done) continue;
-              uint64_t* full = which == 0 ? ms.k_full : ms.v_full;
-              const uint32_t st = r.g % kStages;
-              if (r.left == 0) {
-                if (!mbar_test(bar(ms.item_full[r.i % kRing]), (r.i / kRing) & 1)) continue;
-                const Item& I = ms.item[r.i % kRing];
-                r.done = I.nsplit == 0;
-                r.left = I.t1 - I.t0;
-                r.q = which == 0;
-              } else if (r.q) {
-                if (!mbar_test(bar(ms.q_full), r.i & 1)) continue;
-                arrive_leader(q_leader);
-                r.q = false;
-              } else {
-                if (!mbar_test(bar(full[st]), (r.g / kStages) & 1)) continue;
-                arrive_leader(in_leader(bar(full[st])));
-                ++r.g;
-                if (--r.left == 0) give(r.i++);
-              }
-              moved = true;
-            }
-            if (moved || polls == 0) {
-              t0 = 0;
-            } else if ((polls & 63u) == 0u) {  // bounded, as every wait
-              if (*abort_flag) break;
-              const uint64_t now = global_timer_ns();
-              if (t0 == 0) t0 = now;
-              if (now - t0 > kWaitLimitNs) {
-                atomicOr(a.err, kErrTimeout);
-                *abort_flag = 1;
-                break;
-              }
-            }
+        // ------------------------------------------------------------ the odd CTA's tails
+        // Keys behind a block's last token: their V becomes zeros as soon as it has landed (in the leader the softmax
+        // does that), mostly while the softmax is at the tile before, so that the release costs no one.
+        const uint32_t tail_full = in_leader(bar(ms.tail_full[0]));
+        uint32_t g = 0, tails = 0;  // tiles of the items so far; parity of each stage's tails
+        Item I;
+        for (int i = 0; __all_sync(0xffffffffu, take(i, I)) && I.nsplit > 0; ++i) {
+          g += I.t1 - I.t0;
+          const int end = I.kv_end - (I.t1 - 1) * kKeys;  // keys of the last tile that count
+          if (end < kKeys) {
+            const uint32_t st = (g - 1) % kStages;
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(ms.tail_v[st]), tails >> st & 1, abort_flag, a.err))) break;
+            tails ^= 1u << st;
+            uint8_t* v = smem + kOffV + st * kTile;
+            for (int x = end * 16 + lane; x < kKeys * 16; x += 32)  // 16 bytes: 8 of each d-quarter's row
+              *reinterpret_cast<uint4*>(v + (x >> 3 & 1) * kVQuarter + (x >> 4) * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) release_to_leader(tail_full + st * 8);
           }
+          __syncwarp();
+          if (lane == 0) give(i);
         }
       } else if (warp == 3) {
         // ------------------------------------------------------------ the leader's products
@@ -525,11 +527,16 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         auto waited = [&](const uint64_t& b, uint32_t parity) -> bool {
           return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, a.err));
         };
-        auto pv = [&](uint32_t gg, bool first, bool last, int i) -> bool {
+        uint32_t tails = 0;  // parity of each stage's tails
+        auto pv = [&](uint32_t gg, bool first, bool last, bool tail, int i) -> bool {
           const uint32_t st = gg % kStages, b = gg & 1;
           // the first P.V of an item overwrites O: both CTAs' epilogues of the one before must be done
           if (first && i >= 1 && !waited(ms.o_free, (i - 1) & 1)) return false;
           if (!waited(ms.v_full[st], (gg / kStages) & 1)) return false;
+          if (tail) {  // the odd CTA's V: landed, and zeroed behind the block's keys
+            if (!__all_sync(0xffffffffu, wait_cluster(bar(ms.tail_full[st]), tails >> st & 1, abort_flag, a.err))) return false;
+            tails ^= 1u << st;
+          }
           // P comes in two parts, keys 0-31 and 64-95 of the tile and then the others
   #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -556,6 +563,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
         };
         // The order: S of the next tile, also of the next item, goes before P.V of this one.
         int nt_before = 0;  // tiles of the item before
+        bool tail_before = false;
         for (int i = 0; ok; ++i) {
           if (!(ok = __all_sync(0xffffffffu, take(i, I)))) break;
           const int nt = I.nsplit == 0 ? 0 : I.t1 - I.t0;
@@ -579,15 +587,16 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
               if (j == nt - 1) commit2(bar(ms.q_empty));
             }
             __syncwarp();
-            if (j >= 1) ok = pv(g - 1, j == 1, false, i);
-            else if (i >= 1) ok = pv(g - 1, nt_before == 1, true, i - 1);
+            if (j >= 1) ok = pv(g - 1, j == 1, false, false, i);
+            else if (i >= 1) ok = pv(g - 1, nt_before == 1, true, tail_before, i - 1);
             if (!ok) break;
           }
           if (nt == 0) {  // the end: the last item's last P.V
-            if (i >= 1) ok = pv(g - 1, nt_before == 1, true, i - 1);
+            if (i >= 1) ok = pv(g - 1, nt_before == 1, true, tail_before, i - 1);
             break;
           }
           nt_before = nt;
+          tail_before = I.t1 * kKeys > I.kv_end;
           if (ok && lane == 0) give(i);
         }
         // every product has completed before either CTA may give its TMEM back
@@ -674,12 +683,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             }
             tmem_wait_st();
           }
-          const bool tail = key0 + kKeys > I.kv_end;
+          const bool tail = rank == 0 && key0 + kKeys > I.kv_end;
           if (tail) {
             // keys behind the block's last token (other prompts', later ones'): their V becomes zeros;
             // thread (kh, row) zeroes d-quarter kh of key `row`, each lane of eight beginning with another
             // 16 bytes (another bank). This wait skips the phases of other tiles: V(g - 2) has landed
-            // (P.V(g - 2) is done), V(g + 2) comes after P.V(g).
+            // (P.V(g - 2) is done), V(g + 2) comes after P.V(g). (The odd CTA's warp 3 does its own.)
             mbar_wait(bar(ms.v_full[st]), (g / kStages) & 1, abort_flag, a.err);
             if (key0 + row >= I.kv_end) {
               uint4* dst = reinterpret_cast<uint4*>(smem + kOffV + st * kTile + kh * kVQuarter + row * 128);
@@ -709,9 +718,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_consta
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              const uint32_t full = p_full + (2 * b + h) * 8;
-              if (tail) arrive_leader(full);
-              else signal_leader(full);
+              if (tail) mbar_arrive(bar(ms.p_full[b][h]));
+              else signal_leader(p_full + (2 * b + h) * 8);
             }
           }
         }

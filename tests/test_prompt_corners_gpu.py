@@ -1,4 +1,4 @@
-"""Prompt attention on what its other tests leave out: many prompts of which one is bad, statistics of NaN rows, the launch summary."""
+"""Prompt attention on what its other tests leave out: many prompts of which one is bad, statistics of NaN rows, tails next to NaN, the launch summary."""
 import pytest
 import torch
 
@@ -68,3 +68,22 @@ def test_the_launch_summary_counts_a_captured_calls_kernels():
         g.replay()
         st.synchronize()
     x.check(out, None)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (24, 2), (2, 1)])
+def test_tails_next_to_nan_prompts(hq, hkv, dtype):
+    """Every other prompt is NaN, so a tile that runs past its prompt's end holds V that has to be zeroed in both of a pair's
+    SMs, tile after tile and in items of one tile; again and again, the same bits."""
+    lens = [n for m in (1, 5, 127, 129, 31, 300, 33, 1000, 64, 2, 517, 90) for n in (m, 1 + m % 7)] * 3
+    x = su.Prompt(lens, hq, hkv, dtype, seed=73)
+    for s in range(1, len(lens), 2):
+        for t in (x.q, x.k, x.v):
+            t[x.qsl[s]:x.qsl[s + 1]] = float("nan")
+    out, lse = x.run()
+    x.check(out, lse, rows={s: sorted({0, n // 2, n - 1}) for s, n in enumerate(lens) if s % 2 == 0})
+    good = torch.cat([torch.arange(x.qsl[s], x.qsl[s + 1]) for s in range(0, len(lens), 2)]).cuda()
+    for _ in range(40):
+        again, ls = x.run(check=False)
+        assert torch.equal(again[good], out[good]) and torch.equal(ls[good], lse[good])
+    assert pg.paged_gqa_check_device_errors() == 0
