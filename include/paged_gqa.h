@@ -469,7 +469,7 @@ int paged_gqa_cache_keep(const pg_tensor* k_cache, const pg_tensor* v_cache, con
  *   softmax_scale              multiplies q . k
  *   out        [T, Hq, 256]    of q's type, rows disjoint; overlaps no input (refused)
  *   lse        [T, Hq]         float32 or NULL: natural logarithm of each row's sum of exp(scores), which
- *                              merges this attention with one over other keys
+ *                              merges this attention with one over other keys (NaN where a score is)
  *
  * Scores, the softmax's statistics and the sums of P.V are held in fp32; P is rounded to the inputs'
  * type before P.V. |softmax_scale q . k| may reach 2^25 (there an fp32 score is off by 2 itself; a row beyond it
